@@ -76,7 +76,9 @@ typedef enum {
   RA_ERR_SCRATCH_LIMIT = 8 /* the problem needs more than the library's static scratch holds */
 } ra_status;
 
-typedef enum { RA_BF16 = 0, RA_FP32 = 1 } ra_dtype;
+/* RA_E2M1X2 (bytes of two 4-bit numbers) and RA_E4M3 (8-bit scales) occur in a
+ * ra_kv_cache only. */
+typedef enum { RA_BF16 = 0, RA_FP32 = 1, RA_E2M1X2 = 2, RA_E4M3 = 3 } ra_dtype;
 
 typedef struct {
   void* data;        /* device pointer */
@@ -289,6 +291,110 @@ size_t ring_attn_varlen_workspace_size(int32_t op, int64_t total, int64_t h, int
  * part 256-byte aligned.  Varlen calls use b = 1, s = total.  0 on bad sizes. */
 size_t ring_attn_workspace_size(int32_t op, int64_t b, int64_t h, int64_t s, int64_t d, int32_t n_shards);
 
+/* ---------------------------------------------------------------- paged 4-bit key / value cache
+ * What a server keeps of the sequences that the calls above have computed: the
+ * keys (rotated) and values of every token so far, in 4 bits, in pages.
+ *
+ * ra_kv_cache: n_pages pages of `page` tokens of all hk key / value heads.
+ *   k, v: (n_pages, hk, page, d / 2) RA_E2M1X2: head dim 2c in the low and 2c + 1
+ *   in the high half of byte c.  A 4-bit number is a sign bit over the index of
+ *   its magnitude in 0, 0.5, 1, 1.5, 2, 3, 4, 6 (2 exponent bits, 1 mantissa bit).
+ *   k_scale, v_scale: (n_pages, hk, page, d / 16) RA_E4M3, one scale per 16
+ *   consecutive head dims of a token.  The value is number * scale; both factors
+ *   together have at most 6 significant bits, so bf16 and fp16 hold it exactly.
+ *   d in {64, 128}; page a power of two in [16, 256]; the last dimension is
+ *   contiguous, every other stride of k and v is a multiple of 16 bytes and of
+ *   the scales a multiple of d / 16 bytes, base pointers are 16-byte aligned
+ *   (k, v) and 8-byte aligned (scales).  Any order of the first three
+ *   dimensions is allowed, and k and v may be parts of one allocation.
+ *
+ * ra_kv_seqs: the sequences of one call.
+ *   page_table: (n_seqs, max_pages) int32 device array, rows page_table_stride
+ *   apart: entry [i][j] is the page with tokens [j * page, (j + 1) * page) of
+ *   sequence i.  Entries past a sequence's length are not read.
+ *   kv_lens: (n_seqs) int32 device array: tokens of each sequence in the cache,
+ *   AFTER the call's own tokens were appended.
+ *   cu_seqlens_dev / cu_seqlens_host: as in the varlen calls, over the call's
+ *   new tokens: rows [cu[i], cu[i+1]) of q, k, v belong to sequence i, and new
+ *   token j of its n is the cache's token kv_lens[i] - n + j.  A sequence may
+ *   have no new token.  Rows from cu[n_seqs] on (a padded batch) are left as they
+ *   were.  cu_seqlens_dev must hold what cu_seqlens_host holds.
+ *   Only cu_seqlens is read on the host, so a captured call follows kv_lens,
+ *   the page table and positions as they are when it is replayed.
+ * Device data that the host cannot check is checked by the kernels: a page
+ * outside [0, n_pages), a length above max_pages * page (or max_kv_len) and a
+ * position outside the rotation table are never used; the token counts as
+ * masked (or is not written) and RA_ERR_DEVICE is recorded for
+ * ring_attn_check_device_error (low byte of info: 0x61 length, 0x62 page, 0x63
+ * position). */
+typedef struct {
+  ra_tensor k, k_scale, v, v_scale;
+} ra_kv_cache;
+
+typedef struct {
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* kv_lens;
+  const int32_t* cu_seqlens_dev;
+  const int32_t* cu_seqlens_host;
+  int32_t max_pages;
+  int32_t n_seqs;
+} ra_kv_seqs;
+
+/* Pairs of head dims that the rotation turns: (i, i + r/2) or (2i, 2i + 1), i < r/2. */
+typedef enum { RA_ROPE_HALVES = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope;
+
+/* ring_attn_cache_append: rotates q and k and puts k and v into the cache.
+ *   q (optional), q_out: (rows, h, d) bf16; k, v: (rows, hk, d) bf16; rows >=
+ *   cu_seqlens[n_seqs]; strides and pointers as for the attention calls.  q_out
+ *   may be q itself; any other overlap with q, k or v is RA_ERR_INVALID_ARG.
+ *   rope_cos, rope_sin (both or neither): (positions, r / 2) fp32, r <= d a
+ *   multiple of 16, rows 16-byte aligned.  A pair (a, b) at position p becomes
+ *   (a cos - b sin, b cos + a sin); head dims from r on stay.  Position of a
+ *   token: positions[row] (int32, device) or, with positions NULL, its index in
+ *   the cache.  Without tables nothing is rotated and q is copied.
+ *   The 16 numbers x of a scale group are stored as
+ *     scale = max(e4m3(max|x| / 6), 2^-9),  number = e2m1(x / scale),
+ *   each rounded to nearest, ties to even, and saturating: an infinite or NaN
+ *   input is stored as a finite number.  x is the exact rotation of the bf16
+ *   input by the fp32 table entries, carried to about 2^-47, so the stored bits do
+ *   not depend on the order of the operations.
+ *   A token whose cache index is negative (kv_lens[i] < n) is padding: nothing
+ *   is written for it.  Two tokens of one call must not name the same place. */
+ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                 const ra_tensor* rope_cos, const ra_tensor* rope_sin, int32_t rope,
+                                 const int32_t* positions, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
+                                 ra_tensor* q_out, void* stream);
+
+/* ring_attn_cache_read: the cache's tokens that the call's rows stand for, as
+ * bf16 (exact), the input of the attention calls above: k_out, v_out (rows, hk,
+ * d) bf16, row cu[i] + j getting token kv_lens[i] - n + j of sequence i.  With
+ * n = kv_lens[i] that is the whole sequence.  Rows of negative tokens, and of
+ * tokens that a bad page table hides, are left as they were. */
+ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs, ra_tensor* k_out, ra_tensor* v_out,
+                               void* stream);
+
+/* ring_attn_cache_fwd: attention of the new tokens over the cache.
+ *   q: (rows, h, d) bf16, rotated; h a multiple of hk (query head i attends with
+ *   head i / (h / hk)).  out: (rows, h, d) bf16 or fp32 (fp32: the accumulator of
+ *   lse_merge); lse: (h, rows) fp32, natural log, any strides.
+ *   causal: new token j of n sees the cache's tokens up to its own, kv_lens[i] - n
+ *   + j; else every token of the sequence (what cross attention to cached states
+ *   needs).  A row that sees no token gets out = 0, lse = -inf, so shards of one
+ *   sequence's cache, each with its own call, combine by lse_merge.
+ *   max_kv_len: no kv_lens[i] is above it (0: max_pages * page); it sizes the
+ *   grid, so a tight bound helps short sequences.
+ *   workspace: ring_attn_cache_workspace_size bytes, 256-byte aligned, need not
+ *   be initialised; partial results of sequences that several blocks share. */
+ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs, int32_t causal,
+                              float softmax_scale, int32_t max_kv_len, ra_tensor* out, ra_tensor* lse,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of a ring_attn_cache_fwd call whose sequences have at most
+ * max_new new tokens, total in all; 0 on bad sizes. */
+size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,
+                                      int32_t n_seqs);
+
 /* Synchronises `stream`, then reads and clears this device's error word.
  * Returns RA_OK, RA_ERR_TIMEOUT (a bounded wait ran out: the kernel gave up
  * and returned) or RA_ERR_DEVICE; RA_ERR_CUDA if the synchronisation failed.
@@ -320,7 +426,11 @@ typedef enum {
   RA_KERNEL_BWD_DQ = 3,    /* ring backward: the dQ kernel */
   RA_KERNEL_PERMUTE = 4,   /* permute / unpermute */
   RA_KERNEL_LSE_MERGE = 5,
-  RA_KERNEL_COUNT = 6
+  RA_KERNEL_CACHE_APPEND = 6,
+  RA_KERNEL_CACHE_READ = 7,
+  RA_KERNEL_CACHE_FWD = 8,   /* attention over the 4-bit cache */
+  RA_KERNEL_CACHE_JOIN = 9,  /* joins the partial results of ring_attn_cache_fwd */
+  RA_KERNEL_COUNT = 10
 } ra_kernel;
 ra_status ring_attn_timing_enable(int32_t on);
 ra_status ring_attn_timing_read(int32_t kernel, double* total_ms, int64_t* launches);

@@ -23,10 +23,12 @@ __all__ = [
     "ring_attn_kvpacked_bwd", "ring_attn_varlen_qkvpacked_fwd", "ring_attn_varlen_qkvpacked_bwd",
     "ring_attn_varlen_kvpacked_fwd", "ring_attn_varlen_kvpacked_bwd", "ring_attn_varlen_permute",
     "ring_attn_varlen_unpermute", "ring_attn_llama3_varlen_fwd", "ring_attn_llama3_varlen_bwd", "CuSeqlens",
+    "KVCache", "ring_attn_cache_append", "ring_attn_cache_read", "ring_attn_cache_fwd", "ring_attn_cache_workspace_size",
+    "ring_attn_cache_workspace",
 ]
 
 LAYOUTS = {"contiguous": 0, "zigzag": 1, "stripe": 2}
-RA_BF16, RA_FP32 = 0, 1
+RA_BF16, RA_FP32, RA_E2M1X2, RA_E4M3 = 0, 1, 2, 3
 RA_OP_FWD, RA_OP_BWD = 0, 1
 RA_KNOB_WAIT_LIMIT_NS, RA_KNOB_DEBUG_FLAGS, RA_KNOB_DKDV_PAIR = 0, 1, 2
 
@@ -37,10 +39,12 @@ EXPORTED_SYMBOLS = (
     "ring_attn_check_device_error", "ring_attn_set_knob", "ring_attn_timing_enable", "ring_attn_timing_read",
     "ra_status_string", "ring_attn_version", "ring_attn_bwd_static_scratch", "ring_attn_varlen_permute",
     "ring_attn_varlen_unpermute", "ring_attn_llama3_varlen_fwd", "ring_attn_llama3_varlen_bwd",
-    "ring_attn_debug_bounds", "ring_attn_varlen_workspace_size",
+    "ring_attn_debug_bounds", "ring_attn_varlen_workspace_size", "ring_attn_cache_append", "ring_attn_cache_read",
+    "ring_attn_cache_fwd", "ring_attn_cache_workspace_size",
 )
 RA_STATIC_SCRATCH_BYTES = 16 << 20
-KERNELS = {"fwd": 0, "bwd_dkdv": 1, "bwd_pre": 2, "bwd_dq": 3, "permute": 4, "lse_merge": 5}
+KERNELS = {"fwd": 0, "bwd_dkdv": 1, "bwd_pre": 2, "bwd_dq": 3, "permute": 4, "lse_merge": 5, "cache_append": 6,
+           "cache_read": 7, "cache_fwd": 8, "cache_join": 9}
 
 
 class RingAttnError(RuntimeError):
@@ -52,6 +56,16 @@ class RingAttnError(RuntimeError):
 class _Tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", _Tensor), ("k_scale", _Tensor), ("v", _Tensor), ("v_scale", _Tensor)]
+
+
+class _KVSeqs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("cu_seqlens_dev", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32)]
 
 
 _LIB = None
@@ -79,6 +93,7 @@ def load():
     lib = ctypes.CDLL(path)
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     T = ctypes.POINTER(_Tensor)
+    C, S = ctypes.POINTER(_KVCache), ctypes.POINTER(_KVSeqs)
     sig = {
         "ring_attn_fwd": [T, T, T, I32, I32, I32, F32, T, T, P, SZ, P],
         "ring_attn_fwd_step": [T, T, T, I32, I32, I32, F32, I32, T, T, P],
@@ -93,6 +108,9 @@ def load():
         "ring_attn_varlen_unpermute": [T, T, P, P, I32, I32, I32, I32, P],
         "ring_attn_permute": [T, T, I32, I32, I32, P],
         "ring_attn_unpermute": [T, T, I32, I32, I32, P],
+        "ring_attn_cache_append": [T, T, T, T, T, I32, P, C, S, T, P],
+        "ring_attn_cache_read": [C, S, T, T, P],
+        "ring_attn_cache_fwd": [T, C, S, I32, F32, I32, T, T, P, SZ, P],
         "ring_attn_check_device_error": [P, ctypes.POINTER(I32)],
         "ring_attn_set_knob": [I32, I64],
         "ring_attn_timing_enable": [I32],
@@ -106,6 +124,8 @@ def load():
     lib.ring_attn_workspace_size.restype = SZ
     lib.ring_attn_varlen_workspace_size.argtypes = [I32, I64, I64, I64, I32, I32]
     lib.ring_attn_varlen_workspace_size.restype = SZ
+    lib.ring_attn_cache_workspace_size.argtypes = [I64, I64, I64, I64, I64, I32]
+    lib.ring_attn_cache_workspace_size.restype = SZ
     lib.ra_status_string.argtypes = [I32]
     lib.ra_status_string.restype = ctypes.c_char_p
     lib.ring_attn_version.argtypes = []
@@ -558,6 +578,196 @@ def ring_attn_unpermute(y, layout, n_shards, seq_dim=2, out=None, stream=None):
     _check(lib.ring_attn_unpermute(ctypes.byref(a), ctypes.byref(b_), _layout(layout), int(n_shards),
                                    int(seq_dim), _stream(stream)), "ring_attn_unpermute")
     return out
+
+
+# ---------------------------------------------------------------------------- paged 4-bit cache
+class KVCache:
+    """A paged key / value cache in 4 bits, as the ring_attn_cache_* calls take it.
+
+    k, v: (n_pages, hk, page, d // 2) uint8, two e2m1 numbers per byte; k_scale, v_scale:
+    (n_pages, hk, page, d // 16) float8_e4m3fn.  Any order of the first three dimensions in
+    memory (pass a transposed view).  The handle keeps the tensors, which the caller
+    allocates, and their description, so that a call marshals nothing for them;
+    KVCache.empty allocates a cache of zeros."""
+
+    def __init__(self, k, k_scale, v, v_scale):
+        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        for name, x, dtype in (("k", k, torch.uint8), ("k_scale", k_scale, torch.float8_e4m3fn),
+                               ("v", v, torch.uint8), ("v_scale", v_scale, torch.float8_e4m3fn)):
+            if not isinstance(x, torch.Tensor) or not x.is_cuda:
+                raise ValueError("ring_attn_gb300 takes CUDA tensors only")
+            if x.dtype != dtype or x.dim() != 4:
+                raise ValueError(f"{name} must be a 4-D {dtype} tensor")
+            if x.device != k.device:
+                raise ValueError("the cache's tensors must be on one device")
+        self.device = k.device
+        self.n_pages, self.hk, self.page, self.d = k.shape[0], k.shape[1], k.shape[2], 2 * k.shape[3]
+        self._c = _KVCache(_desc(k, RA_E2M1X2), _desc(k_scale, RA_E4M3), _desc(v, RA_E2M1X2), _desc(v_scale, RA_E4M3))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages, page, hk, d, device="cuda"):
+        code = lambda w: torch.zeros((n_pages, hk, page, w), dtype=torch.uint8, device=device)  # noqa: E731
+        return cls(code(d // 2), code(d // 16).view(torch.float8_e4m3fn), code(d // 2),
+                   code(d // 16).view(torch.float8_e4m3fn))
+
+
+_I64x4 = ctypes.c_int64 * 4
+
+
+def _desc(x, dtype):
+    """The ra_tensor of x (1-D to 4-D)."""
+    return _Tensor(x.data_ptr(), dtype, x.dim(), _I64x4(*x.shape), _I64x4(*x.stride()))
+
+
+_RA_DTYPE = {torch.bfloat16: RA_BF16, torch.float32: RA_FP32}
+
+
+def _on(x, device, dims):
+    """The ra_tensor of a bf16 or fp32 tensor on the cache's device."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("ring_attn_gb300 takes CUDA tensors only")
+    if x.device != device:
+        raise ValueError(f"tensor on {x.device}, cache on {device}")
+    if x.dtype not in _RA_DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if x.dim() != dims:
+        raise ValueError(f"expected a {dims}-D tensor, got {tuple(x.shape)}")
+    return _desc(x, _RA_DTYPE[x.dtype])
+
+
+def _ints(x, device, dims, what):
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.int32 or x.dim() != dims or x.device != device:
+        raise ValueError(f"{what} must be a {dims}-D int32 tensor on {device}")
+    if x.numel() and x.stride(-1) != 1:
+        raise ValueError(f"{what} must be contiguous along its last dimension")
+    return x.data_ptr()
+
+
+class _CacheCall:
+    """Checks and marshals what the three cache calls have in common, and makes the
+    cache's device (and the given stream) current for outputs and launches."""
+
+    def __init__(self, cache, page_table, kv_lens, cu_seqlens, stream):
+        if not isinstance(cache, KVCache):
+            raise ValueError("cache must be a KVCache")
+        dev = self.device = cache.device
+        if not isinstance(cu_seqlens, CuSeqlens):
+            with torch.cuda.stream(stream):  # copied and freed in the stream that reads it
+                cu_seqlens = CuSeqlens(cu_seqlens, dev)
+        elif cu_seqlens.dev.device != dev:
+            raise ValueError(f"CuSeqlens was prepared for {cu_seqlens.dev.device}, not {dev}")
+        self.cu = cu_seqlens
+        table, lens = _ints(page_table, dev, 2, "page_table"), _ints(kv_lens, dev, 1, "kv_lens")
+        n = cu_seqlens.n_seqs
+        if page_table.shape[0] != n or kv_lens.shape[0] != n:
+            raise ValueError(f"page_table and kv_lens must have one row for each of the {n} sequences")
+        self.seqs = _KVSeqs(table, page_table.stride(0) if n > 1 else page_table.shape[1], lens,
+                            cu_seqlens.dev.data_ptr(), cu_seqlens.host.data_ptr(), page_table.shape[1], n)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, cache on {dev}")
+        self.stream = stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.guard = torch.cuda.stream(self.stream)  # also makes its device current
+        elif self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.ptr = ctypes.c_void_p((self.stream or torch.cuda.current_stream()).cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def ring_attn_cache_append(k, v, cache, page_table, kv_lens, cu_seqlens, q=None, rope=None, positions=None,
+                           interleaved=False, q_out=None, stream=None):
+    """Rotates k and q and puts k and v into the paged 4-bit cache.
+
+    k, v: (rows, hk, d) bf16, the new tokens of every sequence (cu_seqlens over them, a CuSeqlens
+    to copy nothing); kv_lens: (n_seqs,) int32, the sequences' lengths after this call; page_table:
+    (n_seqs, max_pages) int32.  q: (rows, h, d) bf16 or None; q_out may be q.  rope: (cos, sin), each
+    (positions, r // 2) fp32, or None; positions: (rows,) int32, or None for the tokens' cache indices.
+    Rows past cu_seqlens[-1] are left as they were.  Returns q_out (None without q)."""
+    lib = load()
+    with _CacheCall(cache, page_table, kv_lens, cu_seqlens, stream) as c:
+        tk, tv = _on(k, c.device, 3), _on(v, c.device, 3)
+        tq = to = tc = ts = pos = None
+        if q is None and q_out is not None:
+            raise ValueError("q_out without q")
+        if q is not None:
+            tq = _on(q, c.device, 3)
+            q_out = torch.empty_like(q) if q_out is None else q_out
+            to = tq if q_out is q else _on(q_out, c.device, 3)
+        if rope is not None:
+            tc, ts = _on(rope[0], c.device, 2), _on(rope[1], c.device, 2)
+        if positions is not None:
+            pos = _ints(positions, c.device, 1, "positions")
+            if positions.shape[0] < c.cu.total:
+                raise ValueError("positions must have an entry for every new token")
+        if c.cu.total:
+            _check(lib.ring_attn_cache_append(tq, tk, tv, tc, ts, int(bool(interleaved)), pos, cache._ref, c.seqs, to,
+                                              c.ptr), "ring_attn_cache_append")
+    return q_out
+
+
+def ring_attn_cache_read(cache, page_table, kv_lens, cu_seqlens, k_out=None, v_out=None, stream=None):
+    """The last cu_seqlens[i + 1] - cu_seqlens[i] cached tokens of every sequence as bf16.
+
+    Returns (k, v), each (rows, hk, d): contiguous input for the attention calls."""
+    lib = load()
+    with _CacheCall(cache, page_table, kv_lens, cu_seqlens, stream) as c:
+        if k_out is None:
+            k_out = torch.empty((c.cu.total, cache.hk, cache.d), dtype=torch.bfloat16, device=c.device)
+        if v_out is None:
+            v_out = torch.empty((c.cu.total, cache.hk, cache.d), dtype=torch.bfloat16, device=c.device)
+        tk, tv = _on(k_out, c.device, 3), _on(v_out, c.device, 3)
+        if c.cu.total:
+            _check(lib.ring_attn_cache_read(cache._ref, c.seqs, tk, tv, c.ptr), "ring_attn_cache_read")
+    return k_out, v_out
+
+
+def ring_attn_cache_workspace_size(total, max_new, h, hk, d, n_seqs) -> int:
+    """Bytes of ring_attn_cache_fwd's workspace for `total` new tokens, at most max_new of one sequence."""
+    return int(load().ring_attn_cache_workspace_size(int(total), int(max_new), int(h), int(hk), int(d), int(n_seqs)))
+
+
+def ring_attn_cache_workspace(q, cache, cu_seqlens):
+    """A workspace for ring_attn_cache_fwd calls with this q, cache and CuSeqlens (calls on one stream can share it)."""
+    n = ring_attn_cache_workspace_size(cu_seqlens.total, cu_seqlens.max_seqlen, q.shape[1], cache.hk, cache.d,
+                                       cu_seqlens.n_seqs)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def ring_attn_cache_fwd(q, cache, page_table, kv_lens, cu_seqlens, causal=True, softmax_scale=None, max_kv_len=0,
+                        out=None, lse=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """Attention of new tokens over the paged 4-bit cache.
+
+    q: (rows, h, d) bf16, rotated, h a multiple of the cache's heads; the new tokens are already in
+    the cache (ring_attn_cache_append), the last ones of each sequence.  causal: a token sees the
+    cache up to itself; else the whole sequence.  max_kv_len: an upper bound of kv_lens (0: what the
+    page table can hold).  workspace: from ring_attn_cache_workspace, or None to allocate it.
+    Returns (out (rows, h, d) bf16 or fp32, lse (h, rows) fp32); rows that see nothing get 0 and -inf."""
+    lib = load()
+    with _CacheCall(cache, page_table, kv_lens, cu_seqlens, stream) as c:
+        tq = _on(q, c.device, 3)
+        rows, h, d = q.shape
+        out = torch.empty((rows, h, d), dtype=out_dtype, device=c.device) if out is None else out
+        lse = torch.empty((h, rows), dtype=torch.float32, device=c.device) if lse is None else lse
+        to, tl = _on(out, c.device, 3), _on(lse, c.device, 2)
+        if c.cu.total:
+            if workspace is None:
+                workspace = ring_attn_cache_workspace(q, cache, c.cu)
+            elif not workspace.is_cuda or workspace.device != c.device:
+                raise ValueError(f"workspace must be on {c.device}")
+            wp, wb = _ws_arg(workspace)
+            _check(lib.ring_attn_cache_fwd(tq, cache._ref, c.seqs, int(bool(causal)), _scale(softmax_scale, d),
+                                           int(max_kv_len), to, tl, wp, wb, c.ptr), "ring_attn_cache_fwd")
+    return out, lse
 
 
 def ring_attn_check_device_error(stream=None):

@@ -929,6 +929,202 @@ ra_status ring_attn_varlen_unpermute(const ra_tensor* y, ra_tensor* x, const int
   return varlen_permute_common(y, x, cu_seqlens_dev, cu_seqlens_host, n_seqs, layout, n_shards, seq_dim, 1, stream);
 }
 
+// ------------------------------------------------------------------ paged 4-bit cache
+// (rows, heads, d) rows of new tokens: at least `total` rows of `heads` heads (-1: any number).
+static ra_status check_rows3(const ra_tensor* t, int32_t dtype, long long total, long long heads, long long d,
+                             Rows3* v) {
+  if (!t || !t->data || t->ndim != 3 || t->dtype != dtype) return RA_ERR_INVALID_ARG;
+  if (t->shape[0] < total || t->shape[1] < 1 || t->shape[2] != d) return RA_ERR_INVALID_ARG;
+  if (heads >= 0 && t->shape[1] != heads) return RA_ERR_INVALID_ARG;
+  const int es = dtype == RA_FP32 ? 4 : 2;
+  if (t->stride[2] != 1) return RA_ERR_ALIGNMENT;
+  for (int i = 0; i < 2; ++i)  // (the stride of a dimension of size 1 is not used)
+    if (t->shape[i] > 1 && (t->stride[i] <= 0 || t->stride[i] % (16 / es) != 0)) return RA_ERR_ALIGNMENT;
+  if (!aligned(t->data, 16)) return RA_ERR_ALIGNMENT;
+  *v = Rows3{t->data, t->shape[0] > 1 ? t->stride[0] : 0, t->shape[1] > 1 ? t->stride[1] : 0};
+  return RA_OK;
+}
+
+// One of the cache's four arrays, (n_pages, hk, page, width) bytes; align: bytes of its row starts.
+static ra_status check_cache_rows(const ra_tensor* t, int32_t dtype, const ra_tensor* like, long long width, int align,
+                                  int base_align, CacheRows* r) {
+  if (!t->data || t->ndim != 4 || t->dtype != dtype || t->shape[3] != width) return RA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (t->shape[i] < 1 || t->shape[i] != like->shape[i]) return RA_ERR_INVALID_ARG;
+  if (t->stride[3] != 1) return RA_ERR_ALIGNMENT;
+  for (int i = 0; i < 3; ++i)
+    if (t->shape[i] > 1 && (t->stride[i] <= 0 || t->stride[i] % align != 0)) return RA_ERR_ALIGNMENT;
+  if (!aligned(t->data, base_align)) return RA_ERR_ALIGNMENT;
+  *r = CacheRows{static_cast<uint8_t*>(t->data), t->shape[0] > 1 ? t->stride[0] : 0,
+                 t->shape[1] > 1 ? t->stride[1] : 0, t->shape[2] > 1 ? t->stride[2] : 0};
+  return RA_OK;
+}
+
+static ra_status check_cache(const ra_kv_cache* c, CacheView* v, long long* d) {
+  if (!c) return RA_ERR_INVALID_ARG;
+  if (c->k.ndim != 4) return RA_ERR_INVALID_ARG;
+  *d = 2 * c->k.shape[3];
+  if (*d < 2 || c->k.shape[0] > INT32_MAX || c->k.shape[1] > 65535) return RA_ERR_INVALID_ARG;
+  if (*d != 64 && *d != 128) return RA_ERR_UNSUPPORTED;
+  const int srow = (int)(*d / 16);
+  RA_TRY(check_cache_rows(&c->k, RA_E2M1X2, &c->k, *d / 2, 16, 16, &v->k));
+  RA_TRY(check_cache_rows(&c->v, RA_E2M1X2, &c->k, *d / 2, 16, 16, &v->v));
+  RA_TRY(check_cache_rows(&c->k_scale, RA_E4M3, &c->k, *d / 16, srow, 8, &v->ks));
+  RA_TRY(check_cache_rows(&c->v_scale, RA_E4M3, &c->k, *d / 16, srow, 8, &v->vs));
+  const long long page = c->k.shape[2];
+  if (page < 16 || page > 256 || (page & (page - 1))) return RA_ERR_UNSUPPORTED;
+  v->n_pages = (int)c->k.shape[0];
+  v->hk = (int)c->k.shape[1];
+  v->page_shift = 0;
+  while ((1LL << v->page_shift) < page) ++v->page_shift;
+  return RA_OK;
+}
+
+// max_new (optional): the most new tokens of one sequence.
+static ra_status check_seqs(const ra_kv_seqs* s, const CacheView& c, CacheSeqs* v, int* max_new) {
+  if (!s || !s->page_table || !s->kv_lens || !s->cu_seqlens_dev || !s->cu_seqlens_host) return RA_ERR_INVALID_ARG;
+  if (s->n_seqs < 1 || s->n_seqs > 65535 || s->max_pages < 1 || s->page_table_stride < (s->n_seqs > 1 ? s->max_pages : 0))
+    return RA_ERR_INVALID_ARG;
+  if (!aligned(s->page_table, 4) || !aligned(s->kv_lens, 4) || !aligned(s->cu_seqlens_dev, 4)) return RA_ERR_ALIGNMENT;
+  if (((long long)s->max_pages << c.page_shift) > (1LL << 30)) return RA_ERR_UNSUPPORTED;
+  const int32_t* cu = s->cu_seqlens_host;
+  if (cu[0] != 0) return RA_ERR_INVALID_ARG;
+  int mx = 0;
+  for (int i = 0; i < s->n_seqs; ++i) {
+    if (cu[i + 1] < cu[i]) return RA_ERR_INVALID_ARG;
+    if (cu[i + 1] - cu[i] > mx) mx = cu[i + 1] - cu[i];
+  }
+  if (cu[s->n_seqs] > (1 << 30)) return RA_ERR_UNSUPPORTED;
+  if (max_new) *max_new = mx;
+  *v = CacheSeqs{s->page_table, s->page_table_stride, s->kv_lens, s->cu_seqlens_dev, s->n_seqs,
+                 (int)(s->max_pages << c.page_shift), cu[s->n_seqs]};
+  return RA_OK;
+}
+
+static ra_status check_rope_table(const ra_tensor* t, const ra_tensor* like, const float** data, long long* stride) {
+  if (!t || !t->data || t->ndim != 2 || t->dtype != RA_FP32) return RA_ERR_INVALID_ARG;
+  if (t->shape[0] < 1 || t->shape[0] != like->shape[0] || t->shape[1] != like->shape[1]) return RA_ERR_INVALID_ARG;
+  if (t->stride[1] != 1 || !aligned(t->data, 16)) return RA_ERR_ALIGNMENT;
+  if (t->shape[0] > 1 && (t->stride[0] <= 0 || t->stride[0] % 4 != 0)) return RA_ERR_ALIGNMENT;
+  *data = static_cast<const float*>(t->data);
+  *stride = t->shape[0] > 1 ? t->stride[0] : 0;
+  return RA_OK;
+}
+
+static bool same_view(const ra_tensor* a, const ra_tensor* b) {
+  if (a->data != b->data || a->ndim != b->ndim) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->shape[i] != b->shape[i] || (a->shape[i] > 1 && a->stride[i] != b->stride[i])) return false;
+  return true;
+}
+
+ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                 const ra_tensor* rope_cos, const ra_tensor* rope_sin, int32_t rope,
+                                 const int32_t* positions, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
+                                 ra_tensor* q_out, void* stream) {
+  AppendArgs a;
+  memset(&a, 0, sizeof(a));
+  long long d = 0;
+  RA_TRY(check_cache(cache, &a.c, &d));
+  RA_TRY(check_seqs(seqs, a.c, &a.s, nullptr));
+  a.d = (int)d;
+  a.hk = a.c.hk;
+  RA_TRY(check_rows3(k, RA_BF16, a.s.total, a.hk, d, &a.k));
+  RA_TRY(check_rows3(v, RA_BF16, a.s.total, a.hk, d, &a.v));
+  if ((q != nullptr) != (q_out != nullptr)) return RA_ERR_INVALID_ARG;
+  if (q) {
+    RA_TRY(check_rows3(q, RA_BF16, a.s.total, -1, d, &a.q));
+    RA_TRY(check_rows3(q_out, RA_BF16, a.s.total, q->shape[1], d, &a.q_out));
+    if (q->shape[1] > 65535 || q->shape[1] % a.hk != 0) return RA_ERR_INVALID_ARG;
+    a.h = (int)q->shape[1];
+    // each row is read and written by the same lanes, so in place is fine, but
+    // nothing else that other rows still have to read may be written
+    if (!same_view(q, q_out) &&
+        (ranges_overlap(q, q_out, 2) || ranges_overlap(k, q_out, 2) || ranges_overlap(v, q_out, 2)))
+      return RA_ERR_INVALID_ARG;
+  }
+  if ((rope_cos != nullptr) != (rope_sin != nullptr)) return RA_ERR_INVALID_ARG;
+  if (rope != RA_ROPE_HALVES && rope != RA_ROPE_INTERLEAVED) return RA_ERR_INVALID_ARG;
+  if (rope_cos) {
+    if (rope_cos->ndim != 2 || rope_cos->shape[1] < 1 || 2 * rope_cos->shape[1] > d || rope_cos->shape[1] % 8 != 0)
+      return RA_ERR_INVALID_ARG;
+    if (rope_cos->shape[0] > INT32_MAX) return RA_ERR_INVALID_ARG;
+    RA_TRY(check_rope_table(rope_cos, rope_cos, &a.cos_t, &a.cos_stride));
+    RA_TRY(check_rope_table(rope_sin, rope_cos, &a.sin_t, &a.sin_stride));
+    a.rot = (int)(2 * rope_cos->shape[1]);
+    a.max_pos = (int)rope_cos->shape[0];
+  }
+  if (positions && !aligned(positions, 4)) return RA_ERR_ALIGNMENT;
+  a.style = rope;
+  a.positions = positions;
+  if (a.s.total == 0) return RA_OK;
+  RA_TRY(dev_ctl(&a.ctl));
+  TimedLaunch tl(RA_KERNEL_CACHE_APPEND, static_cast<cudaStream_t>(stream));
+  return cuda_status(launch_cache_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs, ra_tensor* k_out, ra_tensor* v_out,
+                               void* stream) {
+  ReadArgs a;
+  memset(&a, 0, sizeof(a));
+  long long d = 0;
+  RA_TRY(check_cache(cache, &a.c, &d));
+  RA_TRY(check_seqs(seqs, a.c, &a.s, nullptr));
+  a.d = (int)d;
+  a.hk = a.c.hk;
+  RA_TRY(check_rows3(k_out, RA_BF16, a.s.total, a.hk, d, &a.k_out));
+  RA_TRY(check_rows3(v_out, RA_BF16, a.s.total, a.hk, d, &a.v_out));
+  if (a.s.total == 0) return RA_OK;
+  RA_TRY(dev_ctl(&a.ctl));
+  TimedLaunch tl(RA_KERNEL_CACHE_READ, static_cast<cudaStream_t>(stream));
+  return cuda_status(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs, int32_t causal,
+                              float softmax_scale, int32_t max_kv_len, ra_tensor* out, ra_tensor* lse,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  CacheAttnArgs a;
+  memset(&a, 0, sizeof(a));
+  long long d = 0;
+  RA_TRY(check_cache(cache, &a.c, &d));
+  RA_TRY(check_seqs(seqs, a.c, &a.s, &a.max_new));
+  a.d = (int)d;
+  a.hk = a.c.hk;
+  RA_TRY(check_rows3(q, RA_BF16, a.s.total, -1, d, &a.q));
+  if (q->shape[1] > 65535 || q->shape[1] % a.hk != 0) return RA_ERR_INVALID_ARG;
+  a.h = (int)q->shape[1];
+  a.G = a.h / a.hk;
+  if (!out || (out->dtype != RA_BF16 && out->dtype != RA_FP32)) return RA_ERR_INVALID_ARG;
+  a.out_f32 = out->dtype == RA_FP32;
+  RA_TRY(check_rows3(out, out->dtype, a.s.total, a.h, d, &a.out));
+  if (!lse || !lse->data || lse->ndim != 2 || lse->dtype != RA_FP32 || lse->shape[0] != a.h ||
+      lse->shape[1] < a.s.total || !aligned(lse->data, 4))
+    return RA_ERR_INVALID_ARG;
+  a.lse = static_cast<float*>(lse->data);
+  a.l_sh = lse->stride[0];
+  a.l_ss = lse->stride[1];
+  if (causal != 0 && causal != 1) return RA_ERR_INVALID_ARG;
+  RA_TRY(check_scale(softmax_scale));
+  if (max_kv_len < 0) return RA_ERR_INVALID_ARG;
+  a.causal = causal;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.max_kv = max_kv_len > 0 && max_kv_len < a.s.max_tokens ? max_kv_len : a.s.max_tokens;
+  const size_t need = cache_attn_ws_bytes(a.s.total, a.max_new, a.h, a.hk, a.d, a.s.n_seqs);
+  if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return RA_ERR_WORKSPACE;
+  a.ws = workspace;
+  if (a.s.total == 0) return RA_OK;
+  RA_TRY(dev_ctl(&a.ctl));
+  TimedLaunch tl(RA_KERNEL_CACHE_FWD, static_cast<cudaStream_t>(stream));
+  return cuda_status(launch_cache_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,
+                                      int32_t n_seqs) {
+  if (total < 0 || total > (1 << 30) || max_new < 0 || max_new > total || n_seqs < 1 || n_seqs > 65535) return 0;
+  if (hk < 1 || h < 1 || h > 65535 || h % hk || (d != 64 && d != 128)) return 0;
+  return cache_attn_ws_bytes(total, (int)max_new, (int)h, (int)hk, (int)d, n_seqs);
+}
+
 size_t ring_attn_varlen_workspace_size(int32_t op, int64_t total, int64_t h, int64_t d, int32_t layout,
                                        int32_t n_shards) {
   if (total < 1 || h < 1 || (d != 64 && d != 128) || n_shards < 1 || total % n_shards) return 0;
