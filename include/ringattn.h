@@ -323,10 +323,10 @@ size_t ring_attn_workspace_size(int32_t op, int64_t b, int64_t h, int64_t s, int
  *   the page table and positions as they are when it is replayed.
  * Device data that the host cannot check is checked by the kernels: a page
  * outside [0, n_pages), a length above max_pages * page (or max_kv_len) and a
- * position outside the rotation table are never used; the token counts as
- * masked (or is not written) and RA_ERR_DEVICE is recorded for
- * ring_attn_check_device_error (low byte of info: 0x61 length, 0x62 page, 0x63
- * position). */
+ * position outside the rotation table are never used (nothing out of range is
+ * read or written): RA_ERR_DEVICE is recorded for ring_attn_check_device_error
+ * (low byte of info: 0x61 length, 0x62 page, 0x63 position), a token that has
+ * no place is not stored, and the attention of that sequence is unspecified. */
 typedef struct {
   ra_tensor k, k_scale, v, v_scale;
 } ra_kv_cache;
