@@ -306,7 +306,9 @@ size_t ring_attn_workspace_size(int32_t op, int64_t b, int64_t h, int64_t s, int
  *   contiguous, every other stride of k and v is a multiple of 16 bytes and of
  *   the scales a multiple of d / 16 bytes, base pointers are 16-byte aligned
  *   (k, v) and 8-byte aligned (scales).  Any order of the first three
- *   dimensions is allowed, and k and v may be parts of one allocation.
+ *   dimensions is allowed, and k and v may be parts of one allocation; v has
+ *   k's strides and v_scale k_scale's, and a page's rows of one head lie within
+ *   2 GiB (else RA_ERR_UNSUPPORTED).
  *
  * ra_kv_seqs: the sequences of one call.
  *   page_table: (n_seqs, max_pages) int32 device array, rows page_table_stride

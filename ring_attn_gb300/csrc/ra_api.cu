@@ -971,8 +971,14 @@ static ra_status check_cache(const ra_kv_cache* c, CacheView* v, long long* d) {
   RA_TRY(check_cache_rows(&c->v, RA_E2M1X2, &c->k, *d / 2, 16, 16, &v->v));
   RA_TRY(check_cache_rows(&c->k_scale, RA_E4M3, &c->k, *d / 16, srow, 8, &v->ks));
   RA_TRY(check_cache_rows(&c->v_scale, RA_E4M3, &c->k, *d / 16, srow, 8, &v->vs));
+  // keys and values lie alike, so their rows have the same offsets
+  const CacheRows *a = &v->k, *b = &v->v;
+  for (int i = 0; i < 2; ++i, a = &v->ks, b = &v->vs)
+    if (a->s_page != b->s_page || a->s_head != b->s_head || a->s_row != b->s_row) return RA_ERR_UNSUPPORTED;
   const long long page = c->k.shape[2];
   if (page < 16 || page > 256 || (page & (page - 1))) return RA_ERR_UNSUPPORTED;
+  // offsets inside a page are 32-bit
+  if (v->k.s_row * page > INT32_MAX || v->ks.s_row * page > INT32_MAX) return RA_ERR_UNSUPPORTED;
   v->n_pages = (int)c->k.shape[0];
   v->hk = (int)c->k.shape[1];
   v->page_shift = 0;

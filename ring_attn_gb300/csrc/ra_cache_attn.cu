@@ -35,6 +35,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 32 * kWarps;  // keys per unit
 constexpr float kLift = 8.f;        // log2 of the largest p when M is set
 constexpr float kSlack = 4.f;       // M is raised when a score is this much beyond
+constexpr int kItemCost = 2;
 constexpr float kNone = -3.0e38f;   // M of a row that has seen no key
 
 template <int D, int NT>
@@ -42,17 +43,27 @@ struct Lay {
   static constexpr int R = 8 * NT;
   static constexpr int kK = 0, kV = 32 * D / 2, kKs = 2 * kV, kVs = kKs + 32 * D / 16;
   static constexpr int kStage = kVs + 32 * D / 16;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kOPitch = D + 4;                          // floats per row of a warp's O
-  static constexpr int kMerge = kWarps * R * (kOPitch + 2) * 4;  // reuses the ring
-  static constexpr int kQ = kRing > kMerge ? kRing : kMerge;     // R x D fp16, then R floats
-  static constexpr int kBytes = kQ + R * D * 2 + R * 4;
+  // A warp's results at an item's end: R rows of D floats (padded), M and sums.
+  // With 8 rows they fit into the stage just consumed, so the next item's tiles
+  // stay in flight; with more the ring is drained and reused.
+  static constexpr int kOPitch = D + 4;
+  static constexpr int kResult = R * (kOPitch + 2) * 4;
+  static constexpr bool kFlow = kResult <= kStage;
+  static constexpr int kResultPitch = kFlow ? kStages * kStage : kResult;  // from warp to warp
+  // Queries at an item's start, R x D fp16, then R scales: with 8 rows in the
+  // free stage of warp 0, else behind the ring.  So four blocks fit on an SM.
+  static constexpr int kQ = kRing > kWarps * kResult ? kRing : kWarps * kResult;
+  static constexpr int kBytes = kFlow ? kRing : kQ + R * D * 2 + R * 4;
 };
 
 // Keys of sequence i, its units per (head, row tile) and its row tiles.
 struct SeqWork {
   int len, n_new, units, tiles;
+  // The item's length on the line: starting and finishing one costs about as
+  // much as kItemCost units.
+  __device__ __forceinline__ int cost() const { return units + kItemCost; }
 };
 __device__ __forceinline__ SeqWork seq_work(const CacheAttnArgs& a, int i, int R) {
   SeqWork w;
@@ -60,11 +71,11 @@ __device__ __forceinline__ SeqWork seq_work(const CacheAttnArgs& a, int i, int R
   w.len = __ldg(a.s.lens + i);
   w.len = max(0, min(w.len, a.max_kv));
   w.tiles = (w.n_new * a.G + R - 1) / R;
-  w.units = w.n_new > 0 ? max(1, (w.len + kUnit - 1) / kUnit) : 0;
+  w.units = max(1, (w.len + kUnit - 1) / kUnit);
   return w;
 }
-__device__ __forceinline__ long long total_units(const SeqWork& w, int hk) {
-  return (long long)w.units * w.tiles * hk;
+__device__ __forceinline__ long long line_length(const SeqWork& w, int hk) {
+  return (long long)w.cost() * w.tiles * hk;
 }
 
 // Sum of v over the block (every thread gets it) and the sum over lower threads.
@@ -89,37 +100,101 @@ __device__ __forceinline__ long long block_scan(long long v, long long& below, l
   return all;
 }
 
-// All units of the call.
-__device__ __forceinline__ long long count_units(const CacheAttnArgs& a, int R, long long* sh) {
+// The line's length up to (not including) sequence n.
+__device__ __forceinline__ long long line_to(const CacheAttnArgs& a, int R, int n, long long* sh) {
   long long v = 0, below;
-  for (int i = threadIdx.x; i < a.s.n_seqs; i += kThreads) v += total_units(seq_work(a, i, R), a.hk);
+  for (int i = threadIdx.x; i < n; i += kThreads) v += line_length(seq_work(a, i, R), a.hk);
   return block_scan(v, below, sh);
 }
 
-// The sequence that holds unit u of the line and its first unit (block-wide; u < the total).
-__device__ __forceinline__ int find_seq(const CacheAttnArgs& a, int R, long long u, long long& first, long long* sh) {
+// This block's run [u, u_end) of the line, the sequence in which it starts and
+// where that sequence starts.  False when the run is empty.
+__device__ __forceinline__ bool find_run(const CacheAttnArgs& a, int R, long long& u, long long& u_end, int& seq,
+                                         long long& first, long long* sh) {
   __shared__ int s_seq;
   __shared__ long long s_first;
-  long long base = 0;
-  for (int i0 = 0; i0 < a.s.n_seqs; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const long long v = i < a.s.n_seqs ? total_units(seq_work(a, i, R), a.hk) : 0;
-    long long below;
-    const long long all = block_scan(v, below, sh);
-    if (u >= base + below && u < base + below + v) s_seq = i, s_first = base + below;
-    base += all;
-    if (u < base) break;
+  const bool few = a.s.n_seqs <= kThreads;  // one sequence per thread, read once
+  long long v = 0, below = 0, all;
+  if (few) {
+    if (threadIdx.x < a.s.n_seqs) v = line_length(seq_work(a, threadIdx.x, R), a.hk);
+    all = block_scan(v, below, sh);
+  } else {
+    all = line_to(a, R, a.s.n_seqs, sh);
+  }
+  const long long quota = (all + gridDim.x - 1) / gridDim.x;
+  u = blockIdx.x * quota;
+  u_end = min(all, u + quota);
+  if (u >= u_end) return false;
+  if (few) {
+    if (u >= below && u < below + v) s_seq = threadIdx.x, s_first = below;
+  } else {
+    long long base = 0;
+    for (int i0 = 0; i0 < a.s.n_seqs && base <= u; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      v = i < a.s.n_seqs ? line_length(seq_work(a, i, R), a.hk) : 0;
+      const long long sum = block_scan(v, below, sh);
+      if (u >= base + below && u < base + below + v) s_seq = i, s_first = base + below;
+      base += sum;
+    }
   }
   __syncthreads();
+  seq = s_seq;
   first = s_first;
-  return s_seq;
+  return true;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+// A place on the line that moves unit by unit over the items of [u, u_end).
+struct Cursor {
+  long long left;         // line left in the run, the current unit included; 0: the end
+  SeqWork w;              // the current sequence
+  int seq, item, unit;    // item of the sequence: head * tiles + row tile
+
+  __device__ __forceinline__ void start(const CacheAttnArgs& a, int R, long long u, long long u_end, int s,
+                                        long long first) {
+    seq = s;
+    w = seq_work(a, seq, R);
+    const long long at = u - first;
+    item = (int)(at / w.cost());
+    unit = (int)(at - (long long)item * w.cost()) - kItemCost;
+    left = u_end - u;
+    settle();
+  }
+  // Skips the line that stands for an item's cost.
+  __device__ __forceinline__ void settle() {
+    if (unit < 0) {
+      left = left + unit > 0 ? left + unit : 0;
+      unit = 0;
+    }
+  }
+  // To the next unit; true when that is another item's.
+  __device__ __forceinline__ bool step(const CacheAttnArgs& a, int R) {
+    --left;
+    if (++unit < w.units || left <= 0) return false;
+    unit = -kItemCost;
+    if (++item == w.tiles * a.hk) {
+      item = 0;
+      do {  // (the run ends before the sequences do)
+        w = seq_work(a, ++seq, R);
+      } while (w.tiles == 0);
+    }
+    settle();
+    return true;
+  }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+// zeros unless ok (nothing is read then)
+__device__ __forceinline__ void cp16_or_0(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 template <int N>
-__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool ok) {
+__device__ __forceinline__ void cp_small_or_0(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -179,95 +254,144 @@ __device__ __forceinline__ uint32_t v_offset(int r, int chunk) {
   return slot * (D / 2) + ((D == 128 ? chunk ^ (slot & 2) : chunk) << 4);
 }
 
-// One of a segment's keys tiles: its pages, prefetched, and its copies.
+// A warp's copies: the cursor's unit goes to the ring slot by slot, its pages read
+// one unit ahead.
 template <int D, int NT>
 struct Stream {
   using L = Lay<D, NT>;
   const CacheAttnArgs& a;
-  const int* table;
-  int head, len, pa, pb;
-  uint32_t ring;
+  Cursor c;
+  const int* table;                   // the sequence's page table
+  int pa, pb, k0;                     // pages of the warp's keys [k0, k0 + 16) and the 16 after them
+  const uint8_t *kc, *vc, *ks, *vs;   // the head's rows, this lane's part of the offset included
+  int step_c;                         // bytes between this lane's code chunks
+  uint32_t to, end, slot0;            // ring slot, the ring's end and start
 
-  __device__ __forceinline__ Stream(const CacheAttnArgs& args, int seq, int h, int n, uint32_t r)
-      : a(args), table(args.s.table + (long long)seq * args.s.table_stride), head(h), len(n), pa(0), pb(0), ring(r) {}
-
-  __device__ __forceinline__ void pages(int k0) {
-    if (k0 < len) {
+  __device__ __forceinline__ Stream(const CacheAttnArgs& args, const Cursor& at, uint32_t ring)
+      : a(args), c(at), pa(0), pb(0), to(ring), end(ring + L::kStages * L::kStage), slot0(ring) {
+    constexpr int CPR = D / 32;
+    step_c = (int)a.c.k.s_row * (32 / CPR);
+    item();
+    pages();
+  }
+  // The item's page table and head (a cursor moves to another item rarely).
+  __device__ __forceinline__ void item() {
+    const int lane = threadIdx.x & 31, head = c.item / c.w.tiles;
+    constexpr int CPR = D / 32;  // 16-byte chunks per row
+    const long long oc = head * a.c.k.s_head + (lane / CPR) * a.c.k.s_row + lane % CPR * 16;
+    const long long os = head * a.c.ks.s_head + lane * a.c.ks.s_row;
+    kc = a.c.k.data + oc, vc = a.c.v.data + oc;
+    ks = a.c.ks.data + os, vs = a.c.vs.data + os;
+    table = a.s.table + (long long)c.seq * a.s.table_stride;
+  }
+  __device__ __forceinline__ void pages() {
+    k0 = c.unit * kUnit + (threadIdx.x >> 5) * 32;
+    if (c.left > 0 && k0 < c.w.len) {
       pa = __ldg(table + (k0 >> a.c.page_shift));
-      pb = k0 + 16 < len ? __ldg(table + ((k0 + 16) >> a.c.page_shift)) : pa;
+      if (a.c.page_shift == 4) pb = k0 + 16 < c.w.len ? __ldg(table + (k0 >> 4) + 1) : pa;
     }
   }
-  __device__ __forceinline__ void load(int k0, int slot) {
-    if (k0 < len) {
-      const int lane = threadIdx.x & 31;
-      const bool oka = (unsigned)pa < (unsigned)a.c.n_pages, okb = (unsigned)pb < (unsigned)a.c.n_pages;
-      if (!(oka && okb) && lane == 0) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_PAGE);
-      const int xa = oka ? pa : 0, xb = okb ? pb : 0, mask = (1 << a.c.page_shift) - 1;
-      const uint32_t dst = ring + slot * L::kStage;
-      constexpr int CPR = D / 32;  // 16-byte chunks per row
-#pragma unroll
-      for (int j = 0; j < CPR; ++j) {
-        const int r = j * (32 / CPR) + lane / CPR, c = lane % CPR;
-        const bool ok = k0 + r < len && (j < CPR / 2 ? oka : okb);
-        const int pg = j < CPR / 2 ? xa : xb, row = (k0 + r) & mask;
-        cp16(dst + L::kK + r * (D / 2) + c * 16, a.c.k.data + row_offset(a.c.k, pg, head, row) + c * 16, ok);
-        cp16(dst + L::kV + v_offset<D>(r, c), a.c.v.data + row_offset(a.c.v, pg, head, row) + c * 16, ok);
+  // Copies the unit (nothing at the end of the run) and moves on.
+  __device__ __forceinline__ void load() {
+    if (c.left > 0) {
+      if (k0 < c.w.len) {
+        if (a.c.page_shift > 4 && k0 + 32 <= c.w.len && (unsigned)pa < (unsigned)a.c.n_pages)
+          copy_full();
+        else
+          copy_part();
       }
-      const int pg = lane < 16 ? xa : xb, row = (k0 + lane) & mask;
-      const bool ok = k0 + lane < len && (lane < 16 ? oka : okb);
-      cp_small<D / 16>(dst + L::kKs + lane * (D / 16), a.c.ks.data + row_offset(a.c.ks, pg, head, row), ok);
-      cp_small<D / 16>(dst + L::kVs + lane * (D / 16), a.c.vs.data + row_offset(a.c.vs, pg, head, row), ok);
+      if (c.step(a, L::R)) item();
+      pages();
     }
     cp_commit();
+    to += L::kStage;
+    if (to == end) to = slot0;
+  }
+  // 32 keys of one page
+  __device__ __forceinline__ void copy_full() {
+    const int lane = threadIdx.x & 31, row = k0 & ((1 << a.c.page_shift) - 1);
+    constexpr int CPR = D / 32, RPJ = 32 / CPR;  // rows per step
+    const long long o = (long long)pa * a.c.k.s_page + row * (int)a.c.k.s_row;
+    const uint8_t *k = kc + o, *v = vc + o;
+#pragma unroll
+    for (int j = 0; j < CPR; ++j) {
+      const int r = j * RPJ + lane / CPR, ch = lane % CPR;
+      cp16(to + L::kK + r * (D / 2) + ch * 16, k + j * step_c);
+      cp16(to + L::kV + v_offset<D>(r, ch), v + j * step_c);
+    }
+    const long long os = (long long)pa * a.c.ks.s_page + row * (int)a.c.ks.s_row;
+    cp_small<D / 16>(to + L::kKs + lane * (D / 16), ks + os);
+    cp_small<D / 16>(to + L::kVs + lane * (D / 16), vs + os);
+  }
+  // Fewer keys, two pages or a page that is none: the other rows are zeros.
+  __device__ __forceinline__ void copy_part() {
+    const int lane = threadIdx.x & 31, len = c.w.len, mask = (1 << a.c.page_shift) - 1;
+    if (a.c.page_shift > 4) pb = pa;
+    const bool oka = (unsigned)pa < (unsigned)a.c.n_pages, okb = (unsigned)pb < (unsigned)a.c.n_pages;
+    if (!(oka && okb) && lane == 0) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_PAGE);
+    constexpr int CPR = D / 32, RPJ = 32 / CPR;
+#pragma unroll 1
+    for (int j = 0; j <= CPR; ++j) {  // the last turn copies the scales
+      const int r = j < CPR ? j * RPJ + lane / CPR : lane, ch = lane % CPR;
+      const bool ok = k0 + r < len && (r < 16 ? oka : okb);
+      const int page = ok ? (r < 16 ? pa : pb) : 0, row = (k0 + r) & mask;
+      if (j < CPR) {
+        const long long o = (long long)page * a.c.k.s_page + (row - lane / CPR) * (long long)a.c.k.s_row;
+        cp16_or_0(to + L::kK + r * (D / 2) + ch * 16, kc + o, ok);
+        cp16_or_0(to + L::kV + v_offset<D>(r, ch), vc + o, ok);
+      } else {
+        const long long o = (long long)page * a.c.ks.s_page + (row - lane) * (long long)a.c.ks.s_row;
+        cp_small_or_0<D / 16>(to + L::kKs + lane * (D / 16), ks + o, ok);
+        cp_small_or_0<D / 16>(to + L::kVs + lane * (D / 16), vs + o, ok);
+      }
+    }
   }
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache_attn_kernel(const CacheAttnArgs a) {
   using L = Lay<D, NT>;
   constexpr int R = L::R, KS = D / 16;  // contraction steps of S, row tiles of O^T
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ long long sh[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t sb = smem_u32(smem), ring = sb + warp * L::kStages * L::kStage;
-  __half* sq = reinterpret_cast<__half*>(smem + L::kQ);
-  float* sscale = reinterpret_cast<float*>(smem + L::kQ + R * D * 2);
 
-  const long long all = count_units(a, R, sh);
-  const long long quota = (all + gridDim.x - 1) / gridDim.x;
-  long long u = blockIdx.x * quota;
-  const long long u_end = min(all, u + quota);
-  if (u >= u_end) return;
-  long long first;
-  int seq = find_seq(a, R, u, first, sh);
-  SeqWork w = seq_work(a, seq, R);
-  if (threadIdx.x == 0 && __ldg(a.s.lens + seq) > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+  long long u, u_end, first;
+  int seq0;
+  if (!find_run(a, R, u, u_end, seq0, first, sh)) return;
+  Cursor c;
+  c.start(a, R, u, u_end, seq0, first);
+  Stream<D, NT> st(a, c, ring);
+  uint32_t slot = 0;
+  int seen = -1;
 
-  while (u < u_end) {
+  while (c.left > 0) {
     // ---------------------------------------------------------------- the next item
-    while (u - first >= total_units(w, a.hk)) {
-      first += total_units(w, a.hk);
-      w = seq_work(a, ++seq, R);
-      if (threadIdx.x == 0 && __ldg(a.s.lens + seq) > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
-    }
-    const int item = (int)((u - first) / w.units), ua = (int)((u - first) % w.units);
-    const int ub = (int)min((long long)w.units, ua + (u_end - u));
-    const int head = item / w.tiles, row0 = (item % w.tiles) * R;
+    const SeqWork w = c.w;
+    const int seq = c.seq, ua = c.unit, n_it = (int)min((long long)(w.units - ua), c.left);
+    const int head = c.item / w.tiles, row0 = (c.item % w.tiles) * R;
     const int cu0 = __ldg(a.s.cu + seq), rows = min(R, w.n_new * a.G - row0);
-    const int n_it = ub - ua, kbase = ua * kUnit + warp * 32;
-
-    Stream<D, NT> st(a, seq, head, w.len, ring);
-    st.pages(kbase);
+    if (seq != seen && threadIdx.x == 0 && __ldg(a.s.lens + seq) > a.max_kv)
+      record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+    if (!L::kFlow || seen < 0) {
+      if (seen >= 0) {  // the ring was drained: the copies go on from here
+        st.c = c;
+        st.to = ring;
+        slot = 0;
+        st.item();
+        st.pages();
+      }
+      if (!L::kFlow) st.c.left = n_it;  // and only to the item's end
 #pragma unroll
-    for (int s = 0; s < L::kStages - 1; ++s) {
-      if (s < n_it)
-        st.load(kbase + s * kUnit, s);
-      else
-        cp_commit();
-      if (s + 1 < n_it) st.pages(kbase + (s + 1) * kUnit);
+      for (int s = 0; s < L::kStages - 1; ++s) st.load();
     }
+    seen = seq;
 
     // ---------------------------------------------------------------- queries
+    const int q_at = L::kFlow ? (int)(st.to - ring) : L::kQ;  // the slot that the next copies go to
+    __half* sq = reinterpret_cast<__half*>(smem + q_at);
+    float* sscale = reinterpret_cast<float*>(smem + q_at + R * D * 2);
     {
       constexpr int LPR = D / 8;  // lanes per row
       for (int r = threadIdx.x / LPR; r < R; r += kThreads / LPR) {
@@ -299,15 +423,22 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
       }
     }
     __syncthreads();
-    uint32_t qb[NT][KS][2];
+    // the fragments of Q^T: in registers, or read where they are used when there are many
+    constexpr bool kQReg = NT == 1;
+    uint32_t qb[kQReg ? NT : 1][KS][2];
+    auto q_frag = [&](int n, int s) {
+      return *reinterpret_cast<const uint2*>(sq + (8 * n + g) * D + (D / 4) * t + 4 * s);
+    };
     float sc[NT][2];
     int end[NT][2], min_end = w.len;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      if constexpr (kQReg) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint2 v = *reinterpret_cast<const uint2*>(sq + (8 * n + g) * D + (D / 4) * t + 4 * s);
-        qb[n][s][0] = v.x, qb[n][s][1] = v.y;
+        for (int s = 0; s < KS; ++s) {
+          const uint2 v = q_frag(n, s);
+          qb[n][s][0] = v.x, qb[n][s][1] = v.y;
+        }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -318,6 +449,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
       }
     }
     if (a.causal) min_end = min(w.len, w.len - w.n_new + row0 / a.G + 1);
+    if (L::kFlow) __syncthreads();
 
     // ---------------------------------------------------------------- keys
     float o[NT][KS][4], M[NT][2], l[NT][2];
@@ -328,19 +460,16 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
       M[n][0] = M[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
     }
+    uint32_t stg = 0;
     for (int it = 0; it < n_it; ++it) {
       cp_wait<L::kStages - 2>();
       __syncwarp();
-      const int nx = it + L::kStages - 1;
-      if (nx < n_it) {
-        st.load(kbase + nx * kUnit, nx % L::kStages);
-        if (nx + 1 < n_it) st.pages(kbase + (nx + 1) * kUnit);
-      } else {
-        cp_commit();
-      }
-      const int k0 = kbase + it * kUnit;
+      st.load();
+      const int k0 = (ua + it) * kUnit + warp * 32;
+      stg = ring + slot * L::kStage;
+      if (++slot == L::kStages) slot = 0;
+      c.step(a, R);
       if (k0 >= w.len) continue;
-      const uint32_t stg = ring + (it % L::kStages) * L::kStage;
       // scores of 32 keys: rows g, g + 8 of two tiles
       float s[2][NT][4];
 #pragma unroll
@@ -372,18 +501,27 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
           for (int v = 0; v < 2; ++v) {
             const uint32_t f[4] = {x[2 * v], y[2 * v], x[2 * v + 1], y[2 * v + 1]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(s[mt][n], f, qb[n][2 * wd + v][0], qb[n][2 * wd + v][1]);
+            for (int n = 0; n < NT; ++n) {
+              if constexpr (kQReg) {
+                mma16816(s[mt][n], f, qb[n][2 * wd + v][0], qb[n][2 * wd + v][1]);
+              } else {
+                const uint2 q = q_frag(n, 2 * wd + v);
+                mma16816(s[mt][n], f, q.x, q.y);
+              }
+            }
           }
         }
       }
-      // log2 scores, masked; M is raised only when one of them passes it by far
+      // log2 scores (rounded before M is taken off, so that the largest gives an
+      // exact difference however large it is), masked; M is raised only when one
+      // of them passes it by far
       bool over = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[mt][n][x] *= sc[n][x & 1];
+          for (int x = 0; x < 4; ++x) s[mt][n][x] = __fmul_rn(s[mt][n][x], sc[n][x & 1]);
       if (k0 + 32 > min_end) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -398,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          mx[n][x] = fmaxf(fmaxf(s[0][n][x], s[0][n][x + 2]), fmaxf(s[1][n][x], s[1][n][x + 2]));
+          mx[n][x] = fmaxf(fmax3f(s[0][n][x], s[0][n][x + 2], s[1][n][x]), s[1][n][x + 2]);
           over |= mx[n][x] > M[n][x] + (kLift + kSlack);
         }
       if (__any_sync(0xffffffffu, over)) {
@@ -430,7 +568,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
           float p[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            p[x] = fast_exp2(s[mt][n][x] - M[n][x & 1]);
+            p[x] = fast_exp2(__fsub_rn(s[mt][n][x], M[n][x & 1]));
             l[n][x & 1] += p[x];
           }
           pb[mt][n][0] = transpose8x8(pack_f16x2(p[0], p[1]));
@@ -472,11 +610,17 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
     }
 
     // ---------------------------------------------------------------- the warps' results
-    cp_wait<0>();
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);           // [warp][row][kOPitch]
-    float* sm = so + kWarps * R * L::kOPitch;             // [warp][row] M, then sums
-    float* sl = sm + kWarps * R;
+    if (!L::kFlow) {
+      cp_wait<0>();
+      __syncthreads();
+    } else {
+      __syncwarp();
+    }
+    // warp k's results: R rows of kOPitch floats, then M, then the sums
+    const uint32_t res0 = L::kFlow ? stg - ring : 0;
+    auto result = [&](int k) { return reinterpret_cast<float*>(smem + res0 + k * L::kResultPitch); };
+    constexpr int kM = R * L::kOPitch, kL = kM + R;
+    float* mine = result(warp);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -485,28 +629,29 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
         const int r = 8 * n + 2 * t + x;
-        if (g == 0) sm[warp * R + r] = M[n][x], sl[warp * R + r] = v;
+        if (g == 0) mine[kM + r] = M[n][x], mine[kL + r] = v;
 #pragma unroll
         for (int d = 0; d < KS; ++d)  // head dims D / 8 g + 2 d, + 1 at place 16 d + 2 g
-          *reinterpret_cast<float2*>(so + (warp * R + r) * L::kOPitch + 16 * d + 2 * g) =
+          *reinterpret_cast<float2*>(mine + r * L::kOPitch + 16 * d + 2 * g) =
               make_float2(o[n][d][x], o[n][d][x + 2]);
       }
     }
     __syncthreads();
-    const bool whole = ua == 0 && ub == w.units;
+    const bool whole = n_it == w.units;
     float* part = static_cast<float*>(a.ws) + ((long long)blockIdx.x * 2 + (ua > 0 ? 0 : 1)) * R * (D + 2);
     for (int e = threadIdx.x; e < rows * (D / 2); e += kThreads) {
       const int r = e / (D / 2), d = e % (D / 2) * 2;
       const int at = (d % (D / 8)) / 2 * 16 + d / (D / 8) * 2;
-      float m = sm[r];
+      float m = result(0)[kM + r];
 #pragma unroll
-      for (int k = 1; k < kWarps; ++k) m = fmaxf(m, sm[k * R + r]);
+      for (int k = 1; k < kWarps; ++k) m = fmaxf(m, result(k)[kM + r]);
       float lsum = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float f = fast_exp2(sm[k * R + r] - m);
-        const float2 v = *reinterpret_cast<const float2*>(so + (k * R + r) * L::kOPitch + at);
-        lsum += sl[k * R + r] * f;
+        const float* res = result(k);
+        const float f = fast_exp2(res[kM + r] - m);
+        const float2 v = *reinterpret_cast<const float2*>(res + r * L::kOPitch + at);
+        lsum += res[kL + r] * f;
         o0 += v.x * f, o1 += v.y * f;
       }
       if (!whole) {
@@ -526,7 +671,6 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnArg
       }
     }
     __syncthreads();
-    u += n_it;
   }
 }
 
@@ -539,16 +683,14 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const CacheAttnArg
   __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tok = blockIdx.x, hd = blockIdx.y;
-  const long long all = count_units(a, R, sh);
+  const long long all = line_to(a, R, a.s.n_seqs, sh);
   const long long quota = (all + grid - 1) / grid;
   const int seq = segment_of_warp(a.s.cu, a.s.n_seqs, tok);
-  long long v = 0, below;
-  for (int i = threadIdx.x; i < seq; i += kThreads) v += total_units(seq_work(a, i, R), a.hk);
-  const long long first = block_scan(v, below, sh);
+  const long long first = line_to(a, R, seq, sh);
   const SeqWork w = seq_work(a, seq, R);
   const int rr = (tok - __ldg(a.s.cu + seq)) * a.G + hd % a.G, r = rr % R;
-  const long long u0 = first + ((long long)(hd / a.G) * w.tiles + rr / R) * w.units, u1 = u0 + w.units;
-  const long long c0 = u0 / quota, c1 = (u1 - 1) / quota;
+  const long long u0 = first + ((long long)(hd / a.G) * w.tiles + rr / R) * w.cost();
+  const long long c0 = (u0 + kItemCost) / quota, c1 = (u0 + w.cost() - 1) / quota;
   if (c0 == c1) return;
   constexpr int V = D / 32;
   float m = kNone, lsum = 0.f, o[V] = {};
@@ -590,7 +732,7 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const CacheAttnArg
 }
 
 // Blocks that fit on an SM (registers and shared memory), so the grid is one wave.
-int blocks_per_sm(int nt) { return nt == 4 ? 2 : 3; }
+int blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
 // Query rows of an item in units of 8.
 int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }

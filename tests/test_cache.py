@@ -72,6 +72,8 @@ BAD_CACHE = [
     (cache(v=fake((9, 2, 32, 32), ra.RA_E2M1X2, stride=(4096, 2048, 64, 2))), 3),
     (cache(v_scale=fake((9, 2, 32, 4), ra.RA_E4M3, stride=(256, 128, 6, 1))), 3),
     (cache(k_scale=fake((9, 2, 32, 4), ra.RA_E4M3, data=0x100004)), 3),
+    (cache(v=fake((9, 2, 32, 32), ra.RA_E2M1X2, stride=(4096, 2048, 64, 1))), 2),  # not k's strides
+    (cache(k_scale=fake((9, 2, 32, 4), ra.RA_E4M3, stride=(512, 128, 4, 1))), 2),
 ]
 BAD_SEQS = [
     (seqs(page_table=None), 1), (seqs(kv_lens=None), 1), (seqs(cu_seqlens_dev=None), 1), (seqs(cu_seqlens_host=None), 1),
