@@ -1,13 +1,8 @@
 // Attention of few new tokens (decoding, verified proposals) over the paged 4-bit
 // cache: out = softmax(scale q K^T) V with one pass over the keys.
 //
-// Work.  An item is one key / value head of one sequence with up to R = 8 NT of
-// its query rows (row r is token r / G, head r % G of the group).  Its keys are cut
-// into units of 128, all items' units form one line, and each of the grid's blocks
-// takes an equal run of that line (lengths are read from device memory, so a
-// captured launch follows them).  A run that holds an item whole writes its
-// result; pieces of an item go to the workspace as (O, max, sum) and a second
-// kernel joins them in block order, so results do not depend on timing.
+// An item has up to R = 8 NT query rows; the blocks share the items' units as
+// ra_cache_line.cuh says, in one wave.
 //
 // Each of the 4 warps streams its own 32 keys of a unit through a ring of
 // cp.async stages and keeps its own running maximum, sum and O^T; no barrier in
@@ -25,17 +20,16 @@
 //
 // Bound: 0.5625 bytes per number from HBM; the conversions cost about 1.3 lane
 // instructions per number against the 3 that fit into its memory time.
-#include "ra_cache.cuh"
+#include "ra_cache_line.cuh"
 
 namespace ra {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 32 * kWarps;  // keys per unit
+static_assert(kUnit == 32 * kWarps, "32 keys of a unit per warp");
 constexpr float kLift = 8.f;        // log2 of the largest p when M is set
 constexpr float kSlack = 4.f;       // M is raised when a score is this much beyond
-constexpr int kItemCost = 2;
 constexpr float kNone = -3.0e38f;   // M of a row that has seen no key
 
 template <int D, int NT>
@@ -58,127 +52,14 @@ struct Lay {
   static constexpr int kBytes = kFlow ? kRing : kQ + R * D * 2 + R * 4;
 };
 
-// Keys of sequence i, its units per (head, row tile) and its row tiles.
-struct SeqWork {
-  int len, n_new, units, tiles;
-  // The item's length on the line: starting and finishing one costs about as
-  // much as kItemCost units.
-  __device__ __forceinline__ int cost() const { return units + kItemCost; }
-};
-__device__ __forceinline__ SeqWork seq_work(const CacheAttnArgs& a, int i, int R) {
-  SeqWork w;
-  w.n_new = __ldg(a.s.cu + i + 1) - __ldg(a.s.cu + i);
-  w.len = __ldg(a.s.lens + i);
-  w.len = max(0, min(w.len, a.max_kv));
-  w.tiles = (w.n_new * a.G + R - 1) / R;
-  w.units = max(1, (w.len + kUnit - 1) / kUnit);
-  return w;
-}
-__device__ __forceinline__ long long line_length(const SeqWork& w, int hk) {
-  return (long long)w.cost() * w.tiles * hk;
-}
-
-// Sum of v over the block (every thread gets it) and the sum over lower threads.
-__device__ __forceinline__ long long block_scan(long long v, long long& below, long long* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  long long pre = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    pre += w < warp ? sh[w] : 0;
-    all += sh[w];
-  }
-  below = pre + x - v;
-  return all;
-}
-
-// The line's length up to (not including) sequence n.
-__device__ __forceinline__ long long line_to(const CacheAttnArgs& a, int R, int n, long long* sh) {
-  long long v = 0, below;
-  for (int i = threadIdx.x; i < n; i += kThreads) v += line_length(seq_work(a, i, R), a.hk);
-  return block_scan(v, below, sh);
-}
-
-// This block's run [u, u_end) of the line, the sequence in which it starts and
-// where that sequence starts.  False when the run is empty.
-__device__ __forceinline__ bool find_run(const CacheAttnArgs& a, int R, long long& u, long long& u_end, int& seq,
-                                         long long& first, long long* sh) {
-  __shared__ int s_seq;
-  __shared__ long long s_first;
-  const bool few = a.s.n_seqs <= kThreads;  // one sequence per thread, read once
-  long long v = 0, below = 0, all;
-  if (few) {
-    if (threadIdx.x < a.s.n_seqs) v = line_length(seq_work(a, threadIdx.x, R), a.hk);
-    all = block_scan(v, below, sh);
-  } else {
-    all = line_to(a, R, a.s.n_seqs, sh);
-  }
-  const long long quota = (all + gridDim.x - 1) / gridDim.x;
-  u = blockIdx.x * quota;
-  u_end = min(all, u + quota);
-  if (u >= u_end) return false;
-  if (few) {
-    if (u >= below && u < below + v) s_seq = threadIdx.x, s_first = below;
-  } else {
-    long long base = 0;
-    for (int i0 = 0; i0 < a.s.n_seqs && base <= u; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      v = i < a.s.n_seqs ? line_length(seq_work(a, i, R), a.hk) : 0;
-      const long long sum = block_scan(v, below, sh);
-      if (u >= base + below && u < base + below + v) s_seq = i, s_first = base + below;
-      base += sum;
-    }
-  }
-  __syncthreads();
-  seq = s_seq;
-  first = s_first;
-  return true;
-}
-
-// A place on the line that moves unit by unit over the items of [u, u_end).
-struct Cursor {
-  long long left;         // line left in the run, the current unit included; 0: the end
-  SeqWork w;              // the current sequence
-  int seq, item, unit;    // item of the sequence: head * tiles + row tile
-
-  __device__ __forceinline__ void start(const CacheAttnArgs& a, int R, long long u, long long u_end, int s,
-                                        long long first) {
-    seq = s;
-    w = seq_work(a, seq, R);
-    const long long at = u - first;
-    item = (int)(at / w.cost());
-    unit = (int)(at - (long long)item * w.cost()) - kItemCost;
-    left = u_end - u;
-    settle();
-  }
-  // Skips the line that stands for an item's cost.
-  __device__ __forceinline__ void settle() {
-    if (unit < 0) {
-      left = left + unit > 0 ? left + unit : 0;
-      unit = 0;
-    }
-  }
-  // To the next unit; true when that is another item's.
-  __device__ __forceinline__ bool step(const CacheAttnArgs& a, int R) {
-    --left;
-    if (++unit < w.units || left <= 0) return false;
-    unit = -kItemCost;
-    if (++item == w.tiles * a.hk) {
-      item = 0;
-      do {  // (the run ends before the sequences do)
-        w = seq_work(a, ++seq, R);
-      } while (w.tiles == 0);
-    }
-    settle();
-    return true;
+// Cost in units: starting and finishing an item costs about as much as kItemCost.
+template <int NT>
+struct FewRows {
+  static constexpr int R = 8 * NT, kItemCost = 2;
+  static __device__ __forceinline__ void cost(const CacheAttnArgs&, LineSeq& s) {
+    s.per = 1;
+    s.a = max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
+    s.b = 0;
   }
 };
 
@@ -208,6 +89,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// a where the mask has ones, else b
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(mask));
+  return r;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -260,48 +147,57 @@ template <int D, int NT>
 struct Stream {
   using L = Lay<D, NT>;
   const CacheAttnArgs& a;
-  Cursor c;
+  LinePos at;
+  long long run_end;
+  int unit, unit_end, len;            // the units to come of a piece, and its sequence's keys
   const int* table;                   // the sequence's page table
   int pa, pb, k0;                     // pages of the warp's keys [k0, k0 + 16) and the 16 after them
   const uint8_t *kc, *vc, *ks, *vs;   // the head's rows, this lane's part of the offset included
   int step_c;                         // bytes between this lane's code chunks
   uint32_t to, end, slot0;            // ring slot, the ring's end and start
 
-  __device__ __forceinline__ Stream(const CacheAttnArgs& args, const Cursor& at, uint32_t ring)
-      : a(args), c(at), pa(0), pb(0), to(ring), end(ring + L::kStages * L::kStage), slot0(ring) {
+  __device__ __forceinline__ Stream(const CacheAttnArgs& args, long long e, uint32_t ring)
+      : a(args), run_end(e), unit(0), unit_end(0), pa(0), pb(0), to(ring),
+        end(ring + L::kStages * L::kStage), slot0(ring) {
     constexpr int CPR = D / 32;
     step_c = (int)a.c.k.s_row * (32 / CPR);
-    item();
-    pages();
   }
-  // The item's page table and head (a cursor moves to another item rarely).
-  __device__ __forceinline__ void item() {
-    const int lane = threadIdx.x & 31, head = c.item / c.w.tiles;
+  // The next piece of the run, if there is one.
+  __device__ __forceinline__ void follow() {
+    Piece x;
+    if (next_piece<FewRows<NT>>(a, at, run_end, x)) piece(x);
+  }
+  __device__ __forceinline__ void piece(const Piece& x) {
+    const int lane = threadIdx.x & 31, head = x.head;
+    unit = x.ua, unit_end = x.ub, len = x.len;
     constexpr int CPR = D / 32;  // 16-byte chunks per row
     const long long oc = head * a.c.k.s_head + (lane / CPR) * a.c.k.s_row + lane % CPR * 16;
     const long long os = head * a.c.ks.s_head + lane * a.c.ks.s_row;
     kc = a.c.k.data + oc, vc = a.c.v.data + oc;
     ks = a.c.ks.data + os, vs = a.c.vs.data + os;
-    table = a.s.table + (long long)c.seq * a.s.table_stride;
+    table = a.s.table + (long long)x.seq * a.s.table_stride;
+    pages();
   }
   __device__ __forceinline__ void pages() {
-    k0 = c.unit * kUnit + (threadIdx.x >> 5) * 32;
-    if (c.left > 0 && k0 < c.w.len) {
+    k0 = unit * kUnit + (threadIdx.x >> 5) * 32;
+    if (k0 < len) {
       pa = __ldg(table + (k0 >> a.c.page_shift));
-      if (a.c.page_shift == 4) pb = k0 + 16 < c.w.len ? __ldg(table + (k0 >> 4) + 1) : pa;
+      if (a.c.page_shift == 4) pb = k0 + 16 < len ? __ldg(table + (k0 >> 4) + 1) : pa;
     }
   }
-  // Copies the unit (nothing at the end of the run) and moves on.
+  // Copies the unit (nothing when none is left) and moves on, to the run's next piece with kFlow.
   __device__ __forceinline__ void load() {
-    if (c.left > 0) {
-      if (k0 < c.w.len) {
-        if (a.c.page_shift > 4 && k0 + 32 <= c.w.len && (unsigned)pa < (unsigned)a.c.n_pages)
+    if (unit < unit_end) {
+      if (k0 < len) {
+        if (a.c.page_shift > 4 && k0 + 32 <= len && (unsigned)pa < (unsigned)a.c.n_pages)
           copy_full();
         else
           copy_part();
       }
-      if (c.step(a, L::R)) item();
-      pages();
+      if (++unit < unit_end)
+        pages();
+      else if (L::kFlow)
+        follow();
     }
     cp_commit();
     to += L::kStage;
@@ -325,7 +221,7 @@ struct Stream {
   }
   // Fewer keys, two pages or a page that is none: the other rows are zeros.
   __device__ __forceinline__ void copy_part() {
-    const int lane = threadIdx.x & 31, len = c.w.len, mask = (1 << a.c.page_shift) - 1;
+    const int lane = threadIdx.x & 31, mask = (1 << a.c.page_shift) - 1;
     if (a.c.page_shift > 4) pb = pa;
     const bool oka = (unsigned)pa < (unsigned)a.c.n_pages, okb = (unsigned)pb < (unsigned)a.c.n_pages;
     if (!(oka && okb) && lane == 0) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_PAGE);
@@ -353,40 +249,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
   using L = Lay<D, NT>;
   constexpr int R = L::R, KS = D / 16;  // contraction steps of S, row tiles of O^T
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ long long sh[kWarps];
+  __shared__ LineShared<kWarps> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t sb = smem_u32(smem), ring = sb + warp * L::kStages * L::kStage;
 
-  long long u, u_end, first;
-  int seq0;
-  if (!find_run(a, R, u, u_end, seq0, first, sh)) return;
-  Cursor c;
-  c.start(a, R, u, u_end, seq0, first);
-  Stream<D, NT> st(a, c, ring);
+  LinePos at;
+  long long end_u, quota;
+  JoinNote note = empty_note();
+  if (!find_run<FewRows<NT>, kWarps>(a, at, end_u, quota, sh)) {
+    if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
+    return;
+  }
+  Stream<D, NT> st(a, end_u, ring);
   uint32_t slot = 0;
   int seen = -1;
-
-  while (c.left > 0) {
+  Piece w;
+  while (next_piece<FewRows<NT>>(a, at, end_u, w)) {
     // ---------------------------------------------------------------- the next item
-    const SeqWork w = c.w;
-    const int seq = c.seq, ua = c.unit, n_it = (int)min((long long)(w.units - ua), c.left);
-    const int head = c.item / w.tiles, row0 = (c.item % w.tiles) * R;
-    const int cu0 = __ldg(a.s.cu + seq), rows = min(R, w.n_new * a.G - row0);
-    if (seq != seen && threadIdx.x == 0 && __ldg(a.s.lens + seq) > a.max_kv)
+    const int n_it = w.ub - w.ua, row0 = w.tile * R, cu0 = __ldg(a.s.cu + w.seq), rows = min(R, w.n_new * a.G - row0);
+    if (w.seq != seen && threadIdx.x == 0 && __ldg(a.s.lens + w.seq) > a.max_kv)
       record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
-    if (!L::kFlow || seen < 0) {
-      if (seen >= 0) {  // the ring was drained: the copies go on from here
-        st.c = c;
-        st.to = ring;
-        slot = 0;
-        st.item();
-        st.pages();
-      }
-      if (!L::kFlow) st.c.left = n_it;  // and only to the item's end
+    if (!L::kFlow || seen < 0) {  // a drained ring starts again
+      slot = 0;
+      st.to = ring;
+      st.at = at;
+      st.piece(w);
 #pragma unroll
       for (int s = 0; s < L::kStages - 1; ++s) st.load();
     }
-    seen = seq;
+    seen = w.seq;
 
     // ---------------------------------------------------------------- queries
     const int q_at = L::kFlow ? (int)(st.to - ring) : L::kQ;  // the slot that the next copies go to
@@ -398,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
         const int c = threadIdx.x % LPR, rr = row0 + r;
         uint4 q = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          const int tok = cu0 + rr / a.G, hd = head * a.G + rr % a.G;
+          const int tok = cu0 + rr / a.G, hd = w.head * a.G + rr % a.G;
           q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) + (long long)tok * a.q.s_row +
                                               (long long)hd * a.q.s_head + 8 * c);
         }
@@ -465,10 +356,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
       cp_wait<L::kStages - 2>();
       __syncwarp();
       st.load();
-      const int k0 = (ua + it) * kUnit + warp * 32;
+      const int k0 = (w.ua + it) * kUnit + warp * 32;
       stg = ring + slot * L::kStage;
       if (++slot == L::kStages) slot = 0;
-      c.step(a, R);
       if (k0 >= w.len) continue;
       // scores of 32 keys: rows g, g + 8 of two tiles
       float s[2][NT][4];
@@ -595,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t w0 = v[2 * k][wd], w1 = v[2 * k + 1][wd];
-            e2m1x8_to_f16((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), f[2 * k]);
-            e2m1x8_to_f16(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), f[2 * k + 1]);
+            e2m1x8_to_f16(select_bits(w0, w1 << 4, 0x0f0f0f0fu), f[2 * k]);
+            e2m1x8_to_f16(select_bits(w0 >> 4, w1, 0x0f0f0f0fu), f[2 * k + 1]);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -638,10 +528,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
     }
     __syncthreads();
     const bool whole = n_it == w.units;
-    float* part = static_cast<float*>(a.ws) + ((long long)blockIdx.x * 2 + (ua > 0 ? 0 : 1)) * R * (D + 2);
+    note_piece<FewRows<NT>>(a, w, quota, cu0, note);
+    float* part = slot_of<R, D>(a, gridDim.x, blockIdx.x, w.ua == 0);
     for (int e = threadIdx.x; e < rows * (D / 2); e += kThreads) {
       const int r = e / (D / 2), d = e % (D / 2) * 2;
-      const int at = (d % (D / 8)) / 2 * 16 + d / (D / 8) * 2;
+      const int from = (d % (D / 8)) / 2 * 16 + d / (D / 8) * 2;
       float m = result(0)[kM + r];
 #pragma unroll
       for (int k = 1; k < kWarps; ++k) m = fmaxf(m, result(k)[kM + r]);
@@ -650,85 +541,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
       for (int k = 0; k < kWarps; ++k) {
         const float* res = result(k);
         const float f = fast_exp2(res[kM + r] - m);
-        const float2 v = *reinterpret_cast<const float2*>(res + r * L::kOPitch + at);
+        const float2 v = *reinterpret_cast<const float2*>(res + r * L::kOPitch + from);
         lsum += res[kL + r] * f;
         o0 += v.x * f, o1 += v.y * f;
       }
       if (!whole) {
-        *reinterpret_cast<float2*>(part + r * (D + 2) + 2 + d) = make_float2(o0, o1);
-        if (d == 0) *reinterpret_cast<float2*>(part + r * (D + 2)) = make_float2(m, lsum);
+        *reinterpret_cast<float2*>(part + r * D + d) = make_float2(o0, o1);
+        if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m, lsum);
       } else {
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-        const int rr = row0 + r, tok = cu0 + rr / a.G, hd = head * a.G + rr % a.G;
-        const long long at_o = (long long)tok * a.out.s_row + (long long)hd * a.out.s_head + d;
+        const long long to = out_offset(a, cu0, w.head, row0 + r) + d;
         if (a.out_f32)
-          *reinterpret_cast<float2*>(static_cast<float*>(a.out.data) + at_o) = make_float2(o0 * inv, o1 * inv);
+          *reinterpret_cast<float2*>(static_cast<float*>(a.out.data) + to) = make_float2(o0 * inv, o1 * inv);
         else
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out.data) + at_o) = pack_bf16x2(o0 * inv, o1 * inv);
-        if (d == 0)
-          a.lse[(long long)hd * a.l_sh + (long long)tok * a.l_ss] =
-              lsum > 0.f ? (m + log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out.data) + to) = pack_bf16x2(o0 * inv, o1 * inv);
+        if (d == 0) store_row(a, cu0, w.head, row0 + r, m, lsum);
       }
     }
     __syncthreads();
   }
-}
-
-// Joins the pieces of one query row of one item: the block in which the item
-// begins left its piece in its slot 1, those that begin inside the item in slot 0.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) cache_join_kernel(const CacheAttnArgs a, int grid) {
-  constexpr int R = 8 * NT;
-  __shared__ long long sh[kWarps];
-  __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tok = blockIdx.x, hd = blockIdx.y;
-  const long long all = line_to(a, R, a.s.n_seqs, sh);
-  const long long quota = (all + grid - 1) / grid;
-  const int seq = segment_of_warp(a.s.cu, a.s.n_seqs, tok);
-  const long long first = line_to(a, R, seq, sh);
-  const SeqWork w = seq_work(a, seq, R);
-  const int rr = (tok - __ldg(a.s.cu + seq)) * a.G + hd % a.G, r = rr % R;
-  const long long u0 = first + ((long long)(hd / a.G) * w.tiles + rr / R) * w.cost();
-  const long long c0 = (u0 + kItemCost) / quota, c1 = (u0 + w.cost() - 1) / quota;
-  if (c0 == c1) return;
-  constexpr int V = D / 32;
-  float m = kNone, lsum = 0.f, o[V] = {};
-  for (long long c = c0 + warp; c <= c1; c += kWarps) {
-    const float* part = static_cast<const float*>(a.ws) + ((c * 2 + (c == c0 ? 1 : 0)) * R + r) * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2*>(part);
-    const float to = fmaxf(m, ml.x), f0 = fast_exp2(m - to), f1 = fast_exp2(ml.x - to);
-    m = to;
-    lsum = lsum * f0 + ml.y * f1;
-#pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(part + 2 + lane * V + i);
-      o[i] = o[i] * f0 + x.x * f1;
-      o[i + 1] = o[i + 1] * f0 + x.y * f1;
-    }
-  }
-  if (lane == 0) sm[warp] = m, sl[warp] = lsum;
-#pragma unroll
-  for (int i = 0; i < V; ++i) so[warp][lane * V + i] = o[i];
-  __syncthreads();
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float mm = sm[0];
-    for (int k = 1; k < kWarps; ++k) mm = fmaxf(mm, sm[k]);
-    float ls = 0.f, x = 0.f;
-    for (int k = 0; k < kWarps; ++k) {
-      const float f = fast_exp2(sm[k] - mm);
-      ls += sl[k] * f;
-      x += so[k][d] * f;
-    }
-    x *= ls > 0.f ? 1.f / ls : 0.f;
-    const long long at = (long long)tok * a.out.s_row + (long long)hd * a.out.s_head + d;
-    if (a.out_f32)
-      static_cast<float*>(a.out.data)[at] = x;
-    else
-      static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16(x);
-    if (d == 0)
-      a.lse[(long long)hd * a.l_sh + (long long)tok * a.l_ss] = ls > 0.f ? (mm + log2f(ls)) * 0.6931471805599453f : -INFINITY;
-  }
+  if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
 }
 
 // Blocks that fit on an SM (registers and shared memory), so the grid is one wave.
@@ -746,15 +578,15 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cache_attn_kernel<D, NT><<<grid, kThreads, L::kBytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache_join_kernel<D, NT><<<dim3((unsigned)a.s.total, (unsigned)a.h), kThreads, 0, st>>>(a, grid);
+  cache_join_kernel<L::R, D><<<dim3(grid, NT), 256 * kJoinGroups, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
-  const int nt = row_tiles((long long)max_new * (h / hk));
-  return (size_t)num_sms() * blocks_per_sm(nt) * 2 * 8 * nt * (d + 2) * sizeof(float);
+  const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * blocks_per_sm(nt);
+  return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {

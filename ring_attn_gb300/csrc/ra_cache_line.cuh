@@ -1,0 +1,329 @@
+// How the attention over the paged cache is shared out.
+//
+// An item is one key / value head of one sequence with R of its query rows (row r
+// of the sequence is token r / G, head r % G of the group): a row tile.  Its keys
+// are cut into units of 128.  All items lie one after the other on a line, each
+// with a length that stands for its cost, and each block of the grid takes an
+// equal run of the line: the units of an item go to the blocks in order.
+// The lengths are read from device memory, so a captured launch follows them.
+//
+// A piece that holds all units of its item is written as the result.  The other
+// pieces go to the workspace, two slots per block: slot 1 for a piece that holds
+// its item's first unit (at most the last of the block), slot 0 for one that does not
+// (at most the first).  A note per block says which slots it filled and where the
+// item of slot 1 ends, so the kernel that joins the pieces, in block order, needs
+// no plan of its own.
+#pragma once
+
+#include "ra_cache.cuh"
+
+namespace ra {
+
+constexpr int kUnit = 128;
+
+// Quotient of non-negative numbers, by the short division where they are small.
+__device__ __forceinline__ long long quotient(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
+  return n / d;
+}
+
+// One sequence: its row tiles' costs are a + b * tile places; `per` places stand
+// for a unit, after kItemCost units' worth for starting and finishing the item.
+struct LineSeq {
+  int len, n_new, tiles, per;
+  long long a, b;
+  __device__ __forceinline__ long long before(int tile) const {
+    return a * tile + b * ((long long)tile * (tile - 1) / 2);
+  }
+};
+
+// Kind: R, kItemCost and the cost rule `static void cost(args, LineSeq&)`.
+template <class Kind>
+__device__ __forceinline__ LineSeq line_seq(const CacheAttnArgs& g, int i) {
+  LineSeq s;
+  s.n_new = __ldg(g.s.cu + i + 1) - __ldg(g.s.cu + i);
+  s.len = max(0, min(__ldg(g.s.lens + i), g.max_kv));
+  s.tiles = (int)(((long long)s.n_new * g.G + Kind::R - 1) / Kind::R);
+  Kind::cost(g, s);
+  return s;
+}
+template <class Kind>
+__device__ __forceinline__ long long line_length(const CacheAttnArgs& g, const LineSeq& s) {
+  return g.hk * s.before(s.tiles);
+}
+
+// Keys that the rows of a tile see, the last one's, in units (at least one: a row without
+// keys is written too).
+template <class Kind>
+__device__ __forceinline__ int tile_units(const CacheAttnArgs& g, const LineSeq& s, int tile) {
+  int end = s.len;
+  if (g.causal) {
+    const int last = (int)min((long long)s.n_new - 1, ((long long)tile * Kind::R + Kind::R - 1) / g.G);
+    end = min(end, s.len - s.n_new + last + 1);
+  }
+  return max(1, (end + kUnit - 1) / kUnit);
+}
+
+// The unit at place p of an item of `units` units (p = cost: the end).  The cost
+// may be a few units off, so that it is linear: the last block takes the rest.
+template <class Kind>
+__device__ __forceinline__ int unit_at(long long p, int units, long long cost, int per) {
+  if (p >= cost) return units;
+  const long long u = (per == 1 ? p : quotient(p, per)) - Kind::kItemCost;
+  return (int)min((long long)units, max(0LL, u));
+}
+
+// Sum of v over the block (every thread gets it) and the sum over lower threads.
+template <int WARPS>
+__device__ __forceinline__ long long block_scan(long long v, long long& below, long long* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  long long pre = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    pre += w < warp ? sh[w] : 0;
+    all += sh[w];
+  }
+  below = pre + x - v;
+  return all;
+}
+
+// Shared memory of find_run.
+template <int WARPS>
+struct LineShared {
+  long long sums[WARPS], first;
+  int seq;
+};
+
+// A place on the line: position, sequence and where that sequence begins.
+struct LinePos {
+  long long u, first;
+  int seq;
+};
+
+// This block's run [at.u, end) of the line, found by the whole thread block.  False when it is empty.
+template <class Kind, int WARPS>
+__device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, long long& end, long long& quota,
+                                         LineShared<WARPS>& sh) {
+  constexpr int T = 32 * WARPS;
+  const bool few = g.s.n_seqs <= T;  // one sequence per thread, read once
+  const int tid = threadIdx.x;
+  long long v = 0, below = 0, all;
+  if (few) {
+    if (tid < g.s.n_seqs) v = line_length<Kind>(g, line_seq<Kind>(g, tid));
+  } else {
+    for (int i = tid; i < g.s.n_seqs; i += T) v += line_length<Kind>(g, line_seq<Kind>(g, i));
+  }
+  all = block_scan<WARPS>(v, below, sh.sums);
+  quota = quotient(all + gridDim.x - 1, gridDim.x);
+  at.u = blockIdx.x * quota;
+  end = min(all, at.u + quota);
+  if (at.u >= end) return false;
+  if (few) {
+    if (at.u >= below && at.u < below + v) sh.seq = tid, sh.first = below;
+  } else {
+    long long base = 0;
+    for (int i0 = 0; i0 < g.s.n_seqs && base <= at.u; i0 += T) {
+      const int i = i0 + tid;
+      v = i < g.s.n_seqs ? line_length<Kind>(g, line_seq<Kind>(g, i)) : 0;
+      const long long sum = block_scan<WARPS>(v, below, sh.sums);
+      if (at.u >= base + below && at.u < base + below + v) sh.seq = i, sh.first = base + below;
+      base += sum;
+    }
+  }
+  __syncthreads();
+  at.seq = sh.seq;
+  at.first = sh.first;
+  return true;
+}
+
+// An item and a range of its units.
+struct Piece {
+  int seq, head, tile, len, n_new, units, ua, ub, per;
+  long long start, cost;  // place of the item on the line
+};
+
+// The item at the place (which is on the line).
+template <class Kind>
+__device__ __forceinline__ void item_at(const CacheAttnArgs& g, const LinePos& at, const LineSeq& s, Piece& x) {
+  const long long per = s.before(s.tiles);
+  long long q = at.u - at.first;
+  x.head = (int)quotient(q, per);
+  q -= x.head * per;
+  int lo = 0;
+  if (s.b == 0) {
+    lo = (int)quotient(q, s.a);
+  } else {
+    int hi = s.tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.before(mid) <= q)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+  }
+  x.tile = lo;
+  x.cost = s.a + s.b * lo;
+  x.start = at.first + x.head * per + s.before(lo);
+  x.seq = at.seq;
+  x.len = s.len;
+  x.n_new = s.n_new;
+  x.per = s.per;
+  x.units = tile_units<Kind>(g, s, lo);
+}
+
+// The next piece of the run that ends at `end`, moving `at` behind it.  False at the run's end.
+template <class Kind>
+__device__ __forceinline__ bool next_piece(const CacheAttnArgs& g, LinePos& at, long long end, Piece& x) {
+  while (at.u < end) {
+    LineSeq s = line_seq<Kind>(g, at.seq);
+    for (long long n = line_length<Kind>(g, s); at.u - at.first >= n; n = line_length<Kind>(g, s)) {
+      at.first += n;
+      s = line_seq<Kind>(g, ++at.seq);
+    }
+    item_at<Kind>(g, at, s, x);
+    const long long p0 = at.u - x.start, p1 = min(x.cost, p0 + (end - at.u));
+    x.ua = unit_at<Kind>(p0, x.units, x.cost, x.per);
+    x.ub = unit_at<Kind>(p1, x.units, x.cost, x.per);
+    at.u += p1 - p0;
+    if (x.ua < x.ub) return true;
+  }
+  return false;
+}
+
+// What the joining kernel reads of a block: whether slot 0 is filled, and of the
+// item in slot 1 (last < 0: none) the last block that shares it, its first row and
+// the sequence's rows, first token row and head.
+struct __align__(16) JoinNote {
+  int slot0, last, row0, rows, cu0, head, pad[2];
+};
+template <class Kind>
+__device__ __forceinline__ void note_piece(const CacheAttnArgs& g, const Piece& x, long long quota, int cu0,
+                                           JoinNote& n) {
+  if (x.ub - x.ua == x.units) return;
+  if (x.ua > 0) {
+    n.slot0 = 1;
+  } else {
+    n.last = (int)quotient(x.start + x.cost - 1, quota);
+    n.row0 = x.tile * Kind::R;
+    n.rows = x.n_new * g.G;
+    n.cu0 = cu0;
+    n.head = x.head;
+  }
+}
+__device__ __forceinline__ JoinNote empty_note() { return JoinNote{0, -1, 0, 0, 0, 0, {0, 0}}; }
+__device__ __forceinline__ JoinNote* notes_of(const CacheAttnArgs& g) { return static_cast<JoinNote*>(g.ws); }
+
+// A workspace slot, behind the notes: R rows of D sums, then R (offset M, sum of weights) pairs; the
+// weights are 2^(score - M) and rows without keys have a zero sum.
+template <int R, int D>
+__host__ __device__ constexpr long long slot_floats() {
+  return (long long)R * (D + 2);
+}
+template <int R, int D>
+__device__ __forceinline__ float* slot_of(const CacheAttnArgs& g, int grid, int block, bool begins) {
+  return reinterpret_cast<float*>(notes_of(g) + grid) + ((long long)block * 2 + (begins ? 1 : 0)) * slot_floats<R, D>();
+}
+template <int R>
+size_t line_ws_bytes(int grid, int d) {
+  return (size_t)grid * (sizeof(JoinNote) + 2 * R * (d + 2) * sizeof(float));
+}
+
+__device__ __forceinline__ void store_row(const CacheAttnArgs& g, int cu0, int head, int row, float M, float sum) {
+  const int tok = cu0 + row / g.G, hd = head * g.G + row % g.G;
+  g.lse[(long long)hd * g.l_sh + (long long)tok * g.l_ss] =
+      sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+__device__ __forceinline__ long long out_offset(const CacheAttnArgs& g, int cu0, int head, int row) {
+  return (long long)(cu0 + row / g.G) * g.out.s_row + (long long)(head * g.G + row % g.G) * g.out.s_head;
+}
+
+// Joins the item in slot 1 of block blockIdx.x, if there is one: rows [8 blockIdx.y,
+// 8 blockIdx.y + 8) of its tile, kJoinGroups warps each, which take the pieces in turn.
+constexpr int kJoinGroups = 2;
+template <int R, int D>
+__global__ void __launch_bounds__(32 * 8 * kJoinGroups) cache_join_kernel(const CacheAttnArgs g) {
+  constexpr int V = D / 32;
+  __shared__ float so[8][D], sm[8][2];
+  const JoinNote* notes = notes_of(g);
+  const JoinNote n = notes[blockIdx.x];
+  if (n.last < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp >> 3;
+  const int r = blockIdx.y * 8 + (warp & 7), row = n.row0 + r, grid = gridDim.x;
+  const bool live = row < n.rows;
+  float M = -INFINITY, sum = 0.f, o[V] = {};
+  if (live) {
+    // this group's pieces: every kJoinGroups-th block, 32 at a time, a lane each
+    for (int base = blockIdx.x + group; base <= n.last; base += 32 * kJoinGroups) {
+      const int c = base + lane * kJoinGroups;
+      const bool begins = c == (int)blockIdx.x, there = begins || (c <= n.last && notes[c].slot0);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (there) ml = *reinterpret_cast<const float2*>(slot_of<R, D>(g, grid, c, begins) + R * D + 2 * r);
+      float mx = ml.x;
+#pragma unroll
+      for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+      mx = fmaxf(mx, M);
+      const float f0 = M == -INFINITY ? 0.f : fast_exp2(M - mx), f1 = there ? fast_exp2(ml.x - mx) : 0.f;
+      float part = ml.y * f1;
+#pragma unroll
+      for (int k = 16; k; k >>= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
+      M = mx;
+      sum = sum * f0 + part;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] *= f0;
+      const unsigned all = __ballot_sync(0xffffffffu, there);
+      const int cnt = 32 - __clz(all);  // pieces up to the last that is there
+#pragma unroll 8
+      for (int k = 0; k < cnt; ++k) {
+        const float f = __shfl_sync(0xffffffffu, f1, k);
+        const int ck = base + k * kJoinGroups;
+        const float* q = slot_of<R, D>(g, grid, ck, ck == (int)blockIdx.x) + r * D + lane * V;
+        if ((all >> k) & 1u) {
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const float2 y = *reinterpret_cast<const float2*>(q + i);
+            o[i] = fmaf(y.x, f, o[i]);
+            o[i + 1] = fmaf(y.y, f, o[i + 1]);
+          }
+        }
+      }
+    }
+    if (group == 1) {
+      if (lane == 0) sm[warp & 7][0] = M, sm[warp & 7][1] = sum;
+#pragma unroll
+      for (int i = 0; i < V; ++i) so[warp & 7][lane * V + i] = o[i];
+    }
+  }
+  __syncthreads();
+  if (!live || group == 1) return;
+  {
+    const float m1 = sm[warp][0], mx = fmaxf(M, m1);  // (the first piece is group 0's: M is finite)
+    const float f0 = fast_exp2(M - mx), f1 = fast_exp2(m1 - mx);
+    M = mx;
+    sum = sum * f0 + sm[warp][1] * f1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = o[i] * f0 + so[warp][lane * V + i] * f1;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const long long to = out_offset(g, n.cu0, n.head, row) + lane * V;
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if (g.out_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(g.out.data) + to + i) = make_float2(o[i] * inv, o[i + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(g.out.data) + to + i) =
+          pack_bf16x2(o[i] * inv, o[i + 1] * inv);
+  }
+  if (lane == 0) store_row(g, n.cu0, n.head, row, M, sum);
+}
+
+}  // namespace ra
