@@ -566,6 +566,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
 // Blocks that fit on an SM (registers and shared memory), so the grid is one wave.
 int blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
+// From how many query rows per key / value head on the tensor-core kernel takes over.
+bool many_rows(int max_new, int G) { return (long long)max_new * G > 32; }
+
 // Query rows of an item in units of 8.
 int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
@@ -585,11 +588,13 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
+  if (many_rows(max_new, h / hk)) return cache_chunk_ws_bytes(d);
   const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * blocks_per_sm(nt);
   return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
+  if (many_rows(a.max_new, a.G)) return launch_cache_chunk(a, st);
   const int nt = row_tiles((long long)a.max_new * a.G);
   if (a.d == 64) return nt == 1 ? launch<64, 1>(a, st) : nt == 2 ? launch<64, 2>(a, st) : launch<64, 4>(a, st);
   return nt == 1 ? launch<128, 1>(a, st) : nt == 2 ? launch<128, 2>(a, st) : launch<128, 4>(a, st);

@@ -1,0 +1,522 @@
+// Attention of many new tokens (chunks of prompts) over the paged 4-bit cache, on
+// the tensor cores.
+//
+// An item is 256 query rows (two tiles of 128) of one key / value head; the blocks,
+// one per SM, share the items' units as ra_cache_line.cuh says.  Per unit of 128
+// keys a tile needs S = Q K^T and O += P V, 4 * 128 * 128 * d flops, for which keys
+// and values are converted once per unit and block:
+//   warp 0       MMA issuer (one thread): PV0(j-1), S0(j), PV1(j-1), S1(j), so one
+//                tile's products run while the other's softmax does.  S_t in
+//                tensor-memory columns [128 t, 128 t + 128), O_t from 256 + 128 t.
+//   warp 1       allocates / frees tensor memory.  Warps 2 and 3 are idle.
+//   warps 4-7    one key row per thread: its 4-bit codes and scales go from global
+//                memory through registers to fp16 rows in the 128-byte swizzle that
+//                the MMA reads, K and V two stages each.  About 340 instructions a
+//                thread and unit, a tenth of the unit's issue slots.
+//   warps 8-15   a query row per thread: queries scaled per row by a power of two into
+//                fp16's normal range and stored for the MMA; scores from tensor
+//                memory, running offset M (O is rescaled when a score passes it by
+//                far), P as fp16 over the score columns; the epilogue.
+// Bound: tensor throughput.  fp16 operands hold number * scale exactly.
+#include "ra_cache_line.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kBox = 128 * 128;  // 128 rows x 64 fp16
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 2;       // of K and of V
+constexpr uint32_t kWaitHint = 2000;
+constexpr float kLift = 8.f, kSlack = 4.f;  // largest p between 2^8 and 2^12
+constexpr float kNone = -3.0e38f;           // M of a row that has seen no key
+// Registers per thread of the control, conversion and softmax warpgroups.
+constexpr int kLaunchRegs = 128, kRegsCtl = 56, kRegsConv = 88, kRegsSoft = 184;
+static_assert(128 * (kRegsCtl + kRegsConv + 2 * kRegsSoft) <= kThreads * kLaunchRegs, "register split exceeds the launch");
+
+// G places per unit, so that the causal growth of 256 / G keys per tile is whole.
+struct ManyRows {
+  static constexpr int R = 256, kItemCost = 2;
+  static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
+    s.per = g.causal ? g.G : 1;
+    const int seen = g.causal ? max(0, s.len - s.n_new) : s.len;  // by every row
+    s.a = (long long)s.per * ((seen + kUnit - 1) / kUnit + kItemCost) + 2;
+    s.b = g.causal ? 2 : 0;
+  }
+};
+
+template <int D>
+struct Lay {
+  static constexpr int kTile = D / 64 * kBox;
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
+  static constexpr int kMisc = kBar + 16 * 8;
+  static constexpr int kAlloc = kMisc + 16 + 1024;  // slack to align the base to 1024 bytes
+};
+enum Bar {
+  B_Q_FULL = 0,    // per query tile
+  B_K_FULL = 2,    // kStages
+  B_K_EMPTY = 4,
+  B_V_FULL = 6,
+  B_V_EMPTY = 8,
+  B_S_FULL = 10,   // per query tile
+  B_P_FULL = 12,
+  B_O_DONE = 14,
+  B_TEARDOWN = 15
+};
+
+// kind::f16 with fp16 A and B, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+// A key row's codes and scales.
+template <int D>
+struct RawRow {
+  uint4 code[D / 32];
+  uint32_t scale[D / 64];
+  __device__ __forceinline__ void load(const uint8_t* c, const uint8_t* s, bool ok) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      code[i] = ok ? __ldg(reinterpret_cast<const uint4*>(c) + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) scale[i] = ok ? __ldg(reinterpret_cast<const uint32_t*>(s) + i) : 0u;
+  }
+  // Row `r` of a tile at `tile`.
+  __device__ __forceinline__ void store(uint32_t tile, int r) const {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      const uint32_t two = e4m3x2_to_f16(scale[i >> 1] >> (16 * (i & 1)));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t x[4];
+        e2m1x8_to_f16(w[k], x);
+        const uint32_t s = k < 2 ? half_lo2(two) : half_hi2(two);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = hmul2(x[j], s);
+        const int chunk = 4 * i + k;  // 16 bytes of the row
+        sts128(tile + (chunk >> 3) * kBox + sw128_offset(r, chunk & 7), x);
+      }
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAttnArgs a) {
+  using L = Lay<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ LineShared<kWarps> sh;
+  const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
+  uint8_t* sp = smem_raw + (sb - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = sb + L::kBar;
+  auto BAR = [bar0](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kMisc + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + L::kMisc);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(B_Q_FULL + i), 4);
+      mbar_init(BAR(B_K_FULL + i), 4);
+      mbar_init(BAR(B_K_EMPTY + i), 1);
+      mbar_init(BAR(B_V_FULL + i), 4);
+      mbar_init(BAR(B_V_EMPTY + i), 1);
+      mbar_init(BAR(B_S_FULL + i), 1);
+      mbar_init(BAR(B_P_FULL + i), 4);
+    }
+    mbar_init(BAR(B_O_DONE), 1);
+    mbar_init(BAR(B_TEARDOWN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  LinePos at;
+  long long end_u, quota;
+  JoinNote note = empty_note();
+  if (!find_run<ManyRows, kWarps>(a, at, end_u, quota, sh)) {
+    if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
+    return;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Piece x;
+  // query tiles of an item
+  auto tiles_of = [&](const Piece& p) { return p.n_new * a.G - p.tile * 256 > 128 ? 2 : 1; };
+
+  if (warp < 4) {
+    regs_dec<kRegsCtl>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t kIdS = idesc_f16_f32(128, kUnit, 0), kIdPV = idesc_f16_f32(128, D, 1);
+        constexpr uint32_t kHi = sdesc_sw128_hi(1024);
+        bool ok = true;
+        uint32_t n_k = 0, n_v = 0;        // units whose S, whose PV were issued
+        uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        auto issue_s = [&](int t) {
+          const uint32_t lk = sdesc_sw128_lo(sb + L::kK + (n_k % kStages) * L::kTile, 16);
+          const uint32_t lq = sdesc_sw128_lo(sb + L::kQ + t * L::kTile, 16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + t * 128, sdesc_words(lq + off, kHi), sdesc_words(lk + off, kHi), kIdS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(BAR(B_S_FULL + t));
+        };
+        auto issue_pv = [&](int t, bool first, bool last_tile) -> bool {
+          if (!wait_one<kWaitHint>(BAR(B_P_FULL + t), n_p[t] & 1, abort_flag, a.ctl, 33)) return false;
+          ++n_p[t];
+          if (t == 0 &&
+              !wait_one<kWaitHint>(BAR(B_V_FULL + n_v % kStages), (n_v / kStages) & 1, abort_flag, a.ctl, 34))
+            return false;
+          tc_fence_after();
+          const uint32_t lv = sdesc_sw128_lo(sb + L::kV + (n_v % kStages) * L::kTile, kBox);
+#pragma unroll
+          for (int kk = 0; kk < kUnit / 16; ++kk)
+            mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_words(lv + kk * 128, kHi), kIdPV,
+                        (!first || kk > 0) ? 1u : 0u);
+          if (last_tile) {
+            mma_commit(BAR(B_V_EMPTY + n_v % kStages));
+            ++n_v;
+          }
+          return true;
+        };
+        while (ok && next_piece<ManyRows>(a, at, end_u, x)) {
+          const int nt = tiles_of(x), n = x.ub - x.ua;
+          for (int j = 0; j <= n && ok; ++j) {
+            for (int t = 0; t < nt && ok; ++t) {
+              // PV_t(j-1) reads P_t from the S_t columns, so it goes before S_t(j)
+              if (j >= 1) ok = issue_pv(t, j == 1, t == nt - 1);
+              if (!ok || j == n) continue;
+              if (t == 0)
+                ok = wait_one<kWaitHint>(BAR(B_K_FULL + n_k % kStages), (n_k / kStages) & 1, abort_flag, a.ctl, 35);
+              if (ok && j == 0) {
+                ok = wait_one<kWaitHint>(BAR(B_Q_FULL + t), n_q[t] & 1, abort_flag, a.ctl, 36);
+                ++n_q[t];
+              }
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t);
+            }
+            if (ok && j < n) {
+              mma_commit(BAR(B_K_EMPTY + n_k % kStages));
+              ++n_k;
+            }
+          }
+          if (ok) mma_commit(BAR(B_O_DONE));
+        }
+        // every issued MMA, and every arrival it makes, completes before the block ends
+        mma_commit(BAR(B_TEARDOWN));
+        drain_one(BAR(B_TEARDOWN), 0, a.ctl, 37);
+        for (uint32_t s = 0; s < kStages; ++s) {
+          const uint32_t ck = (n_k + kStages - 1 - s) / kStages, cv = (n_v + kStages - 1 - s) / kStages;
+          if (ck) drain_one(BAR(B_K_EMPTY + s), (ck - 1) & 1, a.ctl, 38);
+          if (cv) drain_one(BAR(B_V_EMPTY + s), (cv - 1) & 1, a.ctl, 39);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- keys and values to fp16
+    regs_dec<kRegsConv>();
+    const int r = threadIdx.x - 128;
+    uint32_t n = 0;  // units converted
+    bool ok = true;
+    while (ok && next_piece<ManyRows>(a, at, end_u, x)) {
+      const int mask = (1 << a.c.page_shift) - 1;
+      const int* table = a.s.table + (long long)x.seq * a.s.table_stride;
+      const long long hc = x.head * a.c.k.s_head, hs = x.head * a.c.ks.s_head;
+      RawRow<D> k, v;
+      long long oc = 0, os = 0;
+      bool live = false;
+      int page = 0;
+      auto page_of = [&](int u) {  // read a unit ahead
+        const int key = u * kUnit + r;
+        live = key < x.len;
+        page = live ? __ldg(table + (key >> a.c.page_shift)) : 0;
+      };
+      auto place = [&](int u) {
+        if (live && (unsigned)page >= (unsigned)a.c.n_pages) {
+          record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_PAGE);
+          live = false;
+        }
+        const int row = (u * kUnit + r) & mask;
+        oc = live ? (long long)page * a.c.k.s_page + row * (int)a.c.k.s_row + hc : 0;
+        os = live ? (long long)page * a.c.ks.s_page + row * (int)a.c.ks.s_row + hs : 0;
+      };
+      page_of(x.ua);
+      place(x.ua);
+      bool ok_row = live;
+      k.load(a.c.k.data + oc, a.c.ks.data + os, ok_row);
+      v.load(a.c.v.data + oc, a.c.vs.data + os, ok_row);
+      if (x.ua + 1 < x.ub) page_of(x.ua + 1);
+      for (int u = x.ua; u < x.ub; ++u, ++n) {
+        const uint32_t s = n % kStages;
+        const bool more = u + 1 < x.ub;
+        if (n >= kStages &&
+            !wait_warp<kWaitHint>(BAR(B_K_EMPTY + s), (n / kStages - 1) & 1, abort_flag, a.ctl, 40)) {
+          ok = false;
+          break;
+        }
+        k.store(sb + L::kK + s * L::kTile, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_K_FULL + s));
+        if (more) {
+          place(u + 1);
+          ok_row = live;
+          k.load(a.c.k.data + oc, a.c.ks.data + os, ok_row);
+        }
+        if (n >= kStages &&
+            !wait_warp<kWaitHint>(BAR(B_V_EMPTY + s), (n / kStages - 1) & 1, abort_flag, a.ctl, 41)) {
+          ok = false;
+          break;
+        }
+        v.store(sb + L::kV + s * L::kTile, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_V_FULL + s));
+        if (more) {
+          v.load(a.c.v.data + oc, a.c.vs.data + os, ok_row);
+          if (u + 2 < x.ub) page_of(u + 2);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax, a row per thread
+    regs_inc<kRegsSoft>();
+    const int t = (warp - 8) >> 2, r = (threadIdx.x - 256) & 127;
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = tl + t * 128, tO = tl + 256 + t * 128;
+    uint32_t n_s = 0, n_o = 0;  // score tiles and results seen
+    int seen = -1;
+    bool ok = true;
+    while (ok && next_piece<ManyRows>(a, at, end_u, x)) {
+      const int cu0 = __ldg(a.s.cu + x.seq), row = x.tile * 256 + t * 128 + r;
+      if (threadIdx.x == 256) {
+        if (x.seq != seen && __ldg(a.s.lens + x.seq) > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+        note_piece<ManyRows>(a, x, quota, cu0, note);
+      }
+      seen = x.seq;
+      if (t >= tiles_of(x)) {  // not this warpgroup's, but its phase passes
+        ok = wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 44);
+        ++n_o;
+        continue;
+      }
+      const bool valid = row < x.n_new * a.G;
+      float sc;
+      int end_row = 0;
+      {
+        uint32_t q[D / 2];
+        const int tok = row / a.G;
+        if (valid) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) +
+                                                            (long long)(cu0 + tok) * a.q.s_row +
+                                                            (long long)(x.head * a.G + row % a.G) * a.q.s_head);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 w = __ldg(src + i);
+            q[4 * i] = w.x, q[4 * i + 1] = w.y, q[4 * i + 2] = w.z, q[4 * i + 3] = w.w;
+          }
+          end_row = a.causal ? min(x.len, x.len - x.n_new + tok + 1) : x.len;
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) q[i] = 0;
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          m = fmax3f(m, fabsf(__uint_as_float(q[i] << 16)), fabsf(__uint_as_float(q[i] & 0xffff0000u)));
+        // the row's largest entry goes to [2^12, 2^13)
+        const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
+        sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e - 12) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            h[i] = pack_f16x2(__uint_as_float(q[4 * c + i] << 16) * up, __uint_as_float(q[4 * c + i] & 0xffff0000u) * up);
+          sts128(sb + L::kQ + t * L::kTile + (c >> 3) * kBox + sw128_offset(r, c & 7), h);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_Q_FULL + t));
+      }
+      float M = kNone, l_run = 0.f;
+      for (int u = x.ua; u < x.ub; ++u, ++n_s) {
+        const int c_hi = end_row - u * kUnit;
+        if (!wait_warp<kWaitHint>(BAR(B_S_FULL + t), n_s & 1, abort_flag, a.ctl, 42)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[kUnit];
+        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(v + 0));
+        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 0));
+        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(v + 64));
+        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(v + 96));
+        float mc[4];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          if (hh == 1) {
+            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
+            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
+          }
+          if (c_hi < kUnit) {
+            const uint64_t mw = bit_window64(0, c_hi - 64 * hh);
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+              v[64 * hh + k] = ((mw >> k) & 1ull) ? v[64 * hh + k] : __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c0 = 64 * hh + 16 * q;
+            float m = hh == 0 ? __uint_as_float(v[c0]) : fmaxf(mc[q], __uint_as_float(v[c0]));
+#pragma unroll
+            for (int c = c0 + 1; c < c0 + 15; c += 2) m = fmax3f(m, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+            mc[q] = fmaxf(m, __uint_as_float(v[c0 + 15]));
+          }
+        }
+        const float mx = __fmul_rn(fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3])), sc);
+        float alpha = 1.f;
+        if (mx > M + (kLift + kSlack)) {
+          alpha = fast_exp2(M - (mx - kLift));
+          M = mx - kLift;
+        }
+        const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(-M, -M);
+        uint64_t acc[4] = {0, 0, 0, 0};
+        // Offsets so large that the product's rounding shows next to them: the
+        // products are rounded first, so that the largest score gives an exact difference.
+        const bool far = __any_sync(0xffffffffu, fabsf(M) > 65536.f && M > kNone);
+        auto weights = [&](auto rounded) {
+#pragma unroll
+          for (int c32 = 0; c32 < kUnit / 32; ++c32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int c = c32 * 32 + 2 * k;
+              float x0 = __uint_as_float(v[c]), x1 = __uint_as_float(v[c + 1]);
+              if constexpr (decltype(rounded)::value)
+                x0 = __fsub_rn(__fmul_rn(x0, sc), M), x1 = __fsub_rn(__fmul_rn(x1, sc), M);
+              else
+                f32x2_split(fma_f32x2(f32x2(x0, x1), sc2, nm2), x0, x1);
+              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+              acc[k & 3] = add_f32x2(acc[k & 3], f32x2(e0, e1));
+              pk[k] = pack_f16x2(e0, e1);
+            }
+            tmem_st16(tS + c32 * 16, pk);
+          }
+        };
+        if (far)
+          weights(Flag<true>{});
+        else
+          weights(Flag<false>{});
+        float s0, s1;
+        f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);
+        l_run = l_run * alpha + (s0 + s1);
+        // O_t is stable here: the commit behind S_FULL covers PV_t of the unit before
+        if (u > x.ua && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_P_FULL + t));
+      }
+      if (!ok || !wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 43)) {
+        ok = false;
+        break;
+      }
+      ++n_o;
+      tc_fence_after();
+      const bool whole = x.ub - x.ua == x.units;
+      const float inv = whole ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f;
+      float* part = slot_of<256, D>(a, gridDim.x, blockIdx.x, x.ua == 0);
+      const int pr = t * 128 + r;
+      const long long to = valid ? out_offset(a, cu0, x.head, row) : 0;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_ld_wait(o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+        if (!valid) {
+        } else if (!whole || a.out_f32) {
+          uint4* dst = reinterpret_cast<uint4*>((whole ? static_cast<float*>(a.out.data) + to : part + (long long)pr * D) + c * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out.data) + to + c * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t* p = o + 8 * k;
+            auto f = [&](int i) { return pack_bf16x2(__uint_as_float(p[i]), __uint_as_float(p[i + 1])); };
+            dst[k] = make_uint4(f(0), f(2), f(4), f(6));
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      if (valid) {
+        if (whole)
+          store_row(a, cu0, x.head, row, M, l_run);
+        else
+          *reinterpret_cast<float2*>(part + 256 * D + 2 * pr) = make_float2(M, l_run);
+      }
+    }
+    if (threadIdx.x == 256) notes_of(a)[blockIdx.x] = note;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
+  cudaError_t e = configure_kernel<cache_chunk_kernel<D>>(kLaunchRegs, Lay<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int grid = num_sms();
+  cache_chunk_kernel<D><<<grid, kThreads, Lay<D>::kAlloc, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cache_join_kernel<256, D><<<dim3(grid, 32), 256 * kJoinGroups, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_chunk_ws_bytes(int d) { return line_ws_bytes<256>(num_sms(), d); }
+
+cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t st) {
+  return a.d == 64 ? launch<64>(a, st) : launch<128>(a, st);
+}
+
+}  // namespace ra

@@ -21,6 +21,11 @@ namespace ra {
 
 constexpr int kUnit = 128;
 
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
 // Quotient of non-negative numbers, by the short division where they are small.
 __device__ __forceinline__ long long quotient(long long n, long long d) {
   if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;

@@ -211,6 +211,9 @@ struct CacheAttnArgs {
 };
 size_t cache_attn_ws_bytes(long long total, int max_new, int h, int hk, int d, int n_seqs);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st);
+// the variant for many query rows per key / value head
+size_t cache_chunk_ws_bytes(int d);
+cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t st);
 
 int num_sms();
 
