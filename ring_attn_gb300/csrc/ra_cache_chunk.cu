@@ -8,7 +8,10 @@
 //   warp 0       MMA issuer (one thread): PV0(j-1), S0(j), PV1(j-1), S1(j), so one
 //                tile's products run while the other's softmax does.  S_t in
 //                tensor-memory columns [128 t, 128 t + 128), O_t from 256 + 128 t.
-//   warp 1       allocates / frees tensor memory.  Warps 2 and 3 are idle.
+//   warp 1       allocates / frees tensor memory.
+//   warp 2       one thread walks the block's pieces of the line and hands them to the
+//                others in shared memory, a few ahead (so that no other role holds a
+//                place on the line in registers).  Warp 3 is idle.
 //   warps 4-7    one key row per thread: its 4-bit codes and scales go from global
 //                memory through registers to fp16 rows in the 128-byte swizzle that
 //                the MMA reads, K and V two stages each.  About 340 instructions a
@@ -26,12 +29,12 @@ namespace {
 constexpr int kBox = 128 * 128;  // 128 rows x 64 fp16
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 2;       // of K and of V
+constexpr int kStages = 2;       // of K and of V (the issuer steps them by xor)
 constexpr uint32_t kWaitHint = 2000;
 constexpr float kLift = 8.f, kSlack = 4.f;  // largest p between 2^8 and 2^12
 constexpr float kNone = -3.0e38f;           // M of a row that has seen no key
 // Registers per thread of the control, conversion and softmax warpgroups.
-constexpr int kLaunchRegs = 128, kRegsCtl = 56, kRegsConv = 88, kRegsSoft = 184;
+constexpr int kLaunchRegs = 128, kRegsCtl = 64, kRegsConv = 80, kRegsSoft = 184;
 static_assert(128 * (kRegsCtl + kRegsConv + 2 * kRegsSoft) <= kThreads * kLaunchRegs, "register split exceeds the launch");
 
 // G places per unit, so that the causal growth of 256 / G keys per tile is whole.
@@ -45,24 +48,36 @@ struct ManyRows {
   }
 };
 
+// A piece as the roles need it; n = 0: the run's end.
+struct Item {
+  int ua, n;                 // first unit, units
+  int head, row0, rows;      // first query row of the item, rows of the sequence
+  int seq, cu0, len, n_new;
+  int whole;                 // the piece is the whole item
+};
+constexpr int kItems = 4;
+
 template <int D>
 struct Lay {
   static constexpr int kTile = D / 64 * kBox;
   static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
-  static constexpr int kMisc = kBar + 16 * 8;
-  static constexpr int kAlloc = kMisc + 16 + 1024;  // slack to align the base to 1024 bytes
+  static constexpr int kMisc = kBar + 24 * 8;
+  static constexpr int kItem = kMisc + 16;
+  static constexpr int kAlloc = kItem + kItems * (int)sizeof(Item) + 1024;  // slack to align the base to 1024 bytes
 };
 enum Bar {
   B_Q_FULL = 0,    // per query tile
-  B_K_FULL = 2,    // kStages
+  B_KV_FULL = 2,   // kStages; K and V of a unit complete on one barrier, so the issuer waits once
   B_K_EMPTY = 4,
-  B_V_FULL = 6,
   B_V_EMPTY = 8,
   B_S_FULL = 10,   // per query tile
   B_P_FULL = 12,
   B_O_DONE = 14,
-  B_TEARDOWN = 15
+  B_TEARDOWN = 15,
+  B_ITEM_FULL = 16,   // kItems
+  B_ITEM_EMPTY = 20
 };
+constexpr int kReaders = 13;  // of an item: the issuer, 4 conversion and 8 softmax warps
 
 // kind::f16 with fp16 A and B, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
@@ -125,12 +140,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(B_Q_FULL + i), 4);
-      mbar_init(BAR(B_K_FULL + i), 4);
+      mbar_init(BAR(B_KV_FULL + i), 4);
       mbar_init(BAR(B_K_EMPTY + i), 1);
-      mbar_init(BAR(B_V_FULL + i), 4);
       mbar_init(BAR(B_V_EMPTY + i), 1);
       mbar_init(BAR(B_S_FULL + i), 1);
       mbar_init(BAR(B_P_FULL + i), 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(BAR(B_ITEM_FULL + i), 1);
+      mbar_init(BAR(B_ITEM_EMPTY + i), kReaders);
     }
     mbar_init(BAR(B_O_DONE), 1);
     mbar_init(BAR(B_TEARDOWN), 1);
@@ -152,9 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Piece x;
+  volatile Item* items = reinterpret_cast<volatile Item*>(sp + L::kItem);
   // query tiles of an item
-  auto tiles_of = [&](const Piece& p) { return p.n_new * a.G - p.tile * 256 > 128 ? 2 : 1; };
+  auto tiles_of = [](const volatile Item& x) { return x.rows - x.row0 > 128 ? 2 : 1; };
 
   if (warp < 4) {
     regs_dec<kRegsCtl>();
@@ -164,10 +182,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         constexpr uint32_t kIdS = idesc_f16_f32(128, kUnit, 0), kIdPV = idesc_f16_f32(128, D, 1);
         constexpr uint32_t kHi = sdesc_sw128_hi(1024);
         bool ok = true;
-        uint32_t n_k = 0, n_v = 0;        // units whose S, whose PV were issued
-        uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
-        auto issue_s = [&](int t) {
-          const uint32_t lk = sdesc_sw128_lo(sb + L::kK + (n_k % kStages) * L::kTile, 16);
+        uint32_t k_at = 0, v_at = 0;    // stages of the next unit's S and PV, 0 or kTile
+        uint32_t par_kv = 0, n_all = 0;
+        uint32_t par_q = 0, par_p = 0;  // phases of the query tiles' barriers, bit t (t is known at compile time)
+        auto issue_s = [&](auto tile) {
+          constexpr int t = decltype(tile)::value;
+          const uint32_t lk = sdesc_sw128_lo(sb + L::kK + k_at, 16);
           const uint32_t lq = sdesc_sw128_lo(sb + L::kQ + t * L::kTile, 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -176,44 +196,54 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           }
           mma_commit(BAR(B_S_FULL + t));
         };
-        auto issue_pv = [&](int t, bool first, bool last_tile) -> bool {
-          if (!wait_one<kWaitHint>(BAR(B_P_FULL + t), n_p[t] & 1, abort_flag, a.ctl, 33)) return false;
-          ++n_p[t];
-          if (t == 0 &&
-              !wait_one<kWaitHint>(BAR(B_V_FULL + n_v % kStages), (n_v / kStages) & 1, abort_flag, a.ctl, 34))
-            return false;
+        auto issue_pv = [&](auto tile, uint32_t first) -> bool {
+          constexpr int t = decltype(tile)::value;
+          if (!wait_one<kWaitHint>(BAR(B_P_FULL + t), (par_p >> t) & 1, abort_flag, a.ctl, 33)) return false;
+          par_p ^= 1u << t;
           tc_fence_after();
-          const uint32_t lv = sdesc_sw128_lo(sb + L::kV + (n_v % kStages) * L::kTile, kBox);
+          const uint32_t lv = sdesc_sw128_lo(sb + L::kV + v_at, kBox);
 #pragma unroll
           for (int kk = 0; kk < kUnit / 16; ++kk)
             mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_words(lv + kk * 128, kHi), kIdPV,
-                        (!first || kk > 0) ? 1u : 0u);
-          if (last_tile) {
-            mma_commit(BAR(B_V_EMPTY + n_v % kStages));
-            ++n_v;
-          }
+                        kk > 0 ? 1u : first ^ 1u);
           return true;
         };
-        while (ok && next_piece<ManyRows>(a, at, end_u, x)) {
-          const int nt = tiles_of(x), n = x.ub - x.ua;
-          for (int j = 0; j <= n && ok; ++j) {
-            for (int t = 0; t < nt && ok; ++t) {
-              // PV_t(j-1) reads P_t from the S_t columns, so it goes before S_t(j)
-              if (j >= 1) ok = issue_pv(t, j == 1, t == nt - 1);
-              if (!ok || j == n) continue;
-              if (t == 0)
-                ok = wait_one<kWaitHint>(BAR(B_K_FULL + n_k % kStages), (n_k / kStages) & 1, abort_flag, a.ctl, 35);
-              if (ok && j == 0) {
-                ok = wait_one<kWaitHint>(BAR(B_Q_FULL + t), n_q[t] & 1, abort_flag, a.ctl, 36);
-                ++n_q[t];
-              }
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(t);
+        // PV_t(j-1) reads P_t from the S_t columns, so it goes before S_t(j)
+        auto turn = [&](auto tile, int j, int n) -> bool {
+          constexpr int t = decltype(tile)::value;
+          if (j >= 1 && !issue_pv(tile, j == 1)) return false;
+          if (j == n) return true;
+          if (t == 0 && !wait_one<kWaitHint>(BAR(B_KV_FULL) + (k_at ? 8u : 0u), par_kv, abort_flag, a.ctl, 35)) return false;
+          if (j == 0) {
+            if (!wait_one<kWaitHint>(BAR(B_Q_FULL + t), (par_q >> t) & 1, abort_flag, a.ctl, 36)) return false;
+            par_q ^= 1u << t;
+          }
+          tc_fence_after();
+          issue_s(tile);
+          return true;
+        };
+        for (int i = 0; ok; ++i) {
+          if (!wait_one<kWaitHint>(BAR(B_ITEM_FULL + i % kItems), (i / kItems) & 1, abort_flag, a.ctl, 45)) {
+            ok = false;
+            break;
+          }
+          const int nt = tiles_of(items[i % kItems]), n = items[i % kItems].n;
+          mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
+          if (n == 0) break;
+          for (int j = 0; j <= n; ++j) {
+            if (!turn(Int<0>{}, j, n) || (nt == 2 && !turn(Int<1>{}, j, n))) {
+              ok = false;
+              break;
             }
-            if (ok && j < n) {
-              mma_commit(BAR(B_K_EMPTY + n_k % kStages));
-              ++n_k;
+            if (j >= 1) {
+              mma_commit(BAR(B_V_EMPTY) + (v_at ? 8u : 0u));
+              v_at ^= L::kTile;
+            }
+            if (j < n) {
+              mma_commit(BAR(B_K_EMPTY) + (k_at ? 8u : 0u));
+              if (k_at) par_kv ^= 1u;
+              k_at ^= L::kTile;
+              ++n_all;
             }
           }
           if (ok) mma_commit(BAR(B_O_DONE));
@@ -222,10 +252,39 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         mma_commit(BAR(B_TEARDOWN));
         drain_one(BAR(B_TEARDOWN), 0, a.ctl, 37);
         for (uint32_t s = 0; s < kStages; ++s) {
-          const uint32_t ck = (n_k + kStages - 1 - s) / kStages, cv = (n_v + kStages - 1 - s) / kStages;
-          if (ck) drain_one(BAR(B_K_EMPTY + s), (ck - 1) & 1, a.ctl, 38);
-          if (cv) drain_one(BAR(B_V_EMPTY + s), (cv - 1) & 1, a.ctl, 39);
+          const uint32_t c = (n_all + kStages - 1 - s) / kStages;
+          if (c && ok) {
+            drain_one(BAR(B_K_EMPTY + s), (c - 1) & 1, a.ctl, 38);
+            drain_one(BAR(B_V_EMPTY + s), (c - 1) & 1, a.ctl, 39);
+          }
         }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // -------------------------------------------------------------- planner
+      if (lane == 0) {
+        Piece x;
+        int seen = -1;
+        for (int i = 0;; ++i) {
+          const bool more = next_piece<ManyRows>(a, at, end_u, x);
+          const int cu0 = more ? __ldg(a.s.cu + x.seq) : 0;
+          if (more) {
+            if (x.seq != seen && __ldg(a.s.lens + x.seq) > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+            seen = x.seq;
+            note_piece<ManyRows>(a, x, quota, cu0, note);
+          }
+          if (i >= kItems && !wait_one<kWaitHint>(BAR(B_ITEM_EMPTY + i % kItems), (i / kItems - 1) & 1, abort_flag,
+                                                  a.ctl, 46))
+            break;
+          volatile Item& y = items[i % kItems];
+          y.ua = x.ua, y.n = more ? x.ub - x.ua : 0;
+          y.head = x.head, y.row0 = x.tile * 256, y.rows = x.n_new * a.G;
+          y.seq = x.seq, y.cu0 = cu0, y.len = x.len, y.n_new = x.n_new;
+          y.whole = x.ub - x.ua == x.units;
+          mbar_arrive(BAR(B_ITEM_FULL + i % kItems));
+          if (!more) break;
+        }
+        notes_of(a)[blockIdx.x] = note;
       }
       __syncwarp();
     }
@@ -235,17 +294,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     const int r = threadIdx.x - 128;
     uint32_t n = 0;  // units converted
     bool ok = true;
-    while (ok && next_piece<ManyRows>(a, at, end_u, x)) {
-      const int mask = (1 << a.c.page_shift) - 1;
+    const int mask = (1 << a.c.page_shift) - 1;
+    for (int i = 0; ok; ++i) {
+      if (!wait_warp<kWaitHint>(BAR(B_ITEM_FULL + i % kItems), (i / kItems) & 1, abort_flag, a.ctl, 47)) break;
+      const volatile Item& x = items[i % kItems];
+      const int len = x.len, u0 = x.ua, u1 = u0 + x.n;
       const int* table = a.s.table + (long long)x.seq * a.s.table_stride;
       const long long hc = x.head * a.c.k.s_head, hs = x.head * a.c.ks.s_head;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
+      if (u0 == u1) break;
       RawRow<D> k, v;
       long long oc = 0, os = 0;
       bool live = false;
       int page = 0;
       auto page_of = [&](int u) {  // read a unit ahead
         const int key = u * kUnit + r;
-        live = key < x.len;
+        live = key < len;
         page = live ? __ldg(table + (key >> a.c.page_shift)) : 0;
       };
       auto place = [&](int u) {
@@ -257,24 +322,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         oc = live ? (long long)page * a.c.k.s_page + row * (int)a.c.k.s_row + hc : 0;
         os = live ? (long long)page * a.c.ks.s_page + row * (int)a.c.ks.s_row + hs : 0;
       };
-      page_of(x.ua);
-      place(x.ua);
+      page_of(u0);
+      place(u0);
       bool ok_row = live;
       k.load(a.c.k.data + oc, a.c.ks.data + os, ok_row);
       v.load(a.c.v.data + oc, a.c.vs.data + os, ok_row);
-      if (x.ua + 1 < x.ub) page_of(x.ua + 1);
-      for (int u = x.ua; u < x.ub; ++u, ++n) {
+      if (u0 + 1 < u1) page_of(u0 + 1);
+      for (int u = u0; u < u1; ++u, ++n) {
         const uint32_t s = n % kStages;
-        const bool more = u + 1 < x.ub;
+        const bool more = u + 1 < u1;
         if (n >= kStages &&
             !wait_warp<kWaitHint>(BAR(B_K_EMPTY + s), (n / kStages - 1) & 1, abort_flag, a.ctl, 40)) {
           ok = false;
           break;
         }
         k.store(sb + L::kK + s * L::kTile, r);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_K_FULL + s));
         if (more) {
           place(u + 1);
           ok_row = live;
@@ -288,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         v.store(sb + L::kV + s * L::kTile, r);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_V_FULL + s));
+        if (lane == 0) mbar_arrive(BAR(B_KV_FULL + s));
         if (more) {
           v.load(a.c.v.data + oc, a.c.vs.data + os, ok_row);
-          if (u + 2 < x.ub) page_of(u + 2);
+          if (u + 2 < u1) page_of(u + 2);
         }
       }
     }
@@ -302,21 +364,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tl + t * 128, tO = tl + 256 + t * 128;
     uint32_t n_s = 0, n_o = 0;  // score tiles and results seen
-    int seen = -1;
     bool ok = true;
-    while (ok && next_piece<ManyRows>(a, at, end_u, x)) {
-      const int cu0 = __ldg(a.s.cu + x.seq), row = x.tile * 256 + t * 128 + r;
-      if (threadIdx.x == 256) {
-        if (x.seq != seen && __ldg(a.s.lens + x.seq) > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
-        note_piece<ManyRows>(a, x, quota, cu0, note);
-      }
-      seen = x.seq;
+    for (int i = 0; ok; ++i) {
+      if (!wait_warp<kWaitHint>(BAR(B_ITEM_FULL + i % kItems), (i / kItems) & 1, abort_flag, a.ctl, 48)) break;
+      const volatile Item& x = items[i % kItems];
+      const int row = x.row0 + t * 128 + r, u0 = x.ua, u1 = u0 + x.n;
+      if (u0 == u1) break;
       if (t >= tiles_of(x)) {  // not this warpgroup's, but its phase passes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
         ok = wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 44);
         ++n_o;
         continue;
       }
-      const bool valid = row < x.n_new * a.G;
+      const bool valid = row < x.rows;
       float sc;
       int end_row = 0;
       {
@@ -324,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         const int tok = row / a.G;
         if (valid) {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) +
-                                                            (long long)(cu0 + tok) * a.q.s_row +
+                                                            (long long)(x.cu0 + tok) * a.q.s_row +
                                                             (long long)(x.head * a.G + row % a.G) * a.q.s_head);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
@@ -357,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         if (lane == 0) mbar_arrive(BAR(B_Q_FULL + t));
       }
       float M = kNone, l_run = 0.f;
-      for (int u = x.ua; u < x.ub; ++u, ++n_s) {
+      for (int u = u0; u < u1; ++u, ++n_s) {
         const int c_hi = end_row - u * kUnit;
         if (!wait_warp<kWaitHint>(BAR(B_S_FULL + t), n_s & 1, abort_flag, a.ctl, 42)) {
           ok = false;
@@ -424,14 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           }
         };
         if (far)
-          weights(Flag<true>{});
+          weights(Int<1>{});
         else
-          weights(Flag<false>{});
+          weights(Int<0>{});
         float s0, s1;
         f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);
         l_run = l_run * alpha + (s0 + s1);
         // O_t is stable here: the commit behind S_FULL covers PV_t of the unit before
-        if (u > x.ua && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (u > u0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -453,11 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       }
       ++n_o;
       tc_fence_after();
-      const bool whole = x.ub - x.ua == x.units;
+      const bool whole = x.whole;
+      const int cu0 = x.cu0, head = x.head;
       const float inv = whole ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f;
-      float* part = slot_of<256, D>(a, gridDim.x, blockIdx.x, x.ua == 0);
+      float* part = slot_of<256, D>(a, gridDim.x, blockIdx.x, u0 == 0);
       const int pr = t * 128 + r;
-      const long long to = valid ? out_offset(a, cu0, x.head, row) : 0;
+      const long long to = valid ? out_offset(a, cu0, head, row) : 0;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -484,12 +546,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       tc_fence_before();
       if (valid) {
         if (whole)
-          store_row(a, cu0, x.head, row, M, l_run);
+          store_row(a, cu0, head, row, M, l_run);
         else
           *reinterpret_cast<float2*>(part + 256 * D + 2 * pr) = make_float2(M, l_run);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
     }
-    if (threadIdx.x == 256) notes_of(a)[blockIdx.x] = note;
   }
   tc_fence_before();
   __syncthreads();

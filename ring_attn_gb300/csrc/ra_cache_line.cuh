@@ -21,9 +21,10 @@ namespace ra {
 
 constexpr int kUnit = 128;
 
-template <bool B>
-struct Flag {
-  static constexpr bool value = B;
+// Numbers that lambdas take as compile-time constants.
+template <int N>
+struct Int {
+  static constexpr int value = N;
 };
 
 // Quotient of non-negative numbers, by the short division where they are small.
