@@ -350,8 +350,8 @@ typedef enum { RA_ROPE_HALVES = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope;
  *   q (optional), q_out: (rows, h, d) bf16; k, v: (rows, hk, d) bf16; rows >=
  *   cu_seqlens[n_seqs]; strides and pointers as for the attention calls.  q_out
  *   may be q itself; any other overlap with q, k or v is RA_ERR_INVALID_ARG.
- *   rope_cos, rope_sin (both or neither): (positions, r / 2) fp32, r <= d a
- *   multiple of 16, rows 16-byte aligned.  A pair (a, b) at position p becomes
+ *   rope_cos, rope_sin (both or neither): (positions, r / 2) fp32, r <= d, 16
+ *   or a multiple of 32, rows 16-byte aligned.  A pair (a, b) at position p becomes
  *   (a cos - b sin, b cos + a sin); head dims from r on stay.  Position of a
  *   token: positions[row] (int32, device) or, with positions NULL, its index in
  *   the cache.  Without tables nothing is rotated and q is copied.

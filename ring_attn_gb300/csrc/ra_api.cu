@@ -1052,7 +1052,8 @@ ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const r
   if ((rope_cos != nullptr) != (rope_sin != nullptr)) return RA_ERR_INVALID_ARG;
   if (rope != RA_ROPE_HALVES && rope != RA_ROPE_INTERLEAVED) return RA_ERR_INVALID_ARG;
   if (rope_cos) {
-    if (rope_cos->ndim != 2 || rope_cos->shape[1] < 1 || 2 * rope_cos->shape[1] > d || rope_cos->shape[1] % 8 != 0)
+    if (rope_cos->ndim != 2 || rope_cos->shape[1] < 1 || 2 * rope_cos->shape[1] > d ||
+        (rope_cos->shape[1] != 8 && rope_cos->shape[1] % 16 != 0))  // 16 head dims, or a multiple of 32
       return RA_ERR_INVALID_ARG;
     if (rope_cos->shape[0] > INT32_MAX) return RA_ERR_INVALID_ARG;
     RA_TRY(check_rope_table(rope_cos, rope_cos, &a.cos_t, &a.cos_stride));

@@ -2,8 +2,6 @@
 //
 // Both are bound by memory: a new token moves 4 d bytes per query head, 2 d per
 // key and value head in and 0.5625 d out, a read token 0.5625 d in and 2 d out.
-// A row (one head of one token) is handled by d / 8 lanes, 8 numbers (16 bytes
-// of bf16, 4 bytes of codes) each, so two neighbouring lanes share a scale.
 #include "ra_cache.cuh"
 
 namespace ra {
@@ -60,22 +58,40 @@ __device__ __forceinline__ uint32_t to_e4m3(float x) {
   return r;
 }
 
-// The scale byte of a group of 16 numbers held 8 each by lanes 2i and 2i + 1,
-// and the four code bytes of the caller's 8.
-__device__ __forceinline__ void quantise8(const float (&x)[8], uint32_t& codes, uint32_t& scale) {
+__device__ __forceinline__ float max8(const float (&x)[8]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = fminf(m, 6.f * 448.f);
-  const float q = div_odd(m, 6.f, 1.f / 6.f);
-  scale = to_e4m3(q);
-  if (scale == 0) scale = 1;  // 2^-9
-  const float s = f16x2_to_f32(e4m3x2_to_f16(scale)).x;
-  const float r = __frcp_rn(s);
-  codes = 0;
+  for (int i = 0; i < 8; i += 2) m = fmax3f(m, fabsf(x[i]), fabsf(x[i + 1]));
+  return m;
+}
+// The scale byte of a group whose largest magnitude is m, given as fp32 rounded to odd.
+__device__ __forceinline__ uint32_t scale_of(float m) {
+  const uint32_t s = to_e4m3(div_odd(fminf(m, 6.f * 448.f), 6.f, 1.f / 6.f));
+  return s ? s : 1u;  // at least 2^-9
+}
+// Four code bytes of 8 numbers of a group with the given scale byte.  ODD: the
+// numbers are rounded to odd; otherwise they are bf16, whose quotients by a scale
+// lie on a border or at least 2^-9 of it away, so that the rounded quotient (one correction step,
+// right to half a unit in the last place) is enough.
+template <bool ODD>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint32_t scale) {
+  const float s = f16x2_to_f32(e4m3x2_to_f16(scale)).x, r = __frcp_rn(s);
+  uint32_t codes = 0;
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) codes |= to_e2m1x2(div_odd(x[i], s, r), div_odd(x[i + 1], s, r)) << (4 * i);
+  for (int i = 0; i < 8; i += 2) {
+    float q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (ODD) {
+        q[k] = div_odd(x[i + k], s, r);
+      } else {
+        const float q0 = __fmul_rn(x[i + k], r);
+        q[k] = fabsf(q0) < 1e30f ? __fmaf_rn(__fmaf_rn(-q0, s, x[i + k]), r, q0) : q0;
+      }
+    }
+    codes |= to_e2m1x2(q[0], q[1]) << (4 * i);
+  }
+  return codes;
 }
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
@@ -91,93 +107,149 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// One warp: `passes` times 32 / (d / 8) rows of one token.  Rows are the query
-// heads, then the key heads, then the value heads.
-template <int D>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(AppendArgs a, int warps_per_token, int passes) {
-  constexpr int LPR = D / 8, RPP = 32 / LPR;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long gw = (long long)blockIdx.x * kWarps + warp;
-  const int t = (int)(gw / warps_per_token);
-  if (t >= a.s.total) return;
-  const int row0 = (int)(gw % warps_per_token) * passes * RPP;
-  const int i = segment_of_warp(a.s.cu, a.s.n_seqs, t);
-  const int n_end = __ldg(a.s.cu + i + 1);
-  const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
-  const int tok = len - n_end + t;
-  if (tok < 0) return;
-  const int c = lane % LPR, half = a.rot >> 4;  // this lane's 8 numbers; chunks in half the rotated part
-  float cs[8], sn[8];
-  if (a.rot) {
-    const int pos = a.positions ? __ldg(a.positions + t) : tok;
-    if ((unsigned)pos >= (unsigned)a.max_pos) {
-      if (lane == 0) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_POS);
-      return;
-    }
-    const bool inter = a.style == 1;
-    const int at = inter ? 4 * c : 8 * (c < half ? c : c - half);
-    const bool turn = 8 * c < a.rot;
-    const float4* pc = reinterpret_cast<const float4*>(a.cos_t + (long long)pos * a.cos_stride + at);
-    const float4* ps = reinterpret_cast<const float4*>(a.sin_t + (long long)pos * a.sin_stride + at);
-    const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 c0 = turn ? __ldg(pc) : one, s0 = turn ? __ldg(ps) : zero;
-    const float4 c1 = turn && !inter ? __ldg(pc + 1) : one, s1 = turn && !inter ? __ldg(ps + 1) : zero;
-    cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w, cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-    sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-  }
-  const int page = cache_page(a.s, a.c, i, tok, a.ctl);
-  if (page < 0) return;
-  const int prow = tok & ((1 << a.c.page_shift) - 1);
-  const int n_rows = a.h + 2 * a.hk;
-  for (int p = 0; p < passes; ++p) {
-    const int row = row0 + p * RPP + lane / LPR;
-    const bool live = row < n_rows;
-    const bool is_q = row < a.h, is_v = row >= a.h + a.hk;
-    const int head = is_q ? row : is_v ? row - a.h - a.hk : row - a.h;
-    const Rows3& src = is_q ? a.q : is_v ? a.v : a.k;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live)
-      w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src.data) + (long long)t * src.s_row +
-                                          (long long)head * src.s_head + 8 * c);
-    float x[8];
-    unpack8(w, x);
-    if (a.rot) {
-      const bool turn = !is_v && 8 * c < a.rot;
-      if (a.style == 1) {
+// A token's rows are the query heads, then the key heads, then the value heads. A
+// row is handled by d / 16 lanes with two 16-byte chunks each: the two that turn
+// together (l, l + r / 16) for pairs (i, i + r / 2), else neighbours (2l, 2l + 1).  Only
+// keys pay for the exact rotation and division (about 300 instructions for 16
+// numbers of a lane, 60 for a query's); they are a sixth of the rows of a model
+// with 4 query heads per key head.  A warp takes `per_warp` passes of 32 / (d / 16)
+// rows of one kind, with the token's table entries in registers.
+template <int D, int STYLE>  // 0: no rotation, 1: halves, 2: interleaved
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a, int warps_per_token, int per_warp) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const long long n_warps = (long long)a.s.total * warps_per_token;
+  for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
+    const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
+    const int i = segment_of_warp(a.s.cu, a.s.n_seqs, t);
+    const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
+    const int tok = len - __ldg(a.s.cu + i + 1) + t;
+    if (tok < 0) continue;
+    const int half = a.rot >> 4;  // chunks in half the rotated part
+    const bool turn = STYLE == 1 ? l < half : STYLE == 2 ? 16 * l < a.rot : false;
+    const int ca = STYLE == 1 && turn ? l : 2 * l, cb = STYLE == 1 && turn ? l + half : 2 * l + 1;
+    const bool own = cb == ca + 1 && !(ca & 1);  // both chunks are one scale group
+    float cs[8], sn[8];
+    if (STYLE) {
+      const int pos = a.positions ? __ldg(a.positions + t) : tok;
+      if ((unsigned)pos >= (unsigned)a.max_pos) {
+        if (lane == 0) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_POS);
+        continue;
+      }
+      const float4* pc = reinterpret_cast<const float4*>(a.cos_t + (long long)pos * a.cos_stride + 8 * l);
+      const float4* ps = reinterpret_cast<const float4*>(a.sin_t + (long long)pos * a.sin_stride + 8 * l);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float xa = x[2 * u], xb = x[2 * u + 1];
-          if (turn) {
-            x[2 * u] = dot2_odd(xa, cs[u], -xb, sn[u]);
-            x[2 * u + 1] = dot2_odd(xb, cs[u], xa, sn[u]);
-          }
-        }
-      } else {
-        const bool first = c < half;
-        const int from = lane - c + (turn ? (first ? c + half : c - half) : c);
-        uint4 z;
-        z.x = __shfl_sync(0xffffffffu, w.x, from);
-        z.y = __shfl_sync(0xffffffffu, w.y, from);
-        z.z = __shfl_sync(0xffffffffu, w.z, from);
-        z.w = __shfl_sync(0xffffffffu, w.w, from);
-        float y[8];
-        unpack8(z, y);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (turn) x[u] = dot2_odd(x[u], cs[u], first ? -y[u] : y[u], sn[u]);
+      for (int k = 0; k < 2; ++k) {
+        const float4 c = turn ? __ldg(pc + k) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 s = turn ? __ldg(ps + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
+        sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
       }
     }
-    uint32_t codes, scale;
-    quantise8(x, codes, scale);
-    if (!live) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out.data) + (long long)t * a.q_out.s_row +
-                                (long long)head * a.q_out.s_head + 8 * c) = pack8(x);
-    } else {
-      const CacheRows& cr = is_v ? a.c.v : a.c.k;
-      const CacheRows& sr = is_v ? a.c.vs : a.c.ks;
-      *reinterpret_cast<uint32_t*>(cr.data + row_offset(cr, page, head, prow) + 4 * c) = codes;
-      if (!(c & 1)) sr.data[row_offset(sr, page, head, prow) + (c >> 1)] = (uint8_t)scale;
+    const int page = cache_page(a.s, a.c, i, tok, a.ctl);
+    if (page < 0) continue;
+    const int prow = tok & ((1 << a.c.page_shift) - 1);
+    const int nq = (a.h + RPP - 1) / RPP, nk = (a.hk + RPP - 1) / RPP;
+    const int p_end = min(nq + 2 * nk, (part + 1) * per_warp);
+    int p = part * per_warp;
+
+    // queries
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + (long long)t * a.q.s_row;
+    __nv_bfloat16* qo = static_cast<__nv_bfloat16*>(a.q_out.data) + (long long)t * a.q_out.s_row;
+#pragma unroll 2
+    for (; p < min(nq, p_end); ++p) {
+      const int head = p * RPP + sub;
+      if (head >= a.h) continue;
+      const __nv_bfloat16* src = q + head * a.q.s_head;
+      __nv_bfloat16* dst = qo + head * a.q_out.s_head;
+      const uint4 wa = *reinterpret_cast<const uint4*>(src + 8 * ca), wb = *reinterpret_cast<const uint4*>(src + 8 * cb);
+      if (STYLE == 0) {
+        *reinterpret_cast<uint4*>(dst + 8 * ca) = wa;
+        *reinterpret_cast<uint4*>(dst + 8 * cb) = wb;
+        continue;
+      }
+      float x[8], y[8], u[8], v[8];
+      unpack8(wa, x);
+      unpack8(wb, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (STYLE == 1) {
+          u[k] = x[k] * cs[k] - y[k] * sn[k], u[k + 4] = x[k + 4] * cs[k + 4] - y[k + 4] * sn[k + 4];
+          v[k] = y[k] * cs[k] + x[k] * sn[k], v[k + 4] = y[k + 4] * cs[k + 4] + x[k + 4] * sn[k + 4];
+        } else {
+          u[2 * k] = x[2 * k] * cs[k] - x[2 * k + 1] * sn[k], u[2 * k + 1] = x[2 * k + 1] * cs[k] + x[2 * k] * sn[k];
+          v[2 * k] = y[2 * k] * cs[k + 4] - y[2 * k + 1] * sn[k + 4];
+          v[2 * k + 1] = y[2 * k + 1] * cs[k + 4] + y[2 * k] * sn[k + 4];
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + 8 * ca) = turn ? pack8(u) : wa;
+      *reinterpret_cast<uint4*>(dst + 8 * cb) = turn ? pack8(v) : wb;
+    }
+    // keys
+    for (; p < min(nq + nk, p_end); ++p) {
+      const int head = (p - nq) * RPP + sub;
+      const bool live = head < a.hk;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k.data) + (long long)t * a.k.s_row + head * a.k.s_head;
+      uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+      if (live) wa = *reinterpret_cast<const uint4*>(src + 8 * ca), wb = *reinterpret_cast<const uint4*>(src + 8 * cb);
+      float x[8], y[8], u[8], v[8];
+      unpack8(wa, x);
+      unpack8(wb, y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = x[k], v[k] = y[k];
+      if (STYLE && turn) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (STYLE == 1) {
+#pragma unroll
+            for (int j = k; j < 8; j += 4) {
+              u[j] = dot2_odd(x[j], cs[j], -y[j], sn[j]);
+              v[j] = dot2_odd(y[j], cs[j], x[j], sn[j]);
+            }
+          } else {
+            u[2 * k] = dot2_odd(x[2 * k], cs[k], -x[2 * k + 1], sn[k]);
+            u[2 * k + 1] = dot2_odd(x[2 * k + 1], cs[k], x[2 * k], sn[k]);
+            v[2 * k] = dot2_odd(y[2 * k], cs[k + 4], -y[2 * k + 1], sn[k + 4]);
+            v[2 * k + 1] = dot2_odd(y[2 * k + 1], cs[k + 4], y[2 * k], sn[k + 4]);
+          }
+        }
+      }
+      float ma = max8(u), mb = max8(v);
+      if (STYLE == 1) {  // groups shared with the neighbour lane
+        const float oa = __shfl_xor_sync(0xffffffffu, ma, 1), ob = __shfl_xor_sync(0xffffffffu, mb, 1);
+        ma = own ? fmaxf(ma, mb) : fmaxf(ma, oa);
+        mb = own ? ma : fmaxf(mb, ob);
+      } else {
+        ma = mb = fmaxf(ma, mb);
+      }
+      const uint32_t sa = scale_of(ma), sbb = STYLE == 1 ? scale_of(mb) : sa;
+      const uint32_t xa = codes_of<true>(u, sa), xb = codes_of<true>(v, sbb);
+      if (!live) continue;
+      uint8_t* row = a.c.k.data + row_offset(a.c.k, page, head, prow);
+      uint8_t* srow = a.c.ks.data + row_offset(a.c.ks, page, head, prow);
+      if (own) {
+        *reinterpret_cast<uint2*>(row + 4 * ca) = make_uint2(xa, xb);
+        srow[ca >> 1] = (uint8_t)sa;
+      } else {
+        *reinterpret_cast<uint32_t*>(row + 4 * ca) = xa;
+        *reinterpret_cast<uint32_t*>(row + 4 * cb) = xb;
+        if (!(l & 1)) srow[ca >> 1] = (uint8_t)sa, srow[cb >> 1] = (uint8_t)sbb;
+      }
+    }
+    // values: a lane's neighbouring chunks are one group
+    for (; p < p_end; ++p) {
+      const int head = (p - nq - nk) * RPP + sub;
+      if (head >= a.hk) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v.data) +
+                                                        (long long)t * a.v.s_row + head * a.v.s_head + 16 * l);
+      const uint4 wa = src[0], wb = src[1];
+      float x[8], y[8];
+      unpack8(wa, x);
+      unpack8(wb, y);
+      const uint32_t sc = scale_of(fmaxf(max8(x), max8(y)));
+      *reinterpret_cast<uint2*>(a.c.v.data + row_offset(a.c.v, page, head, prow) + 8 * l) =
+          make_uint2(codes_of<false>(x, sc), codes_of<false>(y, sc));
+      a.c.vs.data[row_offset(a.c.vs, page, head, prow) + l] = (uint8_t)sc;
     }
   }
 }
@@ -220,15 +292,30 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadArgs a) {
 
 }  // namespace
 
-cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
-  const int rpp = 256 / a.d, need = (a.h + 2 * a.hk + rpp - 1) / rpp;  // passes for all rows of a token
-  const int passes = 1;
-  const int wpt = (need + passes - 1) / passes;
+template <int D>
+void launch_append(const AppendArgs& a, cudaStream_t st) {
+  constexpr int RPP = 512 / D;  // rows per pass
+  const int passes = (a.h + RPP - 1) / RPP + 2 * ((a.hk + RPP - 1) / RPP);
+  // a warp for a whole token, or for fewer passes while that leaves SMs without warps
+  const long long want = (long long)num_sms() * 32;
+  int per_warp = passes;
+  while (per_warp > 1 && (long long)a.s.total * ((passes + per_warp - 1) / per_warp) < want) per_warp = (per_warp + 1) / 2;
+  const int wpt = (passes + per_warp - 1) / per_warp;
   const long long blocks = ((long long)a.s.total * wpt + kWarps - 1) / kWarps;
-  if (a.d == 64)
-    cache_append_kernel<64><<<(unsigned)blocks, kThreads, 0, st>>>(a, wpt, passes);
+  const unsigned grid = (unsigned)(blocks < (1LL << 30) ? blocks : (1LL << 30));
+  if (!a.rot)
+    cache_append_kernel<D, 0><<<grid, kThreads, 0, st>>>(a, wpt, per_warp);
+  else if (a.style == 0)
+    cache_append_kernel<D, 1><<<grid, kThreads, 0, st>>>(a, wpt, per_warp);
   else
-    cache_append_kernel<128><<<(unsigned)blocks, kThreads, 0, st>>>(a, wpt, passes);
+    cache_append_kernel<D, 2><<<grid, kThreads, 0, st>>>(a, wpt, per_warp);
+}
+
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
+  if (a.d == 64)
+    launch_append<64>(a, st);
+  else
+    launch_append<128>(a, st);
   return cudaGetLastError();
 }
 

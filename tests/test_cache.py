@@ -110,7 +110,8 @@ def test_append_refuses(lib):
     assert append(lib, cos=t()) == 1 and append(lib, sin=t()) == 1
     assert append(lib, cos=t(), sin=t(99)) == 1 and append(lib, cos=t(), sin=t(100, 16)) == 1
     assert append(lib, cos=t(r=40), sin=t(r=40)) == 1                # more than d head dims
-    assert append(lib, cos=t(r=12), sin=t(r=12)) == 1                # not a multiple of 16 head dims
+    assert append(lib, cos=t(r=12), sin=t(r=12)) == 1                # 24 head dims: not 16, not a multiple of 32
+    assert append(lib, cos=t(r=24), sin=t(r=24)) == 1
     assert append(lib, cos=fake((100, 32)), sin=t()) == 1            # bf16 table
     assert append(lib, cos=t(data=0x100004), sin=t()) == 3
     assert append(lib, cos=t(stride=(33, 1)), sin=t()) == 3

@@ -40,7 +40,10 @@ APPEND = [
     ((37, 0, 1, 130), (37, 5, 64, 200), 6, 3, 128, 16, 64, False, (0, 2, 1)),
     ((70, 3), (71, 1030), 5, 1, 64, 256, 32, True, (1, 0, 2)),
     ((70, 3), (71, 1030), 14, 2, 128, 128, 16, False, (2, 1, 0)),
-    ((600,), (613,), 2, 2, 64, 64, 48, False, (0, 2, 1)),
+    ((600,), (613,), 2, 2, 64, 64, 32, False, (0, 2, 1)),
+    ((9, 20), (9, 33), 3, 3, 128, 32, 96, False, (0, 1, 2)),
+    ((9, 20), (9, 33), 10, 5, 128, 32, 16, True, (0, 1, 2)),
+    ((12,), (12,), 5, 5, 64, 16, 64, False, (0, 1, 2)),
 ]
 
 
