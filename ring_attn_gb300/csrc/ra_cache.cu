@@ -254,61 +254,108 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
   }
 }
 
-// One warp: 32 / (d / 8) rows at a time of one token; rows are the key heads, then the value heads.
-template <int D>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadArgs a) {
-  constexpr int LPR = D / 8, RPP = 32 / LPR;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= a.s.total) return;
-  const int i = segment_of_warp(a.s.cu, a.s.n_seqs, t);
-  const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
-  const int tok = len - __ldg(a.s.cu + i + 1) + t;
-  if (tok < 0) return;
-  const int page = cache_page(a.s, a.c, i, tok, a.ctl);
-  if (page < 0) return;
-  const int prow = tok & ((1 << a.c.page_shift) - 1);
-  const int c = lane % LPR;
-  for (int row = lane / LPR; row < 2 * a.hk; row += RPP) {
-    const bool is_v = row >= a.hk;
-    const int head = is_v ? row - a.hk : row;
-    const CacheRows& cr = is_v ? a.c.v : a.c.k;
-    const CacheRows& sr = is_v ? a.c.vs : a.c.ks;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(cr.data + row_offset(cr, page, head, prow) + 4 * c);
-    const uint32_t s2 = half_lo2(e4m3x2_to_f16(sr.data[row_offset(sr, page, head, prow) + (c >> 1)]));
-    uint32_t r[4];
-    e2m1x8_to_f16(w, r);
-    float x[8];
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// A lane turns one scale group (8 code bytes) into 16 bf16 numbers, d / 16 lanes a
+// row; a warp takes `per_warp` passes over the rows of one token, first the key
+// heads, then the value heads, kUnroll passes' loads in flight.
+// WIDE: rows of the outputs start on 32-byte boundaries, so a lane stores at once.
+constexpr int kReadUnroll = 4;
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a, int warps_per_token, int per_warp) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const long long n_warps = (long long)a.s.total * warps_per_token;
+  for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
+    const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
+    const int i = segment_of_warp(a.s.cu, a.s.n_seqs, t);
+    const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
+    const int tok = len - __ldg(a.s.cu + i + 1) + t;
+    if (tok < 0) continue;
+    const int page = cache_page(a.s, a.c, i, tok, a.ctl);
+    if (page < 0) continue;
+    const int prow = tok & ((1 << a.c.page_shift) - 1);
+    const long long oc = (long long)page * a.c.k.s_page + prow * (int)a.c.k.s_row + 8 * l;
+    const long long os = (long long)page * a.c.ks.s_page + prow * (int)a.c.ks.s_row + l;
+    const int end = min(2 * a.hk, (part + 1) * per_warp * RPP);
+    for (int row0 = part * per_warp * RPP + sub; row0 < end; row0 += kReadUnroll * RPP) {
+      uint2 w[kReadUnroll];
+      uint32_t sc[kReadUnroll];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float2 f = f16x2_to_f32(hmul2(r[u], s2));
-      x[2 * u] = f.x, x[2 * u + 1] = f.y;
+      for (int k = 0; k < kReadUnroll; ++k) {
+        const int row = row0 + k * RPP;
+        if (row < end) {
+          const bool is_v = row >= a.hk;
+          const int head = is_v ? row - a.hk : row;
+          w[k] = __ldg(reinterpret_cast<const uint2*>((is_v ? a.c.v.data : a.c.k.data) + oc + head * a.c.k.s_head));
+          sc[k] = __ldg((is_v ? a.c.vs.data : a.c.ks.data) + os + head * a.c.ks.s_head);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kReadUnroll; ++k) {
+        const int row = row0 + k * RPP;
+        if (row < end) {
+          const bool is_v = row >= a.hk;
+          const int head = is_v ? row - a.hk : row;
+          const uint32_t s2 = half_lo2(e4m3x2_to_f16(sc[k]));
+          uint32_t r[4], o[8];
+          e2m1x8_to_f16(w[k].x, r);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 f = f16x2_to_f32(hmul2(r[u], s2));
+            o[u] = pack_bf16x2(f.x, f.y);
+          }
+          e2m1x8_to_f16(w[k].y, r);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 f = f16x2_to_f32(hmul2(r[u], s2));
+            o[4 + u] = pack_bf16x2(f.x, f.y);
+          }
+          const Rows3& to = is_v ? a.v_out : a.k_out;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(to.data) + (long long)t * to.s_row + head * to.s_head + 16 * l;
+          if (WIDE) {
+            store32(dst, o);
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      }
     }
-    const Rows3& o = is_v ? a.v_out : a.k_out;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o.data) + (long long)t * o.s_row +
-                              (long long)head * o.s_head + 8 * c) = pack8(x);
   }
 }
 
 }  // namespace
 
+// A warp takes a whole token, or fewer of its passes while that leaves SMs without warps.
+struct Share {
+  int warps_per_token, per_warp;
+  unsigned grid;
+};
+static Share share_of(long long tokens, int passes) {
+  const long long want = (long long)num_sms() * 32;
+  int per_warp = passes;
+  while (per_warp > 1 && tokens * ((passes + per_warp - 1) / per_warp) < want) per_warp = (per_warp + 1) / 2;
+  const int wpt = (passes + per_warp - 1) / per_warp;
+  const long long blocks = (tokens * wpt + kWarps - 1) / kWarps;
+  return Share{wpt, per_warp, (unsigned)(blocks < (1LL << 30) ? blocks : (1LL << 30))};
+}
+
 template <int D>
 void launch_append(const AppendArgs& a, cudaStream_t st) {
   constexpr int RPP = 512 / D;  // rows per pass
   const int passes = (a.h + RPP - 1) / RPP + 2 * ((a.hk + RPP - 1) / RPP);
-  // a warp for a whole token, or for fewer passes while that leaves SMs without warps
-  const long long want = (long long)num_sms() * 32;
-  int per_warp = passes;
-  while (per_warp > 1 && (long long)a.s.total * ((passes + per_warp - 1) / per_warp) < want) per_warp = (per_warp + 1) / 2;
-  const int wpt = (passes + per_warp - 1) / per_warp;
-  const long long blocks = ((long long)a.s.total * wpt + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)(blocks < (1LL << 30) ? blocks : (1LL << 30));
+  const Share s = share_of(a.s.total, passes);
   if (!a.rot)
-    cache_append_kernel<D, 0><<<grid, kThreads, 0, st>>>(a, wpt, per_warp);
+    cache_append_kernel<D, 0><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
   else if (a.style == 0)
-    cache_append_kernel<D, 1><<<grid, kThreads, 0, st>>>(a, wpt, per_warp);
+    cache_append_kernel<D, 1><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
   else
-    cache_append_kernel<D, 2><<<grid, kThreads, 0, st>>>(a, wpt, per_warp);
+    cache_append_kernel<D, 2><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
@@ -319,12 +366,25 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)((a.s.total + kWarps - 1) / kWarps);
-  if (a.d == 64)
-    cache_read_kernel<64><<<blocks, kThreads, 0, st>>>(a);
+template <int D>
+void launch_read(const ReadArgs& a, cudaStream_t st) {
+  constexpr int RPP = 512 / D;
+  const int passes = (2 * a.hk + RPP - 1) / RPP;
+  const Share s = share_of(a.s.total, passes);
+  auto wide = [](const Rows3& r) {
+    return reinterpret_cast<uintptr_t>(r.data) % 32 == 0 && r.s_row % 16 == 0 && r.s_head % 16 == 0;
+  };
+  if (wide(a.k_out) && wide(a.v_out))
+    cache_read_kernel<D, true><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
   else
-    cache_read_kernel<128><<<blocks, kThreads, 0, st>>>(a);
+    cache_read_kernel<D, false><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
+}
+
+cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t st) {
+  if (a.d == 64)
+    launch_read<64>(a, st);
+  else
+    launch_read<128>(a, st);
   return cudaGetLastError();
 }
 
