@@ -107,17 +107,71 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
+// sure_scale and sure_codes: scale_of and codes_of for numbers known to within
+// `off`, setting `unsure` where that leaves two answers.
+__device__ __forceinline__ uint32_t sure_scale(float m, float off, bool& unsure) {
+  const float q = fminf(m, 6.f * 448.f) * (1.f / 6.f), d = fmaf(q, 0x1p-22f, off);
+  const uint32_t lo = to_e4m3(q - d), hi = to_e4m3(q + d);
+  unsure |= lo != hi;
+  return hi ? hi : 1u;
+}
+__device__ __forceinline__ uint32_t sure_codes(const float (&x)[8], uint32_t scale, float off, bool& unsure) {
+  const float s = f16x2_to_f32(e4m3x2_to_f16(scale)).x, r = __frcp_rn(s);
+  const float d = fmaf(off, r, 0x1p-19f);  // quotients up to 8 in fp32 are off by less than the second part
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    lo |= to_e2m1x2(fmaf(x[i], r, -d), fmaf(x[i + 1], r, -d)) << (4 * i);
+    hi |= to_e2m1x2(fmaf(x[i], r, d), fmaf(x[i + 1], r, d)) << (4 * i);
+  }
+  unsure |= lo != hi;
+  return hi;
+}
+
+// The two chunks x, y of a lane turned by its table entries; f(a, c, b, d) = a c + b d.
+template <int STYLE, class F>
+__device__ __forceinline__ void rotate16(const float (&x)[8], const float (&y)[8], const float (&cs)[8],
+                                         const float (&sn)[8], bool turn, float (&u)[8], float (&v)[8], F f) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (STYLE == 1) {
+#pragma unroll
+      for (int j = k; j < 8; j += 4) {
+        u[j] = turn ? f(x[j], cs[j], -y[j], sn[j]) : x[j];
+        v[j] = turn ? f(y[j], cs[j], x[j], sn[j]) : y[j];
+      }
+    } else {
+      u[2 * k] = turn ? f(x[2 * k], cs[k], -x[2 * k + 1], sn[k]) : x[2 * k];
+      u[2 * k + 1] = turn ? f(x[2 * k + 1], cs[k], x[2 * k], sn[k]) : x[2 * k + 1];
+      v[2 * k] = turn ? f(y[2 * k], cs[k + 4], -y[2 * k + 1], sn[k + 4]) : y[2 * k];
+      v[2 * k + 1] = turn ? f(y[2 * k + 1], cs[k + 4], y[2 * k], sn[k + 4]) : y[2 * k + 1];
+    }
+  }
+}
+// Largest magnitudes of the scale groups of a lane's two chunks, which it has whole (own) or
+// shares with its neighbour.
+template <int STYLE>
+__device__ __forceinline__ void group_max(const float (&u)[8], const float (&v)[8], bool own, float& ma, float& mb) {
+  ma = max8(u), mb = max8(v);
+  if (STYLE == 1) {
+    const float oa = __shfl_xor_sync(0xffffffffu, ma, 1), ob = __shfl_xor_sync(0xffffffffu, mb, 1);
+    ma = own ? fmaxf(ma, mb) : fmaxf(ma, oa);
+    mb = own ? ma : fmaxf(mb, ob);
+  } else {
+    ma = mb = fmaxf(ma, mb);
+  }
+}
+
 // A token's rows are the query heads, then the key heads, then the value heads. A
 // row is handled by d / 16 lanes with two 16-byte chunks each: the two that turn
 // together (l, l + r / 16) for pairs (i, i + r / 2), else neighbours (2l, 2l + 1).  Only
-// keys pay for the exact rotation and division (about 300 instructions for 16
-// numbers of a lane, 60 for a query's); they are a sixth of the rows of a model
-// with 4 query heads per key head.  A warp takes `per_warp` passes of 32 / (d / 16)
+// keys ask for more than fp32 (see dot2_odd), and few of them take that way.  A warp takes `per_warp` passes of 32 / (d / 16)
 // rows of one kind, with the token's table entries in registers.
 template <int D, int STYLE>  // 0: no rotation, 1: halves, 2: interleaved
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a, int warps_per_token, int per_warp) {
+__global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendArgs a, int warps_per_token, int per_warp) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  after_previous_kernel();
   const long long n_warps = (long long)a.s.total * warps_per_token;
   for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
     const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
@@ -146,9 +200,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
         sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
       }
     }
-    const int page = cache_page(a.s, a.c, i, tok, a.ctl);
-    if (page < 0) continue;
-    const int prow = tok & ((1 << a.c.page_shift) - 1);
+    const int at_table = __ldg(a.s.table + (long long)i * a.s.table_stride + (tok >> a.c.page_shift));  // used below
     const int nq = (a.h + RPP - 1) / RPP, nk = (a.hk + RPP - 1) / RPP;
     const int p_end = min(nq + 2 * nk, (part + 1) * per_warp);
     int p = part * per_warp;
@@ -171,20 +223,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       float x[8], y[8], u[8], v[8];
       unpack8(wa, x);
       unpack8(wb, y);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (STYLE == 1) {
-          u[k] = x[k] * cs[k] - y[k] * sn[k], u[k + 4] = x[k + 4] * cs[k + 4] - y[k + 4] * sn[k + 4];
-          v[k] = y[k] * cs[k] + x[k] * sn[k], v[k + 4] = y[k + 4] * cs[k + 4] + x[k + 4] * sn[k + 4];
-        } else {
-          u[2 * k] = x[2 * k] * cs[k] - x[2 * k + 1] * sn[k], u[2 * k + 1] = x[2 * k + 1] * cs[k] + x[2 * k] * sn[k];
-          v[2 * k] = y[2 * k] * cs[k + 4] - y[2 * k + 1] * sn[k + 4];
-          v[2 * k + 1] = y[2 * k + 1] * cs[k + 4] + y[2 * k] * sn[k + 4];
-        }
-      }
+      rotate16<STYLE>(x, y, cs, sn, true, u, v, [](float p, float c, float q, float d) { return fmaf(p, c, q * d); });
       *reinterpret_cast<uint4*>(dst + 8 * ca) = turn ? pack8(u) : wa;
       *reinterpret_cast<uint4*>(dst + 8 * cb) = turn ? pack8(v) : wb;
     }
+    if (p >= p_end) continue;
+    const int page = check_page(a.c, at_table, a.ctl), prow = tok & ((1 << a.c.page_shift) - 1);
+    if (page < 0) continue;
     // keys
     for (; p < min(nq + nk, p_end); ++p) {
       const int head = (p - nq) * RPP + sub;
@@ -195,35 +240,31 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       float x[8], y[8], u[8], v[8];
       unpack8(wa, x);
       unpack8(wb, y);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = x[k], v[k] = y[k];
-      if (STYLE && turn) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (STYLE == 1) {
-#pragma unroll
-            for (int j = k; j < 8; j += 4) {
-              u[j] = dot2_odd(x[j], cs[j], -y[j], sn[j]);
-              v[j] = dot2_odd(y[j], cs[j], x[j], sn[j]);
-            }
-          } else {
-            u[2 * k] = dot2_odd(x[2 * k], cs[k], -x[2 * k + 1], sn[k]);
-            u[2 * k + 1] = dot2_odd(x[2 * k + 1], cs[k], x[2 * k], sn[k]);
-            v[2 * k] = dot2_odd(y[2 * k], cs[k + 4], -y[2 * k + 1], sn[k + 4]);
-            v[2 * k + 1] = dot2_odd(y[2 * k + 1], cs[k + 4], y[2 * k], sn[k + 4]);
-          }
+      uint32_t sa, sbb, xa, xb;
+      if (STYLE == 0) {
+        sa = sbb = scale_of(fmaxf(max8(x), max8(y)));
+        xa = codes_of<false>(x, sa), xb = codes_of<false>(y, sa);
+      } else {
+        // The fp32 rotation, with bounds: where the scale or a code would come out
+        // otherwise for numbers a little off (about one row in a few hundred) the
+        // warp takes the exact way below.
+        float in = fmaxf(max8(x), max8(y)) * fmaxf(1.f, fmaxf(max8(cs), max8(sn)));
+        in = fmaxf(in, __shfl_xor_sync(0xffffffffu, in, 1));
+        bool unsure = !(in < 1e30f);
+        rotate16<STYLE>(x, y, cs, sn, turn, u, v, [](float p, float c, float q, float d) { return fmaf(p, c, q * d); });
+        // two products of size up to `in` and their sum: off by at most 3 * 2^-24 of it
+        const float off = in * 0x1p-22f;
+        float ma, mb;
+        group_max<STYLE>(u, v, own, ma, mb);
+        sa = sure_scale(ma, off, unsure), sbb = STYLE == 1 ? sure_scale(mb, off, unsure) : sa;
+        xa = sure_codes(u, sa, off, unsure), xb = sure_codes(v, sbb, off, unsure);
+        if (__any_sync(0xffffffffu, unsure)) {
+          rotate16<STYLE>(x, y, cs, sn, turn, u, v, dot2_odd);
+          group_max<STYLE>(u, v, own, ma, mb);
+          sa = scale_of(ma), sbb = STYLE == 1 ? scale_of(mb) : sa;
+          xa = codes_of<true>(u, sa), xb = codes_of<true>(v, sbb);
         }
       }
-      float ma = max8(u), mb = max8(v);
-      if (STYLE == 1) {  // groups shared with the neighbour lane
-        const float oa = __shfl_xor_sync(0xffffffffu, ma, 1), ob = __shfl_xor_sync(0xffffffffu, mb, 1);
-        ma = own ? fmaxf(ma, mb) : fmaxf(ma, oa);
-        mb = own ? ma : fmaxf(mb, ob);
-      } else {
-        ma = mb = fmaxf(ma, mb);
-      }
-      const uint32_t sa = scale_of(ma), sbb = STYLE == 1 ? scale_of(mb) : sa;
-      const uint32_t xa = codes_of<true>(u, sa), xb = codes_of<true>(v, sbb);
       if (!live) continue;
       uint8_t* row = a.c.k.data + row_offset(a.c.k, page, head, prow);
       uint8_t* srow = a.c.ks.data + row_offset(a.c.ks, page, head, prow);
@@ -269,6 +310,7 @@ template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a, int warps_per_token, int per_warp) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  after_previous_kernel();
   const long long n_warps = (long long)a.s.total * warps_per_token;
   for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
     const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
@@ -346,28 +388,23 @@ static Share share_of(long long tokens, int passes) {
 }
 
 template <int D>
-void launch_append(const AppendArgs& a, cudaStream_t st) {
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
   constexpr int RPP = 512 / D;  // rows per pass
   const int passes = (a.h + RPP - 1) / RPP + 2 * ((a.hk + RPP - 1) / RPP);
   const Share s = share_of(a.s.total, passes);
   if (!a.rot)
-    cache_append_kernel<D, 0><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
-  else if (a.style == 0)
-    cache_append_kernel<D, 1><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
-  else
-    cache_append_kernel<D, 2><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
+    return launch_early(cache_append_kernel<D, 0>, s.grid, kThreads, 0, st, a, s.warps_per_token, s.per_warp);
+  if (a.style == 0)
+    return launch_early(cache_append_kernel<D, 1>, s.grid, kThreads, 0, st, a, s.warps_per_token, s.per_warp);
+  return launch_early(cache_append_kernel<D, 2>, s.grid, kThreads, 0, st, a, s.warps_per_token, s.per_warp);
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
-  if (a.d == 64)
-    launch_append<64>(a, st);
-  else
-    launch_append<128>(a, st);
-  return cudaGetLastError();
+  return a.d == 64 ? launch_append<64>(a, st) : launch_append<128>(a, st);
 }
 
 template <int D>
-void launch_read(const ReadArgs& a, cudaStream_t st) {
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t st) {
   constexpr int RPP = 512 / D;
   const int passes = (2 * a.hk + RPP - 1) / RPP;
   const Share s = share_of(a.s.total, passes);
@@ -375,17 +412,12 @@ void launch_read(const ReadArgs& a, cudaStream_t st) {
     return reinterpret_cast<uintptr_t>(r.data) % 32 == 0 && r.s_row % 16 == 0 && r.s_head % 16 == 0;
   };
   if (wide(a.k_out) && wide(a.v_out))
-    cache_read_kernel<D, true><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
-  else
-    cache_read_kernel<D, false><<<s.grid, kThreads, 0, st>>>(a, s.warps_per_token, s.per_warp);
+    return launch_early(cache_read_kernel<D, true>, s.grid, kThreads, 0, st, a, s.warps_per_token, s.per_warp);
+  return launch_early(cache_read_kernel<D, false>, s.grid, kThreads, 0, st, a, s.warps_per_token, s.per_warp);
 }
 
 cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t st) {
-  if (a.d == 64)
-    launch_read<64>(a, st);
-  else
-    launch_read<128>(a, st);
-  return cudaGetLastError();
+  return a.d == 64 ? launch_read<64>(a, st) : launch_read<128>(a, st);
 }
 
 }  // namespace ra

@@ -8,6 +8,30 @@
 
 namespace ra {
 
+// The cache's kernels are launched so that their blocks may be set up while the
+// stream's previous kernel still runs (programmatic dependent launch): every
+// kernel calls after_previous_kernel before it touches memory, which waits until
+// that kernel has ended and its writes are visible, and allows the same to the next one.
+// Saves about 2 us a launch for single tokens.
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Sites of device-side errors in the low byte of check_device_error's info.
 enum : int { SITE_CACHE_LEN = 0x61, SITE_CACHE_PAGE = 0x62, SITE_CACHE_POS = 0x63 };
 
@@ -20,14 +44,17 @@ __device__ __forceinline__ int cache_len(const CacheSeqs& s, int i, int bound, c
   return n;
 }
 
-// Physical page of token `tok` of sequence i (0 <= tok < max_pages * page), or -1.
-__device__ __forceinline__ int cache_page(const CacheSeqs& s, const CacheView& c, int i, int tok, const DevCtl& ctl) {
-  const int pg = __ldg(s.table + (long long)i * s.table_stride + (tok >> c.page_shift));
+// A page number of the table, or -1 (recorded) when there is no such page.
+__device__ __forceinline__ int check_page(const CacheView& c, int pg, const DevCtl& ctl) {
   if ((unsigned)pg >= (unsigned)c.n_pages) {
     record_error(ctl, DEV_BOUNDS, SITE_CACHE_PAGE);
     return -1;
   }
   return pg;
+}
+// Physical page of token `tok` of sequence i (0 <= tok < max_pages * page), or -1.
+__device__ __forceinline__ int cache_page(const CacheSeqs& s, const CacheView& c, int i, int tok, const DevCtl& ctl) {
+  return check_page(c, __ldg(s.table + (long long)i * s.table_stride + (tok >> c.page_shift)), ctl);
 }
 
 __device__ __forceinline__ long long row_offset(const CacheRows& r, int page, int head, int row) {

@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t sb = smem_u32(smem), ring = sb + warp * L::kStages * L::kStage;
 
+  after_previous_kernel();
   LinePos at;
   long long end_u, quota;
   JoinNote note = empty_note();
@@ -578,11 +579,9 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cudaError_t e = configure_kernel<cache_attn_kernel<D, NT>>(0, L::kBytes);
   if (e != cudaSuccess) return e;
   const int grid = num_sms() * blocks_per_sm(NT);
-  cache_attn_kernel<D, NT><<<grid, kThreads, L::kBytes, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(cache_attn_kernel<D, NT>, grid, kThreads, L::kBytes, st, a);
   if (e != cudaSuccess) return e;
-  cache_join_kernel<L::R, D><<<dim3(grid, NT), 256 * kJoinGroups, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(cache_join_kernel<L::R, D>, dim3(grid, NT), 256 * kJoinGroups, 0, st, a);
 }
 
 }  // namespace

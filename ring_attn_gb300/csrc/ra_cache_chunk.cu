@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     *abort_flag = 0;
     fence_mbar_init();
   }
+  after_previous_kernel();
   LinePos at;
   long long end_u, quota;
   JoinNote note = empty_note();
@@ -567,11 +568,9 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cudaError_t e = configure_kernel<cache_chunk_kernel<D>>(kLaunchRegs, Lay<D>::kAlloc);
   if (e != cudaSuccess) return e;
   const int grid = num_sms();
-  cache_chunk_kernel<D><<<grid, kThreads, Lay<D>::kAlloc, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(cache_chunk_kernel<D>, grid, kThreads, Lay<D>::kAlloc, st, a);
   if (e != cudaSuccess) return e;
-  cache_join_kernel<256, D><<<dim3(grid, 32), 256 * kJoinGroups, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(cache_join_kernel<256, D>, dim3(grid, 32), 256 * kJoinGroups, 0, st, a);
 }
 
 }  // namespace

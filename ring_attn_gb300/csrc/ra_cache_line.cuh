@@ -260,6 +260,7 @@ template <int R, int D>
 __global__ void __launch_bounds__(32 * 8 * kJoinGroups) cache_join_kernel(const CacheAttnArgs g) {
   constexpr int V = D / 32;
   __shared__ float so[8][D], sm[8][2];
+  after_previous_kernel();
   const JoinNote* notes = notes_of(g);
   const JoinNote n = notes[blockIdx.x];
   if (n.last < 0) return;
