@@ -46,18 +46,32 @@ def seqs(cu=(0, 3, 10), **over):
 FAR = 0x9000000
 
 
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def test_packed_arguments_have_the_structures_layout():
+    assert len(ra._PACK_TENSOR(*range(11))) == ctypes.sizeof(ra._Tensor)
+    assert len(ra._PACK_SEQS(*range(7))) == ctypes.sizeof(ra._KVSeqs)
+    assert bytes(fake((2, 3, 4), data=4096)) == ra._PACK_TENSOR(4096, ra.RA_BF16, 3, 2, 3, 4, 0, 12, 4, 1, 0)
+    s = ra._KVSeqs(*range(1, 8))
+    assert bytes(s) == ra._PACK_SEQS(*range(1, 8))
+
+
 def append(lib, c=None, s=None, q=None, k=None, v=None, cos=None, sin=None, rope=0, pos=None, out=None):
-    return lib.ring_attn_cache_append(q, k or fake((10, 2, 64)), v or fake((10, 2, 64)), cos, sin, rope, pos,
-                                      c or cache(), s or seqs(), out, None)
+    r = [ref(x) for x in (q, k or fake((10, 2, 64)), v or fake((10, 2, 64)), cos, sin, c or cache(), s or seqs(), out)]
+    return lib.ring_attn_cache_append(*r[:5], rope, pos, *r[5:], None)
 
 
 def attend(lib, c=None, s=None, q=None, out=None, lse=None, causal=1, scale=0.1, mx=0, ws=0x100000, wb=1 << 40):
-    return lib.ring_attn_cache_fwd(q or fake((10, 4, 64)), c or cache(), s or seqs(), causal, scale, mx,
-                                   out or fake((10, 4, 64)), lse or fake((4, 10), ra.RA_FP32), ws, wb, None)
+    r = [ref(x) for x in (q or fake((10, 4, 64)), c or cache(), s or seqs(), out or fake((10, 4, 64)),
+                          lse or fake((4, 10), ra.RA_FP32))]
+    return lib.ring_attn_cache_fwd(*r[:3], causal, scale, mx, *r[3:], ws, wb, None)
 
 
 def read(lib, c=None, s=None, k=None, v=None):
-    return lib.ring_attn_cache_read(c or cache(), s or seqs(), k or fake((10, 2, 64)), v or fake((10, 2, 64)), None)
+    r = [ref(x) for x in (c or cache(), s or seqs(), k or fake((10, 2, 64)), v or fake((10, 2, 64)))]
+    return lib.ring_attn_cache_read(*r, None)
 
 
 BAD_CACHE = [
