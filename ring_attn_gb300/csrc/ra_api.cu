@@ -1122,7 +1122,7 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (a.s.total == 0) return RA_OK;
   RA_TRY(dev_ctl(&a.ctl));
   TimedLaunch tl(RA_KERNEL_CACHE_FWD, static_cast<cudaStream_t>(stream));
-  return cuda_status(launch_cache_attn(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_cache_attn(a, seqs->cu_seqlens_host, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,

@@ -4,9 +4,9 @@
 // An item has up to R = 8 NT query rows; the blocks share the items' units as
 // ra_cache_line.cuh says, in one wave.
 //
-// Each of the 4 warps streams its own 32 keys of a unit through a ring of
-// cp.async stages and keeps its own running maximum, sum and O^T; no barrier in
-// the loop.  Matrix products are warp-level m16n8k16 on fp16, which holds number *
+// A block's W warps take a piece's tiles of 32 keys in turn.  Each streams its tiles
+// through a ring of cp.async stages of its own and keeps its own running maximum,
+// sum and O^T: no barrier in the loop.  Matrix products are warp-level m16n8k16 on fp16, which holds number *
 // scale exactly, with keys (then head dims) as the 16 rows and 8 query rows as
 // the columns, so a group of 8 heads wastes nothing:
 //   S^T = K Q^T: a lane holds head dims [32 t, 32 t + 32) of rows g, g + 8, one
@@ -20,20 +20,21 @@
 //
 // Bound: 0.5625 bytes per number from HBM; the conversions cost about 1.3 lane
 // instructions per number against the 3 that fit into its memory time.
+#include <algorithm>
+
 #include "ra_cache_line.cuh"
 
 namespace ra {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-static_assert(kUnit == 32 * kWarps, "32 keys of a unit per warp");
+constexpr int kTilesPerUnit = kUnit / 32;
 constexpr float kLift = 8.f;        // log2 of the largest p when M is set
 constexpr float kSlack = 4.f;       // M is raised when a score is this much beyond
 constexpr float kNone = -3.0e38f;   // M of a row that has seen no key
 
-template <int D, int NT>
+template <int D, int NT, int W>
 struct Lay {
+  static constexpr int kWarps = W;
   static constexpr int R = 8 * NT;
   static constexpr int kK = 0, kV = 32 * D / 2, kKs = 2 * kV, kVs = kKs + 32 * D / 16;
   static constexpr int kStage = kVs + 32 * D / 16;
@@ -53,12 +54,13 @@ struct Lay {
 };
 
 // Cost in units: starting and finishing an item costs about as much as kItemCost.
+// `whole`: every item is one place on the line, so none is shared.
 template <int NT>
 struct FewRows {
   static constexpr int R = 8 * NT, kItemCost = 2;
-  static __device__ __forceinline__ void cost(const CacheAttnArgs&, LineSeq& s) {
+  static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.per = 1;
-    s.a = max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
+    s.a = g.whole ? 1 : max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
     s.b = 0;
   }
 };
@@ -141,15 +143,20 @@ __device__ __forceinline__ uint32_t v_offset(int r, int chunk) {
   return slot * (D / 2) + ((D == 128 ? chunk ^ (slot & 2) : chunk) << 4);
 }
 
-// A warp's copies: the cursor's unit goes to the ring slot by slot, its pages read
-// one unit ahead.
-template <int D, int NT>
+// Turns of a block's warps over a piece's tiles.
+template <int W>
+__device__ __forceinline__ int turns_of(const Piece& x) {
+  return ((x.ub - x.ua) * kTilesPerUnit + W - 1) / W;
+}
+
+// A warp's copies: its tiles go to the ring slot by slot, their pages read one turn ahead.
+template <int D, int NT, int W>
 struct Stream {
-  using L = Lay<D, NT>;
+  using L = Lay<D, NT, W>;
   const CacheAttnArgs& a;
   LinePos at;
   long long run_end;
-  int unit, unit_end, len;            // the units to come of a piece, and its sequence's keys
+  int turns, end_key;                 // turns to come of a piece, and the end of its keys
   const int* table;                   // the sequence's page table
   int pa, pb, k0;                     // pages of the warp's keys [k0, k0 + 16) and the 16 after them
   const uint8_t *kc, *vc, *ks, *vs;   // the head's rows, this lane's part of the offset included
@@ -157,7 +164,7 @@ struct Stream {
   uint32_t to, end, slot0;            // ring slot, the ring's end and start
 
   __device__ __forceinline__ Stream(const CacheAttnArgs& args, long long e, uint32_t ring)
-      : a(args), run_end(e), unit(0), unit_end(0), pa(0), pb(0), to(ring),
+      : a(args), run_end(e), turns(0), end_key(0), pa(0), pb(0), k0(0), to(ring),
         end(ring + L::kStages * L::kStage), slot0(ring) {
     constexpr int CPR = D / 32;
     step_c = (int)a.c.k.s_row * (32 / CPR);
@@ -169,7 +176,9 @@ struct Stream {
   }
   __device__ __forceinline__ void piece(const Piece& x) {
     const int lane = threadIdx.x & 31, head = x.head;
-    unit = x.ua, unit_end = x.ub, len = x.len;
+    turns = turns_of<W>(x);
+    k0 = x.ua * kUnit + (threadIdx.x >> 5) * 32;
+    end_key = min(x.len, x.ub * kUnit);
     constexpr int CPR = D / 32;  // 16-byte chunks per row
     const long long oc = head * a.c.k.s_head + (lane / CPR) * a.c.k.s_row + lane % CPR * 16;
     const long long os = head * a.c.ks.s_head + lane * a.c.ks.s_row;
@@ -179,22 +188,23 @@ struct Stream {
     pages();
   }
   __device__ __forceinline__ void pages() {
-    k0 = unit * kUnit + (threadIdx.x >> 5) * 32;
-    if (k0 < len) {
+    if (k0 < end_key) {
       pa = __ldg(table + (k0 >> a.c.page_shift));
-      if (a.c.page_shift == 4) pb = k0 + 16 < len ? __ldg(table + (k0 >> 4) + 1) : pa;
+      if (a.c.page_shift == 4) pb = k0 + 16 < end_key ? __ldg(table + (k0 >> 4) + 1) : pa;
     }
   }
-  // Copies the unit (nothing when none is left) and moves on, to the run's next piece with kFlow.
+  // Copies the warp's tile of a turn (nothing when none is left) and moves on, to the run's
+  // next piece with kFlow.
   __device__ __forceinline__ void load() {
-    if (unit < unit_end) {
-      if (k0 < len) {
-        if (a.c.page_shift > 4 && k0 + 32 <= len && (unsigned)pa < (unsigned)a.c.n_pages)
+    if (turns > 0) {
+      if (k0 < end_key) {
+        if (a.c.page_shift > 4 && k0 + 32 <= end_key && (unsigned)pa < (unsigned)a.c.n_pages)
           copy_full();
         else
           copy_part();
       }
-      if (++unit < unit_end)
+      k0 += 32 * W;
+      if (--turns > 0)
         pages();
       else if (L::kFlow)
         follow();
@@ -229,7 +239,7 @@ struct Stream {
 #pragma unroll 1
     for (int j = 0; j <= CPR; ++j) {  // the last turn copies the scales
       const int r = j < CPR ? j * RPJ + lane / CPR : lane, ch = lane % CPR;
-      const bool ok = k0 + r < len && (r < 16 ? oka : okb);
+      const bool ok = k0 + r < end_key && (r < 16 ? oka : okb);
       const int page = ok ? (r < 16 ? pa : pb) : 0, row = (k0 + r) & mask;
       if (j < CPR) {
         const long long o = (long long)page * a.c.k.s_page + (row - lane / CPR) * (long long)a.c.k.s_row;
@@ -244,9 +254,13 @@ struct Stream {
   }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache_attn_kernel(const CacheAttnArgs a) {
-  using L = Lay<D, NT>;
+// Blocks per SM and warps per block: small blocks for many items, one block per SM for few.
+constexpr int small_blocks(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_attn_kernel(const CacheAttnArgs a) {
+  using L = Lay<D, NT, W>;
+  constexpr int kWarps = W, kThreads = 32 * W;
   constexpr int R = L::R, KS = D / 16;  // contraction steps of S, row tiles of O^T
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ LineShared<kWarps> sh;
@@ -261,13 +275,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
     if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
     return;
   }
-  Stream<D, NT> st(a, end_u, ring);
+  Stream<D, NT, W> st(a, end_u, ring);
   uint32_t slot = 0;
   int seen = -1;
   Piece w;
   while (next_piece<FewRows<NT>>(a, at, end_u, w)) {
     // ---------------------------------------------------------------- the next item
-    const int n_it = w.ub - w.ua, row0 = w.tile * R, cu0 = __ldg(a.s.cu + w.seq), rows = min(R, w.n_new * a.G - row0);
+    const int n_it = turns_of<W>(w), end_key = min(w.len, w.ub * kUnit), row0 = w.tile * R, cu0 = __ldg(a.s.cu + w.seq), rows = min(R, w.n_new * a.G - row0);
     if (w.seq != seen && threadIdx.x == 0 && __ldg(a.s.lens + w.seq) > a.max_kv)
       record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
     if (!L::kFlow || seen < 0) {  // a drained ring starts again
@@ -357,10 +371,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
       cp_wait<L::kStages - 2>();
       __syncwarp();
       st.load();
-      const int k0 = (w.ua + it) * kUnit + warp * 32;
+      const int k0 = w.ua * kUnit + (it * W + warp) * 32;
       stg = ring + slot * L::kStage;
       if (++slot == L::kStages) slot = 0;
-      if (k0 >= w.len) continue;
+      if (k0 >= end_key) continue;
       // scores of 32 keys: rows g, g + 8 of two tiles
       float s[2][NT][4];
 #pragma unroll
@@ -528,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
       }
     }
     __syncthreads();
-    const bool whole = n_it == w.units;
+    const bool whole = w.ub - w.ua == w.units;
     note_piece<FewRows<NT>>(a, w, quota, cu0, note);
     float* part = slot_of<R, D>(a, gridDim.x, blockIdx.x, w.ua == 0);
     for (int e = threadIdx.x; e < rows * (D / 2); e += kThreads) {
@@ -564,37 +578,55 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache
   if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
 }
 
-// Blocks that fit on an SM (registers and shared memory), so the grid is one wave.
-int blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
-
 // From how many query rows per key / value head on the tensor-core kernel takes over.
 bool many_rows(int max_new, int G) { return (long long)max_new * G > 32; }
 
 // Query rows of an item in units of 8.
 int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
+// One block per SM with as many warps as the small blocks have together.
+constexpr int big_warps(int nt) { return 4 * small_blocks(nt); }
+
+template <int D, int NT, int W>
+cudaError_t launch_w(const CacheAttnArgs& a, bool whole, int grid, cudaStream_t st) {
+  using L = Lay<D, NT, W>;
+  cudaError_t e = configure_kernel<cache_attn_kernel<D, NT, W>>(0, L::kBytes);
+  if (e != cudaSuccess) return e;
+  CacheAttnArgs b = a;
+  b.whole = whole;
+  e = launch_early(cache_attn_kernel<D, NT, W>, grid, 32 * W, L::kBytes, st, b);
+  if (e != cudaSuccess || whole) return e;
+  return launch_early(cache_join_kernel<L::R, D>, dim3(grid, (std::min(a.max_new * a.G, L::R) + 7) / 8), 256 * kJoinGroups,
+                      0, st, b);
+}
+
+// Few items (at most one per SM): big blocks, so that an item has few pieces to
+// join, and none when its units are few enough for one block (2048 keys: about
+// 7 us, as long as a second kernel takes).  Many items: small blocks, whose starts
+// and ends overlap.
 template <int D, int NT>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
-  using L = Lay<D, NT>;
-  cudaError_t e = configure_kernel<cache_attn_kernel<D, NT>>(0, L::kBytes);
-  if (e != cudaSuccess) return e;
-  const int grid = num_sms() * blocks_per_sm(NT);
-  e = launch_early(cache_attn_kernel<D, NT>, grid, kThreads, L::kBytes, st, a);
-  if (e != cudaSuccess) return e;
-  return launch_early(cache_join_kernel<L::R, D>, dim3(grid, NT), 256 * kJoinGroups, 0, st, a);
+  const int units = (a.max_kv + kUnit - 1) / kUnit, sms = num_sms();
+  const bool big = a.items <= sms, whole = big && units <= 16;
+  const long long line = a.items * (whole ? 1 : units + FewRows<NT>::kItemCost);  // at most
+  const int grid = (int)std::min(line, (long long)sms * (big ? 1 : small_blocks(NT)));
+  return big ? launch_w<D, NT, big_warps(NT)>(a, whole, grid, st) : launch_w<D, NT, 4>(a, whole, grid, st);
 }
 
 }  // namespace
 
 size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
   if (many_rows(max_new, h / hk)) return cache_chunk_ws_bytes(d);
-  const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * blocks_per_sm(nt);
+  const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * small_blocks(nt);
   return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
 }
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
-  if (many_rows(a.max_new, a.G)) return launch_cache_chunk(a, st);
-  const int nt = row_tiles((long long)a.max_new * a.G);
+cudaError_t launch_cache_attn(const CacheAttnArgs& args, const int* cu_host, cudaStream_t st) {
+  if (many_rows(args.max_new, args.G)) return launch_cache_chunk(args, st);
+  const int nt = row_tiles((long long)args.max_new * args.G);
+  CacheAttnArgs a = args;
+  for (int i = 0; i < a.s.n_seqs; ++i)
+    a.items += ((long long)(cu_host[i + 1] - cu_host[i]) * a.G + 8 * nt - 1) / (8 * nt) * a.hk;
   if (a.d == 64) return nt == 1 ? launch<64, 1>(a, st) : nt == 2 ? launch<64, 2>(a, st) : launch<64, 4>(a, st);
   return nt == 1 ? launch<128, 1>(a, st) : nt == 2 ? launch<128, 2>(a, st) : launch<128, 4>(a, st);
 }

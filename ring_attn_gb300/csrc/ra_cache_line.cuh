@@ -123,6 +123,24 @@ __device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, lo
   const bool few = g.s.n_seqs <= T;  // one sequence per thread, read once
   const int tid = threadIdx.x;
   long long v = 0, below = 0, all;
+  if (g.s.n_seqs <= 32) {  // every warp by itself
+    const int lane = tid & 31;
+    if (lane < g.s.n_seqs) v = line_length<Kind>(g, line_seq<Kind>(g, lane));
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    all = __shfl_sync(0xffffffffu, x, 31);
+    quota = quotient(all + gridDim.x - 1, gridDim.x);
+    at.u = blockIdx.x * quota;
+    end = min(all, at.u + quota);
+    if (at.u >= end) return false;
+    at.seq = 31 - __clz(__ballot_sync(0xffffffffu, v > 0 && x - v <= at.u));
+    at.first = __shfl_sync(0xffffffffu, x - v, at.seq);
+    return true;
+  }
   if (few) {
     if (tid < g.s.n_seqs) v = line_length<Kind>(g, line_seq<Kind>(g, tid));
   } else {
