@@ -143,59 +143,96 @@ __device__ __forceinline__ uint32_t v_offset(int r, int chunk) {
   return slot * (D / 2) + ((D == 128 ? chunk ^ (slot & 2) : chunk) << 4);
 }
 
-// Turns of a block's warps over a piece's tiles.
+// Turns of a block's warps over the tiles of `units` units.
 template <int W>
-__device__ __forceinline__ int turns_of(const Piece& x) {
-  return ((x.ub - x.ua) * kTilesPerUnit + W - 1) / W;
+__device__ __forceinline__ int turns_of(int units) {
+  return (units * kTilesPerUnit + W - 1) / W;
 }
 
-// A warp's copies: its tiles go to the ring slot by slot, their pages read one turn ahead.
+// The block's pieces in shared memory, some ahead of the one being worked on, so that the
+// warps hold no place on the line in registers; ub = 0 ends the run.
+struct BlockPiece {
+  int seq, head, tile, cu0, len, n_new, ua, ub, whole;
+};
+constexpr int kPieces = 8;
+struct Pieces {
+  volatile BlockPiece ring[kPieces];
+  LinePos at;
+  long long end, quota;
+  JoinNote note;
+  int made;
+  bool over;
+};
+// One thread: the next piece goes to the ring.
+template <class Kind>
+__device__ __forceinline__ void make_piece(const CacheAttnArgs& g, Pieces& p) {
+  LinePos at = p.at;
+  Piece x;
+  const bool more = next_piece<Kind>(g, at, p.end, x);
+  volatile BlockPiece& y = p.ring[p.made % kPieces];
+  ++p.made;
+  if (!more) {
+    y.ua = y.ub = 0;
+    p.over = true;
+    return;
+  }
+  p.at = at;
+  const int cu0 = __ldg(g.s.cu + x.seq);
+  JoinNote n = p.note;
+  note_piece<Kind>(g, x, p.quota, cu0, n);
+  p.note = n;
+  y.seq = x.seq, y.head = x.head, y.tile = x.tile, y.cu0 = cu0, y.len = x.len, y.n_new = x.n_new;
+  y.ua = x.ua, y.ub = x.ub, y.whole = x.ub - x.ua == x.units;
+  if (__ldg(g.s.lens + x.seq) > g.max_kv) record_error(g.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+}
+
+// A warp's copies: its tiles go to the ring slot by slot, their pages read two turns ahead.
 template <int D, int NT, int W>
 struct Stream {
   using L = Lay<D, NT, W>;
   const CacheAttnArgs& a;
-  LinePos at;
-  long long run_end;
+  const Pieces& p;
+  int index;                          // of the piece
   int turns, end_key;                 // turns to come of a piece, and the end of its keys
   const int* table;                   // the sequence's page table
   int pa, pb, k0;                     // pages of the warp's keys [k0, k0 + 16) and the 16 after them
+  int na, nb;                         // the same a turn ahead
   const uint8_t *kc, *vc, *ks, *vs;   // the head's rows, this lane's part of the offset included
   int step_c;                         // bytes between this lane's code chunks
   uint32_t to, end, slot0;            // ring slot, the ring's end and start
 
-  __device__ __forceinline__ Stream(const CacheAttnArgs& args, long long e, uint32_t ring)
-      : a(args), run_end(e), turns(0), end_key(0), pa(0), pb(0), k0(0), to(ring),
+  __device__ __forceinline__ Stream(const CacheAttnArgs& args, const Pieces& pieces, uint32_t ring)
+      : a(args), p(pieces), index(0), turns(0), end_key(0), pa(0), pb(0), k0(0), na(0), nb(0), to(ring),
         end(ring + L::kStages * L::kStage), slot0(ring) {
     constexpr int CPR = D / 32;
     step_c = (int)a.c.k.s_row * (32 / CPR);
   }
-  // The next piece of the run, if there is one.
-  __device__ __forceinline__ void follow() {
-    Piece x;
-    if (next_piece<FewRows<NT>>(a, at, run_end, x)) piece(x);
-  }
-  __device__ __forceinline__ void piece(const Piece& x) {
-    const int lane = threadIdx.x & 31, head = x.head;
-    turns = turns_of<W>(x);
-    k0 = x.ua * kUnit + (threadIdx.x >> 5) * 32;
-    end_key = min(x.len, x.ub * kUnit);
+  __device__ __forceinline__ void piece(int i) {
+    index = i;
+    const volatile BlockPiece& x = p.ring[i % kPieces];
+    const int lane = threadIdx.x & 31, head = x.head, ua = x.ua, ub = x.ub;
+    turns = turns_of<W>(ub - ua);
+    k0 = ua * kUnit + (threadIdx.x >> 5) * 32;
+    end_key = min(x.len, ub * kUnit);
     constexpr int CPR = D / 32;  // 16-byte chunks per row
     const long long oc = head * a.c.k.s_head + (lane / CPR) * a.c.k.s_row + lane % CPR * 16;
     const long long os = head * a.c.ks.s_head + lane * a.c.ks.s_row;
     kc = a.c.k.data + oc, vc = a.c.v.data + oc;
     ks = a.c.ks.data + os, vs = a.c.vs.data + os;
     table = a.s.table + (long long)x.seq * a.s.table_stride;
-    pages();
+    pages(k0, pa, pb);
+    pages(k0 + 32 * W, na, nb);
   }
-  __device__ __forceinline__ void pages() {
-    if (k0 < end_key) {
-      pa = __ldg(table + (k0 >> a.c.page_shift));
-      if (a.c.page_shift == 4) pb = k0 + 16 < end_key ? __ldg(table + (k0 >> 4) + 1) : pa;
+  __device__ __forceinline__ void pages(int k, int& p, int& q) {
+    if (k < end_key) {
+      p = __ldg(table + (k >> a.c.page_shift));
+      if (a.c.page_shift == 4) q = k + 16 < end_key ? __ldg(table + (k >> 4) + 1) : p;
     }
   }
   // Copies the warp's tile of a turn (nothing when none is left) and moves on, to the run's
-  // next piece with kFlow.
-  __device__ __forceinline__ void load() {
+  // next piece when `follow`.
+  __device__ __forceinline__ void load(bool follow) {
+    if (turns == 0 && follow && p.ring[(index + 1) % kPieces].ub > 0) piece(index + 1);
     if (turns > 0) {
       if (k0 < end_key) {
         if (a.c.page_shift > 4 && k0 + 32 <= end_key && (unsigned)pa < (unsigned)a.c.n_pages)
@@ -204,10 +241,9 @@ struct Stream {
           copy_part();
       }
       k0 += 32 * W;
-      if (--turns > 0)
-        pages();
-      else if (L::kFlow)
-        follow();
+      --turns;
+      pa = na, pb = nb;
+      pages(k0 + 32 * W, na, nb);
     }
     cp_commit();
     to += L::kStage;
@@ -268,31 +304,47 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
   const uint32_t sb = smem_u32(smem), ring = sb + warp * L::kStages * L::kStage;
 
   after_previous_kernel();
-  LinePos at;
-  long long end_u, quota;
-  JoinNote note = empty_note();
-  if (!find_run<FewRows<NT>, kWarps>(a, at, end_u, quota, sh)) {
-    if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
-    return;
+  using Kind = FewRows<NT>;
+  __shared__ Pieces sp;
+  const bool planner = threadIdx.x == kThreads - 32;
+  {
+    LinePos at;
+    long long end_u, quota;
+    if (!find_run<Kind, W>(a, at, end_u, quota, sh)) {
+      if (planner) notes_of(a)[blockIdx.x] = empty_note();
+      return;
+    }
+    if (planner) {
+      sp.at = at, sp.end = end_u, sp.quota = quota;
+      sp.note = empty_note();
+      sp.made = 0;
+      sp.over = false;
+      make_piece<Kind>(a, sp);
+    }
   }
-  Stream<D, NT, W> st(a, end_u, ring);
+  __syncthreads();
+  Stream<D, NT, W> st(a, sp, ring);
   uint32_t slot = 0;
-  int seen = -1;
-  Piece w;
-  while (next_piece<FewRows<NT>>(a, at, end_u, w)) {
+  for (int i = 0; sp.ring[i % kPieces].ub > 0; ++i) {
     // ---------------------------------------------------------------- the next item
-    const int n_it = turns_of<W>(w), end_key = min(w.len, w.ub * kUnit), row0 = w.tile * R, cu0 = __ldg(a.s.cu + w.seq), rows = min(R, w.n_new * a.G - row0);
-    if (w.seq != seen && threadIdx.x == 0 && __ldg(a.s.lens + w.seq) > a.max_kv)
-      record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
-    if (!L::kFlow || seen < 0) {  // a drained ring starts again
+    const volatile BlockPiece& w = sp.ring[i % kPieces];
+    const int ua = w.ua, n_it = turns_of<W>(w.ub - ua), end_key = min(w.len, w.ub * kUnit), row0 = w.tile * R;
+    const int len = w.len, n_new = w.n_new, rows = min(R, n_new * a.G - row0);
+    if (!L::kFlow || i == 0) {  // a drained ring starts again
       slot = 0;
       st.to = ring;
-      st.at = at;
-      st.piece(w);
-#pragma unroll
-      for (int s = 0; s < L::kStages - 1; ++s) st.load();
+      st.piece(i);
+#pragma unroll 1
+      for (int s = 0; s < L::kStages - 1; ++s) st.load(false);
     }
-    seen = w.seq;
+    if (planner) {  // the pieces that the copies may reach during this one, and the one after it
+      for (int k = i + 1, ahead = 0; k == i + 1 || ahead < L::kStages - 1; ++k) {
+        if (k == sp.made && !sp.over) make_piece<Kind>(a, sp);
+        const int n = sp.ring[k % kPieces].ub - sp.ring[k % kPieces].ua;
+        if (n == 0) break;
+        ahead += turns_of<W>(n);
+      }
+    }
 
     // ---------------------------------------------------------------- queries
     const int q_at = L::kFlow ? (int)(st.to - ring) : L::kQ;  // the slot that the next copies go to
@@ -304,7 +356,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
         const int c = threadIdx.x % LPR, rr = row0 + r;
         uint4 q = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          const int tok = cu0 + rr / a.G, hd = w.head * a.G + rr % a.G;
+          const int tok = w.cu0 + rr / a.G, hd = w.head * a.G + rr % a.G;
           q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) + (long long)tok * a.q.s_row +
                                               (long long)hd * a.q.s_head + 8 * c);
         }
@@ -336,7 +388,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       return *reinterpret_cast<const uint2*>(sq + (8 * n + g) * D + (D / 4) * t + 4 * s);
     };
     float sc[NT][2];
-    int end[NT][2], min_end = w.len;
+    int end[NT][2], min_end = len;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if constexpr (kQReg) {
@@ -350,11 +402,11 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       for (int x = 0; x < 2; ++x) {
         const int r = 8 * n + 2 * t + x;
         sc[n][x] = sscale[r];
-        end[n][x] = w.len;
-        if (a.causal && r < rows) end[n][x] = min(w.len, w.len - w.n_new + (row0 + r) / a.G + 1);
+        end[n][x] = len;
+        if (a.causal && r < rows) end[n][x] = min(len, len - n_new + (row0 + r) / a.G + 1);
       }
     }
-    if (a.causal) min_end = min(w.len, w.len - w.n_new + row0 / a.G + 1);
+    if (a.causal) min_end = min(len, len - n_new + row0 / a.G + 1);
     if (L::kFlow) __syncthreads();
 
     // ---------------------------------------------------------------- keys
@@ -370,8 +422,8 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
     for (int it = 0; it < n_it; ++it) {
       cp_wait<L::kStages - 2>();
       __syncwarp();
-      st.load();
-      const int k0 = w.ua * kUnit + (it * W + warp) * 32;
+      st.load(L::kFlow);
+      const int k0 = ua * kUnit + (it * W + warp) * 32;
       stg = ring + slot * L::kStage;
       if (++slot == L::kStages) slot = 0;
       if (k0 >= end_key) continue;
@@ -542,9 +594,9 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       }
     }
     __syncthreads();
-    const bool whole = w.ub - w.ua == w.units;
-    note_piece<FewRows<NT>>(a, w, quota, cu0, note);
-    float* part = slot_of<R, D>(a, gridDim.x, blockIdx.x, w.ua == 0);
+    const bool whole = w.whole;
+    const int cu0 = w.cu0, head = w.head;
+    float* part = slot_of<R, D>(a, gridDim.x, blockIdx.x, ua == 0);
     for (int e = threadIdx.x; e < rows * (D / 2); e += kThreads) {
       const int r = e / (D / 2), d = e % (D / 2) * 2;
       const int from = (d % (D / 8)) / 2 * 16 + d / (D / 8) * 2;
@@ -565,17 +617,17 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
         if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m, lsum);
       } else {
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-        const long long to = out_offset(a, cu0, w.head, row0 + r) + d;
+        const long long to = out_offset(a, cu0, head, row0 + r) + d;
         if (a.out_f32)
           *reinterpret_cast<float2*>(static_cast<float*>(a.out.data) + to) = make_float2(o0 * inv, o1 * inv);
         else
           *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out.data) + to) = pack_bf16x2(o0 * inv, o1 * inv);
-        if (d == 0) store_row(a, cu0, w.head, row0 + r, m, lsum);
+        if (d == 0) store_row(a, cu0, head, row0 + r, m, lsum);
       }
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
+  if (planner) notes_of(a)[blockIdx.x] = sp.note;
 }
 
 // From how many query rows per key / value head on the tensor-core kernel takes over.

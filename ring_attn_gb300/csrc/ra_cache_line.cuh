@@ -45,13 +45,18 @@ struct LineSeq {
 
 // Kind: R, kItemCost and the cost rule `static void cost(args, LineSeq&)`.
 template <class Kind>
-__device__ __forceinline__ LineSeq line_seq(const CacheAttnArgs& g, int i) {
+__device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int len, int n_new) {
   LineSeq s;
-  s.n_new = __ldg(g.s.cu + i + 1) - __ldg(g.s.cu + i);
-  s.len = max(0, min(__ldg(g.s.lens + i), g.max_kv));
+  s.n_new = n_new;
+  s.len = len;
   s.tiles = (int)(((long long)s.n_new * g.G + Kind::R - 1) / Kind::R);
   Kind::cost(g, s);
   return s;
+}
+template <class Kind>
+__device__ __forceinline__ LineSeq line_seq(const CacheAttnArgs& g, int i) {
+  const int n_new = __ldg(g.s.cu + i + 1) - __ldg(g.s.cu + i);
+  return line_of<Kind>(g, max(0, min(__ldg(g.s.lens + i), g.max_kv)), n_new);
 }
 template <class Kind>
 __device__ __forceinline__ long long line_length(const CacheAttnArgs& g, const LineSeq& s) {
@@ -109,11 +114,40 @@ struct LineShared {
   int seq;
 };
 
-// A place on the line: position, sequence and where that sequence begins.
+// A place on the line, and the item it lies in.
 struct LinePos {
-  long long u, first;
-  int seq;
+  long long u, start;  // place, and the item's first place
+  int seq, head, tile;
+  int len, n_new;      // of the sequence
 };
+
+// The item of sequence `seq`, which begins at `first`, that holds at.u.
+template <class Kind>
+__device__ __forceinline__ void enter_item(const CacheAttnArgs& g, LinePos& at, int seq, long long first) {
+  const LineSeq s = line_seq<Kind>(g, seq);
+  const long long per = s.before(s.tiles);
+  long long q = at.u - first;
+  at.seq = seq;
+  at.len = s.len;
+  at.n_new = s.n_new;
+  at.head = (int)quotient(q, per);
+  q -= at.head * per;
+  int lo = 0;
+  if (s.b == 0) {
+    lo = (int)quotient(q, s.a);
+  } else {
+    int hi = s.tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.before(mid) <= q)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+  }
+  at.tile = lo;
+  at.start = first + at.head * per + s.before(lo);
+}
 
 // This block's run [at.u, end) of the line, found by the whole thread block.  False when it is empty.
 template <class Kind, int WARPS>
@@ -137,8 +171,8 @@ __device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, lo
     at.u = blockIdx.x * quota;
     end = min(all, at.u + quota);
     if (at.u >= end) return false;
-    at.seq = 31 - __clz(__ballot_sync(0xffffffffu, v > 0 && x - v <= at.u));
-    at.first = __shfl_sync(0xffffffffu, x - v, at.seq);
+    const int seq = 31 - __clz(__ballot_sync(0xffffffffu, v > 0 && x - v <= at.u));
+    enter_item<Kind>(g, at, seq, __shfl_sync(0xffffffffu, x - v, seq));
     return true;
   }
   if (few) {
@@ -164,8 +198,7 @@ __device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, lo
     }
   }
   __syncthreads();
-  at.seq = sh.seq;
-  at.first = sh.first;
+  enter_item<Kind>(g, at, sh.seq, sh.first);
   return true;
 }
 
@@ -175,50 +208,38 @@ struct Piece {
   long long start, cost;  // place of the item on the line
 };
 
-// The item at the place (which is on the line).
-template <class Kind>
-__device__ __forceinline__ void item_at(const CacheAttnArgs& g, const LinePos& at, const LineSeq& s, Piece& x) {
-  const long long per = s.before(s.tiles);
-  long long q = at.u - at.first;
-  x.head = (int)quotient(q, per);
-  q -= x.head * per;
-  int lo = 0;
-  if (s.b == 0) {
-    lo = (int)quotient(q, s.a);
-  } else {
-    int hi = s.tiles - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s.before(mid) <= q)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-  }
-  x.tile = lo;
-  x.cost = s.a + s.b * lo;
-  x.start = at.first + x.head * per + s.before(lo);
-  x.seq = at.seq;
-  x.len = s.len;
-  x.n_new = s.n_new;
-  x.per = s.per;
-  x.units = tile_units<Kind>(g, s, lo);
-}
-
 // The next piece of the run that ends at `end`, moving `at` behind it.  False at the run's end.
 template <class Kind>
 __device__ __forceinline__ bool next_piece(const CacheAttnArgs& g, LinePos& at, long long end, Piece& x) {
   while (at.u < end) {
-    LineSeq s = line_seq<Kind>(g, at.seq);
-    for (long long n = line_length<Kind>(g, s); at.u - at.first >= n; n = line_length<Kind>(g, s)) {
-      at.first += n;
-      s = line_seq<Kind>(g, ++at.seq);
-    }
-    item_at<Kind>(g, at, s, x);
-    const long long p0 = at.u - x.start, p1 = min(x.cost, p0 + (end - at.u));
+    LineSeq s = line_of<Kind>(g, at.len, at.n_new);
+    x.seq = at.seq;
+    x.head = at.head;
+    x.tile = at.tile;
+    x.len = at.len;
+    x.n_new = at.n_new;
+    x.per = s.per;
+    x.start = at.start;
+    x.cost = s.a + s.b * at.tile;
+    x.units = tile_units<Kind>(g, s, at.tile);
+    const long long p0 = at.u - at.start, p1 = min(x.cost, p0 + (end - at.u));
     x.ua = unit_at<Kind>(p0, x.units, x.cost, x.per);
     x.ub = unit_at<Kind>(p1, x.units, x.cost, x.per);
     at.u += p1 - p0;
+    if (at.u < end) {  // to the next item
+      at.start = at.u;
+      if (++at.tile == s.tiles) {
+        at.tile = 0;
+        if (++at.head == g.hk) {
+          at.head = 0;
+          do {  // (the run ends before the sequences do)
+            s = line_seq<Kind>(g, ++at.seq);
+          } while (s.tiles == 0);
+          at.len = s.len;
+          at.n_new = s.n_new;
+        }
+      }
+    }
     if (x.ua < x.ub) return true;
   }
   return false;
