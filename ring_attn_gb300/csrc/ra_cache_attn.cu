@@ -58,10 +58,9 @@ struct Lay {
 template <int NT>
 struct FewRows {
   static constexpr int R = 8 * NT, kItemCost = 2;
+  static constexpr bool kOneTile = true;
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
-    s.per = 1;
     s.a = g.whole ? 1 : max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
-    s.b = 0;
   }
 };
 
@@ -152,13 +151,13 @@ __device__ __forceinline__ int turns_of(int units) {
 // The block's pieces in shared memory, some ahead of the one being worked on, so that the
 // warps hold no place on the line in registers; ub = 0 ends the run.
 struct BlockPiece {
-  int seq, head, tile, cu0, len, n_new, ua, ub, whole;
+  int seq, head, cu0, len, n_new, ua, ub, whole;
 };
 constexpr int kPieces = 8;
 struct Pieces {
   volatile BlockPiece ring[kPieces];
   LinePos at;
-  long long end, quota;
+  int end, quota;
   JoinNote note;
   int made;
   bool over;
@@ -181,7 +180,7 @@ __device__ __forceinline__ void make_piece(const CacheAttnArgs& g, Pieces& p) {
   JoinNote n = p.note;
   note_piece<Kind>(g, x, p.quota, cu0, n);
   p.note = n;
-  y.seq = x.seq, y.head = x.head, y.tile = x.tile, y.cu0 = cu0, y.len = x.len, y.n_new = x.n_new;
+  y.seq = x.seq, y.head = x.head, y.cu0 = cu0, y.len = x.len, y.n_new = x.n_new;
   y.ua = x.ua, y.ub = x.ub, y.whole = x.ub - x.ua == x.units;
   if (__ldg(g.s.lens + x.seq) > g.max_kv) record_error(g.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
 }
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
   const bool planner = threadIdx.x == kThreads - 32;
   {
     LinePos at;
-    long long end_u, quota;
+    int end_u, quota;
     if (!find_run<Kind, W>(a, at, end_u, quota, sh)) {
       if (planner) notes_of(a)[blockIdx.x] = empty_note();
       return;
@@ -324,12 +323,15 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
   }
   __syncthreads();
   Stream<D, NT, W> st(a, sp, ring);
+  // a row's token: r / G for r < 32 (a product instead of a division)
+  const uint32_t inv_g = (65536u + a.G - 1) / a.G;
+  auto token_of_row = [inv_g](int r) { return (int)((r * inv_g) >> 16); };
   uint32_t slot = 0;
   for (int i = 0; sp.ring[i % kPieces].ub > 0; ++i) {
     // ---------------------------------------------------------------- the next item
     const volatile BlockPiece& w = sp.ring[i % kPieces];
-    const int ua = w.ua, n_it = turns_of<W>(w.ub - ua), end_key = min(w.len, w.ub * kUnit), row0 = w.tile * R;
-    const int len = w.len, n_new = w.n_new, rows = min(R, n_new * a.G - row0);
+    const int ua = w.ua, n_it = turns_of<W>(w.ub - ua), end_key = min(w.len, w.ub * kUnit);
+    const int len = w.len, n_new = w.n_new, rows = n_new * a.G;
     if (!L::kFlow || i == 0) {  // a drained ring starts again
       slot = 0;
       st.to = ring;
@@ -353,10 +355,10 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
     {
       constexpr int LPR = D / 8;  // lanes per row
       for (int r = threadIdx.x / LPR; r < R; r += kThreads / LPR) {
-        const int c = threadIdx.x % LPR, rr = row0 + r;
+        const int c = threadIdx.x % LPR;
         uint4 q = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          const int tok = w.cu0 + rr / a.G, hd = w.head * a.G + rr % a.G;
+          const int tk = token_of_row(r), tok = w.cu0 + tk, hd = w.head * a.G + r - tk * a.G;
           q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) + (long long)tok * a.q.s_row +
                                               (long long)hd * a.q.s_head + 8 * c);
         }
@@ -403,10 +405,10 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
         const int r = 8 * n + 2 * t + x;
         sc[n][x] = sscale[r];
         end[n][x] = len;
-        if (a.causal && r < rows) end[n][x] = min(len, len - n_new + (row0 + r) / a.G + 1);
+        if (a.causal && r < rows) end[n][x] = min(len, len - n_new + token_of_row(r) + 1);
       }
     }
-    if (a.causal) min_end = min(len, len - n_new + row0 / a.G + 1);
+    if (a.causal) min_end = min(len, len - n_new + 1);
     if (L::kFlow) __syncthreads();
 
     // ---------------------------------------------------------------- keys
@@ -617,12 +619,13 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
         if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m, lsum);
       } else {
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-        const long long to = out_offset(a, cu0, head, row0 + r) + d;
+        const int tk = token_of_row(r), tok = cu0 + tk, hd = head * a.G + r - tk * a.G;
+        const long long to = (long long)tok * a.out.s_row + (long long)hd * a.out.s_head + d;
         if (a.out_f32)
           *reinterpret_cast<float2*>(static_cast<float*>(a.out.data) + to) = make_float2(o0 * inv, o1 * inv);
         else
           *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out.data) + to) = pack_bf16x2(o0 * inv, o1 * inv);
-        if (d == 0) store_row(a, cu0, head, row0 + r, m, lsum);
+        if (d == 0) store_lse(a, tok, hd, m, lsum);
       }
     }
     __syncthreads();
@@ -646,6 +649,7 @@ cudaError_t launch_w(const CacheAttnArgs& a, bool whole, int grid, cudaStream_t 
   if (e != cudaSuccess) return e;
   CacheAttnArgs b = a;
   b.whole = whole;
+  b.line_shift = line_shift_for(a.items, (a.max_kv + kUnit - 1) / kUnit + FewRows<NT>::kItemCost);
   e = launch_early(cache_attn_kernel<D, NT, W>, grid, 32 * W, L::kBytes, st, b);
   if (e != cudaSuccess || whole) return e;
   return launch_early(cache_join_kernel<L::R, D>, dim3(grid, (std::min(a.max_new * a.G, L::R) + 7) / 8), 256 * kJoinGroups,
@@ -674,11 +678,11 @@ size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& args, const int* cu_host, cudaStream_t st) {
-  if (many_rows(args.max_new, args.G)) return launch_cache_chunk(args, st);
-  const int nt = row_tiles((long long)args.max_new * args.G);
   CacheAttnArgs a = args;
-  for (int i = 0; i < a.s.n_seqs; ++i)
-    a.items += ((long long)(cu_host[i + 1] - cu_host[i]) * a.G + 8 * nt - 1) / (8 * nt) * a.hk;
+  const bool many = many_rows(a.max_new, a.G);
+  const int nt = row_tiles((long long)a.max_new * a.G), R = many ? 256 : 8 * nt;
+  for (int i = 0; i < a.s.n_seqs; ++i) a.items += ((long long)(cu_host[i + 1] - cu_host[i]) * a.G + R - 1) / R * a.hk;
+  if (many) return launch_cache_chunk(a, st);
   if (a.d == 64) return nt == 1 ? launch<64, 1>(a, st) : nt == 2 ? launch<64, 2>(a, st) : launch<64, 4>(a, st);
   return nt == 1 ? launch<128, 1>(a, st) : nt == 2 ? launch<128, 2>(a, st) : launch<128, 4>(a, st);
 }

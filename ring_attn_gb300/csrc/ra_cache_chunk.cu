@@ -21,6 +21,8 @@
 //                memory, running offset M (O is rescaled when a score passes it by
 //                far), P as fp16 over the score columns; the epilogue.
 // Bound: tensor throughput.  fp16 operands hold number * scale exactly.
+#include <algorithm>
+
 #include "ra_cache_line.cuh"
 
 namespace ra {
@@ -40,10 +42,11 @@ static_assert(128 * (kRegsCtl + kRegsConv + 2 * kRegsSoft) <= kThreads * kLaunch
 // G places per unit, so that the causal growth of 256 / G keys per tile is whole.
 struct ManyRows {
   static constexpr int R = 256, kItemCost = 2;
+  static constexpr bool kOneTile = false;
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.per = g.causal ? g.G : 1;
     const int seen = g.causal ? max(0, s.len - s.n_new) : s.len;  // by every row
-    s.a = (long long)s.per * ((seen + kUnit - 1) / kUnit + kItemCost) + 2;
+    s.a = s.per * ((seen + kUnit - 1) / kUnit + kItemCost) + 2;
     s.b = g.causal ? 2 : 0;
   }
 };
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   }
   after_previous_kernel();
   LinePos at;
-  long long end_u, quota;
+  int end_u, quota;
   JoinNote note = empty_note();
   if (!find_run<ManyRows, kWarps>(a, at, end_u, quota, sh)) {
     if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
@@ -520,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       const float inv = whole ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f;
       float* part = slot_of<256, D>(a, gridDim.x, blockIdx.x, u0 == 0);
       const int pr = t * 128 + r;
-      const long long to = valid ? out_offset(a, cu0, head, row) : 0;
+      const int tok = cu0 + row / a.G, hd = head * a.G + row % a.G;
+      const long long to = valid ? (long long)tok * a.out.s_row + (long long)hd * a.out.s_head : 0;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       tc_fence_before();
       if (valid) {
         if (whole)
-          store_row(a, cu0, head, row, M, l_run);
+          store_lse(a, tok, hd, M, l_run);
         else
           *reinterpret_cast<float2*>(part + 256 * D + 2 * pr) = make_float2(M, l_run);
       }
@@ -568,9 +572,14 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cudaError_t e = configure_kernel<cache_chunk_kernel<D>>(kLaunchRegs, Lay<D>::kAlloc);
   if (e != cudaSuccess) return e;
   const int grid = num_sms();
-  e = launch_early(cache_chunk_kernel<D>, grid, kThreads, Lay<D>::kAlloc, st, a);
+  // the causal cost of an item is at most G (units + kItemCost) + 2 + 2 tiles places
+  CacheAttnArgs b = a;
+  const long long units = (a.max_kv + kUnit - 1) / kUnit + ManyRows::kItemCost;
+  const long long places = a.causal ? a.G * units + 2 + 2 * (((long long)a.max_new * a.G + 255) / 256) : units;
+  b.line_shift = a.items * (places + 2) < (1LL << 30) ? 0 : std::max(1, line_shift_for(a.items, units));
+  e = launch_early(cache_chunk_kernel<D>, grid, kThreads, Lay<D>::kAlloc, st, b);
   if (e != cudaSuccess) return e;
-  return launch_early(cache_join_kernel<256, D>, dim3(grid, 32), 256 * kJoinGroups, 0, st, a);
+  return launch_early(cache_join_kernel<256, D>, dim3(grid, 32), 256 * kJoinGroups, 0, st, b);
 }
 
 }  // namespace

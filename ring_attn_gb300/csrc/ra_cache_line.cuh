@@ -27,30 +27,29 @@ struct Int {
   static constexpr int value = N;
 };
 
-// Quotient of non-negative numbers, by the short division where they are small.
-__device__ __forceinline__ long long quotient(long long n, long long d) {
-  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
-  return n / d;
-}
-
-// One sequence: its row tiles' costs are a + b * tile places; `per` places stand
-// for a unit, after kItemCost units' worth for starting and finishing the item.
+// One sequence: its row tiles' costs are a + b * tile places.  `per` places stand for a
+// unit (with line_shift, a place for 2^line_shift units, so that any line's length
+// fits 32 bits), after kItemCost units' worth for starting and finishing the item.
 struct LineSeq {
   int len, n_new, tiles, per;
-  long long a, b;
-  __device__ __forceinline__ long long before(int tile) const {
-    return a * tile + b * ((long long)tile * (tile - 1) / 2);
-  }
+  int a, b;
+  __device__ __forceinline__ int before(int tile) const { return a * tile + b * (tile * (tile - 1) / 2); }
 };
 
-// Kind: R, kItemCost and the cost rule `static void cost(args, LineSeq&)`.
+// Kind: R, kItemCost, kOneTile (R holds all of a sequence's rows) and the cost
+// rule `static void cost(args, LineSeq&)` for line_shift 0.
 template <class Kind>
 __device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int len, int n_new) {
   LineSeq s;
   s.n_new = n_new;
   s.len = len;
-  s.tiles = (int)(((long long)s.n_new * g.G + Kind::R - 1) / Kind::R);
-  Kind::cost(g, s);
+  s.tiles = Kind::kOneTile ? min(n_new, 1) : (int)(((long long)n_new * g.G + Kind::R - 1) / Kind::R);
+  s.per = 1;
+  s.b = 0;
+  if (g.line_shift == 0)
+    Kind::cost(g, s);
+  else
+    s.a = ((max(1, (len + kUnit - 1) / kUnit) + Kind::kItemCost - 1) >> g.line_shift) + 1;
   return s;
 }
 template <class Kind>
@@ -59,8 +58,8 @@ __device__ __forceinline__ LineSeq line_seq(const CacheAttnArgs& g, int i) {
   return line_of<Kind>(g, max(0, min(__ldg(g.s.lens + i), g.max_kv)), n_new);
 }
 template <class Kind>
-__device__ __forceinline__ long long line_length(const CacheAttnArgs& g, const LineSeq& s) {
-  return g.hk * s.before(s.tiles);
+__device__ __forceinline__ int line_length(const CacheAttnArgs& g, const LineSeq& s) {
+  return g.hk * (Kind::kOneTile ? s.a * s.tiles : s.before(s.tiles));
 }
 
 // Keys that the rows of a tile see, the last one's, in units (at least one: a row without
@@ -68,7 +67,7 @@ __device__ __forceinline__ long long line_length(const CacheAttnArgs& g, const L
 template <class Kind>
 __device__ __forceinline__ int tile_units(const CacheAttnArgs& g, const LineSeq& s, int tile) {
   int end = s.len;
-  if (g.causal) {
+  if (g.causal && !Kind::kOneTile) {
     const int last = (int)min((long long)s.n_new - 1, ((long long)tile * Kind::R + Kind::R - 1) / g.G);
     end = min(end, s.len - s.n_new + last + 1);
   }
@@ -78,26 +77,31 @@ __device__ __forceinline__ int tile_units(const CacheAttnArgs& g, const LineSeq&
 // The unit at place p of an item of `units` units (p = cost: the end).  The cost
 // may be a few units off, so that it is linear: the last block takes the rest.
 template <class Kind>
-__device__ __forceinline__ int unit_at(long long p, int units, long long cost, int per) {
+__device__ __forceinline__ int unit_at(const CacheAttnArgs& g, int p, int units, int cost, int per) {
   if (p >= cost) return units;
-  const long long u = (per == 1 ? p : quotient(p, per)) - Kind::kItemCost;
-  return (int)min((long long)units, max(0LL, u));
+  const int u = (int)min((long long)units + Kind::kItemCost, (long long)(per == 1 ? p : p / per) << g.line_shift);
+  return max(0, u - Kind::kItemCost);
 }
 
-// Sum of v over the block (every thread gets it) and the sum over lower threads.
-template <int WARPS>
-__device__ __forceinline__ long long block_scan(long long v, long long& below, long long* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+// Sum of v over the warp's lower lanes and this one.
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
   }
+  return v;
+}
+// Sum of v over the block (every thread gets it) and the sum over lower threads.
+template <int WARPS>
+__device__ __forceinline__ int block_scan(int v, int& below, int* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = warp_scan(v);
   __syncthreads();
   if (lane == 31) sh[warp] = x;
   __syncthreads();
-  long long pre = 0, all = 0;
+  int pre = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     pre += w < warp ? sh[w] : 0;
@@ -110,33 +114,31 @@ __device__ __forceinline__ long long block_scan(long long v, long long& below, l
 // Shared memory of find_run.
 template <int WARPS>
 struct LineShared {
-  long long sums[WARPS], first;
-  int seq;
+  int sums[WARPS], first, seq;
 };
 
 // A place on the line, and the item it lies in.
 struct LinePos {
-  long long u, start;  // place, and the item's first place
+  int u, start;        // place, and the item's first place
   int seq, head, tile;
   int len, n_new;      // of the sequence
 };
 
 // The item of sequence `seq`, which begins at `first`, that holds at.u.
 template <class Kind>
-__device__ __forceinline__ void enter_item(const CacheAttnArgs& g, LinePos& at, int seq, long long first) {
+__device__ __forceinline__ void enter_item(const CacheAttnArgs& g, LinePos& at, int seq, int first) {
   const LineSeq s = line_seq<Kind>(g, seq);
-  const long long per = s.before(s.tiles);
-  long long q = at.u - first;
   at.seq = seq;
   at.len = s.len;
   at.n_new = s.n_new;
-  at.head = (int)quotient(q, per);
-  q -= at.head * per;
-  int lo = 0;
-  if (s.b == 0) {
-    lo = (int)quotient(q, s.a);
-  } else {
-    int hi = s.tiles - 1;
+  at.tile = 0;
+  const int per = Kind::kOneTile ? s.a : s.before(s.tiles);
+  int q = at.u - first;
+  at.head = (int)((unsigned)q / (unsigned)per);
+  at.start = first + at.head * per;
+  if (!Kind::kOneTile) {
+    q = at.u - at.start;
+    int lo = 0, hi = s.tiles - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s.before(mid) <= q)
@@ -144,73 +146,70 @@ __device__ __forceinline__ void enter_item(const CacheAttnArgs& g, LinePos& at, 
       else
         hi = mid - 1;
     }
+    at.tile = lo;
+    at.start += s.before(lo);
   }
-  at.tile = lo;
-  at.start = first + at.head * per + s.before(lo);
 }
 
 // This block's run [at.u, end) of the line, found by the whole thread block.  False when it is empty.
 template <class Kind, int WARPS>
-__device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, long long& end, long long& quota,
+__device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, int& end, int& quota,
                                          LineShared<WARPS>& sh) {
   constexpr int T = 32 * WARPS;
-  const bool few = g.s.n_seqs <= T;  // one sequence per thread, read once
-  const int tid = threadIdx.x;
-  long long v = 0, below = 0, all;
-  if (g.s.n_seqs <= 32) {  // every warp by itself
-    const int lane = tid & 31;
-    if (lane < g.s.n_seqs) v = line_length<Kind>(g, line_seq<Kind>(g, lane));
-    long long x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    all = __shfl_sync(0xffffffffu, x, 31);
-    quota = quotient(all + gridDim.x - 1, gridDim.x);
-    at.u = blockIdx.x * quota;
-    end = min(all, at.u + quota);
-    if (at.u >= end) return false;
-    const int seq = 31 - __clz(__ballot_sync(0xffffffffu, v > 0 && x - v <= at.u));
-    enter_item<Kind>(g, at, seq, __shfl_sync(0xffffffffu, x - v, seq));
-    return true;
-  }
+  const int tid = threadIdx.x, lane = tid & 31, n = g.s.n_seqs;
+  const bool one_warp = n <= 32, few = n <= T;  // one sequence per lane, per thread: read once
+  const int mine = one_warp ? lane : tid;
+  int v = 0, below = 0, all;
   if (few) {
-    if (tid < g.s.n_seqs) v = line_length<Kind>(g, line_seq<Kind>(g, tid));
+    if (mine < n) v = line_length<Kind>(g, line_seq<Kind>(g, mine));
   } else {
-    for (int i = tid; i < g.s.n_seqs; i += T) v += line_length<Kind>(g, line_seq<Kind>(g, i));
+    for (int i = tid; i < n; i += T) v += line_length<Kind>(g, line_seq<Kind>(g, i));
   }
-  all = block_scan<WARPS>(v, below, sh.sums);
-  quota = quotient(all + gridDim.x - 1, gridDim.x);
-  at.u = blockIdx.x * quota;
-  end = min(all, at.u + quota);
+  if (one_warp) {  // every warp by itself
+    below = warp_scan(v);
+    all = __shfl_sync(0xffffffffu, below, 31);
+    below -= v;
+  } else {
+    all = block_scan<WARPS>(v, below, sh.sums);
+  }
+  quota = (int)(((unsigned)all + gridDim.x - 1) / gridDim.x);
+  at.u = (int)min((long long)all, (long long)blockIdx.x * quota);
+  end = (int)min((long long)all, (long long)at.u + quota);
   if (at.u >= end) return false;
-  if (few) {
-    if (at.u >= below && at.u < below + v) sh.seq = tid, sh.first = below;
+  int seq, first;
+  if (one_warp) {
+    seq = 31 - __clz(__ballot_sync(0xffffffffu, v > 0 && below <= at.u));
+    first = __shfl_sync(0xffffffffu, below, seq);
   } else {
-    long long base = 0;
-    for (int i0 = 0; i0 < g.s.n_seqs && base <= at.u; i0 += T) {
-      const int i = i0 + tid;
-      v = i < g.s.n_seqs ? line_length<Kind>(g, line_seq<Kind>(g, i)) : 0;
-      const long long sum = block_scan<WARPS>(v, below, sh.sums);
-      if (at.u >= base + below && at.u < base + below + v) sh.seq = i, sh.first = base + below;
-      base += sum;
+    if (few) {
+      if (at.u >= below && at.u < below + v) sh.seq = tid, sh.first = below;
+    } else {
+      int base = 0;
+      for (int i0 = 0; i0 < n && base <= at.u; i0 += T) {
+        const int i = i0 + tid;
+        v = i < n ? line_length<Kind>(g, line_seq<Kind>(g, i)) : 0;
+        const int sum = block_scan<WARPS>(v, below, sh.sums);
+        if (at.u >= base + below && at.u < base + below + v) sh.seq = i, sh.first = base + below;
+        base += sum;
+      }
     }
+    __syncthreads();
+    seq = sh.seq;
+    first = sh.first;
   }
-  __syncthreads();
-  enter_item<Kind>(g, at, sh.seq, sh.first);
+  enter_item<Kind>(g, at, seq, first);
   return true;
 }
 
 // An item and a range of its units.
 struct Piece {
-  int seq, head, tile, len, n_new, units, ua, ub, per;
-  long long start, cost;  // place of the item on the line
+  int seq, head, tile, len, n_new, units, ua, ub;
+  int start, cost;  // place of the item on the line
 };
 
 // The next piece of the run that ends at `end`, moving `at` behind it.  False at the run's end.
 template <class Kind>
-__device__ __forceinline__ bool next_piece(const CacheAttnArgs& g, LinePos& at, long long end, Piece& x) {
+__device__ __forceinline__ bool next_piece(const CacheAttnArgs& g, LinePos& at, int end, Piece& x) {
   while (at.u < end) {
     LineSeq s = line_of<Kind>(g, at.len, at.n_new);
     x.seq = at.seq;
@@ -218,13 +217,12 @@ __device__ __forceinline__ bool next_piece(const CacheAttnArgs& g, LinePos& at, 
     x.tile = at.tile;
     x.len = at.len;
     x.n_new = at.n_new;
-    x.per = s.per;
     x.start = at.start;
     x.cost = s.a + s.b * at.tile;
     x.units = tile_units<Kind>(g, s, at.tile);
-    const long long p0 = at.u - at.start, p1 = min(x.cost, p0 + (end - at.u));
-    x.ua = unit_at<Kind>(p0, x.units, x.cost, x.per);
-    x.ub = unit_at<Kind>(p1, x.units, x.cost, x.per);
+    const int p0 = at.u - at.start, p1 = min(x.cost, p0 + (end - at.u));
+    x.ua = unit_at<Kind>(g, p0, x.units, x.cost, s.per);
+    x.ub = unit_at<Kind>(g, p1, x.units, x.cost, s.per);
     at.u += p1 - p0;
     if (at.u < end) {  // to the next item
       at.start = at.u;
@@ -252,13 +250,13 @@ struct __align__(16) JoinNote {
   int slot0, last, row0, rows, cu0, head, pad[2];
 };
 template <class Kind>
-__device__ __forceinline__ void note_piece(const CacheAttnArgs& g, const Piece& x, long long quota, int cu0,
+__device__ __forceinline__ void note_piece(const CacheAttnArgs& g, const Piece& x, int quota, int cu0,
                                            JoinNote& n) {
   if (x.ub - x.ua == x.units) return;
   if (x.ua > 0) {
     n.slot0 = 1;
   } else {
-    n.last = (int)quotient(x.start + x.cost - 1, quota);
+    n.last = (x.start + x.cost - 1) / quota;
     n.row0 = x.tile * Kind::R;
     n.rows = x.n_new * g.G;
     n.cu0 = cu0;
@@ -278,18 +276,20 @@ template <int R, int D>
 __device__ __forceinline__ float* slot_of(const CacheAttnArgs& g, int grid, int block, bool begins) {
   return reinterpret_cast<float*>(notes_of(g) + grid) + ((long long)block * 2 + (begins ? 1 : 0)) * slot_floats<R, D>();
 }
+// The line_shift for a call: `items` items of at most `units` units.
+inline int line_shift_for(long long items, long long units) {
+  int shift = 0;
+  while (items * ((units >> shift) + 2) >= (1LL << 30)) ++shift;
+  return shift;
+}
 template <int R>
 size_t line_ws_bytes(int grid, int d) {
   return (size_t)grid * (sizeof(JoinNote) + 2 * R * (d + 2) * sizeof(float));
 }
 
-__device__ __forceinline__ void store_row(const CacheAttnArgs& g, int cu0, int head, int row, float M, float sum) {
-  const int tok = cu0 + row / g.G, hd = head * g.G + row % g.G;
+__device__ __forceinline__ void store_lse(const CacheAttnArgs& g, int tok, int hd, float M, float sum) {
   g.lse[(long long)hd * g.l_sh + (long long)tok * g.l_ss] =
       sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-}
-__device__ __forceinline__ long long out_offset(const CacheAttnArgs& g, int cu0, int head, int row) {
-  return (long long)(cu0 + row / g.G) * g.out.s_row + (long long)(head * g.G + row % g.G) * g.out.s_head;
 }
 
 // Joins the item in slot 1 of block blockIdx.x, if there is one: rows [8 blockIdx.y,
@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(32 * 8 * kJoinGroups) cache_join_kernel(const 
     for (int i = 0; i < V; ++i) o[i] = o[i] * f0 + so[warp][lane * V + i] * f1;
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const long long to = out_offset(g, n.cu0, n.head, row) + lane * V;
+  const int tok = n.cu0 + row / g.G, hd = n.head * g.G + row % g.G;
+  const long long to = (long long)tok * g.out.s_row + (long long)hd * g.out.s_head + lane * V;
 #pragma unroll
   for (int i = 0; i < V; i += 2) {
     if (g.out_f32)
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(32 * 8 * kJoinGroups) cache_join_kernel(const 
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(g.out.data) + to + i) =
           pack_bf16x2(o[i] * inv, o[i + 1] * inv);
   }
-  if (lane == 0) store_row(g, n.cu0, n.head, row, M, sum);
+  if (lane == 0) store_lse(g, tok, hd, M, sum);
 }
 
 }  // namespace ra

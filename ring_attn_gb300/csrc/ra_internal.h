@@ -207,6 +207,7 @@ struct CacheAttnArgs {
   void* ws;                 // partial results, cache_attn_ws_bytes
   int whole;                // set by the launcher: items are not shared among blocks
   long long items;          // set by the launcher: row tiles times key / value heads
+  int line_shift;           // set by the launcher, see LineSeq
   CacheView c;
   CacheSeqs s;
   DevCtl ctl;
