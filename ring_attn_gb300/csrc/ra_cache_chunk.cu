@@ -41,7 +41,7 @@ static_assert(128 * (kRegsCtl + kRegsConv + 2 * kRegsSoft) <= kThreads * kLaunch
 
 // G places per unit, so that the causal growth of 256 / G keys per tile is whole.
 struct ManyRows {
-  static constexpr int R = 256, kItemCost = 2;
+  static constexpr int R = 256, kItemCost = 4;
   static constexpr bool kOneTile = false;
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.per = g.causal ? g.G : 1;
@@ -369,58 +369,65 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     const uint32_t tS = tl + t * 128, tO = tl + 256 + t * 128;
     uint32_t n_s = 0, n_o = 0;  // score tiles and results seen
     bool ok = true;
+    float sc = 0.f;             // of this thread's row of the item at hand
+    int end_row = 0;
+    // Item i's query row to shared memory, sc and end_row for it; false when the wait
+    // gives up.  The tile's last S has been computed when this is called.
+    auto take_item = [&](int i) -> bool {
+      if (!wait_warp<kWaitHint>(BAR(B_ITEM_FULL + i % kItems), (i / kItems) & 1, abort_flag, a.ctl, 48)) return false;
+      const volatile Item& x = items[i % kItems];
+      if (x.n == 0 || t >= tiles_of(x)) return true;
+      const int row = x.row0 + t * 128 + r, tok = row / a.G;
+      uint32_t q[D / 2];
+      end_row = 0;
+      if (row < x.rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) +
+                                                          (long long)(x.cu0 + tok) * a.q.s_row +
+                                                          (long long)(x.head * a.G + row % a.G) * a.q.s_head);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 w = __ldg(src + k);
+          q[4 * k] = w.x, q[4 * k + 1] = w.y, q[4 * k + 2] = w.z, q[4 * k + 3] = w.w;
+        }
+        end_row = a.causal ? min(x.len, x.len - x.n_new + tok + 1) : x.len;
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) q[k] = 0;
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 2; ++k)
+        m = fmax3f(m, fabsf(__uint_as_float(q[k] << 16)), fabsf(__uint_as_float(q[k] & 0xffff0000u)));
+      // the row's largest entry goes to [2^12, 2^13)
+      const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
+      sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e - 12) << 23);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          h[k] = pack_f16x2(__uint_as_float(q[4 * c + k] << 16) * up, __uint_as_float(q[4 * c + k] & 0xffff0000u) * up);
+        sts128(sb + L::kQ + t * L::kTile + (c >> 3) * kBox + sw128_offset(r, c & 7), h);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_Q_FULL + t));
+      return true;
+    };
+    ok = take_item(0);
     for (int i = 0; ok; ++i) {
-      if (!wait_warp<kWaitHint>(BAR(B_ITEM_FULL + i % kItems), (i / kItems) & 1, abort_flag, a.ctl, 48)) break;
       const volatile Item& x = items[i % kItems];
       const int row = x.row0 + t * 128 + r, u0 = x.ua, u1 = u0 + x.n;
       if (u0 == u1) break;
       if (t >= tiles_of(x)) {  // not this warpgroup's, but its phase passes
+        ok = take_item(i + 1) && wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 44);
+        ++n_o;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
-        ok = wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 44);
-        ++n_o;
         continue;
       }
       const bool valid = row < x.rows;
-      float sc;
-      int end_row = 0;
-      {
-        uint32_t q[D / 2];
-        const int tok = row / a.G;
-        if (valid) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.data) +
-                                                            (long long)(x.cu0 + tok) * a.q.s_row +
-                                                            (long long)(x.head * a.G + row % a.G) * a.q.s_head);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 w = __ldg(src + i);
-            q[4 * i] = w.x, q[4 * i + 1] = w.y, q[4 * i + 2] = w.z, q[4 * i + 3] = w.w;
-          }
-          end_row = a.causal ? min(x.len, x.len - x.n_new + tok + 1) : x.len;
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 2; ++i) q[i] = 0;
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i)
-          m = fmax3f(m, fabsf(__uint_as_float(q[i] << 16)), fabsf(__uint_as_float(q[i] & 0xffff0000u)));
-        // the row's largest entry goes to [2^12, 2^13)
-        const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
-        const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
-        sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e - 12) << 23);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t h[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            h[i] = pack_f16x2(__uint_as_float(q[4 * c + i] << 16) * up, __uint_as_float(q[4 * c + i] & 0xffff0000u) * up);
-          sts128(sb + L::kQ + t * L::kTile + (c >> 3) * kBox + sw128_offset(r, c & 7), h);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_Q_FULL + t));
-      }
       float M = kNone, l_run = 0.f;
       for (int u = u0; u < u1; ++u, ++n_s) {
         const int c_hi = end_row - u * kUnit;
@@ -512,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_P_FULL + t));
       }
-      if (!ok || !wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 43)) {
+      // the next item's queries first, so that its products start behind this one's
+      if (!ok || !take_item(i + 1) || !wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 43)) {
         ok = false;
         break;
       }
@@ -533,8 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
         if (!valid) {
-        } else if (!whole || a.out_f32) {
-          uint4* dst = reinterpret_cast<uint4*>((whole ? static_cast<float*>(a.out.data) + to : part + (long long)pr * D) + c * 32);
+        } else if (!whole) {
+          // four head dims of all rows together, so that a warp stores 512 bytes at once
+          uint4* dst = reinterpret_cast<uint4*>(part) + (c * 8) * 256 + pr;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[256 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (a.out_f32) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(a.out.data) + to + c * 32);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else {
@@ -567,6 +580,63 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   }
 }
 
+// Joins the item in slot 1 of block blockIdx.x, if there is one: rows [32 blockIdx.y, + 32)
+// of its 256, a row per lane and D / 8 head dims per warp, over the few pieces that
+// an item has here.  (A slot holds four head dims of all rows together.)
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const CacheAttnArgs g) {
+  constexpr int V = D / 8;
+  after_previous_kernel();
+  const JoinNote* notes = notes_of(g);
+  const JoinNote n = notes[blockIdx.x];
+  if (n.last < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grid = gridDim.x;
+  const int r = blockIdx.y * 32 + lane, row = n.row0 + r;
+  if (n.row0 + (int)blockIdx.y * 32 >= n.rows) return;
+  float M = kNone, sum = 0.f, o[V] = {};
+  for (int base = blockIdx.x; base <= n.last; base += 32) {
+    const int c = base + lane;
+    unsigned there = __ballot_sync(0xffffffffu, c == (int)blockIdx.x || (c <= n.last && notes[c].slot0));
+    while (there) {
+      const int b = base + __ffs(there) - 1;
+      there &= there - 1;
+      const float* slot = slot_of<256, D>(g, grid, b, b == (int)blockIdx.x);
+      const float2 ml = *reinterpret_cast<const float2*>(slot + 256 * D + 2 * r);  // (rows behind the sequence's: unused)
+      float4 x[V / 4];
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) x[i] = reinterpret_cast<const float4*>(slot)[(warp * (V / 4) + i) * 256 + r];
+      const float to = fmaxf(M, ml.x), f0 = fast_exp2(M - to), f1 = fast_exp2(ml.x - to);
+      M = to;
+      sum = sum * f0 + ml.y * f1;
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        o[4 * i] = o[4 * i] * f0 + x[i].x * f1;
+        o[4 * i + 1] = o[4 * i + 1] * f0 + x[i].y * f1;
+        o[4 * i + 2] = o[4 * i + 2] * f0 + x[i].z * f1;
+        o[4 * i + 3] = o[4 * i + 3] * f0 + x[i].w * f1;
+      }
+    }
+  }
+  if (row >= n.rows) return;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int tok = n.cu0 + row / g.G, hd = n.head * g.G + row % g.G;
+  const long long to = (long long)tok * g.out.s_row + (long long)hd * g.out.s_head + warp * V;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] *= inv;
+  if (g.out_f32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.out.data) + to);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out.data) + to);
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i)
+      dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+  }
+  if (warp == 0) store_lse(g, tok, hd, M, sum);
+}
+
 template <int D>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cudaError_t e = configure_kernel<cache_chunk_kernel<D>>(kLaunchRegs, Lay<D>::kAlloc);
@@ -579,7 +649,7 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   b.line_shift = a.items * (places + 2) < (1LL << 30) ? 0 : std::max(1, line_shift_for(a.items, units));
   e = launch_early(cache_chunk_kernel<D>, grid, kThreads, Lay<D>::kAlloc, st, b);
   if (e != cudaSuccess) return e;
-  return launch_early(cache_join_kernel<256, D>, dim3(grid, 32), 256 * kJoinGroups, 0, st, b);
+  return launch_early(chunk_join_kernel<D>, dim3(grid, 8), 256, 0, st, b);
 }
 
 }  // namespace
