@@ -734,7 +734,8 @@ def ring_attn_cache_append(k, v, cache, page_table, kv_lens, cu_seqlens, q=None,
             raise ValueError("q_out without q")
         if q is not None:
             tq = _rows3(q, index)
-            q_out = torch.empty_like(q) if q_out is None else q_out
+            if q_out is None:
+                q_out = torch.empty_like(q)
             to = tq if q_out is q else _rows3(q_out, index)
         if rope is not None:
             tc, ts = _rows2(rope[0], index), _rows2(rope[1], index)
@@ -751,7 +752,7 @@ def ring_attn_cache_append(k, v, cache, page_table, kv_lens, cu_seqlens, q=None,
 def ring_attn_cache_read(cache, page_table, kv_lens, cu_seqlens, k_out=None, v_out=None, stream=None):
     """The last cu_seqlens[i + 1] - cu_seqlens[i] cached tokens of every sequence as bf16.
 
-    Returns (k, v), each (rows, hk, d): contiguous input for the attention calls."""
+    Returns (k, v), each (rows, hk, d): input for the attention calls."""
     lib = load()
     with _cache_guard(cache, stream):
         index = cache.index
@@ -797,7 +798,10 @@ def ring_attn_cache_fwd(q, cache, page_table, kv_lens, cu_seqlens, causal=True, 
             out = torch.empty((rows, h, d), dtype=out_dtype, device=cache.device)
         if lse is None:
             lse = torch.empty((h, rows), dtype=torch.float32, device=cache.device)
-        to, tl = _rows3(out, index), _rows2(lse, index)
+            tl = _PACK_TENSOR(lse.data_ptr(), RA_FP32, 2, h, rows, 0, 0, rows, 1, 0, 0)
+        else:
+            tl = _rows2(lse, index)
+        to = _rows3(out, index)
         if cu.total:
             if workspace is None:
                 workspace = ring_attn_cache_workspace(q, cache, cu)
