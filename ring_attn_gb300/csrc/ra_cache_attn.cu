@@ -38,7 +38,8 @@ struct Lay {
   static constexpr int R = 8 * NT;
   static constexpr int kK = 0, kV = 32 * D / 2, kKs = 2 * kV, kVs = kKs + 32 * D / 16;
   static constexpr int kStage = kVs + 32 * D / 16;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  // the shared memory of an SM over its warps
+  static constexpr int kStages = (W == 4 ? 3 : W == 12 ? 4 : 6) * (128 / D);
   static constexpr int kRing = kWarps * kStages * kStage;
   // A warp's results at an item's end: R rows of D floats (padded), M and sums.
   // With 8 rows they fit into the stage just consumed, so the next item's tiles
@@ -57,7 +58,7 @@ struct Lay {
 // `whole`: every item is one place on the line, so none is shared.
 template <int NT>
 struct FewRows {
-  static constexpr int R = 8 * NT, kItemCost = 2;
+  static constexpr int R = 8 * NT, kItemCost = 4;
   static constexpr bool kOneTile = true;
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.a = g.whole ? 1 : max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
@@ -639,8 +640,9 @@ bool many_rows(int max_new, int G) { return (long long)max_new * G > 32; }
 // Query rows of an item in units of 8.
 int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
-// One block per SM with as many warps as the small blocks have together.
-constexpr int big_warps(int nt) { return 4 * small_blocks(nt); }
+// Warps of the block when there is one per SM.  With 8 rows, 12 warps with 4 stages each
+// take 43 us for one query over 128K keys, 16 with 3 stages 49 us.
+constexpr int big_warps(int nt) { return nt == 4 ? 8 : 12; }
 
 template <int D, int NT, int W>
 cudaError_t launch_w(const CacheAttnArgs& a, bool whole, int grid, cudaStream_t st) {
