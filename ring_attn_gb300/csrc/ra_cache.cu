@@ -35,14 +35,17 @@ __device__ __forceinline__ float dot2_odd(float a, float b, float c, float d) {
   return fabsf(hi) <= 3.0e38f ? to_odd(hi, rest) : s;
 }
 
-// x / s rounded to odd (r: the reciprocal of s, rounded): one correction step
-// brings the quotient within a unit of its last place, and the remainder's sign
-// says on which side the exact one lies, so that the conversion to 4 or 8 bits
-// rounds as for the exact quotient.
-__device__ __forceinline__ float div_odd(float x, float s, float r) {
+// x / s (r: the reciprocal of s, rounded): one correction step brings the quotient
+// within half a unit of its last place.
+__device__ __forceinline__ float near_quotient(float x, float s, float r) {
   const float q0 = __fmul_rn(x, r);
-  const float q = __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0);
-  return fabsf(q0) < 1e30f ? to_odd(q, __fmaf_rn(-q, s, x)) : q0;
+  return fabsf(q0) < 1e30f ? __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0) : q0;
+}
+// x / s rounded to odd: the remainder's sign says on which side of the quotient
+// the exact one lies, so that the conversion to 4 or 8 bits rounds as for that.
+__device__ __forceinline__ float div_odd(float x, float s, float r) {
+  const float q = near_quotient(x, s, r);
+  return fabsf(q) < 1e30f ? to_odd(q, __fmaf_rn(-q, s, x)) : q;
 }
 
 __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
@@ -82,12 +85,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint32_t scale
     float q[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (ODD) {
-        q[k] = div_odd(x[i + k], s, r);
-      } else {
-        const float q0 = __fmul_rn(x[i + k], r);
-        q[k] = fabsf(q0) < 1e30f ? __fmaf_rn(__fmaf_rn(-q0, s, x[i + k]), r, q0) : q0;
-      }
+      q[k] = ODD ? div_odd(x[i + k], s, r) : near_quotient(x[i + k], s, r);
     }
     codes |= to_e2m1x2(q[0], q[1]) << (4 * i);
   }
@@ -107,22 +105,25 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// sure_scale and sure_codes: scale_of and codes_of for numbers known to within
-// `off`, setting `unsure` where that leaves two answers.
-__device__ __forceinline__ uint32_t sure_scale(float m, float off, bool& unsure) {
-  const float q = fminf(m, 6.f * 448.f) * (1.f / 6.f), d = fmaf(q, 0x1p-22f, off);
+// sure_scale and sure_codes: scale_of and codes_of for fp32 numbers known to within
+// `off`, setting `unsure` where that leaves two answers.  exact: the numbers are bf16
+// (not rotated; they often lie on borders), and the answers are final.
+__device__ __forceinline__ uint32_t sure_scale(float m, float off, bool exact, bool& unsure) {
+  // (m / 6 as a product: no bf16 m lies so near a border of e4m3 that it matters)
+  const float q = fminf(m, 6.f * 448.f) * (1.f / 6.f), d = exact ? 0.f : fmaf(q, 0x1p-22f, off);
   const uint32_t lo = to_e4m3(q - d), hi = to_e4m3(q + d);
   unsure |= lo != hi;
   return hi ? hi : 1u;
 }
-__device__ __forceinline__ uint32_t sure_codes(const float (&x)[8], uint32_t scale, float off, bool& unsure) {
+__device__ __forceinline__ uint32_t sure_codes(const float (&x)[8], uint32_t scale, float off, bool exact, bool& unsure) {
   const float s = f16x2_to_f32(e4m3x2_to_f16(scale)).x, r = __frcp_rn(s);
-  const float d = fmaf(off, r, 0x1p-19f);  // quotients up to 8 in fp32 are off by less than the second part
+  const float d = exact ? 0.f : fmaf(off, r, 0x1p-19f);  // quotients up to 8 in fp32 are off by less than the second part
   uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    lo |= to_e2m1x2(fmaf(x[i], r, -d), fmaf(x[i + 1], r, -d)) << (4 * i);
-    hi |= to_e2m1x2(fmaf(x[i], r, d), fmaf(x[i + 1], r, d)) << (4 * i);
+    const float q0 = near_quotient(x[i], s, r), q1 = near_quotient(x[i + 1], s, r);
+    lo |= to_e2m1x2(q0 - d, q1 - d) << (4 * i);
+    hi |= to_e2m1x2(q0 + d, q1 + d) << (4 * i);
   }
   unsure |= lo != hi;
   return hi;
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendA
         const float off = in * 0x1p-22f;
         float ma, mb;
         group_max<STYLE>(u, v, own, ma, mb);
-        sa = sure_scale(ma, off, unsure), sbb = STYLE == 1 ? sure_scale(mb, off, unsure) : sa;
-        xa = sure_codes(u, sa, off, unsure), xb = sure_codes(v, sbb, off, unsure);
+        sa = sure_scale(ma, off, !turn, unsure), sbb = STYLE == 1 ? sure_scale(mb, off, !turn, unsure) : sa;
+        xa = sure_codes(u, sa, off, !turn, unsure), xb = sure_codes(v, sbb, off, !turn, unsure);
         if (__any_sync(0xffffffffu, unsure)) {
           rotate16<STYLE>(x, y, cs, sn, turn, u, v, dot2_odd);
           group_max<STYLE>(u, v, own, ma, mb);
@@ -379,7 +380,7 @@ struct Share {
   unsigned grid;
 };
 static Share share_of(long long tokens, int passes) {
-  const long long want = (long long)num_sms() * 32;
+  const long long want = (long long)num_sms() * 16;
   int per_warp = passes;
   while (per_warp > 1 && tokens * ((passes + per_warp - 1) / per_warp) < want) per_warp = (per_warp + 1) / 2;
   const int wpt = (passes + per_warp - 1) / per_warp;
