@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendA
   const long long n_warps = (long long)a.s.total * warps_per_token;
   for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
     const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
-    const int i = segment_of_warp(a.s.cu, a.s.n_seqs, t);
+    const int i = sequence_of(a.s, t);
     const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
-    const int tok = len - __ldg(a.s.cu + i + 1) + t;
+    const int tok = len - a.s.cu[i + 1] + t;
     if (tok < 0) continue;
     const int half = a.rot >> 4;  // chunks in half the rotated part
     const bool turn = STYLE == 1 ? l < half : STYLE == 2 ? 16 * l < a.rot : false;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendA
     const bool own = cb == ca + 1 && !(ca & 1);  // both chunks are one scale group
     float cs[8], sn[8];
     if (STYLE) {
-      const int pos = a.positions ? __ldg(a.positions + t) : tok;
+      const int pos = a.positions ? a.positions[t] : tok;
       if ((unsigned)pos >= (unsigned)a.max_pos) {
         if (lane == 0) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_POS);
         continue;
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendA
       const float4* ps = reinterpret_cast<const float4*>(a.sin_t + (long long)pos * a.sin_stride + 8 * l);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 c = turn ? __ldg(pc + k) : make_float4(1.f, 1.f, 1.f, 1.f);
-        const float4 s = turn ? __ldg(ps + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 c = turn ? pc[k] : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 s = turn ? ps[k] : make_float4(0.f, 0.f, 0.f, 0.f);
         cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
         sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
       }
     }
-    const int at_table = __ldg(a.s.table + (long long)i * a.s.table_stride + (tok >> a.c.page_shift));  // used below
+    const int at_table = a.s.table[(long long)i * a.s.table_stride + (tok >> a.c.page_shift)];  // used below
     const int nq = (a.h + RPP - 1) / RPP, nk = (a.hk + RPP - 1) / RPP;
     const int p_end = min(nq + 2 * nk, (part + 1) * per_warp);
     int p = part * per_warp;
@@ -315,9 +315,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a, 
   const long long n_warps = (long long)a.s.total * warps_per_token;
   for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
     const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
-    const int i = segment_of_warp(a.s.cu, a.s.n_seqs, t);
+    const int i = sequence_of(a.s, t);
     const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
-    const int tok = len - __ldg(a.s.cu + i + 1) + t;
+    const int tok = len - a.s.cu[i + 1] + t;
     if (tok < 0) continue;
     const int page = cache_page(a.s, a.c, i, tok, a.ctl);
     if (page < 0) continue;
@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a, 
         if (row < end) {
           const bool is_v = row >= a.hk;
           const int head = is_v ? row - a.hk : row;
-          w[k] = __ldg(reinterpret_cast<const uint2*>((is_v ? a.c.v.data : a.c.k.data) + oc + head * a.c.k.s_head));
-          sc[k] = __ldg((is_v ? a.c.vs.data : a.c.ks.data) + os + head * a.c.ks.s_head);
+          w[k] = *(reinterpret_cast<const uint2*>((is_v ? a.c.v.data : a.c.k.data) + oc + head * a.c.k.s_head));
+          sc[k] = (is_v ? a.c.vs.data : a.c.ks.data)[os + head * a.c.ks.s_head];
         }
       }
 #pragma unroll

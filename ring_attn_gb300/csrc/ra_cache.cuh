@@ -9,13 +9,15 @@
 namespace ra {
 
 // The cache's kernels are launched so that their blocks may be set up while the
-// stream's previous kernel still runs (programmatic dependent launch): every
-// kernel calls after_previous_kernel before it touches memory, which waits until
-// that kernel has ended and its writes are visible, and allows the same to the next one.
-// Saves about 2 us a launch for single tokens.
+// stream's previous kernel still runs (programmatic dependent launch): every kernel
+// calls after_previous_kernel before it touches memory, which waits until that
+// kernel has ended and its writes are visible, and only then allows the same to
+// the next one, so no more than two kernels overlap.  Global memory is read by
+// plain loads, which stay behind the wait (loads through the read-only path need
+// not).  Saves about 2 us a launch for single tokens.
 __device__ __forceinline__ void after_previous_kernel() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
@@ -35,8 +37,23 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
 // Sites of device-side errors in the low byte of check_device_error's info.
 enum : int { SITE_CACHE_LEN = 0x61, SITE_CACHE_PAGE = 0x62, SITE_CACHE_POS = 0x63 };
 
+// Sequence whose new tokens row t is one of; t is the same in every lane of a full
+// warp, which probes 32 entries of cu a round.
+__device__ __forceinline__ int sequence_of(const CacheSeqs& s, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = s.n_seqs - 1;
+  while (lo < hi) {
+    const int step = (hi - lo + 32) >> 5, at = lo + lane * step;
+    const bool le = at <= hi && s.cu[at] <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, le) | 1u;
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
 __device__ __forceinline__ int cache_len(const CacheSeqs& s, int i, int bound, const DevCtl& ctl) {
-  const int n = __ldg(s.lens + i);
+  const int n = s.lens[i];
   if (n > bound) {
     record_error(ctl, DEV_BOUNDS, SITE_CACHE_LEN);
     return bound;
@@ -54,7 +71,7 @@ __device__ __forceinline__ int check_page(const CacheView& c, int pg, const DevC
 }
 // Physical page of token `tok` of sequence i (0 <= tok < max_pages * page), or -1.
 __device__ __forceinline__ int cache_page(const CacheSeqs& s, const CacheView& c, int i, int tok, const DevCtl& ctl) {
-  return check_page(c, __ldg(s.table + (long long)i * s.table_stride + (tok >> c.page_shift)), ctl);
+  return check_page(c, s.table[(long long)i * s.table_stride + (tok >> c.page_shift)], ctl);
 }
 
 __device__ __forceinline__ long long row_offset(const CacheRows& r, int page, int head, int row) {

@@ -177,13 +177,13 @@ __device__ __forceinline__ void make_piece(const CacheAttnArgs& g, Pieces& p) {
     return;
   }
   p.at = at;
-  const int cu0 = __ldg(g.s.cu + x.seq);
+  const int cu0 = g.s.cu[x.seq];
   JoinNote n = p.note;
   note_piece<Kind>(g, x, p.quota, cu0, n);
   p.note = n;
   y.seq = x.seq, y.head = x.head, y.cu0 = cu0, y.len = x.len, y.n_new = x.n_new;
   y.ua = x.ua, y.ub = x.ub, y.whole = x.ub - x.ua == x.units;
-  if (__ldg(g.s.lens + x.seq) > g.max_kv) record_error(g.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+  if (g.s.lens[x.seq] > g.max_kv) record_error(g.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
 }
 
 // A warp's copies: its tiles go to the ring slot by slot, their pages read two turns ahead.
@@ -225,8 +225,8 @@ struct Stream {
   }
   __device__ __forceinline__ void pages(int k, int& p, int& q) {
     if (k < end_key) {
-      p = __ldg(table + (k >> a.c.page_shift));
-      if (a.c.page_shift == 4) q = k + 16 < end_key ? __ldg(table + (k >> 4) + 1) : p;
+      p = table[k >> a.c.page_shift];
+      if (a.c.page_shift == 4) q = k + 16 < end_key ? table[(k >> 4) + 1] : p;
     }
   }
   // Copies the warp's tile of a turn (nothing when none is left) and moves on, to the run's
@@ -320,6 +320,12 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       sp.made = 0;
       sp.over = false;
       make_piece<Kind>(a, sp);
+      // the first copies may go beyond a short first piece
+      if (L::kFlow)
+        for (int ahead = turns_of<W>(sp.ring[0].ub - sp.ring[0].ua); ahead < L::kStages - 1 && !sp.over;) {
+          make_piece<Kind>(a, sp);
+          ahead += turns_of<W>(sp.ring[sp.made - 1].ub - sp.ring[sp.made - 1].ua);
+        }
     }
   }
   __syncthreads();
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       st.to = ring;
       st.piece(i);
 #pragma unroll 1
-      for (int s = 0; s < L::kStages - 1; ++s) st.load(false);
+      for (int s = 0; s < L::kStages - 1; ++s) st.load(L::kFlow);
     }
     if (planner) {  // the pieces that the copies may reach during this one, and the one after it
       for (int k = i + 1, ahead = 0; k == i + 1 || ahead < L::kStages - 1; ++k) {

@@ -103,9 +103,9 @@ struct RawRow {
   __device__ __forceinline__ void load(const uint8_t* c, const uint8_t* s, bool ok) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-      code[i] = ok ? __ldg(reinterpret_cast<const uint4*>(c) + i) : make_uint4(0, 0, 0, 0);
+      code[i] = ok ? reinterpret_cast<const uint4*>(c)[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) scale[i] = ok ? __ldg(reinterpret_cast<const uint32_t*>(s) + i) : 0u;
+    for (int i = 0; i < D / 64; ++i) scale[i] = ok ? reinterpret_cast<const uint32_t*>(s)[i] : 0u;
   }
   // Row `r` of a tile at `tile`.
   __device__ __forceinline__ void store(uint32_t tile, int r) const {
@@ -271,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         int seen = -1;
         for (int i = 0;; ++i) {
           const bool more = next_piece<ManyRows>(a, at, end_u, x);
-          const int cu0 = more ? __ldg(a.s.cu + x.seq) : 0;
+          const int cu0 = more ? a.s.cu[x.seq] : 0;
           if (more) {
-            if (x.seq != seen && __ldg(a.s.lens + x.seq) > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
+            if (x.seq != seen && a.s.lens[x.seq] > a.max_kv) record_error(a.ctl, DEV_BOUNDS, SITE_CACHE_LEN);
             seen = x.seq;
             note_piece<ManyRows>(a, x, quota, cu0, note);
           }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       auto page_of = [&](int u) {  // read a unit ahead
         const int key = u * kUnit + r;
         live = key < len;
-        page = live ? __ldg(table + (key >> a.c.page_shift)) : 0;
+        page = live ? table[key >> a.c.page_shift] : 0;
       };
       auto place = [&](int u) {
         if (live && (unsigned)page >= (unsigned)a.c.n_pages) {
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                                                           (long long)(x.head * a.G + row % a.G) * a.q.s_head);
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
-          const uint4 w = __ldg(src + k);
+          const uint4 w = src[k];
           q[4 * k] = w.x, q[4 * k + 1] = w.y, q[4 * k + 2] = w.z, q[4 * k + 3] = w.w;
         }
         end_row = a.causal ? min(x.len, x.len - x.n_new + tok + 1) : x.len;

@@ -54,8 +54,8 @@ __device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int len, int 
 }
 template <class Kind>
 __device__ __forceinline__ LineSeq line_seq(const CacheAttnArgs& g, int i) {
-  const int n_new = __ldg(g.s.cu + i + 1) - __ldg(g.s.cu + i);
-  return line_of<Kind>(g, max(0, min(__ldg(g.s.lens + i), g.max_kv)), n_new);
+  const int n_new = g.s.cu[i + 1] - g.s.cu[i];
+  return line_of<Kind>(g, max(0, min(g.s.lens[i], g.max_kv)), n_new);
 }
 template <class Kind>
 __device__ __forceinline__ int line_length(const CacheAttnArgs& g, const LineSeq& s) {

@@ -195,6 +195,37 @@ def test_attention_over_the_cache(ra, n_new, kv, h, hk, d, page, causal, order):
     assert_within("out", o32[:total], ref, tol)
 
 
+@pytest.mark.parametrize("seqs,lo,hi,new,h,hk,d,page", [
+    (60, 1, 400, 1, 16, 8, 64, 32),      # many short items: a block works on several, runs begin and end inside them
+    (60, 1, 3000, 1, 12, 4, 128, 64),
+    (23, 100, 1500, 3, 16, 8, 64, 16),
+    (40, 1, 700, 4, 16, 4, 128, 16),     # 16 rows an item
+    (30, 5, 2500, 5, 24, 6, 64, 64),     # 20 rows
+    (160, 1, 90, 1, 2, 1, 128, 16),      # more sequences than a block has threads
+    (3, 3000, 9000, 1, 8, 8, 128, 64),   # few long items, cut into pieces
+    (2, 2100, 4200, 2, 8, 2, 64, 32),
+    (1, 30000, 30000, 1, 6, 3, 64, 128),
+    (20, 30, 2000, 90, 8, 2, 64, 32),    # many row tiles, tensor-core kernel
+    (150, 1, 300, 40, 4, 2, 64, 16),
+])
+def test_attention_over_many_ragged_sequences(ra, seqs, lo, hi, new, h, hk, d, page):
+    """How the work line is cut: every run of items, pieces and turns has to give the same rows."""
+    g = np.random.default_rng(seqs + hi)
+    kv = np.exp(g.uniform(np.log(lo), np.log(hi), seqs)).astype(int).tolist()
+    n_new = g.integers(0 if seqs > 2 else new, new + 1, seqs).tolist()
+    n_new[0] = new
+    c = Case(n_new, kv, h, hk, d, page, seed=seqs)
+    cache = c.fill(ra)
+    q = c.queries()
+    out, lse = torch.full((c.rows, h, d), float("nan"), dtype=torch.bfloat16, device="cuda"), torch.full((h, c.rows), float("nan"), device="cuda")
+    ws = ra.ring_attn_cache_workspace(q, cache, ra.CuSeqlens(c.cu, "cuda")).fill_(0xff)
+    ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, c.cu.tolist(), out=out, lse=lse, workspace=ws)
+    check_no_device_error(ra)
+    ref, ref_l, tol, tol_l = c.expect(q, True)
+    assert_within("lse", lse, ref_l, tol_l)
+    assert_within("out", out, ref, tol)
+
+
 @pytest.mark.parametrize("h,hk,new", [(4, 1, 1), (8, 2, 60)])
 def test_attention_with_large_and_small_queries(ra, h, hk, new):
     """Scores far apart (one key takes all), queries beyond fp16's range, all-zero queries."""
