@@ -8,11 +8,10 @@ library is missing or a tensor is not on a CUDA device the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.util
 import math
 import os
-import struct
 
 import torch
 
@@ -95,6 +94,7 @@ def load():
     lib = ctypes.CDLL(path)
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     T = ctypes.POINTER(_Tensor)
+    C, S = ctypes.POINTER(_KVCache), ctypes.POINTER(_KVSeqs)
     sig = {
         "ring_attn_fwd": [T, T, T, I32, I32, I32, F32, T, T, P, SZ, P],
         "ring_attn_fwd_step": [T, T, T, I32, I32, I32, F32, I32, T, T, P],
@@ -109,10 +109,9 @@ def load():
         "ring_attn_varlen_unpermute": [T, T, P, P, I32, I32, I32, I32, P],
         "ring_attn_permute": [T, T, I32, I32, I32, P],
         "ring_attn_unpermute": [T, T, I32, I32, I32, P],
-        # ra_tensor, ra_kv_cache and ra_kv_seqs arguments as addresses or packed bytes
-        "ring_attn_cache_append": [P, P, P, P, P, I32, P, P, P, P, P],
-        "ring_attn_cache_read": [P, P, P, P, P],
-        "ring_attn_cache_fwd": [P, P, P, I32, F32, I32, P, P, P, SZ, P],
+        "ring_attn_cache_append": [T, T, T, T, T, I32, P, C, S, T, P],
+        "ring_attn_cache_read": [C, S, T, T, P],
+        "ring_attn_cache_fwd": [T, C, S, I32, F32, I32, T, T, P, SZ, P],
         "ring_attn_check_device_error": [P, ctypes.POINTER(I32)],
         "ring_attn_set_knob": [I32, I64],
         "ring_attn_timing_enable": [I32],
@@ -302,6 +301,9 @@ class CuSeqlens:
         self.n_seqs = host.numel() - 1
         self.total = int(host[-1])
         self.max_seqlen = int((host[1:] - host[:-1]).max())
+        # for the cache calls: arrays' addresses, device and sizes
+        self._call = (self.dev.data_ptr(), host.data_ptr(), self.dev.get_device() if self.dev.is_cuda else -1, self.n_seqs,
+                      self.total, self.max_seqlen)
 
 
 def _max_len(cu_seqlens, host):
@@ -602,10 +604,11 @@ class KVCache:
                 raise ValueError(f"{name} must be a 4-D {dtype} tensor")
             if x.device != k.device:
                 raise ValueError("the cache's tensors must be on one device")
-        self.device, self.index = k.device, k.get_device()
+        self.device = k.device
         self.n_pages, self.hk, self.page, self.d = k.shape[0], k.shape[1], k.shape[2], 2 * k.shape[3]
         self._c = _KVCache(_desc(k, RA_E2M1X2), _desc(k_scale, RA_E4M3), _desc(v, RA_E2M1X2), _desc(v_scale, RA_E4M3))
-        self._ptr = ctypes.addressof(self._c)
+        self.scale = 1.0 / math.sqrt(max(self.d, 1))  # the default softmax scale
+        self._call = (ctypes.addressof(self._c), k.get_device(), self.hk, self.d)
 
     @classmethod
     def empty(cls, n_pages, page, hk, d, device="cuda"):
@@ -622,97 +625,47 @@ def _desc(x, dtype):
     return _Tensor(x.data_ptr(), dtype, x.dim(), _I64x4(*x.shape), _I64x4(*x.stride()))
 
 
-# The cache calls serve single tokens, where marshalling costs more than the
-# kernels: their arguments are packed as bytes (a tenth of the time that filling
-# ctypes structures takes) in the layout of ra_tensor and ra_kv_seqs.
-_PACK_TENSOR = struct.Struct("=Qii8q").pack
-_PACK_SEQS = struct.Struct("=QqQQQii").pack
-_RA_DTYPE = {torch.bfloat16: RA_BF16, torch.float32: RA_FP32}
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_EXT = None
 
 
-def _bad_tensor(x, index, dims):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError("ring_attn_gb300 takes CUDA tensors only")
-    if x.get_device() != index:
-        raise ValueError(f"tensor on {x.device}, cache on cuda:{index}")
-    if x.dtype not in _RA_DTYPE:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    raise ValueError(f"expected a {dims}-D tensor, got {tuple(x.shape)}")
+def _ext():
+    """The compiled marshaller of the cache calls, bound to the loaded library."""
+    global _EXT
+    if _EXT is None:
+        lib = load()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_ra_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with ring_attn_gb300.build.build() "
+                               "(or __graft_entry__.build()); there is no fallback path")
+        spec = importlib.util.spec_from_file_location("_ra_binding", path)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.use(*(ctypes.cast(getattr(lib, "ring_attn_cache_" + f), ctypes.c_void_p).value
+                  for f in ("append", "read", "fwd", "workspace_size")))
+        _EXT = ext
+    return _EXT
 
 
-def _rows3(x, index):
-    """The bytes of the ra_tensor of a 3-D bf16 or fp32 tensor on the cache's device."""
-    dtype = _RA_DTYPE.get(x.dtype) if isinstance(x, torch.Tensor) else None
-    if dtype is None or x.get_device() != index or x.dim() != 3:
-        _bad_tensor(x, index, 3)
-    a, b, c = x.shape
-    d, e, f = x.stride()
-    return _PACK_TENSOR(x.data_ptr(), dtype, 3, a, b, c, 0, d, e, f, 0)
-
-
-def _rows2(x, index):
-    dtype = _RA_DTYPE.get(x.dtype) if isinstance(x, torch.Tensor) else None
-    if dtype is None or x.get_device() != index or x.dim() != 2:
-        _bad_tensor(x, index, 2)
-    a, b = x.shape
-    d, e = x.stride()
-    return _PACK_TENSOR(x.data_ptr(), dtype, 2, a, b, 0, 0, d, e, 0, 0)
-
-
-def _ints(x, index, dims, what):
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.int32 or x.dim() != dims or x.get_device() != index:
-        raise ValueError(f"{what} must be a {dims}-D int32 tensor on cuda:{index}")
-    if x.stride(-1) != 1 and x.shape[-1] > 1:
-        raise ValueError(f"{what} must be contiguous along its last dimension")
-    return x.data_ptr()
-
-
-class _On:
-    """Makes the cache's device, or the given stream, current for a call's outputs and launches."""
-
-    def __init__(self, index, stream):
-        self.guard = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
-        if stream is not None and stream.device.index != index:
-            raise ValueError(f"stream on {stream.device}, cache on cuda:{index}")
-
-    def __enter__(self):
-        self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        self.guard.__exit__(*exc)
-
-
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _cache_guard(cache, stream):
+def _cache_call(name, cache, cu_seqlens, stream, *args):
+    """Runs a cache call on the given stream (None: the current one of the cache's device) and checks its status."""
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
-    if stream is None and cache.index == torch.cuda.current_device():
-        return _NO_GUARD
-    return _On(cache.index, stream)
-
-
-def _seqs(cache, page_table, kv_lens, cu_seqlens):
-    """(CuSeqlens, bytes of the ra_kv_seqs)."""
-    index = cache.index
-    if not isinstance(cu_seqlens, CuSeqlens):
-        cu_seqlens = CuSeqlens(cu_seqlens, cache.device)
-    elif cu_seqlens.dev.get_device() != index:
-        raise ValueError(f"CuSeqlens was prepared for {cu_seqlens.dev.device}, not cuda:{index}")
-    table, lens = _ints(page_table, index, 2, "page_table"), _ints(kv_lens, index, 1, "kv_lens")
-    n = cu_seqlens.n_seqs
-    rows, width = page_table.shape
-    if rows != n or kv_lens.shape[0] != n:
-        raise ValueError(f"page_table and kv_lens must have one row for each of the {n} sequences")
-    return cu_seqlens, _PACK_SEQS(table, page_table.stride(0) if n > 1 else width, lens, cu_seqlens.dev.data_ptr(),
-                                  cu_seqlens.host.data_ptr(), width, n)
-
-
-def _launch_stream(index):
-    """The current stream's handle (torch's own accessor where it has one: a tenth of the time)."""
-    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    f = getattr(_EXT or _ext(), name)
+    if stream is None:
+        if not isinstance(cu_seqlens, CuSeqlens):
+            with torch.cuda.device(cache.device):
+                cu_seqlens = CuSeqlens(cu_seqlens, cache.device)
+        r = f(cache._call, cu_seqlens._call, *args)
+    else:
+        if stream.device != cache.device:
+            raise ValueError(f"stream on {stream.device}, cache on {cache.device}")
+        with torch.cuda.stream(stream):  # outputs, workspace and cu_seqlens belong to it, too
+            if not isinstance(cu_seqlens, CuSeqlens):
+                cu_seqlens = CuSeqlens(cu_seqlens, cache.device)
+            r = f(cache._call, cu_seqlens._call, *args)
+    if r[0] != 0:
+        _check(r[0], "ring_attn_" + name)
+    return r
 
 
 def ring_attn_cache_append(k, v, cache, page_table, kv_lens, cu_seqlens, q=None, rope=None, positions=None,
@@ -724,47 +677,16 @@ def ring_attn_cache_append(k, v, cache, page_table, kv_lens, cu_seqlens, q=None,
     (n_seqs, max_pages) int32.  q: (rows, h, d) bf16 or None; q_out may be q.  rope: (cos, sin), each
     (positions, r // 2) fp32, or None; positions: (rows,) int32, or None for the tokens' cache indices.
     Rows past cu_seqlens[-1] are left as they were.  Returns q_out (None without q)."""
-    lib = load()
-    with _cache_guard(cache, stream):
-        index = cache.index
-        cu, seqs = _seqs(cache, page_table, kv_lens, cu_seqlens)
-        tk, tv = _rows3(k, index), _rows3(v, index)
-        tq = to = tc = ts = pos = None
-        if q is None and q_out is not None:
-            raise ValueError("q_out without q")
-        if q is not None:
-            tq = _rows3(q, index)
-            if q_out is None:
-                q_out = torch.empty_like(q)
-            to = tq if q_out is q else _rows3(q_out, index)
-        if rope is not None:
-            tc, ts = _rows2(rope[0], index), _rows2(rope[1], index)
-        if positions is not None:
-            pos = _ints(positions, index, 1, "positions")
-            if positions.shape[0] < cu.total:
-                raise ValueError("positions must have an entry for every new token")
-        if cu.total:
-            _check(lib.ring_attn_cache_append(tq, tk, tv, tc, ts, 1 if interleaved else 0, pos, cache._ptr, seqs, to,
-                                              _launch_stream(index)), "ring_attn_cache_append")
-    return q_out
+    cos, sin = rope if rope is not None else (None, None)
+    return _cache_call("cache_append", cache, cu_seqlens, stream, k, v, page_table, kv_lens, q, cos, sin, positions,
+                       interleaved, q_out)[1]
 
 
 def ring_attn_cache_read(cache, page_table, kv_lens, cu_seqlens, k_out=None, v_out=None, stream=None):
     """The last cu_seqlens[i + 1] - cu_seqlens[i] cached tokens of every sequence as bf16.
 
     Returns (k, v), each (rows, hk, d): input for the attention calls."""
-    lib = load()
-    with _cache_guard(cache, stream):
-        index = cache.index
-        cu, seqs = _seqs(cache, page_table, kv_lens, cu_seqlens)
-        if k_out is None:
-            k_out = torch.empty((cu.total, cache.hk, cache.d), dtype=torch.bfloat16, device=cache.device)
-        if v_out is None:
-            v_out = torch.empty((cu.total, cache.hk, cache.d), dtype=torch.bfloat16, device=cache.device)
-        tk, tv = _rows3(k_out, index), _rows3(v_out, index)
-        if cu.total:
-            _check(lib.ring_attn_cache_read(cache._ptr, seqs, tk, tv, _launch_stream(index)), "ring_attn_cache_read")
-    return k_out, v_out
+    return _cache_call("cache_read", cache, cu_seqlens, stream, page_table, kv_lens, k_out, v_out)[1:]
 
 
 def ring_attn_cache_workspace_size(total, max_new, h, hk, d, n_seqs) -> int:
@@ -788,29 +710,12 @@ def ring_attn_cache_fwd(q, cache, page_table, kv_lens, cu_seqlens, causal=True, 
     cache up to itself; else the whole sequence.  max_kv_len: an upper bound of kv_lens (0: what the
     page table can hold).  workspace: from ring_attn_cache_workspace, or None to allocate it.
     Returns (out (rows, h, d) bf16 or fp32, lse (h, rows) fp32); rows that see nothing get 0 and -inf."""
-    lib = load()
-    with _cache_guard(cache, stream):
-        index = cache.index
-        cu, seqs = _seqs(cache, page_table, kv_lens, cu_seqlens)
-        tq = _rows3(q, index)
-        rows, h, d = q.shape
-        if out is None:
-            out = torch.empty((rows, h, d), dtype=out_dtype, device=cache.device)
-        if lse is None:
-            lse = torch.empty((h, rows), dtype=torch.float32, device=cache.device)
-            tl = _PACK_TENSOR(lse.data_ptr(), RA_FP32, 2, h, rows, 0, 0, rows, 1, 0, 0)
-        else:
-            tl = _rows2(lse, index)
-        to = _rows3(out, index)
-        if cu.total:
-            if workspace is None:
-                workspace = ring_attn_cache_workspace(q, cache, cu)
-            elif workspace.get_device() != index:
-                raise ValueError(f"workspace must be on cuda:{index}")
-            _check(lib.ring_attn_cache_fwd(tq, cache._ptr, seqs, 1 if causal else 0, _scale(softmax_scale, d), max_kv_len,
-                                           to, tl, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                           _launch_stream(index)), "ring_attn_cache_fwd")
-    return out, lse
+    if out is None and out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported dtype {out_dtype}")
+    if softmax_scale is None and isinstance(cache, KVCache):
+        softmax_scale = cache.scale
+    return _cache_call("cache_fwd", cache, cu_seqlens, stream, q, page_table, kv_lens, causal, softmax_scale, max_kv_len,
+                       out, lse, out_dtype is torch.float32, workspace)[1:]
 
 
 def ring_attn_check_device_error(stream=None):

@@ -1,4 +1,5 @@
-"""Builds libringattn.so in-tree for sm_103a (nvcc, one translation unit per kernel family, in parallel).
+"""Builds libringattn.so in-tree for sm_103a (nvcc, one translation unit per kernel family, in parallel),
+and _ra_binding.so (the host compiler), which marshals torch tensors into its cache calls.
 
 build(debug_bounds=True) builds the debug variant libringattn_dbg.so instead:
 the same sources compiled with RA_DEBUG_BOUNDS, under which every kernel checks
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -27,6 +29,22 @@ HEADERS = [os.path.join(CSRC, h) for h in ("ra_device.cuh", "ra_internal.h", "ra
     os.path.join(ROOT, "include", "ringattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
+
+
+BINDING_SRC = os.path.join(CSRC, "ra_binding.cpp")
+BINDING = os.path.join(PKG, "_ra_binding.so")
+
+
+def _binding_cmd() -> list:
+    import torch
+
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-o", BINDING, BINDING_SRC,
+            *("-I" + i for i in inc if os.path.isdir(i)), "-L" + os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def _nvcc() -> str:
@@ -66,12 +84,15 @@ def build(verbose: bool = False, force: bool = False, debug_bounds: bool = False
         if force or _stale(o, [s] + HEADERS):
             cmd = [nvcc] + ARCH + FLAGS + extra + (["-Xptxas", "-v"] if verbose else []) + ["-c", s, "-o", o]
             jobs.append(cmd)
+    lib_jobs = bool(jobs)
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "ringattn.h")]):
+        jobs.append(_binding_cmd())
     if jobs:
         with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             for out in ex.map(_run, jobs):
                 if verbose and out:
                     sys.stdout.write(out)
-    if force or jobs or _stale(lib, objs):
+    if force or lib_jobs or _stale(lib, objs):
         _run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", lib] + objs)
     return lib
 

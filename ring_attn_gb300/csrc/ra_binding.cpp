@@ -1,0 +1,231 @@
+// Marshals torch tensors into the C ABI's cache calls.  They serve single tokens,
+// whose kernels take a few microseconds; describing a call's tensors through
+// Python and ctypes takes 15 to 27 us on the host, here 5 to 9.
+//
+// Each function checks devices, types and dimensions (ValueError, as the rest of
+// the binding), makes the cache's device current, allocates outputs that were not
+// given, calls the library on the device's current stream and returns
+// (status, outputs).  Everything else is checked by the library.
+#include <Python.h>
+
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/ringattn.h"
+
+namespace {
+
+decltype(&ring_attn_cache_append) g_append;
+decltype(&ring_attn_cache_read) g_read;
+decltype(&ring_attn_cache_fwd) g_fwd;
+decltype(&ring_attn_cache_workspace_size) g_ws_size;
+
+#define RA_REFUSE(cond, ...) TORCH_CHECK_VALUE(!(cond), __VA_ARGS__)
+
+// KVCache._call and CuSeqlens._call.
+struct CacheArg {
+  const ra_kv_cache* cache;
+  int index;
+  int64_t hk, d;
+};
+struct CuArg {
+  const int32_t *dev, *host;
+  int index, n;
+  int64_t total, max_new;
+};
+int64_t item(PyObject* t, Py_ssize_t i) {
+  const long long v = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+CacheArg cache_arg(PyObject* t) {
+  return {reinterpret_cast<const ra_kv_cache*>(item(t, 0)), (int)item(t, 1), item(t, 2), item(t, 3)};
+}
+CuArg cu_arg(PyObject* t, const CacheArg& c) {
+  CuArg u{reinterpret_cast<const int32_t*>(item(t, 0)), reinterpret_cast<const int32_t*>(item(t, 1)), (int)item(t, 2),
+          (int)item(t, 3), item(t, 4), item(t, 5)};
+  RA_REFUSE(u.index != c.index, "CuSeqlens was prepared for cuda:", u.index, ", not cuda:", c.index);
+  return u;
+}
+
+const at::Tensor& tensor(PyObject* o, int index) {
+  RA_REFUSE(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
+  const at::Tensor& t = THPVariable_Unpack(o);
+  RA_REFUSE(t.get_device() != index, "tensor on ", t.device(), ", cache on cuda:", index);
+  return t;
+}
+
+ra_tensor describe(const at::Tensor& t, int64_t dims) {
+  ra_tensor r{};
+  r.data = t.data_ptr();
+  RA_REFUSE(t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat, "unsupported dtype ", t.scalar_type());
+  r.dtype = t.scalar_type() == at::kFloat ? RA_FP32 : RA_BF16;
+  RA_REFUSE(t.dim() != dims, "expected a ", dims, "-D tensor, got ", t.sizes());
+  r.ndim = (int32_t)dims;
+  for (int64_t i = 0; i < dims; ++i) {
+    r.shape[i] = t.size(i);
+    r.stride[i] = t.stride(i);
+  }
+  return r;
+}
+
+const int32_t* ints(PyObject* o, int64_t dims, int index, const char* what) {
+  RA_REFUSE(!THPVariable_Check(o), what, " must be a ", dims, "-D int32 tensor on cuda:", index);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  RA_REFUSE(t.scalar_type() != at::kInt || t.dim() != dims || !t.is_cuda() || t.get_device() != index, what,
+            " must be a ", dims, "-D int32 tensor on cuda:", index);
+  RA_REFUSE(t.size(-1) > 1 && t.stride(-1) != 1, what, " must be contiguous along its last dimension");
+  return t.data_ptr<int32_t>();
+}
+
+ra_kv_seqs sequences(PyObject* page_table, PyObject* kv_lens, const CuArg& cu) {
+  ra_kv_seqs s{};
+  s.page_table = ints(page_table, 2, cu.index, "page_table");
+  s.kv_lens = ints(kv_lens, 1, cu.index, "kv_lens");
+  const at::Tensor& table = THPVariable_Unpack(page_table);
+  RA_REFUSE(table.size(0) != cu.n || THPVariable_Unpack(kv_lens).size(0) != cu.n,
+            "page_table and kv_lens must have one row for each of the ", cu.n, " sequences");
+  RA_REFUSE(table.size(1) > INT32_MAX, "page_table is too wide");
+  s.page_table_stride = cu.n > 1 ? table.stride(0) : table.size(1);
+  s.cu_seqlens_dev = cu.dev;
+  s.cu_seqlens_host = cu.host;
+  s.max_pages = (int32_t)table.size(1);
+  s.n_seqs = cu.n;
+  return s;
+}
+
+void* current_stream(int index) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream(); }
+at::TensorOptions on(int index, at::ScalarType type) {
+  return at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)index));
+}
+bool given(PyObject* o) { return o != Py_None; }
+
+// (cache, cu, k, v, page_table, kv_lens, q, cos, sin, positions, interleaved, q_out) -> (status, q_out)
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 12, "12 arguments");
+  const CacheArg c = cache_arg(a[0]);
+  const CuArg cu = cu_arg(a[1], c);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)c.index));
+  const ra_kv_seqs seqs = sequences(a[4], a[5], cu);
+  const ra_tensor k = describe(tensor(a[2], c.index), 3), v = describe(tensor(a[3], c.index), 3);
+  RA_REFUSE(given(a[11]) && !given(a[6]), "q_out without q");
+  ra_tensor q{}, out{}, cos{}, sin{};
+  at::Tensor q_out;
+  if (given(a[6])) {
+    const at::Tensor& tq = tensor(a[6], c.index);
+    q = describe(tq, 3);
+    q_out = given(a[11]) ? tensor(a[11], c.index) : at::empty(tq.sizes(), tq.options());
+    out = describe(q_out, 3);
+  }
+  if (given(a[7])) {
+    cos = describe(tensor(a[7], c.index), 2);
+    sin = describe(tensor(a[8], c.index), 2);
+  }
+  const int32_t* pos = nullptr;
+  if (given(a[9])) {
+    pos = ints(a[9], 1, c.index, "positions");
+    RA_REFUSE(THPVariable_Unpack(a[9]).size(0) < cu.total, "positions must have an entry for every new token");
+  }
+  const int inter = PyObject_IsTrue(a[10]);
+  int status = RA_OK;
+  if (cu.total > 0)
+    status = g_append(given(a[6]) ? &q : nullptr, &k, &v, given(a[7]) ? &cos : nullptr, given(a[7]) ? &sin : nullptr,
+                      inter, pos, c.cache, &seqs, given(a[6]) ? &out : nullptr, current_stream(c.index));
+  PyObject* r = given(a[11]) ? Py_NewRef(a[11]) : q_out.defined() ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None);
+  return Py_BuildValue("(iN)", status, r);
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, cu, page_table, kv_lens, k_out, v_out) -> (status, k_out, v_out)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 6, "6 arguments");
+  const CacheArg c = cache_arg(a[0]);
+  const CuArg cu = cu_arg(a[1], c);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)c.index));
+  const ra_kv_seqs seqs = sequences(a[2], a[3], cu);
+  at::Tensor t[2];
+  ra_tensor r[2];
+  for (int i = 0; i < 2; ++i) {
+    t[i] = given(a[4 + i]) ? tensor(a[4 + i], c.index) : at::empty({cu.total, c.hk, c.d}, on(c.index, at::kBFloat16));
+    r[i] = describe(t[i], 3);
+  }
+  int status = RA_OK;
+  if (cu.total > 0) status = g_read(c.cache, &seqs, &r[0], &r[1], current_stream(c.index));
+  return Py_BuildValue("(iNN)", status, given(a[4]) ? Py_NewRef(a[4]) : THPVariable_Wrap(t[0]),
+                       given(a[5]) ? Py_NewRef(a[5]) : THPVariable_Wrap(t[1]));
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, cu, q, page_table, kv_lens, causal, scale, max_kv_len, out, lse, out_fp32, workspace) -> (status, out, lse)
+PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 12, "12 arguments");
+  const CacheArg c = cache_arg(a[0]);
+  const CuArg cu = cu_arg(a[1], c);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)c.index));
+  const ra_kv_seqs seqs = sequences(a[3], a[4], cu);
+  const at::Tensor& tq = tensor(a[2], c.index);
+  const ra_tensor q = describe(tq, 3);
+  const int causal = PyObject_IsTrue(a[5]), fp32 = PyObject_IsTrue(a[10]);
+  const double scale = PyFloat_AsDouble(a[6]);
+  const long max_kv = PyLong_AsLong(a[7]);
+  if (PyErr_Occurred()) throw python_error();
+  RA_REFUSE(max_kv < 0 || max_kv > INT32_MAX, "max_kv_len must be 0 or a length");
+  const at::Tensor out = given(a[8]) ? tensor(a[8], c.index)
+                                     : at::empty(tq.sizes(), on(c.index, fp32 ? at::kFloat : at::kBFloat16));
+  const at::Tensor lse = given(a[9]) ? tensor(a[9], c.index) : at::empty({tq.size(1), tq.size(0)}, on(c.index, at::kFloat));
+  ra_tensor o = describe(out, 3), l = describe(lse, 2);
+  int status = RA_OK;
+  if (cu.total > 0) {
+    at::Tensor ws;
+    if (given(a[11])) {
+      ws = tensor(a[11], c.index);
+    } else {
+      ws = at::empty({(int64_t)g_ws_size(cu.total, cu.max_new, tq.size(1), c.hk, c.d, cu.n)}, on(c.index, at::kByte));
+    }
+    status = g_fwd(&q, c.cache, &seqs, causal, (float)scale, (int32_t)max_kv, &o, &l, ws.data_ptr(), ws.nbytes(),
+                   current_stream(c.index));
+  }
+  return Py_BuildValue("(iNN)", status, given(a[8]) ? Py_NewRef(a[8]) : THPVariable_Wrap(out),
+                       given(a[9]) ? Py_NewRef(a[9]) : THPVariable_Wrap(lse));
+  END_HANDLE_TH_ERRORS
+}
+
+// The library's functions, by address.
+PyObject* use(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 4, "4 arguments");
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (!p[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null function");
+      throw python_error();
+    }
+  }
+  g_append = reinterpret_cast<decltype(g_append)>(p[0]);
+  g_read = reinterpret_cast<decltype(g_read)>(p[1]);
+  g_fwd = reinterpret_cast<decltype(g_fwd)>(p[2]);
+  g_ws_size = reinterpret_cast<decltype(g_ws_size)>(p[3]);
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
+}
+PyMethodDef g_methods[] = {{"use", fast(use), METH_FASTCALL, nullptr},
+                           {"cache_append", fast(cache_append), METH_FASTCALL, nullptr},
+                           {"cache_read", fast(cache_read), METH_FASTCALL, nullptr},
+                           {"cache_fwd", fast(cache_fwd), METH_FASTCALL, nullptr},
+                           {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ra_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__ra_binding(void) { return PyModule_Create(&g_module); }
