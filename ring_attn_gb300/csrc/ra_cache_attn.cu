@@ -63,6 +63,10 @@ struct FewRows {
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.a = g.whole ? 1 : max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
   }
+  // a turn of all warps
+  static __device__ __forceinline__ int min_places(const CacheAttnArgs& g, int warps) {
+    return g.whole ? 1 : warps / kTilesPerUnit;
+  }
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {

@@ -49,6 +49,7 @@ struct ManyRows {
     s.a = s.per * ((seen + kUnit - 1) / kUnit + kItemCost) + 2;
     s.b = g.causal ? 2 : 0;
   }
+  static __device__ __forceinline__ int min_places(const CacheAttnArgs& g, int) { return 2 * (g.causal ? g.G : 1); }
 };
 
 // A piece as the roles need it; n = 0: the run's end.
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
 // an item has here.  (A slot holds four head dims of all rows together.)
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const CacheAttnArgs g) {
-  constexpr int V = D / 8;
+  constexpr int V = D / 8, kAtOnce = 4;
   after_previous_kernel();
   const JoinNote* notes = notes_of(g);
   const JoinNote n = notes[blockIdx.x];
@@ -597,23 +598,35 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const CacheAttnArgs g) 
   for (int base = blockIdx.x; base <= n.last; base += 32) {
     const int c = base + lane;
     unsigned there = __ballot_sync(0xffffffffu, c == (int)blockIdx.x || (c <= n.last && notes[c].slot0));
-    while (there) {
-      const int b = base + __ffs(there) - 1;
-      there &= there - 1;
-      const float* slot = slot_of<256, D>(g, grid, b, b == (int)blockIdx.x);
-      const float2 ml = *reinterpret_cast<const float2*>(slot + 256 * D + 2 * r);  // (rows behind the sequence's: unused)
-      float4 x[V / 4];
+    while (there) {  // kAtOnce pieces' loads in flight
+      float2 ml[kAtOnce];
+      float4 x[kAtOnce][V / 4];
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) x[i] = reinterpret_cast<const float4*>(slot)[(warp * (V / 4) + i) * 256 + r];
-      const float to = fmaxf(M, ml.x), f0 = fast_exp2(M - to), f1 = fast_exp2(ml.x - to);
-      M = to;
-      sum = sum * f0 + ml.y * f1;
+      for (int k = 0; k < kAtOnce; ++k) {
+        ml[k] = make_float2(kNone, 0.f);
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        o[4 * i] = o[4 * i] * f0 + x[i].x * f1;
-        o[4 * i + 1] = o[4 * i + 1] * f0 + x[i].y * f1;
-        o[4 * i + 2] = o[4 * i + 2] * f0 + x[i].z * f1;
-        o[4 * i + 3] = o[4 * i + 3] * f0 + x[i].w * f1;
+        for (int i = 0; i < V / 4; ++i) x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there) {
+          const int b = base + __ffs(there) - 1;
+          there &= there - 1;
+          const float* slot = slot_of<256, D>(g, grid, b, b == (int)blockIdx.x);
+          ml[k] = *reinterpret_cast<const float2*>(slot + 256 * D + 2 * r);  // (rows behind the sequence's: unused)
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i) x[k][i] = reinterpret_cast<const float4*>(slot)[(warp * (V / 4) + i) * 256 + r];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float to = fmaxf(M, ml[k].x), f0 = fast_exp2(M - to), f1 = fast_exp2(ml[k].x - to);
+        M = to;
+        sum = sum * f0 + ml[k].y * f1;
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          o[4 * i] = o[4 * i] * f0 + x[k][i].x * f1;
+          o[4 * i + 1] = o[4 * i + 1] * f0 + x[k][i].y * f1;
+          o[4 * i + 2] = o[4 * i + 2] * f0 + x[k][i].z * f1;
+          o[4 * i + 3] = o[4 * i + 3] * f0 + x[k][i].w * f1;
+        }
       }
     }
   }

@@ -36,8 +36,9 @@ struct LineSeq {
   __device__ __forceinline__ int before(int tile) const { return a * tile + b * (tile * (tile - 1) / 2); }
 };
 
-// Kind: R, kItemCost, kOneTile (R holds all of a sequence's rows) and the cost
-// rule `static void cost(args, LineSeq&)` for line_shift 0.
+// Kind: R, kItemCost, kOneTile (R holds all of a sequence's rows), and for line_shift 0
+// the cost rule `static void cost(args, LineSeq&)` and the least places that a block of a
+// number of warps takes, `static int min_places(args, warps)`.
 template <class Kind>
 __device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int len, int n_new) {
   LineSeq s;
@@ -173,6 +174,7 @@ __device__ __forceinline__ bool find_run(const CacheAttnArgs& g, LinePos& at, in
     all = block_scan<WARPS>(v, below, sh.sums);
   }
   quota = (int)(((unsigned)all + gridDim.x - 1) / gridDim.x);
+  if (g.line_shift == 0) quota = max(quota, Kind::min_places(g, WARPS));
   at.u = (int)min((long long)all, (long long)blockIdx.x * quota);
   end = (int)min((long long)all, (long long)at.u + quota);
   if (at.u >= end) return false;
