@@ -8,13 +8,15 @@
 //   warp 0       MMA issuer (one thread): PV0(j-1), S0(j), PV1(j-1), S1(j), so one
 //                tile's products run while the other's softmax does.  S_t in
 //                tensor-memory columns [128 t, 128 t + 128), O_t from 256 + 128 t.
+//                An item with one tile is worked on as two twins instead, which take
+//                its units in turn and are added up at the end.
 //   warp 1       allocates / frees tensor memory.
 //   warp 2       one thread walks the block's pieces of the line and hands them to the
 //                others in shared memory, a few ahead (so that no other role holds a
 //                place on the line in registers).  Warp 3 is idle.
 //   warps 4-7    one key row per thread: its 4-bit codes and scales go from global
 //                memory through registers to fp16 rows in the 128-byte swizzle that
-//                the MMA reads, K and V two stages each.  About 340 instructions a
+//                the MMA reads, K two stages, V three.  About 340 instructions a
 //                thread and unit, a tenth of the unit's issue slots.
 //   warps 8-15   a query row per thread: queries scaled per row by a power of two into
 //                fp16's normal range and stored for the MMA; scores from tensor
@@ -31,12 +33,12 @@ namespace {
 constexpr int kBox = 128 * 128;  // 128 rows x 64 fp16
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 2;       // of K and of V (the issuer steps them by xor)
+constexpr int kKStages = 2, kVStages = 3;  // V is needed up to two units longer (twin tiles)
 constexpr uint32_t kWaitHint = 2000;
 constexpr float kLift = 8.f, kSlack = 4.f;  // largest p between 2^8 and 2^12
 constexpr float kNone = -3.0e38f;           // M of a row that has seen no key
 // Registers per thread of the control, conversion and softmax warpgroups.
-constexpr int kLaunchRegs = 128, kRegsCtl = 64, kRegsConv = 80, kRegsSoft = 184;
+constexpr int kLaunchRegs = 128, kRegsCtl = 72, kRegsConv = 88, kRegsSoft = 176;
 static_assert(128 * (kRegsCtl + kRegsConv + 2 * kRegsSoft) <= kThreads * kLaunchRegs, "register split exceeds the launch");
 
 // G places per unit, so that the causal growth of 256 / G keys per tile is whole.
@@ -61,25 +63,29 @@ struct Item {
 };
 constexpr int kItems = 4;
 
+enum Bar {
+  B_Q_FULL = 0,    // per query tile
+  B_KV_FULL = 2,   // kKStages; K and V of a unit complete on one barrier, so the issuer waits once
+  B_K_EMPTY = 4,   // kKStages
+  B_V_EMPTY = 6,   // kVStages
+  B_S_FULL = 9,    // per query tile
+  B_P_FULL = 11,
+  B_O_DONE = 13,
+  B_TEARDOWN = 14,
+  B_ITEM_FULL = 15,   // kItems
+  B_ITEM_EMPTY = 19,
+  B_TWIN_STATE = 23,  // the second twin's M and sums are in shared memory
+  B_TWIN_DONE = 24,   // the first has read the second's O
+  kNumBars = 25
+};
 template <int D>
 struct Lay {
   static constexpr int kTile = D / 64 * kBox;
-  static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
-  static constexpr int kMisc = kBar + 24 * 8;
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kKStages * kTile, kBar = kV + kVStages * kTile;
+  static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kItem = kMisc + 16;
-  static constexpr int kAlloc = kItem + kItems * (int)sizeof(Item) + 1024;  // slack to align the base to 1024 bytes
-};
-enum Bar {
-  B_Q_FULL = 0,    // per query tile
-  B_KV_FULL = 2,   // kStages; K and V of a unit complete on one barrier, so the issuer waits once
-  B_K_EMPTY = 4,
-  B_V_EMPTY = 8,
-  B_S_FULL = 10,   // per query tile
-  B_P_FULL = 12,
-  B_O_DONE = 14,
-  B_TEARDOWN = 15,
-  B_ITEM_FULL = 16,   // kItems
-  B_ITEM_EMPTY = 20
+  static constexpr int kTwin = kItem + kItems * (int)sizeof(Item);  // 128 rows' M and sums
+  static constexpr int kAlloc = kTwin + 128 * 8 + 1024;  // slack to align the base to 1024 bytes
 };
 constexpr int kReaders = 13;  // of an item: the issuer, 4 conversion and 8 softmax warps
 
@@ -132,7 +138,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAttnArgs a) {
   using L = Lay<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ LineShared<kWarps> sh;
   const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
   uint8_t* sp = smem_raw + (sb - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,11 +147,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + L::kMisc);
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kVStages; ++i) mbar_init(BAR(B_V_EMPTY + i), 1);
+    mbar_init(BAR(B_TWIN_STATE), 4);
+    mbar_init(BAR(B_TWIN_DONE), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(B_Q_FULL + i), 4);
       mbar_init(BAR(B_KV_FULL + i), 4);
       mbar_init(BAR(B_K_EMPTY + i), 1);
-      mbar_init(BAR(B_V_EMPTY + i), 1);
       mbar_init(BAR(B_S_FULL + i), 1);
       mbar_init(BAR(B_P_FULL + i), 4);
     }
@@ -160,6 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     fence_mbar_init();
   }
   after_previous_kernel();
+  // (in the twins' place: an SM's shared memory is all taken)
+  LineShared<kWarps>& sh = *reinterpret_cast<LineShared<kWarps>*>(sp + L::kTwin);
+  static_assert(sizeof(LineShared<kWarps>) <= 128 * 8, "the plan's shared memory");
   LinePos at;
   int end_u, quota;
   JoinNote note = empty_note();
@@ -176,8 +186,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   volatile Item* items = reinterpret_cast<volatile Item*>(sp + L::kItem);
-  // query tiles of an item
+  // query tiles of an item; a single one over several units is worked on by both
+  // softmax warpgroups, which take its units in turn (twins), each with its own O
   auto tiles_of = [](const volatile Item& x) { return x.rows - x.row0 > 128 ? 2 : 1; };
+  auto is_twin = [tiles_of](const volatile Item& x) { return x.n > 1 && tiles_of(x) == 1; };
+  volatile float2* twin_state = reinterpret_cast<volatile float2*>(sp + L::kTwin);
 
   if (warp < 4) {
     regs_dec<kRegsCtl>();
@@ -187,13 +200,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         constexpr uint32_t kIdS = idesc_f16_f32(128, kUnit, 0), kIdPV = idesc_f16_f32(128, D, 1);
         constexpr uint32_t kHi = sdesc_sw128_hi(1024);
         bool ok = true;
-        uint32_t k_at = 0, v_at = 0;    // stages of the next unit's S and PV, 0 or kTile
+        uint32_t k_at = 0, v_at = 0;    // stages of the next unit's S and PV, times kTile
         uint32_t par_kv = 0, n_all = 0;
         uint32_t par_q = 0, par_p = 0;  // phases of the query tiles' barriers, bit t (t is known at compile time)
-        auto issue_s = [&](auto tile) {
-          constexpr int t = decltype(tile)::value;
+        // S_t of the next unit, from query tile `qt`
+        auto issue_s = [&](auto tile, auto qtile) {
+          constexpr int t = decltype(tile)::value, qt = decltype(qtile)::value;
           const uint32_t lk = sdesc_sw128_lo(sb + L::kK + k_at, 16);
-          const uint32_t lq = sdesc_sw128_lo(sb + L::kQ + t * L::kTile, 16);
+          const uint32_t lq = sdesc_sw128_lo(sb + L::kQ + qt * L::kTile, 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
@@ -213,18 +227,47 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                         kk > 0 ? 1u : first ^ 1u);
           return true;
         };
+        auto wait_kv = [&]() -> bool {
+          return wait_one<kWaitHint>(BAR(B_KV_FULL) + (k_at ? 8u : 0u), par_kv, abort_flag, a.ctl, 35);
+        };
+        auto wait_q = [&](auto tile) -> bool {
+          constexpr int t = decltype(tile)::value;
+          if (!wait_one<kWaitHint>(BAR(B_Q_FULL + t), (par_q >> t) & 1, abort_flag, a.ctl, 36)) return false;
+          par_q ^= 1u << t;
+          return true;
+        };
+        auto v_done = [&]() {
+          mma_commit(BAR(B_V_EMPTY) + 8u * (v_at / L::kTile));
+          v_at = v_at == (kVStages - 1) * L::kTile ? 0u : v_at + L::kTile;
+        };
+        auto k_done = [&]() {
+          mma_commit(BAR(B_K_EMPTY) + (k_at ? 8u : 0u));
+          if (k_at) par_kv ^= 1u;
+          k_at ^= L::kTile;
+          ++n_all;
+        };
         // PV_t(j-1) reads P_t from the S_t columns, so it goes before S_t(j)
         auto turn = [&](auto tile, int j, int n) -> bool {
           constexpr int t = decltype(tile)::value;
           if (j >= 1 && !issue_pv(tile, j == 1)) return false;
           if (j == n) return true;
-          if (t == 0 && !wait_one<kWaitHint>(BAR(B_KV_FULL) + (k_at ? 8u : 0u), par_kv, abort_flag, a.ctl, 35)) return false;
-          if (j == 0) {
-            if (!wait_one<kWaitHint>(BAR(B_Q_FULL + t), (par_q >> t) & 1, abort_flag, a.ctl, 36)) return false;
-            par_q ^= 1u << t;
-          }
+          if (t == 0 && !wait_kv()) return false;
+          if (j == 0 && !wait_q(tile)) return false;
           tc_fence_after();
-          issue_s(tile);
+          issue_s(tile, tile);
+          return true;
+        };
+        // one query tile, two S and O: unit j is tile j % 2's
+        auto twin_turn = [&](auto tile, int j, int n) -> bool {
+          if (j >= 2) {
+            if (!issue_pv(tile, j < 4)) return false;
+            v_done();
+          }
+          if (j >= n) return true;
+          if (!wait_kv() || (j == 0 && !wait_q(Int<0>{}))) return false;
+          tc_fence_after();
+          issue_s(tile, Int<0>{});
+          k_done();
           return true;
         };
         for (int i = 0; ok; ++i) {
@@ -235,20 +278,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           const int nt = tiles_of(items[i % kItems]), n = items[i % kItems].n;
           mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
           if (n == 0) break;
-          for (int j = 0; j <= n; ++j) {
-            if (!turn(Int<0>{}, j, n) || (nt == 2 && !turn(Int<1>{}, j, n))) {
-              ok = false;
-              break;
-            }
-            if (j >= 1) {
-              mma_commit(BAR(B_V_EMPTY) + (v_at ? 8u : 0u));
-              v_at ^= L::kTile;
-            }
-            if (j < n) {
-              mma_commit(BAR(B_K_EMPTY) + (k_at ? 8u : 0u));
-              if (k_at) par_kv ^= 1u;
-              k_at ^= L::kTile;
-              ++n_all;
+          if (nt == 1 && n > 1) {
+            for (int j = 0; ok && j < n + 2; j += 2)
+              ok = twin_turn(Int<0>{}, j, n) && (j + 1 >= n + 2 || twin_turn(Int<1>{}, j + 1, n));
+          } else {
+            for (int j = 0; ok && j <= n; ++j) {
+              ok = turn(Int<0>{}, j, n) && (nt == 1 || turn(Int<1>{}, j, n));
+              if (ok && j >= 1) v_done();
+              if (ok && j < n) k_done();
             }
           }
           if (ok) mma_commit(BAR(B_O_DONE));
@@ -256,12 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         // every issued MMA, and every arrival it makes, completes before the block ends
         mma_commit(BAR(B_TEARDOWN));
         drain_one(BAR(B_TEARDOWN), 0, a.ctl, 37);
-        for (uint32_t s = 0; s < kStages; ++s) {
-          const uint32_t c = (n_all + kStages - 1 - s) / kStages;
-          if (c && ok) {
-            drain_one(BAR(B_K_EMPTY + s), (c - 1) & 1, a.ctl, 38);
-            drain_one(BAR(B_V_EMPTY + s), (c - 1) & 1, a.ctl, 39);
-          }
+        for (uint32_t s = 0; ok && s < kVStages; ++s) {
+          const uint32_t ck = (n_all + kKStages - 1 - s) / kKStages, cv = (n_all + kVStages - 1 - s) / kVStages;
+          if (s < kKStages && ck) drain_one(BAR(B_K_EMPTY + s), (ck - 1) & 1, a.ctl, 38);
+          if (cv) drain_one(BAR(B_V_EMPTY + s), (cv - 1) & 1, a.ctl, 39);
         }
       }
       __syncwarp();
@@ -297,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     // ---------------------------------------------------------------- keys and values to fp16
     regs_dec<kRegsConv>();
     const int r = threadIdx.x - 128;
-    uint32_t n = 0;  // units converted
+    uint32_t n = 0, sv = 0, pv = 1;  // units converted; V's stage and the parity of its last release
     bool ok = true;
     const int mask = (1 << a.c.page_shift) - 1;
     for (int i = 0; ok; ++i) {
@@ -334,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       v.load(a.c.v.data + oc, a.c.vs.data + os, ok_row);
       if (u0 + 1 < u1) page_of(u0 + 1);
       for (int u = u0; u < u1; ++u, ++n) {
-        const uint32_t s = n % kStages;
+        const uint32_t s = n % kKStages;
         const bool more = u + 1 < u1;
-        if (n >= kStages &&
-            !wait_warp<kWaitHint>(BAR(B_K_EMPTY + s), (n / kStages - 1) & 1, abort_flag, a.ctl, 40)) {
+        if (n >= kKStages &&
+            !wait_warp<kWaitHint>(BAR(B_K_EMPTY + s), (n / kKStages - 1) & 1, abort_flag, a.ctl, 40)) {
           ok = false;
           break;
         }
@@ -347,12 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           ok_row = live;
           k.load(a.c.k.data + oc, a.c.ks.data + os, ok_row);
         }
-        if (n >= kStages &&
-            !wait_warp<kWaitHint>(BAR(B_V_EMPTY + s), (n / kStages - 1) & 1, abort_flag, a.ctl, 41)) {
+        if (n >= kVStages && !wait_warp<kWaitHint>(BAR(B_V_EMPTY + sv), pv, abort_flag, a.ctl, 41)) {
           ok = false;
           break;
         }
-        v.store(sb + L::kV + s * L::kTile, r);
+        v.store(sb + L::kV + sv * L::kTile, r);
+        if (++sv == kVStages) sv = 0, pv ^= 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_KV_FULL + s));
@@ -368,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     const int t = (warp - 8) >> 2, r = (threadIdx.x - 256) & 127;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tl + t * 128, tO = tl + 256 + t * 128;
-    uint32_t n_s = 0, n_o = 0;  // score tiles and results seen
+    uint32_t n_s = 0, n_o = 0, n_twin = 0;  // score tiles, results and twin items seen
     bool ok = true;
     float sc = 0.f;             // of this thread's row of the item at hand
     int end_row = 0;
@@ -377,8 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     auto take_item = [&](int i) -> bool {
       if (!wait_warp<kWaitHint>(BAR(B_ITEM_FULL + i % kItems), (i / kItems) & 1, abort_flag, a.ctl, 48)) return false;
       const volatile Item& x = items[i % kItems];
-      if (x.n == 0 || t >= tiles_of(x)) return true;
-      const int row = x.row0 + t * 128 + r, tok = row / a.G;
+      const bool twin = is_twin(x);
+      if (x.n == 0 || (t >= tiles_of(x) && !twin)) return true;
+      const int row = x.row0 + (twin ? r : t * 128 + r), tok = row / a.G;
       uint32_t q[D / 2];
       end_row = 0;
       if (row < x.rows) {
@@ -403,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
       const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
       sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e - 12) << 23);
+      if (twin && t == 1) return true;  // the first twin stores the row
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         uint32_t h[4];
@@ -419,9 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     ok = take_item(0);
     for (int i = 0; ok; ++i) {
       const volatile Item& x = items[i % kItems];
-      const int row = x.row0 + t * 128 + r, u0 = x.ua, u1 = u0 + x.n;
+      const bool twin = is_twin(x);
+      const int row = x.row0 + (twin ? r : t * 128 + r), u0 = x.ua, u1 = u0 + x.n;
       if (u0 == u1) break;
-      if (t >= tiles_of(x)) {  // not this warpgroup's, but its phase passes
+      if (t >= tiles_of(x) && !twin) {  // not this warpgroup's, but its phase passes
         ok = take_item(i + 1) && wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 44);
         ++n_o;
         __syncwarp();
@@ -430,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       }
       const bool valid = row < x.rows;
       float M = kNone, l_run = 0.f;
-      for (int u = u0; u < u1; ++u, ++n_s) {
+      const int step = twin ? 2 : 1;
+      for (int u = twin ? u0 + t : u0; u < u1; u += step, ++n_s) {
         const int c_hi = end_row - u * kUnit;
         if (!wait_warp<kWaitHint>(BAR(B_S_FULL + t), n_s & 1, abort_flag, a.ctl, 42)) {
           ok = false;
@@ -504,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);
         l_run = l_run * alpha + (s0 + s1);
         // O_t is stable here: the commit behind S_FULL covers PV_t of the unit before
-        if (u > u0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (u >= u0 + step && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -520,16 +559,42 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_P_FULL + t));
       }
-      // the next item's queries first, so that its products start behind this one's
-      if (!ok || !take_item(i + 1) || !wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 43)) {
+      // The next item's queries first, so that its products start behind this one's
+      // (behind a twin item's only when they have ended: both tiles read its queries).
+      if (!ok || !(twin || take_item(i + 1)) ||
+          !wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 43)) {
         ok = false;
         break;
       }
       ++n_o;
       tc_fence_after();
+      float f_own = 1.f, f_other = 0.f;
+      if (twin) {
+        if (t == 1) {  // hands its state over and waits until its O has been read
+          twin_state[r].x = M;
+          twin_state[r].y = l_run;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_TWIN_STATE));
+          ok = take_item(i + 1) && wait_warp<kWaitHint>(BAR(B_TWIN_DONE), n_twin & 1, abort_flag, a.ctl, 49);
+          ++n_twin;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
+          continue;
+        }
+        if (!take_item(i + 1) || !wait_warp<kWaitHint>(BAR(B_TWIN_STATE), n_twin & 1, abort_flag, a.ctl, 50)) {
+          ok = false;
+          break;
+        }
+        ++n_twin;
+        const float m1 = twin_state[r].x, l1 = twin_state[r].y, m = fmaxf(M, m1);
+        f_own = fast_exp2(M - m), f_other = fast_exp2(m1 - m);
+        l_run = l_run * f_own + l1 * f_other;
+        M = m;
+      }
       const bool whole = x.whole;
       const int cu0 = x.cu0, head = x.head;
       const float inv = whole ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f;
+      f_own *= inv, f_other *= inv;
       float* part = slot_of<256, D>(a, gridDim.x, blockIdx.x, u0 == 0);
       const int pr = t * 128 + r;
       const int tok = cu0 + row / a.G, hd = head * a.G + row % a.G;
@@ -540,7 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         tmem_ld32(tO + c * 32, o);
         tmem_ld_wait(o);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f_own);
+        if (twin) {
+          uint32_t y[32];
+          tmem_ld32(tO + 128 + c * 32, y);
+          tmem_ld_wait(y);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), f_other, __uint_as_float(o[k])));
+        }
         if (!valid) {
         } else if (!whole) {
           // four head dims of all rows together, so that a warp stores 512 bytes at once
@@ -563,6 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         __syncwarp();
       }
       tc_fence_before();
+      if (twin) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_TWIN_DONE));
+      }
       if (valid) {
         if (whole)
           store_lse(a, tok, hd, M, l_run);
