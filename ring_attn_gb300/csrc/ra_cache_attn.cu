@@ -58,7 +58,7 @@ struct Lay {
 // `whole`: every item is one place on the line, so none is shared.
 template <int NT>
 struct FewRows {
-  static constexpr int R = 8 * NT, kItemCost = 4;
+  static constexpr int R = 8 * NT, kItemCost = 3;
   static constexpr bool kOneTile = true;
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.a = g.whole ? 1 : max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
@@ -139,12 +139,17 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&v)[N]) {
 }
 
 // Where V's key row r (0..31) lies in a stage: the first keys 2t of a lane's pairs
-// side by side, then the second ones, and for 64-byte rows chunks swapped in
-// pairs, so that the 16 lanes of a load phase meet all banks once.
+// side by side, then the second ones (slot 4 (r & 1) + r / 2 of every 8 rows), and for
+// 64-byte rows chunks swapped in pairs, so that the 16 lanes of a load phase meet all
+// banks once.  The swap depends on r mod 8 only, so a lane's rows 8 apart lie 8 rows apart.
+template <int D>
+__device__ __forceinline__ uint32_t v_place(int r, int chunk) {  // r < 8
+  const int slot = ((r & 1) << 2) | (r >> 1);
+  return slot * (D / 2) + ((D == 128 ? chunk ^ (slot & 2) : chunk) << 4);
+}
 template <int D>
 __device__ __forceinline__ uint32_t v_offset(int r, int chunk) {
-  const int slot = (r & ~7) | ((r & 1) << 2) | ((r >> 1) & 3);
-  return slot * (D / 2) + ((D == 128 ? chunk ^ (slot & 2) : chunk) << 4);
+  return v_place<D>(r & 7, chunk) + (r & ~7) * (D / 2);
 }
 
 // Turns of a block's warps over the tiles of `units` units.
@@ -202,7 +207,8 @@ struct Stream {
   int pa, pb, k0;                     // pages of the warp's keys [k0, k0 + 16) and the 16 after them
   int na, nb;                         // the same a turn ahead
   const uint8_t *kc, *vc, *ks, *vs;   // the head's rows, this lane's part of the offset included
-  int step_c;                         // bytes between this lane's code chunks
+  int step_c;                         // bytes between this lane's code chunks in the cache (512 in a stage)
+  uint32_t v_at;                      // this lane's first V chunk in a stage
   uint32_t to, end, slot0;            // ring slot, the ring's end and start
 
   __device__ __forceinline__ Stream(const CacheAttnArgs& args, const Pieces& pieces, uint32_t ring)
@@ -210,6 +216,8 @@ struct Stream {
         end(ring + L::kStages * L::kStage), slot0(ring) {
     constexpr int CPR = D / 32;
     step_c = (int)a.c.k.s_row * (32 / CPR);
+    const int lane = threadIdx.x & 31;
+    v_at = v_offset<D>(lane / CPR, lane % CPR);
   }
   __device__ __forceinline__ void piece(int i) {
     index = i;
@@ -256,14 +264,22 @@ struct Stream {
   // 32 keys of one page
   __device__ __forceinline__ void copy_full() {
     const int lane = threadIdx.x & 31, row = k0 & ((1 << a.c.page_shift) - 1);
-    constexpr int CPR = D / 32, RPJ = 32 / CPR;  // rows per step
+    constexpr int CPR = D / 32;
     const long long o = (long long)pa * a.c.k.s_page + row * (int)a.c.k.s_row;
     const uint8_t *k = kc + o, *v = vc + o;
+    const uint32_t tk = to + L::kK + lane * 16, tv = to + L::kV + v_at;
+    if (step_c == 512) {  // packed rows: every offset is a constant
 #pragma unroll
-    for (int j = 0; j < CPR; ++j) {
-      const int r = j * RPJ + lane / CPR, ch = lane % CPR;
-      cp16(to + L::kK + r * (D / 2) + ch * 16, k + j * step_c);
-      cp16(to + L::kV + v_offset<D>(r, ch), v + j * step_c);
+      for (int j = 0; j < CPR; ++j) {
+        cp16(tk + j * 512, k + j * 512);
+        cp16(tv + j * 512, v + j * 512);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < CPR; ++j) {
+        cp16(tk + j * 512, k + (long long)j * step_c);
+        cp16(tv + j * 512, v + (long long)j * step_c);
+      }
     }
     const long long os = (long long)pa * a.c.ks.s_page + row * (int)a.c.ks.s_row;
     cp_small<D / 16>(to + L::kKs + lane * (D / 16), ks + os);
@@ -334,6 +350,8 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
   }
   __syncthreads();
   Stream<D, NT, W> st(a, sp, ring);
+  // this lane's V numbers of key 2t (key 2t + 1 lies 4 rows on)
+  const uint32_t lane_v = L::kV + v_place<D>(2 * t, g * (D / 64) / 4) + (g * (D / 64) % 4) * 4;
   // a row's token: r / G for r < 32 (a product instead of a division)
   const uint32_t inv_g = (65536u + a.G - 1) / a.G;
   auto token_of_row = [inv_g](int r) { return (int)((r * inv_g) >> 16); };
@@ -440,6 +458,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       stg = ring + slot * L::kStage;
       if (++slot == L::kStages) slot = 0;
       if (k0 >= end_key) continue;
+      const uint32_t stv = stg + lane_v;
       // scores of 32 keys: rows g, g + 8 of two tiles
       float s[2][NT][4];
 #pragma unroll
@@ -551,8 +570,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
         uint32_t v[4][W], s2[2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-          const int r = 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1);
-          lds_words(stg + L::kV + v_offset<D>(r, g * W / 4) + (g * W % 4) * 4, v[k]);
+          lds_words(stv + (16 * mt + 8 * (k >> 1) + 4 * (k & 1)) * (D / 2), v[k]);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
