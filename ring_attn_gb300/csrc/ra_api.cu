@@ -1101,6 +1101,7 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (q->shape[1] > 65535 || q->shape[1] % a.hk != 0) return RA_ERR_INVALID_ARG;
   a.h = (int)q->shape[1];
   a.G = a.h / a.hk;
+  if ((long long)a.max_new * a.G > (1LL << 30)) return RA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
   if (!out || (out->dtype != RA_BF16 && out->dtype != RA_FP32)) return RA_ERR_INVALID_ARG;
   a.out_f32 = out->dtype == RA_FP32;
   RA_TRY(check_rows3(out, out->dtype, a.s.total, a.h, d, &a.out));

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendA
         group_max<STYLE>(u, v, own, ma, mb);
         sa = sure_scale(ma, off, !turn, unsure), sbb = STYLE == 1 ? sure_scale(mb, off, !turn, unsure) : sa;
         xa = sure_codes(u, sa, off, !turn, unsure), xb = sure_codes(v, sbb, off, !turn, unsure);
-        if (__any_sync(0xffffffffu, unsure)) {
+        if (__any_sync(0xffffffffu, unsure && live)) {
           rotate16<STYLE>(x, y, cs, sn, turn, u, v, dot2_odd);
           group_max<STYLE>(u, v, own, ma, mb);
           sa = scale_of(ma), sbb = STYLE == 1 ? scale_of(mb) : sa;
