@@ -8,7 +8,7 @@
 //   warp 0       MMA issuer (one thread): PV0(j-1), S0(j), PV1(j-1), S1(j), so one
 //                tile's products run while the other's softmax does.  S_t in
 //                tensor-memory columns [128 t, 128 t + 128), O_t from 256 + 128 t.
-//                An item with one tile is worked on as two twins instead, which take
+//                A sequence's only tile is worked on as two twins instead, which take
 //                its units in turn and are added up at the end.
 //   warp 1       allocates / frees tensor memory.
 //   warp 2       one thread walks the block's pieces of the line and hands them to the
@@ -186,10 +186,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   volatile Item* items = reinterpret_cast<volatile Item*>(sp + L::kItem);
-  // query tiles of an item; a single one over several units is worked on by both
-  // softmax warpgroups, which take its units in turn (twins), each with its own O
+  // Query tiles of an item.  A sequence's only one, over several units, is worked on by
+  // both softmax warpgroups, which take its units in turn (twins), each with its own O:
+  // 64 rows of 16 sequences of 8000 keys and 8 key / value heads take 99 us, 123 without.
+  // Not the last one of many rows: changing between the two ways costs more than it gives
+  // (320 rows of 8 sequences of 8000 keys: 129 us, 155 with).
   auto tiles_of = [](const volatile Item& x) { return x.rows - x.row0 > 128 ? 2 : 1; };
-  auto is_twin = [tiles_of](const volatile Item& x) { return x.n > 1 && tiles_of(x) == 1; };
+  auto is_twin = [](const volatile Item& x) { return x.n > 1 && x.rows <= 128; };
   volatile float2* twin_state = reinterpret_cast<volatile float2*>(sp + L::kTwin);
 
   if (warp < 4) {
@@ -276,9 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             break;
           }
           const int nt = tiles_of(items[i % kItems]), n = items[i % kItems].n;
+          const bool twin = is_twin(items[i % kItems]);
           mbar_arrive(BAR(B_ITEM_EMPTY + i % kItems));
           if (n == 0) break;
-          if (nt == 1 && n > 1) {
+          if (twin) {
             for (int j = 0; ok && j < n + 2; j += 2)
               ok = twin_turn(Int<0>{}, j, n) && (j + 1 >= n + 2 || twin_turn(Int<1>{}, j + 1, n));
           } else {
