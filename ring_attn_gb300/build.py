@@ -25,7 +25,7 @@ LIB_DBG = os.path.join(PKG, "libringattn_dbg.so")
 SOURCES = ["ra_api.cu", "ra_fwd.cu", "ra_bwd.cu", "ra_dkdv_pair.cu", "ra_simple.cu", "ra_cache.cu", "ra_cache_attn.cu",
            "ra_cache_chunk.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("ra_device.cuh", "ra_internal.h", "ra_tiles.cuh", "ra_bwd_common.cuh",
-                                               "ra_cache.cuh", "ra_cache_line.cuh")] + [
+                                               "ra_cache_args.h", "ra_cache.cuh", "ra_cache_line.cuh")] + [
     os.path.join(ROOT, "include", "ringattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/ringattn.h"
+#include "ra_cache_args.h"
 #include "ra_internal.h"
 
 namespace {

@@ -4,7 +4,7 @@
 
 #include <cuda_fp16.h>
 
-#include "ra_internal.h"
+#include "ra_cache_args.h"
 
 namespace ra {
 
