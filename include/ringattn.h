@@ -315,7 +315,7 @@ size_t ring_attn_workspace_size(int32_t op, int64_t b, int64_t h, int64_t s, int
  *   apart: entry [i][j] is the page with tokens [j * page, (j + 1) * page) of
  *   sequence i.  Entries past a sequence's length are not read.
  *   kv_lens: (n_seqs) int32 device array: tokens of each sequence in the cache,
- *   AFTER the call's own tokens were appended.
+ *   AFTER the call's own tokens were appended; a negative one counts as 0.
  *   cu_seqlens_dev / cu_seqlens_host: as in the varlen calls, over the call's
  *   new tokens: rows [cu[i], cu[i+1]) of q, k, v belong to sequence i, and new
  *   token j of its n is the cache's token kv_lens[i] - n + j.  A sequence may

@@ -52,13 +52,14 @@ __device__ __forceinline__ int sequence_of(const CacheSeqs& s, int t) {
   return lo;
 }
 
+// Length of sequence i, a negative one as 0 (so that a token's index, len - n + j, is exact).
 __device__ __forceinline__ int cache_len(const CacheSeqs& s, int i, int bound, const DevCtl& ctl) {
   const int n = s.lens[i];
   if (n > bound) {
     record_error(ctl, DEV_BOUNDS, SITE_CACHE_LEN);
     return bound;
   }
-  return n;
+  return max(n, 0);
 }
 
 // A page number of the table, or -1 (recorded) when there is no such page.

@@ -108,6 +108,28 @@ def test_append_positions_in_place_and_padding(ra):
             assert np.array_equal(host[j][pg, :, row], codes) and np.array_equal(host[j + 1][pg, :, row], scales)
 
 
+def test_negative_lengths_are_empty_sequences(ra):
+    """Also one so low that a token's index would not fit 32 bits: nothing is written, read or seen."""
+    c = Case((3, 40, 2), (-2 ** 31, -2 ** 31 + 7, 2), 2, 1, 64, 16, seed=3, spare=4)
+    cache = c.cache(ra)
+    before = [b.clone() for b in c.bytes]
+    x = c.queries()
+    cu = ra.CuSeqlens(c.cu, "cuda")
+    qo = torch.full_like(x, 5.0)
+    ra.ring_attn_cache_append(x[:, :1], x[:, 1:], cache, c.page_table, c.kv_lens, cu, q=x, q_out=qo, rope=tables(64, 64))
+    ko, vo = (torch.full((c.rows, 1, 64), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ra.ring_attn_cache_read(cache, c.page_table, c.kv_lens, cu, k_out=ko, v_out=vo)
+    for seqs in (1, 2):  # few and many rows
+        out, lse = ra.ring_attn_cache_fwd(x[:c.cu[seqs]], cache, c.page_table[:seqs], c.kv_lens[:seqs], c.cu[:seqs + 1].tolist())
+        assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    check_no_device_error(ra)
+    assert bool((qo[:43] == 5.0).all()) and bool((ko[:43] == 5.0).all()) and bool((vo[:43] == 5.0).all())
+    pg, row = c.where(2, 0, 2)
+    for b, a in zip(before, c.bytes):
+        changed = (a != b).any(-1).nonzero().cpu().numpy()  # only the third sequence's two tokens
+        assert {(p, r) for p, _, r in changed.tolist()} <= set(zip(pg.tolist(), row.tolist()))
+
+
 def test_append_ties_and_extremes(ra):
     """Values on the format's borders go to the even number; infinities and NaN are stored as finite numbers."""
     d, hk = 64, 1
