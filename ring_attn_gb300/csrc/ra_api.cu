@@ -1103,6 +1103,8 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   a.h = (int)q->shape[1];
   a.G = a.h / a.hk;
   if ((long long)a.max_new * a.G > (1LL << 30)) return RA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+  a.items = cache_attn_items(seqs->cu_seqlens_host, a.s.n_seqs, a.max_new, a.G, a.hk);
+  if (a.items > kMaxCacheItems) return RA_ERR_UNSUPPORTED;
   if (!out || (out->dtype != RA_BF16 && out->dtype != RA_FP32)) return RA_ERR_INVALID_ARG;
   a.out_f32 = out->dtype == RA_FP32;
   RA_TRY(check_rows3(out, out->dtype, a.s.total, a.h, d, &a.out));
@@ -1124,7 +1126,7 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (a.s.total == 0) return RA_OK;
   RA_TRY(dev_ctl(&a.ctl));
   TimedLaunch tl(RA_KERNEL_CACHE_FWD, static_cast<cudaStream_t>(stream));
-  return cuda_status(launch_cache_attn(a, seqs->cu_seqlens_host, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_cache_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,

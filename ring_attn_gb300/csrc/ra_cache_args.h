@@ -65,14 +65,16 @@ struct CacheAttnArgs {
   float scale_log2;
   void* ws;                 // partial results, cache_attn_ws_bytes
   int whole;                // set by the launcher: items are not shared among blocks
-  long long items;          // set by the launcher: row tiles times key / value heads
+  long long items;          // row tiles times key / value heads, cache_attn_items
   int line_shift;           // set by the launcher, see LineSeq
   CacheView c;
   CacheSeqs s;
   DevCtl ctl;
 };
 size_t cache_attn_ws_bytes(long long total, int max_new, int h, int hk, int d, int n_seqs);
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, const int* cu_host, cudaStream_t st);
+long long cache_attn_items(const int* cu_host, int n_seqs, int max_new, int G, int hk);
+constexpr long long kMaxCacheItems = 1LL << 28;  // their line's length fits 32 bits
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st);
 // the variant for many query rows per key / value head
 size_t cache_chunk_ws_bytes(int d);
 cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t st);

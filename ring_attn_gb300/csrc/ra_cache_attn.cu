@@ -707,12 +707,16 @@ size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
   return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
 }
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& args, const int* cu_host, cudaStream_t st) {
-  CacheAttnArgs a = args;
-  const bool many = many_rows(a.max_new, a.G);
-  const int nt = row_tiles((long long)a.max_new * a.G), R = many ? 256 : 8 * nt;
-  for (int i = 0; i < a.s.n_seqs; ++i) a.items += ((long long)(cu_host[i + 1] - cu_host[i]) * a.G + R - 1) / R * a.hk;
-  if (many) return launch_cache_chunk(a, st);
+long long cache_attn_items(const int* cu_host, int n_seqs, int max_new, int G, int hk) {
+  const int R = many_rows(max_new, G) ? 256 : 8 * row_tiles((long long)max_new * G);
+  long long tiles = 0;
+  for (int i = 0; i < n_seqs; ++i) tiles += ((long long)(cu_host[i + 1] - cu_host[i]) * G + R - 1) / R;
+  return tiles * hk;
+}
+
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
+  if (many_rows(a.max_new, a.G)) return launch_cache_chunk(a, st);
+  const int nt = row_tiles((long long)a.max_new * a.G);
   if (a.d == 64) return nt == 1 ? launch<64, 1>(a, st) : nt == 2 ? launch<64, 2>(a, st) : launch<64, 4>(a, st);
   return nt == 1 ? launch<128, 1>(a, st) : nt == 2 ? launch<128, 2>(a, st) : launch<128, 4>(a, st);
 }

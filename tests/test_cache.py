@@ -148,6 +148,9 @@ def test_attention_refuses(lib):
     many = 1 << 26  # 2^26 tokens of 32 heads over one: more than 2^30 rows
     big = (many, 32, 64)
     assert attend(lib, c=cache(hk=1), s=seqs((0, many)), q=fake(big), out=fake(big), lse=fake((32, many), ra.RA_FP32)) == 2
+    n, hk = 65535, 10000  # more items than a line of 32 bits holds
+    big = (n, hk, 64)
+    assert attend(lib, c=cache(hk=hk), s=seqs(range(n + 1)), q=fake(big), out=fake(big), lse=fake((hk, n), ra.RA_FP32)) == 2
     need = lib.ring_attn_cache_workspace_size(10, 7, 4, 2, 64, 2)
     assert need > 0
     assert attend(lib, ws=None) == 4 and attend(lib, wb=need - 1) == 4 and attend(lib, ws=0x100010) == 4
