@@ -102,6 +102,11 @@ at::TensorOptions on(int index, at::ScalarType type) {
   return at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)index));
 }
 bool given(PyObject* o) { return o != Py_None; }
+int truth(PyObject* o) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) throw python_error();
+  return r;
+}
 
 // (cache, cu, k, v, page_table, kv_lens, q, cos, sin, positions, interleaved, q_out) -> (status, q_out)
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -130,7 +135,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     pos = ints(a[9], 1, c.index, "positions");
     RA_REFUSE(THPVariable_Unpack(a[9]).size(0) < cu.total, "positions must have an entry for every new token");
   }
-  const int inter = PyObject_IsTrue(a[10]);
+  const int inter = truth(a[10]);
   int status = RA_OK;
   if (cu.total > 0)
     status = g_append(given(a[6]) ? &q : nullptr, &k, &v, given(a[7]) ? &cos : nullptr, given(a[7]) ? &sin : nullptr,
@@ -171,7 +176,7 @@ PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ra_kv_seqs seqs = sequences(a[3], a[4], cu);
   const at::Tensor& tq = tensor(a[2], c.index);
   const ra_tensor q = describe(tq, 3);
-  const int causal = PyObject_IsTrue(a[5]), fp32 = PyObject_IsTrue(a[10]);
+  const int causal = truth(a[5]), fp32 = truth(a[10]);
   const double scale = PyFloat_AsDouble(a[6]);
   const long max_kv = PyLong_AsLong(a[7]);
   if (PyErr_Occurred()) throw python_error();
@@ -185,6 +190,7 @@ PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor ws;
     if (given(a[11])) {
       ws = tensor(a[11], c.index);
+      RA_REFUSE(!ws.is_contiguous(), "workspace must be contiguous");
     } else {
       ws = at::empty({(int64_t)g_ws_size(cu.total, cu.max_new, tq.size(1), c.hk, c.d, cu.n)}, on(c.index, at::kByte));
     }

@@ -410,3 +410,87 @@ def test_bad_pages_lengths_and_positions_are_reported(ra, new):
     ra.ring_attn_cache_read(cache, torch.full_like(c.page_table, -1), c.kv_lens, c.cu.tolist(), k_out=kk, v_out=kk.clone())
     assert ra.ring_attn_check_device_error()[0] == 7 and bool((kk == 9.0).all())
     check_no_device_error(ra)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_graphs_share_a_workspace(ra, new):
+    """Two calls captured with one workspace, replayed behind one another without a wait; and
+    two streams at once, each with a workspace of its own."""
+    calls = []
+    for seed, kv in ((31, (9000, 300)), (32, (77, 5001))):
+        c = Case((new, new), kv, 8, 2, 128, 32, seed=seed)
+        cache = c.fill(ra)
+        q = c.queries()
+        calls.append((c, cache, q, ra.CuSeqlens(c.cu, "cuda"), torch.empty_like(q), torch.empty(8, c.rows, device="cuda"),
+                      c.expect(q, True)))
+
+    def run(x, ws):
+        c, cache, q, cu, out, lse, _ = x
+        ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, cu, out=out, lse=lse, workspace=ws)
+
+    def check():
+        torch.cuda.synchronize()
+        for c, _, _, _, out, lse, (ref, ref_l, tol, tol_l) in calls:
+            assert_within("lse", lse, ref_l, tol_l)
+            assert_within("out", out, ref, tol)
+            out.fill_(9.0)
+            lse.fill_(9.0)
+        torch.cuda.synchronize()
+
+    one = ra.ring_attn_cache_workspace(calls[0][2], calls[0][1], calls[0][3])
+    two = torch.empty_like(one)
+    graphs = []
+    for x in calls:
+        run(x, one)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(x, one)
+        graphs.append(g)
+    check()
+    for _ in range(20):
+        for g in graphs:
+            g.replay()
+    check()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        for x, ws, st in zip(calls, (one, two), streams):
+            with torch.cuda.stream(st):
+                run(x, ws)
+    check()
+    check_no_device_error(ra)
+
+
+def test_binding_refusals(ra):
+    """What only the binding can see; the library's refusals come up as errors, too."""
+    c = Case((1, 2), (5, 9), 4, 2, 64, 16, seed=6)
+    cache, q, cu = c.fill(ra), c.queries(), ra.CuSeqlens(c.cu, "cuda")
+    n = ra.ring_attn_cache_workspace(q, cache, cu).numel()
+
+    def fwd(q=q, cache=cache, page_table=c.page_table, kv_lens=c.kv_lens, cu=cu, **k):
+        return ra.ring_attn_cache_fwd(q, cache, page_table, kv_lens, cu, **k)
+
+    for bad in (dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)),  # fewer bytes than it says
+                dict(q=q.half()), dict(q=q[0]), dict(q=q.cpu()), dict(kv_lens=c.kv_lens.long()), dict(kv_lens=c.kv_lens[:1]),
+                dict(page_table=c.page_table[:1]), dict(kv_lens=c.kv_lens.cpu()), dict(max_kv_len=-1), dict(out=q.cpu()), dict(out_dtype=torch.float16),
+                dict(cache=c.bytes)):
+        with pytest.raises(ValueError):
+            fwd(**bad)
+    for bad in (dict(workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda")), dict(q=q[:2]), dict(q=q[:, :3]),
+                dict(q=q.float()), dict(softmax_scale=-1.0), dict(out=torch.empty_like(q[:, :2]))):
+        with pytest.raises(RuntimeError):
+            fwd(**bad)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    app = lambda **k: ra.ring_attn_cache_append(x, x, cache, c.page_table, c.kv_lens, cu, **k)  # noqa: E731
+    cos, sin = tables(16, 64)
+    for bad in (dict(q_out=q), dict(positions=torch.zeros(2, dtype=torch.int32, device="cuda")), dict(q=q, rope=(cos, sin.cpu())),
+                dict(q=q, positions=c.kv_lens.float())):
+        with pytest.raises(ValueError):
+            app(**bad)
+    for bad in (dict(q=q, rope=(cos, sin[:, :16])), dict(q=q, rope=(cos[:, ::2], sin[:, ::2])), dict(q=q, q_out=q.flip(0)[:2])):
+        with pytest.raises(RuntimeError):
+            app(**bad)
+    out, _ = fwd()
+    ref, _, tol, _ = c.expect(q, True)
+    assert_within("out", out, ref, tol)
+    check_no_device_error(ra)
