@@ -18,8 +18,11 @@
 // exponent's offset M keeps the largest p between 2^8 and 2^12, so p down to
 // 2^-22 of it has all its fp16 bits; O is rescaled only when a score passes that.
 //
-// Bound: 0.5625 bytes per number from HBM; the conversions cost about 1.3 lane
-// instructions per number against the 3 that fit into its memory time.
+// Bound: 0.5625 bytes per number from HBM.  A tile of 32 keys and 8 query rows costs a
+// warp about 670 instructions (d = 128: 140 conversions, 128 products with scales, 32
+// matrix products), half of the issue slots while the cache streams at 82 % of the
+// measured copy rate.  One query of 32 heads over 128K keys of 8: 151 MB in 43 us; 64
+// sequences of 200 to 16384 keys of 4 heads: 39 us, of which about 6 are the joining kernel's.
 #include <algorithm>
 
 #include "ra_cache_line.cuh"
