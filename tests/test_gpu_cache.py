@@ -494,3 +494,29 @@ def test_binding_refusals(ra):
     ref, _, tol, _ = c.expect(q, True)
     assert_within("out", out, ref, tol)
     check_no_device_error(ra)
+
+
+def test_steps_from_an_empty_cache(ra):
+    """KVCache.empty, one page list shared by value and key, tokens one by one; q and rope left out."""
+    g = np.random.default_rng(12)
+    hk, d, n = 2, 64, 3
+    cache = ra.KVCache.empty(n * 3, 16, hk, d)
+    table = torch.arange(n * 3, dtype=torch.int32, device="cuda").flip(0).view(n, 3).contiguous()
+    cu = ra.CuSeqlens(range(n + 1), "cuda")
+    lens = torch.tensor([0, 5, 30], dtype=torch.int32, device="cuda")  # (zeros so far)
+    ks, vs = [np.zeros((m, hk, d)) for m in (0, 5, 30)], [np.zeros((m, hk, d)) for m in (0, 5, 30)]
+    for _ in range(4):
+        lens += 1
+        k, v = (torch.tensor(g.standard_normal((n, hk, d))).bfloat16().cuda() for _ in range(2))
+        assert ra.ring_attn_cache_append(k, v, cache, table, lens, cu) is None
+        q = torch.tensor(g.standard_normal((n, 4, d))).bfloat16().cuda()
+        out, lse = ra.ring_attn_cache_fwd(q, cache, table, lens, cu)
+        for i in range(n):
+            ks[i] = np.concatenate([ks[i], oc.dequantise(*oc.quantise(f64(k[i:i + 1])))])
+            vs[i] = np.concatenate([vs[i], oc.dequantise(*oc.quantise(f64(v[i:i + 1])))])
+    c = Case((1,) * n, lens.tolist(), 4, hk, d, 16)
+    c.k, c.v = ks, vs
+    ref, ref_l, tol, tol_l = c.expect(q, True)
+    assert_within("out", out, ref, tol)
+    assert_within("lse", lse, ref_l, tol_l)
+    check_no_device_error(ra)
