@@ -66,9 +66,9 @@ struct FewRows {
   static __device__ __forceinline__ void cost(const CacheAttnArgs& g, LineSeq& s) {
     s.a = g.whole ? 1 : max(1, (s.len + kUnit - 1) / kUnit) + kItemCost;
   }
-  // a turn of all warps
+  // a turn of all warps, and 2 units (one leaves more to join: 28 rows of 3000 keys 20.4 us, 18.5 with two)
   static __device__ __forceinline__ int min_places(const CacheAttnArgs& g, int warps) {
-    return g.whole ? 1 : warps / kTilesPerUnit;
+    return g.whole ? 1 : max(2, warps / kTilesPerUnit);
   }
 };
 
@@ -335,13 +335,13 @@ struct Stream {
   }
 };
 
-// Blocks per SM and warps per block: small blocks for many items, one block per SM for few.
-// (16 rows with two blocks instead of three, and so without spills: 40 sequences of 2000
-// keys 46 -> 43 us.)
-constexpr int small_blocks(int nt) { return nt == 1 ? 4 : 2; }
+// Small blocks (4 warps) per SM: as many as the registers of a row tile allow without spills.
+// (8 rows of d = 128 with three: 64 sequences of 4000 keys of 4 heads 41.5 us, with four 43.1;
+// 16 rows with two: 40 sequences of 2000 keys of 8 heads 43 us, with three 46.)
+constexpr int small_blocks(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : 2; }
 
 template <int D, int NT, int W>
-__global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_attn_kernel(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(D, NT) : 1) cache_attn_kernel(const CacheAttnArgs a) {
   using L = Lay<D, NT, W>;
   constexpr int kWarps = W, kThreads = 32 * W;
   constexpr int R = L::R, KS = D / 16;  // contraction steps of S, row tiles of O^T
@@ -483,10 +483,9 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(NT) : 1) cache_a
       M[n][0] = M[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
     }
-    // Tiles of 16 keys whose scores are computed side by side: two read a query fragment once
-    // and keep the matrix unit busier, where the registers hold them (one query of 128K
-    // keys 46.3 -> 45.4 us, 16 rows of 72,000 keys 47 -> 45; else they spill, 42 -> 48 us for the small blocks).
-    constexpr int AT = NT == 2 || (NT == 1 && W > 4) ? 2 : 1;
+    // Tiles of 16 keys whose scores are computed side by side: two read a query fragment
+    // once and keep the matrix unit busier, where the registers hold them.
+    constexpr int AT = NT <= 2 ? 2 : 1;
     uint32_t stg = 0;
     for (int it = 0; it < n_it; ++it) {
       cp_wait<L::kStages - 2>();
@@ -742,16 +741,18 @@ cudaError_t launch_w(const CacheAttnArgs& a, bool whole, int grid, cudaStream_t 
                       0, st, b);
 }
 
-// Few items (at most one per SM): big blocks, so that an item has few pieces to
-// join, and none when its units are few enough for one block (2048 keys: about
-// 7 us, as long as a second kernel takes).  Many items: small blocks, whose starts
-// and ends overlap.
+// Items short enough for one block (2048 keys: about 7 us, as long as a second kernel takes)
+// and no more than SMs: a big block for each, nothing to join.  Very few items of 8 rows:
+// big blocks too, so that an item has fewer pieces to join (8 items of 30,000 keys of d = 128:
+// 22.6 us, with small blocks 23.6; d = 64: 18.5 and 20.6; 16 items: 30.4 and 28.7).  Else small
+// blocks, whose starts and ends overlap (64 items of 10,000 keys: 31 us, with big blocks
+// 35; 12 rows: 38 and 44; 28 rows: 56 and 64).
 template <int D, int NT>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   const int units = (a.max_kv + kUnit - 1) / kUnit, sms = num_sms();
-  const bool big = a.items <= sms, whole = big && units <= 16;
+  const bool whole = a.items <= sms && units <= 16, big = whole || (NT == 1 && a.items * 10 <= sms);
   const long long line = a.items * (whole ? 1 : units + FewRows<NT>::kItemCost);  // at most
-  const int grid = (int)std::min(line, (long long)sms * (big ? 1 : small_blocks(NT)));
+  const int grid = (int)std::min(line, (long long)sms * (big ? 1 : small_blocks(D, NT)));
   return big ? launch_w<D, NT, big_warps(NT)>(a, whole, grid, st) : launch_w<D, NT, 4>(a, whole, grid, st);
 }
 
@@ -759,7 +760,7 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
 
 size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
   if (many_rows(max_new, h / hk)) return cache_chunk_ws_bytes(d);
-  const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * small_blocks(nt);
+  const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * small_blocks(d, nt);
   return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
 }
 
