@@ -19,10 +19,10 @@
 // 2^-22 of it has all its fp16 bits; O is rescaled only when a score passes that.
 //
 // Bound: 0.5625 bytes per number from HBM.  A tile of 32 keys and 8 query rows costs a
-// warp about 670 instructions (d = 128: 140 conversions, 128 products with scales, 32
+// warp about 630 instructions (d = 128: 140 conversions, 128 products with scales, 32
 // matrix products), half of the issue slots while the cache streams at 82 % of the
-// measured copy rate.  One query of 32 heads over 128K keys of 8: 151 MB in 43 us; 64
-// sequences of 200 to 16384 keys of 4 heads: 39 us, of which about 6 are the joining kernel's.
+// measured copy rate.  One query of 32 heads over 128K keys of 8: 151 MB in 42 us; 64
+// sequences of 200 to 16384 keys of 4 heads: 38 us, of which about 6 are the joining kernel's.
 #include <algorithm>
 
 #include "ra_cache_line.cuh"
@@ -459,8 +459,6 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(D, NT) : 1) cach
           const uint2 v = q_frag(n, s);
           qb[n][s][0] = v.x, qb[n][s][1] = v.y;
         }
-      }
-      if constexpr (kQReg) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) sc[n][x] = sscale[8 * n + 2 * t + x], end[n][x] = row_end(8 * n + 2 * t + x);
       }
@@ -724,7 +722,7 @@ bool many_rows(int max_new, int G) { return (long long)max_new * G > 32; }
 int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 // Warps of the block when there is one per SM.  With 8 rows, 12 warps with 4 stages each
-// take 43 us for one query over 128K keys, 16 with 3 stages 49 us.
+// take 42 us for one query over 128K keys, 16 with 3 stages 49 us.
 constexpr int big_warps(int nt) { return nt == 4 ? 8 : 12; }
 
 template <int D, int NT, int W>

@@ -24,7 +24,7 @@
 //                far), P as fp16 over the score columns; the epilogue.
 // Bound: tensor throughput, and with it shared memory: of a unit's 2048 tensor cycles
 // (256 rows, d = 128) operand reads take 1536 and the converted tiles' stores 512.
-// 2048 tokens of 32 heads at the end of 65,536 keys of 8 heads: 1.52 ms, 1422 TFLOP/s
+// 2048 tokens of 32 heads at the end of 65,536 keys of 8 heads: 1.53 ms, 1417 TFLOP/s
 // (73 % of the measured bf16 rate); 1.41 ms without the conversions, 1.19 without softmax.
 // fp16 operands hold number * scale exactly.
 #include <algorithm>
