@@ -520,3 +520,45 @@ def test_steps_from_an_empty_cache(ra):
     assert_within("out", out, ref, tol)
     assert_within("lse", lse, ref_l, tol_l)
     check_no_device_error(ra)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_attention_under_a_very_wide_page_table(ra, new):
+    """2^30 tokens could be there: the work line counts in coarser places (its length has to fit 32 bits)."""
+    c = Case((new,), (700,), 130, 130, 64, 256, seed=15)
+    cache = c.fill(ra)
+    wide = torch.full((1, 2 ** 22), -7, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.page_table
+    q = c.queries()
+    ref, ref_l, tol, tol_l = c.expect(q, True)
+    for bound in (0, 2 ** 30 - 1, 700):
+        out, lse = ra.ring_attn_cache_fwd(q, cache, wide, c.kv_lens, c.cu.tolist(), max_kv_len=bound)
+        assert_within("lse", lse, ref_l, tol_l)
+        assert_within("out", out, ref, tol)
+    check_no_device_error(ra)
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_offsets_beyond_32_bits(ra, new):
+    """The last pages of a cache of more than 2^32 bytes an array: the same bits as in a small cache."""
+    hk, d, page, far = 2, 128, 256, 135000
+    c = Case((new, new), (300, 777), 4, hk, d, page, seed=16)
+    small = c.fill(ra)
+    q, x = c.queries(), torch.tensor(c.rng.standard_normal((c.rows, 2, hk, d))).bfloat16().cuda()
+    code = lambda w: torch.empty((far + c.n_pages, hk, page, w), dtype=torch.uint8, device="cuda")  # noqa: E731
+    b = [code(w) for w in (d // 2, d // 16) * 2]
+    assert b[0].numel() > 2 ** 32
+    for y, z in zip(b, c.bytes):
+        y[far:] = z
+    big = ra.KVCache(b[0], b[1].view(torch.float8_e4m3fn), b[2], b[3].view(torch.float8_e4m3fn))
+    cu = ra.CuSeqlens(c.cu, "cuda")
+    got = []
+    for cache, table in ((small, c.page_table), (big, c.page_table + far)):
+        qr = ra.ring_attn_cache_append(x[:, 0], x[:, 1], cache, table, c.kv_lens, cu, q=q, rope=tables(800, d))
+        got.append((qr, *ra.ring_attn_cache_read(cache, table, c.kv_lens, cu),
+                    *ra.ring_attn_cache_fwd(qr, cache, table, c.kv_lens, cu)))
+    for y, z in zip(*got):
+        assert torch.equal(y, z)
+    for y, z in zip(b, c.bytes):
+        assert torch.equal(y[far:], z)
+    check_no_device_error(ra)
