@@ -323,12 +323,14 @@ size_t ring_attn_workspace_size(int32_t op, int64_t b, int64_t h, int64_t s, int
  *   were.  cu_seqlens_dev must hold what cu_seqlens_host holds.
  *   Only cu_seqlens is read on the host, so a captured call follows kv_lens,
  *   the page table and positions as they are when it is replayed.
- * Device data that the host cannot check is checked by the kernels: a page
+ * Device data that the host cannot check is checked by the kernels: for a page
  * outside [0, n_pages), a length above max_pages * page (or max_kv_len) and a
- * position outside the rotation table are never used (nothing out of range is
- * read or written): RA_ERR_DEVICE is recorded for ring_attn_check_device_error
- * (low byte of info: 0x61 length, 0x62 page, 0x63 position), a token that has
- * no place is not stored, and the attention of that sequence is unspecified. */
+ * position outside the rotation table nothing out of range is
+ * read or written, and RA_ERR_DEVICE is recorded for ring_attn_check_device_error
+ * (low byte of info: 0x61 length, 0x62 page, 0x63 position).  A token that has
+ * no place (index max_pages * page or beyond, or a bad page) is neither stored nor
+ * read; under a length that is too long the sequence's other tokens keep the places
+ * that it gives them.  The attention of such a sequence is unspecified. */
 typedef struct {
   ra_tensor k, k_scale, v, v_scale;
 } ra_kv_cache;
@@ -362,7 +364,7 @@ typedef enum { RA_ROPE_HALVES = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope;
  *   input by the fp32 table entries, carried to about 2^-47, so the stored bits do
  *   not depend on the order of the operations.
  *   A token whose cache index is negative (kv_lens[i] < n) is padding: nothing
- *   is written for it.  Two tokens of one call must not name the same place. */
+ *   is written for it, nor for one past the page table or with a bad position.  Two tokens of one call must not name the same place. */
 ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
                                  const ra_tensor* rope_cos, const ra_tensor* rope_sin, int32_t rope,
                                  const int32_t* positions, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
@@ -372,7 +374,7 @@ ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const r
  * bf16 (exact), the input of the attention calls above: k_out, v_out (rows, hk,
  * d) bf16, row cu[i] + j getting token kv_lens[i] - n + j of sequence i.  With
  * n = kv_lens[i] that is the whole sequence.  Rows of negative tokens, and of
- * tokens that a bad page table hides, are left as they were. */
+ * tokens past the page table or that a bad page hides, are left as they were. */
 ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs, ra_tensor* k_out, ra_tensor* v_out,
                                void* stream);
 

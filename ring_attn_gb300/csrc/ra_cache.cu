@@ -181,8 +181,7 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendA
   for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
     const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
     const int i = sequence_of(a.s, t);
-    const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
-    const int tok = len - a.s.cu[i + 1] + t;
+    const int tok = cache_index(a.s, i, t, a.ctl);
     if (tok < 0) continue;
     const int half = a.rot >> 4;  // chunks in half the rotated part
     const bool turn = STYLE == 1 ? l < half : STYLE == 2 ? 16 * l < a.rot : false;
@@ -320,8 +319,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a, 
   for (long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); gw < n_warps; gw += (long long)gridDim.x * kWarps) {
     const int t = (int)(gw / warps_per_token), part = (int)(gw % warps_per_token);
     const int i = sequence_of(a.s, t);
-    const int len = cache_len(a.s, i, a.s.max_tokens, a.ctl);
-    const int tok = len - a.s.cu[i + 1] + t;
+    const int tok = cache_index(a.s, i, t, a.ctl);
     if (tok < 0) continue;
     const int page = cache_page(a.s, a.c, i, tok, a.ctl);
     if (page < 0) continue;

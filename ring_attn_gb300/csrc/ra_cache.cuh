@@ -52,14 +52,17 @@ __device__ __forceinline__ int sequence_of(const CacheSeqs& s, int t) {
   return lo;
 }
 
-// Length of sequence i, a negative one as 0 (so that a token's index, len - n + j, is exact).
-__device__ __forceinline__ int cache_len(const CacheSeqs& s, int i, int bound, const DevCtl& ctl) {
-  const int n = s.lens[i];
-  if (n > bound) {
+// Cache index of row t, one of sequence i's new tokens, or -1 when it has no place: before the
+// cache's start (padding; a negative length counts as 0, so that the index is exact), or
+// past the page table (recorded).  It follows from the length as it is: one cut to the
+// table would move the tokens onto others' places.
+__device__ __forceinline__ int cache_index(const CacheSeqs& s, int i, int t, const DevCtl& ctl) {
+  const int tok = max(s.lens[i], 0) - s.cu[i + 1] + t;
+  if (tok >= s.max_tokens) {
     record_error(ctl, DEV_BOUNDS, SITE_CACHE_LEN);
-    return bound;
+    return -1;
   }
-  return max(n, 0);
+  return tok;
 }
 
 // A page number of the table, or -1 (recorded) when there is no such page.

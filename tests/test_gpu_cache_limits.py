@@ -1,0 +1,51 @@
+"""The paged 4-bit cache at the ends of its ranges: lengths beyond the page table."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from tests.cache_case import Case
+from tests.helpers import check_no_device_error
+from tests.test_gpu_cache import f64, ra, tables  # noqa: F401 (ra: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d,page,rot", [(64, 16, 0), (128, 32, 128)])
+@pytest.mark.parametrize("new,over", [(1, 1), (3, 1), (3, 3), (40, 7), (2, 1000000), (2, 2 ** 31 - 1 - 64)])
+def test_tokens_past_the_page_table_have_no_place(ra, d, page, rot, new, over):  # noqa: F811
+    """A length past the table: its tokens that lie in it are stored at their own places, the
+    others nowhere, and cached tokens and the call's other sequences are as they should be."""
+    c = Case((new, 2), (64, 40), 4, 2, d, page, seed=new + d)
+    cache = c.fill(ra)
+    lens = c.kv_lens.clone()
+    lens[0] = 64 + over
+    q, k, v = c.queries(), *(torch.tensor(c.rng.standard_normal((c.rows, 2, d))).bfloat16().cuda() for _ in range(2))
+    cos, sin = tables(64 + 7, d)
+    want = [b.cpu().numpy() for b in c.bytes]
+    tok = np.concatenate([64 + over - new + np.arange(new, dtype=np.int64), [38, 39]])
+    placed = tok < 64
+    for r in np.flatnonzero(placed):
+        pg, row = c.where(0 if r < new else 1, tok[r], tok[r] + 1)
+        at = slice(tok[r], tok[r] + 1)
+        x = oc.rotate(f64(k)[r:r + 1], cos.cpu().numpy()[at], sin.cpu().numpy()[at], False) if rot else f64(k)[r:r + 1]
+        for j, y in ((0, x), (2, f64(v)[r:r + 1])):
+            want[j][pg, :, row], want[j + 1][pg, :, row] = oc.quantise(y)
+    q_out = torch.full_like(q, 5.0)
+    ra.ring_attn_cache_append(k, v, cache, c.page_table, lens, c.cu.tolist(), q=q, rope=(cos, sin) if rot else None, q_out=q_out)
+    st, info = ra.ring_attn_check_device_error()
+    assert st == 7 and info & 0xff == 0x61
+    for b, w in zip(c.bytes, want):
+        assert np.array_equal(b.cpu().numpy(), w)
+    lost = torch.tensor(~placed)
+    assert bool((q_out[lost] == 5.0).all()) and not bool((q_out[~lost] == 5.0).any(-1).any())
+    ko, vo = (torch.full((c.rows, 2, d), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ra.ring_attn_cache_read(cache, c.page_table, lens, c.cu.tolist(), k_out=ko, v_out=vo)
+    st, info = ra.ring_attn_check_device_error()
+    assert st == 7 and info & 0xff == 0x61
+    assert bool((ko[lost] == 5.0).all()) and bool((vo[lost] == 5.0).all())
+    for r in np.flatnonzero(placed):
+        pg, row = c.where(0 if r < new else 1, tok[r], tok[r] + 1)
+        for got, j in ((ko, 0), (vo, 2)):
+            assert np.array_equal(f64(got)[r:r + 1], oc.dequantise(want[j][pg, :, row], want[j + 1][pg, :, row]))
+    check_no_device_error(ra)
