@@ -301,9 +301,6 @@ class CuSeqlens:
         self.n_seqs = host.numel() - 1
         self.total = int(host[-1])
         self.max_seqlen = int((host[1:] - host[:-1]).max())
-        # for the cache calls: arrays' addresses, device and sizes
-        self._call = (self.dev.data_ptr(), host.data_ptr(), self.dev.get_device() if self.dev.is_cuda else -1, self.n_seqs,
-                      self.total, self.max_seqlen)
 
 
 def _max_len(cu_seqlens, host):
@@ -655,14 +652,14 @@ def _cache_call(name, cache, cu_seqlens, stream, *args):
         if not isinstance(cu_seqlens, CuSeqlens):
             with torch.cuda.device(cache.device):
                 cu_seqlens = CuSeqlens(cu_seqlens, cache.device)
-        r = f(cache._call, cu_seqlens._call, *args)
+        r = f(cache._call, cu_seqlens.dev, cu_seqlens.host, *args)
     else:
         if stream.device != cache.device:
             raise ValueError(f"stream on {stream.device}, cache on {cache.device}")
         with torch.cuda.stream(stream):  # outputs, workspace and cu_seqlens belong to it, too
             if not isinstance(cu_seqlens, CuSeqlens):
                 cu_seqlens = CuSeqlens(cu_seqlens, cache.device)
-            r = f(cache._call, cu_seqlens._call, *args)
+            r = f(cache._call, cu_seqlens.dev, cu_seqlens.host, *args)
     if r[0] != 0:
         _check(r[0], "ring_attn_" + name)
     return r
