@@ -588,11 +588,14 @@ class KVCache:
     k, v: (n_pages, hk, page, d // 2) uint8, two e2m1 numbers per byte; k_scale, v_scale:
     (n_pages, hk, page, d // 16) float8_e4m3fn.  Any order of the first three dimensions in
     memory (pass a transposed view).  The handle keeps the tensors, which the caller
-    allocates, and their description, so that a call marshals nothing for them;
-    KVCache.empty allocates a cache of zeros."""
+    allocates, and their description, so that a call marshals nothing for them (so k, k_scale,
+    v and v_scale cannot be replaced: other tensors are another handle); copies describe their
+    own tensors.  KVCache.empty allocates a cache of zeros."""
+
+    k, k_scale, v, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
     def __init__(self, k, k_scale, v, v_scale):
-        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        self._tensors = (k, k_scale, v, v_scale)
         for name, x, dtype in (("k", k, torch.uint8), ("k_scale", k_scale, torch.float8_e4m3fn),
                                ("v", v, torch.uint8), ("v_scale", v_scale, torch.float8_e4m3fn)):
             if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -607,11 +610,18 @@ class KVCache:
         self.scale = 1.0 / math.sqrt(max(self.d, 1))  # the default softmax scale
         self._call = (ctypes.addressof(self._c), k.get_device(), self.hk, self.d)
 
+    def __reduce__(self):  # copies and pickles (which take no 8-bit floats: as bytes)
+        return _cache_of_bytes, (type(self), *(x.view(torch.uint8) for x in self._tensors))
+
     @classmethod
     def empty(cls, n_pages, page, hk, d, device="cuda"):
         code = lambda w: torch.zeros((n_pages, hk, page, w), dtype=torch.uint8, device=device)  # noqa: E731
         return cls(code(d // 2), code(d // 16).view(torch.float8_e4m3fn), code(d // 2),
                    code(d // 16).view(torch.float8_e4m3fn))
+
+
+def _cache_of_bytes(cls, k, k_scale, v, v_scale):
+    return cls(k, k_scale.view(torch.float8_e4m3fn), v, v_scale.view(torch.float8_e4m3fn))
 
 
 _I64x4 = ctypes.c_int64 * 4

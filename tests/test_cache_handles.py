@@ -66,3 +66,31 @@ def test_a_cu_seqlens_with_other_arrays(calls):
     cu.dev, cu.host = other.dev, other.host
     ra.ring_attn_cache_read(handle(), None, None, cu)
     assert {other.dev.data_ptr(), other.host.data_ptr()} <= set().union(*map(addresses, calls[-1][1]))
+
+
+def test_a_kv_cache_keeps_the_tensors_that_it_describes(monkeypatch):
+    """Replacing one would leave its description, addresses included, to memory that nobody holds."""
+    u8, f8 = torch.zeros(2, 1, 16, 32, dtype=torch.uint8), torch.zeros(2, 1, 16, 4, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: True))
+    cache = ra.KVCache(u8, f8, u8.clone(), f8.clone())
+    monkeypatch.undo()
+    for name in ("k", "k_scale", "v", "v_scale"):
+        x = getattr(cache, name)
+        with pytest.raises(AttributeError):
+            setattr(cache, name, x.clone())
+        assert getattr(cache, name) is x and getattr(cache._c, name).data == x.data_ptr()
+
+
+@pytest.mark.parametrize("duplicate", COPIES)
+def test_a_copied_kv_cache_describes_its_own_tensors(monkeypatch, duplicate):
+    monkeypatch.setattr(ra.torch.Tensor, "is_cuda", property(lambda self: True))
+    both = torch.arange(2 * 16 * 64, dtype=torch.int32).to(torch.uint8).view(2, 1, 16, 64)  # keys and values in one allocation
+    scales = [torch.full((2, 1, 16, 4), x, dtype=torch.uint8).view(torch.float8_e4m3fn) for x in (7, 8)]
+    first = ra.KVCache(both[..., :32], scales[0], both[..., 32:], scales[1])
+    made = duplicate(first)
+    assert made is not first and made._c is not first._c and made._call[1:] == first._call[1:]
+    for name in ("k", "k_scale", "v", "v_scale"):
+        x, y, t = getattr(first, name), getattr(made, name), getattr(made._c, name)
+        assert t.data == y.data_ptr() and list(t.stride) == list(y.stride()) == list(x.stride())
+        assert (x.data_ptr() == y.data_ptr()) == (duplicate is copy.copy)
+        assert x.dtype == y.dtype and torch.equal(x.view(torch.uint8), y.view(torch.uint8))
