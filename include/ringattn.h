@@ -351,7 +351,8 @@ typedef enum { RA_ROPE_HALVES = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope;
 /* ring_attn_cache_append: rotates q and k and puts k and v into the cache.
  *   q (optional), q_out: (rows, h, d) bf16; k, v: (rows, hk, d) bf16; rows >=
  *   cu_seqlens[n_seqs]; strides and pointers as for the attention calls.  q_out
- *   may be q itself; any other overlap with q, k or v is RA_ERR_INVALID_ARG.
+ *   may be q itself; elements shared with q, k or v otherwise are RA_ERR_INVALID_ARG
+ *   (slices of one packed tensor share none).
  *   rope_cos, rope_sin (both or neither): (positions, r / 2) fp32, r <= d, 16
  *   or a multiple of 32, rows 16-byte aligned.  A pair (a, b) at position p becomes
  *   (a cos - b sin, b cos + a sin); head dims from r on stay.  Position of a

@@ -2,6 +2,7 @@
 // and kernel launches.  Every argument error is returned before any launch.
 #include <math.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <mutex>
@@ -1018,6 +1019,33 @@ static ra_status check_rope_table(const ra_tensor* t, const ra_tensor* like, con
   return RA_OK;
 }
 
+// Whether two tensors may share a byte (es_a, es_b: element sizes).  Not when their spans lie
+// apart, nor when, modulo a stride P of either, both reach only runs of bytes that lie
+// apart: slices of one packed tensor, whose rows (P) or heads interleave.
+static bool may_share(const ra_tensor* a, int es_a, const ra_tensor* b, int es_b) {
+  uintptr_t alo, ahi, blo, bhi;
+  byte_span(a, es_a, &alo, &ahi);
+  byte_span(b, es_b, &blo, &bhi);
+  if (alo > bhi || blo > ahi) return false;
+  // bytes from the first that the tensor reaches modulo P, its dimensions of a multiple of P apart
+  auto run = [](const ra_tensor* t, long long es, long long P) {
+    long long n = es;
+    for (int i = 0; i < t->ndim; ++i)
+      if (t->shape[i] > 1 && t->stride[i] * es % P != 0) n += (t->shape[i] - 1) * llabs(t->stride[i]) * es;
+    return n;
+  };
+  for (int k = 0; k < a->ndim + b->ndim; ++k) {
+    const ra_tensor* t = k < a->ndim ? a : b;
+    const int i = k < a->ndim ? k : k - a->ndim;
+    const long long P = t->shape[i] > 1 ? llabs(t->stride[i]) * (k < a->ndim ? es_a : es_b) : 0;
+    if (P == 0) continue;
+    const long long na = run(a, es_a, P), nb = run(b, es_b, P);
+    const long long at = blo >= alo ? (long long)((blo - alo) % P) : (P - (long long)((alo - blo) % P)) % P;
+    if (at >= na && at + nb <= P) return false;
+  }
+  return true;
+}
+
 static bool same_view(const ra_tensor* a, const ra_tensor* b) {
   if (a->data != b->data || a->ndim != b->ndim) return false;
   for (int i = 0; i < a->ndim; ++i)
@@ -1045,9 +1073,8 @@ ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const r
     if (q->shape[1] > 65535 || q->shape[1] % a.hk != 0) return RA_ERR_INVALID_ARG;
     a.h = (int)q->shape[1];
     // each row is read and written by the same lanes, so in place is fine, but
-    // nothing else that other rows still have to read may be written
-    if (!same_view(q, q_out) &&
-        (ranges_overlap(q, q_out, 2) || ranges_overlap(k, q_out, 2) || ranges_overlap(v, q_out, 2)))
+    // nothing else that other warps still have to read may be written
+    if ((!same_view(q, q_out) && may_share(q, 2, q_out, 2)) || may_share(k, 2, q_out, 2) || may_share(v, 2, q_out, 2))
       return RA_ERR_INVALID_ARG;
   }
   if ((rope_cos != nullptr) != (rope_sin != nullptr)) return RA_ERR_INVALID_ARG;

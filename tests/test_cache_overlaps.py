@@ -1,0 +1,45 @@
+"""CPU checks: which overlaps of a cache call's tensors are refused, before any launch."""
+import numpy as np
+import pytest
+
+from tests.test_cache import FAR, append, fake, lib  # noqa: F401 (lib: the fixture)
+
+ODD = 0x1002  # positions there are refused (3) behind the overlaps (1)
+
+
+def part(heads, first, rows=10, d=64, packed=8, base=0x100000, row_of=None):
+    """Heads [first, first + heads) of a packed (rows, packed, d) tensor."""
+    return fake((rows, heads, d), data=base + 2 * d * first, stride=(packed * d, row_of or d, 1))
+
+
+@pytest.mark.parametrize("q,out,k,v,refused", [
+    # in place: keys or values that are some of the queries' own elements
+    (part(4, 0), part(4, 0), part(2, 0), part(2, 6), True),
+    (part(4, 0), part(4, 0), part(2, 2), part(2, 6), True),
+    (part(4, 0), part(4, 0), part(2, 4), part(2, 3), True),
+    (part(4, 4), part(4, 4), part(2, 0), part(2, 3), True),
+    (part(4, 0), part(4, 0), part(2, 4), part(2, 6), False),
+    # slices of one packed tensor that share no element, q elsewhere or another slice
+    (part(4, 0, base=FAR), part(4, 0), part(2, 4), part(2, 6), False),
+    (part(4, 0, base=FAR), part(4, 4), part(2, 0), part(2, 2), False),
+    (part(4, 0, packed=12), part(4, 8, packed=12), part(2, 4, packed=12), part(2, 6, packed=12), False),
+    (part(4, 0, packed=12), part(4, 7, packed=12), part(2, 4, packed=12), part(2, 6, packed=12), True),
+    (part(4, 0, packed=12), part(4, 3, packed=12), part(2, 8, packed=12), part(2, 10, packed=12), True),
+    # a row further on is the same slice again
+    (part(4, 0, base=FAR), part(4, 12), part(2, 4), part(2, 6), True),
+    (part(4, 0, base=FAR), part(4, 8), part(2, 4), part(2, 6), False),
+    # heads that lie apart, between another tensor's
+    (part(4, 0, base=FAR), part(4, 0, row_of=128), part(2, 1, row_of=128), part(2, 5, row_of=128), False),
+    (part(4, 0, base=FAR), part(4, 0, row_of=128), part(2, 1, row_of=128), part(2, 4, row_of=128), True),
+    # apart altogether
+    (part(4, 0), part(4, 0, base=FAR), part(2, 0), part(2, 0), False),
+])
+def test_append_overlaps(lib, q, out, k, v, refused):  # noqa: F811
+    def elements(t):
+        i = np.indices(tuple(t.shape)[:3]).reshape(3, -1)
+        return set((t.data // 2 + np.array(list(t.stride)[:3]) @ i).tolist())
+
+    shared = lambda a, b: bool(elements(a) & elements(b))  # noqa: E731
+    in_place = q.data == out.data and list(q.stride) == list(out.stride)
+    assert refused == (shared(k, out) or shared(v, out) or (not in_place and shared(q, out)))
+    assert append(lib, q=q, out=out, k=k, v=v, pos=ODD) == (1 if refused else 3)
