@@ -375,7 +375,8 @@ ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const r
  * bf16 (exact), the input of the attention calls above: k_out, v_out (rows, hk,
  * d) bf16, row cu[i] + j getting token kv_lens[i] - n + j of sequence i.  With
  * n = kv_lens[i] that is the whole sequence.  Rows of negative tokens, and of
- * tokens past the page table or that a bad page hides, are left as they were. */
+ * tokens past the page table or that a bad page hides, are left as they were.
+ * Elements that k_out and v_out share are RA_ERR_INVALID_ARG. */
 ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs, ra_tensor* k_out, ra_tensor* v_out,
                                void* stream);
 

@@ -1110,6 +1110,7 @@ ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs,
   RA_TRY(check_rows3(k_out, RA_BF16, a.s.total, a.hk, d, &a.k_out));
   RA_TRY(check_rows3(v_out, RA_BF16, a.s.total, a.hk, d, &a.v_out));
   if (a.s.total == 0) return RA_OK;
+  if (may_share(k_out, 2, v_out, 2)) return RA_ERR_INVALID_ARG;
   RA_TRY(dev_ctl(&a.ctl));
   TimedLaunch tl(RA_KERNEL_CACHE_READ, static_cast<cudaStream_t>(stream));
   return cuda_status(launch_cache_read(a, static_cast<cudaStream_t>(stream)));

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests.test_cache import FAR, append, fake, lib  # noqa: F401 (lib: the fixture)
+from tests.test_cache import FAR, append, fake, lib, read  # noqa: F401 (lib: the fixture)
 
 ODD = 0x1002  # positions there are refused (3) behind the overlaps (1)
 
@@ -43,3 +43,9 @@ def test_append_overlaps(lib, q, out, k, v, refused):  # noqa: F811
     in_place = q.data == out.data and list(q.stride) == list(out.stride)
     assert refused == (shared(k, out) or shared(v, out) or (not in_place and shared(q, out)))
     assert append(lib, q=q, out=out, k=k, v=v, pos=ODD) == (1 if refused else 3)
+
+
+def test_read_overlaps(lib):  # noqa: F811
+    assert read(lib, k=part(2, 0), v=part(2, 0)) == 1
+    assert read(lib, k=part(2, 0), v=part(2, 1)) == 1
+    assert read(lib, k=fake((10, 2, 64)), v=fake((10, 2, 64), data=0x100000 + 9 * 256)) == 1
