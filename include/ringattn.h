@@ -388,7 +388,8 @@ ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs,
  *   + j; else every token of the sequence (what cross attention to cached states
  *   needs).  A row that sees no token gets out = 0, lse = -inf, so shards of one
  *   sequence's cache, each with its own call, combine by lse_merge.
- *   out and lse must not overlap an input or each other.  More than 2^30 rows of a
+ *   out and lse must not overlap an input or each other (elements that they share
+ *   with q or each other are RA_ERR_INVALID_ARG, the rest is not checked).  More than 2^30 rows of a
  *   sequence (new tokens times h / hk), or more than 2^28 row tiles in all (8 to
  *   256 rows of a sequence each) times hk, are RA_ERR_UNSUPPORTED.
  *   max_kv_len: no kv_lens[i] is above it (0: max_pages * page); it sizes the

@@ -1152,6 +1152,9 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return RA_ERR_WORKSPACE;
   a.ws = workspace;
   if (a.s.total == 0) return RA_OK;
+  const int out_size = a.out_f32 ? 4 : 2;
+  if (may_share(q, 2, out, out_size) || may_share(q, 2, lse, 4) || may_share(out, out_size, lse, 4))
+    return RA_ERR_INVALID_ARG;
   RA_TRY(dev_ctl(&a.ctl));
   TimedLaunch tl(RA_KERNEL_CACHE_FWD, static_cast<cudaStream_t>(stream));
   return cuda_status(launch_cache_attn(a, static_cast<cudaStream_t>(stream)));

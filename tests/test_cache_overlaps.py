@@ -2,7 +2,8 @@
 import numpy as np
 import pytest
 
-from tests.test_cache import FAR, append, fake, lib, read  # noqa: F401 (lib: the fixture)
+import ring_attn_gb300 as ra
+from tests.test_cache import FAR, append, attend, fake, lib, read  # noqa: F401 (lib: the fixture)
 
 ODD = 0x1002  # positions there are refused (3) behind the overlaps (1)
 
@@ -49,3 +50,13 @@ def test_read_overlaps(lib):  # noqa: F811
     assert read(lib, k=part(2, 0), v=part(2, 0)) == 1
     assert read(lib, k=part(2, 0), v=part(2, 1)) == 1
     assert read(lib, k=fake((10, 2, 64)), v=fake((10, 2, 64), data=0x100000 + 9 * 256)) == 1
+
+
+def test_attention_overlaps(lib):  # noqa: F811
+    far = dict(q=fake((10, 4, 64)), out=fake((10, 4, 64), data=FAR), lse=fake((4, 10), ra.RA_FP32, data=2 * FAR))
+    f = lambda **k: attend(lib, **dict(far, **k))  # noqa: E731
+    assert f(out=far["q"]) == 1 and f(out=part(4, 1), q=part(4, 0)) == 1
+    assert f(out=fake((10, 4, 64), ra.RA_FP32, data=0x100000 + 5120 - 16)) == 1   # q's last bytes
+    assert f(lse=fake((4, 10), ra.RA_FP32, data=0x100000 + 512)) == 1             # in q
+    assert f(lse=fake((4, 10), ra.RA_FP32, data=FAR + 5120 - 4)) == 1             # in out
+    assert f(lse=fake((4, 10), ra.RA_FP32, data=FAR + 128, stride=(64, 128))) == 1

@@ -1,10 +1,10 @@
-"""The paged 4-bit cache at the ends of its ranges: lengths beyond the page table."""
+"""The paged 4-bit cache at the ends of its ranges: lengths beyond the page table, tensors between others."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import cache as oc
-from tests.cache_case import Case
+from tests.cache_case import Case, assert_within
 from tests.helpers import check_no_device_error
 from tests.test_gpu_cache import f64, ra, tables  # noqa: F401 (ra: the fixture)
 
@@ -49,3 +49,28 @@ def test_tokens_past_the_page_table_have_no_place(ra, d, page, rot, new, over): 
         for got, j in ((ko, 0), (vo, 2)):
             assert np.array_equal(f64(got)[r:r + 1], oc.dequantise(want[j][pg, :, row], want[j + 1][pg, :, row]))
     check_no_device_error(ra)
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_slices_of_one_tensor_are_no_overlap(ra, new):  # noqa: F811
+    """q, k, v, their outputs and the results as interleaved slices of one allocation."""
+    h, hk, d = 4, 2, 64
+    c = Case((new, 1), (200, 70), h, hk, d, 16, seed=17)
+    cache, rows = c.fill(ra), c.rows
+    x = torch.tensor(c.rng.standard_normal((rows, 32, d))).bfloat16().cuda()
+    q, k, v, qo, ko, vo, out = (x[:, a:b] for a, b in ((0, 4), (4, 6), (6, 8), (8, 12), (12, 14), (14, 16), (16, 20)))
+    lse = x.view(torch.float32)[:, 20:24, 0].t()  # (h, rows), fp32
+    kept = x[:, :8].clone()
+    cu = ra.CuSeqlens(c.cu, "cuda")
+    ra.ring_attn_cache_append(k, v, cache, c.page_table, c.kv_lens, cu, q=q, q_out=qo)
+    ra.ring_attn_cache_read(cache, c.page_table, c.kv_lens, cu, k_out=ko, v_out=vo)
+    ra.ring_attn_cache_fwd(qo, cache, c.page_table, c.kv_lens, cu, out=out, lse=lse)
+    check_no_device_error(ra)
+    assert torch.equal(x[:, :8], kept) and torch.equal(qo, q)
+    for i, m in enumerate(c.kv):
+        r = slice(c.cu[i], c.cu[i + 1])
+        c.k[i][m - c.n_new[i]:], c.v[i][m - c.n_new[i]:] = (oc.dequantise(*oc.quantise(f64(y)[r])) for y in (k, v))
+        assert np.array_equal(f64(ko)[r], c.k[i][m - c.n_new[i]:]) and np.array_equal(f64(vo)[r], c.v[i][m - c.n_new[i]:])
+    ref, ref_l, tol, tol_l = c.expect(q, True)
+    assert_within("out", out, ref, tol)
+    assert_within("lse", lse, ref_l, tol_l)
