@@ -758,10 +758,18 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// Bytes for calls of up to max_new tokens a sequence: a call of fewer may run as a kind that
+// has smaller slots but more blocks (d = 64: 8 rows in four blocks an SM, 16 in two).
 size_t cache_attn_ws_bytes(long long, int max_new, int h, int hk, int d, int) {
-  if (many_rows(max_new, h / hk)) return cache_chunk_ws_bytes(d);
-  const int nt = row_tiles((long long)max_new * (h / hk)), grid = num_sms() * small_blocks(d, nt);
-  return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
+  auto few = [d](int nt) {
+    const int grid = num_sms() * small_blocks(d, nt);
+    return nt == 1 ? line_ws_bytes<8>(grid, d) : nt == 2 ? line_ws_bytes<16>(grid, d) : line_ws_bytes<32>(grid, d);
+  };
+  const bool many = many_rows(max_new, h / hk);
+  const int up_to = many ? 4 : row_tiles((long long)max_new * (h / hk));
+  size_t n = many ? cache_chunk_ws_bytes(d) : 0;
+  for (int nt = 1; nt <= up_to; nt *= 2) n = std::max(n, few(nt));
+  return n;
 }
 
 long long cache_attn_items(const int* cu_host, int n_seqs, int max_new, int G, int hk) {
