@@ -76,7 +76,7 @@ enum Bar {
   B_V_EMPTY = 6,   // kVStages
   B_S_FULL = 9,    // per query tile
   B_P_FULL = 11,
-  B_O_DONE = 13,
+  B_O_DONE = 13,      // once an item: its products have ended, and the second warpgroup has come to it
   B_TEARDOWN = 14,
   B_ITEM_FULL = 15,   // kItems
   B_ITEM_EMPTY = 19,
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       mbar_init(BAR(B_ITEM_FULL + i), 1);
       mbar_init(BAR(B_ITEM_EMPTY + i), kReaders);
     }
-    mbar_init(BAR(B_O_DONE), 1);
+    mbar_init(BAR(B_O_DONE), 5);
     mbar_init(BAR(B_TEARDOWN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -469,6 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       const bool twin = is_twin(x);
       const int row = x.row0 + (twin ? r : t * 128 + r), u0 = x.ua, u1 = u0 + x.n;
       if (u0 == u1) break;
+      // Items of one tile go on without the second warpgroup.  Its arrival keeps the phase from
+      // ending twice before it has looked (the first one's products are in every item).
+      if (t == 1 && lane == 0) mbar_arrive(BAR(B_O_DONE));
       if (t >= tiles_of(x) && !twin) {  // not this warpgroup's, but its phase passes
         ok = take_item(i + 1) && wait_warp<kWaitHint>(BAR(B_O_DONE), n_o & 1, abort_flag, a.ctl, 44);
         ++n_o;

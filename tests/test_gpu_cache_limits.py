@@ -74,3 +74,25 @@ def test_slices_of_one_tensor_are_no_overlap(ra, new):  # noqa: F811
     ref, ref_l, tol, tol_l = c.expect(q, True)
     assert_within("out", out, ref, tol)
     assert_within("lse", lse, ref_l, tol_l)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_runs_of_items_of_one_and_two_query_tiles(ra, d):  # noqa: F811
+    """Blocks that work through many items of one tile and one unit (one of the softmax warpgroups has no
+    part in them), with items of two tiles and of one tile over several units between them."""
+    g = np.random.default_rng(d)
+    n_new = g.integers(1, 100, 600)
+    kv = np.minimum(n_new + g.integers(0, 30, 600), 128)
+    n_new[11::37], kv[11::37] = 150, 200   # two tiles
+    n_new[5::53], kv[5::53] = 60, 700      # one tile, several units
+    n_new[-1], kv[-1] = 200, 230
+    c = Case(n_new.tolist(), kv.tolist(), 2, 2, d, 32, seed=d)
+    cache, q, cu = c.fill(ra), c.queries(), ra.CuSeqlens(c.cu, "cuda")
+    a, la = ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, cu)
+    for _ in range(50):
+        b, lb = ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, cu)
+    check_no_device_error(ra)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    ref, ref_l, tol, tol_l = c.expect(q, True)
+    assert_within("out", a, ref, tol)
+    assert_within("lse", la, ref_l, tol_l)
