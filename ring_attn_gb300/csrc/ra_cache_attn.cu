@@ -50,6 +50,7 @@ struct Lay {
   static constexpr int kOPitch = D + 4;
   static constexpr int kResult = R * (kOPitch + 2) * 4;
   static constexpr bool kFlow = kResult <= kStage;
+  static constexpr int kAhead = kFlow ? kStages - 1 : 0;  // turns that the copies run ahead, into later pieces
   static constexpr int kResultPitch = kFlow ? kStages * kStage : kResult;  // from warp to warp
   // Queries at an item's start, R x D fp16, then R scales: with 8 rows in the
   // free stage of warp 0, else behind the ring.  So four blocks fit on an SM.
@@ -345,6 +346,8 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(D, NT) : 1) cach
   using L = Lay<D, NT, W>;
   constexpr int kWarps = W, kThreads = 32 * W;
   constexpr int R = L::R, KS = D / 16;  // contraction steps of S, row tiles of O^T
+  // the piece worked on and those planned ahead, of a turn at least each
+  static_assert(kPieces >= 1 + (L::kAhead > 1 ? L::kAhead : 1), "the planner would overwrite a piece in use");
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ LineShared<kWarps> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(D, NT) : 1) cach
       make_piece<Kind>(a, sp);
       // the first copies may go beyond a short first piece
       if (L::kFlow)
-        for (int ahead = turns_of<W>(sp.ring[0].ub - sp.ring[0].ua); ahead < L::kStages - 1 && !sp.over;) {
+        for (int ahead = turns_of<W>(sp.ring[0].ub - sp.ring[0].ua); ahead < L::kAhead && !sp.over;) {
           make_piece<Kind>(a, sp);
           ahead += turns_of<W>(sp.ring[sp.made - 1].ub - sp.ring[sp.made - 1].ua);
         }
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(D, NT) : 1) cach
       for (int s = 0; s < L::kStages - 1; ++s) st.load(L::kFlow);
     }
     if (planner) {  // the pieces that the copies may reach during this one, and the one after it
-      for (int k = i + 1, ahead = 0; k == i + 1 || ahead < L::kStages - 1; ++k) {
+      for (int k = i + 1, ahead = 0; k == i + 1 || ahead < L::kAhead; ++k) {
         if (k == sp.made && !sp.over) make_piece<Kind>(a, sp);
         const int n = sp.ring[k % kPieces].ub - sp.ring[k % kPieces].ua;
         if (n == 0) break;
