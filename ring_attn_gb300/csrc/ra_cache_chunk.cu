@@ -448,7 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       // the row's largest entry goes to [2^12, 2^13)
       const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
       const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
-      sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e - 12) << 23);
+      // not 0 (tiny scales, rows of zeros), so that a masked score, -infinity, stays one; scores
+      // are below 2^33 before it, so below 2^-90 under the least
+      sc = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 + e - 12) << 23), 0x1p-126f);
       if (twin && t == 1) return true;  // the first twin stores the row
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {

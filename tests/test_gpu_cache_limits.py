@@ -96,3 +96,19 @@ def test_runs_of_items_of_one_and_two_query_tiles(ra, d):  # noqa: F811
     ref, ref_l, tol, tol_l = c.expect(q, True)
     assert_within("out", a, ref, tol)
     assert_within("lse", la, ref_l, tol_l)
+
+
+@pytest.mark.parametrize("new", [2, 90])
+@pytest.mark.parametrize("scale", [1e-11, 1e-20, 1e-38])
+def test_tiny_scales_and_queries(ra, new, scale):  # noqa: F811
+    """Scores that vanish next to 1: the mean of what a row sees, the mask included."""
+    c = Case((new, new), (300, 200), 4, 2, 64, 64, seed=1)
+    cache, q = c.fill(ra), c.queries()
+    q[:, 1] = 0
+    q[0] *= 1e-30
+    for causal in (True, False):
+        out, lse = ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, c.cu.tolist(), causal=causal, softmax_scale=scale)
+        ref, ref_l, tol, tol_l = c.expect(q, causal, scale=scale)
+        assert_within("lse", lse, ref_l, tol_l)
+        assert_within("out", out, ref, tol)
+    check_no_device_error(ra)
