@@ -438,8 +438,8 @@ typedef enum {
   RA_KERNEL_LSE_MERGE = 5,
   RA_KERNEL_CACHE_APPEND = 6,
   RA_KERNEL_CACHE_READ = 7,
-  RA_KERNEL_CACHE_FWD = 8,   /* attention over the 4-bit cache */
-  RA_KERNEL_CACHE_JOIN = 9,  /* joins the partial results of ring_attn_cache_fwd */
+  RA_KERNEL_CACHE_FWD = 8,   /* attention over the 4-bit cache, without the next */
+  RA_KERNEL_CACHE_JOIN = 9,  /* joins the partial results of ring_attn_cache_fwd, where blocks share a sequence */
   RA_KERNEL_COUNT = 10
 } ra_kernel;
 ra_status ring_attn_timing_enable(int32_t on);

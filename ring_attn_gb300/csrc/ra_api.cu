@@ -1156,8 +1156,15 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (may_share(q, 2, out, out_size) || may_share(q, 2, lse, 4) || may_share(out, out_size, lse, 4))
     return RA_ERR_INVALID_ARG;
   RA_TRY(dev_ctl(&a.ctl));
-  TimedLaunch tl(RA_KERNEL_CACHE_FWD, static_cast<cudaStream_t>(stream));
-  return cuda_status(launch_cache_attn(a, static_cast<cudaStream_t>(stream)));
+  const CacheAttnPlan p = plan_cache_attn(a);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    TimedLaunch tl(RA_KERNEL_CACHE_FWD, st);
+    RA_TRY(cuda_status(launch_cache_attn(p, st)));
+  }
+  if (!p.joins) return RA_OK;
+  TimedLaunch tl(RA_KERNEL_CACHE_JOIN, st);
+  return cuda_status(launch_cache_join(p, st));
 }
 
 size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,

@@ -64,9 +64,9 @@ struct CacheAttnArgs {
   int causal, max_new, max_kv;
   float scale_log2;
   void* ws;                 // partial results, cache_attn_ws_bytes
-  int whole;                // set by the launcher: items are not shared among blocks
+  int whole;                // set by the plan: items are not shared among blocks
   long long items;          // row tiles times key / value heads, cache_attn_items
-  int line_shift;           // set by the launcher, see LineSeq
+  int line_shift;           // set by the plan, see LineSeq
   CacheView c;
   CacheSeqs s;
   DevCtl ctl;
@@ -74,9 +74,21 @@ struct CacheAttnArgs {
 size_t cache_attn_ws_bytes(long long total, int max_new, int h, int hk, int d, int n_seqs);
 long long cache_attn_items(const int* cu_host, int n_seqs, int max_new, int G, int hk);
 constexpr long long kMaxCacheItems = 1LL << 28;  // their line's length fits 32 bits
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st);
+// How a call runs: the kernel that works through the items' pieces, and the one that
+// joins them where items may be shared.
+struct CacheAttnPlan {
+  CacheAttnArgs args;
+  int row_tiles;            // of 8 rows in an item: 1, 2 or 4; 0: the tensor-core kernel
+  int grid;
+  bool big, joins;          // big: the blocks of few rows take a whole SM
+};
+CacheAttnPlan plan_cache_attn(const CacheAttnArgs& a);
+cudaError_t launch_cache_attn(const CacheAttnPlan& p, cudaStream_t st);
+cudaError_t launch_cache_join(const CacheAttnPlan& p, cudaStream_t st);
 // the variant for many query rows per key / value head
 size_t cache_chunk_ws_bytes(int d);
-cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t st);
+void plan_cache_chunk(CacheAttnPlan& p);
+cudaError_t launch_cache_chunk(const CacheAttnPlan& p, cudaStream_t st);
+cudaError_t launch_chunk_join(const CacheAttnPlan& p, cudaStream_t st);
 
 }  // namespace ra

@@ -731,32 +731,23 @@ int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 constexpr int big_warps(int nt) { return nt == 4 ? 8 : 12; }
 
 template <int D, int NT, int W>
-cudaError_t launch_w(const CacheAttnArgs& a, bool whole, int grid, cudaStream_t st) {
+cudaError_t launch_w(const CacheAttnPlan& p, cudaStream_t st) {
   using L = Lay<D, NT, W>;
-  cudaError_t e = configure_kernel<cache_attn_kernel<D, NT, W>>(0, L::kBytes);
+  const cudaError_t e = configure_kernel<cache_attn_kernel<D, NT, W>>(0, L::kBytes);
   if (e != cudaSuccess) return e;
-  CacheAttnArgs b = a;
-  b.whole = whole;
-  b.line_shift = line_shift_for(a.items, (a.max_kv + kUnit - 1) / kUnit + FewRows<NT>::kItemCost);
-  e = launch_early(cache_attn_kernel<D, NT, W>, grid, 32 * W, L::kBytes, st, b);
-  if (e != cudaSuccess || whole) return e;
-  return launch_early(cache_join_kernel<L::R, D>, dim3(grid, (std::min(a.max_new * a.G, L::R) + 7) / 8), 256 * kJoinGroups,
-                      0, st, b);
+  return launch_early(cache_attn_kernel<D, NT, W>, p.grid, 32 * W, L::kBytes, st, p.args);
 }
 
-// Items short enough for one block (2048 keys: about 7 us, as long as a second kernel takes)
-// and no more than SMs: a big block for each, nothing to join.  Very few items of 8 rows:
-// big blocks too, so that an item has fewer pieces to join (8 items of 30,000 keys of d = 128:
-// 22.6 us, with small blocks 23.6; d = 64: 18.5 and 20.6; 16 items: 30.4 and 28.7).  Else small
-// blocks, whose starts and ends overlap (64 items of 10,000 keys: 31 us, with big blocks
-// 35; 12 rows: 38 and 44; 28 rows: 56 and 64).
 template <int D, int NT>
-cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
-  const int units = (a.max_kv + kUnit - 1) / kUnit, sms = num_sms();
-  const bool whole = a.items <= sms && units <= 16, big = whole || (NT == 1 && a.items * 10 <= sms);
-  const long long line = a.items * (whole ? 1 : units + FewRows<NT>::kItemCost);  // at most
-  const int grid = (int)std::min(line, (long long)sms * (big ? 1 : small_blocks(D, NT)));
-  return big ? launch_w<D, NT, big_warps(NT)>(a, whole, grid, st) : launch_w<D, NT, 4>(a, whole, grid, st);
+cudaError_t launch(const CacheAttnPlan& p, cudaStream_t st) {
+  return p.big ? launch_w<D, NT, big_warps(NT)>(p, st) : launch_w<D, NT, 4>(p, st);
+}
+
+template <int D, int NT>
+cudaError_t launch_join(const CacheAttnPlan& p, cudaStream_t st) {
+  constexpr int R = 8 * NT;
+  return launch_early(cache_join_kernel<R, D>, dim3(p.grid, (std::min(p.args.max_new * p.args.G, R) + 7) / 8),
+                      256 * kJoinGroups, 0, st, p.args);
 }
 
 }  // namespace
@@ -782,11 +773,42 @@ long long cache_attn_items(const int* cu_host, int n_seqs, int max_new, int G, i
   return tiles * hk;
 }
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
-  if (many_rows(a.max_new, a.G)) return launch_cache_chunk(a, st);
-  const int nt = row_tiles((long long)a.max_new * a.G);
-  if (a.d == 64) return nt == 1 ? launch<64, 1>(a, st) : nt == 2 ? launch<64, 2>(a, st) : launch<64, 4>(a, st);
-  return nt == 1 ? launch<128, 1>(a, st) : nt == 2 ? launch<128, 2>(a, st) : launch<128, 4>(a, st);
+// Items short enough for one block (2048 keys: about 7 us, as long as a second kernel takes)
+// and no more than SMs: a big block for each, nothing to join.  Very few items of 8 rows:
+// big blocks too, so that an item has fewer pieces to join (8 items of 30,000 keys of d = 128:
+// 22.6 us, with small blocks 23.6; d = 64: 18.5 and 20.6; 16 items: 30.4 and 28.7).  Else small
+// blocks, whose starts and ends overlap (64 items of 10,000 keys: 31 us, with big blocks
+// 35; 12 rows: 38 and 44; 28 rows: 56 and 64).
+CacheAttnPlan plan_cache_attn(const CacheAttnArgs& a) {
+  CacheAttnPlan p = {a, many_rows(a.max_new, a.G) ? 0 : row_tiles((long long)a.max_new * a.G), 0, false, false};
+  if (p.row_tiles == 0) {
+    plan_cache_chunk(p);
+    return p;
+  }
+  constexpr int kItemCost = FewRows<1>::kItemCost;  // (whatever the rows)
+  const int units = (a.max_kv + kUnit - 1) / kUnit, sms = num_sms();
+  const bool whole = a.items <= sms && units <= 16;
+  p.big = whole || (p.row_tiles == 1 && a.items * 10 <= sms);
+  p.joins = !whole;
+  const long long line = a.items * (whole ? 1 : units + kItemCost);  // at most
+  p.grid = (int)std::min(line, (long long)sms * (p.big ? 1 : small_blocks(a.d, p.row_tiles)));
+  p.args.whole = whole;
+  p.args.line_shift = line_shift_for(a.items, units + kItemCost);
+  return p;
+}
+
+cudaError_t launch_cache_attn(const CacheAttnPlan& p, cudaStream_t st) {
+  const int nt = p.row_tiles;
+  if (nt == 0) return launch_cache_chunk(p, st);
+  if (p.args.d == 64) return nt == 1 ? launch<64, 1>(p, st) : nt == 2 ? launch<64, 2>(p, st) : launch<64, 4>(p, st);
+  return nt == 1 ? launch<128, 1>(p, st) : nt == 2 ? launch<128, 2>(p, st) : launch<128, 4>(p, st);
+}
+
+cudaError_t launch_cache_join(const CacheAttnPlan& p, cudaStream_t st) {
+  const int nt = p.row_tiles;
+  if (nt == 0) return launch_chunk_join(p, st);
+  if (p.args.d == 64) return nt == 1 ? launch_join<64, 1>(p, st) : nt == 2 ? launch_join<64, 2>(p, st) : launch_join<64, 4>(p, st);
+  return nt == 1 ? launch_join<128, 1>(p, st) : nt == 2 ? launch_join<128, 2>(p, st) : launch_join<128, 4>(p, st);
 }
 
 }  // namespace ra

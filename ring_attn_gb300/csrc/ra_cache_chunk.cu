@@ -743,26 +743,32 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const CacheAttnArgs g) 
 }
 
 template <int D>
-cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
-  cudaError_t e = configure_kernel<cache_chunk_kernel<D>>(kLaunchRegs, Lay<D>::kAlloc);
+cudaError_t launch(const CacheAttnPlan& p, cudaStream_t st) {
+  const cudaError_t e = configure_kernel<cache_chunk_kernel<D>>(kLaunchRegs, Lay<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  const int grid = num_sms();
-  // the causal cost of an item is at most G (units + kItemCost) + 2 + 2 tiles places
-  CacheAttnArgs b = a;
-  const long long units = (a.max_kv + kUnit - 1) / kUnit + ManyRows::kItemCost;
-  const long long places = a.causal ? a.G * units + 2 + 2 * (((long long)a.max_new * a.G + 255) / 256) : units;
-  b.line_shift = a.items * (places + 2) < (1LL << 30) ? 0 : std::max(1, line_shift_for(a.items, units));
-  e = launch_early(cache_chunk_kernel<D>, grid, kThreads, Lay<D>::kAlloc, st, b);
-  if (e != cudaSuccess) return e;
-  return launch_early(chunk_join_kernel<D>, dim3(grid, 8), 256, 0, st, b);
+  return launch_early(cache_chunk_kernel<D>, p.grid, kThreads, Lay<D>::kAlloc, st, p.args);
 }
 
 }  // namespace
 
 size_t cache_chunk_ws_bytes(int d) { return line_ws_bytes<256>(num_sms(), d); }
 
-cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t st) {
-  return a.d == 64 ? launch<64>(a, st) : launch<128>(a, st);
+void plan_cache_chunk(CacheAttnPlan& p) {
+  CacheAttnArgs& a = p.args;
+  p.grid = num_sms();
+  p.joins = true;
+  // the causal cost of an item is at most G (units + kItemCost) + 2 + 2 tiles places
+  const long long units = (a.max_kv + kUnit - 1) / kUnit + ManyRows::kItemCost;
+  const long long places = a.causal ? a.G * units + 2 + 2 * (((long long)a.max_new * a.G + 255) / 256) : units;
+  a.line_shift = a.items * (places + 2) < (1LL << 30) ? 0 : std::max(1, line_shift_for(a.items, units));
+}
+
+cudaError_t launch_cache_chunk(const CacheAttnPlan& p, cudaStream_t st) {
+  return p.args.d == 64 ? launch<64>(p, st) : launch<128>(p, st);
+}
+
+cudaError_t launch_chunk_join(const CacheAttnPlan& p, cudaStream_t st) {
+  return launch_early(p.args.d == 64 ? chunk_join_kernel<64> : chunk_join_kernel<128>, dim3(p.grid, 8), 256, 0, st, p.args);
 }
 
 }  // namespace ra
