@@ -933,9 +933,10 @@ ra_status ring_attn_varlen_unpermute(const ra_tensor* y, ra_tensor* x, const int
 
 // ------------------------------------------------------------------ paged 4-bit cache
 // (rows, heads, d) rows of new tokens: at least `total` rows of `heads` heads (-1: any number).
+// A tensor without rows has no address.
 static ra_status check_rows3(const ra_tensor* t, int32_t dtype, long long total, long long heads, long long d,
                              Rows3* v) {
-  if (!t || !t->data || t->ndim != 3 || t->dtype != dtype) return RA_ERR_INVALID_ARG;
+  if (!t || (!t->data && t->shape[0] != 0) || t->ndim != 3 || t->dtype != dtype) return RA_ERR_INVALID_ARG;
   if (t->shape[0] < total || t->shape[1] < 1 || t->shape[2] != d) return RA_ERR_INVALID_ARG;
   if (heads >= 0 && t->shape[1] != heads) return RA_ERR_INVALID_ARG;
   const int es = dtype == RA_FP32 ? 4 : 2;
@@ -1023,6 +1024,9 @@ static ra_status check_rope_table(const ra_tensor* t, const ra_tensor* like, con
 // apart, nor when, modulo a stride P of either, both reach only runs of bytes that lie
 // apart: slices of one packed tensor, whose rows (P) or heads interleave.
 static bool may_share(const ra_tensor* a, int es_a, const ra_tensor* b, int es_b) {
+  for (const ra_tensor* t : {a, b})
+    for (int i = 0; i < t->ndim; ++i)
+      if (t->shape[i] == 0) return false;
   uintptr_t alo, ahi, blo, bhi;
   byte_span(a, es_a, &alo, &ahi);
   byte_span(b, es_b, &blo, &bhi);
@@ -1136,7 +1140,7 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (!out || (out->dtype != RA_BF16 && out->dtype != RA_FP32)) return RA_ERR_INVALID_ARG;
   a.out_f32 = out->dtype == RA_FP32;
   RA_TRY(check_rows3(out, out->dtype, a.s.total, a.h, d, &a.out));
-  if (!lse || !lse->data || lse->ndim != 2 || lse->dtype != RA_FP32 || lse->shape[0] != a.h ||
+  if (!lse || (!lse->data && lse->shape[1] != 0) || lse->ndim != 2 || lse->dtype != RA_FP32 || lse->shape[0] != a.h ||
       lse->shape[1] < a.s.total || !aligned(lse->data, 4))
     return RA_ERR_INVALID_ARG;
   a.lse = static_cast<float*>(lse->data);
@@ -1148,10 +1152,10 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   a.causal = causal;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.max_kv = max_kv_len > 0 && max_kv_len < a.s.max_tokens ? max_kv_len : a.s.max_tokens;
+  if (a.s.total == 0) return RA_OK;
   const size_t need = cache_attn_ws_bytes(a.s.total, a.max_new, a.h, a.hk, a.d, a.s.n_seqs);
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return RA_ERR_WORKSPACE;
   a.ws = workspace;
-  if (a.s.total == 0) return RA_OK;
   const int out_size = a.out_f32 ? 4 : 2;
   if (may_share(q, 2, out, out_size) || may_share(q, 2, lse, 4) || may_share(out, out_size, lse, 4))
     return RA_ERR_INVALID_ARG;

@@ -150,10 +150,8 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     RA_REFUSE(THPVariable_Unpack(a[10]).size(0) < cu.total, "positions must have an entry for every new token");
   }
   const int inter = truth(a[11]);
-  int status = RA_OK;
-  if (cu.total > 0)
-    status = g_append(given(a[7]) ? &q : nullptr, &k, &v, given(a[8]) ? &cos : nullptr, given(a[8]) ? &sin : nullptr,
-                      inter, pos, c.cache, &seqs, given(a[7]) ? &out : nullptr, current_stream(c.index));
+  const int status = g_append(given(a[7]) ? &q : nullptr, &k, &v, given(a[8]) ? &cos : nullptr, given(a[8]) ? &sin : nullptr,
+                              inter, pos, c.cache, &seqs, given(a[7]) ? &out : nullptr, current_stream(c.index));
   PyObject* r = given(a[12]) ? Py_NewRef(a[12]) : q_out.defined() ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None);
   return Py_BuildValue("(iN)", status, r);
   END_HANDLE_TH_ERRORS
@@ -173,8 +171,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     t[i] = given(a[5 + i]) ? tensor(a[5 + i], c.index) : at::empty({cu.total, c.hk, c.d}, on(c.index, at::kBFloat16));
     r[i] = describe(t[i], 3);
   }
-  int status = RA_OK;
-  if (cu.total > 0) status = g_read(c.cache, &seqs, &r[0], &r[1], current_stream(c.index));
+  const int status = g_read(c.cache, &seqs, &r[0], &r[1], current_stream(c.index));
   return Py_BuildValue("(iNN)", status, given(a[5]) ? Py_NewRef(a[5]) : THPVariable_Wrap(t[0]),
                        given(a[6]) ? Py_NewRef(a[6]) : THPVariable_Wrap(t[1]));
   END_HANDLE_TH_ERRORS
@@ -199,18 +196,15 @@ PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                      : at::empty(tq.sizes(), on(c.index, fp32 ? at::kFloat : at::kBFloat16));
   const at::Tensor lse = given(a[10]) ? tensor(a[10], c.index) : at::empty({tq.size(1), tq.size(0)}, on(c.index, at::kFloat));
   ra_tensor o = describe(out, 3), l = describe(lse, 2);
-  int status = RA_OK;
-  if (cu.total > 0) {
-    at::Tensor ws;
-    if (given(a[12])) {
-      ws = tensor(a[12], c.index);
-      RA_REFUSE(!ws.is_contiguous(), "workspace must be contiguous");
-    } else {
-      ws = at::empty({(int64_t)g_ws_size(cu.total, cu.max_new(), tq.size(1), c.hk, c.d, cu.n)}, on(c.index, at::kByte));
-    }
-    status = g_fwd(&q, c.cache, &seqs, causal, (float)scale, (int32_t)max_kv, &o, &l, ws.data_ptr(), ws.nbytes(),
-                   current_stream(c.index));
+  at::Tensor ws;
+  if (given(a[12])) {
+    ws = tensor(a[12], c.index);
+    RA_REFUSE(!ws.is_contiguous(), "workspace must be contiguous");
+  } else if (cu.total > 0) {
+    ws = at::empty({(int64_t)g_ws_size(cu.total, cu.max_new(), tq.size(1), c.hk, c.d, cu.n)}, on(c.index, at::kByte));
   }
+  const int status = g_fwd(&q, c.cache, &seqs, causal, (float)scale, (int32_t)max_kv, &o, &l, ws.defined() ? ws.data_ptr() : nullptr,
+                           ws.defined() ? ws.nbytes() : 0, current_stream(c.index));
   return Py_BuildValue("(iNN)", status, given(a[9]) ? Py_NewRef(a[9]) : THPVariable_Wrap(out),
                        given(a[10]) ? Py_NewRef(a[10]) : THPVariable_Wrap(lse));
   END_HANDLE_TH_ERRORS

@@ -1,9 +1,9 @@
-"""CPU checks: which overlaps of a cache call's tensors are refused, before any launch."""
+"""CPU checks, before any launch: which overlaps of a cache call's tensors are refused, and tensors without rows."""
 import numpy as np
 import pytest
 
 import ring_attn_gb300 as ra
-from tests.test_cache import FAR, append, attend, fake, lib, read  # noqa: F401 (lib: the fixture)
+from tests.test_cache import FAR, append, attend, cache, fake, lib, read, seqs  # noqa: F401 (lib: the fixture)
 
 ODD = 0x1002  # positions there are refused (3) behind the overlaps (1)
 
@@ -60,3 +60,18 @@ def test_attention_overlaps(lib):  # noqa: F811
     assert f(lse=fake((4, 10), ra.RA_FP32, data=0x100000 + 512)) == 1             # in q
     assert f(lse=fake((4, 10), ra.RA_FP32, data=FAR + 5120 - 4)) == 1             # in out
     assert f(lse=fake((4, 10), ra.RA_FP32, data=FAR + 128, stride=(64, 128))) == 1
+
+
+def test_tensors_without_rows(lib):  # noqa: F811
+    """A call without new tokens is checked like any other; its tensors may be empty (and have no address)."""
+    none = lambda heads, dtype=ra.RA_BF16: fake((0, heads, 64), dtype, data=0, stride=(heads * 64, 64, 1))  # noqa: E731
+    s = seqs((0, 0, 0))
+    assert append(lib, s=s, k=none(2), v=none(2)) == 0
+    assert append(lib, s=s, k=none(2), v=none(2), q=none(4), out=none(4)) == 0
+    assert append(lib, s=s, k=none(2), v=none(3)) == 1
+    assert read(lib, s=s, k=none(2), v=none(2)) == 0 and read(lib, s=s, k=none(2), v=none(1)) == 1
+    lse = fake((4, 0), ra.RA_FP32, data=0, stride=(1, 1))
+    assert attend(lib, s=s, q=none(4), out=none(4), lse=lse, ws=None, wb=0) == 0
+    assert attend(lib, s=s, q=none(4), out=none(3), lse=lse, ws=None, wb=0) == 1
+    assert attend(lib, s=s, c=cache(page=48), q=none(4), out=none(4), lse=lse, ws=None, wb=0) == 2
+    assert append(lib, k=none(2)) == 1 and read(lib, v=none(2)) == 1 and attend(lib, q=none(4)) == 1

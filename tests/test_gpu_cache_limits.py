@@ -112,3 +112,23 @@ def test_tiny_scales_and_queries(ra, new, scale):  # noqa: F811
         assert_within("lse", lse, ref_l, tol_l)
         assert_within("out", out, ref, tol)
     check_no_device_error(ra)
+
+
+def test_calls_without_new_tokens(ra):  # noqa: F811
+    """They give empty results, and refuse what any call refuses."""
+    c = Case((0, 0), (30, 5), 4, 2, 64, 64, seed=1)
+    cache, x = c.fill(ra), torch.zeros(0, 8, 64, dtype=torch.bfloat16, device="cuda")
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    lists = (c.page_table, c.kv_lens, [0, 0, 0])
+    out, lse = ra.ring_attn_cache_fwd(q, cache, *lists)
+    assert out.shape == (0, 4, 64) and lse.shape == (4, 0)
+    assert all(y.shape == (0, 2, 64) for y in ra.ring_attn_cache_read(cache, *lists))
+    assert ra.ring_attn_cache_append(k, v, cache, *lists, q=q, rope=tables(9, 64)).shape == (0, 4, 64)
+    odd = [b[:, :, :48].contiguous() for b in c.bytes]  # pages of 48 tokens
+    odd = ra.KVCache(odd[0], odd[1].view(torch.float8_e4m3fn), odd[2], odd[3].view(torch.float8_e4m3fn))
+    for call in (lambda: ra.ring_attn_cache_fwd(q, odd, *lists), lambda: ra.ring_attn_cache_read(odd, *lists),
+                 lambda: ra.ring_attn_cache_append(k, v, odd, *lists), lambda: ra.ring_attn_cache_fwd(q.float(), cache, *lists),
+                 lambda: ra.ring_attn_cache_append(k, v.float(), cache, *lists)):
+        with pytest.raises(RuntimeError):
+            call()
+    check_no_device_error(ra)
