@@ -302,6 +302,10 @@ size_t ring_attn_workspace_size(int32_t op, int64_t b, int64_t h, int64_t s, int
  *   k_scale, v_scale: (n_pages, hk, page, d / 16) RA_E4M3, one scale per 16
  *   consecutive head dims of a token.  The value is number * scale; both factors
  *   together have at most 6 significant bits, so bf16 and fp16 hold it exactly.
+ *   There is no other scale.  The scales go from 2^-9 to 448, so normally distributed
+ *   numbers of size 0.03 to 400 are off by 9.5 % (rms), of size 0.01 by 13 %, 0.001 by 28 %, and
+ *   magnitudes above 2688 become 2688.  Keys and values of other sizes are multiplied by
+ *   a factor before the append; the keys' divides softmax_scale, the values' divides out.
  *   d in {64, 128}; page a power of two in [16, 256]; the last dimension is
  *   contiguous, every other stride of k and v is a multiple of 16 bytes and of
  *   the scales a multiple of d / 16 bytes, base pointers are 16-byte aligned
@@ -383,7 +387,7 @@ ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs,
 /* ring_attn_cache_fwd: attention of the new tokens over the cache.
  *   q: (rows, h, d) bf16, rotated; h a multiple of hk (query head i attends with
  *   head i / (h / hk)).  out: (rows, h, d) bf16 or fp32 (fp32: the accumulator of
- *   lse_merge); lse: (h, rows) fp32, natural log, any strides.
+ *   lse_merge; the weights are rounded to 11 bits in both); lse: (h, rows) fp32, natural log, any strides.
  *   causal: new token j of n sees the cache's tokens up to its own, kv_lens[i] - n
  *   + j; else every token of the sequence (what cross attention to cached states
  *   needs).  A row that sees no token gets out = 0, lse = -inf, so shards of one

@@ -590,7 +590,11 @@ class KVCache:
     memory (pass a transposed view).  The handle keeps the tensors, which the caller
     allocates, and their description, so that a call marshals nothing for them (so k, k_scale,
     v and v_scale cannot be replaced: other tensors are another handle); copies describe their
-    own tensors.  KVCache.empty allocates a cache of zeros."""
+    own tensors.  KVCache.empty allocates a cache of zeros.
+
+    The stored scales go from 2^-9 to 448 and there is no other: keys and values of size 0.03 to
+    400 are kept best.  Multiply others by a factor before they are appended, and divide
+    softmax_scale (keys) or the result (values) by it."""
 
     k, k_scale, v, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 

@@ -14,14 +14,19 @@
 //     free as long as Q has the same).
 //   O^T = V^T P^T: P^T is the transpose of the score fragment (movmatrix); a lane
 //     holds 16 head dims of one scale group, for the keys 2t, 2t + 1, 2t + 8, 2t + 9.
-// Queries are scaled per row by a power of two into fp16's normal range.  The
+// Both operands of a product have 16 bits; fp16 rather than bf16, because that holds number *
+// scale and three more bits of p.  Queries are scaled per row by a power of two, the largest entry to
+// [2^12, 2^13): entries down to 2^-26 of it are exact, those below 2^-36 of it count as 0, which
+// is less than the rounding of the fp32 sums unless a key is 0 wherever its query is not
+// small.  p is rounded to 11 bits (off by at most 2^-11 of it), for an fp32 out, too; the
 // exponent's offset M keeps the largest p between 2^8 and 2^12, so p down to
-// 2^-22 of it has all its fp16 bits; O is rescaled only when a score passes that.
+// 2^-22 of it has all its fp16 bits; O is rescaled only when a score passes that.  Scores, M, sums
+// and O are fp32, the exponential is the hardware's (2^-22).
 //
-// Bound: 0.5625 bytes per number from HBM.  A tile of 32 keys and 8 query rows costs a
-// warp about 630 instructions (d = 128: 140 conversions, 128 products with scales, 32
-// matrix products), half of the issue slots while the cache streams at 82 % of the
-// measured copy rate.  One query of 32 heads over 128K keys of 8: 151 MB in 42 us; 64
+// Bound: 0.5625 bytes per number from HBM, and close behind it the issue slots.  A tile of 32 keys
+// and 8 query rows costs a warp about 630 instructions (d = 128: 140 conversions, 128 products with
+// scales, 32 matrix products): over the whole kernel 53 % of the slots, start and end included,
+// while it reads 3.7 TB/s (56 % of the measured copy rate; 64 ragged sequences).  One query of 32 heads over 128K keys of 8: 151 MB in 42 us; 64
 // sequences of 200 to 16384 keys of 4 heads: 38 us, of which about 6 are the joining kernel's.
 #include <algorithm>
 

@@ -24,9 +24,10 @@
 //                far), P as fp16 over the score columns; the epilogue.
 // Bound: tensor throughput, and with it shared memory: of a unit's 2048 tensor cycles
 // (256 rows, d = 128) operand reads take 1536 and the converted tiles' stores 512.
-// 2048 tokens of 32 heads at the end of 65,536 keys of 8 heads: 1.53 ms, 1417 TFLOP/s
+// 2048 tokens of 32 heads at the end of 65,536 keys of 8 heads: 1.53 ms, 1413 TFLOP/s
 // (73 % of the measured bf16 rate); 1.41 ms without the conversions, 1.19 without softmax.
-// fp16 operands hold number * scale exactly.
+// fp16 operands hold number * scale exactly; queries and p are rounded to fp16 and the rest is
+// fp32, as in ra_cache_attn.cu, whose comment says what that costs.
 #include <algorithm>
 
 #include "ra_cache_line.cuh"
