@@ -47,3 +47,23 @@ def test_a_cu_seqlens_that_does_not_fit_is_refused(ra):  # noqa: F811
         with pytest.raises(ValueError):
             ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, cu)
     check_no_device_error(ra)
+
+
+@pytest.mark.parametrize("duplicate", COPIES)
+def test_a_copied_kv_cache_is_one_of_its_own(ra, duplicate):  # noqa: F811
+    """Calls on the copy use its tensors (copy.copy: the same ones), also when the first is gone."""
+    c = Case((2, 3), (30, 41), 4, 2, 64, 16, seed=23, order=(0, 2, 1))
+    first, q = c.fill(ra), c.queries()
+    before = [b.clone() for b in c.bytes]
+    cache = duplicate(first)
+    del first
+    gc.collect()
+    out, lse = ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, c.cu.tolist())
+    ref, ref_l, tol, tol_l = c.expect(q, True)
+    assert_within("out", out, ref, tol)
+    assert_within("lse", lse, ref_l, tol_l)
+    x = c.queries()
+    ra.ring_attn_cache_append(x[:, :2], x[:, 2:], cache, c.page_table, c.kv_lens, c.cu.tolist())
+    same = all(torch.equal(a, b) for a, b in zip(before, c.bytes))
+    assert same == (duplicate is not copy.copy)
+    check_no_device_error(ra)
