@@ -369,7 +369,8 @@ typedef enum { RA_ROPE_HALVES = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope;
  *   input by the fp32 table entries, carried to about 2^-47, so the stored bits do
  *   not depend on the order of the operations.
  *   A token whose cache index is negative (kv_lens[i] < n) is padding: nothing
- *   is written for it, nor for one past the page table or with a bad position.  Two tokens of one call must not name the same place. */
+ *   is written for it, nor for one past the page table or with a bad position.  Two
+ *   tokens of one call must not name the same place. */
 ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
                                  const ra_tensor* rope_cos, const ra_tensor* rope_sin, int32_t rope,
                                  const int32_t* positions, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
@@ -387,7 +388,8 @@ ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs,
 /* ring_attn_cache_fwd: attention of the new tokens over the cache.
  *   q: (rows, h, d) bf16, rotated; h a multiple of hk (query head i attends with
  *   head i / (h / hk)).  out: (rows, h, d) bf16 or fp32 (fp32: the accumulator of
- *   lse_merge; the weights are rounded to 11 bits in both); lse: (h, rows) fp32, natural log, any strides.
+ *   lse_merge; the weights are rounded to 11 bits in both); lse: (h, rows) fp32, natural
+ *   log, any strides.
  *   causal: new token j of n sees the cache's tokens up to its own, kv_lens[i] - n
  *   + j; else every token of the sequence (what cross attention to cached states
  *   needs).  A row that sees no token gets out = 0, lse = -inf, so shards of one

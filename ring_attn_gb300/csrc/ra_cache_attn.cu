@@ -25,9 +25,10 @@
 //
 // Bound: 0.5625 bytes per number from HBM, and close behind it the issue slots.  A tile of 32 keys
 // and 8 query rows costs a warp about 630 instructions (d = 128: 140 conversions, 128 products with
-// scales, 32 matrix products): over the whole kernel 53 % of the slots, start and end included,
-// while it reads 3.7 TB/s (56 % of the measured copy rate; 64 ragged sequences).  One query of 32 heads over 128K keys of 8: 151 MB in 42 us; 64
-// sequences of 200 to 16384 keys of 4 heads: 38 us, of which about 6 are the joining kernel's.
+// scales, 32 matrix products): over the whole kernel 50 to 53 % of the slots, start and end included,
+// while it reads 3.7 TB/s (56 % of the measured copy rate; 64 ragged sequences).  One query of 32
+// heads over 128K keys of 8: 151 MB in 42 us; 64 sequences of 200 to 16384 keys of 4 heads: 38 us, of
+// which about 6 are the joining kernel's.
 #include <algorithm>
 
 #include "ra_cache_line.cuh"
