@@ -411,6 +411,99 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
 size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,
                                       int32_t n_seqs);
 
+/* ---------------------------------------------------------------- rotary positions
+ * ring_attn_rope: rotates queries and keys by their positions before attention.  A pair
+ * (a, b) of head dims becomes (a cos - b sin, b cos + a sin), with cos and sin from the row
+ * of the tables that the pair's position names; positions may have several axes (time,
+ * height and width of an image's or a video's tokens), and every pair goes by one of them.
+ *   q, q_out: (b, h, s, d); k, k_out (optional, both or neither): (b, hk, s, d), any hk; all bf16
+ *   or all fp32, d in {64, 128}; strides multiples of 16 bytes, pointers 16-byte aligned.  An
+ *   output may be its own input; elements shared otherwise are RA_ERR_INVALID_ARG.
+ *   rope_cos, rope_sin, rope: as for ring_attn_cache_append (r rotated head dims; those from
+ *   r on are copied).
+ *   positions NULL: every pair's position is the row's original token, for rows in the order
+ *   of layout and n_shards (ring_attn_permute).  Else the position on axis a of row i of
+ *   batch n is positions[a * stride_axis + n * stride_b + i * stride_s] (int32, device; the
+ *   strides may be 0), the layout says nothing, and pair f goes by axis pair_axis[f] (host
+ *   array of r / 2 numbers below n_axes; NULL with n_axes = 1).
+ *   inverse: turns back.  A rotation's transpose is its inverse, so this is also the backward:
+ *   dq and dk of the rotated tensors in, of the unrotated ones out.
+ * The products are fp32 and rounded once.  A row with a position outside the table is left as
+ * it was, and RA_ERR_DEVICE is recorded (site 0x63). */
+typedef struct {
+  const int32_t* positions;
+  int64_t stride_axis, stride_b, stride_s; /* in elements */
+  const uint8_t* pair_axis;                /* host */
+  int32_t n_axes;
+} ra_rope_positions;
+
+ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor* rope_cos, const ra_tensor* rope_sin,
+                         int32_t rope, const ra_rope_positions* positions, int32_t layout, int32_t n_shards,
+                         int32_t inverse, ra_tensor* q_out, ra_tensor* k_out, void* stream);
+
+/* ---------------------------------------------------------------- changed scores
+ * Attention of models that change their scores: with x = softmax_scale * <q_i, k_j>,
+ *   y = softcap * tanh(x / softcap),  z = y - slope * |i - j|,
+ * and z in the place of x in everything that the calls above say (out, lse and the gradients
+ * of q, k and v; the slopes and softcap are constants).  i, j: the query's and the key's original
+ * tokens, whatever the layout (varlen: in their sequence; the cache: cache indices).
+ *   softcap: 0 (none), or 2^-10 to 2^20 with softmax_scale / softcap at most 2^10 (else
+ *     RA_ERR_UNSUPPORTED).
+ *   slopes: (h) fp32 device array, one per query head, finite, of any sign; or NULL.
+ *   prefix: int32 device array, or NULL: with causal, tokens that every query sees, the first
+ *     prefix[n] of batch n, or of sequence n (varlen, cache: entry of every sequence), so those see
+ *     each other both ways.  Negative counts as 0, beyond the sequence as all of it.  Without
+ *     causal it is refused (RA_ERR_INVALID_ARG).
+ * Documents packed into one buffer are the varlen calls' cu_seqlens.  The arrays are read by the
+ * kernels, so a captured call follows them as they are when it is replayed.  A ra_scores
+ * without any of the three makes a call the plain one; NULL is refused.
+ *
+ * ring_attn_scored_X is ring_attn_X with scores; everything else is as there.  (The CTA-pair knob
+ * does not concern these calls.) */
+typedef struct {
+  float softcap;
+  const float* slopes;
+  const int32_t* prefix;
+} ra_scores;
+
+ra_status ring_attn_scored_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                               int32_t n_shards, int32_t causal, float softmax_scale, const ra_scores* scores,
+                               ra_tensor* out, ra_tensor* lse, void* stream);
+ra_status ring_attn_scored_fwd_step(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                                    int32_t n_shards, int32_t causal, float softmax_scale, const ra_scores* scores,
+                                    int32_t step, ra_tensor* out_blk, ra_tensor* lse_blk, void* stream);
+ra_status ring_attn_scored_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                               const ra_tensor* out, const ra_tensor* lse, int32_t layout, int32_t n_shards,
+                               int32_t causal, float softmax_scale, const ra_scores* scores, ra_tensor* dq,
+                               ra_tensor* dk, ra_tensor* dv, void* workspace, size_t workspace_bytes, void* stream);
+ra_status ring_attn_scored_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                      const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                      int32_t max_seqlen, int32_t layout, int32_t n_shards, int32_t causal,
+                                      float softmax_scale, const ra_scores* scores, ra_tensor* out, ra_tensor* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+ra_status ring_attn_scored_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                      const ra_tensor* out, const ra_tensor* lse, const int32_t* cu_seqlens_dev,
+                                      const int32_t* cu_seqlens_host, int32_t n_seqs, int32_t max_seqlen,
+                                      int32_t layout, int32_t n_shards, int32_t causal, float softmax_scale,
+                                      const ra_scores* scores, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+ra_status ring_attn_scored_llama3_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                             const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
+                                             int32_t n_seqs, int32_t max_seqlen, int32_t rank, int32_t n_shards,
+                                             int32_t causal, float softmax_scale, const ra_scores* scores,
+                                             ra_tensor* out, ra_tensor* lse, void* stream);
+ra_status ring_attn_scored_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
+                                             const ra_tensor* v, const ra_tensor* out, const ra_tensor* lse,
+                                             const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
+                                             int32_t n_seqs, int32_t max_seqlen, int32_t rank, int32_t n_shards,
+                                             int32_t causal, float softmax_scale, const ra_scores* scores,
+                                             ra_tensor* dq, ra_tensor* dk, ra_tensor* dv, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+ra_status ring_attn_scored_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
+                                     int32_t causal, float softmax_scale, const ra_scores* scores, int32_t max_kv_len,
+                                     ra_tensor* out, ra_tensor* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Synchronises `stream`, then reads and clears this device's error word.
  * Returns RA_OK, RA_ERR_TIMEOUT (a bounded wait ran out: the kernel gave up
  * and returned) or RA_ERR_DEVICE; RA_ERR_CUDA if the synchronisation failed.
@@ -446,7 +539,8 @@ typedef enum {
   RA_KERNEL_CACHE_READ = 7,
   RA_KERNEL_CACHE_FWD = 8,   /* attention over the 4-bit cache, without the next */
   RA_KERNEL_CACHE_JOIN = 9,  /* joins the partial results of ring_attn_cache_fwd, where blocks share a sequence */
-  RA_KERNEL_COUNT = 10
+  RA_KERNEL_ROPE = 10,
+  RA_KERNEL_COUNT = 11
 } ra_kernel;
 ra_status ring_attn_timing_enable(int32_t on);
 ra_status ring_attn_timing_read(int32_t kernel, double* total_ms, int64_t* launches);

@@ -8,6 +8,7 @@ library is missing or a tensor is not on a CUDA device the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import math
@@ -25,7 +26,7 @@ __all__ = [
     "ring_attn_varlen_kvpacked_fwd", "ring_attn_varlen_kvpacked_bwd", "ring_attn_varlen_permute",
     "ring_attn_varlen_unpermute", "ring_attn_llama3_varlen_fwd", "ring_attn_llama3_varlen_bwd", "CuSeqlens",
     "KVCache", "ring_attn_cache_append", "ring_attn_cache_read", "ring_attn_cache_fwd", "ring_attn_cache_workspace_size",
-    "ring_attn_cache_workspace",
+    "ring_attn_cache_workspace", "Scores", "ring_attn_rope", "ring_attn_rope_bwd",
 ]
 
 LAYOUTS = {"contiguous": 0, "zigzag": 1, "stripe": 2}
@@ -41,11 +42,13 @@ EXPORTED_SYMBOLS = (
     "ra_status_string", "ring_attn_version", "ring_attn_bwd_static_scratch", "ring_attn_varlen_permute",
     "ring_attn_varlen_unpermute", "ring_attn_llama3_varlen_fwd", "ring_attn_llama3_varlen_bwd",
     "ring_attn_debug_bounds", "ring_attn_varlen_workspace_size", "ring_attn_cache_append", "ring_attn_cache_read",
-    "ring_attn_cache_fwd", "ring_attn_cache_workspace_size",
+    "ring_attn_cache_fwd", "ring_attn_cache_workspace_size", "ring_attn_rope", "ring_attn_scored_fwd",
+    "ring_attn_scored_fwd_step", "ring_attn_scored_bwd", "ring_attn_scored_varlen_fwd", "ring_attn_scored_varlen_bwd",
+    "ring_attn_scored_llama3_varlen_fwd", "ring_attn_scored_llama3_varlen_bwd", "ring_attn_scored_cache_fwd",
 )
 RA_STATIC_SCRATCH_BYTES = 16 << 20
 KERNELS = {"fwd": 0, "bwd_dkdv": 1, "bwd_pre": 2, "bwd_dq": 3, "permute": 4, "lse_merge": 5, "cache_append": 6,
-           "cache_read": 7, "cache_fwd": 8, "cache_join": 9}
+           "cache_read": 7, "cache_fwd": 8, "cache_join": 9, "rope": 10}
 
 
 class RingAttnError(RuntimeError):
@@ -67,6 +70,15 @@ class _KVSeqs(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
                 ("cu_seqlens_dev", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
                 ("max_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32)]
+
+
+class _Scores(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
+class _RopePositions(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("stride_axis", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+                ("stride_s", ctypes.c_int64), ("pair_axis", ctypes.c_void_p), ("n_axes", ctypes.c_int32)]
 
 
 _LIB = None
@@ -95,6 +107,7 @@ def load():
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     T = ctypes.POINTER(_Tensor)
     C, S = ctypes.POINTER(_KVCache), ctypes.POINTER(_KVSeqs)
+    Z = ctypes.POINTER(_Scores)
     sig = {
         "ring_attn_fwd": [T, T, T, I32, I32, I32, F32, T, T, P, SZ, P],
         "ring_attn_fwd_step": [T, T, T, I32, I32, I32, F32, I32, T, T, P],
@@ -112,6 +125,16 @@ def load():
         "ring_attn_cache_append": [T, T, T, T, T, I32, P, C, S, T, P],
         "ring_attn_cache_read": [C, S, T, T, P],
         "ring_attn_cache_fwd": [T, C, S, I32, F32, I32, T, T, P, SZ, P],
+        "ring_attn_rope": [T, T, T, T, I32, ctypes.POINTER(_RopePositions), I32, I32, I32, T, T, P],
+        "ring_attn_scored_fwd": [T, T, T, I32, I32, I32, F32, Z, T, T, P],
+        "ring_attn_scored_fwd_step": [T, T, T, I32, I32, I32, F32, Z, I32, T, T, P],
+        "ring_attn_scored_bwd": [T, T, T, T, T, T, I32, I32, I32, F32, Z, T, T, T, P, SZ, P],
+        "ring_attn_scored_varlen_fwd": [T, T, T, P, P, I32, I32, I32, I32, I32, F32, Z, T, T, P, SZ, P],
+        "ring_attn_scored_varlen_bwd": [T, T, T, T, T, T, P, P, I32, I32, I32, I32, I32, F32, Z, T, T, T, P, SZ, P],
+        "ring_attn_scored_llama3_varlen_fwd": [T, T, T, P, P, I32, I32, I32, I32, I32, F32, Z, T, T, P],
+        "ring_attn_scored_llama3_varlen_bwd": [T, T, T, T, T, T, P, P, I32, I32, I32, I32, I32, F32, Z, T, T, T, P, SZ,
+                                               P],
+        "ring_attn_scored_cache_fwd": [T, C, S, I32, F32, Z, I32, T, T, P, SZ, P],
         "ring_attn_check_device_error": [P, ctypes.POINTER(I32)],
         "ring_attn_set_knob": [I32, I64],
         "ring_attn_timing_enable": [I32],
@@ -182,38 +205,110 @@ def _scale(scale, d):
     return float(1.0 / math.sqrt(d) if scale is None else scale)
 
 
+class Scores:
+    """What a model does to its scores besides the product, for the `scores` argument of the attention calls.
+
+    With x = softmax_scale * q.k of tokens i and j (of a sequence, whatever the layout):
+    softcap: y = softcap * tanh(x / softcap), 2^-10 to 2^20 (0: y = x).
+    slopes: (h,) fp32, one per query head: z = y - slopes[h] * |i - j|.
+    prefix: (b,) int32, or (n_seqs,) for varlen and cache calls: with causal, every token of a
+    sequence sees its first prefix tokens, so that those see each other both ways.
+    out, lse and the gradients of q, k and v are those of attention with z; softcap and slopes
+    are constants.  The handle keeps the tensors, whose contents the kernels read (so a
+    captured call follows them); they cannot be replaced: other tensors are another handle."""
+
+    softcap, slopes, prefix = (property(lambda self, i=i: self._parts[i]) for i in range(3))
+
+    def __init__(self, softcap=0.0, slopes=None, prefix=None):
+        self._parts = (float(softcap), slopes, prefix)
+        for name, x, dtype in (("slopes", slopes, torch.float32), ("prefix", prefix, torch.int32)):
+            if x is None:
+                continue
+            if not isinstance(x, torch.Tensor) or not x.is_cuda:
+                raise ValueError("ring_attn_gb300 takes CUDA tensors only")
+            if x.dtype != dtype or x.dim() != 1 or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor")
+        if slopes is not None and prefix is not None and slopes.device != prefix.device:
+            raise ValueError("slopes and prefix must be on one device")
+        self.device = slopes.device if slopes is not None else prefix.device if prefix is not None else None
+        self._c = _Scores(float(softcap), None if slopes is None else slopes.data_ptr(),
+                          None if prefix is None else prefix.data_ptr())
+        self._call = (ctypes.addressof(self._c), -1 if self.device is None else self.device.index,
+                      -1 if slopes is None else slopes.numel(), -1 if prefix is None else prefix.numel())
+
+    def __reduce__(self):  # copies and pickles describe their own tensors
+        return type(self), self._parts
+
+    def _arg(self, device, h, n):
+        """The C argument for a call of h query heads and n batches or sequences on the device."""
+        if self.device is not None and self.device != device:
+            raise ValueError(f"scores on {self.device}, call on {device}")
+        if self.slopes is not None and self.slopes.numel() != h:
+            raise ValueError(f"slopes must have one entry for each of the {h} query heads")
+        if self.prefix is not None and self.prefix.numel() != n:
+            raise ValueError(f"prefix must have one entry for each of the {n} sequences")
+        return ctypes.byref(self._c)
+
+
+def _place(scores, q, stream):
+    """Where a call with scores runs and allocates: the stream given, or q's device."""
+    if scores is None:
+        return contextlib.nullcontext()
+    if not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores")
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("ring_attn_gb300 takes CUDA tensors only")
+    if stream is None:
+        return torch.cuda.device(q.device)
+    if stream.device != q.device:
+        raise ValueError(f"stream on {stream.device}, q on {q.device}")
+    return torch.cuda.stream(stream)
+
+
+def _call(name, scores, device, h, n, at, *args):
+    """lib.ring_attn_<name>(*args), or its scored form with the scores at place `at`; checks the status."""
+    if scores is None:
+        _check(getattr(load(), "ring_attn_" + name)(*args), "ring_attn_" + name)
+    else:
+        z = scores._arg(device, h, n)
+        _check(getattr(load(), "ring_attn_scored_" + name)(*args[:at], z, *args[at:]), "ring_attn_scored_" + name)
+
+
 def ring_attn_fwd(q, k, v, layout="contiguous", n_shards=1, causal=False, softmax_scale=None, out=None, lse=None,
-                  stream=None):
+                  stream=None, scores=None):
     """Ring forward with the fp32 LSE merge fused.  q, k, v: (b, h, s, d) bf16 in layout order
     (k and v may have hk heads, hk dividing h: query head i uses key / value head i // (h // hk)).
+    scores: a Scores, or None for plain ones.
 
     Returns (out (b, h, s, d) bf16, lse (b, h, s) fp32), both in layout order."""
-    lib = load()
-    b, h, s, d = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
-    tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
-    _check(lib.ring_attn_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), _layout(layout), int(n_shards),
-                             int(bool(causal)), _scale(softmax_scale, d), ctypes.byref(to), ctypes.byref(tl),
-                             None, 0, _stream(stream)), "ring_attn_fwd")
+    load()
+    with _place(scores, q, stream):
+        b, h, s, d = q.shape
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
+        tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
+        _call("fwd", scores, q.device, h, b, 7, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), _layout(layout),
+              int(n_shards), int(bool(causal)), _scale(softmax_scale, d), ctypes.byref(to), ctypes.byref(tl),
+              *((None, 0) if scores is None else ()), _stream(stream))
     return out, lse
 
 
 def ring_attn_fwd_step(q, k, v, step, layout="contiguous", n_shards=1, causal=False, softmax_scale=None,
-                       out_blk=None, lse_blk=None, out_dtype=torch.float32, stream=None):
+                       out_blk=None, lse_blk=None, out_dtype=torch.float32, stream=None, scores=None):
     """One ring step: every Q shard r against KV shard (r - step) mod N; block out and lse."""
-    lib = load()
-    b, h, s, d = q.shape
-    if out_blk is None:
-        out_blk = torch.empty((b, h, s, d), dtype=out_dtype, device=q.device)
-    if lse_blk is None:
-        lse_blk = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
-    tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out_blk), _t(lse_blk)
-    _check(lib.ring_attn_fwd_step(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), _layout(layout),
-                                  int(n_shards), int(bool(causal)), _scale(softmax_scale, d), int(step),
-                                  ctypes.byref(to), ctypes.byref(tl), _stream(stream)), "ring_attn_fwd_step")
+    load()
+    with _place(scores, q, stream):
+        b, h, s, d = q.shape
+        if out_blk is None:
+            out_blk = torch.empty((b, h, s, d), dtype=out_dtype, device=q.device)
+        if lse_blk is None:
+            lse_blk = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
+        tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out_blk), _t(lse_blk)
+        _call("fwd_step", scores, q.device, h, b, 7, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+              _layout(layout), int(n_shards), int(bool(causal)), _scale(softmax_scale, d), int(step),
+              ctypes.byref(to), ctypes.byref(tl), _stream(stream))
     return out_blk, lse_blk
 
 
@@ -244,21 +339,22 @@ def _ws_arg(workspace):
 
 
 def ring_attn_bwd(dout, q, k, v, out, lse, layout="contiguous", n_shards=1, causal=False, softmax_scale=None,
-                  dq=None, dk=None, dv=None, workspace=None, stream=None):
-    """Gradients (dq like q, dk and dv like k and v), bf16, layout order."""
-    lib = load()
-    b, h, s, d = q.shape
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    ws_bytes = ring_attn_workspace_size(RA_OP_BWD, b, h, s, d, n_shards)
-    if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
-    r = [ctypes.byref(x) for x in ts]
-    _check(lib.ring_attn_bwd(r[0], r[1], r[2], r[3], r[4], r[5], _layout(layout), int(n_shards), int(bool(causal)),
-                             _scale(softmax_scale, d), r[6], r[7], r[8], ctypes.c_void_p(workspace.data_ptr()),
-                             workspace.numel() * workspace.element_size(), _stream(stream)), "ring_attn_bwd")
+                  dq=None, dk=None, dv=None, workspace=None, stream=None, scores=None):
+    """Gradients (dq like q, dk and dv like k and v), bf16, layout order; scores as in the forward."""
+    load()
+    with _place(scores, q, stream):
+        b, h, s, d = q.shape
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        ws_bytes = ring_attn_workspace_size(RA_OP_BWD, b, h, s, d, n_shards)
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
+        r = [ctypes.byref(x) for x in ts]
+        _call("bwd", scores, q.device, h, b, 10, r[0], r[1], r[2], r[3], r[4], r[5], _layout(layout), int(n_shards),
+              int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8], ctypes.c_void_p(workspace.data_ptr()),
+              workspace.numel() * workspace.element_size(), _stream(stream))
     return dq, dk, dv
 
 
@@ -320,7 +416,7 @@ def _cu_pair(cu_seqlens, device):
 
 
 def ring_attn_varlen_fwd(q, k, v, cu_seqlens, max_seqlen=None, n_shards=1, causal=True, softmax_scale=None,
-                         out=None, lse=None, stream=None, layout="contiguous", workspace=None):
+                         out=None, lse=None, stream=None, layout="contiguous", workspace=None, scores=None):
     """Packed sequences, one cu_seqlens.  q, k, v: (total, h, d) or (h, total, d) bf16 in
     layout order ("contiguous" slices of the packed buffer, or "zigzag" per sequence);
     k and v may have fewer heads than q (grouped-query attention, as in ring_attn_fwd).
@@ -329,55 +425,53 @@ def ring_attn_varlen_fwd(q, k, v, cu_seqlens, max_seqlen=None, n_shards=1, causa
     zigzag, the original-order copies the library computes in); pass a tensor to
     reuse one (an empty tensor runs the zigzag kernels directly).
     Returns (out like q, lse (h, total) fp32)."""
-    lib = load()
-    host, dev = _cu_pair(cu_seqlens, q.device)
-    n = host.numel() - 1
-    total = int(host[-1])
-    if max_seqlen is None:
-        max_seqlen = _max_len(cu_seqlens, host)
-    h = q.shape[1] if q.shape[0] == total else q.shape[0]
-    d = q.shape[2]
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((h, total), dtype=torch.float32, device=q.device) if lse is None else lse
-    if workspace is None:
-        need = ring_attn_varlen_workspace_size(RA_OP_FWD, total, h, d, layout, n_shards)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    wp, wb = _ws_arg(workspace)
-    tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
-    _check(lib.ring_attn_varlen_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
-                                    ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n,
-                                    int(max_seqlen), _layout(layout), int(n_shards), int(bool(causal)),
-                                    _scale(softmax_scale, d), ctypes.byref(to), ctypes.byref(tl), wp, wb,
-                                    _stream(stream)),
-           "ring_attn_varlen_fwd")
+    load()
+    with _place(scores, q, stream):
+        host, dev = _cu_pair(cu_seqlens, q.device)
+        n = host.numel() - 1
+        total = int(host[-1])
+        if max_seqlen is None:
+            max_seqlen = _max_len(cu_seqlens, host)
+        h = q.shape[1] if q.shape[0] == total else q.shape[0]
+        d = q.shape[2]
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((h, total), dtype=torch.float32, device=q.device) if lse is None else lse
+        if workspace is None:
+            need = ring_attn_varlen_workspace_size(RA_OP_FWD, total, h, d, layout, n_shards)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        wp, wb = _ws_arg(workspace)
+        tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
+        _call("varlen_fwd", scores, q.device, h, n, 11, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+              ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen),
+              _layout(layout), int(n_shards), int(bool(causal)), _scale(softmax_scale, d), ctypes.byref(to),
+              ctypes.byref(tl), wp, wb, _stream(stream))
     return out, lse
 
 
 def ring_attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, max_seqlen=None, n_shards=1, causal=True,
                          softmax_scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None,
-                         layout="contiguous"):
-    lib = load()
-    host, dev = _cu_pair(cu_seqlens, q.device)
-    n = host.numel() - 1
-    total = int(host[-1])
-    if max_seqlen is None:
-        max_seqlen = _max_len(cu_seqlens, host)
-    h = q.shape[1] if q.shape[0] == total else q.shape[0]
-    d = q.shape[2]
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    if workspace is None:
-        ws_bytes = ring_attn_varlen_workspace_size(RA_OP_BWD, total, h, d, layout, n_shards)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
-    r = [ctypes.byref(x) for x in ts]
-    _check(lib.ring_attn_varlen_bwd(r[0], r[1], r[2], r[3], r[4], r[5], ctypes.c_void_p(dev.data_ptr()),
-                                    ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen), _layout(layout),
-                                    int(n_shards), int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8],
-                                    ctypes.c_void_p(workspace.data_ptr()),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)),
-           "ring_attn_varlen_bwd")
+                         layout="contiguous", scores=None):
+    load()
+    with _place(scores, q, stream):
+        host, dev = _cu_pair(cu_seqlens, q.device)
+        n = host.numel() - 1
+        total = int(host[-1])
+        if max_seqlen is None:
+            max_seqlen = _max_len(cu_seqlens, host)
+        h = q.shape[1] if q.shape[0] == total else q.shape[0]
+        d = q.shape[2]
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            ws_bytes = ring_attn_varlen_workspace_size(RA_OP_BWD, total, h, d, layout, n_shards)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
+        r = [ctypes.byref(x) for x in ts]
+        _call("varlen_bwd", scores, q.device, h, n, 14, r[0], r[1], r[2], r[3], r[4], r[5],
+              ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen),
+              _layout(layout), int(n_shards), int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8],
+              ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), _stream(stream))
     return dq, dk, dv
 
 
@@ -387,53 +481,52 @@ def _heads_of(x, rows):
 
 
 def ring_attn_llama3_varlen_fwd(q, k, v, cu_seqlens, rank, n_shards, causal=True, softmax_scale=None, max_seqlen=None,
-                                out=None, lse=None, stream=None):
+                                out=None, lse=None, stream=None, scores=None):
     """One rank of the llama3 form: q (L, h, d) or (h, L, d), the rank's contiguous slice of the
     packed buffer (L = total / n_shards); k, v: all total rows.  Returns (out like q, lse (h, L))."""
-    lib = load()
-    host, dev = _cu_pair(cu_seqlens, q.device)
-    n = host.numel() - 1
-    total = int(host[-1])
-    if max_seqlen is None:
-        max_seqlen = _max_len(cu_seqlens, host)
-    L = total // int(n_shards)
-    h, d = _heads_of(q, L), q.shape[2]
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((h, L), dtype=torch.float32, device=q.device) if lse is None else lse
-    t = [_t(x) for x in (q, k, v, out, lse)]
-    _check(lib.ring_attn_llama3_varlen_fwd(ctypes.byref(t[0]), ctypes.byref(t[1]), ctypes.byref(t[2]),
-                                           ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n,
-                                           int(max_seqlen), int(rank), int(n_shards), int(bool(causal)),
-                                           _scale(softmax_scale, d), ctypes.byref(t[3]), ctypes.byref(t[4]),
-                                           _stream(stream)), "ring_attn_llama3_varlen_fwd")
+    load()
+    with _place(scores, q, stream):
+        host, dev = _cu_pair(cu_seqlens, q.device)
+        n = host.numel() - 1
+        total = int(host[-1])
+        if max_seqlen is None:
+            max_seqlen = _max_len(cu_seqlens, host)
+        L = total // int(n_shards)
+        h, d = _heads_of(q, L), q.shape[2]
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((h, L), dtype=torch.float32, device=q.device) if lse is None else lse
+        t = [_t(x) for x in (q, k, v, out, lse)]
+        _call("llama3_varlen_fwd", scores, q.device, h, n, 11, ctypes.byref(t[0]), ctypes.byref(t[1]),
+              ctypes.byref(t[2]), ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n,
+              int(max_seqlen), int(rank), int(n_shards), int(bool(causal)), _scale(softmax_scale, d),
+              ctypes.byref(t[3]), ctypes.byref(t[4]), _stream(stream))
     return out, lse
 
 
 def ring_attn_llama3_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, rank, n_shards, causal=True, softmax_scale=None,
-                                max_seqlen=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+                                max_seqlen=None, dq=None, dk=None, dv=None, workspace=None, stream=None, scores=None):
     """Gradient of one rank of the llama3 form: (dq of the rank's rows, the rank's contributions to dk, dv)."""
-    lib = load()
-    host, dev = _cu_pair(cu_seqlens, q.device)
-    n = host.numel() - 1
-    total = int(host[-1])
-    if max_seqlen is None:
-        max_seqlen = _max_len(cu_seqlens, host)
-    L = total // int(n_shards)
-    h, d = _heads_of(q, L), q.shape[2]
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    ws_bytes = ring_attn_workspace_size(RA_OP_BWD, 1, h, L, d, 1)
-    if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
-    r = [ctypes.byref(x) for x in ts]
-    _check(lib.ring_attn_llama3_varlen_bwd(r[0], r[1], r[2], r[3], r[4], r[5], ctypes.c_void_p(dev.data_ptr()),
-                                           ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen), int(rank),
-                                           int(n_shards), int(bool(causal)), _scale(softmax_scale, d), r[6], r[7],
-                                           r[8], ctypes.c_void_p(workspace.data_ptr()),
-                                           workspace.numel() * workspace.element_size(), _stream(stream)),
-           "ring_attn_llama3_varlen_bwd")
+    load()
+    with _place(scores, q, stream):
+        host, dev = _cu_pair(cu_seqlens, q.device)
+        n = host.numel() - 1
+        total = int(host[-1])
+        if max_seqlen is None:
+            max_seqlen = _max_len(cu_seqlens, host)
+        L = total // int(n_shards)
+        h, d = _heads_of(q, L), q.shape[2]
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        ws_bytes = ring_attn_workspace_size(RA_OP_BWD, 1, h, L, d, 1)
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
+        r = [ctypes.byref(x) for x in ts]
+        _call("llama3_varlen_bwd", scores, q.device, h, n, 14, r[0], r[1], r[2], r[3], r[4], r[5],
+              ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen), int(rank),
+              int(n_shards), int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8],
+              ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), _stream(stream))
     return dq, dk, dv
 
 
@@ -453,86 +546,86 @@ def _bshd(x):
 
 
 def ring_attn_qkvpacked_fwd(qkv, layout="contiguous", n_shards=1, causal=False, softmax_scale=None, out=None,
-                            lse=None, stream=None):
+                            lse=None, stream=None, scores=None):
     """qkv: (b, s, 3, h, d) bf16.  Returns (out (b, s, h, d) bf16, lse (b, h, s) fp32)."""
     b, s, three, h, d = qkv.shape
     if three != 3:
         raise ValueError("qkv must be (b, s, 3, h, d)")
     out = torch.empty((b, s, h, d), dtype=qkv.dtype, device=qkv.device) if out is None else out
     _, lse = ring_attn_fwd(_bshd(qkv[:, :, 0]), _bshd(qkv[:, :, 1]), _bshd(qkv[:, :, 2]), layout, n_shards, causal,
-                           softmax_scale, out=_bshd(out), lse=lse, stream=stream)
+                           softmax_scale, out=_bshd(out), lse=lse, stream=stream, scores=scores)
     return out, lse
 
 
 def ring_attn_qkvpacked_bwd(dout, qkv, out, lse, layout="contiguous", n_shards=1, causal=False, softmax_scale=None,
-                            dqkv=None, workspace=None, stream=None):
+                            dqkv=None, workspace=None, stream=None, scores=None):
     """Gradient of ring_attn_qkvpacked_fwd: dqkv (b, s, 3, h, d) bf16."""
     dqkv = torch.empty_like(qkv) if dqkv is None else dqkv
     ring_attn_bwd(_bshd(dout), _bshd(qkv[:, :, 0]), _bshd(qkv[:, :, 1]), _bshd(qkv[:, :, 2]), _bshd(out), lse,
                   layout, n_shards, causal, softmax_scale, dq=_bshd(dqkv[:, :, 0]), dk=_bshd(dqkv[:, :, 1]),
-                  dv=_bshd(dqkv[:, :, 2]), workspace=workspace, stream=stream)
+                  dv=_bshd(dqkv[:, :, 2]), workspace=workspace, stream=stream, scores=scores)
     return dqkv
 
 
 def ring_attn_kvpacked_fwd(q, kv, layout="contiguous", n_shards=1, causal=False, softmax_scale=None, out=None,
-                           lse=None, stream=None):
+                           lse=None, stream=None, scores=None):
     """q: (b, s, h, d), kv: (b, s, 2, h, d) bf16.  Returns (out (b, s, h, d), lse (b, h, s))."""
     if kv.dim() != 5 or kv.shape[2] != 2:
         raise ValueError("kv must be (b, s, 2, h, d)")
     out = torch.empty_like(q) if out is None else out
     _, lse = ring_attn_fwd(_bshd(q), _bshd(kv[:, :, 0]), _bshd(kv[:, :, 1]), layout, n_shards, causal,
-                           softmax_scale, out=_bshd(out), lse=lse, stream=stream)
+                           softmax_scale, out=_bshd(out), lse=lse, stream=stream, scores=scores)
     return out, lse
 
 
 def ring_attn_kvpacked_bwd(dout, q, kv, out, lse, layout="contiguous", n_shards=1, causal=False, softmax_scale=None,
-                           dq=None, dkv=None, workspace=None, stream=None):
+                           dq=None, dkv=None, workspace=None, stream=None, scores=None):
     """Gradient of ring_attn_kvpacked_fwd: (dq (b, s, h, d), dkv (b, s, 2, h, d))."""
     dq = torch.empty_like(q) if dq is None else dq
     dkv = torch.empty_like(kv) if dkv is None else dkv
     ring_attn_bwd(_bshd(dout), _bshd(q), _bshd(kv[:, :, 0]), _bshd(kv[:, :, 1]), _bshd(out), lse, layout, n_shards,
                   causal, softmax_scale, dq=_bshd(dq), dk=_bshd(dkv[:, :, 0]), dv=_bshd(dkv[:, :, 1]),
-                  workspace=workspace, stream=stream)
+                  workspace=workspace, stream=stream, scores=scores)
     return dq, dkv
 
 
 def ring_attn_varlen_qkvpacked_fwd(qkv, cu_seqlens, max_seqlen=None, n_shards=1, causal=True, softmax_scale=None,
-                                   out=None, lse=None, stream=None, layout="contiguous"):
+                                   out=None, lse=None, stream=None, layout="contiguous", scores=None):
     """qkv: (total, 3, h, d) bf16.  Returns (out (total, h, d), lse (h, total))."""
     if qkv.dim() != 4 or qkv.shape[1] != 3:
         raise ValueError("qkv must be (total, 3, h, d)")
     out = torch.empty_like(qkv[:, 0]) if out is None else out
     return ring_attn_varlen_fwd(qkv[:, 0], qkv[:, 1], qkv[:, 2], cu_seqlens, max_seqlen, n_shards, causal,
-                                softmax_scale, out=out, lse=lse, stream=stream, layout=layout)
+                                softmax_scale, out=out, lse=lse, stream=stream, layout=layout, scores=scores)
 
 
 def ring_attn_varlen_qkvpacked_bwd(dout, qkv, out, lse, cu_seqlens, max_seqlen=None, n_shards=1, causal=True,
-                                   softmax_scale=None, dqkv=None, workspace=None, stream=None, layout="contiguous"):
+                                   softmax_scale=None, dqkv=None, workspace=None, stream=None, layout="contiguous", scores=None):
     """Gradient of ring_attn_varlen_qkvpacked_fwd: dqkv (total, 3, h, d)."""
     dqkv = torch.empty_like(qkv) if dqkv is None else dqkv
     ring_attn_varlen_bwd(dout, qkv[:, 0], qkv[:, 1], qkv[:, 2], out, lse, cu_seqlens, max_seqlen, n_shards, causal,
                          softmax_scale, dq=dqkv[:, 0], dk=dqkv[:, 1], dv=dqkv[:, 2], workspace=workspace,
-                         stream=stream, layout=layout)
+                         stream=stream, layout=layout, scores=scores)
     return dqkv
 
 
 def ring_attn_varlen_kvpacked_fwd(q, kv, cu_seqlens, max_seqlen=None, n_shards=1, causal=True, softmax_scale=None,
-                                  out=None, lse=None, stream=None, layout="contiguous"):
+                                  out=None, lse=None, stream=None, layout="contiguous", scores=None):
     """q: (total, h, d), kv: (total, 2, h, d).  Returns (out (total, h, d), lse (h, total))."""
     if kv.dim() != 4 or kv.shape[1] != 2:
         raise ValueError("kv must be (total, 2, h, d)")
     return ring_attn_varlen_fwd(q, kv[:, 0], kv[:, 1], cu_seqlens, max_seqlen, n_shards, causal, softmax_scale,
-                                out=out, lse=lse, stream=stream, layout=layout)
+                                out=out, lse=lse, stream=stream, layout=layout, scores=scores)
 
 
 def ring_attn_varlen_kvpacked_bwd(dout, q, kv, out, lse, cu_seqlens, max_seqlen=None, n_shards=1, causal=True,
                                   softmax_scale=None, dq=None, dkv=None, workspace=None, stream=None,
-                                  layout="contiguous"):
+                                  layout="contiguous", scores=None):
     """Gradient of ring_attn_varlen_kvpacked_fwd: (dq (total, h, d), dkv (total, 2, h, d))."""
     dq = torch.empty_like(q) if dq is None else dq
     dkv = torch.empty_like(kv) if dkv is None else dkv
     ring_attn_varlen_bwd(dout, q, kv[:, 0], kv[:, 1], out, lse, cu_seqlens, max_seqlen, n_shards, causal,
-                         softmax_scale, dq=dq, dk=dkv[:, 0], dv=dkv[:, 1], workspace=workspace, stream=stream,
+                         softmax_scale, dq=dq, dk=dkv[:, 0], dv=dkv[:, 1], workspace=workspace, stream=stream, scores=scores,
                          layout=layout)
     return dq, dkv
 
@@ -640,7 +733,7 @@ _EXT = None
 
 
 def _ext():
-    """The compiled marshaller of the cache calls, bound to the loaded library."""
+    """The compiled marshaller of the cache calls and the rotation, bound to the loaded library."""
     global _EXT
     if _EXT is None:
         lib = load()
@@ -651,8 +744,8 @@ def _ext():
         spec = importlib.util.spec_from_file_location("_ra_binding", path)
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
-        ext.use(*(ctypes.cast(getattr(lib, "ring_attn_cache_" + f), ctypes.c_void_p).value
-                  for f in ("append", "read", "fwd", "workspace_size")))
+        ext.use(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value
+                  for f in ("cache_append", "cache_read", "cache_fwd", "cache_workspace_size", "scored_cache_fwd", "rope")))
         _EXT = ext
     return _EXT
 
@@ -713,20 +806,59 @@ def ring_attn_cache_workspace(q, cache, cu_seqlens):
 
 
 def ring_attn_cache_fwd(q, cache, page_table, kv_lens, cu_seqlens, causal=True, softmax_scale=None, max_kv_len=0,
-                        out=None, lse=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+                        out=None, lse=None, out_dtype=torch.bfloat16, workspace=None, stream=None, scores=None):
     """Attention of new tokens over the paged 4-bit cache.
 
     q: (rows, h, d) bf16, rotated, h a multiple of the cache's heads; the new tokens are already in
     the cache (ring_attn_cache_append), the last ones of each sequence.  causal: a token sees the
     cache up to itself; else the whole sequence.  max_kv_len: an upper bound of kv_lens (0: what the
     page table can hold).  workspace: from ring_attn_cache_workspace, or None to allocate it.
+    scores: a Scores (prefix per sequence; distances between cache indices), or None.
     Returns (out (rows, h, d) bf16 or fp32, lse (h, rows) fp32); rows that see nothing get 0 and -inf."""
     if out is None and out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"unsupported dtype {out_dtype}")
     if softmax_scale is None and isinstance(cache, KVCache):
         softmax_scale = cache.scale
+    if scores is not None and not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores")
     return _cache_call("cache_fwd", cache, cu_seqlens, stream, q, page_table, kv_lens, causal, softmax_scale, max_kv_len,
-                       out, lse, out_dtype is torch.float32, workspace)[1:]
+                       out, lse, out_dtype is torch.float32, workspace, scores and scores._call)[1:]
+
+
+# ---------------------------------------------------------------------------- rotary positions
+def ring_attn_rope(q, k, rope, positions=None, axes=None, interleaved=False, layout="contiguous", n_shards=1, q_out=None,
+                   k_out=None, stream=None):
+    """Rotates q and k (or None) by their positions, on one axis or several.
+
+    q: (b, h, s, d), k: (b, hk, s, d), or both (rows, heads, d); bf16 or fp32.  rope: (cos, sin), each
+    (positions, r // 2) fp32; pairs (i, i + r / 2) of head dims turn, or (2 i, 2 i + 1) if interleaved.
+    positions: int32, (b, s) or (rows), or with a leading dimension of axes: pair f then goes by
+    the position on axis axes[f] (r // 2 numbers, as [0] * 16 + [1] * 24 + [2] * 24 for time, height and width).
+    None: the rows' original tokens, in the order of layout and n_shards.
+    q_out may be q and k_out k.  Returns (q_out, k_out)."""
+    return _rope_call(False, q, k, rope, positions, axes, interleaved, layout, n_shards, q_out, k_out, stream)
+
+
+def ring_attn_rope_bwd(dq, dk, rope, positions=None, axes=None, interleaved=False, layout="contiguous", n_shards=1,
+                       dq_out=None, dk_out=None, stream=None):
+    """Gradient of ring_attn_rope: those of the rotated q and k (or None) in, of the unrotated ones out."""
+    return _rope_call(True, dq, dk, rope, positions, axes, interleaved, layout, n_shards, dq_out, dk_out, stream)
+
+
+def _rope_call(inverse, q, k, rope, positions, axes, interleaved, layout, n_shards, q_out, k_out, stream):
+    f = (_EXT or _ext()).rope
+    args = (q, k, rope[0], rope[1], positions, None if axes is None else bytes(axes), interleaved, inverse,
+            _layout(layout), int(n_shards), q_out, k_out)
+    if stream is None:
+        r = f(*args)
+    else:
+        if isinstance(q, torch.Tensor) and stream.device != q.device:
+            raise ValueError(f"stream on {stream.device}, q on {q.device}")
+        with torch.cuda.stream(stream):
+            r = f(*args)
+    if r[0] != 0:
+        _check(r[0], "ring_attn_rope")
+    return r[1:]
 
 
 def ring_attn_check_device_error(stream=None):

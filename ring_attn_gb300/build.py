@@ -25,9 +25,12 @@ LIB = os.path.join(PKG, "libringattn.so")
 BUILD_DBG = os.path.join(PKG, "_build_dbg")
 LIB_DBG = os.path.join(PKG, "libringattn_dbg.so")
 SOURCES = ["ra_api.cu", "ra_fwd.cu", "ra_bwd.cu", "ra_dkdv_pair.cu", "ra_simple.cu", "ra_cache.cu", "ra_cache_attn.cu",
-           "ra_cache_chunk.cu"]
+           "ra_cache_chunk.cu", *(f"ra_scored_{way}_{what}.cu" for way in ("bwd", "fwd") for what in ("both", "cap", "bias", "prefix")),
+           *(f"ra_cache_chunk_{what}.cu" for what in ("both", "cap", "bias", "prefix")), "ra_cache_attn_scored.cu", "ra_rope.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("ra_device.cuh", "ra_internal.h", "ra_tiles.cuh", "ra_bwd_common.cuh",
-                                               "ra_cache_args.h", "ra_cache.cuh", "ra_cache_line.cuh")] + [
+                                               "ra_cache_args.h", "ra_cache.cuh", "ra_cache_line.cuh", "ra_cache_attn.cuh",
+                                               "ra_cache_chunk.cuh", "ra_fwd.cuh", "ra_bwd.cuh",
+                                               "ra_score.cuh", "ra_scored_fwd.cuh", "ra_scored_bwd.cuh")] + [
     os.path.join(ROOT, "include", "ringattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

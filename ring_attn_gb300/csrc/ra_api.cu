@@ -206,6 +206,71 @@ struct TimedLaunch {
     if (_s != RA_OK) return _s;      \
   } while (0)
 
+// What a call does to its scores; mode 0 (or none): nothing.
+struct Scored {
+  int mode;
+  ScoreParams p;
+};
+
+// unit: log2(e) times what a product is multiplied by (the cache's kernels do that themselves: 1).
+ScoreParams score_params(float softcap, const float* slopes, const int32_t* prefix, double unit) {
+  // tanh(u) = u (1 + w (a1 + w (a2 + w (a3 + w a4)))), w = u^2, |u| <= 0.6 (ra_score.cuh)
+  static const double a[5] = {1.0, -0.3333259750806283, 0.13313116663407254, -0.05221180687723626,
+                              0.015612632993333238};
+  ScoreParams p;
+  memset(&p, 0, sizeof(p));
+  p.slopes = slopes;
+  p.prefix = prefix;
+  p.c[0] = (float)unit;
+  if (softcap > 0.f) {
+    const double cap2 = softcap * 1.4426950408889634, k = unit / cap2;  // u = k s
+    double c = unit;
+    for (int i = 0; i < 5; ++i, c *= k * k) p.c[i] = (float)(c * a[i]);
+    p.cap2 = (float)cap2;
+    p.inv_cap2 = (float)(1.0 / cap2);
+    p.lim = (float)(0.6 / k);
+    p.e2 = (float)(2.0 * k * 1.4426950408889634);
+  }
+  return p;
+}
+
+ra_status check_scores(const ra_scores* x, float scale, int causal, double unit, Scored* out) {
+  out->mode = 0;
+  if (!x) return RA_ERR_INVALID_ARG;
+  if (!(x->softcap >= 0.f) || !isfinite(x->softcap)) return RA_ERR_INVALID_ARG;
+  if (x->prefix && !causal) return RA_ERR_INVALID_ARG;
+  if (!aligned(x->slopes, 4) || !aligned(x->prefix, 4)) return RA_ERR_ALIGNMENT;
+  // (the polynomial's coefficients stay in fp32's range)
+  if (x->softcap > 0.f && (x->softcap < 0x1p-10f || x->softcap > 0x1p20f || scale / x->softcap > 0x1p10f))
+    return RA_ERR_UNSUPPORTED;
+  if (x->softcap > 0.f || x->slopes || x->prefix)
+    out->mode = SC_ON | (x->softcap > 0.f ? SC_CAP : 0) | (x->slopes ? SC_BIAS : 0);
+  out->p = score_params(x->softcap, x->slopes, x->prefix, unit);
+  return RA_OK;
+}
+
+cudaError_t launch_fwd_any(const Scored* sc, int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const FwdParams& p, cudaStream_t st) {
+  switch (sc ? sc->mode : 0) {
+    case SC_ON: return launch_fwd_score<SC_ON>(D, tq, tk, tv, p, sc->p, st);
+    case SC_ON | SC_CAP: return launch_fwd_score<SC_ON | SC_CAP>(D, tq, tk, tv, p, sc->p, st);
+    case SC_ON | SC_BIAS: return launch_fwd_score<SC_ON | SC_BIAS>(D, tq, tk, tv, p, sc->p, st);
+    case SC_ON | SC_CAP | SC_BIAS: return launch_fwd_score<SC_ON | SC_CAP | SC_BIAS>(D, tq, tk, tv, p, sc->p, st);
+    default: return launch_fwd(D, tq, tk, tv, p, st);
+  }
+}
+cudaError_t launch_bwd_any(const Scored* sc, int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const CUtensorMap& tdo, const BwdParams& p, int which, cudaStream_t st) {
+  switch (sc ? sc->mode : 0) {
+    case SC_ON: return launch_bwd_score<SC_ON>(D, tq, tk, tv, tdo, p, sc->p, which, st);
+    case SC_ON | SC_CAP: return launch_bwd_score<SC_ON | SC_CAP>(D, tq, tk, tv, tdo, p, sc->p, which, st);
+    case SC_ON | SC_BIAS: return launch_bwd_score<SC_ON | SC_BIAS>(D, tq, tk, tv, tdo, p, sc->p, which, st);
+    case SC_ON | SC_CAP | SC_BIAS:
+      return launch_bwd_score<SC_ON | SC_CAP | SC_BIAS>(D, tq, tk, tv, tdo, p, sc->p, which, st);
+    default: return launch_bwd(D, tq, tk, tv, tdo, p, which, st);
+  }
+}
+
 // Shared forward: fused ring (step < 0) or one ring step.
 // The argument checks of every backward entry point, made before anything
 // touches the device or the workspace.
@@ -230,7 +295,7 @@ ra_status bwd_check_args(const Bhsd& dout, const Bhsd& q, const Bhsd& k, const B
 ra_status fwd_common(const Bhsd& q, const Bhsd& k, const Bhsd& v, int32_t layout, int32_t n_shards, int32_t causal,
                      float scale, int32_t step, const Bhsd& o, int out_f32, float* lse, long long lsb, long long lsh,
                      long long lss, const int32_t* cu_dev, int32_t n_seqs, void* stream, int32_t rank = -1,
-                     const int* row_map = nullptr) {
+                     const int* row_map = nullptr, const Scored* sc = nullptr) {
   if (!same_shape(k, v) || !same_shape(q, o)) return RA_ERR_INVALID_ARG;
   if (rank < 0 && !kv_matches_q(q, k, 1)) return RA_ERR_INVALID_ARG;
   if (rank >= 0 && (rank >= n_shards || !kv_matches_q(q, k, n_shards))) return RA_ERR_INVALID_ARG;
@@ -276,7 +341,7 @@ ra_status fwd_common(const Bhsd& q, const Bhsd& k, const Bhsd& v, int32_t layout
   RA_TRY(make_tmap(k, &tk));
   RA_TRY(make_tmap(v, &tv));
   TimedLaunch tl(RA_KERNEL_FWD, static_cast<cudaStream_t>(stream));
-  return cuda_status(launch_fwd((int)q.d, tq, tk, tv, p, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_fwd_any(sc, (int)q.d, tq, tk, tv, p, static_cast<cudaStream_t>(stream)));
 }
 
 // Workspace: -D and -lse2, each laid out per shard with rows padded to a
@@ -297,7 +362,7 @@ ra_status bwd_common(const Bhsd& dout, const Bhsd& q, const Bhsd& k, const Bhsd&
                      const float* lse, long long lsb, long long lsh, long long lss, int32_t layout, int32_t n_shards,
                      int32_t causal, float scale, const Bhsd& dq, const Bhsd& dk, const Bhsd& dv, void* ws,
                      size_t ws_bytes, const int32_t* cu_dev, int32_t n_seqs, void* stream, int32_t rank = -1,
-                     const int* row_map = nullptr) {
+                     const int* row_map = nullptr, const Scored* sc = nullptr) {
   RA_TRY(bwd_check_args(dout, q, k, v, out, layout, n_shards, causal, scale, dq, dk, dv, rank));
   const int stat_N = rank >= 0 ? 1 : n_shards;  // shards whose rows the statistics hold
   if (!ws || !aligned(ws, 256) || ws_bytes < bwd_ws_bytes(q.b, q.h, q.s, stat_N)) return RA_ERR_WORKSPACE;
@@ -361,7 +426,7 @@ ra_status bwd_common(const Bhsd& dout, const Bhsd& q, const Bhsd& k, const Bhsd&
     RA_TRY(cuda_status(
         launch_bwd_pre(vdo, vo, LseView{lse, lsb, lsh, lss}, nD, nlse2, stat_N, stat_L, p.ctl, row_map, st)));
   }
-  if (q.d == 128 && q.h == k.h && __atomic_load_n(&g_dkdv_pair, __ATOMIC_RELAXED)) {
+  if (q.d == 128 && q.h == k.h && !(sc && sc->mode) && __atomic_load_n(&g_dkdv_pair, __ATOMIC_RELAXED)) {
     CUtensorMap pq, pk, pv, pdo;  // 64-row boxes: the pair kernel loads 64 x 64 blocks
     RA_TRY(make_tmap(q, &pq, 64));
     RA_TRY(make_tmap(k, &pk, 64));
@@ -371,10 +436,10 @@ ra_status bwd_common(const Bhsd& dout, const Bhsd& q, const Bhsd& k, const Bhsd&
     RA_TRY(cuda_status(launch_dkdv_pair(pq, pk, pv, pdo, p, st)));
   } else {
     TimedLaunch tl(RA_KERNEL_BWD, st);
-    RA_TRY(cuda_status(launch_bwd((int)q.d, tq, tk, tv, tdo, p, 0, st)));
+    RA_TRY(cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 0, st)));
   }
   TimedLaunch tl(RA_KERNEL_BWD_DQ, st);
-  return cuda_status(launch_bwd((int)q.d, tq, tk, tv, tdo, p, 1, st));
+  return cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 1, st));
 }
 
 // Scratch of ring_attn_bwd_static_scratch: one array per device, its device
@@ -514,11 +579,26 @@ ra_status static_scratch(void** out) {
 
 extern "C" {
 
-ra_status ring_attn_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
-                        int32_t n_shards, int32_t causal, float softmax_scale, ra_tensor* out, ra_tensor* lse,
-                        void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
+// The calls below and their ring_attn_scored_ forms: `scored` says which, so that a scored call
+// without scores is refused.
+struct ScoreArg {
+  bool scored;
+  const ra_scores* x;
+};
+// The call's changes to its scores, once softmax_scale and causal have been checked (sc->mode 0: none).
+static ra_status take_scores(const ScoreArg& a, float softmax_scale, int32_t causal, Scored* sc) {
+  sc->mode = 0;
+  if (!a.scored) return RA_OK;
+  RA_TRY(check_scale(softmax_scale));
+  if (causal != 0 && causal != 1) return RA_ERR_INVALID_ARG;
+  return check_scores(a.x, softmax_scale, causal, softmax_scale * 1.4426950408889634, sc);
+}
+static const ScoreArg kPlain = {false, nullptr};
+static ScoreArg scored(const ra_scores* x) { return ScoreArg{true, x}; }
+
+static ra_status any_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout, int32_t n_shards,
+                         int32_t causal, float softmax_scale, ra_tensor* out, ra_tensor* lse, void* stream,
+                         const ScoreArg& scores) {
   Bhsd vq, vk, vv, vo;
   RA_TRY(check_bhsd(q, &vq));
   RA_TRY(check_bhsd(k, &vk));
@@ -526,13 +606,27 @@ ra_status ring_attn_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor*
   RA_TRY(check_bhsd(out, &vo));
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse, vq.b, vq.h, vq.s, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   return fwd_common(vq, vk, vv, layout, n_shards, causal, softmax_scale, -1, vo, 0, static_cast<float*>(lse->data),
-                    lsb, lsh, lss, nullptr, 0, stream);
+                    lsb, lsh, lss, nullptr, 0, stream, -1, nullptr, &sc);
+}
+ra_status ring_attn_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                        int32_t n_shards, int32_t causal, float softmax_scale, ra_tensor* out, ra_tensor* lse,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  return any_fwd(q, k, v, layout, n_shards, causal, softmax_scale, out, lse, stream, kPlain);
+}
+ra_status ring_attn_scored_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                               int32_t n_shards, int32_t causal, float softmax_scale, const ra_scores* scores,
+                               ra_tensor* out, ra_tensor* lse, void* stream) {
+  return any_fwd(q, k, v, layout, n_shards, causal, softmax_scale, out, lse, stream, scored(scores));
 }
 
-ra_status ring_attn_fwd_step(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
-                             int32_t n_shards, int32_t causal, float softmax_scale, int32_t step,
-                             ra_tensor* out_blk, ra_tensor* lse_blk, void* stream) {
+static ra_status any_fwd_step(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                              int32_t n_shards, int32_t causal, float softmax_scale, int32_t step, ra_tensor* out_blk,
+                              ra_tensor* lse_blk, void* stream, const ScoreArg& scores) {
   Bhsd vq, vk, vv;
   RA_TRY(check_bhsd(q, &vq));
   RA_TRY(check_bhsd(k, &vk));
@@ -546,8 +640,20 @@ ra_status ring_attn_fwd_step(const ra_tensor* q, const ra_tensor* k, const ra_te
           out_blk->stride[0], out_blk->stride[1], out_blk->stride[2]};
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse_blk, vq.b, vq.h, vq.s, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   return fwd_common(vq, vk, vv, layout, n_shards, causal, softmax_scale, step, vo, f32,
-                    static_cast<float*>(lse_blk->data), lsb, lsh, lss, nullptr, 0, stream);
+                    static_cast<float*>(lse_blk->data), lsb, lsh, lss, nullptr, 0, stream, -1, nullptr, &sc);
+}
+ra_status ring_attn_fwd_step(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                             int32_t n_shards, int32_t causal, float softmax_scale, int32_t step,
+                             ra_tensor* out_blk, ra_tensor* lse_blk, void* stream) {
+  return any_fwd_step(q, k, v, layout, n_shards, causal, softmax_scale, step, out_blk, lse_blk, stream, kPlain);
+}
+ra_status ring_attn_scored_fwd_step(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v, int32_t layout,
+                                    int32_t n_shards, int32_t causal, float softmax_scale, const ra_scores* scores,
+                                    int32_t step, ra_tensor* out_blk, ra_tensor* lse_blk, void* stream) {
+  return any_fwd_step(q, k, v, layout, n_shards, causal, softmax_scale, step, out_blk, lse_blk, stream, scored(scores));
 }
 
 ra_status lse_merge(ra_tensor* out_acc, ra_tensor* lse_acc, const ra_tensor* out_blk, const ra_tensor* lse_blk,
@@ -644,10 +750,10 @@ ra_status lse_merge(ra_tensor* out_acc, ra_tensor* lse_acc, const ra_tensor* out
   return cuda_status(launch_lse_merge(a, static_cast<cudaStream_t>(stream)));
 }
 
-ra_status ring_attn_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
-                        const ra_tensor* out, const ra_tensor* lse, int32_t layout, int32_t n_shards,
-                        int32_t causal, float softmax_scale, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
-                        void* workspace, size_t workspace_bytes, void* stream) {
+static ra_status any_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                         const ra_tensor* out, const ra_tensor* lse, int32_t layout, int32_t n_shards, int32_t causal,
+                         float softmax_scale, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv, void* workspace,
+                         size_t workspace_bytes, void* stream, const ScoreArg& scores) {
   Bhsd vdo, vq, vk, vv, vo, vdq, vdk, vdv;
   RA_TRY(check_bhsd(dout, &vdo));
   RA_TRY(check_bhsd(q, &vq));
@@ -659,8 +765,25 @@ ra_status ring_attn_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tens
   RA_TRY(check_bhsd(dv, &vdv));
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse, vq.b, vq.h, vq.s, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   return bwd_common(vdo, vq, vk, vv, vo, static_cast<const float*>(lse->data), lsb, lsh, lss, layout, n_shards,
-                    causal, softmax_scale, vdq, vdk, vdv, workspace, workspace_bytes, nullptr, 0, stream);
+                    causal, softmax_scale, vdq, vdk, vdv, workspace, workspace_bytes, nullptr, 0, stream, -1,
+                    nullptr, &sc);
+}
+ra_status ring_attn_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                        const ra_tensor* out, const ra_tensor* lse, int32_t layout, int32_t n_shards,
+                        int32_t causal, float softmax_scale, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return any_bwd(dout, q, k, v, out, lse, layout, n_shards, causal, softmax_scale, dq, dk, dv, workspace,
+                 workspace_bytes, stream, kPlain);
+}
+ra_status ring_attn_scored_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                               const ra_tensor* out, const ra_tensor* lse, int32_t layout, int32_t n_shards,
+                               int32_t causal, float softmax_scale, const ra_scores* scores, ra_tensor* dq,
+                               ra_tensor* dk, ra_tensor* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  return any_bwd(dout, q, k, v, out, lse, layout, n_shards, causal, softmax_scale, dq, dk, dv, workspace,
+                 workspace_bytes, stream, scored(scores));
 }
 
 ra_status ring_attn_bwd_static_scratch(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
@@ -688,11 +811,11 @@ ra_status ring_attn_bwd_static_scratch(const ra_tensor* dout, const ra_tensor* q
                     causal, softmax_scale, vdq, vdk, vdv, scratch, RA_STATIC_SCRATCH_BYTES, nullptr, 0, stream);
 }
 
-ra_status ring_attn_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
-                               const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
-                               int32_t max_seqlen, int32_t layout, int32_t n_shards, int32_t causal,
-                               float softmax_scale, ra_tensor* out, ra_tensor* lse, void* workspace,
-                               size_t workspace_bytes, void* stream) {
+static ra_status any_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                int32_t max_seqlen, int32_t layout, int32_t n_shards, int32_t causal,
+                                float softmax_scale, ra_tensor* out, ra_tensor* lse, void* workspace,
+                                size_t workspace_bytes, void* stream, const ScoreArg& scores) {
   long long total = 0;
   RA_TRY(check_cu(cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, &total));
   RA_TRY(check_varlen_layout(layout, n_shards, cu_seqlens_host, n_seqs));
@@ -703,6 +826,8 @@ ra_status ring_attn_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_
   RA_TRY(check_thd(out, total, &vo));
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse, 1, vq.h, total, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   if (layout == RA_LAYOUT_ZIGZAG && workspace && workspace_bytes >= zz_fwd_bytes(total, vq.h, vq.d)) {
     // original-order path: the same checks as the kernels' before any launch
     if (!kv_matches_q(vq, vk, 1) || !same_shape(vk, vv) || !same_shape(vq, vo)) return RA_ERR_INVALID_ARG;
@@ -722,17 +847,34 @@ ra_status ring_attn_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_
     RA_TRY(zz_in(z, vk, k2.data));
     RA_TRY(zz_in(z, vv, v2.data));
     return fwd_common(q2, k2, v2, RA_LAYOUT_CONTIGUOUS, n_shards, causal, softmax_scale, -1, vo, 0,
-                      static_cast<float*>(lse->data), lsb, lsh, lss, cu_seqlens_dev, n_seqs, stream, -1, z.inv);
+                      static_cast<float*>(lse->data), lsb, lsh, lss, cu_seqlens_dev, n_seqs, stream, -1, z.inv, &sc);
   }
   return fwd_common(vq, vk, vv, layout, n_shards, causal, softmax_scale, -1, vo, 0,
-                    static_cast<float*>(lse->data), lsb, lsh, lss, cu_seqlens_dev, n_seqs, stream);
+                    static_cast<float*>(lse->data), lsb, lsh, lss, cu_seqlens_dev, n_seqs, stream, -1, nullptr, &sc);
+}
+ra_status ring_attn_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                               const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                               int32_t max_seqlen, int32_t layout, int32_t n_shards, int32_t causal,
+                               float softmax_scale, ra_tensor* out, ra_tensor* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return any_varlen_fwd(q, k, v, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, layout, n_shards, causal,
+                        softmax_scale, out, lse, workspace, workspace_bytes, stream, kPlain);
+}
+ra_status ring_attn_scored_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                      const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                      int32_t max_seqlen, int32_t layout, int32_t n_shards, int32_t causal,
+                                      float softmax_scale, const ra_scores* scores, ra_tensor* out, ra_tensor* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  return any_varlen_fwd(q, k, v, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, layout, n_shards, causal,
+                        softmax_scale, out, lse, workspace, workspace_bytes, stream, scored(scores));
 }
 
-ra_status ring_attn_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
-                               const ra_tensor* out, const ra_tensor* lse, const int32_t* cu_seqlens_dev,
-                               const int32_t* cu_seqlens_host, int32_t n_seqs, int32_t max_seqlen,
-                               int32_t layout, int32_t n_shards, int32_t causal, float softmax_scale, ra_tensor* dq,
-                               ra_tensor* dk, ra_tensor* dv, void* workspace, size_t workspace_bytes, void* stream) {
+static ra_status any_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                const ra_tensor* out, const ra_tensor* lse, const int32_t* cu_seqlens_dev,
+                                const int32_t* cu_seqlens_host, int32_t n_seqs, int32_t max_seqlen, int32_t layout,
+                                int32_t n_shards, int32_t causal, float softmax_scale, ra_tensor* dq, ra_tensor* dk,
+                                ra_tensor* dv, void* workspace, size_t workspace_bytes, void* stream,
+                                const ScoreArg& scores) {
   long long total = 0;
   RA_TRY(check_cu(cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, &total));
   RA_TRY(check_varlen_layout(layout, n_shards, cu_seqlens_host, n_seqs));
@@ -747,6 +889,8 @@ ra_status ring_attn_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const 
   RA_TRY(check_thd(dv, total, &vdv));
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse, 1, vq.h, total, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   if (layout == RA_LAYOUT_ZIGZAG && workspace && workspace_bytes >= zz_bwd_bytes(total, vq.h, vq.d, n_shards)) {
     // original-order path: the same checks as the kernels' before any launch
     RA_TRY(bwd_check_args(vdo, vq, vk, vv, vo, layout, n_shards, causal, softmax_scale, vdq, vdk, vdv, -1));
@@ -768,11 +912,28 @@ ra_status ring_attn_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const 
     // them through the inverse map
     return bwd_common(do2, q2, k2, v2, vo, static_cast<const float*>(lse->data), lsb, lsh, lss, RA_LAYOUT_CONTIGUOUS,
                       n_shards, causal, softmax_scale, vdq, vdk, vdv, workspace, SB, cu_seqlens_dev, n_seqs, stream, -1,
-                      z.inv);
+                      z.inv, &sc);
   }
   return bwd_common(vdo, vq, vk, vv, vo, static_cast<const float*>(lse->data), lsb, lsh, lss, layout, n_shards,
                     causal, softmax_scale, vdq, vdk, vdv, workspace, workspace_bytes, cu_seqlens_dev, n_seqs,
-                    stream);
+                    stream, -1, nullptr, &sc);
+}
+ra_status ring_attn_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                               const ra_tensor* out, const ra_tensor* lse, const int32_t* cu_seqlens_dev,
+                               const int32_t* cu_seqlens_host, int32_t n_seqs, int32_t max_seqlen,
+                               int32_t layout, int32_t n_shards, int32_t causal, float softmax_scale, ra_tensor* dq,
+                               ra_tensor* dk, ra_tensor* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  return any_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, layout, n_shards,
+                        causal, softmax_scale, dq, dk, dv, workspace, workspace_bytes, stream, kPlain);
+}
+ra_status ring_attn_scored_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                      const ra_tensor* out, const ra_tensor* lse, const int32_t* cu_seqlens_dev,
+                                      const int32_t* cu_seqlens_host, int32_t n_seqs, int32_t max_seqlen,
+                                      int32_t layout, int32_t n_shards, int32_t causal, float softmax_scale,
+                                      const ra_scores* scores, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  return any_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, layout, n_shards,
+                        causal, softmax_scale, dq, dk, dv, workspace, workspace_bytes, stream, scored(scores));
 }
 
 // One rank of the llama3 form: shapes of the local (L rows) and full (total rows) tensors.
@@ -784,10 +945,11 @@ static ra_status llama3_shapes(const int32_t* cu_dev, const int32_t* cu_host, in
   return RA_OK;
 }
 
-ra_status ring_attn_llama3_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
-                                      const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
-                                      int32_t max_seqlen, int32_t rank, int32_t n_shards, int32_t causal,
-                                      float softmax_scale, ra_tensor* out, ra_tensor* lse, void* stream) {
+static ra_status any_llama3_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                       const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                       int32_t max_seqlen, int32_t rank, int32_t n_shards, int32_t causal,
+                                       float softmax_scale, ra_tensor* out, ra_tensor* lse, void* stream,
+                                       const ScoreArg& scores) {
   long long total = 0, L = 0;
   RA_TRY(llama3_shapes(cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, rank, n_shards, &total, &L));
   Bhsd vq, vk, vv, vo;
@@ -797,16 +959,33 @@ ra_status ring_attn_llama3_varlen_fwd(const ra_tensor* q, const ra_tensor* k, co
   RA_TRY(check_thd(out, L, &vo));
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse, 1, vq.h, L, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   return fwd_common(vq, vk, vv, RA_LAYOUT_CONTIGUOUS, n_shards, causal, softmax_scale, -1, vo, 0,
-                    static_cast<float*>(lse->data), lsb, lsh, lss, cu_seqlens_dev, n_seqs, stream, rank);
+                    static_cast<float*>(lse->data), lsb, lsh, lss, cu_seqlens_dev, n_seqs, stream, rank, nullptr, &sc);
 }
-
-ra_status ring_attn_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
-                                      const ra_tensor* v, const ra_tensor* out, const ra_tensor* lse,
+ra_status ring_attn_llama3_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
                                       const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
                                       int32_t max_seqlen, int32_t rank, int32_t n_shards, int32_t causal,
-                                      float softmax_scale, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
-                                      void* workspace, size_t workspace_bytes, void* stream) {
+                                      float softmax_scale, ra_tensor* out, ra_tensor* lse, void* stream) {
+  return any_llama3_varlen_fwd(q, k, v, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, rank, n_shards, causal,
+                               softmax_scale, out, lse, stream, kPlain);
+}
+ra_status ring_attn_scored_llama3_varlen_fwd(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
+                                             const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
+                                             int32_t n_seqs, int32_t max_seqlen, int32_t rank, int32_t n_shards,
+                                             int32_t causal, float softmax_scale, const ra_scores* scores,
+                                             ra_tensor* out, ra_tensor* lse, void* stream) {
+  return any_llama3_varlen_fwd(q, k, v, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, rank, n_shards, causal,
+                               softmax_scale, out, lse, stream, scored(scores));
+}
+
+static ra_status any_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
+                                       const ra_tensor* v, const ra_tensor* out, const ra_tensor* lse,
+                                       const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                       int32_t max_seqlen, int32_t rank, int32_t n_shards, int32_t causal,
+                                       float softmax_scale, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
+                                       void* workspace, size_t workspace_bytes, void* stream, const ScoreArg& scores) {
   long long total = 0, L = 0;
   RA_TRY(llama3_shapes(cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, rank, n_shards, &total, &L));
   Bhsd vdo, vq, vk, vv, vo, vdq, vdk, vdv;
@@ -820,9 +999,31 @@ ra_status ring_attn_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q,
   RA_TRY(check_thd(dv, total, &vdv));
   long long lsb, lsh, lss;
   RA_TRY(check_lse(lse, 1, vq.h, L, &lsb, &lsh, &lss));
+  Scored sc;
+  RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
   return bwd_common(vdo, vq, vk, vv, vo, static_cast<const float*>(lse->data), lsb, lsh, lss, RA_LAYOUT_CONTIGUOUS,
                     n_shards, causal, softmax_scale, vdq, vdk, vdv, workspace, workspace_bytes, cu_seqlens_dev, n_seqs,
-                    stream, rank);
+                    stream, rank, nullptr, &sc);
+}
+ra_status ring_attn_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
+                                      const ra_tensor* v, const ra_tensor* out, const ra_tensor* lse,
+                                      const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                      int32_t max_seqlen, int32_t rank, int32_t n_shards, int32_t causal,
+                                      float softmax_scale, ra_tensor* dq, ra_tensor* dk, ra_tensor* dv,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  return any_llama3_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, rank,
+                               n_shards, causal, softmax_scale, dq, dk, dv, workspace, workspace_bytes, stream, kPlain);
+}
+ra_status ring_attn_scored_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
+                                             const ra_tensor* v, const ra_tensor* out, const ra_tensor* lse,
+                                             const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
+                                             int32_t n_seqs, int32_t max_seqlen, int32_t rank, int32_t n_shards,
+                                             int32_t causal, float softmax_scale, const ra_scores* scores,
+                                             ra_tensor* dq, ra_tensor* dk, ra_tensor* dv, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  return any_llama3_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens_dev, cu_seqlens_host, n_seqs, max_seqlen, rank,
+                               n_shards, causal, softmax_scale, dq, dk, dv, workspace, workspace_bytes, stream,
+                               scored(scores));
 }
 
 // Byte span [first, last] that a tensor's strides can reach (negative strides
@@ -1057,6 +1258,89 @@ static bool same_view(const ra_tensor* a, const ra_tensor* b) {
   return true;
 }
 
+// A (b, h, s, d) tensor of rows to be turned; es: element size.
+static ra_status check_rope_rows(const ra_tensor* t, const ra_tensor* like, RopeRows* v, int es) {
+  if (!t || !t->data || t->ndim != 4 || t->dtype != like->dtype) return RA_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (t->shape[i] < 1 || t->shape[i] != like->shape[i]) return RA_ERR_INVALID_ARG;
+  if (t->stride[3] != 1 || !aligned(t->data, 16)) return RA_ERR_ALIGNMENT;
+  long long st[3];
+  for (int i = 0; i < 3; ++i) {  // (the stride of a dimension of size 1 is not used)
+    if (t->shape[i] > 1 && (t->stride[i] <= 0 || t->stride[i] % (16 / es) != 0)) return RA_ERR_ALIGNMENT;
+    st[i] = t->shape[i] > 1 ? t->stride[i] : 0;
+  }
+  *v = RopeRows{t->data, st[0], st[1], st[2]};
+  return RA_OK;
+}
+
+ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor* rope_cos, const ra_tensor* rope_sin,
+                         int32_t rope, const ra_rope_positions* positions, int32_t layout, int32_t n_shards,
+                         int32_t inverse, ra_tensor* q_out, ra_tensor* k_out, void* stream) {
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  if (!q || !q_out || (k != nullptr) != (k_out != nullptr)) return RA_ERR_INVALID_ARG;
+  if (q->dtype != RA_BF16 && q->dtype != RA_FP32) return RA_ERR_INVALID_ARG;
+  const int es = q->dtype == RA_FP32 ? 4 : 2;
+  RA_TRY(check_rope_rows(q, q, &a.in[0], es));
+  RA_TRY(check_rope_rows(q_out, q, &a.out[0], es));
+  const long long b = q->shape[0], h = q->shape[1], s = q->shape[2], d = q->shape[3];
+  long long hk = 0;
+  if (k) {
+    if (k->dtype != q->dtype) return RA_ERR_INVALID_ARG;
+    RA_TRY(check_rope_rows(k, k, &a.in[1], es));
+    RA_TRY(check_rope_rows(k_out, k, &a.out[1], es));
+    hk = k->shape[1];
+    if (k->shape[0] != b || k->shape[2] != s || k->shape[3] != d) return RA_ERR_INVALID_ARG;
+  }
+  if (d != 64 && d != 128) return RA_ERR_UNSUPPORTED;
+  RA_TRY(check_layout(layout, n_shards, s));
+  if (s > (1LL << 30) || b > (1LL << 30) || b * s > (1LL << 40) || h > 65535 || hk > 65535) return RA_ERR_UNSUPPORTED;
+  if (rope != RA_ROPE_HALVES && rope != RA_ROPE_INTERLEAVED) return RA_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return RA_ERR_INVALID_ARG;
+  if (!rope_cos || rope_cos->ndim != 2 || rope_cos->shape[1] < 1 || 2 * rope_cos->shape[1] > d ||
+      (rope_cos->shape[1] != 8 && rope_cos->shape[1] % 16 != 0) || rope_cos->shape[0] > INT32_MAX)
+    return RA_ERR_INVALID_ARG;
+  RA_TRY(check_rope_table(rope_cos, rope_cos, &a.cos_t, &a.cos_stride));
+  RA_TRY(check_rope_table(rope_sin, rope_cos, &a.sin_t, &a.sin_stride));
+  const int pairs = (int)rope_cos->shape[1];
+  if (positions) {
+    if (!positions->positions || positions->n_axes < 1 || positions->n_axes > 255) return RA_ERR_INVALID_ARG;
+    if (!aligned(positions->positions, 4)) return RA_ERR_ALIGNMENT;
+    if (!positions->pair_axis && positions->n_axes != 1) return RA_ERR_INVALID_ARG;
+    for (int i = 0; positions->pair_axis && i < pairs; ++i) {
+      if (positions->pair_axis[i] >= positions->n_axes) return RA_ERR_INVALID_ARG;
+      a.axis[i] = positions->pair_axis[i];
+    }
+    a.pos = positions->positions;
+    a.p_axis = positions->stride_axis;
+    a.p_b = positions->stride_b;
+    a.p_s = positions->stride_s;
+  }
+  for (int i = 0; i < pairs; ++i)
+    if (a.axis[i] != a.axis[i & ~3]) a.mixed |= 1u << (i >> 2);
+  // every row is read and written by the same lanes, so in place is fine, but nothing else that others have yet
+  // to read may be written
+  if ((!same_view(q, q_out) && may_share(q, es, q_out, es)) ||
+      (k && ((!same_view(k, k_out) && may_share(k, es, k_out, es)) || may_share(q, es, k_out, es) ||
+             may_share(k, es, q_out, es) || may_share(q_out, es, k_out, es))))
+    return RA_ERR_INVALID_ARG;
+  a.h[0] = (int)h;
+  a.h[1] = (int)hk;
+  a.b = (int)b;
+  a.s = (int)s;
+  a.d = (int)d;
+  a.f32 = es == 4;
+  a.rot = 2 * pairs;
+  a.style = rope;
+  a.inverse = inverse;
+  a.max_pos = (int)rope_cos->shape[0];
+  a.layout = layout;
+  a.N = n_shards;
+  RA_TRY(dev_ctl(&a.ctl));
+  TimedLaunch tl(RA_KERNEL_ROPE, static_cast<cudaStream_t>(stream));
+  return cuda_status(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
 ra_status ring_attn_cache_append(const ra_tensor* q, const ra_tensor* k, const ra_tensor* v,
                                  const ra_tensor* rope_cos, const ra_tensor* rope_sin, int32_t rope,
                                  const int32_t* positions, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
@@ -1120,9 +1404,9 @@ ra_status ring_attn_cache_read(const ra_kv_cache* cache, const ra_kv_seqs* seqs,
   return cuda_status(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
 }
 
-ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs, int32_t causal,
-                              float softmax_scale, int32_t max_kv_len, ra_tensor* out, ra_tensor* lse,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+static ra_status any_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs, int32_t causal,
+                               float softmax_scale, int32_t max_kv_len, ra_tensor* out, ra_tensor* lse,
+                               void* workspace, size_t workspace_bytes, void* stream, const ScoreArg& scores) {
   CacheAttnArgs a;
   memset(&a, 0, sizeof(a));
   long long d = 0;
@@ -1148,6 +1432,12 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   a.l_ss = lse->stride[1];
   if (causal != 0 && causal != 1) return RA_ERR_INVALID_ARG;
   RA_TRY(check_scale(softmax_scale));
+  if (scores.scored) {
+    Scored sc;
+    RA_TRY(check_scores(scores.x, softmax_scale, causal, 1.0, &sc));
+    a.mode = sc.mode;
+    a.sc = sc.p;
+  }
   if (max_kv_len < 0) return RA_ERR_INVALID_ARG;
   a.causal = causal;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -1169,6 +1459,19 @@ ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, cons
   if (!p.joins) return RA_OK;
   TimedLaunch tl(RA_KERNEL_CACHE_JOIN, st);
   return cuda_status(launch_cache_join(p, st));
+}
+ra_status ring_attn_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs, int32_t causal,
+                              float softmax_scale, int32_t max_kv_len, ra_tensor* out, ra_tensor* lse,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  return any_cache_fwd(q, cache, seqs, causal, softmax_scale, max_kv_len, out, lse, workspace, workspace_bytes, stream,
+                       kPlain);
+}
+ra_status ring_attn_scored_cache_fwd(const ra_tensor* q, const ra_kv_cache* cache, const ra_kv_seqs* seqs,
+                                     int32_t causal, float softmax_scale, const ra_scores* scores, int32_t max_kv_len,
+                                     ra_tensor* out, ra_tensor* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  return any_cache_fwd(q, cache, seqs, causal, softmax_scale, max_kv_len, out, lse, workspace, workspace_bytes, stream,
+                       scored(scores));
 }
 
 size_t ring_attn_cache_workspace_size(int64_t total, int64_t max_new, int64_t h, int64_t hk, int64_t d,

@@ -1,9 +1,9 @@
-// Marshals torch tensors into the C ABI's cache calls.  They serve single tokens,
+// Marshals torch tensors into the C ABI's cache calls and the rotation.  They serve single tokens,
 // whose kernels take a few microseconds; describing a call's tensors through
 // Python and ctypes takes 15 to 27 us on the host, here 5 to 9.
 //
 // Each function checks devices, types and dimensions (ValueError, as the rest of
-// the binding), makes the cache's device current, allocates outputs that were not
+// the binding), makes the cache's (the queries') device current, allocates outputs that were not
 // given, calls the library on the device's current stream and returns
 // (status, outputs).  Everything else is checked by the library.
 #include <Python.h>
@@ -24,6 +24,8 @@ decltype(&ring_attn_cache_append) g_append;
 decltype(&ring_attn_cache_read) g_read;
 decltype(&ring_attn_cache_fwd) g_fwd;
 decltype(&ring_attn_cache_workspace_size) g_ws_size;
+decltype(&ring_attn_scored_cache_fwd) g_scored_fwd;
+decltype(&ring_attn_rope) g_rope;
 
 #define RA_REFUSE(cond, ...) TORCH_CHECK_VALUE(!(cond), __VA_ARGS__)
 
@@ -177,16 +179,27 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (cache, cu's device array, its host array, q, page_table, kv_lens, causal, scale, max_kv_len, out, lse, out_fp32, workspace) -> (status, out, lse)
+// Scores._call for a call of h query heads and n sequences on device `index`; null for None.
+const ra_scores* scores_arg(PyObject* t, int index, int64_t h, int64_t n) {
+  if (!given(t)) return nullptr;
+  RA_REFUSE(!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 4, "scores must be a Scores");
+  RA_REFUSE(item(t, 1) >= 0 && item(t, 1) != index, "scores on cuda:", item(t, 1), ", call on cuda:", index);
+  RA_REFUSE(item(t, 2) >= 0 && item(t, 2) != h, "slopes must have one entry for each of the ", h, " query heads");
+  RA_REFUSE(item(t, 3) >= 0 && item(t, 3) != n, "prefix must have one entry for each of the ", n, " sequences");
+  return reinterpret_cast<const ra_scores*>(item(t, 0));
+}
+
+// (cache, cu's device array, its host array, q, page_table, kv_lens, causal, scale, max_kv_len, out, lse, out_fp32, workspace, scores) -> (status, out, lse)
 PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  TORCH_CHECK_VALUE(n == 13, "13 arguments");
+  TORCH_CHECK_VALUE(n == 14, "14 arguments");
   const CacheArg c = cache_arg(a[0]);
   const CuArg cu = cu_arg(a[1], a[2], c);
   const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)c.index));
   const ra_kv_seqs seqs = sequences(a[4], a[5], cu, c.index);
   const at::Tensor& tq = tensor(a[3], c.index);
   const ra_tensor q = describe(tq, 3);
+  const ra_scores* scores = scores_arg(a[13], c.index, tq.size(1), cu.n);
   const int causal = truth(a[6]), fp32 = truth(a[11]);
   const double scale = PyFloat_AsDouble(a[7]);
   const long max_kv = PyLong_AsLong(a[8]);
@@ -203,19 +216,93 @@ PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else if (cu.total > 0) {
     ws = at::empty({(int64_t)g_ws_size(cu.total, cu.max_new(), tq.size(1), c.hk, c.d, cu.n)}, on(c.index, at::kByte));
   }
-  const int status = g_fwd(&q, c.cache, &seqs, causal, (float)scale, (int32_t)max_kv, &o, &l, ws.defined() ? ws.data_ptr() : nullptr,
-                           ws.defined() ? ws.nbytes() : 0, current_stream(c.index));
+  void *wp = ws.defined() ? ws.data_ptr() : nullptr, *stream = current_stream(c.index);
+  const size_t wn = ws.defined() ? ws.nbytes() : 0;
+  const int status = scores ? g_scored_fwd(&q, c.cache, &seqs, causal, (float)scale, scores, (int32_t)max_kv, &o, &l, wp, wn, stream)
+                            : g_fwd(&q, c.cache, &seqs, causal, (float)scale, (int32_t)max_kv, &o, &l, wp, wn, stream);
   return Py_BuildValue("(iNN)", status, given(a[9]) ? Py_NewRef(a[9]) : THPVariable_Wrap(out),
                        given(a[10]) ? Py_NewRef(a[10]) : THPVariable_Wrap(lse));
+  END_HANDLE_TH_ERRORS
+}
+
+// A (b, h, s, d) tensor, or (rows, h, d) as b = 1.
+ra_tensor describe_rows(const at::Tensor& t) {
+  if (t.dim() != 3) return describe(t, 4);
+  const ra_tensor x = describe(t, 3);
+  ra_tensor r = x;
+  r.ndim = 4;
+  const int from[4] = {-1, 1, 0, 2};
+  for (int i = 0; i < 4; ++i) {
+    r.shape[i] = from[i] < 0 ? 1 : x.shape[from[i]];
+    r.stride[i] = from[i] < 0 ? 8 : x.stride[from[i]];
+  }
+  return r;
+}
+
+// (q, k, cos, sin, positions, axes, interleaved, inverse, layout, n_shards, q_out, k_out) -> (status, q_out, k_out)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 12, "12 arguments");
+  RA_REFUSE(!THPVariable_Check(a[0]) || !THPVariable_Unpack(a[0]).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
+  const at::Tensor& tq = THPVariable_Unpack(a[0]);
+  const int index = tq.get_device();
+  auto here = [index](PyObject* o) -> const at::Tensor& {
+    RA_REFUSE(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
+    const at::Tensor& t = THPVariable_Unpack(o);
+    RA_REFUSE(t.get_device() != index, "tensor on ", t.device(), ", q on cuda:", index);
+    return t;
+  };
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)index));
+  const bool has_k = given(a[1]);
+  RA_REFUSE(given(a[11]) && !has_k, "k_out without k");
+  ra_tensor in[2], out[2];
+  at::Tensor made[2];
+  for (int i = 0; i < (has_k ? 2 : 1); ++i) {
+    const at::Tensor& t = here(a[i]);
+    RA_REFUSE(t.dim() != tq.dim(), "q and k must both be (b, h, s, d) or (rows, h, d)");
+    in[i] = describe_rows(t);
+    made[i] = given(a[10 + i]) ? here(a[10 + i]) : at::empty(t.sizes(), t.options());
+    RA_REFUSE(made[i].dim() != tq.dim(), "outputs must have their inputs' shapes");
+    out[i] = describe_rows(made[i]);
+  }
+  const ra_tensor cos = describe(here(a[2]), 2), sin = describe(here(a[3]), 2);
+  ra_rope_positions p{};
+  if (given(a[4])) {
+    const at::Tensor& t = here(a[4]);
+    const int64_t rows = tq.dim() == 3 ? 1 : 2;  // dimensions of one axis
+    RA_REFUSE(t.scalar_type() != at::kInt || (t.dim() != rows && t.dim() != rows + 1),
+              "positions must be int32, ", rows == 1 ? "(rows) or (axes, rows)" : "(b, s) or (axes, b, s)");
+    const bool axes = t.dim() == rows + 1;
+    p.n_axes = axes ? (int32_t)std::min<int64_t>(t.size(0), 256) : 1;
+    p.stride_axis = axes ? t.stride(0) : 0;
+    p.stride_s = t.stride(-1);
+    p.stride_b = rows == 2 ? t.stride(-2) : 0;
+    RA_REFUSE(t.size(-1) != in[0].shape[2] || (rows == 2 && t.size(-2) != in[0].shape[0]),
+              "positions must have an entry for every row");
+    p.positions = t.const_data_ptr<int32_t>();
+  }
+  if (given(a[5])) {
+    RA_REFUSE(!PyBytes_Check(a[5]) || PyBytes_GET_SIZE(a[5]) != cos.shape[1], "axes must name an axis for each of the ", cos.shape[1],
+              " pairs");
+    RA_REFUSE(!given(a[4]), "axes without positions");
+    p.pair_axis = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[5]));
+  }
+  const int inter = truth(a[6]), inverse = truth(a[7]);
+  const long layout = PyLong_AsLong(a[8]), shards = PyLong_AsLong(a[9]);
+  if (PyErr_Occurred()) throw python_error();
+  const int status = g_rope(&in[0], has_k ? &in[1] : nullptr, &cos, &sin, inter, given(a[4]) ? &p : nullptr, (int32_t)layout,
+                            (int32_t)shards, inverse, &out[0], has_k ? &out[1] : nullptr, current_stream(index));
+  return Py_BuildValue("(iNN)", status, given(a[10]) ? Py_NewRef(a[10]) : THPVariable_Wrap(made[0]),
+                       !has_k ? Py_NewRef(Py_None) : given(a[11]) ? Py_NewRef(a[11]) : THPVariable_Wrap(made[1]));
   END_HANDLE_TH_ERRORS
 }
 
 // The library's functions, by address.
 PyObject* use(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  TORCH_CHECK_VALUE(n == 4, "4 arguments");
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  TORCH_CHECK_VALUE(n == 6, "6 arguments");
+  void* p[6];
+  for (int i = 0; i < 6; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null function");
@@ -226,6 +313,8 @@ PyObject* use(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_read = reinterpret_cast<decltype(g_read)>(p[1]);
   g_fwd = reinterpret_cast<decltype(g_fwd)>(p[2]);
   g_ws_size = reinterpret_cast<decltype(g_ws_size)>(p[3]);
+  g_scored_fwd = reinterpret_cast<decltype(g_scored_fwd)>(p[4]);
+  g_rope = reinterpret_cast<decltype(g_rope)>(p[5]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -237,6 +326,7 @@ PyMethodDef g_methods[] = {{"use", fast(use), METH_FASTCALL, nullptr},
                            {"cache_append", fast(cache_append), METH_FASTCALL, nullptr},
                            {"cache_read", fast(cache_read), METH_FASTCALL, nullptr},
                            {"cache_fwd", fast(cache_fwd), METH_FASTCALL, nullptr},
+                           {"rope", fast(rope), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ra_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -67,6 +67,8 @@ struct CacheAttnArgs {
   int whole;                // set by the plan: items are not shared among blocks
   long long items;          // row tiles times key / value heads, cache_attn_items
   int line_shift;           // set by the plan, see LineSeq
+  int mode;                 // SC bits of changed scores, 0: none
+  ScoreParams sc;           // for products that are in log2 units already
   CacheView c;
   CacheSeqs s;
   DevCtl ctl;
@@ -89,6 +91,10 @@ cudaError_t launch_cache_join(const CacheAttnPlan& p, cudaStream_t st);
 size_t cache_chunk_ws_bytes(int d);
 void plan_cache_chunk(CacheAttnPlan& p);
 cudaError_t launch_cache_chunk(const CacheAttnPlan& p, cudaStream_t st);
+template <int SC>  // one translation unit each
+cudaError_t launch_cache_chunk_score(const CacheAttnPlan& p, cudaStream_t st);
+// few query rows with changed scores of any kind
+cudaError_t launch_cache_attn_scored(const CacheAttnPlan& p, cudaStream_t st);
 cudaError_t launch_chunk_join(const CacheAttnPlan& p, cudaStream_t st);
 
 }  // namespace ra

@@ -1,0 +1,11 @@
+// Chunks over the paged cache with a prefix that all tokens see, scores as they are.
+#include "ra_cache_chunk.cuh"
+
+namespace ra {
+
+template <>
+cudaError_t launch_cache_chunk_score<SC_ON>(const CacheAttnPlan& p, cudaStream_t st) {
+  return p.args.d == 64 ? launch_chunk<64, SC_ON>(p, st) : launch_chunk<128, SC_ON>(p, st);
+}
+
+}  // namespace ra

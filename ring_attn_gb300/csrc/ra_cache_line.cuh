@@ -33,15 +33,21 @@ struct Int {
 struct LineSeq {
   int len, n_new, tiles, per;
   int a, b;
+  int pre;  // tokens that every causal row sees (Kind::kPrefix, else 0)
   __device__ __forceinline__ int before(int tile) const { return a * tile + b * (tile * (tile - 1) / 2); }
 };
 
-// Kind: R, kItemCost, kOneTile (R holds all of a sequence's rows), and for line_shift 0
+// Kind: R, kItemCost, kOneTile (R holds all of a sequence's rows), kPrefix (calls may have prefixes), and for line_shift 0
 // the cost rule `static void cost(args, LineSeq&)` and the least places that a block of a
 // number of warps takes, `static int min_places(args, warps)`.
+// Tokens of sequence i's prefix, which all of its causal rows see.
+__device__ __forceinline__ int cache_prefix(const CacheAttnArgs& g, int i) {
+  return g.sc.prefix && g.causal ? min(max(g.sc.prefix[i], 0), 1 << 30) : 0;
+}
 template <class Kind>
-__device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int len, int n_new) {
+__device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int seq, int len, int n_new) {
   LineSeq s;
+  s.pre = Kind::kPrefix ? cache_prefix(g, seq) : 0;
   s.n_new = n_new;
   s.len = len;
   s.tiles = Kind::kOneTile ? min(n_new, 1) : (int)(((long long)n_new * g.G + Kind::R - 1) / Kind::R);
@@ -56,7 +62,7 @@ __device__ __forceinline__ LineSeq line_of(const CacheAttnArgs& g, int len, int 
 template <class Kind>
 __device__ __forceinline__ LineSeq line_seq(const CacheAttnArgs& g, int i) {
   const int n_new = g.s.cu[i + 1] - g.s.cu[i];
-  return line_of<Kind>(g, max(0, min(g.s.lens[i], g.max_kv)), n_new);
+  return line_of<Kind>(g, i, max(0, min(g.s.lens[i], g.max_kv)), n_new);
 }
 template <class Kind>
 __device__ __forceinline__ int line_length(const CacheAttnArgs& g, const LineSeq& s) {
@@ -70,7 +76,7 @@ __device__ __forceinline__ int tile_units(const CacheAttnArgs& g, const LineSeq&
   int end = s.len;
   if (g.causal && !Kind::kOneTile) {
     const int last = (int)min((long long)s.n_new - 1, ((long long)tile * Kind::R + Kind::R - 1) / g.G);
-    end = min(end, s.len - s.n_new + last + 1);
+    end = min(end, Kind::kPrefix ? max(s.len - s.n_new + last + 1, s.pre) : s.len - s.n_new + last + 1);
   }
   return max(1, (end + kUnit - 1) / kUnit);
 }
@@ -213,7 +219,7 @@ struct Piece {
 template <class Kind>
 __device__ __forceinline__ bool next_piece(const CacheAttnArgs& g, LinePos& at, int end, Piece& x) {
   while (at.u < end) {
-    LineSeq s = line_of<Kind>(g, at.len, at.n_new);
+    LineSeq s = line_of<Kind>(g, at.seq, at.len, at.n_new);
     x.seq = at.seq;
     x.head = at.head;
     x.tile = at.tile;

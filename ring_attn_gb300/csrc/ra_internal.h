@@ -59,15 +59,39 @@ struct BwdParams {
   DevCtl ctl;
 };
 
-// The kernel parameters with a compile-time varlen flag: the batched kernels
-// are instantiated with kVarlen = false, so every varlen branch folds away.
-template <bool VL>
-struct FwdParamsT : FwdParams {
-  static constexpr bool kVarlen = VL;
+// What a call does to its scores besides the product (ra_score.cuh), as the kernels
+// are instantiated for it: bits of SC, 0 for plain scores.  A prefix alone is SC_ON.
+enum : int { SC_CAP = 1, SC_BIAS = 2, SC_ON = 4 };
+
+// Scores are carried in log2 units: z = log2(e) * (softcap * tanh(x / softcap) - slope * distance).
+struct ScoreParams {
+  float cap2;               // softcap * log2(e)
+  float c[5];               // z = s (c0 + w (c1 + ...)), w = s^2, of a product s with |s| <= lim
+  float lim;
+  float e2;                 // any s: z = cap2 - 2 cap2 / (1 + 2^(e2 s))
+  float inv_cap2;           // tanh(x / softcap) = z * inv_cap2
+  const float* slopes;      // per query head
+  const int* prefix;        // per batch or sequence, or nullptr
 };
-template <bool VL>
-struct BwdParamsT : BwdParams {
+template <int SC>
+struct ScorePart {
+  ScoreParams sc;
+};
+template <>
+struct ScorePart<0> {};
+
+// The kernel parameters with compile-time varlen and score flags: the batched kernels
+// are instantiated with kVarlen = false, so every varlen branch folds away, and
+// plain scores with SC = 0.
+template <bool VL, int SC = 0>
+struct FwdParamsT : FwdParams, ScorePart<SC> {
   static constexpr bool kVarlen = VL;
+  static constexpr int kScore = SC;
+};
+template <bool VL, int SC = 0>
+struct BwdParamsT : BwdParams, ScorePart<SC> {
+  static constexpr bool kVarlen = VL;
+  static constexpr int kScore = SC;
 };
 
 // Strided 4-D view of a tensor whose last dimension is contiguous.
@@ -80,10 +104,19 @@ struct View4 {
 cudaError_t launch_fwd(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const FwdParams& p, cudaStream_t st);
 size_t fwd_smem_bytes(int D);
+// The same with scores changed as `sc` says; one translation unit per SC (SC_ON and what is set besides).
+template <int SC>
+cudaError_t launch_fwd_score(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const FwdParams& p, const ScoreParams& sc, cudaStream_t st);
 
 // which = 0: the dK / dV kernel; 1: the dQ kernel.
 cudaError_t launch_bwd(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tdo, const BwdParams& p, int which, cudaStream_t st);
+
+template <int SC>
+cudaError_t launch_bwd_score(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const CUtensorMap& tdo, const BwdParams& p, const ScoreParams& sc, int which,
+                             cudaStream_t st);
 
 // The dK / dV kernel on CTA pairs (cta_group::2), head_dim 128 only.  The four
 // tensor maps have 64 x 64 boxes (64 head dims by 64 rows).
@@ -145,6 +178,28 @@ cudaError_t launch_permute(const PermuteArgs& a, cudaStream_t st);
 // With inv non-null also inv[map[p]] = p (the layout position of each original token).
 cudaError_t launch_zigzag_varlen_map(const int* cu, int n_seqs, int N, int total, int* map, int* inv,
                                      cudaStream_t st);
+
+// Rows to be rotated, (b, h, s, d) with element strides and d contiguous.
+struct RopeRows {
+  void* data;
+  long long sb, sh, ss;
+};
+struct RopeArgs {
+  RopeRows in[2], out[2];   // q and k
+  int h[2];                 // heads (h[1] = 0: no k)
+  int b, s, d, f32;
+  const float* cos_t;
+  const float* sin_t;
+  long long cos_stride, sin_stride;
+  int rot, style, inverse, max_pos;
+  const int* pos;           // nullptr: the row's original token
+  long long p_axis, p_b, p_s;
+  int layout, N;
+  uint32_t mixed;           // bit i: pairs 4 i .. 4 i + 3 are not all of one axis
+  uint8_t axis[64];         // of every pair
+  DevCtl ctl;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
 
 int num_sms();
 

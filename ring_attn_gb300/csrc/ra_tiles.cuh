@@ -29,6 +29,28 @@ __device__ __forceinline__ bool vz(const P& p) {
   return cu_of(p) != nullptr && p.layout == LAYOUT_ZIGZAG;
 }
 
+// Tokens of the prefix that all tokens of batch or sequence i see; 0 without one (and
+// without causal, where they see everything anyway).
+template <class P>
+__device__ __forceinline__ int prefix_of(const P& p, int i) {
+  if constexpr (P::kScore != 0)
+    return p.sc.prefix && p.causal ? min(max(__ldg(p.sc.prefix + i), 0), 1 << 30) : 0;
+  else
+    return 0;
+}
+
+// With a prefix of `pre` tokens a query sees the keys that its token or the prefix's last
+// one sees, and a key is seen by the queries from its token on, or by all: the masks take
+// these tokens in place of their own.
+template <class P>
+__device__ __forceinline__ int seeing_token(int gq, int pre) {
+  return P::kScore != 0 ? max(gq, pre - 1) : gq;
+}
+template <class P>
+__device__ __forceinline__ int seen_token(int gk, int pre) {
+  return P::kScore != 0 && gk < pre ? 0 : gk;
+}
+
 // Original token of local position i of shard r.
 template <class P>
 __device__ __forceinline__ int tok(const P& p, int r, int i) {
@@ -52,7 +74,7 @@ __device__ __forceinline__ void zigzag_heavy_first(int k, int N, int tpc, int& s
 // Query rows [i0, i0 + rows) of Q shard r; the valid ones end at i_last.
 struct QRange {
   int r, i0, i_last;
-  int gq_lo, gq_hi;    // original token indices of the first / last valid row
+  int gq_lo, gq_hi;    // original token indices of the first / last valid row (as the masks take them)
   // varlen: the keys any row may see.  Contiguous: tokens [key_lo, key_hi].
   // Zigzag: local positions from key_lo in every shard up to, when causal, the
   // last row's offset zo in its sequence (first local position zb, chunk zc),
@@ -83,8 +105,9 @@ __device__ __forceinline__ void ends_and_segments(const P& p, int r, int ilo, in
   }
 }
 
+// pre: the batch's prefix (varlen calls look up their sequences').
 template <class P>
-__device__ __forceinline__ void make_qrange(const P& p, int r, int i0, int rows, QRange& q) {
+__device__ __forceinline__ void make_qrange(const P& p, int r, int i0, int rows, QRange& q, int pre = 0) {
   q.r = r;
   q.i0 = i0;
   q.i_last = min(i0 + rows, p.L) - 1;
@@ -98,10 +121,17 @@ __device__ __forceinline__ void make_qrange(const P& p, int r, int i0, int rows,
     q.key_hi = cz1 / p.N - 1;
     q.zb = cz / p.N;
     q.zc = (cz1 - cz) / (2 * p.N);
-    q.zo = q.gq_hi - cz;
+    q.zo = seeing_token<P>(q.gq_hi - cz, prefix_of(p, sz));
   } else if (cu_of(p)) {
+    // (the rows before the last one's sequence see keys before it only)
     q.key_lo = __ldg(p.cu + sa);
-    q.key_hi = p.causal ? q.gq_hi : __ldg(p.cu + sz + 1) - 1;
+    const int last = __ldg(p.cu + sz + 1) - 1;
+    q.key_hi = p.causal ? q.gq_hi : last;
+    if constexpr (P::kScore != 0)
+      if (p.causal) q.key_hi = min(last, max(q.gq_hi, __ldg(p.cu + sz) + min(prefix_of(p, sz), p.S) - 1));
+  } else {
+    q.gq_lo = seeing_token<P>(q.gq_lo, pre);
+    q.gq_hi = seeing_token<P>(q.gq_hi, pre);
   }
 }
 
@@ -182,7 +212,7 @@ __device__ __forceinline__ void row_key_window(const P& p, int gq, int s, int kt
 // tiles of a CTA pair, whose query walk is the union of its two tiles').
 struct KRange {
   int s, j0, j_last;
-  int gk_lo, gk_hi;
+  int gk_lo, gk_hi;    // tokens of the first / last valid row (as the masks take them)
   // varlen: the queries any key may serve.  Contiguous: tokens [qry_lo, qry_hi].
   // Zigzag: local positions up to qry_hi in every shard, from (causal) the
   // first local position past offset zo of the first key's sequence (first
@@ -191,7 +221,7 @@ struct KRange {
 };
 
 template <class P>
-__device__ __forceinline__ void make_krange(const P& p, int s, int j0, KRange& k, int rows = kTileN) {
+__device__ __forceinline__ void make_krange(const P& p, int s, int j0, KRange& k, int rows = kTileN, int pre = 0) {
   k.s = s;
   k.j0 = j0;
   k.j_last = min(j0 + rows, p.L) - 1;
@@ -204,10 +234,14 @@ __device__ __forceinline__ void make_krange(const P& p, int s, int j0, KRange& k
     k.qry_hi = __ldg(p.cu + sz + 1) / p.N - 1;
     k.zb = ca / p.N;
     k.zc = (ca1 - ca) / (2 * p.N);
-    k.zo = k.gk_lo - 1 - ca;
+    k.zo = seen_token<P>(k.gk_lo - ca, prefix_of(p, sa)) - 1;
   } else if (cu_of(p)) {
-    k.qry_lo = p.causal ? k.gk_lo : __ldg(p.cu + sa);
+    const int ca = __ldg(p.cu + sa);
+    k.qry_lo = p.causal ? ca + seen_token<P>(k.gk_lo - ca, prefix_of(p, sa)) : ca;
     k.qry_hi = __ldg(p.cu + sz + 1) - 1;
+  } else {
+    k.gk_lo = seen_token<P>(k.gk_lo, pre);
+    k.gk_hi = seen_token<P>(k.gk_hi, pre);
   }
 }
 
@@ -310,6 +344,7 @@ struct RowWin {
   int a, b;         // contiguous: allowed tokens [a, b); zigzag: allowed offsets (a, b] in the sequence
   int base, c;      // zigzag: the sequence's first local position (every shard) and its chunk length
   int cur, lo, hi;  // shard `cur` allows local positions [lo, hi)
+  int first;        // the sequence's first token (read for a bias by distance)
 };
 
 // Window of the row at local position i of shard r; returns its token.
@@ -324,20 +359,22 @@ __device__ __forceinline__ int make_row_win(const P& p, int r, int i, bool key_r
     ck = __ldg(p.cu + k);
     ck1 = __ldg(p.cu + k + 1);
     g = vz_token_in(ck, ck1, p.N, r, i);
-    const int o = g - ck, last = ck1 - ck - 1;
+    const int o = g - ck, last = ck1 - ck - 1, pre = prefix_of(p, k);
     w.base = ck / p.N;
     w.c = (ck1 - ck) / (2 * p.N);
-    w.a = key_row && p.causal ? o - 1 : -1;
-    w.b = !key_row && p.causal ? o : last;
+    w.a = key_row && p.causal ? seen_token<P>(o, pre) - 1 : -1;
+    w.b = !key_row && p.causal ? seeing_token<P>(o, pre) : last;
   } else {
     g = r * p.L + i;
     const int k = segment_of_lanes(p.cu, p.n_seqs, g);
     ck = __ldg(p.cu + k);
     ck1 = __ldg(p.cu + k + 1);
-    w.a = key_row && p.causal ? g : ck;
-    w.b = !key_row && p.causal ? g + 1 : ck1;
+    const int pre = prefix_of(p, k);
+    w.a = key_row && p.causal ? ck + seen_token<P>(g - ck, pre) : ck;
+    w.b = !key_row && p.causal ? min(ck1, ck + seeing_token<P>(g - ck, pre) + 1) : ck1;
     w.base = w.c = 0;
   }
+  w.first = ck;
   w.cur = -1;
   w.lo = w.hi = 0;
   return g;

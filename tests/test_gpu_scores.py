@@ -1,0 +1,271 @@
+"""Attention with capped scores, a bias by distance and prefixes: forward and backward of every form that takes
+`scores`, against the fp64 oracle with bounds from the kernels' roundings (tests/score_case.py)."""
+import numpy as np
+import pytest
+import torch
+
+import ring_attn_gb300 as ra
+from tests.helpers import check_no_device_error, lse_to_original, to_layout, to_original
+from tests.score_case import assert_within, expect
+from workload import cu_seqlens, make_qkv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from ring_attn_gb300.build import build
+
+    build()
+    ra.load()
+
+
+def inputs(b, h, hk, s, d, seed, gain=1.0):
+    x, y = make_qkv(b, h, s, d, seed), make_qkv(b, hk, s, d, seed + 1, with_do=False)
+    do = (x["do"].float() * (hk / h) ** 0.5).bfloat16()
+    return {"q": (x["q"].float() * gain).bfloat16(), "k": y["k"], "v": y["v"], "do": do}
+
+
+def slopes_of(h, kind):
+    s = {None: None, "alibi": [2.0 ** (-8 * (i + 1) / h) for i in range(h)],
+         "mixed": [(0.25, 0.0, -0.01, 1.5)[i % 4] for i in range(h)]}[kind]
+    return None if s is None else torch.tensor(s, dtype=torch.float32)
+
+
+def scores_of(cap, slopes, prefix):
+    return ra.Scores(cap, None if slopes is None else slopes.cuda(),
+                     None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device="cuda"))
+
+
+def rows_first(t):
+    """(1, h, total, d) -> (total, h, d) with plain strides."""
+    t = t[0].transpose(0, 1)
+    return torch.empty(t.shape, dtype=t.dtype, device="cuda").copy_(t)
+
+
+CASES = [
+    # b, h, hk, s, d, layout, n, causal, cap, slopes, prefix, gain
+    (1, 2, 2, 256, 64, "contiguous", 1, True, 20.0, None, None, 1.0),
+    (1, 2, 2, 300, 128, "contiguous", 2, False, 2.0, None, None, 4.0),        # scores beyond the polynomial
+    (2, 4, 2, 390, 64, "contiguous", 3, True, 0.0, "alibi", None, 1.0),
+    (1, 4, 1, 520, 64, "zigzag", 2, False, 0.0, "mixed", None, 1.0),          # seams and diagonals inside tiles
+    (1, 3, 3, 600, 128, "zigzag", 3, True, 0.0, "alibi", None, 1.0),
+    (1, 2, 2, 512, 128, "zigzag", 2, True, 30.0, "alibi", None, 2.0),         # whole tiles left and right of the seam
+    (2, 2, 1, 387, 128, "stripe", 3, False, 5.0, "mixed", None, 2.0),
+    (1, 2, 2, 640, 64, "stripe", 4, True, 50.0, "alibi", None, 1.0),
+    (3, 2, 2, 384, 64, "contiguous", 1, True, 0.0, None, (0, 131, 1000), 1.0),
+    (2, 4, 2, 512, 128, "zigzag", 4, True, 0.0, None, (200, 1), 1.0),
+    (2, 2, 2, 510, 64, "stripe", 3, True, 10.0, "mixed", (129, -3), 1.0),
+    (2, 2, 2, 520, 128, "zigzag", 2, True, 15.0, "mixed", (256, 519), 3.0),
+    (1, 1, 1, 1, 64, "contiguous", 1, True, 3.0, "mixed", (1,), 1.0),
+    (1, 1, 1, 2, 128, "zigzag", 1, True, 3.0, "mixed", (0,), 1.0),
+    (1, 2, 1, 129, 128, "contiguous", 1, False, 0.01, "mixed", None, 1.0),     # a cap far below the scores
+    (1, 1, 1, 200, 64, "contiguous", 1, True, 1e6, None, None, 1.0),           # and far above
+]
+
+
+@pytest.mark.parametrize("b,h,hk,s,d,layout,n,causal,cap,slopes,prefix,gain", CASES)
+def test_batched(b, h, hk, s, d, layout, n, causal, cap, slopes, prefix, gain):
+    x = inputs(b, h, hk, s, d, 9000 + s + h, gain)
+    sl = slopes_of(h, slopes)
+    z = scores_of(cap, sl, prefix)
+    g = {k: to_layout(ra, v.cuda(), layout, n) for k, v in x.items()}
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], layout, n, causal, scores=z)
+    grads = ra.ring_attn_bwd(g["do"], g["q"], g["k"], g["v"], out, lse, layout, n, causal, scores=z)
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], x["do"], d ** -0.5, cap, sl, causal, prefix)
+    assert_within("out", to_original(ra, out, layout, n), want["out"])
+    assert_within("lse", lse_to_original(ra, lse, layout, n), want["lse"])
+    for name, t in zip(("dq", "dk", "dv"), grads):
+        assert_within(name, to_original(ra, t, layout, n), want[name])
+
+
+@pytest.mark.parametrize("layout,causal,cap,slopes,prefix", [
+    ("contiguous", True, 8.0, "alibi", (150,)), ("zigzag", True, 0.0, "alibi", None), ("stripe", False, 8.0, "mixed", None),
+    ("zigzag", True, 0.0, None, (300,)),
+])
+def test_ring_steps_and_merge(layout, causal, cap, slopes, prefix):
+    """Every ring step on its own, merged; steps of a causal ring leave rows without keys."""
+    b, h, hk, s, d, n = 1, 2, 1, 544, 64, 4
+    x = inputs(b, h, hk, s, d, 9100)
+    sl = slopes_of(h, slopes)
+    z = scores_of(cap, sl, prefix)
+    g = {k: to_layout(ra, v.cuda(), layout, n) for k, v in x.items()}
+    acc = torch.zeros((b, h, s, d), device="cuda")
+    lacc = torch.full((b, h, s), -np.inf, device="cuda")
+    for step in range(n):
+        ra.lse_merge(acc, lacc, *ra.ring_attn_fwd_step(g["q"], g["k"], g["v"], step, layout, n, causal, scores=z))
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], None, d ** -0.5, cap, sl, causal, prefix)
+    assert_within("out", to_original(ra, acc, layout, n), want["out"])
+    val, tol = want["lse"]
+    assert_within("lse", lse_to_original(ra, lacc, layout, n), (val, tol + n * 2.0 ** -21))  # n merges
+
+
+@pytest.mark.parametrize("layout,lens,n,ws", [
+    ("contiguous", [100, 300, 1, 350, 273], 4, True), ("zigzag", [256, 640, 96, 1056], 4, True),
+    ("zigzag", [256, 640, 96, 1056], 4, False),
+])
+@pytest.mark.parametrize("causal,cap,slopes,with_prefix", [
+    (True, 0.0, "alibi", False), (False, 6.0, "mixed", False), (True, 0.0, None, True), (True, 6.0, "mixed", True),
+])
+def test_packed_documents(layout, lens, n, ws, causal, cap, slopes, with_prefix):
+    h, hk, d = 2, 1, 64
+    cu = cu_seqlens(lens)
+    total = int(cu[-1])
+    x = inputs(1, h, hk, total, d, 9200 + len(lens))
+    sl = slopes_of(h, slopes)
+    prefix = [m * (i % 3) // 2 for i, m in enumerate(lens)] if with_prefix else None  # nothing, half, all of a sequence
+    z = scores_of(cap, sl, prefix)
+    g = {k: ra.ring_attn_varlen_permute(rows_first(v), cu, layout, n, seq_dim=0) for k, v in x.items()}
+
+    def space(op):
+        m = ra.ring_attn_varlen_workspace_size(op, total, h, d, layout if ws else "contiguous", n)
+        return torch.empty(m, dtype=torch.uint8, device="cuda")
+
+    out, lse = ra.ring_attn_varlen_fwd(g["q"], g["k"], g["v"], cu, None, n, causal, layout=layout,
+                                       workspace=space(ra.RA_OP_FWD), scores=z)
+    grads = ra.ring_attn_varlen_bwd(g["do"], g["q"], g["k"], g["v"], out, lse, cu, None, n, causal, layout=layout,
+                                    workspace=space(ra.RA_OP_BWD), scores=z)
+    check_no_device_error(ra)
+
+    def back(t):
+        t = torch.empty(t.shape, dtype=t.dtype, device="cuda").copy_(t)
+        return ra.ring_attn_varlen_unpermute(t, cu, layout, n, seq_dim=0).transpose(0, 1).unsqueeze(0)
+
+    want = expect(x["q"], x["k"], x["v"], x["do"], d ** -0.5, cap, sl, causal, prefix, cu)
+    assert_within("out", back(out), want["out"])
+    assert_within("lse", back(lse.t().contiguous().unsqueeze(-1)).squeeze(-1), want["lse"])
+    for name, t in zip(("dq", "dk", "dv"), grads):
+        assert_within(name, back(t), want[name])
+
+
+def test_llama3_ranks():
+    """The ranks' rows together, and the sum of their gradients of the keys."""
+    lens, n, h, hk, d = [300, 500, 224], 4, 2, 1, 64
+    cu = cu_seqlens(lens)
+    total = int(cu[-1])
+    L = total // n
+    x = inputs(1, h, hk, total, d, 9300)
+    sl, prefix, cap = slopes_of(h, "alibi"), [120, 400, 0], 12.0
+    z = scores_of(cap, sl, prefix)
+    g = {k: rows_first(v) for k, v in x.items()}
+    got = {k: [] for k in ("out", "lse", "dq", "dk", "dv")}
+    for r in range(n):
+        rows = slice(r * L, (r + 1) * L)
+        q, do = g["q"][rows].contiguous(), g["do"][rows].contiguous()
+        out, lse = ra.ring_attn_llama3_varlen_fwd(q, g["k"], g["v"], cu, r, n, scores=z)
+        grads = ra.ring_attn_llama3_varlen_bwd(do, q, g["k"], g["v"], out, lse, cu, r, n, scores=z)
+        for name, t in zip(got, (out, lse, *grads)):
+            got[name].append(t)
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], x["do"], d ** -0.5, cap, sl, True, prefix, cu)
+    assert_within("out", torch.cat(got["out"]).transpose(0, 1)[None], want["out"])
+    assert_within("lse", torch.cat(got["lse"], 1)[None], want["lse"])
+    assert_within("dq", torch.cat(got["dq"]).transpose(0, 1)[None], want["dq"])
+    for name in ("dk", "dv"):
+        parts = [t.float() for t in got[name]]
+        val, tol = want[name]
+        each = sum(t.abs() for t in parts).transpose(0, 1)[None].double().cpu().numpy()
+        assert_within(name, sum(parts).transpose(0, 1)[None], (val, tol + 2.0 ** -8 * each))  # each rank's is rounded
+
+
+def test_packed_tensors():
+    """qkv in one tensor, read and written in place through its strides."""
+    b, s, h, d = 2, 260, 2, 64
+    x = inputs(b, h, h, s, d, 9400)
+    sl, prefix, cap = slopes_of(h, "mixed"), (30, 200), 9.0
+    z = scores_of(cap, sl, prefix)
+    qkv = torch.stack([x[k].transpose(1, 2) for k in "qkv"], 2).cuda()
+    do = x["do"].transpose(1, 2).contiguous().cuda()
+    out, lse = ra.ring_attn_qkvpacked_fwd(qkv, causal=True, scores=z)
+    dqkv = ra.ring_attn_qkvpacked_bwd(do, qkv, out, lse, causal=True, scores=z)
+    out2, lse2 = ra.ring_attn_kvpacked_fwd(qkv[:, :, 0], qkv[:, :, 1:], causal=True, scores=z)
+    dq2, dkv2 = ra.ring_attn_kvpacked_bwd(do, qkv[:, :, 0], qkv[:, :, 1:], out, lse, causal=True, scores=z)
+    check_no_device_error(ra)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert torch.equal(dqkv[:, :, 0], dq2) and torch.equal(dqkv[:, :, 1:], dkv2)
+    want = expect(x["q"], x["k"], x["v"], x["do"], d ** -0.5, cap, sl, True, prefix)
+    assert_within("out", out.transpose(1, 2), want["out"])
+    assert_within("lse", lse, want["lse"])
+    for i, name in enumerate(("dq", "dk", "dv")):
+        assert_within(name, dqkv[:, :, i].transpose(1, 2), want[name])
+
+
+def test_without_changes_the_calls_are_the_plain_ones():
+    x = {k: v.cuda() for k, v in inputs(1, 2, 2, 384, 128, 9500).items()}
+    plain = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, True)
+    grads = ra.ring_attn_bwd(x["do"], x["q"], x["k"], x["v"], *plain, "zigzag", 3, True)
+    for z in (ra.Scores(), scores_of(0.0, None, (0,)), scores_of(0.0, None, (1,))):  # its own token is seen anyway
+        got = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, True, scores=z)
+        back = ra.ring_attn_bwd(x["do"], x["q"], x["k"], x["v"], *got, "zigzag", 3, True, scores=z)
+        assert all(torch.equal(a, b) for a, b in zip((*plain, *grads), (*got, *back)))
+    # a prefix of everything is no causal mask
+    got = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, True, scores=scores_of(0.0, None, (384,)))
+    both = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, False)
+    assert all(torch.equal(a, b) for a, b in zip(got, both))
+    check_no_device_error(ra)
+
+
+def test_infinite_scores_meet_the_cap():
+    """Huge and infinite products are scores of +-cap."""
+    s, d, cap = 160, 64, 7.0
+    x = inputs(1, 1, 1, s, d, 9600)
+    q, k, v = (x[n].clone() for n in "qkv")
+    q[0, 0, 5] = 1e36
+    k[0, 0, 3] = 1e36   # row 5's product with it is infinite, the others' are about 1e36
+    k[0, 0, 150] = -1e36
+    z = ra.Scores(cap)
+    out, lse = ra.ring_attn_fwd(q.cuda(), k.cuda(), v.cuda(), causal=True, scores=z)
+    check_no_device_error(ra)
+    xs = (q[0, 0].double() @ k[0, 0].double().t()) * d ** -0.5
+    y = cap * torch.tanh(xs / cap)
+    y = y.masked_fill(torch.ones(s, s).triu(1).bool(), -np.inf)
+    ref = torch.softmax(y, -1) @ v[0, 0].double()
+    # a huge key's score is +-cap, by its sign; the fp32 sum of 64 products has it unless they cancel to 64 2^-24 of
+    # their size, about 2e32
+    keep = (xs[:, 3].abs() > 1e34) & ((xs[:, 150].abs() > 1e34) | (torch.arange(s) < 150)) | (torch.arange(s) < 3)
+    size = torch.softmax(y, -1) @ v[0, 0].double().abs()
+    tol = 2.0 ** -8 * ref.abs() + size * (2.0 ** -8 * 1.01 + 4 * cap * 2.0 ** -21 + 2.0 ** -14) + 1e-6
+    err = (out[0, 0].double().cpu() - ref).abs()
+    assert int(keep.sum()) > 100 and bool((err <= tol)[keep].all())
+    assert bool(torch.isfinite(lse).all())
+
+
+def test_captured_calls_follow_slopes_and_prefix_and_repeat_their_bits():
+    b, h, s, d = 2, 2, 400, 64
+    x = {k: v.cuda() for k, v in inputs(b, h, h, s, d, 9700).items()}
+    sl = slopes_of(h, "alibi").cuda()
+    pre = torch.tensor([10, 300], dtype=torch.int32, device="cuda")
+    z = ra.Scores(11.0, sl, pre)
+    out, lse = torch.empty_like(x["q"]), torch.empty((b, h, s), device="cuda")
+    ws = torch.empty(ra.ring_attn_workspace_size(ra.RA_OP_BWD, b, h, s, d), dtype=torch.uint8, device="cuda")
+    grads = [torch.empty_like(x["q"]) for _ in range(3)]
+
+    def step(stream=None):
+        ra.ring_attn_fwd(x["q"], x["k"], x["v"], causal=True, out=out, lse=lse, scores=z, stream=stream)
+        ra.ring_attn_bwd(x["do"], x["q"], x["k"], x["v"], out, lse, causal=True, dq=grads[0], dk=grads[1], dv=grads[2],
+                         workspace=ws, scores=z, stream=stream)
+
+    def bits():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (out, lse, *grads)]
+
+    step()
+    first = bits()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    graph.replay()
+    assert all(torch.equal(a, c) for a, c in zip(first, bits()))
+    sl.mul_(-0.5)
+    pre.copy_(torch.tensor([399, 0], dtype=torch.int32))
+    graph.replay()
+    changed = bits()
+    assert not torch.equal(first[0], changed[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, c) for a, c in zip(changed, bits()))
+    check_no_device_error(ra)
