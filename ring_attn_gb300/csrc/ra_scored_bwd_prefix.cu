@@ -3,4 +3,4 @@
 
 template cudaError_t ra::launch_bwd_score<ra::SC_ON>(int, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                               const CUtensorMap&, const ra::BwdParams&, const ra::ScoreParams&, int,
-                                              cudaStream_t);
+                                              const ra::LseView&, cudaStream_t);

