@@ -265,6 +265,37 @@ def _place(scores, q, stream):
     return torch.cuda.stream(stream)
 
 
+def _of(scores):
+    if not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores")
+    return scores._call
+
+
+def _scored_call(name, q, stream, *args):
+    """Runs a call of the compiled marshaller on the given stream (None: the current one of q's device); its results."""
+    f = getattr(_EXT or _ext(), name)
+    if stream is None:
+        r = f(*args)
+    else:
+        if isinstance(q, torch.Tensor) and stream.device != q.device:
+            raise ValueError(f"stream on {stream.device}, q on {q.device}")
+        with torch.cuda.stream(stream):  # outputs and workspace belong to it, too
+            r = f(*args)
+    if r[0] != 0:
+        _check(r[0], "ring_attn_" + name)
+    return r[1:]
+
+
+def _cu_arrays(cu_seqlens, q, stream):
+    """(device, host) arrays of cu_seqlens, copied where q is if it is not a CuSeqlens."""
+    if not isinstance(cu_seqlens, CuSeqlens):
+        if not isinstance(q, torch.Tensor) or not q.is_cuda:
+            raise ValueError("ring_attn_gb300 takes CUDA tensors only")
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(q.device):
+            cu_seqlens = CuSeqlens(cu_seqlens, q.device)
+    return cu_seqlens.dev, cu_seqlens.host
+
+
 def _call(name, scores, device, h, n, at, *args):
     """lib.ring_attn_<name>(*args), or its scored form with the scores at place `at`; checks the status."""
     if scores is None:
@@ -281,17 +312,19 @@ def ring_attn_fwd(q, k, v, layout="contiguous", n_shards=1, causal=False, softma
     scores: a Scores, or None for plain ones.
 
     Returns (out (b, h, s, d) bf16, lse (b, h, s) fp32), both in layout order."""
-    load()
-    with _place(scores, q, stream):
-        b, h, s, d = q.shape
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
-        tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
-        _call("fwd", scores, q.device, h, b, 7, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), _layout(layout),
-              int(n_shards), int(bool(causal)), _scale(softmax_scale, d), ctypes.byref(to), ctypes.byref(tl),
-              *((None, 0) if scores is None else ()), _stream(stream))
+    if scores is not None:
+        return _scored_call("scored_fwd", q, stream, q, k, v, _layout(layout), n_shards, causal,
+                            _scale(softmax_scale, q.shape[-1]), _of(scores), out, lse)
+    lib = load()
+    b, h, s, d = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
+    tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
+    _check(lib.ring_attn_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), _layout(layout), int(n_shards),
+                             int(bool(causal)), _scale(softmax_scale, d), ctypes.byref(to), ctypes.byref(tl),
+                             None, 0, _stream(stream)), "ring_attn_fwd")
     return out, lse
 
 
@@ -341,20 +374,22 @@ def _ws_arg(workspace):
 def ring_attn_bwd(dout, q, k, v, out, lse, layout="contiguous", n_shards=1, causal=False, softmax_scale=None,
                   dq=None, dk=None, dv=None, workspace=None, stream=None, scores=None):
     """Gradients (dq like q, dk and dv like k and v), bf16, layout order; scores as in the forward."""
-    load()
-    with _place(scores, q, stream):
-        b, h, s, d = q.shape
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        ws_bytes = ring_attn_workspace_size(RA_OP_BWD, b, h, s, d, n_shards)
-        if workspace is None:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
-        r = [ctypes.byref(x) for x in ts]
-        _call("bwd", scores, q.device, h, b, 10, r[0], r[1], r[2], r[3], r[4], r[5], _layout(layout), int(n_shards),
-              int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8], ctypes.c_void_p(workspace.data_ptr()),
-              workspace.numel() * workspace.element_size(), _stream(stream))
+    if scores is not None:
+        return _scored_call("scored_bwd", q, stream, dout, q, k, v, out, lse, _layout(layout), n_shards, causal,
+                            _scale(softmax_scale, q.shape[-1]), _of(scores), dq, dk, dv, workspace)
+    lib = load()
+    b, h, s, d = q.shape
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    ws_bytes = ring_attn_workspace_size(RA_OP_BWD, b, h, s, d, n_shards)
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
+    r = [ctypes.byref(x) for x in ts]
+    _check(lib.ring_attn_bwd(r[0], r[1], r[2], r[3], r[4], r[5], _layout(layout), int(n_shards), int(bool(causal)),
+                             _scale(softmax_scale, d), r[6], r[7], r[8], ctypes.c_void_p(workspace.data_ptr()),
+                             workspace.numel() * workspace.element_size(), _stream(stream)), "ring_attn_bwd")
     return dq, dk, dv
 
 
@@ -425,53 +460,63 @@ def ring_attn_varlen_fwd(q, k, v, cu_seqlens, max_seqlen=None, n_shards=1, causa
     zigzag, the original-order copies the library computes in); pass a tensor to
     reuse one (an empty tensor runs the zigzag kernels directly).
     Returns (out like q, lse (h, total) fp32)."""
-    load()
-    with _place(scores, q, stream):
-        host, dev = _cu_pair(cu_seqlens, q.device)
-        n = host.numel() - 1
-        total = int(host[-1])
-        if max_seqlen is None:
-            max_seqlen = _max_len(cu_seqlens, host)
-        h = q.shape[1] if q.shape[0] == total else q.shape[0]
-        d = q.shape[2]
-        out = torch.empty_like(q) if out is None else out
-        lse = torch.empty((h, total), dtype=torch.float32, device=q.device) if lse is None else lse
-        if workspace is None:
-            need = ring_attn_varlen_workspace_size(RA_OP_FWD, total, h, d, layout, n_shards)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        wp, wb = _ws_arg(workspace)
-        tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
-        _call("varlen_fwd", scores, q.device, h, n, 11, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
-              ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen),
-              _layout(layout), int(n_shards), int(bool(causal)), _scale(softmax_scale, d), ctypes.byref(to),
-              ctypes.byref(tl), wp, wb, _stream(stream))
+    if scores is not None:
+        return _scored_call("scored_varlen_fwd", q, stream, q, k, v, *_cu_arrays(cu_seqlens, q, stream), max_seqlen,
+                            _layout(layout), n_shards, causal, _scale(softmax_scale, q.shape[-1]), _of(scores), out,
+                            lse, workspace)
+    lib = load()
+    host, dev = _cu_pair(cu_seqlens, q.device)
+    n = host.numel() - 1
+    total = int(host[-1])
+    if max_seqlen is None:
+        max_seqlen = _max_len(cu_seqlens, host)
+    h = q.shape[1] if q.shape[0] == total else q.shape[0]
+    d = q.shape[2]
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((h, total), dtype=torch.float32, device=q.device) if lse is None else lse
+    if workspace is None:
+        need = ring_attn_varlen_workspace_size(RA_OP_FWD, total, h, d, layout, n_shards)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    wp, wb = _ws_arg(workspace)
+    tq, tk, tv, to, tl = _t(q), _t(k), _t(v), _t(out), _t(lse)
+    _check(lib.ring_attn_varlen_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+                                    ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n,
+                                    int(max_seqlen), _layout(layout), int(n_shards), int(bool(causal)),
+                                    _scale(softmax_scale, d), ctypes.byref(to), ctypes.byref(tl), wp, wb,
+                                    _stream(stream)),
+           "ring_attn_varlen_fwd")
     return out, lse
 
 
 def ring_attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, max_seqlen=None, n_shards=1, causal=True,
                          softmax_scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None,
                          layout="contiguous", scores=None):
-    load()
-    with _place(scores, q, stream):
-        host, dev = _cu_pair(cu_seqlens, q.device)
-        n = host.numel() - 1
-        total = int(host[-1])
-        if max_seqlen is None:
-            max_seqlen = _max_len(cu_seqlens, host)
-        h = q.shape[1] if q.shape[0] == total else q.shape[0]
-        d = q.shape[2]
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        if workspace is None:
-            ws_bytes = ring_attn_varlen_workspace_size(RA_OP_BWD, total, h, d, layout, n_shards)
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
-        r = [ctypes.byref(x) for x in ts]
-        _call("varlen_bwd", scores, q.device, h, n, 14, r[0], r[1], r[2], r[3], r[4], r[5],
-              ctypes.c_void_p(dev.data_ptr()), ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen),
-              _layout(layout), int(n_shards), int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8],
-              ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), _stream(stream))
+    if scores is not None:
+        return _scored_call("scored_varlen_bwd", q, stream, dout, q, k, v, out, lse,
+                            *_cu_arrays(cu_seqlens, q, stream), max_seqlen, _layout(layout), n_shards, causal,
+                            _scale(softmax_scale, q.shape[-1]), _of(scores), dq, dk, dv, workspace)
+    lib = load()
+    host, dev = _cu_pair(cu_seqlens, q.device)
+    n = host.numel() - 1
+    total = int(host[-1])
+    if max_seqlen is None:
+        max_seqlen = _max_len(cu_seqlens, host)
+    h = q.shape[1] if q.shape[0] == total else q.shape[0]
+    d = q.shape[2]
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if workspace is None:
+        ws_bytes = ring_attn_varlen_workspace_size(RA_OP_BWD, total, h, d, layout, n_shards)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    ts = [_t(x) for x in (dout, q, k, v, out, lse, dq, dk, dv)]
+    r = [ctypes.byref(x) for x in ts]
+    _check(lib.ring_attn_varlen_bwd(r[0], r[1], r[2], r[3], r[4], r[5], ctypes.c_void_p(dev.data_ptr()),
+                                    ctypes.c_void_p(host.data_ptr()), n, int(max_seqlen), _layout(layout),
+                                    int(n_shards), int(bool(causal)), _scale(softmax_scale, d), r[6], r[7], r[8],
+                                    ctypes.c_void_p(workspace.data_ptr()),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)),
+           "ring_attn_varlen_bwd")
     return dq, dk, dv
 
 
@@ -733,7 +778,7 @@ _EXT = None
 
 
 def _ext():
-    """The compiled marshaller of the cache calls and the rotation, bound to the loaded library."""
+    """The compiled marshaller of the cache calls, the rotation and attention with scores, bound to the loaded library."""
     global _EXT
     if _EXT is None:
         lib = load()
@@ -745,7 +790,9 @@ def _ext():
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
         ext.use(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value
-                  for f in ("cache_append", "cache_read", "cache_fwd", "cache_workspace_size", "scored_cache_fwd", "rope")))
+                  for f in ("cache_append", "cache_read", "cache_fwd", "cache_workspace_size", "scored_cache_fwd", "rope",
+                            "scored_fwd", "scored_bwd", "scored_varlen_fwd", "scored_varlen_bwd", "workspace_size",
+                            "varlen_workspace_size")))
         _EXT = ext
     return _EXT
 

@@ -214,21 +214,37 @@ struct Scored {
 
 // unit: log2(e) times what a product is multiplied by (the cache's kernels do that themselves: 1).
 ScoreParams score_params(float softcap, const float* slopes, const int32_t* prefix, double unit) {
-  // tanh(u) = u (1 + w (a1 + w (a2 + w (a3 + w a4)))), w = u^2, |u| <= 0.6 (ra_score.cuh)
-  static const double a[5] = {1.0, -0.3333259750806283, 0.13313116663407254, -0.05221180687723626,
-                              0.015612632993333238};
+  // tanh(u) = u (1 + w P(w)) and its derivative 1 + w G(w), w = u^2, for |u| up to 0.4, 0.6 and 1 (ra_score.cuh)
+  static const double p0[3] = {-0.3333188226164798, 0.1327762900673371, -0.047794219065101964},
+                      p1[4] = {-0.33332597507686307, 0.13313116655333151, -0.05221180641094125, 0.015612632206438055},
+                      p2[6] = {-0.33332986779616663, 0.13326408875629328, -0.05349870759405957, 0.02035975918561412,
+                               -0.006259339053780887, 0.0010582645191130175},
+                      d0[2] = {-0.9962246727531868, 0.5891438049699291},
+                      d1[3] = {-0.9987269598609544, 0.6450333997432267, -0.26778585379807474},
+                      d2[5] = {-0.9995997320729791, 0.6610899884908895, -0.3512581265035661, 0.13764969240636943,
+                               -0.027911494186148036};
   ScoreParams p;
   memset(&p, 0, sizeof(p));
   p.slopes = slopes;
   p.prefix = prefix;
-  p.c[0] = (float)unit;
+  p.c0 = (float)unit;
   if (softcap > 0.f) {
     const double cap2 = softcap * 1.4426950408889634, k = unit / cap2;  // u = k s
-    double c = unit;
-    for (int i = 0; i < 5; ++i, c *= k * k) p.c[i] = (float)(c * a[i]);
+    auto scaled = [k](const double* from, int n, double first, float* to) {  // first, then first k^2 from[0], ...
+      double c = first;
+      for (int i = 0; i < n; ++i) to[i] = (float)((c *= k * k) * from[i]);
+    };
+    p.t0[0] = p.t1[0] = p.t2[0] = (float)unit;
+    scaled(p0, 3, unit, p.t0 + 1);
+    scaled(p1, 4, unit, p.t1 + 1);
+    scaled(p2, 6, unit, p.t2 + 1);
+    scaled(d0, 2, 1.0, p.g0);
+    scaled(d1, 3, 1.0, p.g1);
+    scaled(d2, 5, 1.0, p.g2);
+    const double at[kTiers] = {0.4, 0.6, 1.0};
+    for (int i = 0; i < kTiers; ++i) p.lim[i] = (float)(at[i] / k);
     p.cap2 = (float)cap2;
     p.inv_cap2 = (float)(1.0 / cap2);
-    p.lim = (float)(0.6 / k);
     p.e2 = (float)(2.0 * k * 1.4426950408889634);
   }
   return p;

@@ -1,4 +1,5 @@
-// Marshals torch tensors into the C ABI's cache calls and the rotation.  They serve single tokens,
+// Marshals torch tensors into the C ABI's cache calls, the rotation and the attention with changed scores.  They
+// serve single tokens and short sequences,
 // whose kernels take a few microseconds; describing a call's tensors through
 // Python and ctypes takes 15 to 27 us on the host, here 5 to 9.
 //
@@ -11,6 +12,7 @@
 #include <algorithm>
 
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -26,6 +28,12 @@ decltype(&ring_attn_cache_fwd) g_fwd;
 decltype(&ring_attn_cache_workspace_size) g_ws_size;
 decltype(&ring_attn_scored_cache_fwd) g_scored_fwd;
 decltype(&ring_attn_rope) g_rope;
+decltype(&ring_attn_scored_fwd) g_sfwd;
+decltype(&ring_attn_scored_bwd) g_sbwd;
+decltype(&ring_attn_scored_varlen_fwd) g_svfwd;
+decltype(&ring_attn_scored_varlen_bwd) g_svbwd;
+decltype(&ring_attn_workspace_size) g_bwd_ws;
+decltype(&ring_attn_varlen_workspace_size) g_varlen_ws;
 
 #define RA_REFUSE(cond, ...) TORCH_CHECK_VALUE(!(cond), __VA_ARGS__)
 
@@ -297,12 +305,165 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---------------------------------------------------------------- attention with changed scores
+// Tensors of one call, on q's device.
+struct OnDevice {
+  int index;
+  explicit OnDevice(PyObject* q) : index(-1) {
+    RA_REFUSE(!THPVariable_Check(q) || !THPVariable_Unpack(q).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
+    index = THPVariable_Unpack(q).get_device();
+  }
+  const at::Tensor& operator()(PyObject* o) const {
+    RA_REFUSE(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
+    const at::Tensor& t = THPVariable_Unpack(o);
+    RA_REFUSE(t.get_device() != index, "tensor on ", t.device(), ", q on cuda:", index);
+    return t;
+  }
+};
+// A result that the caller gave, or a new one.
+struct Result {
+  PyObject* mine;
+  at::Tensor t;
+  ra_tensor d;
+  template <class F>
+  Result(PyObject* o, const OnDevice& on, F&& make) : mine(given(o) ? o : nullptr), t(mine ? on(o) : make()), d(describe(t, t.dim())) {}
+  PyObject* out() const { return mine ? Py_NewRef(mine) : THPVariable_Wrap(t); }
+};
+struct Space {
+  at::Tensor t;
+  Space(PyObject* o, const OnDevice& dev, size_t need) {
+    if (given(o)) {
+      t = dev(o);
+      RA_REFUSE(!t.is_contiguous(), "workspace must be contiguous");
+    } else if (need) {
+      t = at::empty({(int64_t)need}, on(dev.index, at::kByte));
+    }
+  }
+  void* data() const { return t.defined() ? t.data_ptr() : nullptr; }
+  size_t bytes() const { return t.defined() ? t.nbytes() : 0; }
+};
+struct How {
+  int layout, shards, causal;
+  float scale;
+};
+// layout, n_shards, causal, scale
+How how(PyObject* const* a) {
+  How h{(int)PyLong_AsLong(a[0]), (int)PyLong_AsLong(a[1]), truth(a[2]), (float)PyFloat_AsDouble(a[3])};
+  if (PyErr_Occurred()) throw python_error();
+  return h;
+}
+const ra_scores* scores_of(PyObject* t, int index, int64_t h, int64_t n) {
+  RA_REFUSE(!given(t), "scores must be a Scores");
+  return scores_arg(t, index, h, n);
+}
+at::Tensor four(const at::Tensor& q) {
+  RA_REFUSE(q.dim() != 4, "expected a 4-D tensor, got ", q.sizes());
+  return q;
+}
+
+// (q, k, v, layout, n_shards, causal, scale, scores, out, lse) -> (status, out, lse)
+PyObject* scored_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 10, "10 arguments");
+  const OnDevice dev(a[0]);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
+  const at::Tensor q = four(dev(a[0]));
+  const ra_tensor tq = describe(q, 4), tk = describe(dev(a[1]), 4), tv = describe(dev(a[2]), 4);
+  const How x = how(a + 3);
+  const ra_scores* z = scores_of(a[7], dev.index, q.size(1), q.size(0));
+  Result out(a[8], dev, [&] { return at::empty_like(q); });
+  Result lse(a[9], dev, [&] { return at::empty({q.size(0), q.size(1), q.size(2)}, on(dev.index, at::kFloat)); });
+  const int status = g_sfwd(&tq, &tk, &tv, x.layout, x.shards, x.causal, x.scale, z, &out.d, &lse.d, current_stream(dev.index));
+  return Py_BuildValue("(iNN)", status, out.out(), lse.out());
+  END_HANDLE_TH_ERRORS
+}
+
+// (dout, q, k, v, out, lse, layout, n_shards, causal, scale, scores, dq, dk, dv, workspace) -> (status, dq, dk, dv)
+PyObject* scored_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 15, "15 arguments");
+  const OnDevice dev(a[1]);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
+  const at::Tensor q = four(dev(a[1]));
+  ra_tensor t[6];
+  for (int i = 0; i < 6; ++i) t[i] = describe(dev(a[i]), dev(a[i]).dim());
+  const How x = how(a + 6);
+  const ra_scores* z = scores_of(a[10], dev.index, q.size(1), q.size(0));
+  Result dq(a[11], dev, [&] { return at::empty_like(q); });
+  Result dk(a[12], dev, [&] { return at::empty_like(dev(a[2])); });
+  Result dv(a[13], dev, [&] { return at::empty_like(dev(a[3])); });
+  const Space ws(a[14], dev, g_bwd_ws(RA_OP_BWD, q.size(0), q.size(1), q.size(2), q.size(3), x.shards));
+  const int status = g_sbwd(&t[0], &t[1], &t[2], &t[3], &t[4], &t[5], x.layout, x.shards, x.causal, x.scale, z, &dq.d, &dk.d,
+                            &dv.d, ws.data(), ws.bytes(), current_stream(dev.index));
+  return Py_BuildValue("(iNNN)", status, dq.out(), dk.out(), dv.out());
+  END_HANDLE_TH_ERRORS
+}
+
+// The prefix sums of a varlen call, its longest sequence (max_seqlen, if given) and q's heads and head dim.
+struct Packed {
+  CuArg cu;
+  int32_t longest;
+  int64_t h, d;
+  Packed(PyObject* dev, PyObject* host, PyObject* max_seqlen, const at::Tensor& q, int index)
+      : cu(cu_arg(dev, host, CacheArg{nullptr, index, 0, 0})), longest(0), h(0), d(0) {
+    RA_REFUSE(q.dim() != 3, "expected a 3-D tensor, got ", q.sizes());
+    const long m = given(max_seqlen) ? PyLong_AsLong(max_seqlen) : (long)cu.max_new();
+    if (PyErr_Occurred()) throw python_error();
+    longest = (int32_t)std::min<long>(std::max<long>(m, -1), INT32_MAX);
+    h = q.size(0) == cu.total ? q.size(1) : q.size(0);
+    d = q.size(2);
+  }
+};
+
+// (q, k, v, cu's device array, its host array, max_seqlen, layout, n_shards, causal, scale, scores, out, lse, workspace) -> (status, out, lse)
+PyObject* scored_varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 14, "14 arguments");
+  const OnDevice dev(a[0]);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
+  const at::Tensor& q = dev(a[0]);
+  const Packed p(a[3], a[4], a[5], q, dev.index);
+  const ra_tensor tq = describe(q, 3), tk = describe(dev(a[1]), 3), tv = describe(dev(a[2]), 3);
+  const How x = how(a + 6);
+  const ra_scores* z = scores_of(a[10], dev.index, p.h, p.cu.n);
+  Result out(a[11], dev, [&] { return at::empty_like(q); });
+  Result lse(a[12], dev, [&] { return at::empty({p.h, p.cu.total}, on(dev.index, at::kFloat)); });
+  const Space ws(a[13], dev, g_varlen_ws(RA_OP_FWD, p.cu.total, p.h, p.d, x.layout, x.shards));
+  const int status = g_svfwd(&tq, &tk, &tv, p.cu.dev, p.cu.host, p.cu.n, p.longest, x.layout, x.shards, x.causal, x.scale, z,
+                             &out.d, &lse.d, ws.data(), ws.bytes(), current_stream(dev.index));
+  return Py_BuildValue("(iNN)", status, out.out(), lse.out());
+  END_HANDLE_TH_ERRORS
+}
+
+// (dout, q, k, v, out, lse, cu's device array, its host array, max_seqlen, layout, n_shards, causal, scale, scores, dq, dk, dv, workspace)
+// -> (status, dq, dk, dv)
+PyObject* scored_varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_VALUE(n == 18, "18 arguments");
+  const OnDevice dev(a[1]);
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
+  const at::Tensor& q = dev(a[1]);
+  const Packed p(a[6], a[7], a[8], q, dev.index);
+  ra_tensor t[6];
+  for (int i = 0; i < 6; ++i) t[i] = describe(dev(a[i]), dev(a[i]).dim());
+  const How x = how(a + 9);
+  const ra_scores* z = scores_of(a[13], dev.index, p.h, p.cu.n);
+  Result dq(a[14], dev, [&] { return at::empty_like(q); });
+  Result dk(a[15], dev, [&] { return at::empty_like(dev(a[2])); });
+  Result dv(a[16], dev, [&] { return at::empty_like(dev(a[3])); });
+  const Space ws(a[17], dev, g_varlen_ws(RA_OP_BWD, p.cu.total, p.h, p.d, x.layout, x.shards));
+  const int status = g_svbwd(&t[0], &t[1], &t[2], &t[3], &t[4], &t[5], p.cu.dev, p.cu.host, p.cu.n, p.longest, x.layout, x.shards,
+                             x.causal, x.scale, z, &dq.d, &dk.d, &dv.d, ws.data(), ws.bytes(), current_stream(dev.index));
+  return Py_BuildValue("(iNNN)", status, dq.out(), dk.out(), dv.out());
+  END_HANDLE_TH_ERRORS
+}
+
 // The library's functions, by address.
 PyObject* use(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  TORCH_CHECK_VALUE(n == 6, "6 arguments");
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  TORCH_CHECK_VALUE(n == 12, "12 arguments");
+  void* p[12];
+  for (int i = 0; i < 12; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null function");
@@ -315,6 +476,12 @@ PyObject* use(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_ws_size = reinterpret_cast<decltype(g_ws_size)>(p[3]);
   g_scored_fwd = reinterpret_cast<decltype(g_scored_fwd)>(p[4]);
   g_rope = reinterpret_cast<decltype(g_rope)>(p[5]);
+  g_sfwd = reinterpret_cast<decltype(g_sfwd)>(p[6]);
+  g_sbwd = reinterpret_cast<decltype(g_sbwd)>(p[7]);
+  g_svfwd = reinterpret_cast<decltype(g_svfwd)>(p[8]);
+  g_svbwd = reinterpret_cast<decltype(g_svbwd)>(p[9]);
+  g_bwd_ws = reinterpret_cast<decltype(g_bwd_ws)>(p[10]);
+  g_varlen_ws = reinterpret_cast<decltype(g_varlen_ws)>(p[11]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -327,6 +494,10 @@ PyMethodDef g_methods[] = {{"use", fast(use), METH_FASTCALL, nullptr},
                            {"cache_read", fast(cache_read), METH_FASTCALL, nullptr},
                            {"cache_fwd", fast(cache_fwd), METH_FASTCALL, nullptr},
                            {"rope", fast(rope), METH_FASTCALL, nullptr},
+                           {"scored_fwd", fast(scored_fwd), METH_FASTCALL, nullptr},
+                           {"scored_bwd", fast(scored_bwd), METH_FASTCALL, nullptr},
+                           {"scored_varlen_fwd", fast(scored_varlen_fwd), METH_FASTCALL, nullptr},
+                           {"scored_varlen_bwd", fast(scored_varlen_bwd), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ra_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

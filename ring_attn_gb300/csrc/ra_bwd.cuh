@@ -355,30 +355,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) pp[c] = pack_bf16x2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
       } else {
-        const uint64_t inv2 = f32x2(p.sc.inv_cap2, p.sc.inv_cap2), one2 = f32x2(1.f, 1.f);
-        ScoreTile<SC> change{p.sc, {}};
-        bool small = true, line = true;
+        ScoreTile<SC> change(p);
+        int tier = 0;
+        bool line = true;
         if constexpr ((SC & SC_BIAS) != 0) {
-          change.bias = bias_line(tile_tokens(p, win, r, qt * kTileM + 64 * half), gk, max(c_lo, 0), min(c_hi, 64), slope2);
+          change.bias =
+              bias_line(tile_tokens(p, win, r, qt * kTileM + 64 * half), gk, max(c_lo, 0), min(c_hi, 64), slope2);
           line = __all_sync(0xffffffffu, change.bias.line);
         }
-        if constexpr ((SC & SC_CAP) != 0) small = all_small(v, p.sc.lim);
+        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
         // v becomes P^T times the cap's derivative
-        with_score_flags<SC>(small, line, [&](auto sm, auto li) {
+        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
+          constexpr int kTier = decltype(ti)::value;
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
             const float4 l = ls4[c / 4];
-            uint64_t y, z;
-            change.template operator()<decltype(sm)::value, decltype(li)::value>(c, __uint_as_float(v[c]),
-                                                                                 __uint_as_float(v[c + 1]), y, z);
+            uint64_t w;
             float x0, x1;
-            f32x2_split(add_f32x2(z, c % 4 ? f32x2(l.z, l.w) : f32x2(l.x, l.y)), x0, x1);
+            f32x2_split(change.template operator()<kTier, decltype(li)::value, false>(
+                            c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                            c % 4 ? f32x2(l.z, l.w) : f32x2(l.x, l.y), w),
+                        x0, x1);
             x0 = fast_exp2(x0), x1 = fast_exp2(x1);
             pp[c / 2] = pack_bf16x2(x0, x1);
-            if constexpr ((SC & SC_CAP) != 0) {
-              const uint64_t th = mul_f32x2(y, inv2);
-              f32x2_split(mul_f32x2(f32x2(x0, x1), fma_f32x2(neg_f32x2(th), th, one2)), x0, x1);
-            }
+            if constexpr ((SC & SC_CAP) != 0)
+              f32x2_split(mul_f32x2(f32x2(x0, x1), change.template derivative<kTier>(w)), x0, x1);
             v[c] = __float_as_uint(x0), v[c + 1] = __float_as_uint(x1);
           }
         });
@@ -718,7 +719,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       gq = tok(p, r, valid ? i : max(qr.i_last, 0));
     // this row's statistics, negated (padding rows: -lse2 = -inf, -D = 0, so P = dS = 0)
     const long long srow = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
-    const uint64_t nl2 = f32x2(__ldg(p.nlse2 + srow), __ldg(p.nlse2 + srow));
+    const float nl = __ldg(p.nlse2 + srow);
+    const uint64_t nl2 = f32x2(nl, nl);
     const uint64_t nD2 = f32x2(__ldg(p.nD + srow), __ldg(p.nD + srow));
     const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
     float slope2 = 0.f;
@@ -778,28 +780,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[c + 1] = __float_as_uint(fast_exp2(x1));
         }
       } else {
-        const uint64_t inv2 = f32x2(p.sc.inv_cap2, p.sc.inv_cap2), one2 = f32x2(1.f, 1.f);
-        ScoreTile<SC> change{p.sc, {}};
-        bool small = true, line = true;
+        ScoreTile<SC> change(p);
+        int tier = 0;
+        bool line = true;
         if constexpr ((SC & SC_BIAS) != 0) {
-          change.bias = bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, max(c_lo, 0), min(c_hi, 64), slope2);
+          change.bias =
+              bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, max(c_lo, 0), min(c_hi, 64), slope2);
           line = __all_sync(0xffffffffu, change.bias.line);
+          change.bias.off += nl;
         }
-        if constexpr ((SC & SC_CAP) != 0) small = all_small(v, p.sc.lim);
+        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
         // P times the cap's derivative
-        with_score_flags<SC>(small, line, [&](auto sm, auto li) {
+        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
+          constexpr int kTier = decltype(ti)::value;
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            uint64_t y, z;
-            change.template operator()<decltype(sm)::value, decltype(li)::value>(c, __uint_as_float(v[c]),
-                                                                                 __uint_as_float(v[c + 1]), y, z);
+            uint64_t w;
             float x0, x1;
-            f32x2_split(add_f32x2(z, nl2), x0, x1);
+            f32x2_split(change.template operator()<kTier, decltype(li)::value, decltype(li)::value>(
+                            c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), nl2, w),
+                        x0, x1);
             x0 = fast_exp2(x0), x1 = fast_exp2(x1);
-            if constexpr ((SC & SC_CAP) != 0) {
-              const uint64_t th = mul_f32x2(y, inv2);
-              f32x2_split(mul_f32x2(f32x2(x0, x1), fma_f32x2(neg_f32x2(th), th, one2)), x0, x1);
-            }
+            if constexpr ((SC & SC_CAP) != 0)
+              f32x2_split(mul_f32x2(f32x2(x0, x1), change.template derivative<kTier>(w)), x0, x1);
             v[c] = __float_as_uint(x0), v[c + 1] = __float_as_uint(x1);
           }
         });
@@ -1098,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       }
       tc_fence_after();
-      ScoreTile<SC> change{p.sc, {}};
+      ScoreTile<SC> change(p);
       TileTokens tokens;
       if constexpr ((SC & SC_BIAS) != 0) tokens = tile_tokens(p, win, s, kt * kTileN);
       // half a row at a time, so that it stays in registers
@@ -1111,25 +1114,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(LY::kSRead + t));
         }
-        bool small = true, line = true;
+        int tier = 0;
+        bool line = true;
         if constexpr ((SC & SC_BIAS) != 0) {
-          tokens.t0 += hh ? 64 * tokens.st : 0, tokens.t1 += hh ? 64 * tokens.st : 0, tokens.cb -= 64 * hh;
+          if (hh) tokens.t0 += 64 * tokens.st, tokens.t1 += 64 * tokens.st, tokens.cb -= 64;
           change.bias = bias_line(tokens, gq, max(c_lo - 64 * hh, 0), min(c_hi - 64 * hh, 64), slope2);
           line = __all_sync(0xffffffffu, change.bias.line);
+          change.bias.off += nl;
         }
-        if constexpr ((SC & SC_CAP) != 0) small = all_small(v, p.sc.lim);
-        with_score_flags<SC>(small, line, [&](auto sm, auto li) {
+        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
+        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            float x0, x1;
+            const uint64_t sv = f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+            uint64_t x;
             if constexpr (kChanged) {
-              uint64_t y, z;
-              change.template operator()<decltype(sm)::value, decltype(li)::value>(c, __uint_as_float(v[c]),
-                                                                                   __uint_as_float(v[c + 1]), y, z);
-              f32x2_split(add_f32x2(z, nl2), x0, x1);
+              uint64_t w;
+              x = change.template operator()<decltype(ti)::value, decltype(li)::value, decltype(li)::value>(c, sv, nl2, w);
             } else {
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nl2), x0, x1);
+              x = fma_f32x2(sv, sc2, nl2);
             }
+            float x0, x1;
+            f32x2_split(x, x0, x1);
             v[c] = __float_as_uint(fast_exp2(x0)), v[c + 1] = __float_as_uint(fast_exp2(x1));
           }
         });

@@ -353,28 +353,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
       tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(v + 64));
       tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(v + 96));
+      // changed scores: in full tiles the largest follows from the largest product (the cap is monotonic, the bias a
+      // line), and a score becomes a weight in one go; else they are changed where they lie first
+      ScoreTile<SC> change(p);
+      int tier = 0;
+      bool in_place = false;
       if constexpr (kChanged) {
-        // scores as they count, in log2 units
         tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
         tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
-        ScoreTile<SC> change{p.sc, {}};
-        bool small = true, line = true;
+        bool line = true, loose = false;
         if constexpr ((SC & SC_BIAS) != 0) {
           change.bias = bias_line(tile_tokens(p, win, s, kt * kTileN), gq, c_lo, c_hi, slope2);
           line = __all_sync(0xffffffffu, change.bias.line);
+          loose = fabsf(change.bias.slp) * kTileN > kLoose;
         }
-        if constexpr ((SC & SC_CAP) != 0) small = all_small(v, p.sc.lim);
-        with_score_flags<SC>(small, line, [&](auto sm, auto li) {
+        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
+        in_place = __any_sync(0xffffffffu, masked || loose) || !line;
+        if (in_place)
+          with_score_flags<SC>(max(tier, 2), line, [&](auto ti, auto li) {
+            if constexpr (decltype(ti)::value >= 2 || (SC & SC_CAP) == 0) {
 #pragma unroll
-          for (int c = 0; c < kTileN; c += 2) {
-            uint64_t y, z;
-            change.template operator()<decltype(sm)::value, decltype(li)::value>(c, __uint_as_float(v[c]),
-                                                                                 __uint_as_float(v[c + 1]), y, z);
-            float z0, z1;
-            f32x2_split(z, z0, z1);
-            v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
-          }
-        });
+              for (int c = 0; c < kTileN; c += 2) {
+                uint64_t w;
+                float z0, z1;
+                f32x2_split(change.template operator()<decltype(ti)::value, decltype(li)::value, decltype(li)::value>(
+                                c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), 0, w),
+                            z0, z1);
+                v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
+              }
+            }
+          });
       }
       float mc[4];
 #pragma unroll
@@ -401,7 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // raw scores: the scale is > 0, so max(s) * scale = max(s * scale)
       float mx = fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3]));
-      if constexpr (!kChanged) mx *= p.scale_log2;
+      if constexpr (!kChanged)
+        mx *= p.scale_log2;
+      else if (!in_place)
+        mx = change.most(mx, tier, kTileN);
       float alpha = 1.f;
       if (mx > -INFINITY) {
         if (m_run == -INFINITY) {
@@ -418,20 +429,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       // s * scale - m and the sums run two lanes per instruction (f32x2).
       const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-m_use, -m_use);
       uint64_t acc[4] = {0, 0, 0, 0};  // four pairs of partial row sums (+0.0f bits)
+      auto weights = [&](auto minus_m) {  // of columns c, c + 1, from their scores
 #pragma unroll
-      for (int c32 = 0; c32 < kTileN / 32; ++c32) {
-        uint32_t pk[16];
+        for (int c32 = 0; c32 < kTileN / 32; ++c32) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int c = c32 * 32 + 2 * u;
-          float x0, x1;
-          const uint64_t sv = f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-          f32x2_split(kChanged ? add_f32x2(sv, nm2) : fma_f32x2(sv, sc2, nm2), x0, x1);
-          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-          acc[u & 3] = add_f32x2(acc[u & 3], f32x2(e0, e1));
-          pk[u] = pack_bf16x2(e0, e1);
+          for (int u = 0; u < 16; ++u) {
+            const int c = c32 * 32 + 2 * u;
+            float x0, x1;
+            f32x2_split(minus_m(c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]))), x0, x1);
+            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+            acc[u & 3] = add_f32x2(acc[u & 3], f32x2(e0, e1));
+            pk[u] = pack_bf16x2(e0, e1);
+          }
+          tmem_st16(tS + c32 * 16, pk);
         }
-        tmem_st16(tS + c32 * 16, pk);
+      };
+      if constexpr (!kChanged) {
+        weights([&](int, uint64_t sv) { return fma_f32x2(sv, sc2, nm2); });
+      } else if (in_place) {
+        weights([&](int, uint64_t sv) { return add_f32x2(sv, nm2); });
+      } else {
+        change.bias.off -= m_use;
+        with_score_flags<SC>(tier, true, [&](auto ti, auto li) {
+          if constexpr (decltype(li)::value != 0)
+            weights([&](int c, uint64_t sv) {
+              uint64_t w;
+              return change.template operator()<decltype(ti)::value, true, true>(c, sv, nm2, w);
+            });
+        });
       }
       float s0, s1;
       f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);

@@ -64,10 +64,15 @@ struct BwdParams {
 enum : int { SC_CAP = 1, SC_BIAS = 2, SC_ON = 4 };
 
 // Scores are carried in log2 units: z = log2(e) * (softcap * tanh(x / softcap) - slope * distance).
+// The cap of a product s is s times a polynomial in w = s^2, of degree 3, 4 or 6 by how large
+// the scores of a tile are, with a polynomial for its derivative.
+constexpr int kTiers = 3;
 struct ScoreParams {
   float cap2;               // softcap * log2(e)
-  float c[5];               // z = s (c0 + w (c1 + ...)), w = s^2, of a product s with |s| <= lim
-  float lim;
+  float c0;                 // without a cap z = c0 s
+  float t0[4], t1[5], t2[7];
+  float g0[2], g1[3], g2[5];  // d z / d (scale s) = 1 + w (g[0] + ...)
+  float lim[kTiers];        // |s| up to which the polynomials hold
   float e2;                 // any s: z = cap2 - 2 cap2 / (1 + 2^(e2 s))
   float inv_cap2;           // tanh(x / softcap) = z * inv_cap2
   const float* slopes;      // per query head

@@ -6,13 +6,15 @@
 // and a gradient with respect to z becomes one with respect to scale * s by the factor
 // 1 - (y / cap2)^2.
 //
-// The cap.  tanh(u) = u (1 + w (c1 + w (c2 + w (c3 + w c4)))), w = u^2, on |u| <= 0.6: minimax
-// coefficients, 2^-23.5 off relatively and 2^-22.4 as evaluated; the scales are folded into the
-// coefficients, so that a score costs five multiply-adds, two lanes an instruction.  Beyond that
-// tanh(u) = 1 - 2 / (1 + e^(2u)) with the hardware's exponential and reciprocal: right for
-// every u (infinite ones too), off by about 2^-22 absolutely, and twice as many instructions of the
-// special-function unit on top of the softmax's.  A warp takes the first way for the scores that it has in
-// registers when none of them is beyond: caps are meant to be far above most scores.
+// The cap.  tanh(u) = u (1 + w P(w)), w = u^2, with P of degree 2, 3 or 5 for |u| up to 0.4, 0.6 or 1: minimax
+// coefficients, off relatively by 2^-23.1, 2^-23.5, 2^-24.1 (2^-22.4 as evaluated).  The scales are folded into
+// the coefficients, so that a score costs five, six or eight multiply-adds where a plain one costs one, and
+// they are what the kernels with a cap wait for: a multiply-add takes a cycle of its pipe for every 32
+// scores, in pairs or not, the exponential four.  The derivative is 1 + w G(w) with G of degree 1, 2 or 4, off
+// by 2^-14.1, 2^-15.4, 2^-16.7, next to the half step of bf16 (2^-8) that the gradient is rounded by as an operand.
+// Beyond 1, tanh(u) = 1 - 2 / (1 + e^(2u)) with the hardware's exponential and reciprocal (4 and 8 cycles on top
+// of the softmax's 4): right for every u, infinite ones too, off by about 2^-22 absolutely.
+// A warp goes by the largest score that it has in registers: caps are meant to be far above most scores.
 //
 // The bias.  In a tile the distance is a - st c for column c, or its negative, or (a tile
 // that the row's own token, or the seam of a zigzag shard's two chunks, lies in) one line left
@@ -35,6 +37,10 @@ struct TileTokens {
   int t0, t1, st, cb;
 };
 constexpr int kNoSeam = 1 << 20;
+
+// A softmax's offset may be this much (log2 units) above the largest score: weights down to 2^-24 of the largest
+// are then still normal numbers, in bf16, too.
+constexpr float kLoose = 88.f;
 
 // Columns: local positions [j0, ...) of shard s (win: the row's window, for varlen).
 template <class P>
@@ -80,79 +86,139 @@ __device__ __forceinline__ BiasLine bias_line(const TileTokens& x, int own, int 
   return r;
 }
 
-// Constants of a tile's transformation, as the compiler keeps them in registers.
+template <int N>
+__device__ __forceinline__ uint64_t polynomial(uint64_t w, const float (&c)[N]) {
+  uint64_t h = f32x2(c[N - 1], c[N - 1]);
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) h = fma_f32x2(w, h, f32x2(c[i], c[i]));
+  return h;
+}
+
+// How a tile's scores are changed.  kTier: which polynomial holds for all of the warp's scores (kTiers: none).
 template <int SC>
 struct ScoreTile {
   const ScoreParams& sc;
   BiasLine bias;
 
-  // Two products s0, s1 of columns c, c + 1: y (capped) and z, pairs.  kSmall: |s| <= lim; kLine: bias.line.
-  template <bool kSmall, bool kLine>
-  __device__ __forceinline__ void operator()(int c, float s0, float s1, uint64_t& y, uint64_t& z) const {
-    uint64_t b = 0;
+  template <class P>  // kernel parameters with `sc`
+  __device__ __forceinline__ explicit ScoreTile(const P& p) : sc(p.sc), bias() {}
+
+  // Two products s of columns c, c + 1: x = z + add, and w, from which `derivative` follows.  kLine: bias.line.
+  // kFolded: add is the same for all columns, and bias.off has it (only where kLine is).
+  template <int kTier, bool kLine, bool kFolded>
+  __device__ __forceinline__ uint64_t operator()(int c, uint64_t s, uint64_t add, uint64_t& w) const {
     if constexpr ((SC & SC_BIAS) != 0) {
       float b0, b1;
       if constexpr (kLine) {
         b0 = fmaf((float)c, bias.slp, bias.off), b1 = fmaf((float)(c + 1), bias.slp, bias.off);
+        add = kFolded ? f32x2(b0, b1) : add_f32x2(f32x2(b0, b1), add);
       } else {
-        b0 = bias.neg * fabsf(fmaf(-(float)c, bias.st, c < bias.cb ? bias.a : bias.b));
-        b1 = bias.neg * fabsf(fmaf(-(float)(c + 1), bias.st, c + 1 < bias.cb ? bias.a : bias.b));
+        float a0, a1;
+        f32x2_split(add, a0, a1);
+        b0 = fmaf(bias.neg, fabsf(fmaf(-(float)c, bias.st, c < bias.cb ? bias.a : bias.b)), a0);
+        b1 = fmaf(bias.neg, fabsf(fmaf(-(float)(c + 1), bias.st, c + 1 < bias.cb ? bias.a : bias.b)), a1);
+        add = f32x2(b0, b1);
       }
-      b = f32x2(b0, b1);
     }
-    const uint64_t s = f32x2(s0, s1);
+    return capped<kTier>(s, add, w);
+  }
+  // The same without the bias.
+  template <int kTier>
+  __device__ __forceinline__ uint64_t capped(uint64_t s, uint64_t add, uint64_t& w) const {
     if constexpr ((SC & SC_CAP) == 0) {
-      y = 0;  // (not asked for)
-      z = (SC & SC_BIAS) ? fma_f32x2(s, f32x2(sc.c[0], sc.c[0]), b) : mul_f32x2(s, f32x2(sc.c[0], sc.c[0]));
-    } else if constexpr (kSmall) {
-      const uint64_t w = mul_f32x2(s, s);
-      uint64_t h = fma_f32x2(w, f32x2(sc.c[4], sc.c[4]), f32x2(sc.c[3], sc.c[3]));
-      h = fma_f32x2(w, h, f32x2(sc.c[2], sc.c[2]));
-      h = fma_f32x2(w, h, f32x2(sc.c[1], sc.c[1]));
-      h = fma_f32x2(w, h, f32x2(sc.c[0], sc.c[0]));
-      y = mul_f32x2(s, h);
-      z = (SC & SC_BIAS) ? fma_f32x2(s, h, b) : y;
+      w = 0;
+      return fma_f32x2(s, f32x2(sc.c0, sc.c0), add);
+    } else if constexpr (kTier < kTiers) {
+      w = mul_f32x2(s, s);
+      return fma_f32x2(s, kTier == 0 ? polynomial(w, sc.t0) : kTier == 1 ? polynomial(w, sc.t1) : polynomial(w, sc.t2), add);
     } else {
       float e0, e1;
       f32x2_split(mul_f32x2(s, f32x2(sc.e2, sc.e2)), e0, e1);
       const uint64_t r = f32x2(fast_rcp(fast_exp2(e0) + 1.f), fast_rcp(fast_exp2(e1) + 1.f));
-      y = fma_f32x2(r, f32x2(-2.f * sc.cap2, -2.f * sc.cap2), f32x2(sc.cap2, sc.cap2));
-      z = (SC & SC_BIAS) ? add_f32x2(y, b) : y;
+      w = fma_f32x2(r, f32x2(-2.f * sc.cap2, -2.f * sc.cap2), f32x2(sc.cap2, sc.cap2));  // the capped score
+      return add_f32x2(w, add);
+    }
+  }
+  // The largest of a tile's z, or more by at most kLoose, from its largest product, for a tile whose bias is a line.
+  __device__ __forceinline__ float most(float s, int tier, int n) const {
+    if (s == -INFINITY) return s;
+    uint64_t w;
+    float z = 0.f, unused;
+    const uint64_t two = f32x2(s, s);
+    f32x2_split(!(SC & SC_CAP) || tier == 0 ? capped<0>(two, 0, w)
+                : tier == 1                 ? capped<1>(two, 0, w)
+                : tier == 2                 ? capped<2>(two, 0, w)
+                                            : capped<kTiers>(two, 0, w),
+                z, unused);
+    return (SC & SC_BIAS) ? z + fmaxf(bias.off, fmaf((float)(n - 1), bias.slp, bias.off)) : z;
+  }
+  // of the cap, from the w of the calls above
+  template <int kTier>
+  __device__ __forceinline__ uint64_t derivative(uint64_t w) const {
+    const uint64_t one = f32x2(1.f, 1.f);
+    if constexpr (kTier < kTiers) {
+      return fma_f32x2(w, kTier == 0 ? polynomial(w, sc.g0) : kTier == 1 ? polynomial(w, sc.g1) : polynomial(w, sc.g2), one);
+    } else {
+      const uint64_t th = mul_f32x2(w, f32x2(sc.inv_cap2, sc.inv_cap2));
+      return fma_f32x2(neg_f32x2(th), th, one);
     }
   }
 };
 
-template <bool B>
-struct Flag {
-  static constexpr bool value = B;
+// Plain scores (or a prefix alone): nothing to change.
+struct NoScoreTile {
+  BiasLine bias;
+  template <class P>
+  __device__ __forceinline__ explicit NoScoreTile(const P&) {}
+  __device__ __forceinline__ float most(float s, int, int) const { return s; }
 };
-// f(small, line) with the flags as compile-time constants; both are the same in the whole warp.
+template <>
+struct ScoreTile<0> : NoScoreTile {
+  using NoScoreTile::NoScoreTile;
+};
+template <>
+struct ScoreTile<SC_ON> : NoScoreTile {
+  using NoScoreTile::NoScoreTile;
+};
+
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+// f(tier, line) with both, which are the same in the whole warp, as compile-time constants.  Tiles without a line
+// are few: one polynomial serves them.
 template <int SC, class F>
-__device__ __forceinline__ void with_score_flags(bool small, bool line, F&& f) {
-  if (!(SC & SC_CAP) || small) {
-    if (!(SC & SC_BIAS) || line)
-      f(Flag<true>{}, Flag<true>{});
-    else
-      f(Flag<true>{}, Flag<false>{});
-  } else {
-    if (!(SC & SC_BIAS) || line)
-      f(Flag<false>{}, Flag<true>{});
-    else
-      f(Flag<false>{}, Flag<false>{});
-  }
+__device__ __forceinline__ void with_score_flags(int tier, bool line, F&& f) {
+  if constexpr ((SC & SC_BIAS) != 0)
+    if (!line) {
+      if ((SC & SC_CAP) && tier == kTiers)
+        f(Const<kTiers>{}, Const<0>{});
+      else
+        f(Const<2>{}, Const<0>{});
+      return;
+    }
+  if (!(SC & SC_CAP) || tier == 0)
+    f(Const<0>{}, Const<1>{});
+  else if (tier == 1)
+    f(Const<1>{}, Const<1>{});
+  else if (tier == 2)
+    f(Const<2>{}, Const<1>{});
+  else
+    f(Const<kTiers>{}, Const<1>{});
 }
 
-// Whether no product of N is beyond the polynomial's range, for the whole warp.
+// The polynomial that holds for N products of every lane.
 template <int N>
-__device__ __forceinline__ bool all_small(const uint32_t (&v)[N], float lim) {
-  static_assert(N % 32 == 0, "chains of 16");
+__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, float factor = 1.f) {
   float m[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < N; c += 4) {
     m[0] = fmax3f(m[0], fabsf(__uint_as_float(v[c])), fabsf(__uint_as_float(v[c + 1])));
     m[1] = fmax3f(m[1], fabsf(__uint_as_float(v[c + 2])), fabsf(__uint_as_float(v[c + 3])));
   }
-  return !__any_sync(0xffffffffu, fmaxf(m[0], m[1]) > lim);
+  // (not negative and no NaN: the bits are in the numbers' order)
+  const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(m[0], m[1]) * factor)));
+  return all <= sc.lim[0] ? 0 : all <= sc.lim[1] ? 1 : all <= sc.lim[2] ? 2 : kTiers;
 }
 
 }  // namespace ra
