@@ -22,13 +22,11 @@
 // Each tile row is split between two threads (query or key columns [0, 64) and
 // [64, 128)); ra_bwd_common.cuh describes the packed TMEM operands this gives.
 //
-// SC (ra_score.cuh): 0 for plain scores (ra_bwd.cu), else a call's cap, bias by distance or
-// prefix (ra_scored_*.cu).  The elementwise threads then change the scores as the forward does, and
-// hold P times the cap's derivative for dS.
+// SC: 0, or SC_ON for calls with a prefix that all tokens see, which changes masks only.  Capped or
+// biased scores have kernels of their own (ra_scored_bwd.cuh).
 #pragma once
 
 #include "ra_bwd_common.cuh"
-#include "ra_score.cuh"
 
 namespace ra {
 namespace {
@@ -99,7 +97,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                      const BwdParamsT<VL, SC> p) {
   using LY = DkdvLayout<D>;
-  constexpr bool kChanged = (SC & (SC_CAP | SC_BIAS)) != 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -299,12 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     RowWin win;
     int gk = 0;
     if constexpr (VL)
-      gk = make_row_win(p, k.s, min(j, p.L - 1), true, win);
+      make_row_win(p, k.s, min(j, p.L - 1), true, win);
     else
-      gk = tok(p, k.s, valid_k ? j : k.j_last);
+      gk = seen_token<decltype(p)>(tok(p, k.s, valid_k ? j : k.j_last), pre);
     bool ok = true;
     int i = 0;
-    float slope2 = 0.f;  // of the query head at hand
     auto tile = [&](int r, int qt) {
       const int st = i & 1;
       // padding query rows have -lse2 = -inf and -D = 0 (P = 0, dS = 0) without a mask
@@ -313,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         row_win_cols(p, win, r, qt * kTileM, kTileM, c_lo, c_hi);
         if (!valid_k) c_lo = c_hi = 0;
       } else if (!q_tile_full<kTileM>(p, k, r, qt)) {
-        key_query_window<kTileM>(p, valid_k, seen_token<decltype(p)>(gk, pre), r, qt, c_lo, c_hi);
+        key_query_window<kTileM>(p, valid_k, gk, r, qt, c_lo, c_hi);
       }
       c_lo -= 64 * half;
       c_hi -= 64 * half;
@@ -329,75 +325,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint32_t v[64];
       tmem_ld64(tl + LY::kTmemS + 64 * half, v);
-      uint32_t pp[32];  // P^T, bf16 pairs
-      if constexpr (!kChanged) {
-        // P^T = exp2(s * scale - lse2), s * scale - lse2 two lanes per instruction
-        const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
+      // P^T = exp2(s * scale - lse2), s * scale - lse2 two lanes per instruction
+      const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
 #pragma unroll
-        for (int c4 = 0; c4 < 16; ++c4) {
-          const float4 l = ls4[c4];
-          float x0, x1, x2, x3;
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[4 * c4]), __uint_as_float(v[4 * c4 + 1])), sc2, f32x2(l.x, l.y)),
-                      x0, x1);
-          f32x2_split(
-              fma_f32x2(f32x2(__uint_as_float(v[4 * c4 + 2]), __uint_as_float(v[4 * c4 + 3])), sc2, f32x2(l.z, l.w)),
-              x2, x3);
-          v[4 * c4 + 0] = __float_as_uint(fast_exp2(x0));
-          v[4 * c4 + 1] = __float_as_uint(fast_exp2(x1));
-          v[4 * c4 + 2] = __float_as_uint(fast_exp2(x2));
-          v[4 * c4 + 3] = __float_as_uint(fast_exp2(x3));
-        }
-        if (masked) {
-          const uint64_t mw = bit_window64(c_lo, c_hi);
+      for (int c4 = 0; c4 < 16; ++c4) {
+        const float4 l = ls4[c4];
+        float x0, x1, x2, x3;
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[4 * c4]), __uint_as_float(v[4 * c4 + 1])), sc2, f32x2(l.x, l.y)),
+                    x0, x1);
+        f32x2_split(
+            fma_f32x2(f32x2(__uint_as_float(v[4 * c4 + 2]), __uint_as_float(v[4 * c4 + 3])), sc2, f32x2(l.z, l.w)),
+            x2, x3);
+        v[4 * c4 + 0] = __float_as_uint(fast_exp2(x0));
+        v[4 * c4 + 1] = __float_as_uint(fast_exp2(x1));
+        v[4 * c4 + 2] = __float_as_uint(fast_exp2(x2));
+        v[4 * c4 + 3] = __float_as_uint(fast_exp2(x3));
+      }
+      if (masked) {
+        const uint64_t mw = bit_window64(c_lo, c_hi);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) v[c] = ((mw >> c) & 1ull) ? v[c] : 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c) pp[c] = pack_bf16x2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
-      } else {
-        ScoreTile<SC> change(p);
-        int tier = 0;
-        bool line = true;
-        if constexpr ((SC & SC_BIAS) != 0) {
-          change.bias =
-              bias_line(tile_tokens(p, win, r, qt * kTileM + 64 * half), gk, max(c_lo, 0), min(c_hi, 64), slope2);
-          line = __all_sync(0xffffffffu, change.bias.line);
-        }
-        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
-        // v becomes P^T times the cap's derivative
-        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-          constexpr int kTier = decltype(ti)::value;
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float4 l = ls4[c / 4];
-            uint64_t w;
-            float x0, x1;
-            f32x2_split(change.template operator()<kTier, decltype(li)::value, false>(
-                            c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                            c % 4 ? f32x2(l.z, l.w) : f32x2(l.x, l.y), w),
-                        x0, x1);
-            x0 = fast_exp2(x0), x1 = fast_exp2(x1);
-            pp[c / 2] = pack_bf16x2(x0, x1);
-            if constexpr ((SC & SC_CAP) != 0)
-              f32x2_split(mul_f32x2(f32x2(x0, x1), change.template derivative<kTier>(w)), x0, x1);
-            v[c] = __float_as_uint(x0), v[c + 1] = __float_as_uint(x1);
-          }
-        });
-        if (masked) {
-          const uint64_t mw = bit_window64(c_lo, c_hi);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const bool m0 = (mw >> (2 * c)) & 1ull, m1 = (mw >> (2 * c + 1)) & 1ull;
-            pp[c] &= (m0 ? 0xffffu : 0u) | (m1 ? 0xffff0000u : 0u);
-            v[2 * c] = m0 ? v[2 * c] : 0u, v[2 * c + 1] = m1 ? v[2 * c + 1] : 0u;
-          }
-        }
+        for (int c = 0; c < 64; ++c) v[c] = ((mw >> c) & 1ull) ? v[c] : 0u;
       }
       // P^T packed over the first 32 of the thread's 64 S^T columns (column m:
       // queries 2m, 2m + 1), the A operand of dV += P^T dO; the MMA thread then
       // computes the next tile's S^T over it
       {
         const uint32_t ts = tl + LY::kTmemS + 64 * half;
+        uint32_t pp[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pp[c] = pack_bf16x2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
         tmem_st16(ts, *reinterpret_cast<uint32_t(*)[16]>(pp));
         tmem_st16(ts + 16, *reinterpret_cast<uint32_t(*)[16]>(pp + 16));
         tmem_st_wait();
@@ -448,10 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     // every query head of the group meets the same tiles; the walk does not depend on the head
-    for (int g = 0; ok && g < p.G; ++g) {
-      if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + hk * p.G + g) * 1.4426950408889634f;
-      walk_q_tiles<kTileM>(p, k, p.n_qtiles, tile);
-    }
+    for (int g = 0; ok && g < p.G; ++g) walk_q_tiles<kTileM>(p, k, p.n_qtiles, tile);
     // ---------------- epilogue: warpgroup 1 writes the dV rows, warpgroup 2 the dK rows
     const long long prow = (long long)k.s * p.L + j;
     const int* rmap = VL ? p.row_map : nullptr;  // varlen in original order: rows of the caller's layout
@@ -538,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const BwdParamsT<VL, SC> p) {
   using LY = DqLayout<D>;
   constexpr int KS = LY::kKStages, VS = LY::kVStages;
-  constexpr bool kChanged = (SC & (SC_CAP | SC_BIAS)) != 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -714,17 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     RowWin win;
     int gq = 0;
     if constexpr (VL)
-      gq = make_row_win(p, r, min(i, p.L - 1), false, win);
+      make_row_win(p, r, min(i, p.L - 1), false, win);
     else
-      gq = tok(p, r, valid ? i : max(qr.i_last, 0));
+      gq = seeing_token<decltype(p)>(tok(p, r, valid ? i : max(qr.i_last, 0)), pre);
     // this row's statistics, negated (padding rows: -lse2 = -inf, -D = 0, so P = dS = 0)
     const long long srow = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
-    const float nl = __ldg(p.nlse2 + srow);
-    const uint64_t nl2 = f32x2(nl, nl);
+    const uint64_t nl2 = f32x2(__ldg(p.nlse2 + srow), __ldg(p.nlse2 + srow));
     const uint64_t nD2 = f32x2(__ldg(p.nD + srow), __ldg(p.nD + srow));
     const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
-    float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
     // warpgroup 1 copies the row's Q, warpgroup 2 its dO, into tensor memory as
     // packed bf16 (column m: head-dim elements 2m, 2m + 1) for the S and dP MMAs
     bool ok = n_tiles == 0 || wait_warp(BAR(F_QDO_FULL), 0, abort_flag, p.ctl, 64);
@@ -755,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (VL)
         row_win_cols(p, win, s, kt * kTileN, kTileN, c_lo, c_hi);
       else if (!kv_tile_full(p, qr, s, kt))
-        row_key_window(p, seeing_token<decltype(p)>(gq, pre), s, kt, c_lo, c_hi);
+        row_key_window(p, gq, s, kt, c_lo, c_hi);
       c_lo -= 64 * half;
       c_hi -= 64 * half;
       const bool masked = c_lo > 0 || c_hi < 64;
@@ -770,42 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(F_S_READ));
-      if constexpr (!kChanged) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          // P = exp2(s * scale - lse2), s * scale - lse2 two lanes per instruction
-          float x0, x1;
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nl2), x0, x1);
-          v[c] = __float_as_uint(fast_exp2(x0));
-          v[c + 1] = __float_as_uint(fast_exp2(x1));
-        }
-      } else {
-        ScoreTile<SC> change(p);
-        int tier = 0;
-        bool line = true;
-        if constexpr ((SC & SC_BIAS) != 0) {
-          change.bias =
-              bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, max(c_lo, 0), min(c_hi, 64), slope2);
-          line = __all_sync(0xffffffffu, change.bias.line);
-          change.bias.off += nl;
-        }
-        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
-        // P times the cap's derivative
-        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-          constexpr int kTier = decltype(ti)::value;
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            uint64_t w;
-            float x0, x1;
-            f32x2_split(change.template operator()<kTier, decltype(li)::value, decltype(li)::value>(
-                            c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), nl2, w),
-                        x0, x1);
-            x0 = fast_exp2(x0), x1 = fast_exp2(x1);
-            if constexpr ((SC & SC_CAP) != 0)
-              f32x2_split(mul_f32x2(f32x2(x0, x1), change.template derivative<kTier>(w)), x0, x1);
-            v[c] = __float_as_uint(x0), v[c + 1] = __float_as_uint(x1);
-          }
-        });
+      for (int c = 0; c < 64; c += 2) {
+        // P = exp2(s * scale - lse2), s * scale - lse2 two lanes per instruction
+        float x0, x1;
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nl2), x0, x1);
+        v[c] = __float_as_uint(fast_exp2(x0));
+        v[c + 1] = __float_as_uint(fast_exp2(x1));
       }
       if (masked) {
         const uint64_t mw = bit_window64(c_lo, c_hi);
@@ -876,308 +796,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ======================================================================== D
-// Changed scores only: D_i = sum_j P_ij <dO_i, v_j> and the statistics that the other two kernels
-// read, -lse * log2(e) and -D of every row.
-//
-// With plain scores D is rowsum(dO * O) of the bf16 out.  O's rounding is an error of D that the sums over a row's keys
-// do not average away, and where a bias or a small cap leaves a row few keys, dP - D is small next
-// to dP: dQ and dK were off by up to 0.54 % (one head with a slope of 1), and 0.24 % with D from the
-// products themselves, which is what the rounding of dS and of the results leaves.  The price: two products of
-// the backward's nine.
-//
-// The forward's shape: a CTA owns two 128-row query tiles; warp 0 loads (K and V tiles in turn into one
-// ring), warp 1 issues S_t = Q_t K^T and dP_t = dO_t V^T (t = 0, 1), warpgroups 1 and 2 take a row
-// per thread: P from S in registers, then sum P dP.  Nothing goes back to the tensor cores, so the S and
-// dP columns (all 512) are free again as soon as they are read.
-template <int D>
-struct RowDotLayout {
-  static constexpr int kTile = (D / 64) * kBox;
-  static constexpr int kSlots = D == 128 ? 3 : 6;  // of the ring of K(0), V(0), K(1), V(1), ...
-  static constexpr int kQ = 0, kDO = 2 * kTile, kRing = 4 * kTile;
-  static constexpr int kBar = kRing + kSlots * kTile;
-  static constexpr int kNumBars = 1 + 2 * kSlots + 8 + 1;
-  static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kAlloc = kMisc + 16 + 1024;
-  // barriers
-  static constexpr int kQFull = 0, kFull = 1, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots, kDpFull = kSFull + 2,
-                       kSRead = kDpFull + 2, kDpRead = kSRead + 2, kTeardown = kDpRead + 2;
-};
-
-template <int D, bool VL, int SC>
-__global__ void __launch_bounds__(kThreads, 1)
-    ring_rowdot_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                       const BwdParamsT<VL, SC> p, const LseView lse, float* nD, float* nlse2) {
-  using LY = RowDotLayout<D>;
-  constexpr bool kChanged = (SC & (SC_CAP | SC_BIAS)) != 0;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sb = (raw + 1023u) & ~1023u;
-  uint8_t* sp = smem_raw + (sb - raw);
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
-  const int n_pairs = (p.L + 2 * kTileM - 1) / (2 * kTileM);
-  int r, i0;  // heavy rows first, as in the forward
-  if (!VL && p.causal && p.layout == LAYOUT_ZIGZAG && p.r_only < 0 && p.L % (4 * kTileM) == 0) {
-    int pr;
-    zigzag_heavy_first((int)blockIdx.x, p.N, n_pairs / 2, r, pr);
-    i0 = pr * 2 * kTileM;
-  } else {
-    const int x = p.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    r = p.r_only >= 0 ? p.r_only : x / n_pairs;
-    i0 = (x % n_pairs) * 2 * kTileM;
-  }
-  const uint32_t bar0 = sb + LY::kBar;
-  auto BAR = [bar0](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + LY::kMisc);
-  if (threadIdx.x == 0) {
-    mbar_init(BAR(LY::kQFull), 1);
-    for (int i = 0; i < LY::kSlots; ++i) {
-      mbar_init(BAR(LY::kFull + i), 1);
-      mbar_init(BAR(LY::kEmpty + i), 1);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(BAR(LY::kSFull + t), 1);
-      mbar_init(BAR(LY::kDpFull + t), 1);
-      mbar_init(BAR(LY::kSRead + t), 4);
-      mbar_init(BAR(LY::kDpRead + t), 4);
-    }
-    mbar_init(BAR(LY::kTeardown), 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-    prefetch_tmap(&tmDO);
-    const int qrow = r * p.L + i0 - p.q_base;
-    mbar_expect_tx(BAR(LY::kQFull), 4 * LY::kTile);
-    for (int t = 0; t < 2; ++t)
-      for (int c = 0; c < D / 64; ++c)
-        if (in_bounds(tma_coords_ok(TmaExtent{D, p.q_rows, p.H, p.B}, c * 64, qrow + t * kTileM, h, b), p.ctl, 20)) {
-          tma_load_4d(sb + LY::kQ + t * LY::kTile + c * kBox, &tmQ, BAR(LY::kQFull), c * 64, qrow + t * kTileM, h, b);
-          tma_load_4d(sb + LY::kDO + t * LY::kTile + c * kBox, &tmDO, BAR(LY::kQFull), c * 64, qrow + t * kTileM, h, b);
-        }
-  }
-  const int pre = VL ? 0 : prefix_of(p, b);
-  QRange cta;  // both query tiles
-  make_qrange(p, r, i0, 2 * kTileM, cta, pre);
-  const int nkt = (p.L + kTileN - 1) / kTileN;
-  int n_tiles = 0;
-  walk_kv_tiles(p, cta, nkt, 0, p.N, [&](int, int) {
-    ++n_tiles;
-    return true;
-  });
-  if (warp == 2) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S_t at 128 t, dP_t at 256 + 128 t
-
-  if (warp < 4) {
-    regs_dec<kDkdvRegsLow>();
-    if (warp == 0) {
-      // ------------------------------------------------------------ TMA producer
-      if (lane == 0 && n_tiles > 0) {
-        const int hk = h / p.G;
-        int n = 0, slot = 0;
-        uint32_t par = 1;  // of the slot's last release
-        auto load = [&](const CUtensorMap* tm, int row) -> bool {
-          if (n >= LY::kSlots && !wait_one(BAR(LY::kEmpty + slot), par, abort_flag, p.ctl, 70)) return false;
-          mbar_expect_tx(BAR(LY::kFull + slot), LY::kTile);
-          for (int c = 0; c < D / 64; ++c)
-            if (in_bounds(tma_coords_ok(TmaExtent{D, p.S, p.Hk, p.B}, c * 64, row, hk, b), p.ctl, 21))
-              tma_load_4d(sb + LY::kRing + slot * LY::kTile + c * kBox, tm, BAR(LY::kFull + slot), c * 64, row, hk, b);
-          ++n;
-          if (++slot == LY::kSlots) slot = 0, par ^= 1u;
-          return true;
-        };
-        walk_kv_tiles(p, cta, nkt, 0, p.N, [&](int s, int kt) {
-          const int row = s * p.L + kt * kTileN;
-          return load(&tmK, row) && load(&tmV, row);
-        });
-        // every load lands before the CTA ends
-        for (int i = 0; i < LY::kSlots; ++i) {
-          const int times = (n + LY::kSlots - 1 - i) / LY::kSlots;
-          if (times) drain_one(BAR(LY::kFull + i), (times - 1) & 1, p.ctl, 71);
-        }
-      }
-      if (lane == 0) drain_one(BAR(LY::kQFull), 0, p.ctl, 72);  // issued at entry
-      __syncwarp();
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      if (lane == 0 && n_tiles > 0) {
-        constexpr uint32_t kId = idesc_bf16_f32(128, kTileN, 0, 0);
-        constexpr uint32_t kHi = sdesc_sw128_hi(1024);
-        auto issue = [&](uint32_t dcol, uint32_t a, uint32_t bt, int bar) {
-          const uint32_t la = sdesc_sw128_lo(a, 16), lb = sdesc_sw128_lo(bt, 16);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + dcol, sdesc_words(la + off, kHi), sdesc_words(lb + off, kHi), kId, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(BAR(bar));
-        };
-        bool ok = wait_one(BAR(LY::kQFull), 0, abort_flag, p.ctl, 73);
-        int slot = 0;
-        uint32_t par = 0;
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          const uint32_t kat = sb + LY::kRing + slot * LY::kTile;
-          const int kslot = slot;
-          const uint32_t kpar = par;
-          if (++slot == LY::kSlots) slot = 0, par ^= 1u;
-          const uint32_t vat = sb + LY::kRing + slot * LY::kTile;
-          const int vslot = slot;
-          const uint32_t vpar = par;
-          if (++slot == LY::kSlots) slot = 0, par ^= 1u;
-          for (int t = 0; ok && t < 2; ++t) {
-            ok = (t > 0 || wait_one(BAR(LY::kFull + kslot), kpar, abort_flag, p.ctl, 74)) &&
-                 (j == 0 || wait_one(BAR(LY::kSRead + t), (j - 1) & 1, abort_flag, p.ctl, 75));
-            if (!ok) break;
-            tc_fence_after();
-            issue(128 * t, sb + LY::kQ + t * LY::kTile, kat, LY::kSFull + t);
-            if (t == 1 && 2 * j + LY::kSlots < 2 * n_tiles) mma_commit(BAR(LY::kEmpty + kslot));
-            ok = (t > 0 || wait_one(BAR(LY::kFull + vslot), vpar, abort_flag, p.ctl, 76)) &&
-                 (j == 0 || wait_one(BAR(LY::kDpRead + t), (j - 1) & 1, abort_flag, p.ctl, 77));
-            if (!ok) break;
-            tc_fence_after();
-            issue(256 + 128 * t, sb + LY::kDO + t * LY::kTile, vat, LY::kDpFull + t);
-            if (t == 1 && 2 * j + 1 + LY::kSlots < 2 * n_tiles) mma_commit(BAR(LY::kEmpty + vslot));
-          }
-        }
-        // every issued MMA completes before the CTA frees TMEM
-        mma_commit(BAR(LY::kTeardown));
-        drain_one(BAR(LY::kTeardown), 0, p.ctl, 78);
-      }
-      __syncwarp();
-    }
-  } else {
-    regs_inc<kDkdvRegsHigh>();
-    // ------------------------------------------------------------ P and sum P dP, a query row per thread
-    const int t = (warp - 4) >> 2;
-    const int row = ((warp - 4) & 3) * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + 128 * t, tP = tl + 256 + 128 * t;
-    const int i = i0 + t * kTileM + row;
-    const bool valid = i < p.L;
-    QRange qt;
-    RowWin win;
-    int gq = 0;
-    if constexpr (VL) {
-      gq = make_row_win(p, r, min(i, p.L - 1), false, win);
-    } else {
-      make_qrange(p, r, i0 + t * kTileM, kTileM, qt, pre);
-      gq = tok(p, r, valid ? i : max(qt.i_last, 0));
-    }
-    float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
-    // the row's lse: padding rows have +infinity, so that their weights are 0
-    float l = INFINITY;
-    if (valid) {
-      const long long q_row = (long long)r * p.L + i - p.q_base;
-      const long long lrow = VL && p.row_map ? (long long)__ldg(p.row_map + q_row) : q_row;
-      if (in_bounds(lrow >= 0 && lrow < p.q_rows, p.ctl, 22))
-        l = lse.data[(long long)b * lse.sb + (long long)h * lse.sh + lrow * lse.ss];
-    }
-    const float nl = l * -1.4426950408889634f;
-    const uint64_t nl2 = f32x2(nl, nl), sc2 = f32x2(p.scale_log2, p.scale_log2);
-    uint64_t acc[4] = {0, 0, 0, 0};
-    bool ok = true;
-    int j = 0;
-    walk_kv_tiles(p, cta, nkt, 0, p.N, [&](int s, int kt) {
-      int c_lo = 0, c_hi = kTileN;
-      if constexpr (VL)
-        row_win_cols(p, win, s, kt * kTileN, kTileN, c_lo, c_hi);
-      else if (!kv_tile_full(p, qt, s, kt))
-        row_key_window(p, seeing_token<decltype(p)>(gq, pre), s, kt, c_lo, c_hi);
-      const bool masked = c_lo > 0 || c_hi < kTileN;
-      if (!wait_warp(BAR(LY::kSFull + t), j & 1, abort_flag, p.ctl, 79)) {
-        ok = false;
-        return false;
-      }
-      tc_fence_after();
-      ScoreTile<SC> change(p);
-      TileTokens tokens;
-      if constexpr ((SC & SC_BIAS) != 0) tokens = tile_tokens(p, win, s, kt * kTileN);
-      // half a row at a time, so that it stays in registers
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t v[64];
-        tmem_ld64(tS + 64 * hh, v);
-        if (hh == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(LY::kSRead + t));
-        }
-        int tier = 0;
-        bool line = true;
-        if constexpr ((SC & SC_BIAS) != 0) {
-          if (hh) tokens.t0 += 64 * tokens.st, tokens.t1 += 64 * tokens.st, tokens.cb -= 64;
-          change.bias = bias_line(tokens, gq, max(c_lo - 64 * hh, 0), min(c_hi - 64 * hh, 64), slope2);
-          line = __all_sync(0xffffffffu, change.bias.line);
-          change.bias.off += nl;
-        }
-        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
-        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const uint64_t sv = f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            uint64_t x;
-            if constexpr (kChanged) {
-              uint64_t w;
-              x = change.template operator()<decltype(ti)::value, decltype(li)::value, decltype(li)::value>(c, sv, nl2, w);
-            } else {
-              x = fma_f32x2(sv, sc2, nl2);
-            }
-            float x0, x1;
-            f32x2_split(x, x0, x1);
-            v[c] = __float_as_uint(fast_exp2(x0)), v[c + 1] = __float_as_uint(fast_exp2(x1));
-          }
-        });
-        if (masked) {
-          const uint64_t mw = bit_window64(c_lo - 64 * hh, c_hi - 64 * hh);
-#pragma unroll
-          for (int u = 0; u < 64; ++u) v[u] = ((mw >> u) & 1ull) ? v[u] : 0u;
-        }
-        if (hh == 0 && !wait_warp(BAR(LY::kDpFull + t), j & 1, abort_flag, p.ctl, 80)) {
-          ok = false;
-          return false;
-        }
-        tc_fence_after();
-        uint32_t d[64];
-        tmem_ld64(tP + 64 * hh, d);
-#pragma unroll
-        for (int u = 0; u < 64; u += 2)
-          acc[(u >> 1) & 3] = fma_f32x2(f32x2(__uint_as_float(v[u]), __uint_as_float(v[u + 1])),
-                                        f32x2(__uint_as_float(d[u]), __uint_as_float(d[u + 1])), acc[(u >> 1) & 3]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(LY::kDpRead + t));
-      ++j;
-      return true;
-    });
-    if (i < p.stat_L) {
-      float a0, a1;
-      f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), a0, a1);
-      const long long at = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
-      nD[at] = valid && ok ? -(a0 + a1) : 0.f;
-      nlse2[at] = nl;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
-}
-
 template <int D, bool VL, int SC>
 cudaError_t launch_bwd_v(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const BwdParamsT<VL, SC>& p, int which, cudaStream_t st) {
@@ -1193,18 +811,6 @@ cudaError_t launch_bwd_v(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * p.n_qtiles), (unsigned)(p.B * p.H));
     ring_dq_kernel<D, VL, SC><<<grid, kThreads, DqLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, p);
   }
-  return cudaGetLastError();
-}
-
-template <int D, bool VL, int SC>
-cudaError_t launch_rowdot_v(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                            const CUtensorMap& tdo, const BwdParamsT<VL, SC>& p, const LseView& lse, float* nD,
-                            float* nlse2, cudaStream_t st) {
-  cudaError_t e = configure_kernel<ring_rowdot_kernel<D, VL, SC>>(kDkdvLaunchRegs, RowDotLayout<D>::kAlloc);
-  if (e != cudaSuccess) return e;
-  const int n_pairs = (p.L + 2 * kTileM - 1) / (2 * kTileM);
-  dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * n_pairs), (unsigned)(p.B * p.H));
-  ring_rowdot_kernel<D, VL, SC><<<grid, kThreads, RowDotLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, p, lse, nD, nlse2);
   return cudaGetLastError();
 }
 

@@ -514,21 +514,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           // scores as they count, in log2 units
           tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
           tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
-          ScoreTile<SC> change(a);
+          BiasLine bias = {};
           int tier = 0;
           bool line = true;
           if constexpr ((SC & SC_BIAS) != 0) {
-            change.bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
-            line = __all_sync(0xffffffffu, change.bias.line);
+            bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
+            line = __all_sync(0xffffffffu, bias.line);
           }
           if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, sc);
           with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
+            const Cap<SC, decltype(ti)::value> cap(a.sc);
 #pragma unroll
             for (int c = 0; c < kUnit; c += 2) {
               uint64_t w;
               float z0, z1;
-              f32x2_split(change.template operator()<decltype(ti)::value, decltype(li)::value, decltype(li)::value>(
-                              c, mul_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f32x2(sc, sc)), 0, w),
+              f32x2_split(cap(mul_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f32x2(sc, sc)),
+                              with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, 0), w),
                           z0, z1);
               v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
             }

@@ -38,12 +38,11 @@
 // soon as its S tile is ready.  Empty key tiles are never loaded; only
 // partial tiles are masked element by element.
 //
-// SC (ra_score.cuh): 0 for plain scores (ra_fwd.cu), else a call's cap, bias by distance or
-// prefix (ra_scored_fwd_*.cu), for which the softmax threads change their scores where they lie, in
-// registers, before the mask.
+// SC: 0, or SC_ON for calls with a prefix that all tokens see, which changes masks only.  Capped or
+// biased scores have a kernel of their own (ra_scored_fwd.cuh).
 #pragma once
 
-#include "ra_score.cuh"
+#include "ra_tiles.cuh"
 
 namespace ra {
 namespace {
@@ -113,7 +112,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParamsT<VL, SC> p) {
   using LY = FwdLayout<D>;
-  constexpr bool kChanged = (SC & (SC_CAP | SC_BIAS)) != 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -320,13 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     RowWin win;
     int gq = 0;
     if constexpr (VL) {
-      gq = make_row_win(p, r, min(i, p.L - 1), false, win);
+      make_row_win(p, r, min(i, p.L - 1), false, win);
     } else {
       make_qrange(p, r, i0 + t * kTileM, kTileM, qt, pre);
-      gq = tok(p, r, valid ? i : max(qt.i_last, 0));
+      gq = seeing_token<decltype(p)>(tok(p, r, valid ? i : max(qt.i_last, 0)), pre);
     }
-    float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
     float m_run = -INFINITY;  // running max, in log2 units (scores * scale * log2 e)
     float l_run = 0.f;        // running sum of exp2(x - m_run)
     bool ok = true;
@@ -337,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (VL)
         row_win_cols(p, win, s, kt * kTileN, kTileN, c_lo, c_hi);
       else if (!kv_tile_full(p, qt, s, kt))
-        row_key_window(p, seeing_token<decltype(p)>(gq, pre), s, kt, c_lo, c_hi);
+        row_key_window(p, gq, s, kt, c_lo, c_hi);
       const bool masked = c_lo > 0 || c_hi < kTileN;
       if (!wait_warp<kWaitHint>(BAR(B_S_FULL + t), j & 1, abort_flag, p.ctl, 7)) {
         ok = false;
@@ -353,41 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
       tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(v + 64));
       tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(v + 96));
-      // changed scores: in full tiles the largest follows from the largest product (the cap is monotonic, the bias a
-      // line), and a score becomes a weight in one go; else they are changed where they lie first
-      ScoreTile<SC> change(p);
-      int tier = 0;
-      bool in_place = false;
-      if constexpr (kChanged) {
-        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
-        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
-        bool line = true, loose = false;
-        if constexpr ((SC & SC_BIAS) != 0) {
-          change.bias = bias_line(tile_tokens(p, win, s, kt * kTileN), gq, c_lo, c_hi, slope2);
-          line = __all_sync(0xffffffffu, change.bias.line);
-          loose = fabsf(change.bias.slp) * kTileN > kLoose;
-        }
-        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
-        in_place = __any_sync(0xffffffffu, masked || loose) || !line;
-        if (in_place)
-          with_score_flags<SC>(max(tier, 2), line, [&](auto ti, auto li) {
-            if constexpr (decltype(ti)::value >= 2 || (SC & SC_CAP) == 0) {
-#pragma unroll
-              for (int c = 0; c < kTileN; c += 2) {
-                uint64_t w;
-                float z0, z1;
-                f32x2_split(change.template operator()<decltype(ti)::value, decltype(li)::value, decltype(li)::value>(
-                                c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), 0, w),
-                            z0, z1);
-                v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
-              }
-            }
-          });
-      }
       float mc[4];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        if (!kChanged && hh == 1) {
+        if (hh == 1) {
           tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
           tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
         }
@@ -408,11 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // raw scores: the scale is > 0, so max(s) * scale = max(s * scale)
-      float mx = fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3]));
-      if constexpr (!kChanged)
-        mx *= p.scale_log2;
-      else if (!in_place)
-        mx = change.most(mx, tier, kTileN);
+      const float mx = fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3])) * p.scale_log2;
       float alpha = 1.f;
       if (mx > -INFINITY) {
         if (m_run == -INFINITY) {
@@ -429,35 +390,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // s * scale - m and the sums run two lanes per instruction (f32x2).
       const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-m_use, -m_use);
       uint64_t acc[4] = {0, 0, 0, 0};  // four pairs of partial row sums (+0.0f bits)
-      auto weights = [&](auto minus_m) {  // of columns c, c + 1, from their scores
 #pragma unroll
-        for (int c32 = 0; c32 < kTileN / 32; ++c32) {
-          uint32_t pk[16];
+      for (int c32 = 0; c32 < kTileN / 32; ++c32) {
+        uint32_t pk[16];
 #pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const int c = c32 * 32 + 2 * u;
-            float x0, x1;
-            f32x2_split(minus_m(c, f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]))), x0, x1);
-            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-            acc[u & 3] = add_f32x2(acc[u & 3], f32x2(e0, e1));
-            pk[u] = pack_bf16x2(e0, e1);
-          }
-          tmem_st16(tS + c32 * 16, pk);
+        for (int u = 0; u < 16; ++u) {
+          const int c = c32 * 32 + 2 * u;
+          float x0, x1;
+          f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nm2), x0, x1);
+          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+          acc[u & 3] = add_f32x2(acc[u & 3], f32x2(e0, e1));
+          pk[u] = pack_bf16x2(e0, e1);
         }
-      };
-      if constexpr (!kChanged) {
-        weights([&](int, uint64_t sv) { return fma_f32x2(sv, sc2, nm2); });
-      } else if (in_place) {
-        weights([&](int, uint64_t sv) { return add_f32x2(sv, nm2); });
-      } else {
-        change.bias.off -= m_use;
-        with_score_flags<SC>(tier, true, [&](auto ti, auto li) {
-          if constexpr (decltype(li)::value != 0)
-            weights([&](int c, uint64_t sv) {
-              uint64_t w;
-              return change.template operator()<decltype(ti)::value, true, true>(c, sv, nm2, w);
-            });
-        });
+        tmem_st16(tS + c32 * 16, pk);
       }
       float s0, s1;
       f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);

@@ -26,6 +26,12 @@
 
 namespace ra {
 
+// Eight fp32 numbers times mul, as bf16.
+__device__ __forceinline__ uint4 scaled_bf16x8(const uint32_t* o, float mul) {
+  auto two = [&](int i) { return pack_bf16x2(__uint_as_float(o[i]) * mul, __uint_as_float(o[i + 1]) * mul); };
+  return make_uint4(two(0), two(2), two(4), two(6));
+}
+
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -66,6 +72,11 @@ struct BiasLine {
   float a, b, st, neg;    // else neg * |(c < cb ? a : b) - st c|
   int cb;
   bool line;
+  // The same for columns counted from c0.
+  __device__ __forceinline__ BiasLine from(int c0) const {
+    const float f = (float)c0;
+    return BiasLine{fmaf(f, slp, off), slp, fmaf(-f, st, a), fmaf(-f, st, b), st, neg, cb - c0, line};
+  }
 };
 
 // own: the row's token; [lo, hi): its columns that count.
@@ -86,100 +97,93 @@ __device__ __forceinline__ BiasLine bias_line(const TileTokens& x, int own, int 
   return r;
 }
 
+// x in both lanes, in registers of its own: the compiler would otherwise make such a pair anew from the uniform
+// registers for every use, two moves next to each multiply-add of two scores.
+__device__ __forceinline__ uint64_t both_lanes(float x) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
 template <int N>
-__device__ __forceinline__ uint64_t polynomial(uint64_t w, const float (&c)[N]) {
-  uint64_t h = f32x2(c[N - 1], c[N - 1]);
+__device__ __forceinline__ uint64_t polynomial(uint64_t w, const uint64_t (&c)[N]) {
+  uint64_t h = c[N - 1];
 #pragma unroll
-  for (int i = N - 2; i >= 0; --i) h = fma_f32x2(w, h, f32x2(c[i], c[i]));
+  for (int i = N - 2; i >= 0; --i) h = fma_f32x2(w, h, c[i]);
   return h;
 }
 
-// How a tile's scores are changed.  kTier: which polynomial holds for all of the warp's scores (kTiers: none).
-template <int SC>
-struct ScoreTile {
-  const ScoreParams& sc;
-  BiasLine bias;
+// Scores without their bias: the cap, or the plain scale.  kTier: the polynomial that holds for all of the warp's
+// products (kTiers: none).  kGrad: with the derivative.  Its constants are loaded when it is made.
+template <int SC, int kTier, bool kGrad = false>
+struct Cap {
+  static constexpr bool kCap = (SC & SC_CAP) != 0, kAny = kTier == kTiers;
+  static constexpr int kT = !kCap ? 1 : kAny ? 3 : kTier == 0 ? 4 : kTier == 1 ? 5 : 7;
+  static constexpr int kG = !kCap || !kGrad || kAny ? 1 : kTier == 0 ? 2 : kTier == 1 ? 3 : 5;
+  uint64_t t[kT], g[kG];
 
-  template <class P>  // kernel parameters with `sc`
-  __device__ __forceinline__ explicit ScoreTile(const P& p) : sc(p.sc), bias() {}
-
-  // Two products s of columns c, c + 1: x = z + add, and w, from which `derivative` follows.  kLine: bias.line.
-  // kFolded: add is the same for all columns, and bias.off has it (only where kLine is).
-  template <int kTier, bool kLine, bool kFolded>
-  __device__ __forceinline__ uint64_t operator()(int c, uint64_t s, uint64_t add, uint64_t& w) const {
-    if constexpr ((SC & SC_BIAS) != 0) {
-      float b0, b1;
-      if constexpr (kLine) {
-        b0 = fmaf((float)c, bias.slp, bias.off), b1 = fmaf((float)(c + 1), bias.slp, bias.off);
-        add = kFolded ? f32x2(b0, b1) : add_f32x2(f32x2(b0, b1), add);
-      } else {
-        float a0, a1;
-        f32x2_split(add, a0, a1);
-        b0 = fmaf(bias.neg, fabsf(fmaf(-(float)c, bias.st, c < bias.cb ? bias.a : bias.b)), a0);
-        b1 = fmaf(bias.neg, fabsf(fmaf(-(float)(c + 1), bias.st, c + 1 < bias.cb ? bias.a : bias.b)), a1);
-        add = f32x2(b0, b1);
-      }
+  __device__ __forceinline__ explicit Cap(const ScoreParams& sc) {
+    if constexpr (!kCap) {
+      t[0] = both_lanes(sc.c0);
+    } else if constexpr (kAny) {
+      t[0] = both_lanes(sc.e2), t[1] = both_lanes(-2.f * sc.cap2), t[2] = both_lanes(sc.cap2);
+      if (kGrad) g[0] = both_lanes(sc.inv_cap2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kT; ++i) t[i] = both_lanes(kTier == 0 ? sc.t0[i % 4] : kTier == 1 ? sc.t1[i % 5] : sc.t2[i]);
+      if (kGrad)
+#pragma unroll
+        for (int i = 0; i < kG; ++i) g[i] = both_lanes(kTier == 0 ? sc.g0[i % 2] : kTier == 1 ? sc.g1[i % 3] : sc.g2[i]);
     }
-    return capped<kTier>(s, add, w);
   }
-  // The same without the bias.
-  template <int kTier>
-  __device__ __forceinline__ uint64_t capped(uint64_t s, uint64_t add, uint64_t& w) const {
-    if constexpr ((SC & SC_CAP) == 0) {
+  // Two products s: their scores + add, and w, from which their derivatives follow.
+  __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add, uint64_t& w) const {
+    if constexpr (!kCap) {
       w = 0;
-      return fma_f32x2(s, f32x2(sc.c0, sc.c0), add);
-    } else if constexpr (kTier < kTiers) {
+      return fma_f32x2(s, t[0], add);
+    } else if constexpr (!kAny) {
       w = mul_f32x2(s, s);
-      return fma_f32x2(s, kTier == 0 ? polynomial(w, sc.t0) : kTier == 1 ? polynomial(w, sc.t1) : polynomial(w, sc.t2), add);
+      return fma_f32x2(s, polynomial(w, t), add);
     } else {
       float e0, e1;
-      f32x2_split(mul_f32x2(s, f32x2(sc.e2, sc.e2)), e0, e1);
-      const uint64_t r = f32x2(fast_rcp(fast_exp2(e0) + 1.f), fast_rcp(fast_exp2(e1) + 1.f));
-      w = fma_f32x2(r, f32x2(-2.f * sc.cap2, -2.f * sc.cap2), f32x2(sc.cap2, sc.cap2));  // the capped score
+      f32x2_split(mul_f32x2(s, t[0]), e0, e1);
+      w = fma_f32x2(f32x2(fast_rcp(fast_exp2(e0) + 1.f), fast_rcp(fast_exp2(e1) + 1.f)), t[1], t[2]);  // the capped score
       return add_f32x2(w, add);
     }
   }
-  // The largest of a tile's z, or more by at most kLoose, from its largest product, for a tile whose bias is a line.
-  __device__ __forceinline__ float most(float s, int tier, int n) const {
-    if (s == -INFINITY) return s;
-    uint64_t w;
-    float z = 0.f, unused;
-    const uint64_t two = f32x2(s, s);
-    f32x2_split(!(SC & SC_CAP) || tier == 0 ? capped<0>(two, 0, w)
-                : tier == 1                 ? capped<1>(two, 0, w)
-                : tier == 2                 ? capped<2>(two, 0, w)
-                                            : capped<kTiers>(two, 0, w),
-                z, unused);
-    return (SC & SC_BIAS) ? z + fmaxf(bias.off, fmaf((float)(n - 1), bias.slp, bias.off)) : z;
-  }
-  // of the cap, from the w of the calls above
-  template <int kTier>
   __device__ __forceinline__ uint64_t derivative(uint64_t w) const {
     const uint64_t one = f32x2(1.f, 1.f);
-    if constexpr (kTier < kTiers) {
-      return fma_f32x2(w, kTier == 0 ? polynomial(w, sc.g0) : kTier == 1 ? polynomial(w, sc.g1) : polynomial(w, sc.g2), one);
-    } else {
-      const uint64_t th = mul_f32x2(w, f32x2(sc.inv_cap2, sc.inv_cap2));
-      return fma_f32x2(neg_f32x2(th), th, one);
-    }
+    if constexpr (!kAny) return fma_f32x2(w, polynomial(w, g), one);
+    const uint64_t th = mul_f32x2(w, g[0]);
+    return fma_f32x2(neg_f32x2(th), th, one);
   }
 };
 
-// Plain scores (or a prefix alone): nothing to change.
-struct NoScoreTile {
-  BiasLine bias;
-  template <class P>
-  __device__ __forceinline__ explicit NoScoreTile(const P&) {}
-  __device__ __forceinline__ float most(float s, int, int) const { return s; }
-};
-template <>
-struct ScoreTile<0> : NoScoreTile {
-  using NoScoreTile::NoScoreTile;
-};
-template <>
-struct ScoreTile<SC_ON> : NoScoreTile {
-  using NoScoreTile::NoScoreTile;
-};
+// What is added to the scores of columns c, c + 1 before the exponential: their bias and `add` (kLine: bias.line).
+// kFolded: add is the same for all columns, and where kLine is, bias.off has it.
+template <int SC, bool kLine, bool kFolded>
+__device__ __forceinline__ uint64_t with_bias(const BiasLine& bias, int c, uint64_t add) {
+  if constexpr ((SC & SC_BIAS) == 0) {
+    return add;
+  } else if constexpr (kLine) {
+    const uint64_t b = f32x2(fmaf((float)c, bias.slp, bias.off), fmaf((float)(c + 1), bias.slp, bias.off));
+    return kFolded ? b : add_f32x2(b, add);
+  } else {
+    float a0, a1;
+    f32x2_split(add, a0, a1);
+    return f32x2(fmaf(bias.neg, fabsf(fmaf(-(float)c, bias.st, c < bias.cb ? bias.a : bias.b)), a0),
+                 fmaf(bias.neg, fabsf(fmaf(-(float)(c + 1), bias.st, c + 1 < bias.cb ? bias.a : bias.b)), a1));
+  }
+}
+
+// The largest score of n columns whose bias is a line, or more by at most what that rises over them, from their largest
+// product.
+template <int SC>
+__device__ __forceinline__ float most(const ScoreParams& sc, const BiasLine& bias, float s, int n) {
+  if (s == -INFINITY) return s;
+  float z = s * sc.c0;
+  if constexpr ((SC & SC_CAP) != 0) z = fmaf(fast_rcp(fast_exp2(s * sc.e2) + 1.f), -2.f * sc.cap2, sc.cap2);
+  return (SC & SC_BIAS) ? z + fmaxf(bias.off, fmaf((float)(n - 1), bias.slp, bias.off)) : z;
+}
 
 template <int N>
 struct Const {
@@ -207,18 +211,26 @@ __device__ __forceinline__ void with_score_flags(int tier, bool line, F&& f) {
     f(Const<kTiers>{}, Const<1>{});
 }
 
-// The polynomial that holds for N products of every lane.
+// The largest magnitude of N products (none that is NaN).
 template <int N>
-__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, float factor = 1.f) {
+__device__ __forceinline__ float largest(const uint32_t (&v)[N]) {
   float m[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < N; c += 4) {
     m[0] = fmax3f(m[0], fabsf(__uint_as_float(v[c])), fabsf(__uint_as_float(v[c + 1])));
     m[1] = fmax3f(m[1], fabsf(__uint_as_float(v[c + 2])), fabsf(__uint_as_float(v[c + 3])));
   }
+  return fmaxf(m[0], m[1]);
+}
+// The polynomial that holds for products of up to `size` in every lane.
+__device__ __forceinline__ int tier_of(float size, const ScoreParams& sc) {
   // (not negative and no NaN: the bits are in the numbers' order)
-  const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(m[0], m[1]) * factor)));
+  const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(size)));
   return all <= sc.lim[0] ? 0 : all <= sc.lim[1] ? 1 : all <= sc.lim[2] ? 2 : kTiers;
+}
+template <int N>
+__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, float factor = 1.f) {
+  return tier_of(largest(v) * factor, sc);
 }
 
 }  // namespace ra
