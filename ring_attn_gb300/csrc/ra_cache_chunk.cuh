@@ -98,7 +98,8 @@ struct Lay {
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kItem = kMisc + 16;
   static constexpr int kTwin = kItem + kItems * (int)sizeof(Item);  // 128 rows' M and sums
-  static constexpr int kAlloc = kTwin + 128 * 8 + 1024;  // slack to align the base to 1024 bytes
+  static constexpr int kCaps = kTwin + 128 * 8;  // constants of the cap (scored calls only)
+  static constexpr int kAlloc = kCaps + 1024;    // slack to align the base to 1024 bytes
 };
 constexpr int kReaders = 13;  // of an item: the issuer, 4 conversion and 8 softmax warps
 
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = note;
     return;
   }
+  if constexpr (kChanged) fill_cap_table(sp + L::kCaps, a.sc);
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           }
           if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, sc);
           with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-            const Cap<SC, decltype(ti)::value> cap(a.sc);
+            const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
 #pragma unroll
             for (int c = 0; c < kUnit; c += 2) {
               uint64_t w;
@@ -715,9 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
 
 template <int D, int SC>
 cudaError_t launch_chunk(const CacheAttnPlan& p, cudaStream_t st) {
-  const cudaError_t e = configure_kernel<cache_chunk_kernel<D, SC>>(kLaunchRegs, Lay<D>::kAlloc);
+  constexpr int bytes = Lay<D>::kAlloc + (SC != 0 ? kCapTable : 0);
+  const cudaError_t e = configure_kernel<cache_chunk_kernel<D, SC>>(kLaunchRegs, bytes);
   if (e != cudaSuccess) return e;
-  return launch_early(cache_chunk_kernel<D, SC>, p.grid, kThreads, Lay<D>::kAlloc, st, p.args);
+  return launch_early(cache_chunk_kernel<D, SC>, p.grid, kThreads, bytes, st, p.args);
 }
 
 }  // namespace

@@ -97,13 +97,6 @@ __device__ __forceinline__ BiasLine bias_line(const TileTokens& x, int own, int 
   return r;
 }
 
-// x in both lanes, in registers of its own: the compiler would otherwise make such a pair anew from the uniform
-// registers for every use, two moves next to each multiply-add of two scores.
-__device__ __forceinline__ uint64_t both_lanes(float x) {
-  uint64_t r;
-  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
-  return r;
-}
 template <int N>
 __device__ __forceinline__ uint64_t polynomial(uint64_t w, const uint64_t (&c)[N]) {
   uint64_t h = c[N - 1];
@@ -112,8 +105,39 @@ __device__ __forceinline__ uint64_t polynomial(uint64_t w, const uint64_t (&c)[N
   return h;
 }
 
+// The constants of the caps, each twice for the two lanes of a packed instruction, in shared memory, for kernels
+// short of registers: there the assembler makes pairs of kernel parameters anew next to their uses, two moves for a
+// multiply-add of two scores, while pairs that are loaded stay (16,384 tokens capped: 1.82 ms, 1.88 without).
+constexpr int kCapConsts = 31;
+constexpr int kCapTable = 8 * kCapConsts;  // bytes
+__device__ __forceinline__ void fill_cap_table(uint8_t* table, const ScoreParams& sc) {
+  const int i = threadIdx.x;
+  if (i >= kCapConsts) return;
+  float x;
+  if (i < 4)
+    x = sc.t0[i];
+  else if (i < 6)
+    x = sc.g0[i - 4];
+  else if (i < 11)
+    x = sc.t1[i - 6];
+  else if (i < 14)
+    x = sc.g1[i - 11];
+  else if (i < 21)
+    x = sc.t2[i - 14];
+  else if (i < 26)
+    x = sc.g2[i - 21];
+  else
+    x = i == 26 ? sc.e2 : i == 27 ? -2.f * sc.cap2 : i == 28 ? sc.cap2 : i == 29 ? sc.inv_cap2 : sc.c0;
+  reinterpret_cast<float2*>(table)[i] = make_float2(x, x);
+}
+__device__ __forceinline__ uint64_t cap_const(uint32_t table, int i) {
+  uint64_t v;
+  asm volatile("ld.volatile.shared.b64 %0, [%1];" : "=l"(v) : "r"(table + 8 * i));
+  return v;
+}
+
 // Scores without their bias: the cap, or the plain scale.  kTier: the polynomial that holds for all of the warp's
-// products (kTiers: none).  kGrad: with the derivative.  Its constants are loaded when it is made.
+// products (kTiers: none).  kGrad: with the derivative.  It is made from the parameters or the table's address.
 template <int SC, int kTier, bool kGrad = false>
 struct Cap {
   static constexpr bool kCap = (SC & SC_CAP) != 0, kAny = kTier == kTiers;
@@ -122,18 +146,25 @@ struct Cap {
   uint64_t t[kT], g[kG];
 
   __device__ __forceinline__ explicit Cap(const ScoreParams& sc) {
+    auto two = [](float x) { return f32x2(x, x); };
     if constexpr (!kCap) {
-      t[0] = both_lanes(sc.c0);
+      t[0] = two(sc.c0);
     } else if constexpr (kAny) {
-      t[0] = both_lanes(sc.e2), t[1] = both_lanes(-2.f * sc.cap2), t[2] = both_lanes(sc.cap2);
-      if (kGrad) g[0] = both_lanes(sc.inv_cap2);
+      t[0] = two(sc.e2), t[1] = two(-2.f * sc.cap2), t[2] = two(sc.cap2), g[0] = two(sc.inv_cap2);
     } else {
 #pragma unroll
-      for (int i = 0; i < kT; ++i) t[i] = both_lanes(kTier == 0 ? sc.t0[i % 4] : kTier == 1 ? sc.t1[i % 5] : sc.t2[i]);
-      if (kGrad)
+      for (int i = 0; i < kT; ++i) t[i] = two(kTier == 0 ? sc.t0[i % 4] : kTier == 1 ? sc.t1[i % 5] : sc.t2[i % 7]);
 #pragma unroll
-        for (int i = 0; i < kG; ++i) g[i] = both_lanes(kTier == 0 ? sc.g0[i % 2] : kTier == 1 ? sc.g1[i % 3] : sc.g2[i]);
+      for (int i = 0; i < kG; ++i) g[i] = two(kTier == 0 ? sc.g0[i % 2] : kTier == 1 ? sc.g1[i % 3] : sc.g2[i % 5]);
     }
+  }
+  __device__ __forceinline__ explicit Cap(uint32_t table) {
+    constexpr int at = !kCap ? 30 : kAny ? 26 : kTier == 0 ? 0 : kTier == 1 ? 6 : 14;
+#pragma unroll
+    for (int i = 0; i < kT; ++i) t[i] = cap_const(table, at + i);
+    if (kCap && kGrad)
+#pragma unroll
+      for (int i = 0; i < kG; ++i) g[i] = cap_const(table, at + kT + i);
   }
   // Two products s: their scores + add, and w, from which their derivatives follow.
   __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add, uint64_t& w) const {

@@ -13,7 +13,8 @@
 //      a zigzag seam inside), or too steep a one, go over their changed scores instead.
 //   2. the two threads of a row exchange their bounds through shared memory (as bf16, rounded up) and take the
 //      larger as the offset, if it passes the running one by 2^8.
-//   3. scores again, changed and turned into weights in one go, packed as bf16 over the first 32 of the thread's own 64
+//   With a cap that is not too high neither is needed: a fixed offset will do, and halves do not wait for one another.
+//   3. scores are changed and turned into weights in one go, packed as bf16 over the first 32 of the thread's own 64
 //      columns; sums of weights stay with the thread until the end.
 //
 // Measured: see the kernels' table; 16,384 tokens of 32 heads of 128, causal, softcap 50: @TIME@.
@@ -35,7 +36,8 @@ template <int D>
 struct ScoredFwdLayout : FwdLayout<D> {
   using Base = FwdLayout<D>;
   static constexpr int kBound = Base::kMisc + 16;  // bf16 [2 tiles][2 halves][128 rows]
-  static constexpr int kAlloc = kBound + 2 * 2 * 128 * 2 + 1024;
+  static constexpr int kCaps = (kBound + 2 * 2 * 128 * 2 + 7) / 8 * 8;  // constants
+  static constexpr int kAlloc = kCaps + kCapTable + 1024;
   // the epilogue's row slots (16 warps x 32 rows of half a head, bf16) and sums reuse the operand buffers
   static_assert(16 * 32 * D + 2048 <= Base::kBar, "output slots exceed the operand buffers");
 };
@@ -106,6 +108,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       q_issued = true;
     }
   }
+  fill_cap_table(sp + LY::kCaps, p.sc);
   QRange cta;  // both query tiles together: decides which key tiles are visited
   const int pre = VL ? 0 : prefix_of(p, b);
   make_qrange(p, r, i0, kRowsPerCta, cta, pre);
@@ -248,6 +251,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     bool valid = i < p.L;
     __nv_bfloat16* bounds = reinterpret_cast<__nv_bfloat16*>(sp + LY::kBound) + t * 256 + row;
     const int pair_bar = 1 + t * 4 + (warp & 3);  // the two warps of 32 rows
+    const uint32_t cap_table = sb + LY::kCaps;
     QRange qt;
     RowWin win;
     int gq = 0;
@@ -259,26 +263,103 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     }
     float slope2 = 0.f;
     if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
-    float m_run = -INFINITY;  // offset of the weights, in log2 units
+    // Capped scores lie within +-cap2, so where that is small enough one offset serves all rows: weights up to 2^60
+    // and, for the rows whose scores are the least, down to 2^-102.  A bias only takes off, and nothing from the row's
+    // own token, which every row of a whole call sees.
+    const bool fixed = (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
+    float m_run = fixed ? fmaxf(p.sc.cap2 - 60.f, 0.f) : -INFINITY;  // offset of the weights, in log2 units
     float l_run = 0.f;        // running sum of this half's weights
     bool ok = true;
     int j = 0;
-    walk_tiles(p, cta, nkt, [&](int s, int kt) {
-      // allowed columns [c_lo, c_hi) of the thread's 64
-      int c_lo = 0, c_hi = kTileN;
+    // allowed columns [c_lo, c_hi) of the thread's 64, as bits
+    auto window = [&](int s, int kt, int& c_lo, int& c_hi) {
+      c_lo = 0, c_hi = kTileN;
       if constexpr (VL)
         row_win_cols(p, win, s, kt * kTileN, kTileN, c_lo, c_hi);
       else if (!kv_tile_full(p, qt, s, kt))
         row_key_window(p, seeing_token<decltype(p)>(gq, pre), s, kt, c_lo, c_hi);
       c_lo = max(c_lo - 64 * half, 0), c_hi = min(c_hi - 64 * half, 64);
+      return bit_window64(c_lo, c_hi);
+    };
+    if constexpr ((SC & SC_CAP) != 0) {
+      if (fixed) {
+        const uint64_t nm2 = f32x2(-m_run, -m_run);
+        const Cap<SC, 0> most_often(cap_table);
+        uint64_t acc[2] = {0, 0};
+        walk_tiles(p, cta, nkt, [&](int s, int kt) {
+          int c_lo, c_hi;
+          const uint64_t mw = window(s, kt, c_lo, c_hi);
+          const bool any_masked = __any_sync(0xffffffffu, c_lo > 0 || c_hi < 64);
+          BiasLine bias = {};
+          bool line = true;
+          if constexpr ((SC & SC_BIAS) != 0) {
+            bias = bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, c_lo, c_hi, slope2);
+            line = __all_sync(0xffffffffu, bias.line);
+            bias.off -= m_run;
+          }
+          if (!wait_warp<kWaitHint>(BAR(B_S_FULL + t), j & 1, abort_flag, p.ctl, 7)) {
+            ok = false;
+            return false;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(tS + 32 * ch, v);
+            const BiasLine part = bias.from(32 * ch);
+            tmem_ld_wait(v);
+            const int tier = tier_of(largest(v), p.sc);
+            auto weights = [&](const auto& cap, auto li, auto mask) {
+              const uint32_t m32 = (uint32_t)(mw >> (32 * ch));
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const int c = 2 * u;
+                uint64_t w;
+                float x0, x1;
+                f32x2_split(cap(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                with_bias<SC, decltype(li)::value, decltype(li)::value>(part, c, nm2), w),
+                            x0, x1);
+                float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                if constexpr (decltype(mask)::value != 0)
+                  e0 = (m32 >> c) & 1u ? e0 : 0.f, e1 = (m32 >> (c + 1)) & 1u ? e1 : 0.f;
+                acc[u & 1] = add_f32x2(acc[u & 1], f32x2(e0, e1));
+                pk[u] = pack_bf16x2(e0, e1);
+              }
+              tmem_st16(tS + 16 * ch, pk);
+            };
+            if (tier == 0 && line && !any_masked)
+              weights(most_often, Const<1>{}, Const<0>{});
+            else if (any_masked)
+              with_score_flags<SC>(max(tier, 2), line, [&](auto ti, auto li) {
+                if constexpr (decltype(ti)::value >= 2) weights(Cap<SC, decltype(ti)::value>(cap_table), li, Const<1>{});
+              });
+            else
+              with_score_flags<SC>(max(tier, 1), line, [&](auto ti, auto li) {
+                if constexpr (decltype(ti)::value >= 1) weights(Cap<SC, decltype(ti)::value>(cap_table), li, Const<0>{});
+              });
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_P_FULL + t));
+          ++j;
+          return true;
+        });
+        float s0, s1;
+        f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
+        l_run = s0 + s1;
+      }
+    }
+    if (!fixed) walk_tiles(p, cta, nkt, [&](int s, int kt) {
+      int c_lo, c_hi;
+      const uint64_t mw = window(s, kt, c_lo, c_hi);
       const bool masked = c_lo > 0 || c_hi < 64;
-      const uint64_t mw = bit_window64(c_lo, c_hi);
       BiasLine bias = {};
       bool line = true, exact = false;
       if constexpr ((SC & SC_BIAS) != 0) {
         bias = bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, c_lo, c_hi, slope2);
         line = __all_sync(0xffffffffu, bias.line);
-        exact = __any_sync(0xffffffffu, fabsf(bias.slp) * 64.f > kLoose) || !line;
+        exact = !line || __any_sync(0xffffffffu, fabsf(bias.slp) * 64.f > kLoose);
       }
       if (!wait_warp<kWaitHint>(BAR(B_S_FULL + t), j & 1, abort_flag, p.ctl, 7)) {
         // the other warp of the pair may have seen the tile: it waits for this one once more at most, since its
@@ -288,26 +369,30 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         return false;
       }
       tc_fence_after();
-      // the largest score, or a bound of it
       const bool any_masked = __any_sync(0xffffffffu, masked);
-      float mx = -INFINITY, size = 0.f;
+      uint32_t v[64];
+      tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(v));
+      tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v));
+      tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      float size = 0.f, alpha = 1.f;
+      if constexpr ((SC & SC_CAP) != 0) size = largest(v);
+      const int tier = (SC & SC_CAP) ? tier_of(size, p.sc) : 0;
       {
-        uint32_t v[64];
-        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        // the largest score, or a bound of it
+        float mx = -INFINITY;
         bool loose = false;  // whether the largest magnitude will do
         if constexpr ((SC & SC_CAP) != 0) {
-          size = largest(v);
-          const float z = most<SC & SC_CAP>(p.sc, bias, size, 64);
-          loose = !exact && __all_sync(0xffffffffu, 2.f * z + ((SC & SC_BIAS) ? fabsf(bias.slp) * 64.f : 0.f) <= kLoose);
+          mx = most<SC>(p.sc, bias, size, 64);
+          const float rise = (SC & SC_BIAS) ? fabsf(bias.slp) * 64.f : 0.f;
+          loose = !exact && __all_sync(0xffffffffu, 2.f * most<SC & SC_CAP>(p.sc, bias, size, 64) + rise <= kLoose);
         }
         if (loose) {
-          if (c_lo < c_hi) mx = most<SC>(p.sc, bias, size, 64);
+          if (c_lo >= c_hi) mx = -INFINITY;
         } else if (exact) {
+          mx = -INFINITY;
           auto over = [&](auto li) {
-            const Cap<SC, kTiers> cap(p.sc);
+            const Cap<SC, kTiers> cap(cap_table);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               uint64_t w;
@@ -323,31 +408,29 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
           else
             over(Const<0>{});
         } else {
+          float mc[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mc[q] = -INFINITY;
           if (any_masked) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) v[c] = (mw >> c) & 1ull ? v[c] : __float_as_uint(-INFINITY);
-          }
-          float m2 = __uint_as_float(v[0]);
+            for (int c = 0; c < 64; ++c) mc[c & 3] = fmaxf(mc[c & 3], (mw >> c) & 1ull ? __uint_as_float(v[c]) : -INFINITY);
+          } else {
 #pragma unroll
-          for (int c = 1; c < 61; c += 4) {
-            mx = fmax3f(mx, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            m2 = fmax3f(m2, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+            for (int c = 0; c < 64; c += 2)
+              mc[(c >> 1) & 3] = fmax3f(mc[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
           }
-          mx = fmax3f(mx, __uint_as_float(v[61]), __uint_as_float(v[62]));
-          mx = most<SC>(p.sc, bias, fmax3f(mx, m2, __uint_as_float(v[63])), 64);
+          mx = most<SC>(p.sc, bias, fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3])), 64);
         }
-      }
-      const int tier = (SC & SC_CAP) ? tier_of(size, p.sc) : 0;
-      bounds[half * 128] = __float2bfloat16_ru(mx);
-      named_bar_sync(pair_bar, 64);
-      mx = fmaxf(__bfloat162float(bounds[0]), __bfloat162float(bounds[128]));
-      float alpha = 1.f;
-      if (mx > -INFINITY) {
-        if (m_run == -INFINITY) {
-          m_run = mx;  // nothing accumulated yet for this row
-        } else if (mx > m_run + 8.f) {
-          alpha = fast_exp2(m_run - mx);
-          m_run = mx;
+        bounds[half * 128] = __float2bfloat16_ru(mx);
+        named_bar_sync(pair_bar, 64);
+        mx = fmaxf(__bfloat162float(bounds[0]), __bfloat162float(bounds[128]));
+        if (mx > -INFINITY) {
+          if (m_run == -INFINITY) {
+            m_run = mx;  // nothing accumulated yet for this row
+          } else if (mx > m_run + 8.f) {
+            alpha = fast_exp2(m_run - mx);
+            m_run = mx;
+          }
         }
       }
       const float m_use = m_run == -INFINITY ? 0.f : m_run;
@@ -356,25 +439,21 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       uint64_t acc[2] = {0, 0};
       // weights of the 64 columns and their sums; mask: of those that the row sees
       auto weights = [&](auto ti, auto li, auto mask) {
-        const Cap<SC, decltype(ti)::value> cap(p.sc);
-#pragma unroll 1
+        const Cap<SC, decltype(ti)::value> cap(cap_table);
+#pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
-          uint32_t v[32], pk[16];
-          tmem_ld32(tS + 32 * ch, v);
-          const BiasLine part = bias.from(32 * ch);
-          const uint32_t m32 = (uint32_t)(mw >> (32 * ch));
-          tmem_ld_wait(v);
+          uint32_t pk[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            const int c = 2 * u;
+            const int c = 32 * ch + 2 * u;
             uint64_t w;
             float x0, x1;
             f32x2_split(cap(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                            with_bias<SC, decltype(li)::value, decltype(li)::value>(part, c, nm2), w),
+                            with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, nm2), w),
                         x0, x1);
             float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
             if constexpr (decltype(mask)::value != 0)
-              e0 = (m32 >> c) & 1u ? e0 : 0.f, e1 = (m32 >> (c + 1)) & 1u ? e1 : 0.f;
+              e0 = (mw >> c) & 1ull ? e0 : 0.f, e1 = (mw >> (c + 1)) & 1ull ? e1 : 0.f;
             acc[u & 1] = add_f32x2(acc[u & 1], f32x2(e0, e1));
             pk[u] = pack_bf16x2(e0, e1);
           }
