@@ -276,14 +276,13 @@ cudaError_t launch_fwd_any(const Scored* sc, int D, const CUtensorMap& tq, const
   }
 }
 cudaError_t launch_bwd_any(const Scored* sc, int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const CUtensorMap& tdo, const BwdParams& p, int which, const LseView& lse,
-                           cudaStream_t st) {
+                           const CUtensorMap& tdo, const BwdParams& p, int which, cudaStream_t st) {
   switch (sc ? sc->mode : 0) {
-    case SC_ON: return launch_bwd_score<SC_ON>(D, tq, tk, tv, tdo, p, sc->p, which, lse, st);
-    case SC_ON | SC_CAP: return launch_bwd_score<SC_ON | SC_CAP>(D, tq, tk, tv, tdo, p, sc->p, which, lse, st);
-    case SC_ON | SC_BIAS: return launch_bwd_score<SC_ON | SC_BIAS>(D, tq, tk, tv, tdo, p, sc->p, which, lse, st);
+    case SC_ON: return launch_bwd_score<SC_ON>(D, tq, tk, tv, tdo, p, sc->p, which, st);
+    case SC_ON | SC_CAP: return launch_bwd_score<SC_ON | SC_CAP>(D, tq, tk, tv, tdo, p, sc->p, which, st);
+    case SC_ON | SC_BIAS: return launch_bwd_score<SC_ON | SC_BIAS>(D, tq, tk, tv, tdo, p, sc->p, which, st);
     case SC_ON | SC_CAP | SC_BIAS:
-      return launch_bwd_score<SC_ON | SC_CAP | SC_BIAS>(D, tq, tk, tv, tdo, p, sc->p, which, lse, st);
+      return launch_bwd_score<SC_ON | SC_CAP | SC_BIAS>(D, tq, tk, tv, tdo, p, sc->p, which, st);
     default: return launch_bwd(D, tq, tk, tv, tdo, p, which, st);
   }
 }
@@ -436,18 +435,19 @@ ra_status bwd_common(const Bhsd& dout, const Bhsd& q, const Bhsd& k, const Bhsd&
   RA_TRY(make_tmap(k, &tk));
   RA_TRY(make_tmap(v, &tv));
   RA_TRY(make_tmap(dout, &tdo));
-  const LseView vl{lse, lsb, lsh, lss};
-  if (sc && sc->mode) {
-    TimedLaunch tl(RA_KERNEL_BWD_PRE, st);
-    RA_TRY(cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 2, vl, st)));
-  } else {
+  {
     TimedLaunch tl(RA_KERNEL_BWD_PRE, st);
     // with a row map (varlen in original order), out and lse stay in the
     // caller's layout order and are read through it
     RA_TRY(cuda_status(
-        launch_bwd_pre(vdo, vo, vl, nD, nlse2, stat_N, stat_L, p.ctl, row_map, st)));
+        launch_bwd_pre(vdo, vo, LseView{lse, lsb, lsh, lss}, nD, nlse2, stat_N, stat_L, p.ctl, row_map, st)));
   }
-  if (q.d == 128 && q.h == k.h && !(sc && sc->mode) && __atomic_load_n(&g_dkdv_pair, __ATOMIC_RELAXED)) {
+  const bool scored = sc && sc->mode;
+  if (scored) {  // corrects nD for the dK / dV kernel
+    TimedLaunch tl(RA_KERNEL_BWD_DQ, st);
+    RA_TRY(cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 1, st)));
+  }
+  if (q.d == 128 && q.h == k.h && !scored && __atomic_load_n(&g_dkdv_pair, __ATOMIC_RELAXED)) {
     CUtensorMap pq, pk, pv, pdo;  // 64-row boxes: the pair kernel loads 64 x 64 blocks
     RA_TRY(make_tmap(q, &pq, 64));
     RA_TRY(make_tmap(k, &pk, 64));
@@ -457,10 +457,11 @@ ra_status bwd_common(const Bhsd& dout, const Bhsd& q, const Bhsd& k, const Bhsd&
     RA_TRY(cuda_status(launch_dkdv_pair(pq, pk, pv, pdo, p, st)));
   } else {
     TimedLaunch tl(RA_KERNEL_BWD, st);
-    RA_TRY(cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 0, vl, st)));
+    RA_TRY(cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 0, st)));
   }
+  if (scored) return RA_OK;
   TimedLaunch tl(RA_KERNEL_BWD_DQ, st);
-  return cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 1, vl, st));
+  return cuda_status(launch_bwd_any(sc, (int)q.d, tq, tk, tv, tdo, p, 1, st));
 }
 
 // Scratch of ring_attn_bwd_static_scratch: one array per device, its device

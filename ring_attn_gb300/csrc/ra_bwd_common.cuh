@@ -34,10 +34,11 @@ static __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[6
 // [0, nvalid) are written: row l goes to row row0 + l of base (pitch `stride`),
 // or, with a row map, to row rmap[row0 + l] (a varlen call computed in
 // original order that writes its results in the caller's layout order).
-template <int N32>
+// LESS: `less` times the numbers at `other` are taken off before they are multiplied.
+template <int N32, bool LESS = false>
 static __device__ __forceinline__ void store_rows_bf16(uint32_t taddr, float mul, uint8_t* slot, __nv_bfloat16* base,
-                                                       long long stride, long long row0, int nvalid,
-                                                       const int* rmap) {
+                                                       long long stride, long long row0, int nvalid, const int* rmap,
+                                                       uint32_t other = 0, float less = 0.f) {
   constexpr int kPieces = 4 * N32;                      // 16-byte pieces per segment
   constexpr int kSwz = kPieces < 8 ? kPieces - 1 : 7;  // XOR mask on the piece index
   const int lane = threadIdx.x & 31;
@@ -47,6 +48,13 @@ static __device__ __forceinline__ void store_rows_bf16(uint32_t taddr, float mul
     uint32_t o[32];
     tmem_ld32(taddr + c * 32, o);
     tmem_ld_wait(o);
+    if constexpr (LESS) {
+      uint32_t y[32];
+      tmem_ld32(other + c * 32, y);
+      tmem_ld_wait(y);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(-less, __uint_as_float(y[k]), __uint_as_float(o[k])));
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       uint4 w;

@@ -118,6 +118,13 @@ cudaError_t launch_fwd_score(int D, const CUtensorMap& tq, const CUtensorMap& tk
 cudaError_t launch_bwd(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tdo, const BwdParams& p, int which, cudaStream_t st);
 
+// The backward with changed scores; one translation unit per SC.  The dQ kernel (which = 1) runs first: it corrects
+// the statistics nD, which the dK / dV kernel reads.
+template <int SC>
+cudaError_t launch_bwd_score(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const CUtensorMap& tdo, const BwdParams& p, const ScoreParams& sc, int which,
+                             cudaStream_t st);
+
 // The dK / dV kernel on CTA pairs (cta_group::2), head_dim 128 only.  The four
 // tensor maps have 64 x 64 boxes (64 head dims by 64 rows).
 cudaError_t launch_dkdv_pair(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -130,12 +137,6 @@ struct LseView {
   const float* data;
   long long sb, sh, ss;
 };
-// The backward with changed scores; one translation unit per SC.  which = 2, first: the statistics
-// (nD and nlse2 of p are written), from the products rather than from out.
-template <int SC>
-cudaError_t launch_bwd_score(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const CUtensorMap& tdo, const BwdParams& p, const ScoreParams& sc, int which,
-                             const LseView& lse, cudaStream_t st);
 // out_row: null, or out and lse rows by position (out and lse of position p
 // are row out_row[p] of their tensors; dout is read at p)
 cudaError_t launch_bwd_pre(const View4& dout, const View4& out, const LseView& lse, float* nD, float* nlse2, int N,

@@ -1,10 +1,11 @@
 // The ring backward with capped scores or a bias by distance.  Each ra_scored_bwd_*.cu makes it for one kind
 // of change, so that they compile side by side.
 //
-// The statistics pass, for every kind of change (a prefix alone, too), then the plain backward's two kernels
-// (ra_bwd.cuh: their tiles, their loads and their order of products) with scores changed as the forward does, P for dV, and
-// P times the cap's derivative for dS.  Two threads a row, as there: four, as in the forward with changed scores,
-// measured 2 % to 20 % slower, since each waits for two products a tile, not for its own instructions.
+// The plain backward's two kernels (ra_bwd.cuh: their tiles, their loads and their order of products) with scores
+// changed as the forward does, P for dV, and P times the cap's derivative for dS, and with an exact D (a prefix alone
+// takes the plain dK / dV kernel behind the dQ kernel here).  Two threads a row, as there: four, as in the
+// forward with changed scores, measured 2 % to 20 % slower, since each waits for two products a tile, not for its
+// own instructions.
 #pragma once
 
 #include "ra_bwd.cuh"
@@ -12,303 +13,6 @@
 
 namespace ra {
 namespace {
-
-// ======================================================================== D
-// Changed scores only: D_i = sum_j P_ij <dO_i, v_j> and the statistics that the other two kernels
-// read, -lse * log2(e) and -D of every row.
-//
-// With plain scores D is rowsum(dO * O) of the bf16 out.  O's rounding is an error of D that the sums over a row's keys
-// do not average away, and where a bias or a small cap leaves a row few keys, dP - D is small next
-// to dP: dQ and dK were off by up to 0.54 % (one head with a slope of 1), and 0.24 % with D from the
-// products themselves, which is what the rounding of dS and of the results leaves.  The price: two products of
-// the backward's nine.
-//
-// The forward's shape: a CTA owns two 128-row query tiles; warp 0 loads (K and V tiles in turn into one
-// ring), warp 1 issues S_t = Q_t K^T and dP_t = dO_t V^T (t = 0, 1), warpgroups 1 and 2 take a row
-// per thread: P from S in registers, then sum P dP.  Nothing goes back to the tensor cores, so the S and
-// dP columns (all 512) are free again as soon as they are read.
-template <int D>
-struct RowDotLayout {
-  static constexpr int kTile = (D / 64) * kBox;
-  static constexpr int kSlots = D == 128 ? 3 : 6;  // of the ring of K(0), V(0), K(1), V(1), ...
-  static constexpr int kQ = 0, kDO = 2 * kTile, kRing = 4 * kTile;
-  static constexpr int kBar = kRing + kSlots * kTile;
-  static constexpr int kNumBars = 1 + 2 * kSlots + 8 + 1;
-  static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kAlloc = kMisc + 16 + 1024;
-  // barriers
-  static constexpr int kQFull = 0, kFull = 1, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots, kDpFull = kSFull + 2,
-                       kSRead = kDpFull + 2, kDpRead = kSRead + 2, kTeardown = kDpRead + 2;
-};
-
-template <int D, bool VL, int SC>
-__global__ void __launch_bounds__(kThreads, 1)
-    ring_rowdot_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                       const BwdParamsT<VL, SC> p, const LseView lse, float* nD, float* nlse2) {
-  using LY = RowDotLayout<D>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sb = (raw + 1023u) & ~1023u;
-  uint8_t* sp = smem_raw + (sb - raw);
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
-  const int n_pairs = (p.L + 2 * kTileM - 1) / (2 * kTileM);
-  int r, i0;  // heavy rows first, as in the forward
-  if (!VL && p.causal && p.layout == LAYOUT_ZIGZAG && p.r_only < 0 && p.L % (4 * kTileM) == 0) {
-    int pr;
-    zigzag_heavy_first((int)blockIdx.x, p.N, n_pairs / 2, r, pr);
-    i0 = pr * 2 * kTileM;
-  } else {
-    const int x = p.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    r = p.r_only >= 0 ? p.r_only : x / n_pairs;
-    i0 = (x % n_pairs) * 2 * kTileM;
-  }
-  const uint32_t bar0 = sb + LY::kBar;
-  auto BAR = [bar0](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + LY::kMisc);
-  if (threadIdx.x == 0) {
-    mbar_init(BAR(LY::kQFull), 1);
-    for (int i = 0; i < LY::kSlots; ++i) {
-      mbar_init(BAR(LY::kFull + i), 1);
-      mbar_init(BAR(LY::kEmpty + i), 1);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(BAR(LY::kSFull + t), 1);
-      mbar_init(BAR(LY::kDpFull + t), 1);
-      mbar_init(BAR(LY::kSRead + t), 4);
-      mbar_init(BAR(LY::kDpRead + t), 4);
-    }
-    mbar_init(BAR(LY::kTeardown), 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-    prefetch_tmap(&tmDO);
-    const int qrow = r * p.L + i0 - p.q_base;
-    mbar_expect_tx(BAR(LY::kQFull), 4 * LY::kTile);
-    for (int t = 0; t < 2; ++t)
-      for (int c = 0; c < D / 64; ++c)
-        if (in_bounds(tma_coords_ok(TmaExtent{D, p.q_rows, p.H, p.B}, c * 64, qrow + t * kTileM, h, b), p.ctl, 20)) {
-          tma_load_4d(sb + LY::kQ + t * LY::kTile + c * kBox, &tmQ, BAR(LY::kQFull), c * 64, qrow + t * kTileM, h, b);
-          tma_load_4d(sb + LY::kDO + t * LY::kTile + c * kBox, &tmDO, BAR(LY::kQFull), c * 64, qrow + t * kTileM, h, b);
-        }
-  }
-  const int pre = VL ? 0 : prefix_of(p, b);
-  QRange cta;  // both query tiles
-  make_qrange(p, r, i0, 2 * kTileM, cta, pre);
-  const int nkt = (p.L + kTileN - 1) / kTileN;
-  int n_tiles = 0;
-  walk_kv_tiles(p, cta, nkt, 0, p.N, [&](int, int) {
-    ++n_tiles;
-    return true;
-  });
-  if (warp == 2) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S_t at 128 t, dP_t at 256 + 128 t
-
-  if (warp < 4) {
-    regs_dec<kDkdvRegsLow>();
-    if (warp == 0) {
-      // ------------------------------------------------------------ TMA producer
-      if (lane == 0 && n_tiles > 0) {
-        const int hk = h / p.G;
-        int n = 0, slot = 0;
-        uint32_t par = 1;  // of the slot's last release
-        auto load = [&](const CUtensorMap* tm, int row) -> bool {
-          if (n >= LY::kSlots && !wait_one(BAR(LY::kEmpty + slot), par, abort_flag, p.ctl, 70)) return false;
-          mbar_expect_tx(BAR(LY::kFull + slot), LY::kTile);
-          for (int c = 0; c < D / 64; ++c)
-            if (in_bounds(tma_coords_ok(TmaExtent{D, p.S, p.Hk, p.B}, c * 64, row, hk, b), p.ctl, 21))
-              tma_load_4d(sb + LY::kRing + slot * LY::kTile + c * kBox, tm, BAR(LY::kFull + slot), c * 64, row, hk, b);
-          ++n;
-          if (++slot == LY::kSlots) slot = 0, par ^= 1u;
-          return true;
-        };
-        walk_kv_tiles(p, cta, nkt, 0, p.N, [&](int s, int kt) {
-          const int row = s * p.L + kt * kTileN;
-          return load(&tmK, row) && load(&tmV, row);
-        });
-        // every load lands before the CTA ends
-        for (int i = 0; i < LY::kSlots; ++i) {
-          const int times = (n + LY::kSlots - 1 - i) / LY::kSlots;
-          if (times) drain_one(BAR(LY::kFull + i), (times - 1) & 1, p.ctl, 71);
-        }
-      }
-      if (lane == 0) drain_one(BAR(LY::kQFull), 0, p.ctl, 72);  // issued at entry
-      __syncwarp();
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      if (lane == 0 && n_tiles > 0) {
-        constexpr uint32_t kId = idesc_bf16_f32(128, kTileN, 0, 0);
-        constexpr uint32_t kHi = sdesc_sw128_hi(1024);
-        auto issue = [&](uint32_t dcol, uint32_t a, uint32_t bt, int bar) {
-          const uint32_t la = sdesc_sw128_lo(a, 16), lb = sdesc_sw128_lo(bt, 16);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + dcol, sdesc_words(la + off, kHi), sdesc_words(lb + off, kHi), kId, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(BAR(bar));
-        };
-        bool ok = wait_one(BAR(LY::kQFull), 0, abort_flag, p.ctl, 73);
-        int slot = 0;
-        uint32_t par = 0;
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          const uint32_t kat = sb + LY::kRing + slot * LY::kTile;
-          const int kslot = slot;
-          const uint32_t kpar = par;
-          if (++slot == LY::kSlots) slot = 0, par ^= 1u;
-          const uint32_t vat = sb + LY::kRing + slot * LY::kTile;
-          const int vslot = slot;
-          const uint32_t vpar = par;
-          if (++slot == LY::kSlots) slot = 0, par ^= 1u;
-          for (int t = 0; ok && t < 2; ++t) {
-            ok = (t > 0 || wait_one(BAR(LY::kFull + kslot), kpar, abort_flag, p.ctl, 74)) &&
-                 (j == 0 || wait_one(BAR(LY::kSRead + t), (j - 1) & 1, abort_flag, p.ctl, 75));
-            if (!ok) break;
-            tc_fence_after();
-            issue(128 * t, sb + LY::kQ + t * LY::kTile, kat, LY::kSFull + t);
-            if (t == 1 && 2 * j + LY::kSlots < 2 * n_tiles) mma_commit(BAR(LY::kEmpty + kslot));
-            ok = (t > 0 || wait_one(BAR(LY::kFull + vslot), vpar, abort_flag, p.ctl, 76)) &&
-                 (j == 0 || wait_one(BAR(LY::kDpRead + t), (j - 1) & 1, abort_flag, p.ctl, 77));
-            if (!ok) break;
-            tc_fence_after();
-            issue(256 + 128 * t, sb + LY::kDO + t * LY::kTile, vat, LY::kDpFull + t);
-            if (t == 1 && 2 * j + 1 + LY::kSlots < 2 * n_tiles) mma_commit(BAR(LY::kEmpty + vslot));
-          }
-        }
-        // every issued MMA completes before the CTA frees TMEM
-        mma_commit(BAR(LY::kTeardown));
-        drain_one(BAR(LY::kTeardown), 0, p.ctl, 78);
-      }
-      __syncwarp();
-    }
-  } else {
-    regs_inc<kDkdvRegsHigh>();
-    // ------------------------------------------------------------ P and sum P dP, a query row per thread
-    const int t = (warp - 4) >> 2;
-    const int row = ((warp - 4) & 3) * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + 128 * t, tP = tl + 256 + 128 * t;
-    const int i = i0 + t * kTileM + row;
-    const bool valid = i < p.L;
-    QRange qt;
-    RowWin win;
-    int gq = 0;
-    if constexpr (VL) {
-      gq = make_row_win(p, r, min(i, p.L - 1), false, win);
-    } else {
-      make_qrange(p, r, i0 + t * kTileM, kTileM, qt, pre);
-      gq = tok(p, r, valid ? i : max(qt.i_last, 0));
-    }
-    float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
-    // the row's lse: padding rows have +infinity, so that their weights are 0
-    float l = INFINITY;
-    if (valid) {
-      const long long q_row = (long long)r * p.L + i - p.q_base;
-      const long long lrow = VL && p.row_map ? (long long)__ldg(p.row_map + q_row) : q_row;
-      if (in_bounds(lrow >= 0 && lrow < p.q_rows, p.ctl, 22))
-        l = lse.data[(long long)b * lse.sb + (long long)h * lse.sh + lrow * lse.ss];
-    }
-    const float nl = l * -1.4426950408889634f;
-    const uint64_t nl2 = f32x2(nl, nl);
-    uint64_t acc[4] = {0, 0, 0, 0};
-    bool ok = true;
-    int j = 0;
-    walk_kv_tiles(p, cta, nkt, 0, p.N, [&](int s, int kt) {
-      int c_lo = 0, c_hi = kTileN;
-      if constexpr (VL)
-        row_win_cols(p, win, s, kt * kTileN, kTileN, c_lo, c_hi);
-      else if (!kv_tile_full(p, qt, s, kt))
-        row_key_window(p, seeing_token<decltype(p)>(gq, pre), s, kt, c_lo, c_hi);
-      const bool masked = c_lo > 0 || c_hi < kTileN;
-      if (!wait_warp(BAR(LY::kSFull + t), j & 1, abort_flag, p.ctl, 79)) {
-        ok = false;
-        return false;
-      }
-      tc_fence_after();
-      BiasLine bias = {};
-      TileTokens tokens;
-      if constexpr ((SC & SC_BIAS) != 0) tokens = tile_tokens(p, win, s, kt * kTileN);
-      // half a row at a time, so that it stays in registers
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t v[64];
-        tmem_ld64(tS + 64 * hh, v);
-        if (hh == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(LY::kSRead + t));
-        }
-        int tier = 0;
-        bool line = true;
-        if constexpr ((SC & SC_BIAS) != 0) {
-          if (hh) tokens.t0 += 64 * tokens.st, tokens.t1 += 64 * tokens.st, tokens.cb -= 64;
-          bias = bias_line(tokens, gq, max(c_lo - 64 * hh, 0), min(c_hi - 64 * hh, 64), slope2);
-          line = __all_sync(0xffffffffu, bias.line);
-          bias.off += nl;
-        }
-        if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
-        with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-          const Cap<SC, decltype(ti)::value> cap(p.sc);
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            uint64_t w;
-            float x0, x1;
-            f32x2_split(cap(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                            with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, nl2), w),
-                        x0, x1);
-            v[c] = __float_as_uint(fast_exp2(x0)), v[c + 1] = __float_as_uint(fast_exp2(x1));
-          }
-        });
-        if (masked) {
-          const uint64_t mw = bit_window64(c_lo - 64 * hh, c_hi - 64 * hh);
-#pragma unroll
-          for (int u = 0; u < 64; ++u) v[u] = ((mw >> u) & 1ull) ? v[u] : 0u;
-        }
-        if (hh == 0 && !wait_warp(BAR(LY::kDpFull + t), j & 1, abort_flag, p.ctl, 80)) {
-          ok = false;
-          return false;
-        }
-        tc_fence_after();
-        uint32_t d[64];
-        tmem_ld64(tP + 64 * hh, d);
-#pragma unroll
-        for (int u = 0; u < 64; u += 2)
-          acc[(u >> 1) & 3] = fma_f32x2(f32x2(__uint_as_float(v[u]), __uint_as_float(v[u + 1])),
-                                        f32x2(__uint_as_float(d[u]), __uint_as_float(d[u + 1])), acc[(u >> 1) & 3]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(LY::kDpRead + t));
-      ++j;
-      return true;
-    });
-    if (i < p.stat_L) {
-      float a0, a1;
-      f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), a0, a1);
-      const long long at = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
-      nD[at] = valid && ok ? -(a0 + a1) : 0.f;
-      nlse2[at] = nl;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
-}
 
 // ======================================================================== dK / dV
 template <int D, bool VL, int SC>
@@ -678,12 +382,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ======================================================================== dQ
+// D = rowsum(dO * O) comes from the bf16 out, and O's rounding is an error of D that the sums over a row's keys do not
+// average away: where a bias or a small cap leaves a row few keys, dP - D is small next to dP, and dQ and dK
+// were off by up to 0.54 % (one head with a slope of 1).  Since the weights of a row sum to 1, the dQ pass gets the
+// missing part for a multiply-add a score:
+//   e = sum_j P_ij (dP_ij - D_i),  D_i + e is exact,  dQ_i = scale (sum_j dS_ij k_j - e sum_j P'_ij k_j)
+// (P': P times the cap's derivative), for which it keeps a second product's sum.  It runs first and corrects the
+// statistics for the dK / dV pass.  dQ and dK are then off by 0.24 %, which is what the rounding of dS and of the
+// results leaves.  (A pass of its own for sum P dP, two products more, took 0.52 ms at 8192 tokens of 32 + 8 heads
+// of 128, where this takes 0.31 ms.)
+//
+// TMEM: S [0, 128), dP [128, 256).  d = 128: the sums of dS K and of P' K take the rest, so that Q and dO stay in shared
+// memory; d = 64: as in the plain kernel, with the second sum behind the first.  P' is packed beside dS, over the
+// second 32 of a thread's 64 dP columns.
+template <int D>
+struct ScoredDqLayout : DqLayout<D> {
+  using Base = DqLayout<D>;
+  static constexpr bool kQInTmem = D == 64;
+  static constexpr int kSums = Base::kMisc + 16;  // 2 halves x 128 rows
+  static constexpr int kAlloc = kSums + 1024 + 1024;
+  static constexpr uint32_t kTmemDQ = kQInTmem ? 384 : 256, kTmemPK = kTmemDQ + D;
+};
+
 template <int D, bool VL, int SC>
 __global__ void __launch_bounds__(kThreads, 1)
     ring_scored_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                    const BwdParamsT<VL, SC> p) {
-  using LY = DqLayout<D>;
+  using LY = ScoredDqLayout<D>;
   constexpr int KS = LY::kKStages, VS = LY::kVStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -761,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (warp < 4) regs_dec<kDkdvRegsLow>();
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ TMA producers
     if (warp == 0 && lane == 0 && n_tiles > 0) {
@@ -795,14 +522,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && n_tiles > 0) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kTileN, 0, 0);  // S = Q K^T, dP = dO V^T: TMEM A, K-major B
       constexpr uint32_t kIdQ = idesc_bf16_f32(128, D, 0, 1);       // dQ += dS K: TMEM A, MN-major B
-      bool ok = wait_one(BAR(F_QDO_TMEM), 0, abort_flag, p.ctl, 55);
-      // X = A B^T over D with A (Q or dO) packed in TMEM, 16 head-dim columns = 8 TMEM columns per step
-      auto issue_t = [&](uint32_t dcol, uint32_t acol, uint32_t bt) {
-        const uint64_t db = sdesc_sw128(bt, 16, 1024);
+      bool ok = wait_one(BAR(LY::kQInTmem ? F_QDO_TMEM : F_QDO_FULL), 0, abort_flag, p.ctl, 55);
+      // X = A B^T over D with A (Q or dO) packed in TMEM, 16 head-dim columns = 8 TMEM columns per step, or in
+      // shared memory, K-major like B
+      auto issue_t = [&](uint32_t dcol, uint32_t acol, uint32_t at, uint32_t bt) {
+        const uint64_t da = sdesc_sw128(at, 16, 1024), db = sdesc_sw128(bt, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-          mma_bf16_ts(tmem + dcol, tmem + acol + 8 * kk, sdesc_add(db, off), kIdS, kk > 0 ? 1u : 0u);
+          if constexpr (LY::kQInTmem)
+            mma_bf16_ts(tmem + dcol, tmem + acol + 8 * kk, sdesc_add(db, off), kIdS, kk > 0 ? 1u : 0u);
+          else
+            mma_bf16_ss(tmem + dcol, sdesc_add(da, off), sdesc_add(db, off), kIdS, kk > 0 ? 1u : 0u);
         }
       };
       auto issue_s = [&](int j) -> bool {
@@ -810,14 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_one(BAR(F_V_FULL + j % VS), (j / VS) & 1, abort_flag, p.ctl, 56)) return false;
         if (j > 0 && !wait_one(BAR(F_S_READ), (j - 1) & 1, abort_flag, p.ctl, 57)) return false;
         tc_fence_after();
-        issue_t(LY::kTmemS, LY::kTmemQ, sb + LY::kK + ks * LY::kTile);
+        issue_t(LY::kTmemS, LY::kTmemQ, sb + LY::kQ, sb + LY::kK + ks * LY::kTile);
         mma_commit(BAR(F_S_FULL));
         return true;
       };
       // dP(j) overwrites dS(j-1), which the dQ MMA issued before it has read
       auto issue_dp = [&](int j) -> bool {
         const int vs = j % VS;  // V(j) landed with K(j), waited for before S(j)
-        issue_t(LY::kTmemDP, LY::kTmemDO, sb + LY::kV + vs * LY::kTile);
+        issue_t(LY::kTmemDP, LY::kTmemDO, sb + LY::kDO, sb + LY::kV + vs * LY::kTile);
         mma_commit(BAR(F_DP_FULL));
         if (j + VS < n_tiles) mma_commit(BAR(F_V_EMPTY + vs));
         return true;
@@ -832,6 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_bf16_ts(tmem + LY::kTmemDQ, tmem + LY::kTmemDP + pcol(kk), sdesc_add(dkb, kk * 2048),
                       kIdQ, (j > 0 || kk > 0) ? 1u : 0u);
         }
+#pragma unroll
+        for (int kk = 0; kk < kTileN / 16; ++kk)  // P' K
+          mma_bf16_ts(tmem + LY::kTmemPK, tmem + LY::kTmemDP + pcol(kk) + 32, sdesc_add(dkb, kk * 2048), kIdQ,
+                      (j > 0 || kk > 0) ? 1u : 0u);
         if (j + KS < n_tiles) mma_commit(BAR(F_K_EMPTY + j % KS));
         return true;
       };
@@ -850,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
+    regs_inc<kDkdvRegsHigh>();
     // ------------------------------------------------------------ P and dS, half a query row per thread
     const int half = (warp - 4) >> 2;  // key columns [64 half, 64 half + 64)
     const int row = ((warp - 4) & 3) * 32 + lane;
@@ -867,13 +603,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long srow = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
     const float nl = __ldg(p.nlse2 + srow);
     const uint64_t nl2 = f32x2(nl, nl);
-    const uint64_t nD2 = f32x2(__ldg(p.nD + srow), __ldg(p.nD + srow));
+    const float nD = p.nD[srow];
+    const uint64_t nD2 = f32x2(nD, nD);
     float slope2 = 0.f;
     if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
     // warpgroup 1 copies the row's Q, warpgroup 2 its dO, into tensor memory as
     // packed bf16 (column m: head-dim elements 2m, 2m + 1) for the S and dP MMAs
-    bool ok = n_tiles == 0 || wait_warp(BAR(F_QDO_FULL), 0, abort_flag, p.ctl, 64);
-    if (ok && n_tiles > 0) {
+    bool ok = n_tiles == 0 || !LY::kQInTmem || wait_warp(BAR(F_QDO_FULL), 0, abort_flag, p.ctl, 64);
+    if (LY::kQInTmem && ok && n_tiles > 0) {
       const uint8_t* src = sp + (half == 0 ? LY::kQ : LY::kDO);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -894,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(F_QDO_TMEM));
     }
+    uint64_t miss[2] = {0, 0};  // sums of P (dP - D)
     int j = 0;
     if (ok) walk_kv_tiles(p, qr, nkt, 0, p.N, [&](int s, int kt) {
       int c_lo = 0, c_hi = kTileN;
@@ -919,13 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tier = 0;
       bool line = true;
       if constexpr ((SC & SC_BIAS) != 0) {
-        bias =
-            bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, max(c_lo, 0), min(c_hi, 64), slope2);
+        bias = bias_line(tile_tokens(p, win, s, kt * kTileN + 64 * half), gq, max(c_lo, 0), min(c_hi, 64), slope2);
         line = __all_sync(0xffffffffu, bias.line);
         bias.off += nl;
       }
       if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
-      // P times the cap's derivative
+      uint32_t g[(SC & SC_CAP) != 0 ? 64 : 1];  // P times the cap's derivative
       with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
         const Cap<SC, decltype(ti)::value, true> cap(p.sc);
 #pragma unroll
@@ -936,42 +673,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                           with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, nl2), w),
                       x0, x1);
           x0 = fast_exp2(x0), x1 = fast_exp2(x1);
-          if constexpr ((SC & SC_CAP) != 0)
-            f32x2_split(mul_f32x2(f32x2(x0, x1), cap.derivative(w)), x0, x1);
           v[c] = __float_as_uint(x0), v[c + 1] = __float_as_uint(x1);
+          if constexpr ((SC & SC_CAP) != 0) {
+            f32x2_split(mul_f32x2(f32x2(x0, x1), cap.derivative(w)), x0, x1);
+            g[c] = __float_as_uint(x0), g[c + 1] = __float_as_uint(x1);
+          }
         }
       });
       if (masked) {
         const uint64_t mw = bit_window64(c_lo, c_hi);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) v[c] = ((mw >> c) & 1ull) ? v[c] : 0u;
+        for (int c = 0; c < 64; ++c) {
+          v[c] = ((mw >> c) & 1ull) ? v[c] : 0u;
+          if constexpr ((SC & SC_CAP) != 0) g[c] = ((mw >> c) & 1ull) ? g[c] : 0u;
+        }
       }
       if (!wait_warp(BAR(F_DP_FULL), j & 1, abort_flag, p.ctl, 62)) {
         ok = false;
         return false;
       }
       tc_fence_after();
-      // dS = P * (dP - D), 32 dP columns at a time, packed (column m: keys 2m, 2m + 1)
-      // over the first 32 of this thread's 64 dP columns once they are read
+      // dS = P' * (dP - D) and P', packed (column m: keys 2m, 2m + 1) over this thread's 64 dP columns once they are read
       const uint32_t tdp = tl + LY::kTmemDP + 64 * half;
+      uint32_t ds[32], pp[32];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         uint32_t d[32];
         tmem_ld32(tdp + 32 * hh, d);
         tmem_ld_wait(d);
-        uint32_t pk[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
           const int c = 32 * hh + 2 * u;
-          // dS = P * (dP + (-D)), two lanes per instruction
-          float s0, s1;
-          f32x2_split(mul_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                                add_f32x2(f32x2(__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])), nD2)),
-                      s0, s1);
-          pk[u] = pack_bf16x2(s0, s1);
+          const uint64_t pair = f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+          const uint64_t diff = add_f32x2(f32x2(__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])), nD2);
+          miss[u & 1] = fma_f32x2(pair, diff, miss[u & 1]);
+          uint64_t grad = pair;
+          if constexpr ((SC & SC_CAP) != 0) grad = f32x2(__uint_as_float(g[c]), __uint_as_float(g[c + 1]));
+          float s0, s1, p0, p1;
+          f32x2_split(mul_f32x2(grad, diff), s0, s1);
+          f32x2_split(grad, p0, p1);
+          ds[c / 2] = pack_bf16x2(s0, s1);
+          pp[c / 2] = pack_bf16x2(p0, p1);
         }
-        tmem_st16(tdp + 16 * hh, pk);
       }
+      tmem_st32(tdp, ds);
+      tmem_st32(tdp + 32, pp);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -979,7 +725,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++j;
       return true;
     });
-    // ---------------- epilogue: dQ = scale * (dS K), half the head dim per thread
+    // the row's missing part of D, of both halves (every warp of a pair comes here, whatever happened before)
+    float e0, e1;
+    f32x2_split(add_f32x2(miss[0], miss[1]), e0, e1);
+    float* sums = reinterpret_cast<float*>(sp + LY::kSums) + row;
+    sums[half * 128] = e0 + e1;
+    named_bar_sync(1 + (warp & 3), 64);
+    const float missing = sums[0] + sums[128];
+    if (half == 0 && valid && ok) const_cast<float*>(p.nD)[srow] = nD - missing;
+    // ---------------- epilogue: dQ = scale * (dS K - missing P' K), half the head dim per thread
     const int* rmap = VL ? p.row_map : nullptr;  // varlen in original order: rows of the caller's layout
     __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(p.dq) + (long long)b * p.q_sb + (long long)h * p.q_sh +
                           half * (D / 2);
@@ -993,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nvalid = min(max(p.L - i_w, 0), 32);
         const long long row_w = (long long)r * p.L + i_w - p.q_base;  // the warp's first row of dq
         if (in_bounds(nvalid == 0 || (row_w >= 0 && row_w + nvalid <= p.q_rows), p.ctl, 18))
-          store_rows_bf16<D / 64>(tl + LY::kTmemDQ + half * (D / 2), p.scale, sp + (warp - 4) * (32 * D), base,
-                                  p.q_ss, row_w, nvalid, rmap);
+          store_rows_bf16<D / 64, true>(tl + LY::kTmemDQ + half * (D / 2), p.scale, sp + (warp - 4) * (32 * D), base,
+                                        p.q_ss, row_w, nvalid, rmap, tl + LY::kTmemPK + half * (D / 2), missing);
       }
     } else if (valid && in_bounds(qrow < p.q_rows, p.ctl, 19)) {
       __nv_bfloat16* dst = base + (rmap ? (long long)__ldg(rmap + qrow) : qrow) * p.q_ss;
@@ -1012,33 +766,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int SC, int D, bool VL>
 cudaError_t launch_bwd_sdv(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
-                           const BwdParams& p, const ScoreParams& sc, int which, const LseView& lse, cudaStream_t st) {
+                           const BwdParams& p, const ScoreParams& sc, int which, cudaStream_t st) {
   BwdParamsT<VL, SC> pv;
   static_cast<BwdParams&>(pv) = p;
   pv.sc = sc;
   // the register splits inside the kernels are only safe with the launch allocation they were sized for
-  if (which == 2) {
-    using LY = RowDotLayout<D>;
-    cudaError_t e = configure_kernel<ring_rowdot_kernel<D, VL, SC>>(kDkdvLaunchRegs, LY::kAlloc);
+  if (which == 1) {
+    using LY = ScoredDqLayout<D>;
+    cudaError_t e = configure_kernel<ring_scored_dq_kernel<D, VL, SC>>(kDkdvLaunchRegs, LY::kAlloc);
     if (e != cudaSuccess) return e;
-    const int n_pairs = (p.L + 2 * kTileM - 1) / (2 * kTileM);
-    dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * n_pairs), (unsigned)(p.B * p.H));
-    ring_rowdot_kernel<D, VL, SC><<<grid, kThreads, LY::kAlloc, st>>>(
-        tq, tk, tv, tdo, pv, lse, const_cast<float*>(p.nD), const_cast<float*>(p.nlse2));
-    return cudaGetLastError();
-  }
-  if constexpr (SC == SC_ON) {
-    return launch_bwd_v<D, VL, SC>(tq, tk, tv, tdo, pv, which, st);
-  } else if (which == 0) {
+    dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * p.n_qtiles), (unsigned)(p.B * p.H));
+    ring_scored_dq_kernel<D, VL, SC><<<grid, kThreads, LY::kAlloc, st>>>(tq, tk, tv, tdo, pv);
+  } else if constexpr (SC == SC_ON) {
+    return launch_bwd_v<D, VL, SC>(tq, tk, tv, tdo, pv, 0, st);
+  } else {
     cudaError_t e = configure_kernel<ring_scored_dkdv_kernel<D, VL, SC>>(kDkdvLaunchRegs, DkdvLayout<D>::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(p.N * p.n_ktiles), (unsigned)(p.B * p.Hk));
     ring_scored_dkdv_kernel<D, VL, SC><<<grid, kThreads, DkdvLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, pv);
-  } else {
-    cudaError_t e = configure_kernel<ring_scored_dq_kernel<D, VL, SC>>(0, DqLayout<D>::kAlloc);
-    if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * p.n_qtiles), (unsigned)(p.B * p.H));
-    ring_scored_dq_kernel<D, VL, SC><<<grid, kThreads, DqLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, pv);
   }
   return cudaGetLastError();
 }
@@ -1048,12 +793,12 @@ cudaError_t launch_bwd_sdv(const CUtensorMap& tq, const CUtensorMap& tk, const C
 template <int SC>
 cudaError_t launch_bwd_score(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const CUtensorMap& tdo, const BwdParams& p, const ScoreParams& sc, int which,
-                             const LseView& lse, cudaStream_t st) {
+                             cudaStream_t st) {
   if (D == 64)
-    return p.cu ? launch_bwd_sdv<SC, 64, true>(tq, tk, tv, tdo, p, sc, which, lse, st)
-                : launch_bwd_sdv<SC, 64, false>(tq, tk, tv, tdo, p, sc, which, lse, st);
-  return p.cu ? launch_bwd_sdv<SC, 128, true>(tq, tk, tv, tdo, p, sc, which, lse, st)
-              : launch_bwd_sdv<SC, 128, false>(tq, tk, tv, tdo, p, sc, which, lse, st);
+    return p.cu ? launch_bwd_sdv<SC, 64, true>(tq, tk, tv, tdo, p, sc, which, st)
+                : launch_bwd_sdv<SC, 64, false>(tq, tk, tv, tdo, p, sc, which, st);
+  return p.cu ? launch_bwd_sdv<SC, 128, true>(tq, tk, tv, tdo, p, sc, which, st)
+              : launch_bwd_sdv<SC, 128, false>(tq, tk, tv, tdo, p, sc, which, st);
 }
 
 }  // namespace ra

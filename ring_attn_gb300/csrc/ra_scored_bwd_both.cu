@@ -3,4 +3,4 @@
 
 template cudaError_t ra::launch_bwd_score<ra::SC_ON | ra::SC_CAP | ra::SC_BIAS>(int, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                               const CUtensorMap&, const ra::BwdParams&, const ra::ScoreParams&, int,
-                                              const ra::LseView&, cudaStream_t);
+                                              cudaStream_t);
