@@ -27,7 +27,7 @@
 // 2048 tokens of 32 heads at the end of 65,536 keys of 8 heads: 1.53 ms, 1413 TFLOP/s
 // (73 % of the measured bf16 rate); 1.41 ms without the conversions, 1.19 without softmax.
 // SC (ra_score.cuh): 0 for plain scores, else a call's cap, bias by distance or prefix
-// (ra_cache_chunk_*.cu): the softmax warps change a row's scores where they lie, in registers, before the mask.
+// (ra_cache_chunk_*.cu), which the softmax warps apply.
 // fp16 operands hold number * scale exactly; queries and p are rounded to fp16 and the rest is
 // fp32, as in ra_cache_attn.cu, whose comment says what that costs.
 #pragma once
@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
       }
       const bool valid = row < x.rows;
       float M = kNone, l_run = 0.f;
+      int at_least = 0;
       const int step = twin ? 2 : 1;
       for (int u = twin ? u0 + t : u0; u < u1; u += step, ++n_s) {
         const int c_hi = end_row - u * kUnit;
@@ -505,100 +506,167 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           break;
         }
         tc_fence_after();
-        uint32_t v[kUnit];
-        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(v + 0));
-        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 0));
-        tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
-        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(v + 64));
-        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(v + 96));
-        if constexpr (kChanged) {
-          // scores as they count, in log2 units
-          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
-          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
-          BiasLine bias = {};
-          int tier = 0;
-          bool line = true;
-          if constexpr ((SC & SC_BIAS) != 0) {
-            bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
-            line = __all_sync(0xffffffffu, bias.line);
-          }
-          if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, sc);
-          with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-            const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
-#pragma unroll
-            for (int c = 0; c < kUnit; c += 2) {
-              uint64_t w;
-              float z0, z1;
-              f32x2_split(cap(mul_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f32x2(sc, sc)),
-                              with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, 0), w),
-                          z0, z1);
-              v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
-            }
-          });
-        }
-        float mc[4];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (!kChanged && hh == 1) {
-            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
-            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
-          }
-          if (c_hi < kUnit) {
-            const uint64_t mw = bit_window64(0, c_hi - 64 * hh);
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              v[64 * hh + k] = ((mw >> k) & 1ull) ? v[64 * hh + k] : __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c0 = 64 * hh + 16 * q;
-            float m = hh == 0 ? __uint_as_float(v[c0]) : fmaxf(mc[q], __uint_as_float(v[c0]));
-#pragma unroll
-            for (int c = c0 + 1; c < c0 + 15; c += 2) m = fmax3f(m, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            mc[q] = fmaxf(m, __uint_as_float(v[c0 + 15]));
-          }
-        }
-        float mx = fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3]));
-        if constexpr (!kChanged) mx = __fmul_rn(mx, sc);
-        float alpha = 1.f;
-        if (mx > M + (kLift + kSlack)) {
-          alpha = fast_exp2(M - (mx - kLift));
-          M = mx - kLift;
-        }
-        const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(-M, -M);
-        uint64_t acc[4] = {0, 0, 0, 0};
-        // Offsets so large that the product's rounding shows next to them: the
-        // products are rounded first, so that the largest score gives an exact difference.
-        const bool far = __any_sync(0xffffffffu, fabsf(M) > 65536.f && M > kNone);
-        auto weights = [&](auto rounded) {
-#pragma unroll
-          for (int c32 = 0; c32 < kUnit / 32; ++c32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int c = c32 * 32 + 2 * k;
-              float x0 = __uint_as_float(v[c]), x1 = __uint_as_float(v[c + 1]);
-              if constexpr (kChanged)
-                f32x2_split(add_f32x2(f32x2(x0, x1), nm2), x0, x1);
-              else if constexpr (decltype(rounded)::value)
-                x0 = __fsub_rn(__fmul_rn(x0, sc), M), x1 = __fsub_rn(__fmul_rn(x1, sc), M);
-              else
-                f32x2_split(fma_f32x2(f32x2(x0, x1), sc2, nm2), x0, x1);
-              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-              acc[k & 3] = add_f32x2(acc[k & 3], f32x2(e0, e1));
-              pk[k] = pack_f16x2(e0, e1);
-            }
-            tmem_st16(tS + c32 * 16, pk);
+        float alpha = 1.f, sum;
+        auto raise = [&](float mx) {
+          if (mx > M + (kLift + kSlack)) {
+            alpha = fast_exp2(M - (mx - kLift));
+            M = mx - kLift;
           }
         };
-        if (!kChanged && far)
-          weights(Int<1>{});
-        else
-          weights(Int<0>{});
-        float s0, s1;
-        f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);
-        l_run = l_run * alpha + (s0 + s1);
+        if constexpr (SC == (SC_ON | SC_CAP)) {
+          // A cap keeps the products' order, so the largest product gives the offset, and the scores are made on their
+          // way to the exponential.  The products are read twice, 32 at a time, in loops: little code, for which the
+          // warps wait less (three chunks of up to 700 tokens over up to 20,000 keys, 32 heads of 8: 0.30 ms; 64 at a
+          // time 0.37, all 128 in registers 0.60, changed there as with a bias below 0.34).
+          float hi[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
+          const bool cut = __any_sync(0xffffffffu, c_hi < kUnit);
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t v[32];
+            tmem_ld32(tS + 32 * ch, v);
+            tmem_ld_wait(v);
+            auto at = [&](int k) { return __uint_as_float(v[k]); };
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) size[(k >> 1) & 1] = fmax3f(size[(k >> 1) & 1], fabsf(at(k)), fabsf(at(k + 1)));
+            if (cut) {
+              const uint32_t m32 = (uint32_t)bit_window64(0, c_hi - 32 * ch);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) hi[k & 1] = fmaxf(hi[k & 1], (m32 >> k) & 1u ? at(k) : -INFINITY);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) hi[(k >> 1) & 1] = fmax3f(hi[(k >> 1) & 1], at(k), at(k + 1));
+            }
+          }
+          raise(most<SC>(a.sc, BiasLine{}, fmaxf(hi[0], hi[1]) * sc, kUnit));
+          const int tier = max(tier_of(fmaxf(size[0], size[1]) * sc, a.sc), at_least);
+          at_least = min(tier, 1);  // (nor do warps go back and forth between the least two: 0.33 ms with it)
+          const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(-M, -M);
+          uint64_t acc[2] = {0, 0};
+          auto weights = [&](auto ti, auto mask) {
+            const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t v[32], pk[16];
+              tmem_ld32(tS + 32 * ch, v);
+              const uint32_t m32 = decltype(mask)::value ? (uint32_t)bit_window64(0, c_hi - 32 * ch) : 0u;
+              tmem_ld_wait(v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                uint64_t w;
+                float e0, e1;
+                f32x2_split(cap(mul_f32x2(f32x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc2), nm2, w),
+                            e0, e1);
+                e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+                if constexpr (decltype(mask)::value != 0)
+                  e0 = (m32 >> (2 * k)) & 1u ? e0 : 0.f, e1 = (m32 >> (2 * k + 1)) & 1u ? e1 : 0.f;
+                acc[k & 1] = add_f32x2(acc[k & 1], f32x2(e0, e1));
+                pk[k] = pack_f16x2(e0, e1);
+              }
+              tmem_st16(tS + ch * 16, pk);
+            }
+          };
+          if (cut)
+            with_score_flags<SC>(max(tier, 2), true, [&](auto ti, auto) {
+              if constexpr (decltype(ti)::value >= 2) weights(ti, Int<1>{});
+            });
+          else
+            with_score_flags<SC>(tier, true, [&](auto ti, auto) { weights(ti, Int<0>{}); });
+          float s0, s1;
+          f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
+          sum = s0 + s1;
+        } else {
+          uint32_t v[kUnit];
+          tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(v + 0));
+          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 0));
+          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(v + 64));
+          tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(v + 96));
+          if constexpr (kChanged) {
+            // scores as they count, in log2 units
+            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
+            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
+            BiasLine bias = {};
+            int tier = 0;
+            bool line = true;
+            if constexpr ((SC & SC_BIAS) != 0) {
+              bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
+              line = __all_sync(0xffffffffu, bias.line);
+            }
+            if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, sc);
+            with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
+              const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
+#pragma unroll
+              for (int c = 0; c < kUnit; c += 2) {
+                uint64_t w;
+                float z0, z1;
+                f32x2_split(cap(mul_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f32x2(sc, sc)),
+                                with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, 0), w),
+                            z0, z1);
+                v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
+              }
+            });
+          }
+          float mc[4];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (!kChanged && hh == 1) {
+              tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
+              tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
+            }
+            if (c_hi < kUnit) {
+              const uint64_t mw = bit_window64(0, c_hi - 64 * hh);
+#pragma unroll
+              for (int k = 0; k < 64; ++k)
+                v[64 * hh + k] = ((mw >> k) & 1ull) ? v[64 * hh + k] : __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int c0 = 64 * hh + 16 * q;
+              float m = hh == 0 ? __uint_as_float(v[c0]) : fmaxf(mc[q], __uint_as_float(v[c0]));
+#pragma unroll
+              for (int c = c0 + 1; c < c0 + 15; c += 2) m = fmax3f(m, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+              mc[q] = fmaxf(m, __uint_as_float(v[c0 + 15]));
+            }
+          }
+          float mx = fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3]));
+          if constexpr (!kChanged) mx = __fmul_rn(mx, sc);
+          raise(mx);
+          const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(-M, -M);
+          uint64_t acc[4] = {0, 0, 0, 0};
+          // Offsets so large that the product's rounding shows next to them: the
+          // products are rounded first, so that the largest score gives an exact difference.
+          const bool far = __any_sync(0xffffffffu, fabsf(M) > 65536.f && M > kNone);
+          auto weights = [&](auto rounded) {
+#pragma unroll
+            for (int c32 = 0; c32 < kUnit / 32; ++c32) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const int c = c32 * 32 + 2 * k;
+                float x0 = __uint_as_float(v[c]), x1 = __uint_as_float(v[c + 1]);
+                if constexpr (kChanged)
+                  f32x2_split(add_f32x2(f32x2(x0, x1), nm2), x0, x1);
+                else if constexpr (decltype(rounded)::value)
+                  x0 = __fsub_rn(__fmul_rn(x0, sc), M), x1 = __fsub_rn(__fmul_rn(x1, sc), M);
+                else
+                  f32x2_split(fma_f32x2(f32x2(x0, x1), sc2, nm2), x0, x1);
+                const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                acc[k & 3] = add_f32x2(acc[k & 3], f32x2(e0, e1));
+                pk[k] = pack_f16x2(e0, e1);
+              }
+              tmem_st16(tS + c32 * 16, pk);
+            }
+          };
+          if (!kChanged && far)
+            weights(Int<1>{});
+          else
+            weights(Int<0>{});
+          float s0, s1;
+          f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])), s0, s1);
+          sum = s0 + s1;
+        }
+        l_run = l_run * alpha + sum;
         // O_t is stable here: the commit behind S_FULL covers PV_t of the unit before
         if (u >= u0 + step && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
