@@ -242,6 +242,32 @@ __device__ __forceinline__ void with_score_flags(int tier, bool line, F&& f) {
     f(Const<kTiers>{}, Const<1>{});
 }
 
+// The tile and the head of this block, of a grid of (shards' tiles, batch x heads): every head's heaviest tiles first,
+// so that the light ones end the grid (a head after the other, the last heads' heavy tiles kept few SMs busy at the
+// end: 16,384 tokens of 32 heads 1.82 ms, so 1.72; dK and dV of 8192 tokens of 32 + 8 heads 1.10 and 0.88).
+// Causal calls: late query tiles see more keys, early key tiles are seen by more queries (kLate).
+struct Start {
+  int r, i0, head;  // shard, first row there, batch x heads
+};
+template <bool VL, bool kLate, int kRows, class P>
+__device__ __forceinline__ Start start_of(const P& p, int n, int only) {  // n: tiles a shard
+  const unsigned lin = blockIdx.y * gridDim.x + blockIdx.x;
+  const int x = (int)(lin / gridDim.y), total = (int)gridDim.x, late = kLate ? x : total - 1 - x;
+  Start s;
+  s.head = (int)(lin % gridDim.y);
+  int tile;
+  if (!VL && p.causal && p.layout == LAYOUT_ZIGZAG && only < 0 && p.L % (2 * kRows) == 0) {
+    zigzag_heavy_first(late, p.N, n / 2, s.r, tile);
+  } else {
+    const int o = p.causal && kLate ? total - 1 - x : x;
+    const bool dealt = !VL && p.causal && p.layout == LAYOUT_STRIPE && only < 0;  // tile t of every shard: alike
+    s.r = only >= 0 ? only : dealt ? o % p.N : o / n;
+    tile = dealt ? o / p.N : o % n;
+  }
+  s.i0 = tile * kRows;
+  return s;
+}
+
 // The largest magnitude of N products (none that is NaN).
 template <int N>
 __device__ __forceinline__ float largest(const uint32_t (&v)[N]) {

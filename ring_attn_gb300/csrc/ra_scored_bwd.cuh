@@ -28,9 +28,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // one key / value head; with grouped-query attention its G query heads share it
-  const int b = blockIdx.y / p.Hk, hk = blockIdx.y % p.Hk;
-
-  const int ks = (int)blockIdx.x / p.n_ktiles, kj0 = ((int)blockIdx.x % p.n_ktiles) * kTileN;
+  const Start start = start_of<VL, false, kTileN>(p, p.n_ktiles, -1);
+  const int b = start.head / p.Hk, hk = start.head % p.Hk, ks = start.r, kj0 = start.i0;
   const uint32_t bar0 = sb + LY::kBar;
   auto BAR = [bar0](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 4);
@@ -417,20 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sp = smem_raw + (sb - raw);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
+  const Start start = start_of<VL, true, kTileM>(p, p.n_qtiles, p.r_only);
+  const int b = start.head / p.H, h = start.head % p.H, r = start.r, i0 = start.i0;
   const int hk = h / p.G;  // the key / value head of query head h (grouped-query attention)
-  // causal: the later query tiles carry more work, start them first (the
-  // batched zigzag split by chunk, so that every head's heaviest tiles lead)
-  int r, i0;
-  if (!VL && p.causal && p.layout == LAYOUT_ZIGZAG && p.r_only < 0 && p.L % (2 * kTileM) == 0) {
-    int qt;
-    zigzag_heavy_first((int)blockIdx.x, p.N, p.n_qtiles / 2, r, qt);
-    i0 = qt * kTileM;
-  } else {
-    const int x = p.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    r = p.r_only >= 0 ? p.r_only : x / p.n_qtiles;
-    i0 = (x % p.n_qtiles) * kTileM;
-  }
   const uint32_t bar0 = sb + LY::kBar;
   auto BAR = [bar0](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 4);

@@ -54,21 +54,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  const int b = blockIdx.y / p.H;
-  const int h = blockIdx.y % p.H;
-  // causal: the later query rows carry more work, start them first (the
-  // batched zigzag split by chunk, so that every head's heaviest tiles lead)
   const int n_pairs = (p.L + kRowsPerCta - 1) / kRowsPerCta;
-  int r, i0;
-  if (!VL && p.causal && p.layout == LAYOUT_ZIGZAG && p.r_only < 0 && p.L % (2 * kRowsPerCta) == 0) {
-    int pr;
-    zigzag_heavy_first((int)blockIdx.x, p.N, n_pairs / 2, r, pr);
-    i0 = pr * kRowsPerCta;
-  } else {
-    const int x = p.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    r = p.r_only >= 0 ? p.r_only : x / n_pairs;
-    i0 = (x % n_pairs) * kRowsPerCta;
-  }
+  const Start start = start_of<VL, true, kRowsPerCta>(p, n_pairs, p.r_only);
+  const int b = start.head / p.H, h = start.head % p.H, r = start.r, i0 = start.i0;
   const uint32_t bar0 = sb + LY::kBar;
   auto BAR = [bar0](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 4);
@@ -148,7 +136,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         if (j >= kVStages &&
             !wait_one<kWaitHint>(BAR(B_V_FULL + sv), (j / kVStages - 1) & 1, abort_flag, p.ctl, 6))
           return false;
-        const int hk = (int)(blockIdx.y % p.H) / p.G;
+        const int hk = h / p.G;
         const int krow = s * p.L + kt * kTileN;
         const bool rows_ok = in_bounds(tma_coords_ok(TmaExtent{D, p.S, p.Hk, p.B}, 0, krow, hk, b), p.ctl, 2);
         mbar_add_tx(BAR(B_V_FULL + sv), LY::kTile);
