@@ -676,14 +676,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr ((SC & SC_CAP) != 0) g[c] = ((mw >> c) & 1ull) ? g[c] : 0u;
         }
       }
+      uint32_t pp[32];  // P', packed while dP is on its way
+#pragma unroll
+      for (int m = 0; m < 32; ++m) {
+        if constexpr ((SC & SC_CAP) != 0)
+          pp[m] = pack_bf16x2(__uint_as_float(g[2 * m]), __uint_as_float(g[2 * m + 1]));
+        else
+          pp[m] = pack_bf16x2(__uint_as_float(v[2 * m]), __uint_as_float(v[2 * m + 1]));
+      }
       if (!wait_warp(BAR(F_DP_FULL), j & 1, abort_flag, p.ctl, 62)) {
         ok = false;
         return false;
       }
       tc_fence_after();
-      // dS = P' * (dP - D) and P', packed (column m: keys 2m, 2m + 1) over this thread's 64 dP columns once they are read
+      // dS = P' * (dP - D), packed too (column m: keys 2m, 2m + 1): both over this thread's 64 dP columns once these
+      // are read
       const uint32_t tdp = tl + LY::kTmemDP + 64 * half;
-      uint32_t ds[32], pp[32];
+      uint32_t ds[32];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         uint32_t d[32];
@@ -697,11 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           miss[u & 1] = fma_f32x2(pair, diff, miss[u & 1]);
           uint64_t grad = pair;
           if constexpr ((SC & SC_CAP) != 0) grad = f32x2(__uint_as_float(g[c]), __uint_as_float(g[c + 1]));
-          float s0, s1, p0, p1;
+          float s0, s1;
           f32x2_split(mul_f32x2(grad, diff), s0, s1);
-          f32x2_split(grad, p0, p1);
           ds[c / 2] = pack_bf16x2(s0, s1);
-          pp[c / 2] = pack_bf16x2(p0, p1);
         }
       }
       tmem_st32(tdp, ds);
