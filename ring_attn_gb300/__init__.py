@@ -48,7 +48,8 @@ EXPORTED_SYMBOLS = (
 )
 RA_STATIC_SCRATCH_BYTES = 16 << 20
 KERNELS = {"fwd": 0, "bwd_dkdv": 1, "bwd_pre": 2, "bwd_dq": 3, "permute": 4, "lse_merge": 5, "cache_append": 6,
-           "cache_read": 7, "cache_fwd": 8, "cache_join": 9, "rope": 10}
+           "cache_read": 7, "cache_fwd": 8, "cache_join": 9}
+_KINDS = {**KERNELS, "rope": 10}
 
 
 class RingAttnError(RuntimeError):
@@ -925,8 +926,8 @@ def ring_attn_timing_enable(on: bool = True):
 
 
 def ring_attn_timing_read(kernel) -> tuple:
-    """(total device ms, launches) of one kernel kind since the last read; resets it."""
-    k = KERNELS[kernel] if isinstance(kernel, str) else int(kernel)
+    """(total device ms, launches) of one kernel kind (of KERNELS, or "rope") since the last read; resets it."""
+    k = _KINDS[kernel] if isinstance(kernel, str) else int(kernel)
     ms = ctypes.c_double(0.0)
     n = ctypes.c_int64(0)
     _check(load().ring_attn_timing_read(k, ctypes.byref(ms), ctypes.byref(n)), "ring_attn_timing_read")

@@ -163,3 +163,16 @@ def test_rotated_attention_is_its_own_gradient_chain():
     for name, got, t in (("dq", dq, dqr), ("dk", dk, dkr)):
         assert_within(name, t, want[name])
         check(name, got[0].transpose(0, 1), t[0].transpose(0, 1), cos, sin, pos, [0] * 32, False, True)
+
+
+def test_launches_are_recorded():
+    q = torch.randn(1, 2, 40, 64, device="cuda").bfloat16()
+    table = torch.rand(40, 32, device="cuda")
+    ra.ring_attn_timing_enable(True)
+    try:
+        ra.ring_attn_rope(q, None, (table, table))
+        ra.ring_attn_rope_bwd(q, None, (table, table))
+        ms, n = ra.ring_attn_timing_read("rope")
+    finally:
+        ra.ring_attn_timing_enable(False)
+    assert n == 2 and ms > 0
