@@ -230,19 +230,32 @@ ScoreParams score_params(float softcap, const float* slopes, const int32_t* pref
   p.c0 = (float)unit;
   if (softcap > 0.f) {
     const double cap2 = softcap * 1.4426950408889634, k = unit / cap2;  // u = k s
-    auto scaled = [k](const double* from, int n, double first, float* to) {  // first, then first k^2 from[0], ...
+    // coefficients of s, s^3 .. (odd: unit is the first) or s^2, s^4 ..; and up to which u, `at` at most, they will do:
+    // those that leave fp32's range may lose `loss` of the result
+    auto scaled = [k](const double* from, int n, double first, double at, double loss, float* to) {
       double c = first;
-      for (int i = 0; i < n; ++i) to[i] = (float)((c *= k * k) * from[i]);
+      bool all = true, finite = true;
+      for (int i = 0; i < n; ++i) {
+        to[i] = (float)((c *= k * k) * from[i]);
+        all = all && fabs(to[i]) >= 0x1p-126f;
+        finite = finite && isfinite(to[i]);
+      }
+      if (!finite) return -1.0;
+      for (; !all && at > 1e-6; at *= 0.9) {
+        double lost = 0.0, s2 = at / k * (at / k), s = 1.0, t = first;
+        for (int i = 0; i < n; ++i) lost += fabs((t *= k * k) * from[i] - to[i]) * (s *= s2);
+        if (lost / first <= loss) break;
+      }
+      return at;
     };
     p.t0[0] = p.t1[0] = p.t2[0] = (float)unit;
-    scaled(p0, 3, unit, p.t0 + 1);
-    scaled(p1, 4, unit, p.t1 + 1);
-    scaled(p2, 6, unit, p.t2 + 1);
-    scaled(d0, 2, 1.0, p.g0);
-    scaled(d1, 3, 1.0, p.g1);
-    scaled(d2, 5, 1.0, p.g2);
-    const double at[kTiers] = {0.4, 0.6, 1.0};
-    for (int i = 0; i < kTiers; ++i) p.lim[i] = (float)(at[i] / k);
+    constexpr double kLoss = 0x1p-24, kGradLoss = 0x1p-16;
+    double at[kTiers] = {
+        std::min(scaled(p0, 3, unit, 0.4, kLoss, p.t0 + 1), scaled(d0, 2, 1.0, 0.4, kGradLoss, p.g0)),
+        std::min(scaled(p1, 4, unit, 0.6, kLoss, p.t1 + 1), scaled(d1, 3, 1.0, 0.6, kGradLoss, p.g1)),
+        std::min(scaled(p2, 6, unit, 1.0, kLoss, p.t2 + 1), scaled(d2, 5, 1.0, 1.0, kGradLoss, p.g2))};
+    at[0] = std::min(at[0], at[1]);  // (where polynomial 0 holds, 1 does)
+    for (int i = 0; i < kTiers; ++i) p.lim[i] = (float)std::min(at[i] / k, 0x1p62);  // (its square is in fp32's range)
     p.cap2 = (float)cap2;
     p.inv_cap2 = (float)(1.0 / cap2);
     p.e2 = (float)(2.0 * k * 1.4426950408889634);

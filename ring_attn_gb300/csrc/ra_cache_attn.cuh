@@ -580,13 +580,24 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? small_blocks(D, NT) : 1) cach
       }
       if constexpr (kScored) {
         if (a.mode & SC_CAP) {
+          // 1 - 2 / (1 + e^(2u)), off by cap2 2^-22; above a cap of 128 that shows, and small scores take the polynomial
+          auto change = [&](auto high) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+              for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                s[mt][n][x] = fmaf(fast_rcp(fast_exp2(s[mt][n][x] * a.sc.e2) + 1.f), -2.f * a.sc.cap2, a.sc.cap2);
+                for (int x = 0; x < 4; ++x) {
+                  const float u = s[mt][n][x], w = u * u;
+                  s[mt][n][x] = fmaf(fast_rcp(fast_exp2(u * a.sc.e2) + 1.f), -2.f * a.sc.cap2, a.sc.cap2);
+                  if (decltype(high)::value && fabsf(u) <= a.sc.lim[0])
+                    s[mt][n][x] = u * fmaf(w, fmaf(w, fmaf(w, a.sc.t0[3], a.sc.t0[2]), a.sc.t0[1]), a.sc.t0[0]);
+                }
+          };
+          if (a.sc.cap2 <= 185.f)
+            change(Const<0>{});
+          else
+            change(Const<1>{});
         }
         if (a.mode & SC_BIAS) {
 #pragma unroll

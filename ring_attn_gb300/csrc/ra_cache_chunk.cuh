@@ -538,8 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             }
           }
           raise(most<SC>(a.sc, BiasLine{}, fmaxf(hi[0], hi[1]) * sc, kUnit));
-          const int tier = max(tier_of(fmaxf(size[0], size[1]) * sc, a.sc), at_least);
-          at_least = min(tier, 1);  // (nor do warps go back and forth between the least two: 0.33 ms with it)
+          // (warps do not go back and forth between the least two polynomials: 0.33 ms with that)
+          const int tier = max(tier_of(fmaxf(size[0], size[1]) * sc, a.sc, !cut), at_least);
+          if (!cut) at_least = min(tier, 1);
           const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(-M, -M);
           uint64_t acc[2] = {0, 0};
           auto weights = [&](auto ti, auto mask) {
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
               bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
               line = __all_sync(0xffffffffu, bias.line);
             }
-            if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, sc);
+            if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, line, sc);
             with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
               const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
 #pragma unroll

@@ -221,7 +221,7 @@ struct Const {
   static constexpr int value = N;
 };
 // f(tier, line) with both, which are the same in the whole warp, as compile-time constants.  Tiles without a line
-// are few: one polynomial serves them.
+// are few: one polynomial serves them (tier: not the least).
 template <int SC, class F>
 __device__ __forceinline__ void with_score_flags(int tier, bool line, F&& f) {
   if constexpr ((SC & SC_BIAS) != 0)
@@ -279,15 +279,17 @@ __device__ __forceinline__ float largest(const uint32_t (&v)[N]) {
   }
   return fmaxf(m[0], m[1]);
 }
-// The polynomial that holds for products of up to `size` in every lane.
-__device__ __forceinline__ int tier_of(float size, const ScoreParams& sc) {
+// The polynomial that holds for products of up to `size` in every lane: the least one, or (not `least`: code that has
+// one polynomial for all) 2 or none.
+__device__ __forceinline__ int tier_of(float size, const ScoreParams& sc, bool least = true) {
   // (not negative and no NaN: the bits are in the numbers' order)
   const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(size)));
+  if (!least) return all <= sc.lim[2] ? 2 : kTiers;
   return all <= sc.lim[0] ? 0 : all <= sc.lim[1] ? 1 : all <= sc.lim[2] ? 2 : kTiers;
 }
 template <int N>
-__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, float factor = 1.f) {
-  return tier_of(largest(v) * factor, sc);
+__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, bool least, float factor = 1.f) {
+  return tier_of(largest(v) * factor, sc, least);
 }
 
 }  // namespace ra

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bias_line(tile_tokens(p, win, r, qt * kTileM + 64 * half), gk, max(c_lo, 0), min(c_hi, 64), slope2);
         line = __all_sync(0xffffffffu, bias.line);
       }
-      if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
+      if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc, line);
       // v becomes P^T times the cap's derivative
       with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
         const Cap<SC, decltype(ti)::value, true> cap(p.sc);
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         line = __all_sync(0xffffffffu, bias.line);
         bias.off += nl;
       }
-      if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc);
+      if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, p.sc, line);
       uint32_t g[(SC & SC_CAP) != 0 ? 64 : 1];  // P times the cap's derivative
       with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
         const Cap<SC, decltype(ti)::value, true> cap(p.sc);

@@ -251,11 +251,14 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     }
     float slope2 = 0.f;
     if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
-    // Capped scores lie within +-cap2, so where that is small enough one offset serves all rows: weights up to 2^60
-    // and, for the rows whose scores are the least, down to 2^-102.  A bias only takes off, and nothing from the row's
-    // own token, which every row of a whole call sees.
-    const bool fixed = (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
-    float m_run = fixed ? fmaxf(p.sc.cap2 - 60.f, 0.f) : -INFINITY;  // offset of the weights, in log2 units
+    // Capped scores lie within +-cap2, so where that is small enough one offset serves all rows: weights are at most
+    // 1, or 2^60 for the largest of these caps, and the largest one of a row whose scores are the least is 2^-102 or
+    // more, 2^24 above what fp32 and bf16 still have.  A bias only takes off, and nothing from the row's own token, which
+    // every row of a whole call sees.
+    const bool fixed =
+        (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
+    // offset of the weights, in log2 units
+    float m_run = fixed ? fminf(p.sc.cap2, 102.f - p.sc.cap2) : -INFINITY;
     float l_run = 0.f;        // running sum of this half's weights
     bool ok = true;
     int j = 0;
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
             tmem_ld32(tS + 32 * ch, v);
             const BiasLine part = bias.from(32 * ch);
             tmem_ld_wait(v);
-            const int tier = tier_of(largest(v), p.sc);
+            const int tier = tier_of(largest(v), p.sc, line && !any_masked);
             auto weights = [&](const auto& cap, auto li, auto mask) {
               const uint32_t m32 = (uint32_t)(mw >> (32 * ch));
 #pragma unroll
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
       float size = 0.f, alpha = 1.f;
       if constexpr ((SC & SC_CAP) != 0) size = largest(v);
-      const int tier = (SC & SC_CAP) ? tier_of(size, p.sc) : 0;
+      const int tier = (SC & SC_CAP) ? tier_of(size, p.sc, line && !any_masked) : 0;
       {
         // the largest score, or a bound of it
         float mx = -INFINITY;

@@ -179,3 +179,20 @@ def test_a_prompt_and_its_next_token():
     vmax = float(vc.float().abs().max())
     assert float((got - ref.float()).abs().max()) <= (3 * 2.0 ** -8 + 2.0 ** -11 + 1e-4) * vmax
     assert float((got_lse - ref_lse).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("n_new", [1, 5, 200])  # few rows, and the tensor cores' kernel
+@pytest.mark.parametrize("cap", [200.0, 1000.0, 2.0 ** 20])
+def test_a_cap_far_above_the_scores_leaves_them(n_new, cap):
+    """x - softcap tanh(x / softcap) <= |x|^3 / (3 softcap^2): with scores below 40, 0.54, 0.022 and nothing; lse sums fp32
+    numbers, so it shows what the cap's evaluation adds: |x| 2^-20 for the scores, 2^-21 |lse| for lse."""
+    c = Case((n_new, n_new), (900, 333), 4, 2, 64, 32, seed=77)
+    cache, q, cu = c.fill(ra), c.queries(2.0), ra.CuSeqlens(c.cu, "cuda")
+    total = int(c.cu[-1])
+    plain, capped = (ra.ring_attn_cache_fwd(q, cache, c.page_table, c.kv_lens, cu, scores=z)[1][:, :total].double().cpu()
+                     for z in (None, ra.Scores(cap)))
+    check_no_device_error(ra)
+    assert float(plain.abs().max()) < 40.0
+    change = (40.0 ** 3 / (3 * cap ** 2)) if cap < 2.0 ** 20 else 0.0
+    over = (capped - plain).abs() - (change + 40.0 * 2.0 ** -20 + 2.0 ** -21 * plain.abs())
+    assert float(over.max()) <= 0

@@ -80,6 +80,61 @@ def test_batched(b, h, hk, s, d, layout, n, causal, cap, slopes, prefix, gain):
         assert_within(name, to_original(ra, t, layout, n), want[name])
 
 
+@pytest.mark.parametrize("scale,cap,gain", [
+    (1e-3, 50.0, 45.0),      # scores up to the cap, of products whose sixth powers times the coefficients leave fp32
+    (1e-3, 50.0, 30.0),
+    (128 ** -0.5, 1000.0, 17.0),
+    (2.0 ** 8, 1.0, 0.25),
+    (2.0 ** 20, 2.0 ** 10, 0.008),  # and that leave it upwards
+    (1e-30, 50.0, 2.0),      # nothing is left of the scores
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_scale_far_from_the_cap(scale, cap, gain, causal):
+    b, h, hk, s, d = 1, 2, 1, 328, 128
+    x = inputs(b, h, hk, s, d, 9050, gain)
+    x["k"] = (x["k"].float() * gain).bfloat16()
+    g = {k: v.cuda() for k, v in x.items()}
+    z = scores_of(cap, None, None)
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], "contiguous", 1, causal, scale, scores=z)
+    grads = ra.ring_attn_bwd(g["do"], g["q"], g["k"], g["v"], out, lse, "contiguous", 1, causal, scale, scores=z)
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], x["do"], scale, cap, None, causal, None)
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        assert_within(name, t, want[name])
+
+
+@pytest.mark.parametrize("d,causal", [(64, True), (128, False)])
+def test_a_cap_far_above_the_scores_leaves_them(d, causal):
+    """With softcap 2^20 a score of up to 40 changes by less than 2^-24: lse, which sums fp32 numbers, is the plain call's
+    but for the roundings of scores (2^-20 of 40) and of lse itself."""
+    x = inputs(1, 2, 2, 520, d, 9070, 2.0)
+    q, k, v = (x[n].cuda() for n in "qkv")
+    plain, capped = (ra.ring_attn_fwd(q, k, v, "contiguous", 1, causal, scores=z)[1].double().cpu()
+                     for z in (None, ra.Scores(2.0 ** 20)))
+    check_no_device_error(ra)
+    assert float(plain.abs().max()) < 40.0
+    assert float(((capped - plain).abs() - 40.0 * 2.0 ** -20 - 2.0 ** -21 * plain.abs()).max()) <= 0
+
+
+@pytest.mark.parametrize("cap", [25.0, 56.0, 57.0])  # one offset for all rows, up to which cap, and above
+@pytest.mark.parametrize("slopes", [None, "alibi"])
+def test_rows_at_both_ends_of_the_cap(cap, slopes):
+    """Rows whose scores are all at the cap, or all at its negative; with a bias, up to 32 below that."""
+    b, h, hk, s, d = 1, 2, 1, 512, 64
+    x = inputs(b, h, hk, s, d, 9060)
+    sign = torch.where(torch.arange(s) % 3 == 0, -1.0, 1.0)[None, None, :, None]
+    x["q"] = (x["q"].float() + 60.0 * sign).bfloat16()
+    x["k"] = (x["k"].float() + 20.0).bfloat16()
+    sl = slopes_of(h, slopes)
+    g = {k: v.cuda() for k, v in x.items()}
+    z = scores_of(cap, sl, None)
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], "contiguous", 1, True, scores=z)
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], None, d ** -0.5, cap, sl, True, None)
+    assert_within("out", out, want["out"])
+    assert_within("lse", lse, want["lse"])
+
+
 @pytest.mark.parametrize("layout,causal,cap,slopes,prefix", [
     ("contiguous", True, 8.0, "alibi", (150,)), ("zigzag", True, 0.0, "alibi", None), ("stripe", False, 8.0, "mixed", None),
     ("zigzag", True, 0.0, None, (300,)),
