@@ -448,7 +448,7 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  * of q, k and v; the slopes and softcap are constants).  i, j: the query's and the key's original
  * tokens, whatever the layout (varlen: in their sequence; the cache: cache indices).
  *   softcap: 0 (none), or 2^-10 to 2^20 with softmax_scale / softcap at most 2^10 (else
- *     RA_ERR_UNSUPPORTED).
+ *     RA_ERR_UNSUPPORTED).  y is off by at most softcap 2^-21, next to what x is.
  *   slopes: (h) fp32 device array, one per query head, finite, of any sign; or NULL.
  *   prefix: int32 device array, or NULL: with causal, tokens that every query sees, the first
  *     prefix[n] of batch n, or of sequence n (varlen, cache: entry of every sequence), so those see
@@ -458,8 +458,9 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  * kernels, so a captured call follows them as they are when it is replayed.  A ra_scores
  * without any of the three makes a call the plain one; NULL is refused.
  *
- * ring_attn_scored_X is ring_attn_X with scores; everything else is as there.  (The CTA-pair knob
- * does not concern these calls.) */
+ * ring_attn_scored_X is ring_attn_X with scores; everything else is as there, but that dq, dk and dv
+ * may share no element with dout, q, k, v or each other (RA_ERR_INVALID_ARG; slices of one packed tensor
+ * share none).  The CTA-pair knob does not concern these calls. */
 typedef struct {
   float softcap;
   const float* slopes;

@@ -628,6 +628,21 @@ static ra_status take_scores(const ScoreArg& a, float softmax_scale, int32_t cau
   if (causal != 0 && causal != 1) return RA_ERR_INVALID_ARG;
   return check_scores(a.x, softmax_scale, causal, softmax_scale * 1.4426950408889634, sc);
 }
+static bool may_share(const ra_tensor* a, int es_a, const ra_tensor* b, int es_b);
+// The gradients of a call with changed scores come in another order than the plain ones (dq first), so that none may
+// lie on what the others are made from; slices of one packed tensor may.
+static ra_status check_grads(const Scored& sc, const ra_tensor* dout, const ra_tensor* q, const ra_tensor* k,
+                             const ra_tensor* v, const ra_tensor* dq, const ra_tensor* dk, const ra_tensor* dv) {
+  if (!sc.mode) return RA_OK;
+  const ra_tensor* grads[3] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    for (const ra_tensor* t : {dout, q, k, v})
+      if (may_share(grads[i], 2, t, 2)) return RA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (may_share(grads[i], 2, grads[j], 2)) return RA_ERR_INVALID_ARG;
+  }
+  return RA_OK;
+}
 static const ScoreArg kPlain = {false, nullptr};
 static ScoreArg scored(const ra_scores* x) { return ScoreArg{true, x}; }
 
@@ -802,6 +817,7 @@ static ra_status any_bwd(const ra_tensor* dout, const ra_tensor* q, const ra_ten
   RA_TRY(check_lse(lse, vq.b, vq.h, vq.s, &lsb, &lsh, &lss));
   Scored sc;
   RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
+  RA_TRY(check_grads(sc, dout, q, k, v, dq, dk, dv));
   return bwd_common(vdo, vq, vk, vv, vo, static_cast<const float*>(lse->data), lsb, lsh, lss, layout, n_shards,
                     causal, softmax_scale, vdq, vdk, vdv, workspace, workspace_bytes, nullptr, 0, stream, -1,
                     nullptr, &sc);
@@ -926,6 +942,7 @@ static ra_status any_varlen_bwd(const ra_tensor* dout, const ra_tensor* q, const
   RA_TRY(check_lse(lse, 1, vq.h, total, &lsb, &lsh, &lss));
   Scored sc;
   RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
+  RA_TRY(check_grads(sc, dout, q, k, v, dq, dk, dv));
   if (layout == RA_LAYOUT_ZIGZAG && workspace && workspace_bytes >= zz_bwd_bytes(total, vq.h, vq.d, n_shards)) {
     // original-order path: the same checks as the kernels' before any launch
     RA_TRY(bwd_check_args(vdo, vq, vk, vv, vo, layout, n_shards, causal, softmax_scale, vdq, vdk, vdv, -1));
@@ -1036,6 +1053,7 @@ static ra_status any_llama3_varlen_bwd(const ra_tensor* dout, const ra_tensor* q
   RA_TRY(check_lse(lse, 1, vq.h, L, &lsb, &lsh, &lss));
   Scored sc;
   RA_TRY(take_scores(scores, softmax_scale, causal, &sc));
+  RA_TRY(check_grads(sc, dout, q, k, v, dq, dk, dv));
   return bwd_common(vdo, vq, vk, vv, vo, static_cast<const float*>(lse->data), lsb, lsh, lss, RA_LAYOUT_CONTIGUOUS,
                     n_shards, causal, softmax_scale, vdq, vdk, vdv, workspace, workspace_bytes, cu_seqlens_dev, n_seqs,
                     stream, rank, nullptr, &sc);

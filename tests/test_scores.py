@@ -62,6 +62,34 @@ def _ok(shape=(1, 2, 256, 64)):
     return [ctypes.byref(_fake(shape)) for _ in range(4)], ctypes.byref(_fake(shape[:3], ra.RA_FP32))
 
 
+@pytest.mark.parametrize("grad,other", [(g, o) for g in ("dq", "dk", "dv") for o in ("do", "q", "k", "v", "dq", "dk", "dv")
+                                        if g != o])
+def test_gradients_on_one_another_or_on_inputs_are_refused(lib, grad, other):
+    names = ("do", "q", "k", "v", "out", "dq", "dk", "dv")
+    at = {n: 0x1000000 * (i + 1) for i, n in enumerate(names)}
+    odd = ctypes.c_void_p(0x20000008)  # a workspace that is refused last: nothing is launched
+
+    def status(at, shape, call):
+        t = {n: ctypes.byref(_fake(shape, data=a)) for n, a in at.items()}
+        return call(*(t[n] for n in ("do", "q", "k", "v", "out")), *(t[n] for n in ("dq", "dk", "dv")))
+
+    cu = (ctypes.c_int32 * 2)(0, 256)
+    host, dev, lse = ctypes.cast(cu, ctypes.c_void_p), ctypes.c_void_p(0x2000), ctypes.byref(_fake((1, 2, 256), ra.RA_FP32))
+    l2, z = ctypes.byref(_fake((2, 256), ra.RA_FP32)), _scores(5.0)
+    calls = [
+        ((1, 2, 256, 64), lambda do, q, k, v, out, dq, dk, dv: lib.ring_attn_scored_bwd(
+            do, q, k, v, out, lse, 0, 2, 1, 0.125, z, dq, dk, dv, odd, 1 << 24, None)),
+        ((256, 2, 64), lambda do, q, k, v, out, dq, dk, dv: lib.ring_attn_scored_varlen_bwd(
+            do, q, k, v, out, l2, dev, host, 1, 256, 0, 1, 1, 0.125, z, dq, dk, dv, odd, 1 << 24, None)),
+        ((256, 2, 64), lambda do, q, k, v, out, dq, dk, dv: lib.ring_attn_scored_llama3_varlen_bwd(
+            do, q, k, v, out, l2, dev, host, 1, 256, 0, 1, 1, 0.125, z, dq, dk, dv, odd, 1 << 24, None)),
+    ]
+    for shape, call in calls:
+        assert status(at, shape, call) == 4  # the workspace
+        assert status(dict(at, **{grad: at[other] + 128}), shape, call) == 1
+        assert status(dict(at, **{grad: at[other] + 2 * 256 * 64 * 2}), shape, call) == 4  # right behind it
+
+
 @pytest.mark.parametrize("z,causal,scale,status", [
     (None, 1, 0.125, 1), (_scores(-1.0), 1, 0.125, 1), (_scores(float("nan")), 1, 0.125, 1), (_scores(float("inf")), 1, 0.125, 1),
     (_scores(1e-4), 1, 0.125, 2), (_scores(1e7), 1, 0.125, 2), (_scores(0.001), 1, 2.0, 2),
