@@ -1,4 +1,4 @@
-// Pieces shared by the backward kernels (ra_bwd.cu: the one-CTA dK / dV and
+// Pieces shared by the backward kernels (ra_bwd.cuh: the one-CTA dK / dV and
 // dQ kernels; ra_dkdv_pair.cu: the CTA-pair dK / dV kernel).
 //
 // In the backward the per-element work needs no row reduction (lse and D are

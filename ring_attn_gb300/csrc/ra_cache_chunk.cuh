@@ -29,7 +29,7 @@
 // SC (ra_score.cuh): 0 for plain scores, else a call's cap, bias by distance or prefix
 // (ra_cache_chunk_*.cu), which the softmax warps apply.
 // fp16 operands hold number * scale exactly; queries and p are rounded to fp16 and the rest is
-// fp32, as in ra_cache_attn.cu, whose comment says what that costs.
+// fp32, as in ra_cache_attn.cuh, whose comment says what that costs.
 #pragma once
 
 #include <algorithm>

@@ -1,7 +1,7 @@
 // dK / dV of the ring-attention backward with CTA pairs (tcgen05 cta_group::2),
 // head_dim 128.
 //
-// The work is that of the one-CTA dK / dV kernel in ra_bwd.cu: per 128-row key
+// The work is that of the one-CTA dK / dV kernel in ra_bwd.cuh: per 128-row key
 // tile of KV shard s, walk the query tiles of the shards (s + t) mod N in ring
 // order (guijiagi.com "Ring Attention：突破百万 Token 上下文的分布式注意力",
 // "详细流程"), and with P recomputed from the saved log-sum-exp ("Ring Flash

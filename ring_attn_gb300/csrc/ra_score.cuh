@@ -15,6 +15,8 @@
 // Beyond 1, tanh(u) = 1 - 2 / (1 + e^(2u)) with the hardware's exponential and reciprocal (4 and 8 cycles on top
 // of the softmax's 4): right for every u, infinite ones too, off by about 2^-22 absolutely.
 // A warp goes by the largest score that it has in registers: caps are meant to be far above most scores.
+// (Coefficients have powers of scale / softcap up to the twelfth.  Where those leave fp32's range a polynomial holds
+// up to a smaller u, or not at all: ScoreParams::lim.)
 //
 // The bias.  In a tile the distance is a - st c for column c, or its negative, or (a tile
 // that the row's own token, or the seam of a zigzag shard's two chunks, lies in) one line left

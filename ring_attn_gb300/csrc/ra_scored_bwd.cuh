@@ -6,6 +6,13 @@
 // takes the plain dK / dV kernel behind the dQ kernel here).  Two threads a row, as there: four, as in the
 // forward with changed scores, measured 2 % to 20 % slower, since each waits for two products a tile, not for its
 // own instructions.
+//
+// Bound, d = 128: a tile of 128 x 128 needs 2048 cycles of the tensor cores in either kernel (four products), its
+// scores about 1300 of a scheduler's multiply-add pipe; what is above that are the waits of a tile's chain (product,
+// weights, product) that two buffers do not hide, tensor memory being full.  8192 tokens of 32 + 8 heads of 128,
+// softcap 30 and a prefix: dK and dV 0.88 ms (plain scores 0.79), dQ 1.00 (0.57, with three products); 12 documents of 200
+// to 4000 tokens, 16 + 4 heads, a bias: 254 and 238 us (251, 185); 2 x 4096 tokens of 16 heads of 64, 4 striped shards,
+// a bias: 219 and 222 us (222, 170).
 #pragma once
 
 #include "ra_bwd.cuh"
@@ -387,9 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // missing part for a multiply-add a score:
 //   e = sum_j P_ij (dP_ij - D_i),  D_i + e is exact,  dQ_i = scale (sum_j dS_ij k_j - e sum_j P'_ij k_j)
 // (P': P times the cap's derivative), for which it keeps a second product's sum.  It runs first and corrects the
-// statistics for the dK / dV pass.  dQ and dK are then off by 0.24 %, which is what the rounding of dS and of the
-// results leaves.  (A pass of its own for sum P dP, two products more, took 0.52 ms at 8192 tokens of 32 + 8 heads
-// of 128, where this takes 0.31 ms.)
+// statistics for the dK / dV pass.  (A pass of its own for sum P dP, two products more, took 0.52 ms at 8192 tokens of
+// 32 + 8 heads of 128, where this takes 0.31 ms.)
+//
+// dS is rounded to bf16 as an operand, and since a row's dS nearly cancel in its sum, the rounding errors weigh more
+// than they do in each: 0.182 % of dQ at softcap 30, 0.199 % at 15, where one rounding is 0.166 %.  Most of that is the sum
+// of a row's errors times what its keys have in common, so that is taken off by P' K too: the sum of the rounded dS less
+// the sum of dS joins e (as if P' summed to 1, which caps nearly leave).  With the rounding of dQ itself it is off by
+// 0.22 and 0.23 %, 0.25 and 0.26 without.  It costs dQ 3 to 5 % (short rows of 64: 11 %).
 //
 // TMEM: S [0, 128), dP [128, 256).  d = 128: the sums of dS K and of P' K take the rest, so that Q and dO stay in shared
 // memory; d = 64: as in the plain kernel, with the second sum behind the first.  P' is packed beside dS, over the
@@ -619,7 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(F_QDO_TMEM));
     }
-    uint64_t miss[2] = {0, 0};  // sums of P (dP - D)
+    // sums of P (dP - D), of dS as rounded, and (cap; else the first) of dS
+    uint64_t miss[2] = {0, 0}, rounded = 0, exact = 0;
     int j = 0;
     if (ok) walk_kv_tiles(p, qr, nkt, 0, p.N, [&](int s, int kt) {
       int c_lo = 0, c_hi = kTileN;
@@ -706,8 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           miss[u & 1] = fma_f32x2(pair, diff, miss[u & 1]);
           uint64_t grad = pair;
           if constexpr ((SC & SC_CAP) != 0) grad = f32x2(__uint_as_float(g[c]), __uint_as_float(g[c + 1]));
+          grad = mul_f32x2(grad, diff);
+          if constexpr ((SC & SC_CAP) != 0) exact = add_f32x2(exact, grad);
           float s0, s1;
-          f32x2_split(mul_f32x2(grad, diff), s0, s1);
+          f32x2_split(grad, s0, s1);
           ds[c / 2] = pack_bf16x2(s0, s1);
         }
       }
@@ -717,18 +732,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(F_DS_FULL));
+#pragma unroll
+      for (int m = 0; m < 32; ++m)
+        rounded = add_f32x2(rounded, f32x2(__uint_as_float(ds[m] << 16), __uint_as_float(ds[m] & 0xffff0000u)));
       ++j;
       return true;
     });
-    // the row's missing part of D, of both halves (every warp of a pair comes here, whatever happened before)
-    float e0, e1;
-    f32x2_split(add_f32x2(miss[0], miss[1]), e0, e1);
+    // a row's sums over both halves (every warp of a pair comes here, whatever happened before)
     float* sums = reinterpret_cast<float*>(sp + LY::kSums) + row;
-    sums[half * 128] = e0 + e1;
-    named_bar_sync(1 + (warp & 3), 64);
-    const float missing = sums[0] + sums[128];
+    auto of_row = [&](uint64_t x) -> float {
+      float x0, x1;
+      f32x2_split(x, x0, x1);
+      sums[half * 128] = x0 + x1;
+      named_bar_sync(1 + (warp & 3), 64);
+      const float all = sums[0] + sums[128];
+      named_bar_sync(1 + (warp & 3), 64);
+      return all;
+    };
+    const float missing = of_row(add_f32x2(miss[0], miss[1]));
+    const float too_much = of_row(rounded) - ((SC & SC_CAP) != 0 ? of_row(exact) : missing);
     if (half == 0 && valid && ok) const_cast<float*>(p.nD)[srow] = nD - missing;
-    // ---------------- epilogue: dQ = scale * (dS K - missing P' K), half the head dim per thread
+    // ---------------- epilogue: dQ = scale * (dS K - (missing + too_much) P' K), half the head dim per thread
     const int* rmap = VL ? p.row_map : nullptr;  // varlen in original order: rows of the caller's layout
     __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(p.dq) + (long long)b * p.q_sb + (long long)h * p.q_sh +
                           half * (D / 2);
@@ -743,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long row_w = (long long)r * p.L + i_w - p.q_base;  // the warp's first row of dq
         if (in_bounds(nvalid == 0 || (row_w >= 0 && row_w + nvalid <= p.q_rows), p.ctl, 18))
           store_rows_bf16<D / 64, true>(tl + LY::kTmemDQ + half * (D / 2), p.scale, sp + (warp - 4) * (32 * D), base,
-                                        p.q_ss, row_w, nvalid, rmap, tl + LY::kTmemPK + half * (D / 2), missing);
+                                        p.q_ss, row_w, nvalid, rmap, tl + LY::kTmemPK + half * (D / 2), missing + too_much);
       }
     } else if (valid && in_bounds(qrow < p.q_rows, p.ctl, 19)) {
       __nv_bfloat16* dst = base + (rmap ? (long long)__ldg(rmap + qrow) : qrow) * p.q_ss;

@@ -7,17 +7,26 @@
 // instruction waits for the one before and their long straight code for its fetching.  So a row is two threads' here
 // (key columns [0, 64) and [64, 128) of a tile), four warps a scheduler, and the code of 32 columns is a loop's body.
 //
-//   1. largest product of the half row.  The cap is
-//      monotonic and the bias a line along a tile's columns, so that an upper bound of the largest score follows; the
-//      offset of a softmax may lie above it by kLoose.  Tiles in which the bias is no line (the row's own token or
-//      a zigzag seam inside), or too steep a one, go over their changed scores instead.
+// A call with a cap that is not too high has one offset for all rows (`fixed` below).  In a loop over 32 columns the
+// products come out of tensor memory, the polynomial for the largest of them is chosen, and they become weights,
+// packed as bf16 over the first 32 of the thread's own 64 columns; sums of weights stay with the thread until the end.
+// Else a tile takes two steps before that:
+//   1. largest product of the half row.  The cap is monotonic and the bias a line along a tile's columns, so an upper
+//      bound of the largest score follows; the offset of a softmax may lie above it by kLoose.  Tiles in which the
+//      bias is no line (the row's own token or a zigzag seam inside), or too steep a one, go over their changed
+//      scores instead.
 //   2. the two threads of a row exchange their bounds through shared memory (as bf16, rounded up) and take the
 //      larger as the offset, if it passes the running one by 2^8.
-//   With a cap that is not too high neither is needed: a fixed offset will do, and halves do not wait for one another.
-//   3. scores are changed and turned into weights in one go, packed as bf16 over the first 32 of the thread's own 64
-//      columns; sums of weights stay with the thread until the end.
 //
-// Measured: see the kernels' table; 16,384 tokens of 32 heads of 128, causal, softcap 50: @TIME@.
+// Bound, d = 128: a tile of 128 x 128 needs 1024 cycles of the tensor cores, and a scheduler's four warps 2 cycles
+// of the multiply-add pipe for 64 of its scores and each of (cap) 7 or (bias) 4 packed instructions, and 4 cycles of
+// the special function unit for 32 exponentials: the cap's 1150 cycles are just over, and waits for one another
+// (a product, its weights, the next product) come on top of both.  Causal, 16,384 tokens of 32 heads of 128, softcap 50:
+// 1.72 to 1.75 ms, 1276 TFLOP/s (66 % of the measured bf16 rate), without the cap 1.55; 8192 tokens of 32 + 8 heads,
+// softcap 30 and a prefix 0.50 ms (0.46); 2 x 4096 tokens of 16 heads of 64, a bias, 4 striped shards 178 us (157).
+// What led here, for the first: a row a thread 2.36 ms, half a row 2.14, one offset and 32 columns at a time 1.82 (1.88
+// with the polynomials' constants from the parameters), heavy tiles first 1.72.  Choosing the polynomial afterwards
+// and doing the few other tiles again took 1.79 for 1.82, but 0.59 for 0.56 where scores are larger next to their cap.
 #pragma once
 
 #include "ra_fwd.cuh"

@@ -1,5 +1,9 @@
 """Attention with capped scores, a bias by distance and prefixes: forward and backward of every form that takes
 `scores`, against the fp64 oracle with bounds from the kernels' roundings (tests/score_case.py)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -137,7 +141,7 @@ def test_rows_at_both_ends_of_the_cap(cap, slopes):
 
 @pytest.mark.parametrize("layout,causal,cap,slopes,prefix", [
     ("contiguous", True, 8.0, "alibi", (150,)), ("zigzag", True, 0.0, "alibi", None), ("stripe", False, 8.0, "mixed", None),
-    ("zigzag", True, 0.0, None, (300,)),
+    ("zigzag", True, 0.0, None, (300,)), ("contiguous", True, 8.0, None, None), ("zigzag", True, 80.0, None, (9,)),
 ])
 def test_ring_steps_and_merge(layout, causal, cap, slopes, prefix):
     """Every ring step on its own, merged; steps of a causal ring leave rows without keys."""
@@ -326,3 +330,53 @@ def test_captured_calls_follow_slopes_and_prefix_and_repeat_their_bits():
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, c) for a, c in zip(changed, bits()))
     check_no_device_error(ra)
+
+
+@pytest.mark.parametrize("flag", [1, 2, 4], ids=["fwd", "dkdv", "dq"])
+@pytest.mark.parametrize("cap,slopes,d", [(20.0, None, 64), (70.0, None, 128), (0.0, "alibi", 64), (20.0, "alibi", 128)])
+def test_a_wait_that_runs_out_is_reported_and_the_context_survives(flag, cap, slopes, d):
+    """A load that the others wait for is left out (of Q, of K and V, of Q and dO): their waits end after 2 ms, the halves
+    of a row let one another go, and the next call is right."""
+    h, s = 2, 512
+    x = inputs(1, h, h, s, d, 9800)
+    sl = slopes_of(h, slopes)
+    z = scores_of(cap, sl, None)
+    g = {k: v.cuda() for k, v in x.items()}
+    how = dict(layout="contiguous", n_shards=2, causal=True, scores=z)
+
+    def call(out, lse):
+        return ra.ring_attn_bwd(g["do"], g["q"], g["k"], g["v"], out, lse, **how)
+
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], **how)
+    check_no_device_error(ra)
+    try:
+        ra.ring_attn_set_knob(ra.RA_KNOB_WAIT_LIMIT_NS, 2_000_000)
+        ra.ring_attn_set_knob(ra.RA_KNOB_DEBUG_FLAGS, flag)
+        if flag == 1:
+            ra.ring_attn_fwd(g["q"], g["k"], g["v"], **how)
+        else:
+            call(out, lse)
+        st, info = ra.ring_attn_check_device_error()
+    finally:
+        ra.ring_attn_set_knob(ra.RA_KNOB_DEBUG_FLAGS, 0)
+        ra.ring_attn_set_knob(ra.RA_KNOB_WAIT_LIMIT_NS, int(os.environ.get("RA_TEST_WAIT_LIMIT_NS", 4_000_000_000)))
+    assert st == 6, (st, info)
+    assert ra.ring_attn_check_device_error() == (0, 0)
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], **how)
+    grads = call(out, lse)
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], x["do"], d ** -0.5, cap, sl, True, None)
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        assert_within(name, t, want[name])
+
+
+def test_the_sweep_passes_under_the_bounds_checks():
+    """The tests above once more, in a child process on the library whose kernels check every tiled copy and row store."""
+    from ring_attn_gb300.build import build
+
+    build(debug_bounds=True)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider", __file__,
+                        "-k", "not bounds_checks"], env=dict(os.environ, RA_LIB_VARIANT="debug_bounds"),
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), stdout=subprocess.PIPE,
+                       stderr=subprocess.STDOUT, text=True, timeout=1200)
+    assert r.returncode == 0 and " passed" in r.stdout, "\n".join(r.stdout.splitlines()[-30:])
