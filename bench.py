@@ -453,9 +453,9 @@ def main():
     fwd_tflops = FWD_FLOP / (fwd_ms * 1e-3) / 1e12
     peak_sus = peaks["bf16_sustained"]
     # FLOP each kernel performs: forward 2 GEMMs, dK/dV 4 GEMMs, dQ 3 GEMMs (S and dP recomputed)
-    bwd_src = ["ring_attn_gb300/csrc/ra_bwd.cu", "ring_attn_gb300/csrc/ra_bwd_common.cuh"]
+    bwd_src = ["ring_attn_gb300/csrc/ra_bwd.cuh", "ring_attn_gb300/csrc/ra_bwd_common.cuh"]
     kernels = {
-        "ring_fwd_kernel<128>": (fwd_ms, FWD_FLOP, ["ring_attn_gb300/csrc/ra_fwd.cu"], "ring_fwd_kernel_zigzag_h32_s64k.md"),
+        "ring_fwd_kernel<128>": (fwd_ms, FWD_FLOP, ["ring_attn_gb300/csrc/ra_fwd.cuh"], "ring_fwd_kernel_zigzag_h32_s64k.md"),
         "ring_dkdv_kernel<128>": (dkdv_ms, 2.0 * FWD_FLOP, bwd_src, "ring_dkdv_kernel_zigzag_h32_s64k.md"),
         "ring_dq_kernel<128>": (dq_ms, 1.5 * FWD_FLOP, bwd_src, "ring_dq_kernel_zigzag_h32_s64k.md"),
     }
@@ -480,7 +480,7 @@ def main():
         "fwd": {"tflops": fwd_tflops, "ms": fwd_ms, "frac_of_peak": fwd_tflops / peak_sus,
                 "frac_of_burst": fwd_tflops / peaks["bf16"],
                 "traffic": _profiled_traffic("ring_fwd_kernel_zigzag_h32_s64k.md",
-                                             ["ring_attn_gb300/csrc/ra_fwd.cu"] + common)},
+                                             ["ring_attn_gb300/csrc/ra_fwd.cuh"] + common)},
         "bwd": {"tflops": bwd_tflops, "ms": bwd_ms, "frac_of_peak": bwd_tflops / peak_sus,
                 "flop_credited": "2.5 x forward (the 5 backward GEMMs; the 2 recomputed in the dQ pass are not)",
                 "dkdv_ms": dkdv_ms, "dkdv_tflops_performed": 2.0 * FWD_FLOP / (dkdv_ms * 1e-3) / 1e12,

@@ -18,10 +18,10 @@
 //   2. the two threads of a row exchange their bounds through shared memory (as bf16, rounded up) and take the
 //      larger as the offset, if it passes the running one by 2^8.
 //
-// Bound, d = 128: a tile of 128 x 128 needs 1024 cycles of the tensor cores, and a scheduler's four warps 2 cycles
-// of the multiply-add pipe for 64 of its scores and each of (cap) 7 or (bias) 4 packed instructions, and 4 cycles of
-// the special function unit for 32 exponentials: the cap's 1150 cycles are just over, and waits for one another
-// (a product, its weights, the next product) come on top of both.  Causal, 16,384 tokens of 32 heads of 128, softcap 50:
+// Bound, d = 128: a tile of 128 x 128 needs 1024 cycles of the tensor cores, which are busy half of the time; the
+// multiply-add pipes are for 39 %, the issue slots for 53 %.  The rest are a tile's steps that wait for one another (a
+// product, its weights, the next product), with two tiles in flight, which fill tensor memory.  Causal, 16,384 tokens of
+// 32 heads of 128, softcap 50:
 // 1.72 to 1.75 ms, 1276 TFLOP/s (66 % of the measured bf16 rate), without the cap 1.55; 8192 tokens of 32 + 8 heads,
 // softcap 30 and a prefix 0.50 ms (0.46); 2 x 4096 tokens of 16 heads of 64, a bias, 4 striped shards 178 us (157).
 // What led here, for the first: a row a thread 2.36 ms, half a row 2.14, one offset and 32 columns at a time 1.82 (1.88
