@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           // A cap keeps the products' order, so the largest product gives the offset, and the scores are made on their
           // way to the exponential.  The products are read twice, 32 at a time, in loops: little code, for which the
           // warps wait less (three chunks of up to 700 tokens over up to 20,000 keys, 32 heads of 8: 0.30 ms; 64 at a
-          // time 0.37, all 128 in registers 0.60, changed there as with a bias below 0.34).
+          // time 0.37, all 128 in registers 0.60).
           float hi[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
           const bool cut = __any_sync(0xffffffffu, c_hi < kUnit);
 #pragma unroll 1
@@ -575,6 +575,66 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           float s0, s1;
           f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
           sum = s0 + s1;
+        } else if constexpr (kChanged) {
+          // With a bias the scores themselves are compared: changed, put back over the products, and read again.
+          // (The chunks above with softcap 20 and a bias: 0.40 ms; all 128 in registers, as with plain scores, 0.52.)
+          float mx[2] = {-INFINITY, -INFINITY};
+          const BiasLine bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
+          const bool line = __all_sync(0xffffffffu, bias.line), cut = __any_sync(0xffffffffu, c_hi < kUnit);
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t v[32];
+            tmem_ld32(tS + 32 * ch, v);
+            const BiasLine part = bias.from(32 * ch);
+            const uint32_t m32 = (uint32_t)bit_window64(0, c_hi - 32 * ch);
+            tmem_ld_wait(v);
+            int tier = 0;
+            if constexpr ((SC & SC_CAP) != 0) {
+              tier = max(tier_of(largest(v) * sc, a.sc, line), at_least);
+              if (line) at_least = min(tier, 1);
+            }
+            with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
+              const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                uint64_t w;
+                float z0, z1;
+                f32x2_split(cap(mul_f32x2(f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f32x2(sc, sc)),
+                                with_bias<SC, decltype(li)::value, decltype(li)::value>(part, k, 0), w),
+                            z0, z1);
+                v[k] = __float_as_uint(z0), v[k + 1] = __float_as_uint(z1);
+              }
+            });
+            if (cut)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = (m32 >> k) & 1u ? v[k] : __float_as_uint(-INFINITY);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2)
+              mx[(k >> 1) & 1] = fmax3f(mx[(k >> 1) & 1], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+            tmem_st32(tS + 32 * ch, v);
+          }
+          tmem_st_wait();
+          raise(fmaxf(mx[0], mx[1]));
+          const uint64_t nm2 = f32x2(-M, -M);
+          uint64_t acc[2] = {0, 0};
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(tS + 32 * ch, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float e0, e1;
+              f32x2_split(add_f32x2(f32x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), nm2), e0, e1);
+              e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+              acc[k & 1] = add_f32x2(acc[k & 1], f32x2(e0, e1));
+              pk[k] = pack_f16x2(e0, e1);
+            }
+            tmem_st16(tS + ch * 16, pk);
+          }
+          float s0, s1;
+          f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
+          sum = s0 + s1;
         } else {
           uint32_t v[kUnit];
           tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(v + 0));
@@ -583,35 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
           tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
           tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(v + 64));
           tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(v + 96));
-          if constexpr (kChanged) {
-            // scores as they count, in log2 units
-            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
-            tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
-            BiasLine bias = {};
-            int tier = 0;
-            bool line = true;
-            if constexpr ((SC & SC_BIAS) != 0) {
-              bias = bias_line(TileTokens{u * kUnit, 0, 1, kNoSeam}, own, 0, min(c_hi, kUnit), slope2);
-              line = __all_sync(0xffffffffu, bias.line);
-            }
-            if constexpr ((SC & SC_CAP) != 0) tier = score_tier(v, a.sc, line, sc);
-            with_score_flags<SC>(tier, line, [&](auto ti, auto li) {
-              const Cap<SC, decltype(ti)::value> cap(sb + L::kCaps);
-#pragma unroll
-              for (int c = 0; c < kUnit; c += 2) {
-                uint64_t w;
-                float z0, z1;
-                f32x2_split(cap(mul_f32x2(f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f32x2(sc, sc)),
-                                with_bias<SC, decltype(li)::value, decltype(li)::value>(bias, c, 0), w),
-                            z0, z1);
-                v[c] = __float_as_uint(z0), v[c + 1] = __float_as_uint(z1);
-              }
-            });
-          }
           float mc[4];
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            if (!kChanged && hh == 1) {
+            if (hh == 1) {
               tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 64));
               tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(v + 96));
             }
@@ -631,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             }
           }
           float mx = fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3]));
-          if constexpr (!kChanged) mx = __fmul_rn(mx, sc);
+          mx = __fmul_rn(mx, sc);
           raise(mx);
           const uint64_t sc2 = f32x2(sc, sc), nm2 = f32x2(-M, -M);
           uint64_t acc[4] = {0, 0, 0, 0};
@@ -646,9 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
               for (int k = 0; k < 16; ++k) {
                 const int c = c32 * 32 + 2 * k;
                 float x0 = __uint_as_float(v[c]), x1 = __uint_as_float(v[c + 1]);
-                if constexpr (kChanged)
-                  f32x2_split(add_f32x2(f32x2(x0, x1), nm2), x0, x1);
-                else if constexpr (decltype(rounded)::value)
+                if constexpr (decltype(rounded)::value)
                   x0 = __fsub_rn(__fmul_rn(x0, sc), M), x1 = __fsub_rn(__fmul_rn(x1, sc), M);
                 else
                   f32x2_split(fma_f32x2(f32x2(x0, x1), sc2, nm2), x0, x1);
@@ -659,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
               tmem_st16(tS + c32 * 16, pk);
             }
           };
-          if (!kChanged && far)
+          if (far)
             weights(Int<1>{});
           else
             weights(Int<0>{});
