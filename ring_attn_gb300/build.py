@@ -1,6 +1,6 @@
 """Builds libringattn.so in-tree for sm_103a (nvcc, one translation unit per kernel family, in parallel),
-and _ra_binding.so (the host compiler), which marshals torch tensors into its cache calls.  The
-library needs nvcc alone; where torch is not installed, only it is built.
+and _ra_binding.so (the host compiler), which marshals torch tensors into its cache calls, the
+rotation and attention with changed scores.  The library needs nvcc alone; where torch is not installed, only it is built.
 
 build(debug_bounds=True) builds the debug variant libringattn_dbg.so instead:
 the same sources compiled with RA_DEBUG_BOUNDS, under which every kernel checks
@@ -30,7 +30,7 @@ SOURCES = ["ra_api.cu", "ra_fwd.cu", "ra_bwd.cu", "ra_dkdv_pair.cu", "ra_simple.
 HEADERS = [os.path.join(CSRC, h) for h in ("ra_device.cuh", "ra_internal.h", "ra_tiles.cuh", "ra_bwd_common.cuh",
                                                "ra_cache_args.h", "ra_cache.cuh", "ra_cache_line.cuh", "ra_cache_attn.cuh",
                                                "ra_cache_chunk.cuh", "ra_fwd.cuh", "ra_bwd.cuh",
-                                               "ra_score.cuh", "ra_scored_fwd.cuh", "ra_scored_bwd.cuh")] + [
+                                               "ra_early.cuh", "ra_score.cuh", "ra_scored_fwd.cuh", "ra_scored_bwd.cuh")] + [
     os.path.join(ROOT, "include", "ringattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

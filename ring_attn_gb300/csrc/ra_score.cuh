@@ -24,6 +24,7 @@
 // Distances are fp32 numbers, exact up to 2^24.
 #pragma once
 
+#include "ra_early.cuh"
 #include "ra_tiles.cuh"
 
 namespace ra {
@@ -268,6 +269,12 @@ __device__ __forceinline__ Start start_of(const P& p, int n, int only) {  // n: 
   }
   s.i0 = tile * kRows;
   return s;
+}
+
+// Batch i's prefix, as prefix_of gives it, behind after_previous_kernel.
+template <class P>
+__device__ __forceinline__ int prefix_now(const P& p, int i) {
+  return p.sc.prefix && p.causal ? min(max(load_now(p.sc.prefix + i), 0), 1 << 30) : 0;
 }
 
 // The largest magnitude of N products (none that is NaN).

@@ -60,6 +60,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
     prefetch_tmap(&tmDO);
+  }
+  if constexpr (!VL) after_previous_kernel();
+  if (threadIdx.x == 0) {
     // the key tile's K and V depend on nothing the walk below computes: issued
     // first, their latency overlaps the CTA's set-up
     const int krow = ks * p.L + kj0;
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   }
   KRange k;
-  const int pre = VL ? 0 : prefix_of(p, b);
+  const int pre = VL ? 0 : prefix_now(p, b);
   make_krange(p, ks, kj0, k, kTileN, pre);
   int n_tiles = 0;  // over all query heads of the group (every head meets the same tiles)
   walk_q_tiles<kTileM>(p, k, p.n_qtiles, [&](int, int) {
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // every query head of the group meets the same tiles; the walk does not depend on the head
     for (int g = 0; ok && g < p.G; ++g) {
-      if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + hk * p.G + g) * 1.4426950408889634f;
+      if constexpr ((SC & SC_BIAS) != 0) slope2 = load_now(p.sc.slopes + hk * p.G + g) * 1.4426950408889634f;
       walk_q_tiles<kTileM>(p, k, p.n_qtiles, tile);
     }
     // ---------------- epilogue: warpgroup 1 writes the dV rows, warpgroup 2 the dK rows
@@ -457,6 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
     prefetch_tmap(&tmDO);
+  }
+  if constexpr (!VL) after_previous_kernel();
+  if (threadIdx.x == 0) {
     // the tile's Q and dO depend on nothing the tile walk below computes:
     // issued first, their latency overlaps the CTA's set-up
     const int qrow = r * p.L + i0 - p.q_base;
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   }
   QRange qr;
-  const int pre = VL ? 0 : prefix_of(p, b);
+  const int pre = VL ? 0 : prefix_now(p, b);
   make_qrange(p, r, i0, kTileM, qr, pre);
   const int nkt = (p.L + kTileN - 1) / kTileN;
   int n_tiles = 0;
@@ -601,12 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       gq = tok(p, r, valid ? i : max(qr.i_last, 0));
     // this row's statistics, negated (padding rows: -lse2 = -inf, -D = 0, so P = dS = 0)
     const long long srow = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
-    const float nl = __ldg(p.nlse2 + srow);
+    const float nl = load_now(p.nlse2 + srow);
     const uint64_t nl2 = f32x2(nl, nl);
     const float nD = p.nD[srow];
     const uint64_t nD2 = f32x2(nD, nD);
     float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
+    if constexpr ((SC & SC_BIAS) != 0) slope2 = load_now(p.sc.slopes + h) * 1.4426950408889634f;
     // warpgroup 1 copies the row's Q, warpgroup 2 its dO, into tensor memory as
     // packed bf16 (column m: head-dim elements 2m, 2m + 1) for the S and dP MMAs
     bool ok = n_tiles == 0 || !LY::kQInTmem || wait_warp(BAR(F_QDO_FULL), 0, abort_flag, p.ctl, 64);
@@ -795,6 +801,8 @@ cudaError_t launch_bwd_sdv(const CUtensorMap& tq, const CUtensorMap& tk, const C
     cudaError_t e = configure_kernel<ring_scored_dq_kernel<D, VL, SC>>(kDkdvLaunchRegs, LY::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * p.n_qtiles), (unsigned)(p.B * p.H));
+    if constexpr (!VL)
+      return launch_early(ring_scored_dq_kernel<D, VL, SC>, grid, kThreads, LY::kAlloc, st, tq, tk, tv, tdo, pv);
     ring_scored_dq_kernel<D, VL, SC><<<grid, kThreads, LY::kAlloc, st>>>(tq, tk, tv, tdo, pv);
   } else if constexpr (SC == SC_ON) {
     return launch_bwd_v<D, VL, SC>(tq, tk, tv, tdo, pv, 0, st);
@@ -802,6 +810,8 @@ cudaError_t launch_bwd_sdv(const CUtensorMap& tq, const CUtensorMap& tk, const C
     cudaError_t e = configure_kernel<ring_scored_dkdv_kernel<D, VL, SC>>(kDkdvLaunchRegs, DkdvLayout<D>::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(p.N * p.n_ktiles), (unsigned)(p.B * p.Hk));
+    if constexpr (!VL)
+      return launch_early(ring_scored_dkdv_kernel<D, VL, SC>, grid, kThreads, DkdvLayout<D>::kAlloc, st, tq, tk, tv, tdo, pv);
     ring_scored_dkdv_kernel<D, VL, SC><<<grid, kThreads, DkdvLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, pv);
   }
   return cudaGetLastError();

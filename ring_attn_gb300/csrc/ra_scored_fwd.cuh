@@ -92,6 +92,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
+  }
+  if constexpr (!VL) after_previous_kernel();  // (varlen reads cu_seqlens through the read-only path)
+  if (threadIdx.x == 0) {
     // the CTA's Q tiles depend on nothing the tile walk below computes: issued
     // first, their latency overlaps the CTA's set-up
     if (!(p.ctl.debug_flags & DBG_SKIP_Q_LOAD)) {
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   }
   fill_cap_table(sp + LY::kCaps, p.sc);
   QRange cta;  // both query tiles together: decides which key tiles are visited
-  const int pre = VL ? 0 : prefix_of(p, b);
+  const int pre = VL ? 0 : prefix_now(p, b);
   make_qrange(p, r, i0, kRowsPerCta, cta, pre);
   const int nkt = (p.L + kTileN - 1) / kTileN;
   int n_tiles = 0;
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       gq = tok(p, r, valid ? i : max(qt.i_last, 0));
     }
     float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = __ldg(p.sc.slopes + h) * 1.4426950408889634f;
+    if constexpr ((SC & SC_BIAS) != 0) slope2 = load_now(p.sc.slopes + h) * 1.4426950408889634f;
     // Capped scores lie within +-cap2, so where that is small enough one offset serves all rows: weights are at most
     // 1, or 2^60 for the largest of these caps, and the largest one of a row whose scores are the least is 2^-102 or
     // more, 2^24 above what fp32 and bf16 still have.  A bias only takes off, and nothing from the row's own token, which
@@ -598,6 +601,8 @@ cudaError_t launch_fwd_sdv(const CUtensorMap& tq, const CUtensorMap& tk, const C
     if (e != cudaSuccess) return e;
     const int n_pairs = (p.L + kRowsPerCta - 1) / kRowsPerCta;
     dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * n_pairs), (unsigned)(p.B * p.H));
+    if constexpr (!VL)
+      return launch_early(ring_scored_fwd_kernel<D, VL, SC>, grid, kScoredThreads, LY::kAlloc, st, tq, tk, tv, pv);
     ring_scored_fwd_kernel<D, VL, SC><<<grid, kScoredThreads, LY::kAlloc, st>>>(tq, tk, tv, pv);
     return cudaGetLastError();
   }

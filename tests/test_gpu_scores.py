@@ -332,6 +332,41 @@ def test_captured_calls_follow_slopes_and_prefix_and_repeat_their_bits():
     check_no_device_error(ra)
 
 
+@pytest.mark.parametrize("d,n", [(64, 3), (128, 400)])
+def test_calls_that_follow_one_another_wait_for_one_another(d, n):
+    """Kernels are set up while the one before still runs: what that one writes (rotated rows, slopes, prefixes, statistics)
+    they read behind it.  The same steps with a wait after each give the same bits."""
+    b, h = 2, 2
+    x = {k: v.cuda() for k, v in inputs(b, h, h, n, d, 9750).items()}
+    angle = torch.rand(4 * n, d // 2, device="cuda") * 6.0
+    table = (angle.cos(), angle.sin())
+    places = torch.arange(b * n, dtype=torch.int32, device="cuda").view(b, n)
+
+    def steps(wait):
+        sl, pre = torch.zeros(h, device="cuda"), torch.zeros(b, dtype=torch.int32, device="cuda")
+        z, got, q = ra.Scores(9.0, sl, pre), [], x["q"].clone()
+        for i in range(12):
+            sl.add_(0.02)
+            wait()
+            pre.add_(n // 12)
+            wait()
+            q, k = ra.ring_attn_rope(q, x["k"], table, places)
+            wait()
+            out, lse = ra.ring_attn_fwd(q, k, x["v"], causal=True, scores=z)
+            wait()
+            dq, dk, dv = ra.ring_attn_bwd(x["do"], q, k, x["v"], out, lse, causal=True, scores=z)
+            wait()
+            dq, dk = ra.ring_attn_rope_bwd(dq, dk, table, places, dq_out=dq, dk_out=dk)
+            wait()
+            got += [out, lse, dq, dk, dv]
+        return got
+
+    first = steps(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, c) for a, c in zip(first, steps(lambda: None)))
+    check_no_device_error(ra)
+
+
 @pytest.mark.parametrize("flag", [1, 2, 4], ids=["fwd", "dkdv", "dq"])
 @pytest.mark.parametrize("cap,slopes,d", [(20.0, None, 64), (70.0, None, 128), (0.0, "alibi", 64), (20.0, "alibi", 128)])
 def test_a_wait_that_runs_out_is_reported_and_the_context_survives(flag, cap, slopes, d):
