@@ -111,7 +111,7 @@ __device__ __forceinline__ uint64_t polynomial(uint64_t w, const uint64_t (&c)[N
 // The constants of the caps, each twice for the two lanes of a packed instruction, in shared memory, for kernels
 // short of registers: there the assembler makes pairs of kernel parameters anew next to their uses, two moves for a
 // multiply-add of two scores, while pairs that are loaded stay (16,384 tokens capped: 1.82 ms, 1.88 without).
-constexpr int kCapConsts = 31;
+constexpr int kCapConsts = 20;
 constexpr int kCapTable = 8 * kCapConsts;  // bytes
 __device__ __forceinline__ void fill_cap_table(uint8_t* table, const ScoreParams& sc) {
   const int i = threadIdx.x;
@@ -119,18 +119,12 @@ __device__ __forceinline__ void fill_cap_table(uint8_t* table, const ScoreParams
   float x;
   if (i < 4)
     x = sc.t0[i];
-  else if (i < 6)
-    x = sc.g0[i - 4];
-  else if (i < 11)
-    x = sc.t1[i - 6];
-  else if (i < 14)
-    x = sc.g1[i - 11];
-  else if (i < 21)
-    x = sc.t2[i - 14];
-  else if (i < 26)
-    x = sc.g2[i - 21];
+  else if (i < 9)
+    x = sc.t1[i - 4];
+  else if (i < 16)
+    x = sc.t2[i - 9];
   else
-    x = i == 26 ? sc.e2 : i == 27 ? -2.f * sc.cap2 : i == 28 ? sc.cap2 : i == 29 ? sc.inv_cap2 : sc.c0;
+    x = i == 16 ? sc.e2 : i == 17 ? -2.f * sc.cap2 : i == 18 ? sc.cap2 : sc.c0;
   reinterpret_cast<float2*>(table)[i] = make_float2(x, x);
 }
 __device__ __forceinline__ uint64_t cap_const(uint32_t table, int i) {
@@ -162,12 +156,10 @@ struct Cap {
     }
   }
   __device__ __forceinline__ explicit Cap(uint32_t table) {
-    constexpr int at = !kCap ? 30 : kAny ? 26 : kTier == 0 ? 0 : kTier == 1 ? 6 : 14;
+    static_assert(!kGrad, "the derivative's coefficients are not in the table");
+    constexpr int at = !kCap ? 19 : kAny ? 16 : kTier == 0 ? 0 : kTier == 1 ? 4 : 9;
 #pragma unroll
     for (int i = 0; i < kT; ++i) t[i] = cap_const(table, at + i);
-    if (kCap && kGrad)
-#pragma unroll
-      for (int i = 0; i < kG; ++i) g[i] = cap_const(table, at + kT + i);
   }
   // Two products s: their scores + add, and w, from which their derivatives follow.
   __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add, uint64_t& w) const {
@@ -297,8 +289,8 @@ __device__ __forceinline__ int tier_of(float size, const ScoreParams& sc, bool l
   return all <= sc.lim[0] ? 0 : all <= sc.lim[1] ? 1 : all <= sc.lim[2] ? 2 : kTiers;
 }
 template <int N>
-__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, bool least, float factor = 1.f) {
-  return tier_of(largest(v) * factor, sc, least);
+__device__ __forceinline__ int score_tier(const uint32_t (&v)[N], const ScoreParams& sc, bool least) {
+  return tier_of(largest(v), sc, least);
 }
 
 }  // namespace ra
