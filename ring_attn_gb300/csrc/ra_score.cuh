@@ -48,8 +48,24 @@ struct TileTokens {
 constexpr int kNoSeam = 1 << 20;
 
 // A softmax's offset may be this much (log2 units) above the largest score: weights down to 2^-24 of the largest
-// are then still normal numbers, in bf16, too.
+// are then still normal numbers, in bf16, too.  (So bounds are fp32 numbers wherever they are kept: those of steep
+// biases are 2^14 and more, and with the bits of bf16 they would be off by that much themselves.)
 constexpr float kLoose = 88.f;
+
+// Numbers (no NaN) as integers in the same order, and a word of shared memory that is raised to the larger.
+__device__ __forceinline__ int to_ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+__device__ __forceinline__ void raise_shared(uint32_t at, int x) {
+  asm volatile("red.shared.max.s32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ int load_shared(uint32_t at) {
+  int x;
+  asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
 
 // Columns: local positions [j0, ...) of shard s (win: the row's window, for varlen).
 template <class P>

@@ -15,8 +15,8 @@
 //      bound of the largest score follows; the offset of a softmax may lie above it by kLoose.  Tiles in which the
 //      bias is no line (the row's own token or a zigzag seam inside), or too steep a one, go over their changed
 //      scores instead.
-//   2. the two threads of a row exchange their bounds through shared memory (as bf16, rounded up) and take the
-//      larger as the offset, if it passes the running one by 2^8.
+//   2. the two threads of a row raise the row's bound, a word of shared memory, and take it as the offset, if it passes
+//      the running one by 2^8.
 //
 // Bound, d = 128: a tile of 128 x 128 needs 1024 cycles of the tensor cores, which are busy half of the time; the
 // multiply-add pipes are for 39 %, the issue slots for 53 %.  The rest are a tile's steps that wait for one another (a
@@ -44,8 +44,8 @@ static_assert(128 * kScoredRegsLow + 512 * kScoredRegsHigh <= kScoredThreads * k
 template <int D>
 struct ScoredFwdLayout : FwdLayout<D> {
   using Base = FwdLayout<D>;
-  static constexpr int kBound = Base::kMisc + 16;  // bf16 [2 tiles][2 halves][128 rows]
-  static constexpr int kCaps = (kBound + 2 * 2 * 128 * 2 + 7) / 8 * 8;  // constants
+  static constexpr int kBound = Base::kMisc + 16;  // [2 tiles][128 rows], as to_ordered
+  static constexpr int kCaps = (kBound + 2 * 128 * 4 + 7) / 8 * 8;  // constants
   static constexpr int kAlloc = kCaps + kCapTable + 1024;
   // the epilogue's row slots (16 warps x 32 rows of half a head, bf16) and sums reuse the operand buffers
   static_assert(16 * 32 * D + 2048 <= Base::kBar, "output slots exceed the operand buffers");
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     }
   }
   fill_cap_table(sp + LY::kCaps, p.sc);
+  if (threadIdx.x < 256) reinterpret_cast<int*>(sp + LY::kBound)[threadIdx.x] = to_ordered(-INFINITY);
   QRange cta;  // both query tiles together: decides which key tiles are visited
   const int pre = VL ? 0 : prefix_now(p, b);
   make_qrange(p, r, i0, kRowsPerCta, cta, pre);
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     const uint32_t tO = tl + LY::kTmemO + t * 128 + half * (D / 2);
     const int i = i0 + t * kTileM + row;
     bool valid = i < p.L;
-    __nv_bfloat16* bounds = reinterpret_cast<__nv_bfloat16*>(sp + LY::kBound) + t * 256 + row;
+    const uint32_t bound = sb + LY::kBound + 4 * (t * 128 + row);  // of the row's scores so far
     const int pair_bar = 1 + t * 4 + (warp & 3);  // the two warps of 32 rows
     const uint32_t cap_table = sb + LY::kCaps;
     QRange qt;
@@ -424,9 +425,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
           }
           mx = most<SC>(p.sc, bias, fmax3f(mc[0], mc[1], fmaxf(mc[2], mc[3])), 64);
         }
-        bounds[half * 128] = __float2bfloat16_ru(mx);
+        raise_shared(bound, to_ordered(mx));
         named_bar_sync(pair_bar, 64);
-        mx = fmaxf(__bfloat162float(bounds[0]), __bfloat162float(bounds[128]));
+        mx = from_ordered(load_shared(bound));
         if (mx > -INFINITY) {
           if (m_run == -INFINITY) {
             m_run = mx;  // nothing accumulated yet for this row
