@@ -458,6 +458,10 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  * kernels, so a captured call follows them as they are when it is replayed.  A ra_scores
  * without any of the three makes a call the plain one; NULL is refused.
  *
+ * The backward makes D more exact than the bf16 out has it, from the call's own products, for rows whose weights
+ * 2^(z - lse) sum to 1 within 2^-10.  Other rows (out and lse of more keys than the call's, for a block's share of the
+ * gradients) have D = rowsum(dO * O).
+ *
  * ring_attn_scored_X is ring_attn_X with scores; everything else is as there, but that dq, dk and dv
  * may share no element with dout, q, k, v or each other (RA_ERR_INVALID_ARG; slices of one packed tensor
  * share none).  The CTA-pair knob does not concern these calls. */

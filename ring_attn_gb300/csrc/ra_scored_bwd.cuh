@@ -400,6 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // statistics for the dK / dV pass.  (A pass of its own for sum P dP, two products more, took 0.52 ms at 8192 tokens of
 // 32 + 8 heads of 128, where this takes 0.31 ms.)
 //
+// That holds for a row whose keys are all here.  A call may also have a block of a row's keys, with out and lse of the
+// whole row (a ring whose blocks are called one by one): its weights sum to less, and D stays as the given out has it,
+// as in the plain backward.  kWholeRow is by how much a sum may miss 1: keys of that weight elsewhere put at most
+// as much of dP - D into D, a quarter of what dS is rounded by, and lse's own rounding stays below it up to 2^11.  The
+// sum of the weights costs dQ 1 to 2 % (d = 64: 4 %; added up while dP is awaited it cost 3.5 and 3 %).
+//
 // dS is rounded to bf16 as an operand, and since a row's dS nearly cancel in its sum, the rounding errors weigh more
 // than they do in each: 0.182 % of dQ at softcap 30, 0.199 % at 15, where one rounding is 0.166 %.  Most of that is the sum
 // of a row's errors times what its keys have in common, so that is taken off by P' K too: the sum of the rounded dS less
@@ -409,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // TMEM: S [0, 128), dP [128, 256).  d = 128: the sums of dS K and of P' K take the rest, so that Q and dO stay in shared
 // memory; d = 64: as in the plain kernel, with the second sum behind the first.  P' is packed beside dS, over the
 // second 32 of a thread's 64 dP columns.
+constexpr float kWholeRow = 0x1p-10f;
 template <int D>
 struct ScoredDqLayout : DqLayout<D> {
   using Base = DqLayout<D>;
@@ -637,8 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(F_QDO_TMEM));
     }
-    // sums of P (dP - D), of dS as rounded, and (cap; else the first) of dS
-    uint64_t miss[2] = {0, 0}, rounded = 0, exact = 0;
+    // sums of P (dP - D), of P, of dS as rounded, and (cap; else the first) of dS
+    uint64_t miss[2] = {0, 0}, weights = 0, rounded = 0, exact = 0;
     int j = 0;
     if (ok) walk_kv_tiles(p, qr, nkt, 0, p.N, [&](int s, int kt) {
       int c_lo = 0, c_hi = kTileN;
@@ -712,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // are read
       const uint32_t tdp = tl + LY::kTmemDP + 64 * half;
       uint32_t ds[32];
+      uint64_t in_tile = 0;  // (single weights of a long row are too small next to 1)
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         uint32_t d[32];
@@ -723,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t pair = f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
           const uint64_t diff = add_f32x2(f32x2(__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])), nD2);
           miss[u & 1] = fma_f32x2(pair, diff, miss[u & 1]);
+          in_tile = add_f32x2(in_tile, pair);
           uint64_t grad = pair;
           if constexpr ((SC & SC_CAP) != 0) grad = f32x2(__uint_as_float(g[c]), __uint_as_float(g[c + 1]));
           grad = mul_f32x2(grad, diff);
@@ -732,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ds[c / 2] = pack_bf16x2(s0, s1);
         }
       }
+      weights = add_f32x2(weights, in_tile);
       tmem_st32(tdp, ds);
       tmem_st32(tdp + 32, pp);
       tmem_st_wait();
@@ -755,8 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1 + (warp & 3), 64);
       return all;
     };
-    const float missing = of_row(add_f32x2(miss[0], miss[1]));
-    const float too_much = of_row(rounded) - ((SC & SC_CAP) != 0 ? of_row(exact) : missing);
+    const float sum = of_row(add_f32x2(miss[0], miss[1]));
+    const float missing = fabsf(of_row(weights) - 1.f) <= kWholeRow ? sum : 0.f;
+    const float too_much = of_row(rounded) - ((SC & SC_CAP) != 0 ? of_row(exact) : sum);
     if (half == 0 && valid && ok) const_cast<float*>(p.nD)[srow] = nD - missing;
     // ---------------- epilogue: dQ = scale * (dS K - (missing + too_much) P' K), half the head dim per thread
     const int* rmap = VL ? p.row_map : nullptr;  // varlen in original order: rows of the caller's layout

@@ -70,3 +70,52 @@ def test_far_scores_of_whole_calls(causal, cap, slope, gain):
     want = expect(x["q"], x["k"], x["v"], None, d ** -0.5, cap, sl, causal, None)
     assert_within("lse", lse, want["lse"])
     assert_within("out", out, want["out"])
+
+
+@pytest.mark.parametrize("d,cap,slope,gain", [(64, 12.0, 0.0, 2.0), (128, 0.0, 0.02, 2.0), (128, 12.0, 0.02, 1.0)])
+@pytest.mark.parametrize("share", [0, 1])
+def test_a_blocks_share_of_the_gradients(d, cap, slope, gain, share):
+    """The keys of a row in two calls with the whole row's out and lse: each gives its share of dq, and dk and dv of its
+    keys, with D = rowsum(dout * out) of the out that it was given."""
+    b, h, hk, s = 1, 2, 1, 256
+    x = inputs(b, h, hk, 2 * s, d, 9150, gain)
+    scale, sl = d ** -0.5, None if not slope else steep(h, slope)
+    q, do = x["q"][:, :, :s].contiguous(), x["do"][:, :, :s].contiguous()
+    t = np.arange(s)
+    out, lse = torch.zeros(b, h, s, d), torch.zeros(b, h, s)
+    # (both blocks take distances from tokens 0 to s - 1, as a call has them)
+    tokens = np.concatenate([t, t])
+    heads = [head_bounds(q[0, a], x["k"][0, 0], x["v"][0, 0], t, tokens, scale, cap, 0.0 if sl is None else float(sl[a]),
+                         False, 0, do[0, a]) for a in range(h)]
+    for a, r in enumerate(heads):
+        out[0, a], lse[0, a] = torch.from_numpy(r["out"]).float(), torch.from_numpy(r["lse"]).float()
+    out = out.bfloat16()
+    here = slice(share * s, (share + 1) * s)
+    k, v = (x[n][:, :, here].contiguous() for n in "kv")
+    z = scores_of(cap, sl, None)
+    dq, dk, dv = ra.ring_attn_bwd(do.cuda(), q.cuda(), k.cuda(), v.cuda(), out.cuda(), lse.cuda(), "contiguous", 1, False,
+                                  scale, scores=z)
+    check_no_device_error(ra)
+    want = {n: np.zeros((s, d)) for n in ("dk", "dv")}
+    bound = {n: np.zeros((s, d)) for n in ("dk", "dv")}
+    k64, v64 = f64(k[0, 0]), f64(v[0, 0])
+    for a, r in enumerate(heads):
+        q64, do64, o64 = f64(q[0, a]), f64(do[0, a]), f64(out[0, a])
+        P, gr = r["P"][:, here], r["g"][:, here]
+        D = (do64 * o64).sum(1)
+        dP, ado = do64 @ v64.T, np.abs(do64)
+        aw = dP - D[:, None]
+        dx = P * aw * gr
+        rel = r["tol"]["lse"][:, None] + 2.0 ** -20
+        off = np.abs(dx) * (2.0 ** -8 * 1.02 + rel) + P * np.abs(aw) * 2.0 ** -19 * (cap > 0)
+        off += P * gr * d * EPS * (ado @ np.abs(v64).T + (ado * np.abs(o64)).sum(1)[:, None])
+        # the sum of a row's roundings, at most 2^-8 of its dS, is taken off as P' would share it out
+        off_q = off + P * gr * (np.abs(dx) * 2.0 ** -8).sum(1)[:, None]
+        dq64 = scale * dx @ k64
+        assert_within("dq", dq[0, a], (dq64, scale * off_q @ np.abs(k64) + 2.0 ** -8 * np.abs(dq64)))
+        want["dk"] += scale * dx.T @ q64
+        bound["dk"] += scale * off.T @ np.abs(q64)
+        want["dv"] += P.T @ do64
+        bound["dv"] += (P * (2.0 ** -8 * 1.01 + rel)).T @ ado
+    for name, got in (("dk", dk), ("dv", dv)):
+        assert_within(name, got[0, 0], (want[name], bound[name] + 2.0 ** -8 * np.abs(want[name])))
