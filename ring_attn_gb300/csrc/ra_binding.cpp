@@ -84,10 +84,11 @@ const at::Tensor& tensor(PyObject* o, int index) {
 
 ra_tensor describe(const at::Tensor& t, int64_t dims) {
   ra_tensor r{};
+  RA_REFUSE(t.dim() != dims, "expected a ", dims, "-D tensor, got ", t.sizes());
+  RA_REFUSE(dims < 1 || dims > (int64_t)(sizeof(r.shape) / sizeof(r.shape[0])), "tensors must have 1 to 4 dimensions");
   r.data = t.data_ptr();
   RA_REFUSE(t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat, "unsupported dtype ", t.scalar_type());
   r.dtype = t.scalar_type() == at::kFloat ? RA_FP32 : RA_BF16;
-  RA_REFUSE(t.dim() != dims, "expected a ", dims, "-D tensor, got ", t.sizes());
   r.ndim = (int32_t)dims;
   for (int64_t i = 0; i < dims; ++i) {
     r.shape[i] = t.size(i);
@@ -306,12 +307,19 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // ---------------------------------------------------------------- attention with changed scores
-// Tensors of one call, on q's device.
+// Tensors of one call, on q's device: the inputs a[0 .. n) and the results r[0 .. m), where given, are checked first.
 struct OnDevice {
   int index;
-  explicit OnDevice(PyObject* q) : index(-1) {
+  OnDevice(PyObject* q, PyObject* const* a, int n, PyObject* const* r, int m) : index(-1) {
     RA_REFUSE(!THPVariable_Check(q) || !THPVariable_Unpack(q).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
     index = THPVariable_Unpack(q).get_device();
+    auto check = [this](PyObject* o) {
+      const at::Tensor& t = (*this)(o);
+      RA_REFUSE(t.dim() < 1 || t.dim() > 4, "tensors must have 1 to 4 dimensions, got ", t.sizes());
+    };
+    for (int i = 0; i < n; ++i) check(a[i]);
+    for (int i = 0; i < m; ++i)
+      if (given(r[i])) check(r[i]);
   }
   const at::Tensor& operator()(PyObject* o) const {
     RA_REFUSE(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
@@ -365,7 +373,7 @@ at::Tensor four(const at::Tensor& q) {
 PyObject* scored_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   TORCH_CHECK_VALUE(n == 10, "10 arguments");
-  const OnDevice dev(a[0]);
+  const OnDevice dev(a[0], a, 3, a + 8, 2);
   const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   const at::Tensor q = four(dev(a[0]));
   const ra_tensor tq = describe(q, 4), tk = describe(dev(a[1]), 4), tv = describe(dev(a[2]), 4);
@@ -382,7 +390,7 @@ PyObject* scored_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* scored_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   TORCH_CHECK_VALUE(n == 15, "15 arguments");
-  const OnDevice dev(a[1]);
+  const OnDevice dev(a[1], a, 6, a + 11, 3);
   const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   const at::Tensor q = four(dev(a[1]));
   ra_tensor t[6];
@@ -419,7 +427,7 @@ struct Packed {
 PyObject* scored_varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   TORCH_CHECK_VALUE(n == 14, "14 arguments");
-  const OnDevice dev(a[0]);
+  const OnDevice dev(a[0], a, 3, a + 11, 2);
   const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   const at::Tensor& q = dev(a[0]);
   const Packed p(a[3], a[4], a[5], q, dev.index);
@@ -440,7 +448,7 @@ PyObject* scored_varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* scored_varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   TORCH_CHECK_VALUE(n == 18, "18 arguments");
-  const OnDevice dev(a[1]);
+  const OnDevice dev(a[1], a, 6, a + 14, 3);
   const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   const at::Tensor& q = dev(a[1]);
   const Packed p(a[6], a[7], a[8], q, dev.index);

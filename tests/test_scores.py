@@ -210,3 +210,48 @@ def test_rotation_takes_cuda_tensors_only(lib):
     x = torch.zeros(3, 2, 64)
     with pytest.raises(ValueError, match="CUDA"):
         ra.ring_attn_rope(x, None, (x, x))
+
+
+@pytest.fixture(scope="module")
+def marshaller(lib):
+    """The compiled marshaller, and a maker of tensors that say they are on a GPU and have no memory."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    mode = FakeTensorMode()
+
+    def tensor(*shape, dtype=torch.bfloat16):
+        with mode:
+            return torch.empty(shape, dtype=dtype, device="cuda")
+
+    return ra._ext(), tensor
+
+
+@pytest.mark.parametrize("bad", [(), (1, 1, 2, 64, 64), (1,) * 9])
+@pytest.mark.parametrize("at", range(9))
+def test_tensors_of_other_ranks_are_refused(marshaller, at, bad):
+    """A C tensor has four dimensions: what has none or more is refused before any tensor is described, inputs and results."""
+    ext, tensor = marshaller
+    z = ra.Scores(5.0)
+    names = ["dout", "q", "k", "v", "out", "lse", "dq", "dk", "dv"]
+
+    def args(shape):
+        t = [tensor(*shape) for _ in names]
+        t[5] = tensor(*shape[:-1], dtype=torch.float32)
+        t[at] = tensor(*bad)
+        return t
+
+    if bad == () and at == 1:
+        return  # (no head dim to take the scale from: an IndexError)
+    message = "1 to 4 dimensions|expected a [34]-D"
+    t = args((1, 2, 64, 64))
+    with pytest.raises(ValueError, match=message):
+        ra.ring_attn_bwd(*t[:6], dq=t[6], dk=t[7], dv=t[8], scores=z)
+    if 1 <= at <= 5:
+        with pytest.raises(ValueError, match=message):
+            ra.ring_attn_fwd(*t[1:4], out=t[4], lse=t[5], scores=z)
+    t, cu = args((64, 2, 64)), torch.tensor([0, 64], dtype=torch.int32)
+    with pytest.raises(ValueError, match=message):
+        ext.scored_varlen_bwd(*t[:6], cu, cu, None, 0, 1, True, 0.125, ra._of(z), *t[6:], None)
+    if 1 <= at <= 5:
+        with pytest.raises(ValueError, match=message):
+            ext.scored_varlen_fwd(*t[1:4], cu, cu, None, 0, 1, True, 0.125, ra._of(z), *t[4:6], None)
