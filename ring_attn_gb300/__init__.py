@@ -215,40 +215,45 @@ class Scores:
     prefix: (b,) int32, or (n_seqs,) for varlen and cache calls: with causal, every token of a
     sequence sees its first prefix tokens, so that those see each other both ways.
     out, lse and the gradients of q, k and v are those of attention with z; softcap and slopes
-    are constants.  The handle keeps the tensors, whose contents the kernels read (so a
-    captured call follows them); they cannot be replaced: other tensors are another handle."""
+    are constants.  The handle keeps the tensors; the kernels read their contents (so a captured call
+    follows them), from where the tensors are at the call.  Other tensors are another handle."""
 
     softcap, slopes, prefix = (property(lambda self, i=i: self._parts[i]) for i in range(3))
 
     def __init__(self, softcap=0.0, slopes=None, prefix=None):
         self._parts = (float(softcap), slopes, prefix)
-        for name, x, dtype in (("slopes", slopes, torch.float32), ("prefix", prefix, torch.int32)):
+        self._check()
+        if slopes is not None and prefix is not None and slopes.device != prefix.device:
+            raise ValueError("slopes and prefix must be on one device")
+
+    def __reduce__(self):  # copies and pickles describe their own tensors
+        return type(self), self._parts
+
+    @property
+    def device(self):
+        return next((x.device for x in self._parts[1:] if x is not None), None)
+
+    def _check(self):
+        for name, x, dtype in (("slopes", self.slopes, torch.float32), ("prefix", self.prefix, torch.int32)):
             if x is None:
                 continue
             if not isinstance(x, torch.Tensor) or not x.is_cuda:
                 raise ValueError("ring_attn_gb300 takes CUDA tensors only")
             if x.dtype != dtype or x.dim() != 1 or not x.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor")
-        if slopes is not None and prefix is not None and slopes.device != prefix.device:
-            raise ValueError("slopes and prefix must be on one device")
-        self.device = slopes.device if slopes is not None else prefix.device if prefix is not None else None
-        self._c = _Scores(float(softcap), None if slopes is None else slopes.data_ptr(),
-                          None if prefix is None else prefix.data_ptr())
-        self._call = (ctypes.addressof(self._c), -1 if self.device is None else self.device.index,
-                      -1 if slopes is None else slopes.numel(), -1 if prefix is None else prefix.numel())
-
-    def __reduce__(self):  # copies and pickles describe their own tensors
-        return type(self), self._parts
 
     def _arg(self, device, h, n):
         """The C argument for a call of h query heads and n batches or sequences on the device."""
-        if self.device is not None and self.device != device:
-            raise ValueError(f"scores on {self.device}, call on {device}")
-        if self.slopes is not None and self.slopes.numel() != h:
-            raise ValueError(f"slopes must have one entry for each of the {h} query heads")
-        if self.prefix is not None and self.prefix.numel() != n:
-            raise ValueError(f"prefix must have one entry for each of the {n} sequences")
-        return ctypes.byref(self._c)
+        self._check()
+        for name, x, m, of in (("slopes", self.slopes, h, "query heads"), ("prefix", self.prefix, n, "sequences")):
+            if x is None:
+                continue
+            if x.device != device:
+                raise ValueError(f"scores on {x.device}, call on {device}")
+            if x.numel() != m:
+                raise ValueError(f"{name} must have one entry for each of the {m} {of}")
+        return ctypes.byref(_Scores(self.softcap, None if self.slopes is None else self.slopes.data_ptr(),
+                                    None if self.prefix is None else self.prefix.data_ptr()))
 
 
 def _place(scores, q, stream):
@@ -269,7 +274,7 @@ def _place(scores, q, stream):
 def _of(scores):
     if not isinstance(scores, Scores):
         raise ValueError("scores must be a Scores")
-    return scores._call
+    return scores._parts
 
 
 def _scored_call(name, q, stream, *args):
@@ -870,7 +875,7 @@ def ring_attn_cache_fwd(q, cache, page_table, kv_lens, cu_seqlens, causal=True, 
     if scores is not None and not isinstance(scores, Scores):
         raise ValueError("scores must be a Scores")
     return _cache_call("cache_fwd", cache, cu_seqlens, stream, q, page_table, kv_lens, causal, softmax_scale, max_kv_len,
-                       out, lse, out_dtype is torch.float32, workspace, scores and scores._call)[1:]
+                       out, lse, out_dtype is torch.float32, workspace, scores and scores._parts)[1:]
 
 
 # ---------------------------------------------------------------------------- rotary positions

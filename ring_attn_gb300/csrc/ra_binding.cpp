@@ -188,14 +188,32 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// Scores._call for a call of h query heads and n sequences on device `index`; null for None.
-const ra_scores* scores_arg(PyObject* t, int index, int64_t h, int64_t n) {
-  if (!given(t)) return nullptr;
-  RA_REFUSE(!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 4, "scores must be a Scores");
-  RA_REFUSE(item(t, 1) >= 0 && item(t, 1) != index, "scores on cuda:", item(t, 1), ", call on cuda:", index);
-  RA_REFUSE(item(t, 2) >= 0 && item(t, 2) != h, "slopes must have one entry for each of the ", h, " query heads");
-  RA_REFUSE(item(t, 3) >= 0 && item(t, 3) != n, "prefix must have one entry for each of the ", n, " sequences");
-  return reinterpret_cast<const ra_scores*>(item(t, 0));
+// Scores._parts (softcap, slopes, prefix) for a call of h query heads and n sequences on device `index`, with the
+// tensors as they are now; `given` is false for None.
+struct ScoresArg {
+  bool given;
+  ra_scores c;
+  const ra_scores* get() const { return given ? &c : nullptr; }
+};
+const void* per_entry(PyObject* o, at::ScalarType type, int index, int64_t n, const char* what, const char* of) {
+  if (!given(o)) return nullptr;
+  RA_REFUSE(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "ring_attn_gb300 takes CUDA tensors only");
+  const at::Tensor& t = THPVariable_Unpack(o);
+  RA_REFUSE(t.scalar_type() != type || t.dim() != 1 || !t.is_contiguous(), what, " must be a contiguous 1-D ", type, " tensor");
+  RA_REFUSE(t.get_device() != index, "scores on cuda:", t.get_device(), ", call on cuda:", index);
+  RA_REFUSE(t.numel() != n, what, " must have one entry for each of the ", n, " ", of);
+  return t.data_ptr();
+}
+ScoresArg scores_arg(PyObject* t, int index, int64_t h, int64_t n) {
+  ScoresArg r{};
+  if (!given(t)) return r;
+  RA_REFUSE(!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 3, "scores must be a Scores");
+  r.given = true;
+  r.c.softcap = (float)PyFloat_AsDouble(PyTuple_GET_ITEM(t, 0));
+  if (PyErr_Occurred()) throw python_error();
+  r.c.slopes = static_cast<const float*>(per_entry(PyTuple_GET_ITEM(t, 1), at::kFloat, index, h, "slopes", "query heads"));
+  r.c.prefix = static_cast<const int32_t*>(per_entry(PyTuple_GET_ITEM(t, 2), at::kInt, index, n, "prefix", "sequences"));
+  return r;
 }
 
 // (cache, cu's device array, its host array, q, page_table, kv_lens, causal, scale, max_kv_len, out, lse, out_fp32, workspace, scores) -> (status, out, lse)
@@ -208,7 +226,7 @@ PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ra_kv_seqs seqs = sequences(a[4], a[5], cu, c.index);
   const at::Tensor& tq = tensor(a[3], c.index);
   const ra_tensor q = describe(tq, 3);
-  const ra_scores* scores = scores_arg(a[13], c.index, tq.size(1), cu.n);
+  const ScoresArg scores = scores_arg(a[13], c.index, tq.size(1), cu.n);
   const int causal = truth(a[6]), fp32 = truth(a[11]);
   const double scale = PyFloat_AsDouble(a[7]);
   const long max_kv = PyLong_AsLong(a[8]);
@@ -227,7 +245,7 @@ PyObject* cache_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   void *wp = ws.defined() ? ws.data_ptr() : nullptr, *stream = current_stream(c.index);
   const size_t wn = ws.defined() ? ws.nbytes() : 0;
-  const int status = scores ? g_scored_fwd(&q, c.cache, &seqs, causal, (float)scale, scores, (int32_t)max_kv, &o, &l, wp, wn, stream)
+  const int status = scores.given ? g_scored_fwd(&q, c.cache, &seqs, causal, (float)scale, scores.get(), (int32_t)max_kv, &o, &l, wp, wn, stream)
                             : g_fwd(&q, c.cache, &seqs, causal, (float)scale, (int32_t)max_kv, &o, &l, wp, wn, stream);
   return Py_BuildValue("(iNN)", status, given(a[9]) ? Py_NewRef(a[9]) : THPVariable_Wrap(out),
                        given(a[10]) ? Py_NewRef(a[10]) : THPVariable_Wrap(lse));
@@ -360,7 +378,7 @@ How how(PyObject* const* a) {
   if (PyErr_Occurred()) throw python_error();
   return h;
 }
-const ra_scores* scores_of(PyObject* t, int index, int64_t h, int64_t n) {
+ScoresArg scores_of(PyObject* t, int index, int64_t h, int64_t n) {
   RA_REFUSE(!given(t), "scores must be a Scores");
   return scores_arg(t, index, h, n);
 }
@@ -374,14 +392,14 @@ PyObject* scored_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   TORCH_CHECK_VALUE(n == 10, "10 arguments");
   const OnDevice dev(a[0], a, 3, a + 8, 2);
-  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   const at::Tensor q = four(dev(a[0]));
-  const ra_tensor tq = describe(q, 4), tk = describe(dev(a[1]), 4), tv = describe(dev(a[2]), 4);
   const How x = how(a + 3);
-  const ra_scores* z = scores_of(a[7], dev.index, q.size(1), q.size(0));
+  const ScoresArg z = scores_of(a[7], dev.index, q.size(1), q.size(0));
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
+  const ra_tensor tq = describe(q, 4), tk = describe(dev(a[1]), 4), tv = describe(dev(a[2]), 4);
   Result out(a[8], dev, [&] { return at::empty_like(q); });
   Result lse(a[9], dev, [&] { return at::empty({q.size(0), q.size(1), q.size(2)}, on(dev.index, at::kFloat)); });
-  const int status = g_sfwd(&tq, &tk, &tv, x.layout, x.shards, x.causal, x.scale, z, &out.d, &lse.d, current_stream(dev.index));
+  const int status = g_sfwd(&tq, &tk, &tv, x.layout, x.shards, x.causal, x.scale, z.get(), &out.d, &lse.d, current_stream(dev.index));
   return Py_BuildValue("(iNN)", status, out.out(), lse.out());
   END_HANDLE_TH_ERRORS
 }
@@ -391,17 +409,17 @@ PyObject* scored_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   TORCH_CHECK_VALUE(n == 15, "15 arguments");
   const OnDevice dev(a[1], a, 6, a + 11, 3);
-  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   const at::Tensor q = four(dev(a[1]));
+  const How x = how(a + 6);
+  const ScoresArg z = scores_of(a[10], dev.index, q.size(1), q.size(0));
+  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)dev.index));
   ra_tensor t[6];
   for (int i = 0; i < 6; ++i) t[i] = describe(dev(a[i]), dev(a[i]).dim());
-  const How x = how(a + 6);
-  const ra_scores* z = scores_of(a[10], dev.index, q.size(1), q.size(0));
   Result dq(a[11], dev, [&] { return at::empty_like(q); });
   Result dk(a[12], dev, [&] { return at::empty_like(dev(a[2])); });
   Result dv(a[13], dev, [&] { return at::empty_like(dev(a[3])); });
   const Space ws(a[14], dev, g_bwd_ws(RA_OP_BWD, q.size(0), q.size(1), q.size(2), q.size(3), x.shards));
-  const int status = g_sbwd(&t[0], &t[1], &t[2], &t[3], &t[4], &t[5], x.layout, x.shards, x.causal, x.scale, z, &dq.d, &dk.d,
+  const int status = g_sbwd(&t[0], &t[1], &t[2], &t[3], &t[4], &t[5], x.layout, x.shards, x.causal, x.scale, z.get(), &dq.d, &dk.d,
                             &dv.d, ws.data(), ws.bytes(), current_stream(dev.index));
   return Py_BuildValue("(iNNN)", status, dq.out(), dk.out(), dv.out());
   END_HANDLE_TH_ERRORS
@@ -433,11 +451,11 @@ PyObject* scored_varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Packed p(a[3], a[4], a[5], q, dev.index);
   const ra_tensor tq = describe(q, 3), tk = describe(dev(a[1]), 3), tv = describe(dev(a[2]), 3);
   const How x = how(a + 6);
-  const ra_scores* z = scores_of(a[10], dev.index, p.h, p.cu.n);
+  const ScoresArg z = scores_of(a[10], dev.index, p.h, p.cu.n);
   Result out(a[11], dev, [&] { return at::empty_like(q); });
   Result lse(a[12], dev, [&] { return at::empty({p.h, p.cu.total}, on(dev.index, at::kFloat)); });
   const Space ws(a[13], dev, g_varlen_ws(RA_OP_FWD, p.cu.total, p.h, p.d, x.layout, x.shards));
-  const int status = g_svfwd(&tq, &tk, &tv, p.cu.dev, p.cu.host, p.cu.n, p.longest, x.layout, x.shards, x.causal, x.scale, z,
+  const int status = g_svfwd(&tq, &tk, &tv, p.cu.dev, p.cu.host, p.cu.n, p.longest, x.layout, x.shards, x.causal, x.scale, z.get(),
                              &out.d, &lse.d, ws.data(), ws.bytes(), current_stream(dev.index));
   return Py_BuildValue("(iNN)", status, out.out(), lse.out());
   END_HANDLE_TH_ERRORS
@@ -455,13 +473,13 @@ PyObject* scored_varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   ra_tensor t[6];
   for (int i = 0; i < 6; ++i) t[i] = describe(dev(a[i]), dev(a[i]).dim());
   const How x = how(a + 9);
-  const ra_scores* z = scores_of(a[13], dev.index, p.h, p.cu.n);
+  const ScoresArg z = scores_of(a[13], dev.index, p.h, p.cu.n);
   Result dq(a[14], dev, [&] { return at::empty_like(q); });
   Result dk(a[15], dev, [&] { return at::empty_like(dev(a[2])); });
   Result dv(a[16], dev, [&] { return at::empty_like(dev(a[3])); });
   const Space ws(a[17], dev, g_varlen_ws(RA_OP_BWD, p.cu.total, p.h, p.d, x.layout, x.shards));
   const int status = g_svbwd(&t[0], &t[1], &t[2], &t[3], &t[4], &t[5], p.cu.dev, p.cu.host, p.cu.n, p.longest, x.layout, x.shards,
-                             x.causal, x.scale, z, &dq.d, &dk.d, &dv.d, ws.data(), ws.bytes(), current_stream(dev.index));
+                             x.causal, x.scale, z.get(), &dq.d, &dk.d, &dv.d, ws.data(), ws.bytes(), current_stream(dev.index));
   return Py_BuildValue("(iNNN)", status, dq.out(), dk.out(), dv.out());
   END_HANDLE_TH_ERRORS
 }

@@ -119,3 +119,35 @@ def test_a_blocks_share_of_the_gradients(d, cap, slope, gain, share):
         bound["dv"] += (P * (2.0 ** -8 * 1.01 + rel)).T @ ado
     for name, got in (("dk", dk), ("dv", dv)):
         assert_within(name, got[0, 0], (want[name], bound[name] + 2.0 ** -8 * np.abs(want[name])))
+
+
+def test_slopes_and_prefixes_are_read_from_where_they_are_at_the_call():
+    """The storage of a handle's tensors is exchanged: every call gives what a new handle gives."""
+    b, h, s, d = 2, 2, 200, 64
+    x = {k: v.cuda() for k, v in inputs(b, h, h, s, d, 9170).items()}
+    p = {k: v[0].transpose(0, 1).contiguous() for k, v in x.items()}
+    cu = ra.CuSeqlens([0, 120, 200], "cuda")
+    cache = ra.KVCache.empty(8, 64, h, d)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    lens = torch.tensor([120, 80], dtype=torch.int32, device="cuda")
+    ra.ring_attn_cache_append(p["k"], p["v"], cache, table, lens, cu)
+
+    def calls(z):
+        out, lse = ra.ring_attn_fwd(x["q"], x["k"], x["v"], causal=True, scores=z)
+        r = [out, lse, *ra.ring_attn_bwd(x["do"], x["q"], x["k"], x["v"], out, lse, causal=True, scores=z)]
+        r += ra.ring_attn_fwd_step(x["q"], x["k"], x["v"], 0, causal=True, scores=z)
+        out, lse = ra.ring_attn_varlen_fwd(p["q"], p["k"], p["v"], cu, scores=z)
+        r += [out, lse, *ra.ring_attn_varlen_bwd(p["do"], p["q"], p["k"], p["v"], out, lse, cu, scores=z)]
+        half = [p[n][:100].contiguous() for n in ("q", "do")]
+        out, lse = ra.ring_attn_llama3_varlen_fwd(half[0], p["k"], p["v"], cu, 0, 2, scores=z)
+        r += [out, lse, *ra.ring_attn_llama3_varlen_bwd(half[1], half[0], p["k"], p["v"], out, lse, cu, 0, 2, scores=z)]
+        return r + list(ra.ring_attn_cache_fwd(p["q"], cache, table, lens, cu, scores=z))
+
+    sl, pre = slopes_of(h, "alibi").cuda(), torch.tensor([10, 60], dtype=torch.int32, device="cuda")
+    z = ra.Scores(11.0, sl, pre)
+    first = calls(z)
+    sl.data = slopes_of(h, "mixed").cuda()
+    pre.data = torch.tensor([0, 30], dtype=torch.int32, device="cuda")
+    now, fresh = calls(z), calls(ra.Scores(11.0, slopes_of(h, "mixed").cuda(), torch.tensor([0, 30], dtype=torch.int32, device="cuda")))
+    check_no_device_error(ra)
+    assert not torch.equal(first[0], now[0]) and all(torch.equal(a, c) for a, c in zip(now, fresh))

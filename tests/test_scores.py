@@ -255,3 +255,17 @@ def test_tensors_of_other_ranks_are_refused(marshaller, at, bad):
     if 1 <= at <= 5:
         with pytest.raises(ValueError, match=message):
             ext.scored_varlen_fwd(*t[1:4], cu, cu, None, 0, 1, True, 0.125, ra._of(z), *t[4:6], None)
+
+
+def test_a_handles_tensors_are_taken_as_they_are_at_the_call(marshaller):
+    """Storage that was exchanged (x.data = y, x.resize_, x.set_) is described anew: lengths are those of now."""
+    _, tensor = marshaller
+    slopes, prefix = tensor(2, dtype=torch.float32), tensor(1, dtype=torch.int32)
+    x = [tensor(1, 2, 64, 64) for _ in range(3)]
+    for z, held, other, message in ((ra.Scores(0.0, slopes), slopes, tensor(3, dtype=torch.float32), "2 query heads"),
+                                    (ra.Scores(0.0, None, prefix), prefix, tensor(2, dtype=torch.int32), "1 sequences")):
+        held.data = other
+        with pytest.raises(ValueError, match=message):
+            z._arg(x[0].device, 2, 1)
+        with pytest.raises(ValueError, match=message):
+            ra.ring_attn_fwd(*x, causal=True, scores=z)
