@@ -448,7 +448,8 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  * of q, k and v; the slopes and softcap are constants).  i, j: the query's and the key's original
  * tokens, whatever the layout (varlen: in their sequence; the cache: cache indices).
  *   softcap: 0 (none), or 2^-10 to 2^20 with softmax_scale / softcap at most 2^10 (else
- *     RA_ERR_UNSUPPORTED).  y is off by at most softcap 2^-21, next to what x is.
+ *     RA_ERR_UNSUPPORTED).  y is off by at most softcap 2^-21, next to what x is, and the
+ *     gradients' factor 1 - (y / softcap)^2 by at most 2^-14 of itself.
  *   slopes: (h) fp32 device array, one per query head, finite, of any sign; or NULL.
  *   prefix: int32 device array, or NULL: with causal, tokens that every query sees, the first
  *     prefix[n] of batch n, or of sequence n (varlen, cache: entry of every sequence), so those see

@@ -257,7 +257,6 @@ ScoreParams score_params(float softcap, const float* slopes, const int32_t* pref
     at[0] = std::min(at[0], at[1]);  // (where polynomial 0 holds, 1 does)
     for (int i = 0; i < kTiers; ++i) p.lim[i] = (float)std::min(at[i] / k, 0x1p62);  // (its square is in fp32's range)
     p.cap2 = (float)cap2;
-    p.inv_cap2 = (float)(1.0 / cap2);
     p.e2 = (float)(2.0 * k * 1.4426950408889634);
   }
   return p;

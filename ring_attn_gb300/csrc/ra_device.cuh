@@ -481,8 +481,6 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ uint64_t neg_f32x2(uint64_t a) { return a ^ 0x8000000080000000ull; }
-
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -74,7 +74,6 @@ struct ScoreParams {
   float g0[2], g1[3], g2[5];  // d z / d (scale s) = 1 + w (g[0] + ...)
   float lim[kTiers];        // |s| up to which the polynomials hold
   float e2;                 // any s: z = cap2 - 2 cap2 / (1 + 2^(e2 s))
-  float inv_cap2;           // tanh(x / softcap) = z * inv_cap2
   const float* slopes;      // per query head
   const int* prefix;        // per batch or sequence, or nullptr
 };

@@ -13,7 +13,9 @@
 // scores, in pairs or not, the exponential four.  The derivative is 1 + w G(w) with G of degree 1, 2 or 4, off
 // by 2^-14.1, 2^-15.4, 2^-16.7, next to the half step of bf16 (2^-8) that the gradient is rounded by as an operand.
 // Beyond 1, tanh(u) = 1 - 2 / (1 + e^(2u)) with the hardware's exponential and reciprocal (4 and 8 cycles on top
-// of the softmax's 4): right for every u, infinite ones too, off by about 2^-22 absolutely.
+// of the softmax's 4): right for every u, infinite ones too, off by about 2^-22 absolutely.  The backward takes e^(-2|u|)
+// there, e, and the derivative as 4 e / (1 + e)^2, which keeps its bits where tanh is next to 1 (from the rounded tanh,
+// 1 - tanh^2 is off by 4 % at |u| = 7 and by all of it at 9).
 // A warp goes by the largest score that it has in registers: caps are meant to be far above most scores.
 // (Coefficients have powers of scale / softcap up to the twelfth.  Where those leave fp32's range a polynomial holds
 // up to a smaller u, or not at all: ScoreParams::lim.)
@@ -163,7 +165,7 @@ struct Cap {
     if constexpr (!kCap) {
       t[0] = two(sc.c0);
     } else if constexpr (kAny) {
-      t[0] = two(sc.e2), t[1] = two(-2.f * sc.cap2), t[2] = two(sc.cap2), g[0] = two(sc.inv_cap2);
+      t[0] = two(sc.e2), t[1] = two(-2.f * sc.cap2), t[2] = two(sc.cap2);
     } else {
 #pragma unroll
       for (int i = 0; i < kT; ++i) t[i] = two(kTier == 0 ? sc.t0[i % 4] : kTier == 1 ? sc.t1[i % 5] : sc.t2[i % 7]);
@@ -177,7 +179,7 @@ struct Cap {
 #pragma unroll
     for (int i = 0; i < kT; ++i) t[i] = cap_const(table, at + i);
   }
-  // Two products s: their scores + add, and w, from which their derivatives follow.
+  // Two products s: their scores + add, and w, from which their derivatives follow (kAny: the derivatives).
   __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add, uint64_t& w) const {
     if constexpr (!kCap) {
       w = 0;
@@ -185,6 +187,15 @@ struct Cap {
     } else if constexpr (!kAny) {
       w = mul_f32x2(s, s);
       return fma_f32x2(s, polynomial(w, t), add);
+    } else if constexpr (kGrad) {
+      float a0, a1, m0, m1;
+      f32x2_split(mul_f32x2(s, t[0]), a0, a1);
+      const float e0 = fast_exp2(-fabsf(a0)), e1 = fast_exp2(-fabsf(a1));
+      const uint64_t e = f32x2(e0, e1), r = f32x2(fast_rcp(e0 + 1.f), fast_rcp(e1 + 1.f));
+      const uint64_t r2 = add_f32x2(r, r);
+      w = mul_f32x2(mul_f32x2(e, r2), r2);
+      f32x2_split(fma_f32x2(r, t[1], t[2]), m0, m1);
+      return add_f32x2(f32x2(copysignf(m0, a0), copysignf(m1, a1)), add);
     } else {
       float e0, e1;
       f32x2_split(mul_f32x2(s, t[0]), e0, e1);
@@ -193,10 +204,10 @@ struct Cap {
     }
   }
   __device__ __forceinline__ uint64_t derivative(uint64_t w) const {
-    const uint64_t one = f32x2(1.f, 1.f);
-    if constexpr (!kAny) return fma_f32x2(w, polynomial(w, g), one);
-    const uint64_t th = mul_f32x2(w, g[0]);
-    return fma_f32x2(neg_f32x2(th), th, one);
+    if constexpr (kAny)
+      return w;
+    else
+      return fma_f32x2(w, polynomial(w, g), f32x2(1.f, 1.f));
   }
 };
 

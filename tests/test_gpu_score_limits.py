@@ -151,3 +151,40 @@ def test_slopes_and_prefixes_are_read_from_where_they_are_at_the_call():
     now, fresh = calls(z), calls(ra.Scores(11.0, slopes_of(h, "mixed").cuda(), torch.tensor([0, 30], dtype=torch.int32, device="cuda")))
     check_no_device_error(ra)
     assert not torch.equal(first[0], now[0]) and all(torch.equal(a, c) for a, c in zip(now, fresh))
+
+
+@pytest.mark.parametrize("d,causal,slope", [(64, False, 0.0), (128, True, 0.0), (64, True, 0.05)])
+@pytest.mark.parametrize("u", [4.0, 7.0, 9.0, -8.0])
+def test_gradients_of_saturated_scores(d, causal, slope, u):
+    """x / softcap of u: the derivative is 4 e^(-2|u|) and small, and dq and dk have all of its bits that bf16 keeps.
+    x is off by d 2^-24 sum |q k|, which the derivative takes twice over (relatively, next to softcap), and its own
+    exponential, reciprocal and products by 2^-18 (the exponential's argument, 26 at most, is rounded)."""
+    b, h, hk, s, cap = 1, 2, 1, 320, 1.0
+    x = inputs(b, h, hk, s, d, 9140)
+    x["q"] = (x["q"].float() * 0.2 + u * 0.5).bfloat16()
+    x["k"] = (x["k"].float() * 0.1 + 1.0).bfloat16()
+    scale = 2.0 * cap / d  # x is about u cap
+    sl = None if not slope else steep(h, slope)
+    g = {k: v.cuda() for k, v in x.items()}
+    z = scores_of(cap, sl, None)
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], "contiguous", 1, causal, scale, scores=z)
+    dq, dk, dv = ra.ring_attn_bwd(g["do"], g["q"], g["k"], g["v"], out, lse, "contiguous", 1, causal, scale, scores=z)
+    check_no_device_error(ra)
+    t = np.arange(s)
+    want_dk, tol_dk = np.zeros((s, d)), np.zeros((s, d))
+    for a in range(h):
+        q, k, v, do = (f64(x[n][0, 0 if n in "kv" else a]) for n in ("q", "k", "v", "do"))
+        r = head_bounds(q, k, v, t, t, scale, cap, 0.0 if sl is None else float(sl[a]), causal, 0, do)
+        xs = scale * (q @ k.T)
+        gr = 1.0 / np.cosh(xs / cap) ** 2  # (1 - tanh^2 in 64 bits has but half of them here)
+        dx = r["P"] * (r["dP"] - r["D"][:, None]) * gr
+        ado = np.abs(do)
+        err = 2 * d * EPS * scale * (np.abs(q) @ np.abs(k).T) / cap + 2.0 ** -18
+        rel = 2.0 ** -8 * 1.02 + 2.0 ** -17 + err
+        dD = (ado * r["tol"]["out"]).sum(1) + d * EPS * (ado * np.abs(r["out"])).sum(1)
+        off = np.abs(dx) * rel + r["P"] * gr * (dD[:, None] + d * EPS * (ado @ np.abs(v).T))
+        dq64, tol = scale * dx @ k, scale * off @ np.abs(k)
+        assert (np.abs(f64(dq[0, a]) - dq64) <= tol + 2.0 ** -8 * np.abs(dq64)).all()
+        want_dk += scale * dx.T @ q
+        tol_dk += scale * off.T @ np.abs(q)
+    assert (np.abs(f64(dk[0, 0]) - want_dk) <= tol_dk + 2.0 ** -8 * np.abs(want_dk)).all()
