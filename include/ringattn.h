@@ -455,6 +455,7 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  *     prefix[n] of batch n, or of sequence n (varlen, cache: entry of every sequence), so those see
  *     each other both ways.  Negative counts as 0, beyond the sequence as all of it.  Without
  *     causal it is refused (RA_ERR_INVALID_ARG).
+ * Values of v from 2^-60 to 2^80 in magnitude (or 0) have all of their bits' weight in out.
  * Documents packed into one buffer are the varlen calls' cu_seqlens.  The arrays are read by the
  * kernels, so a captured call follows them as they are when it is replayed.  A ra_scores
  * without any of the three makes a call the plain one; NULL is refused.

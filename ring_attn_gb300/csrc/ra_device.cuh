@@ -81,6 +81,10 @@ __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// A barrier with nothing in flight, before it is initialised again.
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void fence_mbar_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -619,14 +623,15 @@ __device__ __forceinline__ int vz_prefix_end(int base, int c, int N, int s, int 
 namespace ra {
 // Wait that ignores the abort flag (bounded by time only): used at teardown to
 // let copies and MMAs already in flight land before the CTA exits.
-static __device__ __forceinline__ void drain_one(uint32_t bar, uint32_t parity, const DevCtl& c, int site) {
+static __device__ __forceinline__ bool drain_one(uint32_t bar, uint32_t parity, const DevCtl& c, int site) {
   unsigned long long t0 = globaltimer();
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer() - t0 > c.wait_limit_ns) {
       record_error(c, DEV_TIMEOUT, site);
-      return;
+      return false;
     }
   }
+  return true;
 }
 }  // namespace ra
 

@@ -49,10 +49,10 @@ struct TileTokens {
 };
 constexpr int kNoSeam = 1 << 20;
 
-// A softmax's offset may be this much (log2 units) above the largest score: weights down to 2^-24 of the largest
-// are then still normal numbers, in bf16, too.  (So bounds are fp32 numbers wherever they are kept: those of steep
+// A softmax's offset may be this much (log2 units) above the largest score: that one's products with values of 2^-60
+// are then still normal numbers, and those of smaller weights as far as they count.  (So bounds are fp32 numbers wherever they are kept: those of steep
 // biases are 2^14 and more, and with the bits of bf16 they would be off by that much themselves.)
-constexpr float kLoose = 88.f;
+constexpr float kLoose = 48.f;
 
 // Numbers (no NaN) as integers in the same order, and a word of shared memory that is raised to the larger.
 __device__ __forceinline__ int to_ordered(float x) {

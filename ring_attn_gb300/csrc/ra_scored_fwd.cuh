@@ -7,10 +7,11 @@
 // instruction waits for the one before and their long straight code for its fetching.  So a row is two threads' here
 // (key columns [0, 64) and [64, 128) of a tile), four warps a scheduler, and the code of 32 columns is a loop's body.
 //
-// A call with a cap that is not too high has one offset for all rows (`fixed` below).  In a loop over 32 columns the
-// products come out of tensor memory, the polynomial for the largest of them is chosen, and they become weights,
+// A call with a cap that is not too high has one offset for all rows at first (`fixed` below).  In a loop over 32 columns
+// the products come out of tensor memory, the polynomial for the largest of them is chosen, and they become weights,
 // packed as bf16 over the first 32 of the thread's own 64 columns; sums of weights stay with the thread until the end.
-// Else a tile takes two steps before that:
+// Where a row's sum shows that the offset was far from its scores, the block starts again, as a call without such a
+// cap does.  There a tile takes two steps before that:
 //   1. largest product of the half row.  The cap is monotonic and the bias a line along a tile's columns, so an upper
 //      bound of the largest score follows; the offset of a softmax may lie above it by kLoose.  Tiles in which the
 //      bias is no line (the row's own token or a zigzag seam inside), or too steep a one, go over their changed
@@ -71,24 +72,33 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + LY::kMisc);
 
+  volatile int* again_flag = reinterpret_cast<volatile int*>(sp + LY::kMisc + 8);
   bool q_issued = false;  // by thread 0, the Q / K producer
-  if (threadIdx.x == 0) {
-    mbar_init(BAR(B_Q_FULL), 1);
+  auto init_tile_barriers = [&](bool anew) {
+    auto init = [&](int i, uint32_t count) {
+      if (anew) mbar_inval(BAR(i));
+      mbar_init(BAR(i), count);
+    };
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(BAR(B_K_EMPTY + i), 1);
+      init(B_K_EMPTY + i, 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(BAR(B_V_FULL + i), 1);
-      mbar_init(BAR(B_V_EMPTY + i), 1);
+      init(B_V_FULL + i, 1);
+      init(B_V_EMPTY + i, 1);
     }
     for (int t = 0; t < kQTiles; ++t) {
-      mbar_init(BAR(B_S_FULL + t), 1);
-      mbar_init(BAR(B_P_FULL + t), 8);  // one elected arrival per softmax warp
+      init(B_S_FULL + t, 1);
+      init(B_P_FULL + t, 8);  // one elected arrival per softmax warp
     }
-    mbar_init(BAR(B_O_DONE), 1);
-    mbar_init(BAR(B_TEARDOWN), 1);
-    *abort_flag = 0;
+    init(B_O_DONE, 1);
+    init(B_TEARDOWN, 1);
     fence_mbar_init();
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(BAR(B_Q_FULL), 1);
+    *abort_flag = 0;
+    *again_flag = 0;
+    init_tile_barriers(false);
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -109,7 +119,10 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     }
   }
   fill_cap_table(sp + LY::kCaps, p.sc);
-  if (threadIdx.x < 256) reinterpret_cast<int*>(sp + LY::kBound)[threadIdx.x] = to_ordered(-INFINITY);
+  auto init_bounds = [&]() {
+    if (threadIdx.x < 256) reinterpret_cast<volatile int*>(sp + LY::kBound)[threadIdx.x] = to_ordered(-INFINITY);
+  };
+  init_bounds();
   QRange cta;  // both query tiles together: decides which key tiles are visited
   const int pre = VL ? 0 : prefix_now(p, b);
   make_qrange(p, r, i0, kRowsPerCta, cta, pre);
@@ -128,9 +141,30 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  float slope2 = 0.f;
+  if constexpr ((SC & SC_BIAS) != 0) slope2 = load_now(p.sc.slopes + h) * 1.4426950408889634f;
+  // Capped scores lie within +-cap2, so where that is small enough one offset will do for nearly all rows: a weight is
+  // 2^-101 to 2^61.  A bias only takes off, and nothing from the row's own token, which every row of a whole call sees.  A
+  // row's sum tells afterwards how far its largest weight is from 1.  Within kSums values of 2^-60 to 2^80
+  // have products with it in fp32's range, and so have smaller weights as far as they count; else the block starts again,
+  // with running offsets.  (With softcap 50: where the largest
+  // score lies below -17, or at the cap.)
+  const bool fixed = (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
+  // Whether the block, all of whose threads come here with nothing in flight, starts again.
+  auto again = [&]() -> bool {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (!*again_flag || *abort_flag) return false;
+    init_bounds();
+    if (threadIdx.x == 0) init_tile_barriers(true);
+    __syncthreads();
+    return true;
+  };
   if (warp < 4) {
     // ------------------------------------------------------------ control warpgroup
     regs_dec<kScoredRegsLow>();
+    auto control = [&]() {
     if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ TMA producer (warp 0)
     if (warp == 0 && lane == 0 && n_tiles > 0) {
@@ -170,7 +204,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         return true;
       });
       for (int st = 0; st < kVStages; ++st)
-        if (issued[st]) drain_one(BAR(B_V_FULL + st), (issued[st] - 1) & 1, p.ctl, 21);
+        if (issued[st] && !drain_one(BAR(B_V_FULL + st), (issued[st] - 1) & 1, p.ctl, 21)) *abort_flag = 1;
     }
     if (threadIdx.x == 0 && q_issued) drain_one(BAR(B_Q_FULL), 0, p.ctl, 20);
     __syncwarp();
@@ -233,12 +267,16 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
           for (int t = 0; t < kQTiles && ok; ++t) ok = issue_pv(t, j - 1);
         if (ok) mma_commit(BAR(B_O_DONE));
       }
-      // every issued MMA completes before the CTA frees TMEM
+      // every issued MMA completes before the CTA frees TMEM, or starts again
       mma_commit(BAR(B_TEARDOWN));
-      drain_one(BAR(B_TEARDOWN), 0, p.ctl, 23);
+      if (!drain_one(BAR(B_TEARDOWN), 0, p.ctl, 23) || (ok && !drain_one(BAR(B_O_DONE), 0, p.ctl, 22))) *abort_flag = 1;
     }
     __syncwarp();
     }
+    };
+    // (not a loop: what it keeps from one walk to the next is too much for these few registers, 3 % of the kernel's time)
+    control();
+    if (fixed && again()) control();
   } else {
     // ------------------------------------------------------------ softmax / epilogue
     regs_inc<kScoredRegsHigh>();
@@ -252,6 +290,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     bool valid = i < p.L;
     const uint32_t bound = sb + LY::kBound + 4 * (t * 128 + row);  // of the row's scores so far
     const int pair_bar = 1 + t * 4 + (warp & 3);  // the two warps of 32 rows
+    constexpr float kOffset = 20.f, kSums[2] = {0x1p-45f, 0x1p44f};  // of half a row
     const uint32_t cap_table = sb + LY::kCaps;
     QRange qt;
     RowWin win;
@@ -262,18 +301,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       make_qrange(p, r, i0 + t * kTileM, kTileM, qt, pre);
       gq = tok(p, r, valid ? i : max(qt.i_last, 0));
     }
-    float slope2 = 0.f;
-    if constexpr ((SC & SC_BIAS) != 0) slope2 = load_now(p.sc.slopes + h) * 1.4426950408889634f;
-    // Capped scores lie within +-cap2, so where that is small enough one offset serves all rows: weights are at most
-    // 1, or 2^60 for the largest of these caps, and the largest one of a row whose scores are the least is 2^-102 or
-    // more, 2^24 above what fp32 and bf16 still have.  A bias only takes off, and nothing from the row's own token, which
-    // every row of a whole call sees.
-    const bool fixed =
-        (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
-    // offset of the weights, in log2 units
-    float m_run = fixed ? fminf(p.sc.cap2, 102.f - p.sc.cap2) : -INFINITY;
-    float l_run = 0.f;        // running sum of this half's weights
-    bool ok = true;
+    // offset of the weights, in log2 units, and the running sum of this half's
+    float m_run = fixed ? fminf(p.sc.cap2, kOffset) : -INFINITY, l_run = 0.f;
+    bool ok = true, running = !fixed;
     int j = 0;
     // allowed columns [c_lo, c_hi) of the thread's 64, as bits
     auto window = [&](int s, int kt, int& c_lo, int& c_hi) {
@@ -352,9 +382,17 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         float s0, s1;
         f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
         l_run = s0 + s1;
+        // the halves' larger sum (0: the row sees nothing)
+        raise_shared(bound, to_ordered(l_run));
+        named_bar_sync(pair_bar, 64);
+        const float l = from_ordered(load_shared(bound));
+        if (valid && ok && l > 0.f && (l < kSums[0] || l > kSums[1])) *again_flag = 1;
+        __syncwarp();
+        running = again();
+        if (running) m_run = -INFINITY, l_run = 0.f, j = 0;
       }
     }
-    if (!fixed) walk_tiles(p, cta, nkt, [&](int s, int kt) {
+    if (running) walk_tiles(p, cta, nkt, [&](int s, int kt) {
       int c_lo, c_hi;
       const uint64_t mw = window(s, kt, c_lo, c_hi);
       const bool masked = c_lo > 0 || c_hi < 64;

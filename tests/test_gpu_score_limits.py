@@ -8,7 +8,7 @@ import oracle
 import ring_attn_gb300 as ra
 from tests.helpers import check_no_device_error, lse_to_original, to_layout, to_original
 from tests.score_case import EPS, assert_within, expect, f64, head_bounds
-from tests.test_gpu_scores import inputs, scores_of, slopes_of
+from tests.test_gpu_scores import inputs, rows_first, scores_of, slopes_of
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +188,65 @@ def test_gradients_of_saturated_scores(d, causal, slope, u):
         want_dk += scale * dx.T @ q
         tol_dk += scale * off.T @ np.abs(q)
     assert (np.abs(f64(dk[0, 0]) - want_dk) <= tol_dk + 2.0 ** -8 * np.abs(want_dk)).all()
+
+
+@pytest.mark.parametrize("power", [80, -60])
+@pytest.mark.parametrize("cap", [12.0, 30.0, 50.0, 56.0, 70.0])
+@pytest.mark.parametrize("end", [-1.0, 0.0, 1.0])
+def test_values_far_from_one(power, cap, end):
+    """Rows at an end of the cap, or near 0, over values of 2^80 and 2^-60: weights are those of the row's largest."""
+    b, h, hk, s, d = 1, 2, 1, 384, 64
+    x = inputs(b, h, hk, s, d, 9130)
+    x["q"] = (x["q"].float() + 60.0 * end).bfloat16()
+    x["k"] = (x["k"].float() + 20.0).bfloat16() if end else x["k"]
+    x["v"] = (x["v"].float() * 2.0 ** power).bfloat16()
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], "contiguous", 1, True, scores=ra.Scores(cap))
+    check_no_device_error(ra)
+    want = expect(x["q"], x["k"], x["v"], None, d ** -0.5, cap, None, True, None)
+    assert_within("out", out, want["out"])
+    assert_within("lse", lse, want["lse"])
+
+
+@pytest.mark.parametrize("form", ["contiguous", "zigzag", "stripe", "packed", "packed zigzag", "step"])
+@pytest.mark.parametrize("d,slopes,rows", [(64, None, "third"), (128, None, "one"), (128, "alibi", "third")])
+def test_blocks_whose_rows_need_offsets_of_their_own(form, d, slopes, rows):
+    """A few rows at the cap's negative end among others near 0, in every form of the forward, over values of 2^70."""
+    h, hk, n, cap = 2, 1, 2, 50.0
+    lens = [256, 640, 128] if form.startswith("packed") else None
+    b, s = (1, 1024) if lens else (2, 640)
+    if form == "step" and slopes:
+        slopes = None
+    x = inputs(b, h, hk, s, d, 9180)
+    low = torch.arange(s) % 3 == 0 if rows == "third" else torch.arange(s) == s // 2 + 5
+    x["k"] = (x["k"].float() + 8.0).bfloat16()
+    x["q"] = (x["q"].float() * 0.1 - 20.0 * low[None, None, :, None]).bfloat16()
+    x["v"] = (x["v"].float() * 2.0 ** 70).bfloat16()
+    sl = slopes_of(h, slopes)
+    z = scores_of(cap, sl, None)
+    if lens:
+        layout = "zigzag" if "zigzag" in form else "contiguous"
+        cu = ra.CuSeqlens([0, *np.cumsum(lens)], "cuda")
+        g = {k: ra.ring_attn_varlen_permute(rows_first(v), cu, layout, n, seq_dim=0) for k, v in x.items()}
+        out, lse = ra.ring_attn_varlen_fwd(g["q"], g["k"], g["v"], cu, None, n, True, layout=layout, scores=z)
+
+        def back(t):
+            t = torch.empty(t.shape, dtype=t.dtype, device="cuda").copy_(t)
+            return ra.ring_attn_varlen_unpermute(t, cu, layout, n, seq_dim=0).transpose(0, 1).unsqueeze(0)
+
+        out, lse = back(out), back(lse.t().contiguous().unsqueeze(-1)).squeeze(-1)
+        want = expect(x["q"], x["k"], x["v"], None, d ** -0.5, cap, sl, True, None, [0, *np.cumsum(lens)])
+    else:
+        layout = "contiguous" if form == "step" else form
+        shards = 1 if form == "step" else n
+        g = {k: to_layout(ra, v.cuda(), layout, shards) for k, v in x.items()}
+        if form == "step":
+            out, lse = ra.ring_attn_fwd_step(g["q"], g["k"], g["v"], 0, causal=True, scores=z)
+        else:
+            out, lse = ra.ring_attn_fwd(g["q"], g["k"], g["v"], layout, shards, True, scores=z)
+        out, lse = to_original(ra, out, layout, shards), lse_to_original(ra, lse, layout, shards)
+        want = expect(x["q"], x["k"], x["v"], None, d ** -0.5, cap, sl, True, None)
+    check_no_device_error(ra)
+    assert float(want["lse"][0].min()) < -25.0 and float(want["lse"][0].max()) > 0.0
+    assert_within("lse", lse, want["lse"])
+    assert_within("out", out, want["out"])
