@@ -898,9 +898,21 @@ def ring_attn_rope_bwd(dq, dk, rope, positions=None, axes=None, interleaved=Fals
     return _rope_call(True, dq, dk, rope, positions, axes, interleaved, layout, n_shards, dq_out, dk_out, stream)
 
 
+def _axes(axes):
+    """The axes of the pairs as bytes (bytes(n) of a number would be n zeros, of an array its memory)."""
+    if axes is None or isinstance(axes, bytes):
+        return axes
+    if not isinstance(axes, (list, tuple)):
+        try:
+            axes = [int(a) for a in axes]
+        except TypeError:
+            raise ValueError("axes must name an axis for each pair") from None
+    return bytes(axes)
+
+
 def _rope_call(inverse, q, k, rope, positions, axes, interleaved, layout, n_shards, q_out, k_out, stream):
     f = (_EXT or _ext()).rope
-    args = (q, k, rope[0], rope[1], positions, None if axes is None else bytes(axes), interleaved, inverse,
+    args = (q, k, rope[0], rope[1], positions, _axes(axes), interleaved, inverse,
             _layout(layout), int(n_shards), q_out, k_out)
     if stream is None:
         r = f(*args)

@@ -269,3 +269,17 @@ def test_a_handles_tensors_are_taken_as_they_are_at_the_call(marshaller):
             z._arg(x[0].device, 2, 1)
         with pytest.raises(ValueError, match=message):
             ra.ring_attn_fwd(*x, causal=True, scores=z)
+
+
+def test_axes_are_a_row_of_numbers(lib):
+    """A number is no row (bytes(32) would be 32 pairs on axis 0), and an array means its numbers, not its memory."""
+    x = torch.zeros(3, 2, 64)
+    for axes in (32, 2.0, torch.tensor(32), np.int64(32)):
+        for call in (ra.ring_attn_rope, ra.ring_attn_rope_bwd):
+            with pytest.raises(ValueError, match="axes"):
+                call(x, None, (x, x), x, axes)
+    with pytest.raises(ValueError):
+        ra.ring_attn_rope(x, None, (x, x), x, [0, 256])
+    want = bytes([0, 1, 2, 1])
+    for axes in (want, [0, 1, 2, 1], (0, 1, 2, 1), np.array([0, 1, 2, 1]), torch.tensor([0, 1, 2, 1]), iter([0, 1, 2, 1])):
+        assert ra._axes(axes) == want
