@@ -214,7 +214,8 @@ struct Scored {
 
 // unit: log2(e) times what a product is multiplied by (the cache's kernels do that themselves: 1).
 ScoreParams score_params(float softcap, const float* slopes, const int32_t* prefix, double unit) {
-  // tanh(u) = u (1 + w P(w)) and its derivative 1 + w G(w), w = u^2, for |u| up to 0.4, 0.6 and 1 (ra_score.cuh)
+  // tanh(u) = u (1 + w P(w)) and its derivative 1 + w G(w), w = u^2, for |u| up to 0.4, 0.6 and 1 (ra_score.cuh): minimax by
+  // Lawson's algorithm, remade and measured by tests/test_score_polynomials.py
   static const double p0[3] = {-0.3333188226164798, 0.1327762900673371, -0.047794219065101964},
                       p1[4] = {-0.33332597507686307, 0.13313116655333151, -0.05221180641094125, 0.015612632206438055},
                       p2[6] = {-0.33332986779616663, 0.13326408875629328, -0.05349870759405957, 0.02035975918561412,
