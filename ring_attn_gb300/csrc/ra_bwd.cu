@@ -9,7 +9,7 @@ cudaError_t launch_plain(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
                          const BwdParams& p, int which, cudaStream_t st) {
   BwdParamsT<VL> pv;
   static_cast<BwdParams&>(pv) = p;
-  return launch_bwd_v<D, VL, 0>(tq, tk, tv, tdo, pv, which, st);
+  return which == 0 ? launch_dkdv_v<D, VL, 0>(tq, tk, tv, tdo, pv, st) : launch_dq_v<D, VL>(tq, tk, tv, tdo, pv, st);
 }
 
 }  // namespace

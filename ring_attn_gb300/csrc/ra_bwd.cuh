@@ -22,8 +22,8 @@
 // Each tile row is split between two threads (query or key columns [0, 64) and
 // [64, 128)); ra_bwd_common.cuh describes the packed TMEM operands this gives.
 //
-// SC: 0, or SC_ON for calls with a prefix that all tokens see, which changes masks only.  Capped or
-// biased scores have kernels of their own (ra_scored_bwd.cuh).
+// SC (dK / dV): 0, or SC_ON for calls with a prefix that all tokens see, which changes masks only.  The other kernels
+// of calls with changed scores are in ra_scored_bwd.cuh.
 #pragma once
 
 #include "ra_bwd_common.cuh"
@@ -484,11 +484,11 @@ enum DqBar {
   F_TEARDOWN = 17
 };
 
-template <int D, bool VL, int SC>
+template <int D, bool VL>
 __global__ void __launch_bounds__(kThreads, 1)
     ring_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                   const BwdParamsT<VL, SC> p) {
+                   const BwdParamsT<VL> p) {
   using LY = DqLayout<D>;
   constexpr int KS = LY::kKStages, VS = LY::kVStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -549,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   }
   QRange qr;
-  const int pre = VL ? 0 : prefix_of(p, b);
-  make_qrange(p, r, i0, kTileM, qr, pre);
+  make_qrange(p, r, i0, kTileM, qr);
   const int nkt = (p.L + kTileN - 1) / kTileN;
   int n_tiles = 0;
   walk_kv_tiles(p, qr, nkt, 0, p.N, [&](int, int) {
@@ -668,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (VL)
       make_row_win(p, r, min(i, p.L - 1), false, win);
     else
-      gq = seeing_token<decltype(p)>(tok(p, r, valid ? i : max(qr.i_last, 0)), pre);
+      gq = tok(p, r, valid ? i : max(qr.i_last, 0));
     // this row's statistics, negated (padding rows: -lse2 = -inf, -D = 0, so P = dS = 0)
     const long long srow = (((long long)b * p.H + h) * p.stat_N + (r - p.stat_r0)) * p.stat_L + i;
     const uint64_t nl2 = f32x2(__ldg(p.nlse2 + srow), __ldg(p.nlse2 + srow));
@@ -797,20 +796,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool VL, int SC>
-cudaError_t launch_bwd_v(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                         const CUtensorMap& tdo, const BwdParamsT<VL, SC>& p, int which, cudaStream_t st) {
-  if (which == 0) {
-    // the register split inside the kernel is only safe with the launch allocation it was sized for
-    cudaError_t e = configure_kernel<ring_dkdv_kernel<D, VL, SC>>(kDkdvLaunchRegs, DkdvLayout<D>::kAlloc);
-    if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)(p.N * p.n_ktiles), (unsigned)(p.B * p.Hk));
-    ring_dkdv_kernel<D, VL, SC><<<grid, kThreads, DkdvLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, p);
-  } else {
-    cudaError_t e = configure_kernel<ring_dq_kernel<D, VL, SC>>(0, DqLayout<D>::kAlloc);
-    if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * p.n_qtiles), (unsigned)(p.B * p.H));
-    ring_dq_kernel<D, VL, SC><<<grid, kThreads, DqLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, p);
-  }
+cudaError_t launch_dkdv_v(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const CUtensorMap& tdo, const BwdParamsT<VL, SC>& p, cudaStream_t st) {
+  // the register split inside the kernel is only safe with the launch allocation it was sized for
+  cudaError_t e = configure_kernel<ring_dkdv_kernel<D, VL, SC>>(kDkdvLaunchRegs, DkdvLayout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  dim3 grid((unsigned)(p.N * p.n_ktiles), (unsigned)(p.B * p.Hk));
+  ring_dkdv_kernel<D, VL, SC><<<grid, kThreads, DkdvLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool VL>
+cudaError_t launch_dq_v(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
+                        const BwdParamsT<VL>& p, cudaStream_t st) {
+  cudaError_t e = configure_kernel<ring_dq_kernel<D, VL>>(0, DqLayout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  dim3 grid((unsigned)((p.r_only >= 0 ? 1 : p.N) * p.n_qtiles), (unsigned)(p.B * p.H));
+  ring_dq_kernel<D, VL><<<grid, kThreads, DqLayout<D>::kAlloc, st>>>(tq, tk, tv, tdo, p);
   return cudaGetLastError();
 }
 

@@ -816,7 +816,7 @@ cudaError_t launch_bwd_sdv(const CUtensorMap& tq, const CUtensorMap& tk, const C
       return launch_early(ring_scored_dq_kernel<D, VL, SC>, grid, kThreads, LY::kAlloc, st, tq, tk, tv, tdo, pv);
     ring_scored_dq_kernel<D, VL, SC><<<grid, kThreads, LY::kAlloc, st>>>(tq, tk, tv, tdo, pv);
   } else if constexpr (SC == SC_ON) {
-    return launch_bwd_v<D, VL, SC>(tq, tk, tv, tdo, pv, 0, st);
+    return launch_dkdv_v<D, VL, SC>(tq, tk, tv, tdo, pv, st);
   } else {
     cudaError_t e = configure_kernel<ring_scored_dkdv_kernel<D, VL, SC>>(kDkdvLaunchRegs, DkdvLayout<D>::kAlloc);
     if (e != cudaSuccess) return e;
