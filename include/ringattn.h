@@ -450,12 +450,13 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  *   softcap: 0 (none), or 2^-10 to 2^20 with softmax_scale / softcap at most 2^10 (else
  *     RA_ERR_UNSUPPORTED).  y is off by at most softcap 2^-21, next to what x is, and the
  *     gradients' factor 1 - (y / softcap)^2 by at most 2^-14 of itself.
- *   slopes: (h) fp32 device array, one per query head, finite, of any sign; or NULL.
+ *   slopes: (h) fp32 device array, one per query head, finite, of any sign; or NULL.  slope * |i - j| is off by
+ *     at most 2^-22 of slope * (|i - j| + 128), stripe layout + 128 n_shards.
  *   prefix: int32 device array, or NULL: with causal, tokens that every query sees, the first
  *     prefix[n] of batch n, or of sequence n (varlen, cache: entry of every sequence), so those see
  *     each other both ways.  Negative counts as 0, beyond the sequence as all of it.  Without
  *     causal it is refused (RA_ERR_INVALID_ARG).
- * Values of v from 2^-60 to 2^80 in magnitude (or 0) have all of their bits' weight in out.
+ * Values of v of 2^-60 to 2^80 in magnitude (and 0) have their part in out; smaller ones may vanish, larger ones overflow.
  * Documents packed into one buffer are the varlen calls' cu_seqlens.  The arrays are read by the
  * kernels, so a captured call follows them as they are when it is replayed.  A ra_scores
  * without any of the three makes a call the plain one; NULL is refused.
@@ -466,7 +467,7 @@ ra_status ring_attn_rope(const ra_tensor* q, const ra_tensor* k, const ra_tensor
  *
  * ring_attn_scored_X is ring_attn_X with scores; everything else is as there, but that dq, dk and dv
  * may share no element with dout, q, k, v or each other (RA_ERR_INVALID_ARG; slices of one packed tensor
- * share none).  The CTA-pair knob does not concern these calls. */
+ * share none).  The CTA-pair knob does not concern these calls; ring_attn_bwd_static_scratch has no form with scores. */
 typedef struct {
   float softcap;
   const float* slopes;

@@ -11,7 +11,7 @@ namespace ra {
 // kernel has ended and its writes are visible, and only then allows the same to
 // the next one, so no more than two kernels overlap.  Global memory is read by
 // plain loads, which stay behind the wait (loads through the read-only path need
-// not).  Saves about 2 us a launch for single tokens and short sequences (257 capped tokens of 4 heads: 11.0 us,
+// not).  Saves about 2 us a launch for single tokens and short sequences (257 capped tokens of 4 heads: 11.1 us,
 // 13.4 without).
 __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

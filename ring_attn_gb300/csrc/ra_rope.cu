@@ -6,7 +6,8 @@
 // at a time, with their tokens' entries in registers, and goes through a range of heads, four in flight (two: 2 %
 // slower, eight: 3 %; the first four asked for before the positions are looked up: 18 %, for the registers).
 // 65,536 tokens of 32 + 8 heads of 128, three axes: 200 us, 6.9 TB/s (101 % of the measured copy rate); 9001 tokens
-// of 16 + 16 heads of 64, turned back: 17.3 us, 4.4 TB/s, of which a launch that moves nothing takes about 6.
+// of 16 + 16 heads of 64, turned back: 14.5 us a launch within a graph, 5.2 TB/s, and 17.3 as separate calls: 1126 blocks,
+// of which 760 are resident at a time (95 registers: 20 warps an SM), a wave and a half.
 #include "ra_cache.cuh"
 
 namespace ra {
@@ -167,8 +168,8 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
   constexpr int RPW = 32 / (D / 16);
   const long long groups = ((long long)a.b * a.s + RPW - 1) / RPW;
   const int heads = a.h[0] + a.h[1], most = (heads + kAhead - 1) / kAhead;
-  // few tokens: their heads go to several warps, up to 32 warps on every SM (9001 tokens of 32 heads of 64: 17.3 us,
-  // 18.5 with 16, 18.3 with 64)
+  // few tokens: their heads go to several warps, up to 32 for every SM, of which 20 are resident (9001 tokens of 32 heads
+  // of 64: 17.3 us, 18.5 with 16, 18.3 with 64)
   const long long want = (32LL * num_sms() + groups - 1) / groups;
   const int turns = (most + (int)(want < most ? want : most) - 1) / (int)(want < most ? want : most);
   const int parts = (most + turns - 1) / turns;

@@ -21,10 +21,10 @@
 //
 // Bound, d = 128: a tile of 128 x 128 needs 1024 cycles of the tensor cores, which are busy half of the time; the
 // multiply-add pipes are for 39 %, the issue slots for 53 %.  The rest are a tile's steps that wait for one another (a
-// product, its weights, the next product), with two tiles in flight, which fill tensor memory.  Causal, 16,384 tokens of
-// 32 heads of 128, softcap 50:
-// 1.72 to 1.75 ms, 1276 TFLOP/s (66 % of the measured bf16 rate), without the cap 1.55; 8192 tokens of 32 + 8 heads,
-// softcap 30 and a prefix 0.50 ms (0.46); 2 x 4096 tokens of 16 heads of 64, a bias, 4 striped shards 178 us (157).
+// product, its weights, the next product), with two tiles in flight, which fill tensor memory (d = 64 leaves 128 columns,
+// which would hold a third score tile).  Causal, 16,384 tokens of 32 heads of 128, softcap 50: 1.75 ms, 1252 TFLOP/s (65 %
+// of the measured bf16 rate), 1.86 between other work; without the cap 1.54.  8192 tokens of 32 + 8 heads, softcap 30
+// and a prefix 0.51 ms (0.45); 2 x 4096 tokens of 16 heads of 64, a bias, 4 striped shards 184 us (157).
 // What led here, for the first: a row a thread 2.36 ms, half a row 2.14, one offset and 32 columns at a time 1.82 (1.88
 // with the polynomials' constants from the parameters), heavy tiles first 1.72.  Choosing the polynomial afterwards
 // and doing the few other tiles again took 1.79 for 1.82, but 0.59 for 0.56 where scores are larger next to their cap.
