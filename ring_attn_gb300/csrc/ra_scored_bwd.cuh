@@ -8,7 +8,7 @@
 // own instructions.
 //
 // Bound, d = 128: a tile of 128 x 128 needs 2048 cycles of the tensor cores in either kernel (four products), which are
-// busy 45 (dQ) and 55 % of the time; the multiply-add pipes are for 40 and 36 %, the issue slots for 45 and 40.  The rest are
+// busy 44 (dQ) and 54 % of the time; the multiply-add pipes are for 41 and 35 %, the issue slots for 46 and 39.  The rest are
 // a tile's steps that wait for one another, with tensor memory full (d = 64: dK / dV leave 128 columns).  8192 tokens
 // of 32 + 8 heads of 128, softcap 30 and a prefix: dK and dV 0.89 ms (plain scores 0.79), dQ 1.02 (0.57, with three
 // products); 12 documents of 200 to 4000 tokens, 16 + 4 heads, a bias: 255 and 241 us (250, 185); 2 x 4096 tokens of

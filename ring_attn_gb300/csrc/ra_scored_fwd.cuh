@@ -20,7 +20,7 @@
 //      the running one by 2^8.
 //
 // Bound, d = 128: a tile of 128 x 128 needs 1024 cycles of the tensor cores, which are busy half of the time; the
-// multiply-add pipes are for 39 %, the issue slots for 53 %.  The rest are a tile's steps that wait for one another (a
+// multiply-add pipes are for 40 %, the issue slots for 52 %.  The rest are a tile's steps that wait for one another (a
 // product, its weights, the next product), with two tiles in flight, which fill tensor memory (d = 64 leaves 128 columns,
 // which would hold a third score tile).  Causal, 16,384 tokens of 32 heads of 128, softcap 50: 1.75 ms, 1252 TFLOP/s (65 %
 // of the measured bf16 rate), 1.86 between other work; without the cap 1.54.  8192 tokens of 32 + 8 heads, softcap 30
@@ -145,10 +145,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   if constexpr ((SC & SC_BIAS) != 0) slope2 = load_now(p.sc.slopes + h) * 1.4426950408889634f;
   // Capped scores lie within +-cap2, so where that is small enough one offset will do for nearly all rows: a weight is
   // 2^-101 to 2^61.  A bias only takes off, and nothing from the row's own token, which every row of a whole call sees.  A
-  // row's sum tells afterwards how far its largest weight is from 1.  Within kSums values of 2^-60 to 2^80
-  // have products with it in fp32's range, and so have smaller weights as far as they count; else the block starts again,
-  // with running offsets.  (With softcap 50: where the largest
-  // score lies below -17, or at the cap.)
+  // row's sum tells afterwards how far its largest weight is from 1.  Within kSums values of 2^-60 to 2^80 have products
+  // with it in fp32's range, and so have smaller weights as far as they count; else the block starts again, with
+  // running offsets.  (With softcap 50: where a row's largest score lies below -17, or at the cap.)
   const bool fixed = (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
   // Whether the block, all of whose threads come here with nothing in flight, starts again.
   auto again = [&]() -> bool {
