@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   // 2^-101 to 2^61.  A bias only takes off, and nothing from the row's own token, which every row of a whole call sees.  A
   // row's sum tells afterwards how far its largest weight is from 1.  Within kSums values of 2^-60 to 2^80 have products
   // with it in fp32's range, and so have smaller weights as far as they count; else the block starts again, with
-  // running offsets.  (With softcap 50: where a row's largest score lies below -17, or at the cap.)
+  // running offsets.  (With softcap 50: where a row's largest score lies below -17, or at the cap.  The 16,384 tokens above
+  // take 1.73 ms, with every row at an end of the cap, so that all blocks start again, 5.5, and with running offsets from
+  // the first on 2.2 and 2.9: scores near the cap are what caps are not meant for.)
   const bool fixed = (SC & SC_CAP) != 0 && p.sc.cap2 <= 81.f && ((SC & SC_BIAS) == 0 || (slope2 >= 0.f && p.step < 0));
   // Whether the block, all of whose threads come here with nothing in flight, starts again.
   auto again = [&]() -> bool {
